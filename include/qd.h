@@ -69,6 +69,7 @@ enum {
   QD_DEVERR_NAN = 4,       /* an all-NaN logit row in argmax */
   QD_DEVERR_STEPS = 8,     /* step >= max_steps in argmax_advance */
   QD_DEVERR_TIMEOUT = 16,  /* a bounded wait on an asynchronous copy gave up */
+  QD_DEVERR_CACHE = 32,    /* a page operation that could not be carried out whole (nothing changed) */
 };
 
 /* Weight formats: BF16; Q8_0 (32-wide int8 blocks with an fp16 scale); INT4 (W4A16: */
@@ -207,6 +208,106 @@ int qd_attn_decode_paged_noalloc(const float* q, const void* k_pages, const void
                                  int n_q_heads, int n_kv_heads, int head_dim, int page_size,
                                  int max_pages, int n_pages, float scale, float* out,
                                  cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Attention over the packed rows of several prompts (the batched form of       */
+/* qd_prefill's attention; [KL-FUN], [KL-PAGED]). Sequence b owns the rows        */
+/* cu_rows[b] .. cu_rows[b + 1) of q; its keys, the rows' own included, are        */
+/* already in the cache, seq_lens[b] of them. Row j of its n rows is the token at  */
+/* position seq_lens[b] - n + j and sees that position and all before:            */
+/*   out[r, h, :] = sum_{t <= seq_lens[b] - n + j} softmax_t(scale * q[r,h,:].K_b[t,g,:]) */
+/*                  * V_b[t, g, :],   g = h / (n_q_heads / n_kv_heads)               */
+/* A row before position 0 (seq_lens[b] < n) sees nothing and gives 0. Rows of q  */
+/* outside every sequence are not read, and out is left as it was there.          */
+/* q: [n_rows, n_q_heads, head_dim], q_stride elements from one row to the next    */
+/* (>= n_q_heads * head_dim, a multiple of 16 bytes: q may be part of the QKV       */
+/* projection's rows); q_is_f32 = 1: q and out f32 (q and the softmax weights       */
+/* enter the bf16 matrix products as hi + lo pairs), 0: both bf16 (the weights      */
+/* rounded to bf16, sums and softmax statistics in f32). out: [n_rows, n_q_heads,   */
+/* head_dim], contiguous, not q. Caches and page_table as in qd_attn_decode_paged;   */
+/* cu_rows: int32 [batch + 1], ascending from >= 0 to <= n_rows; seq_lens: int32      */
+/* [batch] (both device). Keys a row does not see have no effect on it, NaN and       */
+/* infinities included. Errors on the device (QD_DEVERR_POS: cu_rows not ascending     */
+/* or past n_rows, which leaves all of out; a length past the table, which leaves the   */
+/* sequence's rows). workspace: device scratch of qd_attn_prompt_workspace_bytes()       */
+/* bytes for the current device, zero-filled before its first use (each call leaves it    */
+/* ready for the next); two calls that overlap on the GPU need two.                      */
+/* Limits: head_dim == 128, n_q_heads / n_kv_heads in {1, 2, 4, 8}, batch <= 1024,      */
+/* n_rows <= 2^20.                                                                     */
+size_t qd_attn_prompt_workspace_bytes(void);
+int qd_attn_prompt(const void* q, int q_is_f32, int64_t q_stride, const void* k_pages, const void* v_pages,
+                   const int32_t* page_table, const int32_t* cu_rows, const int32_t* seq_lens, int batch,
+                   int n_rows, int n_q_heads, int n_kv_heads, int head_dim, int page_size, int max_pages,
+                   int n_pages, float scale, void* out, void* workspace, size_t workspace_bytes,
+                   cudaStream_t stream);
+
+/* Decode attention of sequences that share prefixes: the result of                 */
+/* qd_attn_decode_paged for sequences whose page tables name the same pages at their  */
+/* start (qd_pages_fork), each shared page read once for all of them. Group i holds    */
+/* the sequences cu_seqs[i] .. cu_seqs[i + 1); their first shared_lens[i] tokens lie in  */
+/* the pages of the group's first sequence's row (a sequence shorter than that sees its   */
+/* own seq_lens tokens of them). Sequences outside every group are left as they were.      */
+/* shared_lens[i] may be 0 and need not be a multiple of page_size. Arguments as            */
+/* in qd_attn_prompt with one row per sequence: q, out [batch, n_q_heads, head_dim];          */
+/* page_table [batch, max_pages], seq_lens [batch]; cu_seqs: int32 [n_groups + 1],            */
+/* ascending; shared_lens: int32 [n_groups] (both device). seq_lens[b] == 0 gives out = 0.      */
+/* workspace: qd_attn_shared_workspace_bytes(...) bytes, zero-filled before its first use.       */
+/* Limits: as qd_attn_prompt, n_groups <= 1024, batch <= 65535.                                 */
+size_t qd_attn_shared_workspace_bytes(int batch, int n_q_heads, int n_kv_heads);
+int qd_attn_decode_shared(const void* q, int q_is_f32, int64_t q_stride, const void* k_pages, const void* v_pages,
+                          const int32_t* page_table, const int32_t* seq_lens, const int32_t* cu_seqs,
+                          const int32_t* shared_lens, int n_groups, int batch, int n_q_heads, int n_kv_heads,
+                          int head_dim, int page_size, int max_pages, int n_pages, float scale, void* out,
+                          void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Page operations on the K/V cache ([KL-PAGED]: fixed physical pages behind a      */
+/* page table). The state is in device memory, owned by the caller:                 */
+/*   page_table int32 [max_seqs, max_pages]: the pages of each sequence in order,     */
+/*     -1 past its last;  seq_lens int32 [max_seqs]: its tokens;                        */
+/*   refs int32 [n_pages]: how many page-table entries name the page (0: free).          */
+/* New pages are the lowest free ids, taken in sequence order, so a call's result           */
+/* follows from its arguments alone. A call that cannot be carried out whole changes         */
+/* nothing and sets QD_DEVERR_CACHE.                                                          */
+/* k_cache, v_cache: host arrays of n_layers device pointers, each [n_pages,                  */
+/* n_kv_heads, page_size, head_dim] bf16. workspace: qd_pages_workspace_bytes(cache)            */
+/* bytes, zero-filled before its first use. 4-byte alignment for the int32 arrays.              */
+/* Limits: head_dim % 8 == 0, max_seqs <= 2048.                                                 */
+typedef struct {
+  void* const* k_cache;
+  void* const* v_cache;
+  int n_layers, n_kv_heads, page_size, head_dim, n_pages;
+  int32_t* page_table;
+  int32_t* seq_lens;
+  int32_t* refs;
+  int max_seqs, max_pages;
+  void* workspace;
+  size_t workspace_bytes;
+} qd_page_cache;
+size_t qd_pages_workspace_bytes(const qd_page_cache* cache);
+/* K and V of page src[i] to page dst[i], i < n, in every layer (src, dst: int32 [n],     */
+/* device). A pair with a negative id is skipped. No page may be a destination twice, or    */
+/* both a source and a destination of different pairs (the contents of those pages would     */
+/* depend on the order of the copies). Uses neither the state nor the workspace.              */
+int qd_pages_copy(const qd_page_cache* cache, const int32_t* src, const int32_t* dst, int n, cudaStream_t stream);
+/* Sequence children[i] becomes a copy of sequence parents[i] (as it was before the         */
+/* call), i < n (int32 [n], device): the page-table row and the length; every page is        */
+/* shared, the partly filled last one too (qd_pages_extend gives the writer its own).         */
+/* Children must be empty (length 0) and named once, and not be their own parent.             */
+int qd_pages_fork(const qd_page_cache* cache, const int32_t* parents, const int32_t* children, int n,
+                  cudaStream_t stream);
+/* Room for n_new[s] more tokens (int32 [max_seqs], device; <= 0: none): seq_lens[s] +=         */
+/* n_new[s], new pages for them, and where the sequence's partly filled last page is shared       */
+/* a copy of that page (of the sequences that are extended in one call, the last one in         */
+/* sequence order keeps the page if nobody else names it). The tokens' K/V are the caller's    */
+/* to write (the decode step, qd_prefill).                                                    */
+int qd_pages_extend(const qd_page_cache* cache, const int32_t* n_new, cudaStream_t stream);
+/* Sequence s cut to new_lens[s] tokens (int32 [max_seqs], device; negative or not below          */
+/* its length: unchanged; 0 frees it): pages past the new length lose a reference.                 */
+int qd_pages_trim(const qd_page_cache* cache, const int32_t* new_lens, cudaStream_t stream);
+/* Moves the pages in use to the ids 0 .. n_live - 1 (those above go, in ascending order, to      */
+/* the free ids below), with the page tables and counts; n_live: int32 [1], device.                */
+int qd_pages_compact(const qd_page_cache* cache, int32_t* n_live, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Greedy argmax + on-device advance ([KL-DEC] "LM-head GEMV + argmax +        */
@@ -355,6 +456,31 @@ int qd_graph_destroy(qd_graph* g);
 size_t qd_verify_workspace_bytes(const qd_step_args* args, int k);
 int qd_verify_step(const qd_step_args* args, const int32_t* draft, int k, float* logits, int32_t* target,
                    int32_t* n_accept, cudaStream_t stream);
+
+/* Sampled verification of drafted tokens, beside qd_verify_step's greedy rule, for a    */
+/* batch: sequence b has n = n_draft[b] drafts (n_draft NULL: k - 1 each) draft[b, i]     */
+/* drawn from draft_probs[b, i, :]; target_probs[b, i, :] is the target's distribution     */
+/* after draft i - 1. Draft i is accepted while                                             */
+/*   u[b, i] * draft_probs[b, i, draft[b, i]] < target_probs[b, i, draft[b, i]];             */
+/* with m accepted, the next token t is the least index whose running sum of r passes         */
+/* u[b, k - 1] times the sum of r, r = max(target_probs[b, m, :] - draft_probs[b, m, :], 0)    */
+/* if m < n (target_probs[b, m, :] if that is zero everywhere), r = target_probs[b, n, :] if    */
+/* m == n. Entries of r that are not finite count as 0; a row without mass gives 0 and sets       */
+/* QD_DEVERR_NAN; a draft outside the vocabulary is rejected; n_draft outside 0 .. k - 1 is        */
+/* clamped and sets QD_DEVERR_POS. Sums in 48 bits or more. The state advances as in                */
+/* qd_verify_step: n_accept[b] = m; out_tokens[b, step ..] = the m drafts, t; tok = t;               */
+/* pos += m + 1; step += m + 1 (past max_steps: QD_DEVERR_STEPS).                                    */
+/* target_probs: f32, row (b, i) at (b * k + i) * target_stride; draft_probs: f32, row (b, i) at       */
+/* (b * (k - 1) + i) * draft_stride (may be NULL with draft when k == 1); draft: int32 [batch,          */
+/* k - 1]; u: f32 [batch, k] in [0, 1); n_accept: int32 [batch]; all device. workspace:                  */
+/* qd_verify_sample_workspace_bytes(batch) bytes, zero-filled before its first use. Limits:              */
+/* 1 <= k <= 1024, vocab <= 4194304, batch <= 65535.                                                     */
+size_t qd_verify_sample_workspace_bytes(int batch);
+int qd_verify_sample(const float* target_probs, int64_t target_stride, const float* draft_probs,
+                     int64_t draft_stride, const int32_t* draft, const int32_t* n_draft, const float* u, int vocab,
+                     int batch, int k, int32_t* tok, int32_t* pos, int32_t* step, int32_t* out_tokens,
+                     int max_steps, int32_t* n_accept, void* workspace, size_t workspace_bytes,
+                     cudaStream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Prefill ("qwen3-8b-rtx4080-cutedsl" README, "Flash Attention 2" and           */

@@ -21,12 +21,13 @@ HEADER = os.path.join(os.path.dirname(_HERE), "include", "qd.h")
 QD_OK = 0
 QD_W_BF16, QD_W_Q8_0, QD_W_INT4 = 0, 1, 2
 QD_ACT_F32, QD_ACT_I8 = 0, 1
-DEVERR = {1: "page", 2: "pos", 4: "nan", 8: "steps", 16: "timeout"}
+DEVERR = {1: "page", 2: "pos", 4: "nan", 8: "steps", 16: "timeout", 32: "cache"}
 
 _vp = C.c_void_p
 _i = C.c_int
 _f = C.c_float
 _sz = C.c_size_t
+_l = C.c_int64
 
 
 class LayerDims(C.Structure):
@@ -52,6 +53,13 @@ class StepArgs(C.Structure):
                 ("lm_wtype", _i), ("top_k", _i), ("topk_ids", _vp), ("topk_vals", _vp)]
 
 
+class PageCacheArgs(C.Structure):
+    _fields_ = [("k_cache", _vp), ("v_cache", _vp),
+                ("n_layers", _i), ("n_kv_heads", _i), ("page_size", _i), ("head_dim", _i), ("n_pages", _i),
+                ("page_table", _vp), ("seq_lens", _vp), ("refs", _vp), ("max_seqs", _i), ("max_pages", _i),
+                ("workspace", _vp), ("workspace_bytes", _sz)]
+
+
 _SIGS = {
     "qd_last_error": (C.c_char_p, []),
     "qd_version": (_i, []),
@@ -66,6 +74,18 @@ _SIGS = {
     "qd_attn_workspace_bytes": (_sz, [_i, _i, _i, _i]),
     "qd_attn_decode_paged": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _vp, _vp, _sz, _vp]),
     "qd_attn_decode_paged_noalloc": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _vp, _vp]),
+    "qd_attn_prompt_workspace_bytes": (_sz, []),
+    "qd_attn_prompt": (_i, [_vp, _i, _l] + [_vp] * 5 + [_i] * 8 + [_f, _vp, _vp, _sz, _vp]),
+    "qd_attn_shared_workspace_bytes": (_sz, [_i, _i, _i]),
+    "qd_attn_decode_shared": (_i, [_vp, _i, _l] + [_vp] * 6 + [_i] * 8 + [_f, _vp, _vp, _sz, _vp]),
+    "qd_pages_workspace_bytes": (_sz, [C.POINTER(PageCacheArgs)]),
+    "qd_pages_copy": (_i, [C.POINTER(PageCacheArgs), _vp, _vp, _i, _vp]),
+    "qd_pages_fork": (_i, [C.POINTER(PageCacheArgs), _vp, _vp, _i, _vp]),
+    "qd_pages_extend": (_i, [C.POINTER(PageCacheArgs), _vp, _vp]),
+    "qd_pages_trim": (_i, [C.POINTER(PageCacheArgs), _vp, _vp]),
+    "qd_pages_compact": (_i, [C.POINTER(PageCacheArgs), _vp, _vp]),
+    "qd_verify_sample_workspace_bytes": (_sz, [_i]),
+    "qd_verify_sample": (_i, [_vp, _l, _vp, _l, _vp, _vp, _vp, _i, _i, _i] + [_vp] * 4 + [_i, _vp, _vp, _sz, _vp]),
     "qd_argmax_workspace_bytes": (_sz, [_i]),
     "qd_argmax_advance": (_i, [_vp, _i, _i, _vp, _vp, _vp, _vp, _i, _vp, _sz, _vp]),
     "qd_rope_table_init": (_i, [_vp, _i, _i, _f, _vp]),
@@ -244,6 +264,234 @@ def attn_decode_paged_noalloc(q, k_pages, v_pages, page_table, seq_lens, scale, 
                                               Hq, Hkv, D, ps, page_table.shape[1], n_pages, float(scale), _p(out),
                                               _stream(stream)))
     return out
+
+
+def _on(t, stream):
+    """The device of t current, and `stream` (its current stream by default) with it, so that
+    what a call allocates belongs to the stream that its kernels run on."""
+    if stream is None or stream == torch.cuda.current_stream(t.device):
+        return torch.cuda.device(t.device)
+    return torch.cuda.stream(stream)
+
+
+def _want(name, t, dtype, dims, device, shape=None):
+    """Refuses a tensor that the C entry could not take as it is (contiguous, on `device`)."""
+    if t.device != device or device.type != "cuda":
+        raise ValueError(f"{name}: on {t.device}, expected {device} (a CUDA device)")
+    if t.dtype != dtype or t.dim() != dims or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dims}-dimensional {dtype} tensor, got {t.dtype} {tuple(t.shape)}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _rows(fn, q, k_pages, v_pages, page_table, seq_lens, cu, out):
+    """The common checks of attn_prompt and attn_decode_shared."""
+    if q.dim() != 3 or q.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{fn}: q must be [rows, heads, head_dim] in float32 or bfloat16")
+    if q.shape[0] and (q.stride(2) != 1 or q.stride(1) != q.shape[2]):
+        raise ValueError(f"{fn}: a row's heads must be contiguous (strides {q.stride()})")
+    _want(f"{fn}: k_pages", k_pages, torch.bfloat16, 4, q.device)
+    _want(f"{fn}: v_pages", v_pages, torch.bfloat16, 4, q.device, k_pages.shape)
+    if k_pages.shape[3] != q.shape[2]:
+        raise ValueError(f"{fn}: head_dim {q.shape[2]} and {k_pages.shape[3]}")
+    _want(f"{fn}: page_table", page_table, torch.int32, 2, q.device)
+    _want(f"{fn}: seq_lens", seq_lens, torch.int32, 1, q.device, page_table.shape[:1])
+    _want(f"{fn}: segment starts", cu, torch.int32, 1, q.device)
+    if out is not None:
+        _want(f"{fn}: out", out, q.dtype, 3, q.device, q.shape)
+    return q.stride(0) if q.shape[0] > 1 else q.shape[1] * q.shape[2]
+
+
+def _scratch(fn, workspace, nbytes, device):
+    if workspace is None:
+        return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    _want(f"{fn}: workspace", workspace, torch.uint8, 1, device)
+    return workspace
+
+
+def attn_prompt_workspace_bytes() -> int:
+    return int(lib().qd_attn_prompt_workspace_bytes())
+
+
+def attn_prompt(q, k_pages, v_pages, page_table, cu_rows, seq_lens, scale, out=None, workspace=None, stream=None):
+    """Causal attention over the packed rows of several prompts: q f32 or bf16 [rows, Hq, D] (rows may be
+    strided), sequence b's rows cu_rows[b] .. cu_rows[b + 1), the last of them at position seq_lens[b] - 1;
+    caches bf16 [n_pages, Hkv, ps, D] with the rows' K/V written. -> [rows, Hq, D] of q's type."""
+    q_stride = _rows("attn_prompt", q, k_pages, v_pages, page_table, seq_lens, cu_rows, out)
+    n, Hq, D = q.shape
+    B, max_pages = page_table.shape
+    n_pages, Hkv, ps, _ = k_pages.shape
+    if cu_rows.numel() != B + 1:
+        raise ValueError(f"attn_prompt: {cu_rows.numel()} segment starts for {B} sequences")
+    with _on(q, stream):
+        if out is None:
+            out = torch.empty((n, Hq, D), dtype=q.dtype, device=q.device)
+        if n == 0:
+            return out
+        workspace = _scratch("attn_prompt", workspace, attn_prompt_workspace_bytes(), q.device)
+        _check(lib().qd_attn_prompt(_p(q), int(q.dtype == torch.float32), q_stride, _p(k_pages), _p(v_pages),
+                                    _p(page_table), _p(cu_rows), _p(seq_lens), B, n, Hq, Hkv, D, ps, max_pages,
+                                    n_pages, float(scale), _p(out), _p(workspace), workspace.numel(),
+                                    _stream(stream)))
+    return out
+
+
+def attn_shared_workspace_bytes(batch: int, hq: int, hkv: int) -> int:
+    return int(lib().qd_attn_shared_workspace_bytes(batch, hq, hkv))
+
+
+def attn_decode_shared(q, k_pages, v_pages, page_table, seq_lens, cu_seqs, shared_lens, scale, out=None,
+                       workspace=None, stream=None):
+    """attn_decode_paged for sequences that share prefixes: group i is the sequences cu_seqs[i] ..
+    cu_seqs[i + 1), whose first shared_lens[i] tokens lie in the same pages (read once per group).
+    q f32 or bf16 [B, Hq, D] -> [B, Hq, D] of q's type."""
+    q_stride = _rows("attn_decode_shared", q, k_pages, v_pages, page_table, seq_lens, cu_seqs, out)
+    B, Hq, D = q.shape
+    n_pages, Hkv, ps, _ = k_pages.shape
+    _want("attn_decode_shared: shared_lens", shared_lens, torch.int32, 1, q.device)
+    if page_table.shape[0] != B or cu_seqs.numel() != shared_lens.numel() + 1:
+        raise ValueError(f"attn_decode_shared: {page_table.shape[0]} page tables for {B} rows, {cu_seqs.numel()} "
+                         f"group starts for {shared_lens.numel()} lengths")
+    with _on(q, stream):
+        if out is None:
+            out = torch.empty((B, Hq, D), dtype=q.dtype, device=q.device)
+        if B == 0:
+            return out
+        workspace = _scratch("attn_decode_shared", workspace, attn_shared_workspace_bytes(B, Hq, Hkv), q.device)
+        _check(lib().qd_attn_decode_shared(_p(q), int(q.dtype == torch.float32), q_stride, _p(k_pages), _p(v_pages),
+                                           _p(page_table), _p(seq_lens), _p(cu_seqs), _p(shared_lens),
+                                           shared_lens.numel(), B, Hq, Hkv, D, ps, page_table.shape[1], n_pages,
+                                           float(scale), _p(out), _p(workspace), workspace.numel(),
+                                           _stream(stream)))
+    return out
+
+
+def verify_sample_workspace_bytes(batch: int) -> int:
+    return int(lib().qd_verify_sample_workspace_bytes(batch))
+
+
+def verify_sample(target_probs, draft_probs, draft, u, tok, pos, step, out_tokens, n_draft=None, n_accept=None,
+                  workspace=None, stream=None):
+    """Sampled verification of drafts: target_probs f32 [B, k, V], draft_probs f32 [B, k - 1, V] (rows may be
+    padded), draft int32 [B, k - 1], u f32 [B, k]. Advances tok, pos, step [B] and out_tokens [B, max_steps] and
+    returns n_accept int32 [B]."""
+    fn = "verify_sample"
+    if target_probs.dim() != 3 or target_probs.dtype != torch.float32:
+        raise ValueError(f"{fn}: target_probs must be float32 [B, k, V]")
+    B, k, V = target_probs.shape
+    dev = target_probs.device
+
+    def stride(name, t, rows):
+        if t.device != dev or t.dtype != torch.float32 or tuple(t.shape) != (B, rows, V):
+            raise ValueError(f"{fn}: {name} must be float32 {(B, rows, V)} on {dev}")
+        s = t.stride(1) if rows > 1 else (t.stride(0) if B > 1 else V)
+        if t.numel() and (t.stride(2) != 1 and V > 1 or (B > 1 and t.stride(0) != rows * s)):
+            raise ValueError(f"{fn}: {name}'s rows must be evenly spaced (strides {t.stride()})")
+        return s
+
+    t_stride = stride("target_probs", target_probs, k)
+    d_stride = stride("draft_probs", draft_probs, k - 1) if k > 1 else V
+    if k > 1:
+        _want(f"{fn}: draft", draft, torch.int32, 2, dev, (B, k - 1))
+    _want(f"{fn}: u", u, torch.float32, 2, dev, (B, k))
+    for name, t in (("tok", tok), ("pos", pos), ("step", step), ("n_draft", n_draft), ("n_accept", n_accept)):
+        if t is not None:
+            _want(f"{fn}: {name}", t, torch.int32, 1, dev, (B,))
+    _want(f"{fn}: out_tokens", out_tokens, torch.int32, 2, dev)
+    if out_tokens.shape[0] != B:
+        raise ValueError(f"{fn}: out_tokens has {out_tokens.shape[0]} rows for {B} sequences")
+    with _on(target_probs, stream):
+        if n_accept is None:
+            n_accept = torch.empty(B, dtype=torch.int32, device=dev)
+        if B == 0:
+            return n_accept
+        workspace = _scratch(fn, workspace, verify_sample_workspace_bytes(B), dev)
+        _check(lib().qd_verify_sample(_p(target_probs), t_stride, _p(draft_probs) if k > 1 else None, d_stride,
+                                      _p(draft) if k > 1 else None, _p(n_draft), _p(u), V, B, k, _p(tok), _p(pos),
+                                      _p(step), _p(out_tokens), out_tokens.shape[1], _p(n_accept), _p(workspace),
+                                      workspace.numel(), _stream(stream)))
+    return n_accept
+
+
+class PageCache:
+    """Page operations on the K/V caches of all layers (bf16 [n_pages, Hkv, ps, D] each).
+
+    ``page_table`` int32 [max_seqs, max_pages] (-1 past a sequence's pages), ``seq_lens`` int32
+    [max_seqs] and ``refs`` int32 [n_pages] (how many entries name each page, 0: free) are the
+    state, device tensors that the calls update; without them only ``copy`` works. ``empty``
+    makes the state of an empty cache. One PageCache serves one stream at a time.
+    """
+
+    def __init__(self, k_cache, v_cache, page_table=None, seq_lens=None, refs=None):
+        if not k_cache or len(k_cache) != len(v_cache):
+            raise ValueError(f"PageCache: {len(k_cache)} K and {len(v_cache)} V caches")
+        self.k_cache, self.v_cache = list(k_cache), list(v_cache)
+        first = self.k_cache[0]
+        for t in self.k_cache + self.v_cache:
+            _want("PageCache: a cache", t, torch.bfloat16, 4, first.device, first.shape)
+        self.device = first.device
+        L = len(self.k_cache)
+        a = PageCacheArgs()
+        self._k_arr = (_vp * L)(*[_p(t) for t in self.k_cache])
+        self._v_arr = (_vp * L)(*[_p(t) for t in self.v_cache])
+        a.k_cache, a.v_cache = C.cast(self._k_arr, _vp), C.cast(self._v_arr, _vp)
+        a.n_layers = L
+        a.n_pages, a.n_kv_heads, a.page_size, a.head_dim = first.shape
+        self.page_table, self.seq_lens, self.refs = page_table, seq_lens, refs
+        if page_table is not None:
+            _want("PageCache: page_table", page_table, torch.int32, 2, self.device)
+            _want("PageCache: seq_lens", seq_lens, torch.int32, 1, self.device, page_table.shape[:1])
+            _want("PageCache: refs", refs, torch.int32, 1, self.device, first.shape[:1])
+            a.page_table, a.seq_lens, a.refs = _p(page_table), _p(seq_lens), _p(refs)
+            a.max_seqs, a.max_pages = page_table.shape
+            self.workspace = torch.zeros(int(lib().qd_pages_workspace_bytes(C.byref(a))), dtype=torch.uint8,
+                                         device=self.device)
+            a.workspace, a.workspace_bytes = _p(self.workspace), self.workspace.numel()
+        self.args = a
+
+    @classmethod
+    def empty(cls, k_cache, v_cache, max_seqs: int, max_pages: int):
+        dev = k_cache[0].device
+        return cls(k_cache, v_cache, torch.full((max_seqs, max_pages), -1, dtype=torch.int32, device=dev),
+                   torch.zeros(max_seqs, dtype=torch.int32, device=dev),
+                   torch.zeros(k_cache[0].shape[0], dtype=torch.int32, device=dev))
+
+    def _list(self, name, t, n=None):
+        _want(f"PageCache.{name}", t, torch.int32, 1, self.device, None if n is None else (n,))
+        return _p(t)
+
+    def copy(self, src, dst, stream=None):
+        """Page src[i] to page dst[i] in every layer's K and V (device int32 lists)."""
+        s, d = self._list("copy: src", src), self._list("copy: dst", dst, src.numel())
+        with _on(self.k_cache[0], stream):
+            _check(lib().qd_pages_copy(C.byref(self.args), s, d, src.numel(), _stream(stream)))
+
+    def fork(self, parents, children, stream=None):
+        """Sequence children[i] (empty) becomes a copy of parents[i], its pages shared."""
+        a, b = self._list("fork: parents", parents), self._list("fork: children", children, parents.numel())
+        with _on(self.k_cache[0], stream):
+            _check(lib().qd_pages_fork(C.byref(self.args), a, b, parents.numel(), _stream(stream)))
+
+    def extend(self, n_new, stream=None):
+        """Pages for n_new[s] more tokens of each sequence; shared partial pages are copied."""
+        n = self._list("extend: n_new", n_new, self.args.max_seqs)
+        with _on(self.k_cache[0], stream):
+            _check(lib().qd_pages_extend(C.byref(self.args), n, _stream(stream)))
+
+    def trim(self, new_lens, stream=None):
+        """Sequence s cut to new_lens[s] tokens (negative: unchanged; 0 frees it)."""
+        n = self._list("trim: new_lens", new_lens, self.args.max_seqs)
+        with _on(self.k_cache[0], stream):
+            _check(lib().qd_pages_trim(C.byref(self.args), n, _stream(stream)))
+
+    def compact(self, n_live=None, stream=None):
+        """The pages in use moved to the lowest ids; returns their number (device int32 [1])."""
+        with _on(self.k_cache[0], stream):
+            if n_live is None:
+                n_live = torch.empty(1, dtype=torch.int32, device=self.device)
+            p = self._list("compact: n_live", n_live, 1)
+            _check(lib().qd_pages_compact(C.byref(self.args), p, _stream(stream)))
+        return n_live
 
 
 def argmax_advance(logits, tok, pos, step, out_tokens, workspace=None, stream=None):

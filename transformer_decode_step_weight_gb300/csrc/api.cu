@@ -415,6 +415,192 @@ int qd_attn_decode_paged_noalloc(const float* q, const void* k_pages, const void
   return e == cudaSuccess ? QD_OK : cuda_fail(e, "qd_attn_decode_paged_noalloc");
 }
 
+// ------------------------------------------------------------------ packed rows
+size_t qd_attn_prompt_workspace_bytes(void) { return attn_rows_workspace_bytes(); }
+
+size_t qd_attn_shared_workspace_bytes(int batch, int n_q_heads, int n_kv_heads) {
+  if (batch < 1 || n_kv_heads < 1 || n_q_heads < n_kv_heads) return 0;
+  return attn_shared_workspace_bytes(batch, n_q_heads, n_kv_heads);
+}
+
+// The checks that qd_attn_prompt and qd_attn_decode_shared have in common; fills a.
+static int check_attn_rows(const char* fn, AttnRowsArgs& a, const void* q, int q_is_f32, int64_t q_stride,
+                           const void* k_pages, const void* v_pages, const int32_t* page_table, const int32_t* cu,
+                           const int32_t* seq_lens, int n_seg, int n_rows, int hq, int hkv, int hd, int ps,
+                           int max_pages, int n_pages, float scale, void* out, void* workspace,
+                           size_t workspace_bytes, size_t need) {
+  int rc = check_attn_shape(fn, n_seg, hq, hkv, hd, ps, max_pages, n_pages);
+  if (rc) return rc;
+  if (n_rows < 1) return fail(QD_ERR_INVALID_ARG, "%s: rows=%d", fn, n_rows);
+  if (n_seg > 1024 || n_rows > (1 << 20))
+    return fail(QD_ERR_UNSUPPORTED, "%s: %d sequences or groups (at most 1024), %d rows (at most 2^20)", fn, n_seg, n_rows);
+  if (!q || !k_pages || !v_pages || !page_table || !cu || !seq_lens || !out || !workspace)
+    return fail(QD_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if (q_is_f32 != 0 && q_is_f32 != 1) return fail(QD_ERR_INVALID_ARG, "%s: q_is_f32=%d", fn, q_is_f32);
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) || !aligned16(workspace))
+    return fail(QD_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
+  if (q_stride < (int64_t)hq * hd || q_stride % (q_is_f32 ? 4 : 8) || q_stride > ((int64_t)1 << 40))
+    return fail(QD_ERR_INVALID_ARG, "%s: q_stride=%lld", fn, (long long)q_stride);
+  if ((int64_t)n_pages * hkv * ps > INT32_MAX)
+    return fail(QD_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 (page, kv head, slot) rows in the cache", fn);
+  if (q == out) return fail(QD_ERR_INVALID_ARG, "%s: out must not be q", fn);
+  if (!std::isfinite(scale)) return fail(QD_ERR_INVALID_ARG, "%s: scale not finite", fn);
+  if (workspace_bytes < need) return fail(QD_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, workspace_bytes, need);
+  a.q = q; a.q_f32 = q_is_f32; a.q_stride = q_stride; a.k_pages = k_pages; a.v_pages = v_pages;
+  a.page_table = page_table; a.cu = cu; a.seq_lens = seq_lens; a.n_seg = n_seg; a.n_rows = n_rows;
+  a.Hq = hq; a.Hkv = hkv; a.page_size = ps; a.max_pages = max_pages; a.n_pages = n_pages; a.scale = scale;
+  a.out = out; a.workspace = workspace;
+  return QD_OK;
+}
+
+int qd_attn_prompt(const void* q, int q_is_f32, int64_t q_stride, const void* k_pages, const void* v_pages,
+                   const int32_t* page_table, const int32_t* cu_rows, const int32_t* seq_lens, int batch, int n_rows,
+                   int n_q_heads, int n_kv_heads, int head_dim, int page_size, int max_pages, int n_pages,
+                   float scale, void* out, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  AttnRowsArgs a = {};
+  const int rc = check_attn_rows("qd_attn_prompt", a, q, q_is_f32, q_stride, k_pages, v_pages, page_table, cu_rows,
+                                 seq_lens, batch, n_rows, n_q_heads, n_kv_heads, head_dim, page_size, max_pages,
+                                 n_pages, scale, out, workspace, workspace_bytes, attn_rows_workspace_bytes());
+  if (rc) return rc;
+  cudaError_t e = launch_attn_prompt(a, make_launch(stream, false));
+  return e == cudaSuccess ? QD_OK : cuda_fail(e, "qd_attn_prompt");
+}
+
+int qd_attn_decode_shared(const void* q, int q_is_f32, int64_t q_stride, const void* k_pages, const void* v_pages,
+                          const int32_t* page_table, const int32_t* seq_lens, const int32_t* cu_seqs,
+                          const int32_t* shared_lens, int n_groups, int batch, int n_q_heads, int n_kv_heads,
+                          int head_dim, int page_size, int max_pages, int n_pages, float scale, void* out,
+                          void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  AttnRowsArgs a = {};
+  const int rc = check_attn_rows("qd_attn_decode_shared", a, q, q_is_f32, q_stride, k_pages, v_pages, page_table,
+                                 cu_seqs, seq_lens, n_groups, batch, n_q_heads, n_kv_heads, head_dim, page_size,
+                                 max_pages, n_pages, scale, out, workspace, workspace_bytes,
+                                 qd_attn_shared_workspace_bytes(batch, n_q_heads, n_kv_heads));
+  if (rc) return rc;
+  if (!shared_lens) return fail(QD_ERR_INVALID_ARG, "qd_attn_decode_shared: null pointer");
+  if (batch > 65535) return fail(QD_ERR_UNSUPPORTED, "qd_attn_decode_shared: batch=%d (at most 65535)", batch);
+  a.shared_lens = shared_lens;
+  cudaError_t e = launch_attn_shared(a, make_launch(stream, true));
+  return e == cudaSuccess ? QD_OK : cuda_fail(e, "qd_attn_decode_shared");
+}
+
+// ------------------------------------------------------------------ cache pages
+static int check_page_cache(const char* fn, const qd_page_cache* c, bool copies, bool state) {
+  if (!c) return fail(QD_ERR_INVALID_ARG, "%s: null cache", fn);
+  if (c->n_pages < 1) return fail(QD_ERR_INVALID_ARG, "%s: n_pages=%d", fn, c->n_pages);
+  if (copies) {
+    if (!c->k_cache || !c->v_cache || c->n_layers < 1 || c->n_kv_heads < 1 || c->page_size < 1 || c->head_dim < 1)
+      return fail(QD_ERR_INVALID_ARG, "%s: null caches or bad sizes (layers=%d kv_heads=%d page_size=%d head_dim=%d)", fn,
+                  c->n_layers, c->n_kv_heads, c->page_size, c->head_dim);
+    if (c->head_dim % 8) return fail(QD_ERR_UNSUPPORTED, "%s: head_dim=%d (a multiple of 8)", fn, c->head_dim);
+    for (int i = 0; i < c->n_layers; ++i)
+      if (!c->k_cache[i] || !c->v_cache[i] || !aligned16(c->k_cache[i]) || !aligned16(c->v_cache[i]))
+        return fail(QD_ERR_INVALID_ARG, "%s: layer %d's cache is null or not 16-byte aligned", fn, i);
+  }
+  if (state) {
+    if (!c->page_table || !c->seq_lens || !c->refs || !c->workspace)
+      return fail(QD_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (c->max_seqs < 1 || c->max_pages < 1 || c->page_size < 1 || (long long)c->max_pages * c->page_size > (1LL << 30))
+      return fail(QD_ERR_INVALID_ARG, "%s: max_seqs=%d max_pages=%d page_size=%d", fn, c->max_seqs, c->max_pages,
+                  c->page_size);
+    if (c->max_seqs > kPagesMaxSeqs)
+      return fail(QD_ERR_UNSUPPORTED, "%s: max_seqs=%d (at most %d)", fn, c->max_seqs, kPagesMaxSeqs);
+    if (!aligned16(c->workspace)) return fail(QD_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", fn);
+    if (c->workspace_bytes < pages_workspace_bytes(c->max_seqs, c->n_pages))
+      return fail(QD_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, c->workspace_bytes,
+                  pages_workspace_bytes(c->max_seqs, c->n_pages));
+  }
+  return QD_OK;
+}
+
+static PageState page_state(const qd_page_cache* c) {
+  return PageState{c->page_table, c->seq_lens, c->refs, c->max_seqs, c->max_pages, c->page_size, c->n_pages};
+}
+static PageCopy page_copy(const qd_page_cache* c) {
+  return PageCopy{c->k_cache, c->v_cache, c->n_layers, (size_t)c->n_kv_heads * c->page_size * c->head_dim * 2};
+}
+
+size_t qd_pages_workspace_bytes(const qd_page_cache* c) {
+  if (!c || c->max_seqs < 1 || c->n_pages < 1) return 0;
+  return pages_workspace_bytes(c->max_seqs, c->n_pages);
+}
+
+int qd_pages_copy(const qd_page_cache* c, const int32_t* src, const int32_t* dst, int n, cudaStream_t stream) {
+  const int rc = check_page_cache("qd_pages_copy", c, true, false);
+  if (rc) return rc;
+  if (n < 0 || (n > 0 && (!src || !dst))) return fail(QD_ERR_INVALID_ARG, "qd_pages_copy: n=%d or a null list", n);
+  if (n == 0) return QD_OK;
+  cudaError_t e = launch_pages_copy(page_copy(c), src, dst, n, c->n_pages, make_launch(stream, false));
+  return e == cudaSuccess ? QD_OK : cuda_fail(e, "qd_pages_copy");
+}
+
+int qd_pages_fork(const qd_page_cache* c, const int32_t* parents, const int32_t* children, int n,
+                  cudaStream_t stream) {
+  const int rc = check_page_cache("qd_pages_fork", c, false, true);
+  if (rc) return rc;
+  if (n < 0 || (n > 0 && (!parents || !children)))
+    return fail(QD_ERR_INVALID_ARG, "qd_pages_fork: n=%d or a null list", n);
+  if (n > c->max_seqs) return fail(QD_ERR_INVALID_ARG, "qd_pages_fork: n=%d children of %d sequences", n, c->max_seqs);
+  if (n == 0) return QD_OK;
+  cudaError_t e = launch_pages_fork(page_state(c), parents, children, n, c->workspace, make_launch(stream, false));
+  return e == cudaSuccess ? QD_OK : cuda_fail(e, "qd_pages_fork");
+}
+
+int qd_pages_extend(const qd_page_cache* c, const int32_t* n_new, cudaStream_t stream) {
+  const int rc = check_page_cache("qd_pages_extend", c, true, true);
+  if (rc) return rc;
+  if (!n_new) return fail(QD_ERR_INVALID_ARG, "qd_pages_extend: null pointer");
+  cudaError_t e = launch_pages_extend(page_state(c), page_copy(c), n_new, c->workspace, make_launch(stream, false));
+  return e == cudaSuccess ? QD_OK : cuda_fail(e, "qd_pages_extend");
+}
+
+int qd_pages_trim(const qd_page_cache* c, const int32_t* new_lens, cudaStream_t stream) {
+  const int rc = check_page_cache("qd_pages_trim", c, false, true);
+  if (rc) return rc;
+  if (!new_lens) return fail(QD_ERR_INVALID_ARG, "qd_pages_trim: null pointer");
+  cudaError_t e = launch_pages_trim(page_state(c), new_lens, make_launch(stream, false));
+  return e == cudaSuccess ? QD_OK : cuda_fail(e, "qd_pages_trim");
+}
+
+int qd_pages_compact(const qd_page_cache* c, int32_t* n_live, cudaStream_t stream) {
+  const int rc = check_page_cache("qd_pages_compact", c, true, true);
+  if (rc) return rc;
+  if (!n_live) return fail(QD_ERR_INVALID_ARG, "qd_pages_compact: null pointer");
+  cudaError_t e = launch_pages_compact(page_state(c), page_copy(c), n_live, c->workspace, make_launch(stream, false));
+  return e == cudaSuccess ? QD_OK : cuda_fail(e, "qd_pages_compact");
+}
+
+// ------------------------------------------------------------------ sampled verification
+size_t qd_verify_sample_workspace_bytes(int batch) { return batch < 1 ? 0 : verify_sample_workspace_bytes(batch); }
+
+int qd_verify_sample(const float* target_probs, int64_t target_stride, const float* draft_probs,
+                     int64_t draft_stride, const int32_t* draft, const int32_t* n_draft, const float* u, int vocab,
+                     int batch, int k, int32_t* tok, int32_t* pos, int32_t* step, int32_t* out_tokens,
+                     int max_steps, int32_t* n_accept, void* workspace, size_t workspace_bytes,
+                     cudaStream_t stream) {
+  if (vocab < 1 || batch < 1 || k < 1 || max_steps < 1)
+    return fail(QD_ERR_INVALID_ARG, "qd_verify_sample: vocab=%d batch=%d k=%d max_steps=%d", vocab, batch, k, max_steps);
+  if (vocab > verify_sample_max_vocab() || batch > 65535 || k > 1024)
+    return fail(QD_ERR_UNSUPPORTED, "qd_verify_sample: vocab=%d (at most %d) batch=%d (65535) k=%d (1024)", vocab,
+                verify_sample_max_vocab(), batch, k);
+  if (!target_probs || !u || !tok || !pos || !step || !out_tokens || !n_accept || !workspace ||
+      (k > 1 && (!draft_probs || !draft)))
+    return fail(QD_ERR_INVALID_ARG, "qd_verify_sample: null pointer");
+  if (target_stride < vocab || (k > 1 && draft_stride < vocab))
+    return fail(QD_ERR_INVALID_ARG, "qd_verify_sample: a row stride below the vocabulary");
+  if (!aligned16(workspace)) return fail(QD_ERR_INVALID_ARG, "qd_verify_sample: workspace must be 16-byte aligned");
+  if (workspace_bytes < verify_sample_workspace_bytes(batch))
+    return fail(QD_ERR_WORKSPACE, "qd_verify_sample: workspace %zu < %zu bytes", workspace_bytes,
+                verify_sample_workspace_bytes(batch));
+  VerifySampleArgs a = {};
+  a.target = target_probs; a.t_stride = target_stride; a.draft_probs = draft_probs; a.d_stride = draft_stride;
+  a.draft = draft; a.n_draft = n_draft; a.u = u; a.V = vocab; a.B = batch; a.k = k;
+  a.tok = tok; a.pos = pos; a.step = step; a.out_tokens = out_tokens; a.max_steps = max_steps;
+  a.n_accept = n_accept; a.workspace = workspace;
+  cudaError_t e = launch_verify_sample(a, make_launch(stream, false));
+  return e == cudaSuccess ? QD_OK : cuda_fail(e, "qd_verify_sample");
+}
+
 // ------------------------------------------------------------------ argmax
 size_t qd_argmax_workspace_bytes(int batch) { return batch < 1 ? 0 : argmax_workspace_bytes(batch); }
 

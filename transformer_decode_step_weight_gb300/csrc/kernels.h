@@ -286,6 +286,69 @@ cudaError_t launch_prefill_attention_tc(const PrefillAttnArgs& a, void* scratch,
 cudaError_t launch_prefill_prep(const int32_t* pos, int n, int32_t* vpos, const Launch& L);
 cudaError_t launch_prefill_finish(int32_t* pos, int n, const Launch& L);
 
+// ----------------------------------------------------------------- packed rows (attention_rows.cu)
+// Rows of q packed by segments [cu[i], cu[i + 1]), each head's keys read through the
+// segment's page-table row. Prompt form (shared_lens null): segment i is sequence i, row
+// j of its n rows sees keys 0 .. seq_lens[i] - n + j. Shared form: the segments are groups
+// of sequences (row = sequence) whose first shared_lens[i] tokens lie in the same pages.
+struct AttnRowsArgs {
+  const void* q;           // f32 or bf16 [n_rows, Hq, D], rows q_stride elements apart
+  int q_f32;
+  long long q_stride;
+  const void *k_pages, *v_pages;
+  const int32_t* page_table;   // [segments or sequences, max_pages]
+  const int32_t* cu;           // [n_seg + 1]
+  const int32_t* seq_lens;     // per segment (prompt form) or per row (shared form)
+  const int32_t* shared_lens;  // [n_seg] or null
+  int n_seg, n_rows, Hq, Hkv;
+  int page_size, max_pages, n_pages;
+  float scale;
+  void* out;               // as q's type, rows contiguous
+  void* workspace;
+};
+size_t attn_rows_workspace_bytes();
+size_t attn_shared_workspace_bytes(int B, int Hq, int Hkv);
+cudaError_t launch_attn_prompt(const AttnRowsArgs& a, const Launch& L);
+cudaError_t launch_attn_shared(const AttnRowsArgs& a, const Launch& L);
+
+// ----------------------------------------------------------------- cache pages (pages.cu)
+struct PageState {
+  int32_t *table, *lens, *refs;
+  int max_seqs, max_pages, page_size, n_pages;
+};
+struct PageCopy {
+  void* const* k_cache;    // host arrays [n_layers]
+  void* const* v_cache;
+  int n_layers;
+  size_t page_bytes;       // of one page of K (or V) in one layer
+};
+constexpr int kPagesMaxSeqs = 2048;
+size_t pages_workspace_bytes(int max_seqs, int n_pages);
+cudaError_t launch_pages_copy(const PageCopy& pc, const int32_t* src, const int32_t* dst, int n, int n_pages,
+                              const Launch& L);
+cudaError_t launch_pages_fork(const PageState& c, const int32_t* parents, const int32_t* children, int n,
+                              void* workspace, const Launch& L);
+cudaError_t launch_pages_extend(const PageState& c, const PageCopy& pc, const int32_t* n_new, void* workspace,
+                                const Launch& L);
+cudaError_t launch_pages_trim(const PageState& c, const int32_t* new_lens, const Launch& L);
+cudaError_t launch_pages_compact(const PageState& c, const PageCopy& pc, int32_t* n_live, void* workspace,
+                                 const Launch& L);
+
+// ----------------------------------------------------------------- sampled verification (verify_sample.cu)
+struct VerifySampleArgs {
+  const float *target, *draft_probs, *u;
+  long long t_stride, d_stride;
+  const int32_t *draft, *n_draft;
+  int B, k, V;
+  int32_t *tok, *pos, *step, *out_tokens;
+  int max_steps;
+  int32_t* n_accept;
+  void* workspace;
+};
+size_t verify_sample_workspace_bytes(int B);
+int verify_sample_max_vocab();
+cudaError_t launch_verify_sample(const VerifySampleArgs& a, const Launch& L);
+
 // ----------------------------------------------------------------- persistent batch-1 step
 // The whole decode step of a BF16 model at batch 1 as one cooperative kernel
 // (step_stream.cu). res / qkv / attn / h are the step workspace's activation
