@@ -1,76 +1,943 @@
-// Attention of packed rows over the paged cache: prompts of several sequences, and decode
-// rows of sequences that share a prefix.
+// Attention of packed rows over the paged cache on tcgen05: the prompts of several
+// sequences in one launch, and the shared prefixes of decode rows.
+//
+// A row tile is 128 rows of one kv head: consecutive packed tokens (prompt form) or
+// sequences (shared form) times the Hq / Hkv q heads that read it, so a K/V tile is read
+// once for all of them. Work is counted in units of one row tile times 128 keys, ordered
+// by (segment, kv head, row tile, keys); CTA c of the one-per-SM grid takes the units
+// [c U / G, (c + 1) U / G). So ragged prompts, one long prompt and one row behind a long
+// cache all split evenly without the host knowing a length; a row tile that several CTAs
+// share is joined, in key order, by the last of them (ticket). A causal row tile counts
+// only the tiles that some row of it sees.
+//
+// Per 128 keys: S = Q K^T (M 128, N 128) into tensor memory, the softmax warps read it,
+// keep a reference maximum that moves when a score passes it by more than 2^8 (so that O
+// is rescaled rarely), and write the weights back over S as the A operand of O += P V.
+// V is read as it lies in the cache (keys x dims) through an MN-major descriptor, so no
+// transposed copy exists. A ring of 32 KB slots holds K and V tiles in the order the
+// products need them.
+//   * bf16 q: weights rounded to bf16 (each off by 2^-8 of itself at most, as the
+//     result's own rounding); sums, statistics and O in f32.
+//   * f32 q: q and the weights as three bf16 parts each (24 bits; two would leave
+//     2.4e-6 of each weight, above what an f32 sum of the same length loses), three times
+//     the products.
+// Two tile shapes. One row tile per CTA (NT 1): each row is held by two threads that take
+// 64 of the 128 keys each and trade maxima; S is double-buffered. Two (NT 2, bf16 only, 256
+// rows): one thread per row, the two tiles' products and softmaxes alternate.
+//
+// Keys a row must not see: scores are masked by selection, and V rows that only some rows
+// of the tile see are checked for NaN and infinities (0 * NaN would reach every row):
+// those entries enter the products as 0 and are added afterwards to the rows that see
+// them. Every wait is bounded; after a timeout all roles run through without touching
+// anything, so nobody is left waiting.
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.cuh"
+#include "tc_common.cuh"
 
 #include <algorithm>
+#include <cstring>
 
 namespace qd {
 namespace {
 
 constexpr int kD = 128;
+constexpr int kRows = 128;               // rows of a row tile (M, TMEM lanes)
+constexpr int kKeys = 128;               // keys of a tile
+constexpr int kChunk = 128 * 128;        // [128 rows x 64 bf16], 128-byte swizzle
+constexpr int kSlot = 2 * kChunk;        // a K or V tile, or one part of a row tile of Q
+constexpr int kSoftWarps = 8;
+constexpr int kSoft = 32 * kSoftWarps;
+constexpr int kIssuer = kSoftWarps;      // warp roles behind the softmax warps
+constexpr int kProducer = kSoftWarps + 1;
+constexpr int kFixer = kSoftWarps + 2;   // and the one after it
+constexpr int kThreads = 32 * (kSoftWarps + 4);
+constexpr int kMisc = 3072;              // barriers and small arrays in front of Q and the ring
+constexpr int kData = 7 * kSlot;         // 224 KB: Q parts and ring slots
+constexpr size_t kSmem = kMisc + kData;  // 227 KB, the whole opt-in shared memory
+constexpr int kMaxSlots = 6;
+constexpr int kMinUnits = 2;             // units per CTA below which fewer CTAs are used
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kMove = 8.0f;            // log2 units a score may pass the reference maximum
+constexpr int kMaxGrid = 192;            // CTAs (SMs) the workspace has room for
+constexpr int kPartRows = 2 * kRows;     // rows of a partial (NT 2)
+constexpr size_t kPartFloats = (size_t)kPartRows * (kD + 2);
 
-// One warp per (row, q head), four dims per lane, one key at a time.
-template <typename T>
-__global__ void __launch_bounds__(128) attn_rows_kernel(const AttnRowsArgs a, int* err) {
-  const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int row = (int)(w / a.Hq), h = (int)(w % a.Hq), g = h / (a.Hq / a.Hkv);
-  bool bad = a.cu[0] < 0 || a.cu[a.n_seg] > a.n_rows;
-  for (int i = lane; i < a.n_seg; i += 32) bad = bad || a.cu[i + 1] < a.cu[i];
-  if (__any_sync(0xffffffffu, bad)) {
-    if (w == 0 && lane == 0) set_error(err, QD_DEVERR_POS);
+struct Params {
+  const void* q;
+  long long q_stride;
+  const __nv_bfloat16 *k_pages, *v_pages;
+  const int32_t *page_table, *cu, *seq_lens, *shared_lens;
+  int n_seg, n_rows, Hq, Hkv, rep, log_rep, page_size, max_pages, n_pages;
+  long long cap;
+  int box;                 // rows per TMA box; 0: cp.async loads
+  float scale_log2, q_sign;
+  void* out;
+  float* part;             // [grid][2][kPartFloats]: O [rows][128], m [rows], l [rows]
+  int* tickets;            // [grid], zero between calls
+  float *pre_o, *pre_m, *pre_l;   // shared form: O, m, l of each (sequence, q head)
+  int* err;
+};
+
+QD_DEV float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+QD_DEV uint32_t bf2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  uint32_t u;
+  memcpy(&u, &v, 4);
+  return u;
+}
+QD_DEV void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+
+// ---- tensor memory
+QD_DEV void ld32(uint32_t taddr, float* v) {   // 32 columns, not waited for
+  uint32_t* r = (uint32_t*)v;
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+QD_DEV void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+QD_DEV void st16(uint32_t taddr, const uint32_t* r) {   // 16 columns, not waited for
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+QD_DEV void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// O += P V: A (P) in tensor memory, B (V) in shared memory as [keys][dims], i.e. MN-major:
+// 64 dims per 128-byte row, 8 keys per swizzle atom; the leading offset leads to the next
+// 64 dims, the stride offset to the next 8 keys.
+QD_DEV uint64_t desc_v(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3FFF) | (uint64_t)(kChunk >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+QD_DEV void mma_pv(uint32_t tmem_d, uint32_t tmem_a, uint64_t db, uint32_t accumulate) {
+  constexpr uint32_t kIdesc = tc::idesc_m128(kD) | (1u << 16);   // B MN-major
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(db), "r"(kIdesc), "r"(accumulate)
+      : "memory");
+}
+
+QD_DEV void cp16(uint32_t dst, const void* src, int bytes) {   // bytes 0: zeros, nothing read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// ---- the work of one segment
+struct Seg {
+  int row0, n;     // its packed rows (prompt tokens, or sequences)
+  int off;         // prompt form: row j sees off + j + 1 keys
+  int len;         // keys
+  int tiles;       // row tiles per kv head; 0: no work
+  bool bad;
+};
+
+// sum over j < n of floor(j / r)
+QD_DEV long long floor_sum(long long n, int r) {
+  const long long q = n / r;
+  return r * (q * (q - 1) / 2) + q * (n - q * r);
+}
+
+template <int NT>
+struct Work {
+  int tpt;   // packed rows (tokens or sequences) per row tile
+  bool prompt;
+
+  QD_DEV Seg seg(const Params& p, int s) const {
+    Seg a;
+    a.row0 = p.cu[s];
+    a.n = p.cu[s + 1] - a.row0;
+    a.len = prompt ? p.seq_lens[s] : p.shared_lens[s];
+    a.bad = a.n > 0 && (a.len < 0 || a.len > p.cap);
+    a.off = a.len - a.n;
+    a.tiles = a.bad || a.n <= 0 || (!prompt && a.len == 0) ? 0 : (a.n + tpt - 1) / tpt;
+    return a;
+  }
+  // keys that the last row of row tile t sees (prompt form), at least 0
+  QD_DEV int seen(const Seg& a, int t) const { return prompt ? max(0, a.off + min((t + 1) * tpt, a.n)) : a.len; }
+  QD_DEV int units(const Seg& a, int t) const { return max(1, (seen(a, t) + kKeys - 1) / kKeys); }
+  // units of the row tiles before t (t <= tiles)
+  QD_DEV long long before(const Seg& a, int t) const {
+    if (!prompt) return (long long)t * units(a, 0);
+    const int full = min(t, a.tiles - 1);
+    long long sum = t == a.tiles && t > 0 ? units(a, t - 1) : 0;
+    if (full <= 0) return sum;
+    // tile i < full ends at off + (i + 1) tpt keys: one unit up to 128, else the quotient
+    const int one = a.off > kKeys ? 0 : min(full, (kKeys - a.off) / tpt);
+    sum += one;
+    const long long c = (long long)a.off + (long long)(one + 1) * tpt + kKeys - 1;
+    const long long rest = full - one;
+    if (rest > 0) {
+      if (tpt <= kKeys) {   // tpt divides 128
+        const int r = kKeys / tpt;
+        sum += floor_sum(c / tpt + rest, r) - floor_sum(c / tpt, r);
+      } else {
+        sum += rest * (c / kKeys) + (tpt / kKeys) * (rest * (rest - 1) / 2);
+      }
+    }
+    return sum;
+  }
+};
+
+template <typename T, int PARTS, int NT>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p) {
+  static_assert(PARTS == 1 || NT == 1, "");
+  constexpr int kQ = PARTS * NT;              // Q slots
+  constexpr int kRing = 7 - kQ < kMaxSlots ? 7 - kQ : kMaxSlots;
+  constexpr int kCols = NT == 2 ? 128 : 64;   // keys of a tile per softmax thread
+  constexpr int kOCols = NT == 2 ? 128 : 64;  // O columns per softmax thread
+  extern __shared__ __align__(1024) unsigned char smem[];
+  unsigned char* data = smem + kMisc;
+  uint64_t* full = (uint64_t*)smem;      // [kRing] a K or V tile landed
+  uint64_t* empty = full + kMaxSlots;    // [kRing] its products are done
+  uint64_t* s_full = empty + kMaxSlots;  // [2] S in buffer b
+  uint64_t* p_full = s_full + 2;         // [2] the weights in buffer b, O rescaled
+  uint64_t* o_done = p_full + 2;         // [2] the P V products of buffer b done
+  uint64_t* v_go = o_done + 2;           // a masked V tile landed (the issuer saw it)
+  uint64_t* v_fixed = v_go + 1;          // ... and was put right
+  uint32_t* tslot = (uint32_t*)(v_fixed + 1);
+  int* s_abort = (int*)(tslot + 1);
+  int* s_patch = s_abort + 1;            // the last piece with NaN or infinities in a masked V tile
+  int* s_last = s_patch + 1;
+  long long* s_find = (long long*)(smem + 256);   // [0] segment, [1] units before it, [2] U, [3] bad
+  long long* s_scan = (long long*)(smem + 320);   // [warps] sums of the scan
+  float* xm = (float*)(smem + 512);               // [2][2][128] traded maxima and sums
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  Work<NT> W;
+  W.prompt = p.shared_lens == nullptr;
+  W.tpt = NT * kRows >> p.log_rep;
+  pdl_launch_dependents();
+
+  if (smem_u32(smem) & 1023u) {   // the swizzled tiles rest on it (there is no static shared memory)
+    if (tid == 0) set_error(p.err, QD_DEVERR_TIMEOUT);
     return;
   }
-  if (row < a.cu[0] || row >= a.cu[a.n_seg] || row >= a.n_rows) return;
-  int lo = 0, hi = a.n_seg;   // the last segment that starts at or before the row
-  while (hi - lo > 1) {
+
+  // ---- this CTA's units
+  {
+    const int per = (p.n_seg + kThreads - 1) / kThreads;
+    long long own = 0;
+    bool bad = false;
+    for (int i = 0; i < per; ++i) {
+      const int s = tid * per + i;
+      if (s >= p.n_seg) break;
+      const Seg a = W.seg(p, s);
+      bad = bad || a.n < 0 || a.row0 < 0 || a.row0 + a.n > p.n_rows;
+      if (a.bad && blockIdx.x == 0) set_error(p.err, QD_DEVERR_POS);
+      if (!bad && a.tiles) own += W.before(a, a.tiles) * p.Hkv;
+    }
+    if (tid == 0) *s_abort = 0;
+    const int any_bad = __syncthreads_or(bad);
+    if (any_bad) {
+      if (blockIdx.x == 0 && tid == 0) set_error(p.err, QD_DEVERR_POS);
+      return;
+    }
+    long long v = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += x;
+    }
+    if (lane == 31) s_scan[warp] = v;
+    __syncthreads();
+    long long base = 0, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) base += s_scan[w];
+      total += s_scan[w];
+    }
+    const long long G = min((long long)gridDim.x, (total + kMinUnits - 1) / kMinUnits);
+    if ((long long)blockIdx.x >= G) return;
+    const long long u0 = blockIdx.x * total / G;
+    long long at = base + v - own;
+    if (tid == 0) s_find[2] = total;
+    if (own > 0 && at <= u0 && u0 < at + own) {
+      for (int i = 0; i < per; ++i) {
+        const int s = tid * per + i;
+        const Seg a = W.seg(p, s);
+        const long long n = a.tiles ? W.before(a, a.tiles) * p.Hkv : 0;
+        if (u0 < at + n) {
+          s_find[0] = s;
+          s_find[1] = at;
+          break;
+        }
+        at += n;
+      }
+    }
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kMaxSlots; ++i) {
+      mbar_init(&full[i], p.box ? 1 : 32);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], NT == 2 ? kRows : kSoft);
+      mbar_init(&o_done[i], 1);
+    }
+    mbar_init(v_go, 1);
+    mbar_init(v_fixed, 64);
+    fence_mbar_init();
+    *s_patch = 0;
+  }
+  if (warp == 0) tc::alloc(tslot, 512);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tb = *tslot;
+  const uint32_t tS = tb, tO = tb + 256, tX = tb + 384;   // NT 2: O of tile j at tO + 128 j
+  const long long U = s_find[2];
+  const long long G = min((long long)gridDim.x, (U + kMinUnits - 1) / kMinUnits);
+  const long long u1 = (blockIdx.x + 1) * U / G;
+  long long u = blockIdx.x * U / G;
+
+  // a bounded wait; after a timeout anywhere in the CTA it returns at once
+  auto wait = [&](uint64_t* bar, uint32_t ph) {
+    if (mbar_try_wait(bar, ph)) return;
+    const uint64_t t0 = global_ns();
+    for (int i = 0; i < (1 << 24); ++i) {
+      if (mbar_try_wait(bar, ph)) return;
+      if ((i & 63) == 63) {
+        if (*(volatile int*)s_abort) return;
+        if (global_ns() - t0 > 1000000000ull) break;
+      }
+    }
+    set_error(p.err, QD_DEVERR_TIMEOUT);
+    *(volatile int*)s_abort = 1;
+  };
+
+  // position of unit u
+  int s = (int)s_find[0];
+  Seg a = W.seg(p, s);
+  long long w = (u - s_find[1]) % W.before(a, a.tiles);
+  int g = (int)((u - s_find[1]) / W.before(a, a.tiles));
+  int t = 0;
+  for (int lo = 0, hi = a.tiles; hi - lo > 1;) {   // the last row tile whose units start at or before w
     const int mid = (lo + hi) / 2;
-    if (a.cu[mid] <= row) lo = mid; else hi = mid;
+    if (W.before(a, mid) <= w) lo = mid; else hi = mid;
+    t = lo;
   }
-  const int seq = a.shared_lens ? row : lo;
-  const int len = a.seq_lens[seq];
-  const int n = a.shared_lens ? len : len - (a.cu[lo + 1] - row) + 1;
-  if (len < 0 || len > a.max_pages * a.page_size) {
-    if (lane == 0) set_error(err, QD_DEVERR_POS);
-    return;
-  }
-  const size_t o = (size_t)h * kD + 4 * lane;
-  float q[4], acc[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
+  int k0 = (int)(w - W.before(a, t));
+  // running counts, the same in every role that uses them: ring slots, tiles, fixed tiles, trades
+  uint32_t ring = 0, tile = 0, fixes = 0, trades = 0;
+  int piece_no = 0;
+
+  while (true) {
+    // ================= one piece: row tile t of kv head g, key tiles k0 .. k1 - 1 of nk
+    ++piece_no;
+    const int nk = W.units(a, t);
+    const int k1 = (int)min((long long)nk, k0 + (u1 - u));
+    const int n = k1 - k0;
+    const int first_row = a.row0 + t * W.tpt;                   // packed row
+    const int packed = min(W.tpt, a.n - t * W.tpt);             // packed rows in the tile
+    const int seen_max = W.seen(a, t);                          // keys past it are nobody's
+    int seen_min;                                               // keys before it are everybody's
+    if (W.prompt) {
+      seen_min = max(0, a.off + t * W.tpt + 1);
+    } else {
+      int m = a.len;
+      for (int i = lane; i < packed; i += 32) {
+        const int l = p.seq_lens[first_row + i];
+        m = min(m, l < 0 || l > p.cap ? 0 : l);
+      }
+      seen_min = __reduce_min_sync(0xffffffffu, m);
+    }
+    const int32_t* pt = p.page_table + (size_t)(W.prompt ? s : a.row0) * p.max_pages;
+
+    if (warp == kProducer) {
+      // ---- K and V tiles in the order of the products
+      auto load = [&](const CUtensorMap* map, const __nv_bfloat16* pages, int key0) {
+        const uint32_t slot = ring % kRing, use = ring / kRing;
+        ++ring;
+        if (use) wait(&empty[slot], (use - 1) & 1);
+        unsigned char* dst = data + (kQ + slot) * kSlot;
+        const int keys = max(0, min(kKeys, seen_max - key0));
+        if (p.box) {
+          const int boxes = (keys + p.box - 1) / p.box;
+          const bool go = !__any_sync(0xffffffffu, *(volatile int*)s_abort != 0);
+          if (lane == 0) {
+            if (go && boxes) mbar_arrive_expect_tx(&full[slot], (uint32_t)boxes * p.box * 256);
+            else mbar_arrive(&full[slot]);
+          }
+          __syncwarp();
+          if (go && lane < 2 * boxes) {
+            const int b = lane >> 1, half = lane & 1, key = key0 + b * p.box;
+            const PagedSlot sl = paged_slot(pt, key, p.page_size, p.n_pages);
+            if (!sl.ok) set_error(p.err, QD_DEVERR_PAGE);
+            tma_load_2d(dst + half * kChunk + b * p.box * 128, map, half * 64,
+                        (sl.page * p.Hkv + g) * p.page_size + sl.slot, &full[slot]);
+          }
+          __syncwarp();
+        } else {
+          // 16 lanes copy one key's 256 bytes; lane i looks up keys i, i + 32, ...
+          const uint32_t d0 = smem_u32(dst);
+          for (int kb = 0; kb < kKeys; kb += 32) {
+            long long off = -1;
+            if (kb + lane < keys) {
+              const PagedSlot sl = paged_slot(pt, key0 + kb + lane, p.page_size, p.n_pages);
+              if (!sl.ok) set_error(p.err, QD_DEVERR_PAGE);
+              off = (((long long)sl.page * p.Hkv + g) * p.page_size + sl.slot) * kD;
+            }
+#pragma unroll 4
+            for (int i = 0; i < 32; i += 2) {
+              const int r = i + (lane >> 4), c = lane & 15;
+              const long long o = __shfl_sync(0xffffffffu, off, r);
+              cp16(d0 + (c >> 3) * kChunk + tc::sw128_off(kb + r, c & 7), pages + (o < 0 ? 0 : o) + c * 8, o < 0 ? 0 : 16);
+            }
+          }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
+          fence_proxy_async_smem();
+          mbar_arrive(&full[slot]);
+        }
+      };
+      load(&tmK, p.k_pages, k0 * kKeys);
+      if (NT == 1 && n > 1) load(&tmK, p.k_pages, (k0 + 1) * kKeys);
+      for (int i = 0; i < n; ++i) {
+        load(&tmV, p.v_pages, (k0 + i) * kKeys);
+        const int nx = i + (NT == 1 ? 2 : 1);
+        if (nx < n) load(&tmK, p.k_pages, (k0 + nx) * kKeys);
+      }
+    } else if (warp >= kFixer) {
+      // ---- V tiles that some row must not see whole: rows past everybody's keys to zero,
+      // NaN and infinities in the others taken out
+      // (the issuer says when: a slot's own barrier may be several phases behind a tile that is
+      // still to come, which a wait on its parity cannot tell)
+      uint32_t r = ring + (NT == 1 && n > 1 ? 2 : 1), fx = fixes;
+      for (int i = 0; i < n; ++i) {
+        const int key0 = (k0 + i) * kKeys;
+        if (key0 + kKeys > seen_min) {
+          const uint32_t slot = r % kRing;
+          wait(v_go, fx++ & 1);
+          wait(&full[slot], (r / kRing) & 1);   // done; orders the copy before this thread's reads
+          unsigned char* v = data + (kQ + slot) * kSlot;
+          const int lo = max(0, seen_min - key0), hi = seen_max - key0;
+          for (int e = lo * 16 + tid - 32 * kFixer; e < kKeys * 16; e += 64) {
+            const int key = e >> 4, c = e & 15;
+            uint4* at = (uint4*)(v + (c >> 3) * kChunk + tc::sw128_off(key, c & 7));
+            if (key >= hi) {
+              *at = make_uint4(0u, 0u, 0u, 0u);
+            } else {
+              uint32_t x[4] = {at->x, at->y, at->z, at->w};
+              bool hit = false;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) q[e] = (float)((const T*)a.q)[(size_t)row * a.q_stride + o + e] * a.scale * kLog2e;
-  for (int t = 0; t < n; ++t) {
-    const PagedSlot sl = paged_slot(a.page_table + (size_t)seq * a.max_pages, t, a.page_size, a.n_pages);
-    if (!sl.ok && lane == 0) set_error(err, QD_DEVERR_PAGE);
-    const size_t at = (((size_t)sl.page * a.Hkv + g) * a.page_size + sl.slot) * kD + 4 * lane;
-    const uint2 k = *(const uint2*)((const __nv_bfloat16*)a.k_pages + at);
-    const uint2 v = *(const uint2*)((const __nv_bfloat16*)a.v_pages + at);
-    const float s = warp_sum(q[0] * bf_lo(k.x) + q[1] * bf_hi(k.x) + q[2] * bf_lo(k.y) + q[3] * bf_hi(k.y));
-    const float mn = fmaxf(m, s), al = m == -INFINITY ? 0.f : exp2f(m - mn), p = exp2f(s - mn);
-    l = l * al + p;
-    acc[0] = acc[0] * al + p * bf_lo(v.x);
-    acc[1] = acc[1] * al + p * bf_hi(v.x);
-    acc[2] = acc[2] * al + p * bf_lo(v.y);
-    acc[3] = acc[3] * al + p * bf_hi(v.y);
-    m = mn;
-  }
+              for (int j = 0; j < 4; ++j) {
+                if ((x[j] & 0x7f80u) == 0x7f80u) { x[j] &= 0xffff0000u; hit = true; }
+                if ((x[j] & 0x7f800000u) == 0x7f800000u) { x[j] &= 0xffffu; hit = true; }
+              }
+              if (hit) {
+                *at = make_uint4(x[0], x[1], x[2], x[3]);
+                *(volatile int*)s_patch = piece_no;
+              }
+            }
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(v_fixed);
+        }
+        r += i + (NT == 1 ? 2 : 1) < n ? 2 : 1;
+      }
+    }
+
+    if (warp < kSoftWarps) {
+      // ---- Q: warp w writes rows 16 NT w .. of the row tile(s); lane: dims 4 lane .. + 3
+      const T* q = (const T*)p.q;
+      constexpr int kPer = 16 * NT;
+      const int rows = packed << p.log_rep;
+      for (int rb = 0; rb < kPer; rb += 8) {
+        float x[8][4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) ((T*)a.out)[(size_t)row * a.Hq * kD + o + e] = (T)(n > 0 ? acc[e] / l : 0.f);
+        for (int i = 0; i < 8; ++i) {
+          const int r = warp * kPer + rb + i;
+          const bool ok = r < rows;
+          const T* src = q + (long long)(first_row + (ok ? r >> p.log_rep : 0)) * p.q_stride +
+                         (long long)((g << p.log_rep) + (ok ? r & (p.rep - 1) : 0)) * kD + 4 * lane;
+          if constexpr (PARTS == 1) {
+            const uint2 b = ok ? *(const uint2*)src : make_uint2(0u, 0u);
+            x[i][0] = bf_lo(b.x); x[i][1] = bf_hi(b.x); x[i][2] = bf_lo(b.y); x[i][3] = bf_hi(b.y);
+          } else {
+            const float4 f = ok ? *(const float4*)src : make_float4(0.f, 0.f, 0.f, 0.f);
+            x[i][0] = f.x; x[i][1] = f.y; x[i][2] = f.z; x[i][3] = f.w;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = warp * kPer + rb + i, lr = r & (kRows - 1);
+          const uint32_t o = (uint32_t)((lane >> 4) * kChunk) + tc::sw128_off(lr, (lane & 15) >> 1) + (uint32_t)((lane & 1) * 8);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[i][e] *= p.q_sign;
+#pragma unroll
+          for (int part = 0; part < PARTS; ++part) {
+            const uint32_t b0 = bf2(x[i][0], x[i][1]), b1 = bf2(x[i][2], x[i][3]);
+            *(uint2*)(data + ((NT == 2 ? r >> 7 : 0) + part) * kSlot + o) = make_uint2(b0, b1);
+            if (part + 1 < PARTS) {
+              x[i][0] -= bf_lo(b0); x[i][1] -= bf_hi(b0); x[i][2] -= bf_lo(b1); x[i][3] -= bf_hi(b1);
+            }
+          }
+        }
+      }
+      fence_proxy_async_smem();
+    }
+    if (warp <= kIssuer) bar_sync(1, kSoft + 32);   // Q is there
+
+    if (warp == kIssuer) {
+      if (lane == 0) {
+        // ---- the products, in the order K0 (K1) V0 K2 V1 ... of the ring
+        const uint32_t dq = smem_u32(data);
+        uint32_t r = ring, fx = fixes;
+        auto slot_of = [&](uint32_t c) { return smem_u32(data + (kQ + c % kRing) * kSlot); };
+        auto live = [&] { return *(volatile int*)s_abort == 0; };
+        // S of row tile j (buffer b) from the K tile in slot c
+        auto mma_s = [&](int j, int b, uint32_t kaddr) {
+#pragma unroll
+          for (int part = PARTS - 1; part >= 0; --part)
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint32_t o = (kk >> 2) * kChunk + (kk & 3) * 32;
+              tc::mma<kKeys>(tS + 128 * b, tc::desc_sw128(dq + (j + part) * kSlot + o), tc::desc_sw128(kaddr + o),
+                             part != PARTS - 1 || kk != 0);
+            }
+          tc::commit(&s_full[b]);
+        };
+        auto mma_o = [&](int b, uint32_t to, uint32_t vaddr, bool first) {
+#pragma unroll
+          for (int part = PARTS - 1; part >= 0; --part)
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              uint32_t ta = tS + 128 * b + 8 * kk;   // NT 2: 64 columns of pairs of keys
+              if (NT == 1)                           // NT 1: each half of the keys in its half of the buffer
+                ta = part < 2 ? tS + 128 * b + 64 * (kk >> 2) + 32 * part + 8 * (kk & 3)
+                              : tX + 64 * b + 32 * (kk >> 2) + 8 * (kk & 3);
+              mma_pv(to, ta, desc_v(vaddr + kk * 2048), !first || part != PARTS - 1 || kk != 0);
+            }
+          tc::commit(&o_done[b]);
+        };
+        auto s_tile = [&](int i) {   // takes the next K tile of the ring
+          wait(&full[r % kRing], (r / kRing) & 1);
+          tc::fence_after();
+          if (live()) {
+            mma_s(0, (tile + i) & 1, slot_of(r));
+            tc::commit(&empty[r % kRing]);
+          }
+          ++r;
+        };
+        if constexpr (NT == 1) {
+          s_tile(0);
+          if (n > 1) s_tile(1);
+          for (int i = 0; i < n; ++i) {
+            const int b = (tile + i) & 1;
+            wait(&full[r % kRing], (r / kRing) & 1);
+            if ((k0 + i + 1) * kKeys > seen_min) {
+              mbar_arrive(v_go);
+              wait(v_fixed, fx++ & 1);
+            }
+            wait(&p_full[b], ((tile + i) >> 1) & 1);
+            tc::fence_after();
+            if (live()) {
+              mma_o(b, tO, slot_of(r), i == 0);
+              tc::commit(&empty[r % kRing]);
+            }
+            ++r;
+            if (i + 2 < n) s_tile(i + 2);
+          }
+        } else {
+          wait(&full[r % kRing], (r / kRing) & 1);
+          tc::fence_after();
+          if (live()) {
+            mma_s(0, 0, slot_of(r));
+            mma_s(1, 1, slot_of(r));
+            tc::commit(&empty[r % kRing]);
+          }
+          ++r;
+          for (int i = 0; i < n; ++i) {
+            const uint32_t rv = r, rk = r + 1;
+            wait(&full[rv % kRing], (rv / kRing) & 1);
+            if ((k0 + i + 1) * kKeys > seen_min) {
+              mbar_arrive(v_go);
+              wait(v_fixed, fx++ & 1);
+            }
+            if (i + 1 < n) wait(&full[rk % kRing], (rk / kRing) & 1);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              wait(&p_full[j], (tile + i) & 1);
+              tc::fence_after();
+              if (live()) {
+                mma_o(j, tO + 128 * j, slot_of(rv), i == 0);
+                if (j) tc::commit(&empty[rv % kRing]);
+                if (i + 1 < n) {
+                  mma_s(j, j, slot_of(rk));
+                  if (j) tc::commit(&empty[rk % kRing]);
+                }
+              }
+            }
+            r += i + 1 < n ? 2 : 1;
+          }
+        }
+      }
+      __syncwarp();
+    } else if (warp < kSoftWarps) {
+      // ---- softmax. NT 1: warps w and w + 4 hold the same rows (TMEM lanes), 64 keys and 64
+      // O columns each; NT 2: warps 4 .. 7 hold the second row tile.
+      const int hf = warp >> 2, lr = (warp & 3) * 32 + lane;
+      const int row = NT == 2 ? hf * kRows + lr : lr;
+      const int rows = packed << p.log_rep;
+      const bool valid = row < rows;
+      const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+      const uint32_t to = NT == 2 ? tO + 128 * hf : tO + 64 * hf;
+      int lim = 0;   // keys this row sees
+      if (valid) {
+        const int j = t * W.tpt + (row >> p.log_rep);
+        if (W.prompt) {
+          lim = max(0, a.off + j + 1);
+        } else {
+          const int l = p.seq_lens[a.row0 + j];
+          lim = l < 0 || l > p.cap ? 0 : min(l, a.len);
+        }
+      }
+      const float c = p.scale_log2;
+      float ms = -INFINITY, l = 0.f;
+      auto trade = [&](float v) -> float {   // with the other holder of the row
+        const int par = trades & 1;
+        ++trades;
+        xm[(par * 2 + hf) * kRows + lr] = v;
+        bar_sync(2 + (warp & 3), 64);
+        return xm[(par * 2 + (hf ^ 1)) * kRows + lr];
+      };
+      for (int i = 0; i < n; ++i) {
+        const uint32_t ct = tile + i;
+        const int b = NT == 2 ? hf : (int)(ct & 1);
+        const uint32_t ph = NT == 2 ? ct & 1 : (ct >> 1) & 1;
+        wait(&s_full[b], ph);
+        tc::fence_after();
+        float sv[kCols];
+#pragma unroll
+        for (int e = 0; e < kCols; e += 32) ld32(tS + 128 * b + lanes + (NT == 2 ? 0 : 64 * hf) + e, sv + e);
+        wait_ld();
+        const int key0 = (k0 + i) * kKeys + (NT == 2 ? 0 : 64 * hf);
+        const bool masked = (k0 + i + 1) * kKeys > seen_min;   // the same for the whole CTA
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < kCols; ++e)
+            if (key0 + e >= lim) sv[e] = -INFINITY;
+        }
+        float mt[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) mt[e] = fmaxf(sv[e], sv[e + 16]);
+#pragma unroll
+        for (int k = 32; k < kCols; k += 16)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) mt[e] = fmaxf(mt[e], sv[k + e]);
+#pragma unroll
+        for (int k = 8; k >= 1; k >>= 1)
+#pragma unroll
+          for (int e = 0; e < k; ++e) mt[e] = fmaxf(mt[e], mt[e + k]);
+        float mx = mt[0];
+        if (NT == 1) mx = fmaxf(mx, trade(mx));
+        mx = mx == -INFINITY ? mx : mx * c;
+        const bool move = mx > ms + kMove;
+        const float alpha = move ? ex2(ms - mx) : 1.f;   // 0 while ms is -inf
+        // the barrier of the products before the last ones: already complete (they were issued
+        // before this S), waited for so that the phases are followed one by one
+        if (NT == 1 && ct >= 2) wait(&o_done[b], ((ct - 2) >> 1) & 1);
+        if (NT == 2 && i > 0) wait(&o_done[b], (ct - 1) & 1);
+        if (i > 0 && __any_sync(0xffffffffu, move)) {
+          if (NT == 1) wait(&o_done[b ^ 1], ((ct - 1) >> 1) & 1);
+          tc::fence_after();
+#pragma unroll
+          for (int e = 0; e < kOCols; e += 32) {
+            float ov[32];
+            tc::ld_32x32(to + lanes + e, ov);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) ov[k] *= alpha;
+            tc::st_32x32(to + lanes + e, ov);
+          }
+        }
+        if (move) {
+          l *= alpha;
+          ms = mx;
+        }
+        float ps[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int e0 = 0; e0 < kCols; e0 += 32) {
+          uint32_t w0[16], w1[PARTS == 3 ? 16 : 1], w2[PARTS == 3 ? 16 : 1];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float x = ex2(fmaf(sv[e0 + e], c, -ms)), y = ex2(fmaf(sv[e0 + e + 1], c, -ms));
+            if (masked) {   // a masked score gives 0 (also where ms is still -inf, or c is 0)
+              x = key0 + e0 + e < lim ? x : 0.f;
+              y = key0 + e0 + e + 1 < lim ? y : 0.f;
+            }
+            ps[e & 2] += x;
+            ps[(e & 2) + 1] += y;
+            w0[e / 2] = bf2(x, y);
+            if constexpr (PARTS == 3) {
+              x -= bf_lo(w0[e / 2]);
+              y -= bf_hi(w0[e / 2]);
+              w1[e / 2] = bf2(x, y);
+              w2[e / 2] = bf2(x - bf_lo(w1[e / 2]), y - bf_hi(w1[e / 2]));
+            }
+          }
+          const uint32_t ta = tS + 128 * b + lanes + (NT == 2 ? 0 : 64 * hf) + e0 / 2;
+          st16(ta, w0);
+          if constexpr (PARTS == 3) {
+            st16(ta + 32, w1);
+            st16(tX + 64 * b + lanes + 32 * hf + e0 / 2, w2);
+          }
+        }
+        l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+        wait_st();
+        tc::fence_before();
+        mbar_arrive(&p_full[b]);
+      }
+      // ---- the piece's O, m, l
+      if (NT == 1) {
+        if (tile + n >= 2) wait(&o_done[(tile + n) & 1], ((tile + n - 2) >> 1) & 1);
+        wait(&o_done[(tile + n - 1) & 1], ((tile + n - 1) >> 1) & 1);
+        const float other = trade(l);
+        l = hf == 0 ? l + other : other + l;
+      } else {
+        wait(&o_done[hf], (tile + n - 1) & 1);
+      }
+      tc::fence_after();
+      const bool dead_now = *(volatile int*)s_abort != 0;
+      const bool whole = k0 == 0 && k1 == nk;
+      // where the tile's units lie: the CTAs of its first and last
+      const long long ua = u - k0, ub = ua + nk - 1;
+      const int c0 = (int)(((ua + 1) * G - 1) / U), c1 = (int)(((ub + 1) * G - 1) / U);
+      float* part = p.part + ((size_t)blockIdx.x * 2 + (k0 == 0 ? 1 : 0)) * kPartFloats;
+      const bool patch = *(volatile int*)s_patch == piece_no;
+      const int pr = valid ? row >> p.log_rep : 0;
+      const size_t orow = ((size_t)(first_row + pr) * p.Hq + (g << p.log_rep) + (valid ? row & (p.rep - 1) : 0));
+      const int col0 = NT == 2 ? 0 : 64 * hf;
+      const float inv = l == 0.f ? 0.f : 1.0f / l;   // a row that saw nothing gives 0
+#pragma unroll 1
+      for (int e = 0; e < kOCols; e += 32) {
+        float ov[32];
+        tc::ld_32x32(to + lanes + e, ov);
+        // a value that is not finite: which of V's own NaN and infinities the row sees decides
+        // (a product of a weight's part and an infinity may have given NaN)
+        bool odd = patch;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) odd = odd || !(fabsf(ov[k]) < INFINITY);
+        if (odd && valid && l == l) {
+          float add[32];
+          uint32_t any = 0;
+#pragma unroll
+          for (int k = 0; k < 32; ++k) add[k] = 0.f;
+          const int last = min(lim, k1 * kKeys);
+          for (int key = k0 * kKeys; key < last; ++key) {
+            const PagedSlot sl = paged_slot(pt, key, p.page_size, p.n_pages);
+            const uint4* v = (const uint4*)(p.v_pages + (((size_t)sl.page * p.Hkv + g) * p.page_size + sl.slot) * kD + col0 + e);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint4 x = v[k];
+              const uint32_t h[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float f0 = bf_lo(h[j]), f1 = bf_hi(h[j]);
+                if (!(fabsf(f0) < INFINITY)) { add[8 * k + 2 * j] += f0; any |= 1u << (8 * k + 2 * j); }
+                if (!(fabsf(f1) < INFINITY)) { add[8 * k + 2 * j + 1] += f1; any |= 2u << (8 * k + 2 * j); }
+              }
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if ((any >> k) & 1) ov[k] = add[k];
+        }
+        if (valid && !dead_now) {
+          if (!whole) {
+            float4* o = (float4*)(part + (size_t)row * kD + col0 + e);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] = make_float4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
+          } else if (!W.prompt) {
+            float4* o = (float4*)(p.pre_o + orow * kD + col0 + e);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] = make_float4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
+          } else if constexpr (PARTS == 1) {
+            uint4* o = (uint4*)((__nv_bfloat16*)p.out + orow * kD + col0 + e);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              o[k] = make_uint4(bf2(ov[8 * k] * inv, ov[8 * k + 1] * inv), bf2(ov[8 * k + 2] * inv, ov[8 * k + 3] * inv),
+                                bf2(ov[8 * k + 4] * inv, ov[8 * k + 5] * inv), bf2(ov[8 * k + 6] * inv, ov[8 * k + 7] * inv));
+          } else {
+            float4* o = (float4*)((float*)p.out + orow * kD + col0 + e);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              o[k] = make_float4(ov[4 * k] * inv, ov[4 * k + 1] * inv, ov[4 * k + 2] * inv, ov[4 * k + 3] * inv);
+          }
+        }
+      }
+      if (valid && !dead_now && (NT == 2 || hf == 0)) {
+        if (!whole) {
+          part[(size_t)kPartRows * kD + row] = ms;
+          part[(size_t)kPartRows * kD + kPartRows + row] = l;
+        } else if (!W.prompt) {
+          p.pre_m[orow] = ms;
+          p.pre_l[orow] = l;
+        }
+      }
+      // ---- a shared row tile: the last of its CTAs joins the pieces in key order
+      if (!whole) {   // the same in all softmax threads
+        bar_sync(6, kSoft);
+        if (tid == 0) *s_last = !*(volatile int*)s_abort && atom_add_acq_rel_gpu(p.tickets + c0, 1) == c1 - c0;
+        bar_sync(6, kSoft);
+        if (*(volatile int*)s_last) {
+          const int np = c1 - c0 + 1;
+          float* wt = (float*)(data + kQ * kSlot);   // [pieces][rows] weights in the idle ring
+          float* total = wt + (size_t)np * rows;     // [rows] sums
+          auto piece = [&](int k) { return p.part + ((size_t)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * kPartFloats; };
+          for (int r = tid; r < rows; r += kSoft) {
+            float M = -INFINITY, L = 0.f;
+            for (int k = 0; k < np; ++k) {
+              const float m = __ldcg(piece(k) + (size_t)kPartRows * kD + r);
+              wt[k * rows + r] = m;
+              M = fmaxf(M, m);
+            }
+            for (int k = 0; k < np; ++k) {
+              const float m = wt[k * rows + r], x = m == -INFINITY ? 0.f : ex2(m - M);
+              wt[k * rows + r] = x;
+              if (x != 0.f) L = fmaf(x, __ldcg(piece(k) + (size_t)kPartRows * kD + kPartRows + r), L);
+            }
+            total[r] = L;
+            if (!W.prompt) {
+              const size_t o = (size_t)(first_row + (r >> p.log_rep)) * p.Hq + (g << p.log_rep) + (r & (p.rep - 1));
+              p.pre_m[o] = M;
+              p.pre_l[o] = L;
+            }
+          }
+          bar_sync(6, kSoft);
+          for (int e = tid; e < rows * (kD / 4); e += kSoft) {
+            const int r = e >> 5, c4 = e & 31;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int k = 0; k < np; ++k) {
+              const float x = wt[k * rows + r];
+              const float4 v = __ldcg((const float4*)(piece(k) + (size_t)r * kD) + c4);
+              if (x != 0.f) {
+                acc.x = fmaf(x, v.x, acc.x);
+                acc.y = fmaf(x, v.y, acc.y);
+                acc.z = fmaf(x, v.z, acc.z);
+                acc.w = fmaf(x, v.w, acc.w);
+              }
+            }
+            const size_t o = ((size_t)(first_row + (r >> p.log_rep)) * p.Hq + (g << p.log_rep) + (r & (p.rep - 1))) * kD + 4 * c4;
+            if (!W.prompt) {
+              *(float4*)(p.pre_o + o) = acc;
+            } else {
+              const float L = total[r], iv = L == 0.f ? 0.f : 1.0f / L;
+              if constexpr (PARTS == 1)
+                *(uint2*)((__nv_bfloat16*)p.out + o) = make_uint2(bf2(acc.x * iv, acc.y * iv), bf2(acc.z * iv, acc.w * iv));
+              else
+                *(float4*)((float*)p.out + o) = make_float4(acc.x * iv, acc.y * iv, acc.z * iv, acc.w * iv);
+            }
+          }
+          if (tid == 0) p.tickets[c0] = 0;
+          fence_proxy_async_smem();   // the ring is written by copies again
+        }
+      }
+      tc::fence_before();
+    }
+    // counts of the piece, for every role
+    ring = ring + (warp == kProducer ? 0 : 2 * n);
+    tile += n;
+    for (int i = 0; i < n; ++i) fixes += (k0 + i + 1) * kKeys > seen_min;
+    __syncthreads();
+    tc::fence_after();
+    u += n;
+    if (u >= u1 || *(volatile int*)s_abort) break;
+    // the next piece starts a row tile
+    k0 = 0;
+    if (++t == a.tiles) {
+      t = 0;
+      if (++g == p.Hkv) {
+        g = 0;
+        do {
+          a = W.seg(p, ++s);
+        } while (a.tiles == 0);
+      }
+    }
+  }
+  if (warp == kProducer && *(volatile int*)s_abort && p.box && lane == 0) {
+    // a timeout: the copies that are still under way land before the CTA leaves (bounded)
+    for (uint32_t c = ring > kRing ? ring - kRing : 0; c < ring; ++c)
+      mbar_wait_limit(&full[c % kRing], (c / kRing) & 1, p.err, 10000000ull);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    tc::fence_after();
+    tc::dealloc(tb, 512);
+  }
+}
+
+int grid_ctas() { return std::min(dev_info().sm_count, kMaxGrid); }
+
+template <typename T, int PARTS, int NT>
+cudaError_t launch(const Params& p, const CUtensorMap& tk, const CUtensorMap& tv, const Launch& L) {
+  auto k = attn_rows_kernel<T, PARTS, NT>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_ex(k, dim3(grid_ctas()), dim3(kThreads), kSmem, L, tk, tv, p);
+}
+
+// Workspace: tickets, then the partials; the shared form's prefix results behind them.
+constexpr size_t kTicketBytes = 1024;
+
+cudaError_t run(const AttnRowsArgs& a, float* pre_o, const Launch& L) {
+  Params p = {};
+  p.q = a.q; p.q_stride = a.q_stride;
+  p.k_pages = (const __nv_bfloat16*)a.k_pages; p.v_pages = (const __nv_bfloat16*)a.v_pages;
+  p.page_table = a.page_table; p.cu = a.cu; p.seq_lens = a.seq_lens; p.shared_lens = a.shared_lens;
+  p.n_seg = a.n_seg; p.n_rows = a.n_rows; p.Hq = a.Hq; p.Hkv = a.Hkv; p.rep = a.Hq / a.Hkv;
+  while ((1 << p.log_rep) < p.rep) ++p.log_rep;
+  p.page_size = a.page_size; p.max_pages = a.max_pages; p.n_pages = a.n_pages;
+  p.cap = (long long)a.max_pages * a.page_size;
+  p.scale_log2 = fabsf(a.scale) * kLog2e;
+  p.q_sign = a.scale < 0.f ? -1.f : 1.f;
+  p.out = a.out;
+  p.tickets = (int*)a.workspace;
+  p.part = (float*)((unsigned char*)a.workspace + kTicketBytes);
+  p.pre_o = pre_o;
+  p.pre_m = pre_o ? pre_o + (size_t)a.n_rows * a.Hq * kD : nullptr;
+  p.pre_l = pre_o ? p.pre_m + (size_t)a.n_rows * a.Hq : nullptr;
+  p.err = L.err;
+  // boxes of whole 16-row pieces of a page; other page sizes by 16-byte asynchronous copies
+  alignas(64) CUtensorMap tk, tv;
+  memset(&tk, 0, sizeof(tk));
+  memset(&tv, 0, sizeof(tv));
+  if (a.page_size % 16 == 0) {
+    p.box = 16;
+    while (p.box < kKeys && a.page_size % (2 * p.box) == 0) p.box *= 2;
+    const uint64_t rows = (uint64_t)a.n_pages * a.Hkv * a.page_size;
+    cudaError_t e = encode_tmap_bf16_2d(&tk, a.k_pages, rows, kD, p.box);
+    if (e == cudaSuccess) e = encode_tmap_bf16_2d(&tv, a.v_pages, rows, kD, p.box);
+    if (e != cudaSuccess) return e;
+  }
+  if (a.q_f32) return launch<float, 3, 1>(p, tk, tv, L);
+  // two row tiles per CTA where the segments have the rows for them on average
+  const bool two = (long long)a.n_rows * p.rep > (long long)a.n_seg * kRows;
+  return two ? launch<__nv_bfloat16, 1, 2>(p, tk, tv, L) : launch<__nv_bfloat16, 1, 1>(p, tk, tv, L);
 }
 
 }  // namespace
 
-size_t attn_rows_workspace_bytes() { return 16; }
-size_t attn_shared_workspace_bytes(int, int, int) { return 16; }
+size_t attn_rows_workspace_bytes() { return kTicketBytes + (size_t)grid_ctas() * 2 * kPartFloats * 4; }
 
-cudaError_t launch_attn_prompt(const AttnRowsArgs& a, const Launch& L) {
-  const dim3 grid((unsigned)(((long long)a.n_rows * a.Hq + 3) / 4));
-  return a.q_f32 ? launch_ex(attn_rows_kernel<float>, grid, dim3(128), 0, L, a, L.err)
-                 : launch_ex(attn_rows_kernel<__nv_bfloat16>, grid, dim3(128), 0, L, a, L.err);
-}
-
-cudaError_t launch_attn_shared(const AttnRowsArgs& a, const Launch& L) { return launch_attn_prompt(a, L); }
+cudaError_t launch_attn_prompt(const AttnRowsArgs& a, const Launch& L) { return run(a, nullptr, L); }
+cudaError_t launch_attn_prefix(const AttnRowsArgs& a, float* pre, const Launch& L) { return run(a, pre, L); }
 
 }  // namespace qd

@@ -309,6 +309,9 @@ struct AttnRowsArgs {
 size_t attn_rows_workspace_bytes();
 size_t attn_shared_workspace_bytes(int B, int Hq, int Hkv);
 cudaError_t launch_attn_prompt(const AttnRowsArgs& a, const Launch& L);
+// The groups' shared tokens alone: pre = O [n_rows, Hq, D], m, l [n_rows, Hq] (f32; reference
+// maximum in log2 units) of every row whose group shares any.
+cudaError_t launch_attn_prefix(const AttnRowsArgs& a, float* pre, const Launch& L);
 cudaError_t launch_attn_shared(const AttnRowsArgs& a, const Launch& L);
 
 // ----------------------------------------------------------------- cache pages (pages.cu)
