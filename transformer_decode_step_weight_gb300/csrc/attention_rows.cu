@@ -202,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kRing = 7 - kQ < kMaxSlots ? 7 - kQ : kMaxSlots;
   constexpr int kCols = NT == 2 ? 128 : 64;   // keys of a tile per softmax thread
   constexpr int kOCols = NT == 2 ? 128 : 64;  // O columns per softmax thread
+  constexpr bool kFresh = PARTS == 3;         // O of each tile alone in TMEM, summed in registers
   extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char* data = smem + kMisc;
   uint64_t* full = (uint64_t*)smem;      // [kRing] a K or V tile landed
@@ -520,9 +521,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
               uint32_t ta = tS + 128 * b + 8 * kk;   // NT 2: 64 columns of pairs of keys
-              if (NT == 1)                           // NT 1: each half of the keys in its half of the buffer
-                ta = part < 2 ? tS + 128 * b + 64 * (kk >> 2) + 32 * part + 8 * (kk & 3)
-                              : tX + 64 * b + 32 * (kk >> 2) + 8 * (kk & 3);
+              if (NT == 1)                           // NT 1: 32 keys' weights over their own 32 scores
+                ta = part < 2 ? tS + 128 * b + 32 * (kk >> 1) + 16 * part + 8 * (kk & 1) : tX + 64 * b + 8 * kk;
               mma_pv(to, ta, desc_v(vaddr + kk * 2048), !first || part != PARTS - 1 || kk != 0);
             }
           tc::commit(&o_done[b]);
@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait(&p_full[b], ((tile + i) >> 1) & 1);
             tc::fence_after();
             if (live()) {
-              mma_o(b, tO, slot_of(r), i == 0);
+              mma_o(b, tO, slot_of(r), kFresh || i == 0);
               tc::commit(&empty[r % kRing]);
             }
             ++r;
@@ -611,6 +611,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float c = p.scale_log2;
       float ms = -INFINITY, l = 0.f;
+      float osum[kFresh ? kOCols : 1];
+      if constexpr (kFresh) {
+#pragma unroll
+        for (int k = 0; k < kOCols; ++k) osum[k] = 0.f;
+      }
       auto trade = [&](float v) -> float {   // with the other holder of the row
         const int par = trades & 1;
         ++trades;
@@ -624,47 +629,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ph = NT == 2 ? ct & 1 : (ct >> 1) & 1;
         wait(&s_full[b], ph);
         tc::fence_after();
-        float sv[kCols];
-#pragma unroll
-        for (int e = 0; e < kCols; e += 32) ld32(tS + 128 * b + lanes + (NT == 2 ? 0 : 64 * hf) + e, sv + e);
-        wait_ld();
         const int key0 = (k0 + i) * kKeys + (NT == 2 ? 0 : 64 * hf);
+        const uint32_t ts = tS + 128 * b + lanes + (NT == 2 ? 0 : 64 * hf);
         const bool masked = (k0 + i + 1) * kKeys > seen_min;   // the same for the whole CTA
-        if (masked) {
+        // the scores are read twice, 32 at a time (for the maximum, for the weights): registers
+        // for all of them are not left beside O
+        float mx = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < kCols; ++e)
-            if (key0 + e >= lim) sv[e] = -INFINITY;
+        for (int e0 = 0; e0 < kCols; e0 += 32) {
+          float sv[32];
+          ld32(ts + e0, sv);
+          wait_ld();
+          if (masked) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (key0 + e0 + e >= lim) sv[e] = -INFINITY;
+          }
+#pragma unroll
+          for (int k = 16; k >= 1; k >>= 1)
+#pragma unroll
+            for (int e = 0; e < k; ++e) sv[e] = fmaxf(sv[e], sv[e + k]);
+          mx = fmaxf(mx, sv[0]);
         }
-        float mt[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) mt[e] = fmaxf(sv[e], sv[e + 16]);
-#pragma unroll
-        for (int k = 32; k < kCols; k += 16)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) mt[e] = fmaxf(mt[e], sv[k + e]);
-#pragma unroll
-        for (int k = 8; k >= 1; k >>= 1)
-#pragma unroll
-          for (int e = 0; e < k; ++e) mt[e] = fmaxf(mt[e], mt[e + k]);
-        float mx = mt[0];
         if (NT == 1) mx = fmaxf(mx, trade(mx));
         mx = mx == -INFINITY ? mx : mx * c;
         const bool move = mx > ms + kMove;
         const float alpha = move ? ex2(ms - mx) : 1.f;   // 0 while ms is -inf
-        // the barrier of the products before the last ones: already complete (they were issued
-        // before this S), waited for so that the phases are followed one by one
-        if (NT == 1 && ct >= 2) wait(&o_done[b], ((ct - 2) >> 1) & 1);
-        if (NT == 2 && i > 0) wait(&o_done[b], (ct - 1) & 1);
-        if (i > 0 && __any_sync(0xffffffffu, move)) {
-          if (NT == 1) wait(&o_done[b ^ 1], ((ct - 1) >> 1) & 1);
-          tc::fence_after();
+        if constexpr (!kFresh) {
+          // the barrier of the products before the last ones: already complete (they were issued
+          // before this S), waited for so that the phases are followed one by one
+          if (NT == 1 && ct >= 2) wait(&o_done[b], ((ct - 2) >> 1) & 1);
+          if (NT == 2 && i > 0) wait(&o_done[b], (ct - 1) & 1);
+          if (i > 0 && __any_sync(0xffffffffu, move)) {
+            if (NT == 1) wait(&o_done[b ^ 1], ((ct - 1) >> 1) & 1);
+            tc::fence_after();
 #pragma unroll
-          for (int e = 0; e < kOCols; e += 32) {
-            float ov[32];
-            tc::ld_32x32(to + lanes + e, ov);
+            for (int e = 0; e < kOCols; e += 32) {
+              float ov[32];
+              tc::ld_32x32(to + lanes + e, ov);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) ov[k] *= alpha;
-            tc::st_32x32(to + lanes + e, ov);
+              for (int k = 0; k < 32; ++k) ov[k] *= alpha;
+              tc::st_32x32(to + lanes + e, ov);
+            }
           }
         }
         if (move) {
@@ -674,10 +680,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         float ps[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int e0 = 0; e0 < kCols; e0 += 32) {
+          float sv[32];
+          ld32(ts + e0, sv);
+          wait_ld();
           uint32_t w0[16], w1[PARTS == 3 ? 16 : 1], w2[PARTS == 3 ? 16 : 1];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            float x = ex2(fmaf(sv[e0 + e], c, -ms)), y = ex2(fmaf(sv[e0 + e + 1], c, -ms));
+            float x = ex2(fmaf(sv[e], c, -ms)), y = ex2(fmaf(sv[e + 1], c, -ms));
             if (masked) {   // a masked score gives 0 (also where ms is still -inf, or c is 0)
               x = key0 + e0 + e < lim ? x : 0.f;
               y = key0 + e0 + e + 1 < lim ? y : 0.f;
@@ -692,11 +701,30 @@ __global__ void __launch_bounds__(kThreads, 1)
               w2[e / 2] = bf2(x - bf_lo(w1[e / 2]), y - bf_hi(w1[e / 2]));
             }
           }
-          const uint32_t ta = tS + 128 * b + lanes + (NT == 2 ? 0 : 64 * hf) + e0 / 2;
-          st16(ta, w0);
+          st16(NT == 2 ? ts + e0 / 2 : ts + e0, w0);   // over scores that have been read
           if constexpr (PARTS == 3) {
-            st16(ta + 32, w1);
+            st16(ts + e0 + 16, w1);
             st16(tX + 64 * b + lanes + 32 * hf + e0 / 2, w2);
+          }
+        }
+        if constexpr (kFresh) {
+          // O of the tile before, while S of the tile after is made; the next P V products,
+          // which overwrite it, wait for this thread
+          if (i > 0) {
+            wait(&o_done[b ^ 1], ((ct - 1) >> 1) & 1);
+            tc::fence_after();
+            const bool any = __any_sync(0xffffffffu, move);
+#pragma unroll
+            for (int e = 0; e < kOCols; e += 32) {
+              float ov[32];
+              ld32(to + lanes + e, ov);
+              wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) osum[e + k] += ov[k];
+            }
+            if (any)
+#pragma unroll
+              for (int k = 0; k < kOCols; ++k) osum[k] *= alpha;
           }
         }
         l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
@@ -706,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // ---- the piece's O, m, l
       if (NT == 1) {
-        if (tile + n >= 2) wait(&o_done[(tile + n) & 1], ((tile + n - 2) >> 1) & 1);
+        if (!kFresh && tile + n >= 2) wait(&o_done[(tile + n) & 1], ((tile + n - 2) >> 1) & 1);
         wait(&o_done[(tile + n - 1) & 1], ((tile + n - 1) >> 1) & 1);
         const float other = trade(l);
         l = hf == 0 ? l + other : other + l;
@@ -725,10 +753,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const size_t orow = ((size_t)(first_row + pr) * p.Hq + (g << p.log_rep) + (valid ? row & (p.rep - 1) : 0));
       const int col0 = NT == 2 ? 0 : 64 * hf;
       const float inv = l == 0.f ? 0.f : 1.0f / l;   // a row that saw nothing gives 0
-#pragma unroll 1
+#pragma unroll(kFresh ? kOCols / 32 : 1)
       for (int e = 0; e < kOCols; e += 32) {
         float ov[32];
         tc::ld_32x32(to + lanes + e, ov);
+        if constexpr (kFresh) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) ov[k] += osum[e + k];
+        }
         // a value that is not finite: which of V's own NaN and infinities the row sees decides
         // (a product of a weight's part and an infinity may have given NaN)
         bool odd = patch;

@@ -238,8 +238,17 @@ __global__ void __launch_bounds__(kTh) attn_suffix_kernel(const SParams p) {
     for (int mt = 0; mt < 8; ++mt) {
       uint32_t a[4];
       ldsm_x4_t(a, sV + swz(rV, 2 * mt + cV));
+      if constexpr (PARTS == 1) {
+        mma16816(o[mt], a, pb[0][0], pb[0][1]);
+      } else {
+        // each block's sum alone, the smallest parts first, then added with rounding: the
+        // products' own accumulation truncates (about 2^-24 of the sum at every step)
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int part = PARTS - 1; part >= 0; --part) mma16816(o[mt], a, pb[part][0], pb[part][1]);
+        for (int part = PARTS - 1; part >= 0; --part) mma16816(x, a, pb[part][0], pb[part][1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][e] += x[e];
+      }
     }
     __syncwarp();
   }
