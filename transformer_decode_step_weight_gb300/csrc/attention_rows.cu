@@ -37,6 +37,7 @@
 
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
 namespace qd {
 namespace {
@@ -147,17 +148,17 @@ struct Seg {
   bool bad;
 };
 
-// sum over j < n of floor(j / r)
-QD_DEV long long floor_sum(long long n, int r) {
-  const long long q = n / r;
-  return r * (q * (q - 1) / 2) + q * (n - q * r);
+// a / b; 64-bit divisions are long, and few calls need them
+QD_DEV long long quot(long long a, long long b) {
+  return ((unsigned long long)(a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 template <int NT>
 struct Work {
-  int tpt;   // packed rows (tokens or sequences) per row tile
+  int log_tpt;   // 2^log_tpt packed rows (tokens or sequences) per row tile
   bool prompt;
 
+  QD_DEV int tpt() const { return 1 << log_tpt; }
   QD_DEV Seg seg(const Params& p, int s) const {
     Seg a;
     a.row0 = p.cu[s];
@@ -165,12 +166,19 @@ struct Work {
     a.len = prompt ? p.seq_lens[s] : p.shared_lens[s];
     a.bad = a.n > 0 && (a.len < 0 || a.len > p.cap);
     a.off = a.len - a.n;
-    a.tiles = a.bad || a.n <= 0 || (!prompt && a.len == 0) ? 0 : (a.n + tpt - 1) / tpt;
+    a.tiles = a.bad || a.n <= 0 || (!prompt && a.len == 0) ? 0 : (a.n + tpt() - 1) >> log_tpt;
     return a;
   }
   // keys that the last row of row tile t sees (prompt form), at least 0
-  QD_DEV int seen(const Seg& a, int t) const { return prompt ? max(0, a.off + min((t + 1) * tpt, a.n)) : a.len; }
-  QD_DEV int units(const Seg& a, int t) const { return max(1, (seen(a, t) + kKeys - 1) / kKeys); }
+  QD_DEV int seen(const Seg& a, int t) const {
+    return prompt ? max(0, a.off + min((t + 1) << log_tpt, a.n)) : a.len;
+  }
+  QD_DEV int units(const Seg& a, int t) const { return max(1, (seen(a, t) + kKeys - 1) >> 7); }
+  // sum over j < n of floor(j / 2^k)
+  QD_DEV static long long floor_sum(long long n, int k) {
+    const long long q = n >> k;
+    return ((q * (q - 1)) >> 1 << k) + q * (n - (q << k));
+  }
   // units of the row tiles before t (t <= tiles)
   QD_DEV long long before(const Seg& a, int t) const {
     if (!prompt) return (long long)t * units(a, 0);
@@ -178,21 +186,42 @@ struct Work {
     long long sum = t == a.tiles && t > 0 ? units(a, t - 1) : 0;
     if (full <= 0) return sum;
     // tile i < full ends at off + (i + 1) tpt keys: one unit up to 128, else the quotient
-    const int one = a.off > kKeys ? 0 : min(full, (kKeys - a.off) / tpt);
+    const int one = a.off > kKeys ? 0 : min(full, (kKeys - a.off) >> log_tpt);
     sum += one;
-    const long long c = (long long)a.off + (long long)(one + 1) * tpt + kKeys - 1;
+    const long long c = (long long)a.off + ((long long)(one + 1) << log_tpt) + kKeys - 1;
     const long long rest = full - one;
     if (rest > 0) {
-      if (tpt <= kKeys) {   // tpt divides 128
-        const int r = kKeys / tpt;
-        sum += floor_sum(c / tpt + rest, r) - floor_sum(c / tpt, r);
-      } else {
-        sum += rest * (c / kKeys) + (tpt / kKeys) * (rest * (rest - 1) / 2);
-      }
+      if (log_tpt <= 7)   // tpt divides 128
+        sum += floor_sum((c >> log_tpt) + rest, 7 - log_tpt) - floor_sum(c >> log_tpt, 7 - log_tpt);
+      else
+        sum += rest * (c >> 7) + ((rest * (rest - 1) / 2) << (log_tpt - 7));
     }
     return sum;
   }
 };
+
+// two floats at a time
+QD_DEV uint64_t pack2(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+QD_DEV void unpack2(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+QD_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+QD_DEV uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+QD_DEV float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 
 template <typename T, int PARTS, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -223,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Work<NT> W;
   W.prompt = p.shared_lens == nullptr;
-  W.tpt = NT * kRows >> p.log_rep;
+  W.log_tpt = (NT == 2 ? 8 : 7) - p.log_rep;
   pdl_launch_dependents();
 
   if (smem_u32(smem) & 1023u) {   // the swizzled tiles rest on it (there is no static shared memory)
@@ -265,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const long long G = min((long long)gridDim.x, (total + kMinUnits - 1) / kMinUnits);
     if ((long long)blockIdx.x >= G) return;
-    const long long u0 = blockIdx.x * total / G;
+    const long long u0 = quot(blockIdx.x * total, G);
     long long at = base + v - own;
     if (tid == 0) s_find[2] = total;
     if (own > 0 && at <= u0 && u0 < at + own) {
@@ -305,8 +334,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tS = tb, tO = tb + 256, tX = tb + 384;   // NT 2: O of tile j at tO + 128 j
   const long long U = s_find[2];
   const long long G = min((long long)gridDim.x, (U + kMinUnits - 1) / kMinUnits);
-  const long long u1 = (blockIdx.x + 1) * U / G;
-  long long u = blockIdx.x * U / G;
+  const long long u1 = quot((blockIdx.x + 1) * U, G);
+  long long u = quot(blockIdx.x * U, G);
 
   // a bounded wait; after a timeout anywhere in the CTA it returns at once
   auto wait = [&](uint64_t* bar, uint32_t ph) {
@@ -326,8 +355,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // position of unit u
   int s = (int)s_find[0];
   Seg a = W.seg(p, s);
-  long long w = (u - s_find[1]) % W.before(a, a.tiles);
-  int g = (int)((u - s_find[1]) / W.before(a, a.tiles));
+  const long long head_units = W.before(a, a.tiles);
+  int g = (int)quot(u - s_find[1], head_units);
+  const long long w = u - s_find[1] - g * head_units;
   int t = 0;
   for (int lo = 0, hi = a.tiles; hi - lo > 1;) {   // the last row tile whose units start at or before w
     const int mid = (lo + hi) / 2;
@@ -335,9 +365,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     t = lo;
   }
   int k0 = (int)(w - W.before(a, t));
-  // running counts, the same in every role that uses them: ring slots, tiles, fixed tiles, trades
+  // running counts, the same in every role that uses them: ring entries, tiles, fixed tiles,
+  // trades. The producer runs ahead into the next piece; the others meet at its end.
   uint32_t ring = 0, tile = 0, fixes = 0, trades = 0;
-  int piece_no = 0;
+  int piece_no = 0, late = -1;
 
   while (true) {
     // ================= one piece: row tile t of kv head g, key tiles k0 .. k1 - 1 of nk
@@ -345,12 +376,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int nk = W.units(a, t);
     const int k1 = (int)min((long long)nk, k0 + (u1 - u));
     const int n = k1 - k0;
-    const int first_row = a.row0 + t * W.tpt;                   // packed row
-    const int packed = min(W.tpt, a.n - t * W.tpt);             // packed rows in the tile
+    const int first_row = a.row0 + (t << W.log_tpt);                   // packed row
+    const int packed = min(W.tpt(), a.n - (t << W.log_tpt));             // packed rows in the tile
     const int seen_max = W.seen(a, t);                          // keys past it are nobody's
     int seen_min;                                               // keys before it are everybody's
     if (W.prompt) {
-      seen_min = max(0, a.off + t * W.tpt + 1);
+      seen_min = max(0, a.off + (t << W.log_tpt) + 1);
     } else {
       int m = a.len;
       for (int i = lane; i < packed; i += 32) {
@@ -362,58 +393,81 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int32_t* pt = p.page_table + (size_t)(W.prompt ? s : a.row0) * p.max_pages;
 
     if (warp == kProducer) {
-      // ---- K and V tiles in the order of the products
-      auto load = [&](const CUtensorMap* map, const __nv_bfloat16* pages, int key0) {
+      // ---- K and V tiles in the order of the products. A lane's cache rows of a tile are
+      // looked up once, for K and V, a tile ahead of their use. TMA: lane l, box l / 2 and
+      // dims 64 (l & 1); asynchronous copies: keys l, l + 32, ... (-1: past the keys)
+      constexpr int kAhead = NT == 1 ? 2 : 1;   // K tiles issued before the first V tile
+      constexpr int kMine = 4;
+      struct Look {
+        int row[kMine];
+      };
+      auto look = [&](int i) {
+        Look x;
+        const int key0 = (k0 + i) * kKeys;
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) {
+          const int key = p.box ? key0 + (lane >> 1) * p.box : key0 + 32 * j + lane;
+          x.row[j] = -1;
+          if (i < n && key < min(seen_max, key0 + kKeys) && (j == 0 || !p.box)) {
+            const PagedSlot sl = paged_slot(pt, key, p.page_size, p.n_pages);
+            if (!sl.ok) set_error(p.err, QD_DEVERR_PAGE);
+            x.row[j] = (sl.page * p.Hkv + g) * p.page_size + sl.slot;
+          }
+        }
+        return x;
+      };
+      auto load = [&](const CUtensorMap* map, const __nv_bfloat16* pages, const Look& x) {
         const uint32_t slot = ring % kRing, use = ring / kRing;
         ++ring;
         if (use) wait(&empty[slot], (use - 1) & 1);
         unsigned char* dst = data + (kQ + slot) * kSlot;
-        const int keys = max(0, min(kKeys, seen_max - key0));
         if (p.box) {
-          const int boxes = (keys + p.box - 1) / p.box;
           const bool go = !__any_sync(0xffffffffu, *(volatile int*)s_abort != 0);
+          const unsigned boxes = __popc(__ballot_sync(0xffffffffu, x.row[0] >= 0));   // half boxes
           if (lane == 0) {
-            if (go && boxes) mbar_arrive_expect_tx(&full[slot], (uint32_t)boxes * p.box * 256);
+            if (go && boxes) mbar_arrive_expect_tx(&full[slot], boxes * p.box * 128);
             else mbar_arrive(&full[slot]);
           }
           __syncwarp();
-          if (go && lane < 2 * boxes) {
-            const int b = lane >> 1, half = lane & 1, key = key0 + b * p.box;
-            const PagedSlot sl = paged_slot(pt, key, p.page_size, p.n_pages);
-            if (!sl.ok) set_error(p.err, QD_DEVERR_PAGE);
-            tma_load_2d(dst + half * kChunk + b * p.box * 128, map, half * 64,
-                        (sl.page * p.Hkv + g) * p.page_size + sl.slot, &full[slot]);
-          }
+          if (go && x.row[0] >= 0)
+            tma_load_2d(dst + (lane & 1) * kChunk + (lane >> 1) * p.box * 128, map, (lane & 1) * 64, x.row[0], &full[slot]);
           __syncwarp();
         } else {
-          // 16 lanes copy one key's 256 bytes; lane i looks up keys i, i + 32, ...
+          // 16 lanes copy one key's 256 bytes
           const uint32_t d0 = smem_u32(dst);
-          for (int kb = 0; kb < kKeys; kb += 32) {
-            long long off = -1;
-            if (kb + lane < keys) {
-              const PagedSlot sl = paged_slot(pt, key0 + kb + lane, p.page_size, p.n_pages);
-              if (!sl.ok) set_error(p.err, QD_DEVERR_PAGE);
-              off = (((long long)sl.page * p.Hkv + g) * p.page_size + sl.slot) * kD;
-            }
+#pragma unroll
+          for (int j = 0; j < kMine; ++j)
 #pragma unroll 4
             for (int i = 0; i < 32; i += 2) {
               const int r = i + (lane >> 4), c = lane & 15;
-              const long long o = __shfl_sync(0xffffffffu, off, r);
-              cp16(d0 + (c >> 3) * kChunk + tc::sw128_off(kb + r, c & 7), pages + (o < 0 ? 0 : o) + c * 8, o < 0 ? 0 : 16);
+              const int row = __shfl_sync(0xffffffffu, x.row[j], r);
+              cp16(d0 + (c >> 3) * kChunk + tc::sw128_off(32 * j + r, c & 7),
+                   pages + (long long)max(row, 0) * kD + c * 8, row < 0 ? 0 : 16);
             }
-          }
           asm volatile("cp.async.commit_group;" ::: "memory");
-          asm volatile("cp.async.wait_group 0;" ::: "memory");
-          fence_proxy_async_smem();
-          mbar_arrive(&full[slot]);
+          if (late >= 0) {   // the entry before this one
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            fence_proxy_async_smem();
+            mbar_arrive(&full[late]);
+          }
+          late = (int)slot;
         }
       };
-      load(&tmK, p.k_pages, k0 * kKeys);
-      if (NT == 1 && n > 1) load(&tmK, p.k_pages, (k0 + 1) * kKeys);
+      Look l0 = look(0), l1 = look(1);
+      load(&tmK, p.k_pages, l0);
+      if (kAhead == 2 && n > 1) load(&tmK, p.k_pages, l1);
       for (int i = 0; i < n; ++i) {
-        load(&tmV, p.v_pages, (k0 + i) * kKeys);
-        const int nx = i + (NT == 1 ? 2 : 1);
-        if (nx < n) load(&tmK, p.k_pages, (k0 + nx) * kKeys);
+        const Look l2 = look(i + 2);
+        load(&tmV, p.v_pages, l0);
+        if (i + kAhead < n) load(&tmK, p.k_pages, kAhead == 2 ? l2 : l1);
+        l0 = l1;
+        l1 = l2;
+      }
+      if (late >= 0) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        fence_proxy_async_smem();
+        mbar_arrive(&full[late]);
+        late = -1;
       }
     } else if (warp >= kFixer) {
       // ---- V tiles that some row must not see whole: rows past everybody's keys to zero,
@@ -429,6 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait(&full[slot], (r / kRing) & 1);   // done; orders the copy before this thread's reads
           unsigned char* v = data + (kQ + slot) * kSlot;
           const int lo = max(0, seen_min - key0), hi = seen_max - key0;
+#pragma unroll 4
           for (int e = lo * 16 + tid - 32 * kFixer; e < kKeys * 16; e += 64) {
             const int key = e >> 4, c = e & 15;
             uint4* at = (uint4*)(v + (c >> 3) * kChunk + tc::sw128_off(key, c & 7));
@@ -456,39 +511,53 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     if (warp < kSoftWarps) {
-      // ---- Q: warp w writes rows 16 NT w .. of the row tile(s); lane: dims 4 lane .. + 3
+      // ---- Q
       const T* q = (const T*)p.q;
-      constexpr int kPer = 16 * NT;
       const int rows = packed << p.log_rep;
-      for (int rb = 0; rb < kPer; rb += 8) {
-        float x[8][4];
+      if constexpr (PARTS == 1) {
+        // warp w copies rows 16 NT w .. of the row tile(s) as they are, two rows at a time
+        constexpr int kPer = 16 * NT;
+        const uint32_t d0 = smem_u32(data);
+        const int c = lane & 15;
+#pragma unroll 4
+        for (int i = 0; i < kPer; i += 2) {
+          const int r = warp * kPer + i + (lane >> 4);
+          const bool ok = r < rows;
+          const T* src = q + (long long)(first_row + (ok ? r >> p.log_rep : 0)) * p.q_stride +
+                         (long long)((g << p.log_rep) + (ok ? r & (p.rep - 1) : 0)) * kD + 8 * c;
+          cp16(d0 + (r >> 7) * kSlot + (c >> 3) * kChunk + tc::sw128_off(r & (kRows - 1), c & 7), src, ok ? 16 : 0);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        if (p.q_sign < 0.f) {   // a negative scale: this thread's pieces negated
+          for (int i = 0; i < kPer; i += 2) {
+            const int r = warp * kPer + i + (lane >> 4);
+            uint4* at = (uint4*)(data + (r >> 7) * kSlot + (c >> 3) * kChunk + tc::sw128_off(r & (kRows - 1), c & 7));
+            const uint4 v = *at;
+            *at = make_uint4(v.x ^ 0x80008000u, v.y ^ 0x80008000u, v.z ^ 0x80008000u, v.w ^ 0x80008000u);
+          }
+        }
+      } else {
+        // warp w splits rows 16 w ..; lane: dims 4 lane .. + 3
+        float4 f[16];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = warp * kPer + rb + i;
+        for (int i = 0; i < 16; ++i) {
+          const int r = warp * 16 + i;
           const bool ok = r < rows;
           const T* src = q + (long long)(first_row + (ok ? r >> p.log_rep : 0)) * p.q_stride +
                          (long long)((g << p.log_rep) + (ok ? r & (p.rep - 1) : 0)) * kD + 4 * lane;
-          if constexpr (PARTS == 1) {
-            const uint2 b = ok ? *(const uint2*)src : make_uint2(0u, 0u);
-            x[i][0] = bf_lo(b.x); x[i][1] = bf_hi(b.x); x[i][2] = bf_lo(b.y); x[i][3] = bf_hi(b.y);
-          } else {
-            const float4 f = ok ? *(const float4*)src : make_float4(0.f, 0.f, 0.f, 0.f);
-            x[i][0] = f.x; x[i][1] = f.y; x[i][2] = f.z; x[i][3] = f.w;
-          }
+          f[i] = ok ? *(const float4*)src : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = warp * kPer + rb + i, lr = r & (kRows - 1);
-          const uint32_t o = (uint32_t)((lane >> 4) * kChunk) + tc::sw128_off(lr, (lane & 15) >> 1) + (uint32_t)((lane & 1) * 8);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[i][e] *= p.q_sign;
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t o = (uint32_t)((lane >> 4) * kChunk) + tc::sw128_off(warp * 16 + i, (lane & 15) >> 1) +
+                             (uint32_t)((lane & 1) * 8);
+          float x[4] = {f[i].x * p.q_sign, f[i].y * p.q_sign, f[i].z * p.q_sign, f[i].w * p.q_sign};
 #pragma unroll
           for (int part = 0; part < PARTS; ++part) {
-            const uint32_t b0 = bf2(x[i][0], x[i][1]), b1 = bf2(x[i][2], x[i][3]);
-            *(uint2*)(data + ((NT == 2 ? r >> 7 : 0) + part) * kSlot + o) = make_uint2(b0, b1);
-            if (part + 1 < PARTS) {
-              x[i][0] -= bf_lo(b0); x[i][1] -= bf_hi(b0); x[i][2] -= bf_lo(b1); x[i][3] -= bf_hi(b1);
-            }
+            const uint32_t b0 = bf2(x[0], x[1]), b1 = bf2(x[2], x[3]);
+            *(uint2*)(data + part * kSlot + o) = make_uint2(b0, b1);
+            x[0] -= bf_lo(b0); x[1] -= bf_hi(b0); x[2] -= bf_lo(b1); x[3] -= bf_hi(b1);
           }
         }
       }
@@ -601,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t to = NT == 2 ? tO + 128 * hf : tO + 64 * hf;
       int lim = 0;   // keys this row sees
       if (valid) {
-        const int j = t * W.tpt + (row >> p.log_rep);
+        const int j = (t << W.log_tpt) + (row >> p.log_rep);
         if (W.prompt) {
           lim = max(0, a.off + j + 1);
         } else {
@@ -632,24 +701,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int key0 = (k0 + i) * kKeys + (NT == 2 ? 0 : 64 * hf);
         const uint32_t ts = tS + 128 * b + lanes + (NT == 2 ? 0 : 64 * hf);
         const bool masked = (k0 + i + 1) * kKeys > seen_min;   // the same for the whole CTA
-        // the scores are read twice, 32 at a time (for the maximum, for the weights): registers
+        // the scores are read twice, 64 at a time (for the maximum, for the weights): registers
         // for all of them are not left beside O
         float mx = -INFINITY;
 #pragma unroll
-        for (int e0 = 0; e0 < kCols; e0 += 32) {
-          float sv[32];
+        for (int e0 = 0; e0 < kCols; e0 += 64) {
+          float sv[64];
           ld32(ts + e0, sv);
+          ld32(ts + e0 + 32, sv + 32);
           wait_ld();
           if (masked) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
+            for (int e = 0; e < 64; ++e)
               if (key0 + e0 + e >= lim) sv[e] = -INFINITY;
           }
+          float m4[4] = {mx, mx, mx, mx};
 #pragma unroll
-          for (int k = 16; k >= 1; k >>= 1)
+          for (int e = 0; e < 64; e += 8)
 #pragma unroll
-            for (int e = 0; e < k; ++e) sv[e] = fmaxf(sv[e], sv[e + k]);
-          mx = fmaxf(mx, sv[0]);
+            for (int k = 0; k < 4; ++k) m4[k] = max3(m4[k], sv[e + 2 * k], sv[e + 2 * k + 1]);
+          mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
         }
         if (NT == 1) mx = fmaxf(mx, trade(mx));
         mx = mx == -INFINITY ? mx : mx * c;
@@ -677,36 +748,44 @@ __global__ void __launch_bounds__(kThreads, 1)
           l *= alpha;
           ms = mx;
         }
-        float ps[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t c2 = pack2(c, c), nm2 = pack2(-ms, -ms);
+        uint64_t ps[2] = {0, 0};   // pairs of sums, +0 each
+        auto weights = [&](auto with_mask) {
 #pragma unroll
-        for (int e0 = 0; e0 < kCols; e0 += 32) {
-          float sv[32];
-          ld32(ts + e0, sv);
-          wait_ld();
-          uint32_t w0[16], w1[PARTS == 3 ? 16 : 1], w2[PARTS == 3 ? 16 : 1];
+          for (int e0 = 0; e0 < kCols; e0 += 32) {
+            float sv[32];
+            ld32(ts + e0, sv);
+            wait_ld();
+            uint32_t w0[16];
+            [[maybe_unused]] uint32_t w1[PARTS == 3 ? 16 : 1], w2[PARTS == 3 ? 16 : 1];
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            float x = ex2(fmaf(sv[e], c, -ms)), y = ex2(fmaf(sv[e + 1], c, -ms));
-            if (masked) {   // a masked score gives 0 (also where ms is still -inf, or c is 0)
-              x = key0 + e0 + e < lim ? x : 0.f;
-              y = key0 + e0 + e + 1 < lim ? y : 0.f;
+            for (int e = 0; e < 32; e += 2) {
+              float x, y;
+              unpack2(fma2(pack2(sv[e], sv[e + 1]), c2, nm2), x, y);
+              x = ex2(x);
+              y = ex2(y);
+              if constexpr (decltype(with_mask)::value) {   // a masked score gives 0 (also where ms is still -inf, or c is 0)
+                x = key0 + e0 + e < lim ? x : 0.f;
+                y = key0 + e0 + e + 1 < lim ? y : 0.f;
+              }
+              ps[(e >> 1) & 1] = add2(ps[(e >> 1) & 1], pack2(x, y));
+              w0[e / 2] = bf2(x, y);
+              if constexpr (PARTS == 3) {
+                x -= bf_lo(w0[e / 2]);
+                y -= bf_hi(w0[e / 2]);
+                w1[e / 2] = bf2(x, y);
+                w2[e / 2] = bf2(x - bf_lo(w1[e / 2]), y - bf_hi(w1[e / 2]));
+              }
             }
-            ps[e & 2] += x;
-            ps[(e & 2) + 1] += y;
-            w0[e / 2] = bf2(x, y);
+            st16(NT == 2 ? ts + e0 / 2 : ts + e0, w0);   // over scores that have been read
             if constexpr (PARTS == 3) {
-              x -= bf_lo(w0[e / 2]);
-              y -= bf_hi(w0[e / 2]);
-              w1[e / 2] = bf2(x, y);
-              w2[e / 2] = bf2(x - bf_lo(w1[e / 2]), y - bf_hi(w1[e / 2]));
+              st16(ts + e0 + 16, w1);
+              st16(tX + 64 * b + lanes + 32 * hf + e0 / 2, w2);
             }
           }
-          st16(NT == 2 ? ts + e0 / 2 : ts + e0, w0);   // over scores that have been read
-          if constexpr (PARTS == 3) {
-            st16(ts + e0 + 16, w1);
-            st16(tX + 64 * b + lanes + 32 * hf + e0 / 2, w2);
-          }
-        }
+        };
+        if (masked) weights(std::true_type{});
+        else weights(std::false_type{});
         if constexpr (kFresh) {
           // O of the tile before, while S of the tile after is made; the next P V products,
           // which overwrite it, wait for this thread
@@ -727,7 +806,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int k = 0; k < kOCols; ++k) osum[k] *= alpha;
           }
         }
-        l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+        {
+          float x, y;
+          unpack2(add2(ps[0], ps[1]), x, y);
+          l += x + y;
+        }
         wait_st();
         tc::fence_before();
         mbar_arrive(&p_full[b]);
@@ -744,9 +827,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::fence_after();
       const bool dead_now = *(volatile int*)s_abort != 0;
       const bool whole = k0 == 0 && k1 == nk;
-      // where the tile's units lie: the CTAs of its first and last
-      const long long ua = u - k0, ub = ua + nk - 1;
-      const int c0 = (int)(((ua + 1) * G - 1) / U), c1 = (int)(((ub + 1) * G - 1) / U);
       float* part = p.part + ((size_t)blockIdx.x * 2 + (k0 == 0 ? 1 : 0)) * kPartFloats;
       const bool patch = *(volatile int*)s_patch == piece_no;
       const int pr = valid ? row >> p.log_rep : 0;
@@ -800,12 +880,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             float4* o = (float4*)(p.pre_o + orow * kD + col0 + e);
 #pragma unroll
             for (int k = 0; k < 8; ++k) o[k] = make_float4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
-          } else if constexpr (PARTS == 1) {
-            uint4* o = (uint4*)((__nv_bfloat16*)p.out + orow * kD + col0 + e);
+          } else if constexpr (PARTS == 1) {   // through the place of Q, 256 bytes a row, pieces swizzled
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              o[k] = make_uint4(bf2(ov[8 * k] * inv, ov[8 * k + 1] * inv), bf2(ov[8 * k + 2] * inv, ov[8 * k + 3] * inv),
-                                bf2(ov[8 * k + 4] * inv, ov[8 * k + 5] * inv), bf2(ov[8 * k + 6] * inv, ov[8 * k + 7] * inv));
+              *(uint4*)(data + row * 256 + ((((col0 + e) / 8 + k) ^ (row & 15)) << 4)) =
+                  make_uint4(bf2(ov[8 * k] * inv, ov[8 * k + 1] * inv), bf2(ov[8 * k + 2] * inv, ov[8 * k + 3] * inv),
+                             bf2(ov[8 * k + 4] * inv, ov[8 * k + 5] * inv), bf2(ov[8 * k + 6] * inv, ov[8 * k + 7] * inv));
           } else {
             float4* o = (float4*)((float*)p.out + orow * kD + col0 + e);
 #pragma unroll
@@ -823,63 +903,91 @@ __global__ void __launch_bounds__(kThreads, 1)
           p.pre_l[orow] = l;
         }
       }
+      if constexpr (PARTS == 1) {
+        if (whole && W.prompt) {   // out by whole rows, two at a time
+          if (NT == 2) __syncwarp();
+          else bar_sync(2 + (warp & 3), 64);
+          constexpr int kPer = NT == 2 ? 32 : 16;
+          const int r0 = NT == 2 ? warp * 32 : (warp & 3) * 32 + hf * 16;
+#pragma unroll 4
+          for (int i = 0; i < kPer; i += 2) {
+            const int r = r0 + i + (lane >> 4), pc = lane & 15;
+            if (r < rows && !dead_now)
+              *(uint4*)((__nv_bfloat16*)p.out +
+                        ((size_t)(first_row + (r >> p.log_rep)) * p.Hq + (g << p.log_rep) + (r & (p.rep - 1))) * kD + pc * 8) =
+                  *(const uint4*)(data + r * 256 + ((pc ^ (r & 15)) << 4));
+          }
+        }
+      }
       // ---- a shared row tile: the last of its CTAs joins the pieces in key order
       if (!whole) {   // the same in all softmax threads
+        // where the tile's units lie: the CTAs of its first and last
+        const long long ua = u - k0, ub = ua + nk - 1;
+        const int c0 = k0 == 0 ? (int)blockIdx.x : (int)quot((ua + 1) * G - 1, U);
+        const int c1 = k1 == nk ? (int)blockIdx.x : (int)quot((ub + 1) * G - 1, U);
         bar_sync(6, kSoft);
         if (tid == 0) *s_last = !*(volatile int*)s_abort && atom_add_acq_rel_gpu(p.tickets + c0, 1) == c1 - c0;
         bar_sync(6, kSoft);
         if (*(volatile int*)s_last) {
           const int np = c1 - c0 + 1;
-          float* wt = (float*)(data + kQ * kSlot);   // [pieces][rows] weights in the idle ring
-          float* total = wt + (size_t)np * rows;     // [rows] sums
+          // weights [pieces][batch of rows] and sums [batch] in the place of Q, as many rows at
+          // a time as fit
+          const int batch = min(rows, kQ * kSlot / 4 / (np + 1));
+          float* wt = (float*)data;
+          float* total = wt + (size_t)np * batch;
           auto piece = [&](int k) { return p.part + ((size_t)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * kPartFloats; };
-          for (int r = tid; r < rows; r += kSoft) {
-            float M = -INFINITY, L = 0.f;
-            for (int k = 0; k < np; ++k) {
-              const float m = __ldcg(piece(k) + (size_t)kPartRows * kD + r);
-              wt[k * rows + r] = m;
-              M = fmaxf(M, m);
-            }
-            for (int k = 0; k < np; ++k) {
-              const float m = wt[k * rows + r], x = m == -INFINITY ? 0.f : ex2(m - M);
-              wt[k * rows + r] = x;
-              if (x != 0.f) L = fmaf(x, __ldcg(piece(k) + (size_t)kPartRows * kD + kPartRows + r), L);
-            }
-            total[r] = L;
-            if (!W.prompt) {
-              const size_t o = (size_t)(first_row + (r >> p.log_rep)) * p.Hq + (g << p.log_rep) + (r & (p.rep - 1));
-              p.pre_m[o] = M;
-              p.pre_l[o] = L;
-            }
-          }
-          bar_sync(6, kSoft);
-          for (int e = tid; e < rows * (kD / 4); e += kSoft) {
-            const int r = e >> 5, c4 = e & 31;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int k = 0; k < np; ++k) {
-              const float x = wt[k * rows + r];
-              const float4 v = __ldcg((const float4*)(piece(k) + (size_t)r * kD) + c4);
-              if (x != 0.f) {
-                acc.x = fmaf(x, v.x, acc.x);
-                acc.y = fmaf(x, v.y, acc.y);
-                acc.z = fmaf(x, v.z, acc.z);
-                acc.w = fmaf(x, v.w, acc.w);
+          for (int r0 = 0; r0 < rows; r0 += batch) {
+            const int nb = min(batch, rows - r0);
+            for (int r = tid; r < nb; r += kSoft) {
+              float M = -INFINITY, L = 0.f;
+              for (int k = 0; k < np; ++k) {
+                const float m = __ldcg(piece(k) + (size_t)kPartRows * kD + r0 + r);
+                wt[k * batch + r] = m;
+                M = fmaxf(M, m);
+              }
+              for (int k = 0; k < np; ++k) {
+                const float m = wt[k * batch + r], x = m == -INFINITY ? 0.f : ex2(m - M);
+                wt[k * batch + r] = x;
+                if (x != 0.f) L = fmaf(x, __ldcg(piece(k) + (size_t)kPartRows * kD + kPartRows + r0 + r), L);
+              }
+              total[r] = L;
+              if (!W.prompt) {
+                const int rr = r0 + r;
+                const size_t o = (size_t)(first_row + (rr >> p.log_rep)) * p.Hq + (g << p.log_rep) + (rr & (p.rep - 1));
+                p.pre_m[o] = M;
+                p.pre_l[o] = L;
               }
             }
-            const size_t o = ((size_t)(first_row + (r >> p.log_rep)) * p.Hq + (g << p.log_rep) + (r & (p.rep - 1))) * kD + 4 * c4;
-            if (!W.prompt) {
-              *(float4*)(p.pre_o + o) = acc;
-            } else {
-              const float L = total[r], iv = L == 0.f ? 0.f : 1.0f / L;
-              if constexpr (PARTS == 1)
-                *(uint2*)((__nv_bfloat16*)p.out + o) = make_uint2(bf2(acc.x * iv, acc.y * iv), bf2(acc.z * iv, acc.w * iv));
-              else
-                *(float4*)((float*)p.out + o) = make_float4(acc.x * iv, acc.y * iv, acc.z * iv, acc.w * iv);
+            bar_sync(6, kSoft);
+            for (int e = tid; e < nb * (kD / 4); e += kSoft) {
+              const int r = e >> 5, rr = r0 + r, c4 = e & 31;
+              float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+              for (int k = 0; k < np; ++k) {
+                const float x = wt[k * batch + r];
+                const float4 v = __ldcg((const float4*)(piece(k) + (size_t)rr * kD) + c4);
+                if (x != 0.f) {
+                  acc.x = fmaf(x, v.x, acc.x);
+                  acc.y = fmaf(x, v.y, acc.y);
+                  acc.z = fmaf(x, v.z, acc.z);
+                  acc.w = fmaf(x, v.w, acc.w);
+                }
+              }
+              const size_t o =
+                  ((size_t)(first_row + (rr >> p.log_rep)) * p.Hq + (g << p.log_rep) + (rr & (p.rep - 1))) * kD + 4 * c4;
+              if (!W.prompt) {
+                *(float4*)(p.pre_o + o) = acc;
+              } else {
+                const float L = total[r], iv = L == 0.f ? 0.f : 1.0f / L;
+                if constexpr (PARTS == 1)
+                  *(uint2*)((__nv_bfloat16*)p.out + o) = make_uint2(bf2(acc.x * iv, acc.y * iv), bf2(acc.z * iv, acc.w * iv));
+                else
+                  *(float4*)((float*)p.out + o) = make_float4(acc.x * iv, acc.y * iv, acc.z * iv, acc.w * iv);
+              }
             }
+            bar_sync(6, kSoft);
           }
           if (tid == 0) p.tickets[c0] = 0;
-          fence_proxy_async_smem();   // the ring is written by copies again
         }
       }
       tc::fence_before();
@@ -888,7 +996,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ring = ring + (warp == kProducer ? 0 : 2 * n);
     tile += n;
     for (int i = 0; i < n; ++i) fixes += (k0 + i + 1) * kKeys > seen_min;
-    __syncthreads();
+    if (warp != kProducer) bar_sync(7, kThreads - 32);
     tc::fence_after();
     u += n;
     if (u >= u1 || *(volatile int*)s_abort) break;
@@ -904,6 +1012,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
+  __syncwarp();
   if (warp == kProducer && *(volatile int*)s_abort && p.box && lane == 0) {
     // a timeout: the copies that are still under way land before the CTA leaves (bounded)
     for (uint32_t c = ring > kRing ? ring - kRing : 0; c < ring; ++c)
