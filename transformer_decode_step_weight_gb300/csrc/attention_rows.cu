@@ -37,7 +37,6 @@
 
 #include <algorithm>
 #include <cstring>
-#include <type_traits>
 
 namespace qd {
 namespace {
@@ -104,6 +103,15 @@ QD_DEV void ld32(uint32_t taddr, float* v) {   // 32 columns, not waited for
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
         "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+QD_DEV void ld16(uint32_t taddr, float* v) {   // 16 columns, not waited for
+  uint32_t* r = (uint32_t*)v;
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
 }
@@ -223,15 +231,48 @@ QD_DEV float max3(float a, float b, float c) {
   return d;
 }
 
+// A place in the work: row tile t of kv head g of segment s, from key tile k0 on.
+struct Place {
+  int s, g, t, k0;
+  Seg a;
+};
+
+// Values of O that are not finite: what the row sees of V's own NaN and infinities in dims
+// [d0, d0 + 32) of the keys [first, last) decides (the product of a weight's part and an
+// infinity may have given NaN, or an entry was taken out of a masked tile).
+__device__ __noinline__ void patch_row(const Params& p, const int32_t* pt, int g, int first, int last, int d0, float* ov) {
+  float add[32];
+  uint32_t any = 0;
+  for (int k = 0; k < 32; ++k) add[k] = 0.f;
+  for (int key = first; key < last; ++key) {
+    const PagedSlot sl = paged_slot(pt, key, p.page_size, p.n_pages);
+    const __nv_bfloat16* v = p.v_pages + (((size_t)sl.page * p.Hkv + g) * p.page_size + sl.slot) * kD + d0;
+    for (int k = 0; k < 32; ++k) {
+      const float f = __bfloat162float(v[k]);
+      if (!(fabsf(f) < INFINITY)) {
+        add[k] += f;
+        any |= 1u << k;
+      }
+    }
+  }
+  for (int k = 0; k < 32; ++k)
+    if ((any >> k) & 1) ov[k] = add[k];
+}
+
 template <typename T, int PARTS, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p) {
+    attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                     const __grid_constant__ Params p) {
   static_assert(PARTS == 1 || NT == 1, "");
-  constexpr int kQ = PARTS * NT;              // Q slots
-  constexpr int kRing = 7 - kQ < kMaxSlots ? 7 - kQ : kMaxSlots;
+  constexpr int kQBufs = PARTS == 1 ? 2 : 1;  // Q of the next piece is loaded during this one
+  constexpr int kQ1 = PARTS * NT;             // slots of one Q
+  constexpr int kQ = kQ1 * kQBufs;
+  constexpr int kRing = 7 - kQ;
+  constexpr int kAhead = NT == 1 ? 2 : 1;     // K tiles in the ring before the first V tile
   constexpr int kCols = NT == 2 ? 128 : 64;   // keys of a tile per softmax thread
   constexpr int kOCols = NT == 2 ? 128 : 64;  // O columns per softmax thread
   constexpr bool kFresh = PARTS == 3;         // O of each tile alone in TMEM, summed in registers
+  static_assert(kRing >= 3 && kRing <= kMaxSlots, "");
   extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char* data = smem + kMisc;
   uint64_t* full = (uint64_t*)smem;      // [kRing] a K or V tile landed
@@ -239,13 +280,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* s_full = empty + kMaxSlots;  // [2] S in buffer b
   uint64_t* p_full = s_full + 2;         // [2] the weights in buffer b, O rescaled
   uint64_t* o_done = p_full + 2;         // [2] the P V products of buffer b done
-  uint64_t* v_go = o_done + 2;           // a masked V tile landed (the issuer saw it)
+  uint64_t* q_full = o_done + 2;         // [kQBufs] Q of a piece
+  uint64_t* v_go = q_full + 2;           // a masked V tile landed (the issuer saw it)
   uint64_t* v_fixed = v_go + 1;          // ... and was put right
   uint32_t* tslot = (uint32_t*)(v_fixed + 1);
   int* s_abort = (int*)(tslot + 1);
-  int* s_patch = s_abort + 1;            // the last piece with NaN or infinities in a masked V tile
-  int* s_last = s_patch + 1;
-  long long* s_find = (long long*)(smem + 256);   // [0] segment, [1] units before it, [2] U, [3] bad
+  int* s_patch = s_abort + 1;            // [2] the last piece with NaN or infinities in a masked V tile
+  int* s_last = s_patch + 2;
+  long long* s_find = (long long*)(smem + 256);   // [0] segment, [1] units before it, [2] U
   long long* s_scan = (long long*)(smem + 320);   // [warps] sums of the scan
   float* xm = (float*)(smem + 512);               // [2][2][128] traded maxima and sums
 
@@ -254,7 +296,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   W.prompt = p.shared_lens == nullptr;
   W.log_tpt = (NT == 2 ? 8 : 7) - p.log_rep;
   pdl_launch_dependents();
-
   if (smem_u32(smem) & 1023u) {   // the swizzled tiles rest on it (there is no static shared memory)
     if (tid == 0) set_error(p.err, QD_DEVERR_TIMEOUT);
     return;
@@ -312,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   if (tid == 0) {
-    for (int i = 0; i < kMaxSlots; ++i) {
+    for (int i = 0; i < kRing; ++i) {
       mbar_init(&full[i], p.box ? 1 : 32);
       mbar_init(&empty[i], 1);
     }
@@ -320,11 +361,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], NT == 2 ? kRows : kSoft);
       mbar_init(&o_done[i], 1);
+      mbar_init(&q_full[i], kSoft);
+      s_patch[i] = 0;
     }
     mbar_init(v_go, 1);
     mbar_init(v_fixed, 64);
     fence_mbar_init();
-    *s_patch = 0;
   }
   if (warp == 0) tc::alloc(tslot, 512);
   tc::fence_before();
@@ -352,32 +394,50 @@ __global__ void __launch_bounds__(kThreads, 1)
     *(volatile int*)s_abort = 1;
   };
 
-  // position of unit u
-  int s = (int)s_find[0];
-  Seg a = W.seg(p, s);
-  const long long head_units = W.before(a, a.tiles);
-  int g = (int)quot(u - s_find[1], head_units);
-  const long long w = u - s_find[1] - g * head_units;
-  int t = 0;
-  for (int lo = 0, hi = a.tiles; hi - lo > 1;) {   // the last row tile whose units start at or before w
-    const int mid = (lo + hi) / 2;
-    if (W.before(a, mid) <= w) lo = mid; else hi = mid;
-    t = lo;
+  // the place of unit u
+  Place at;
+  {
+    at.s = (int)s_find[0];
+    at.a = W.seg(p, at.s);
+    const long long head_units = W.before(at.a, at.a.tiles);
+    at.g = (int)quot(u - s_find[1], head_units);
+    const long long w = u - s_find[1] - at.g * head_units;
+    int lo = 0;
+    for (int hi = at.a.tiles; hi - lo > 1;) {   // the last row tile whose units start at or before w
+      const int mid = (lo + hi) / 2;
+      if (W.before(at.a, mid) <= w) lo = mid; else hi = mid;
+    }
+    at.t = lo;
+    at.k0 = (int)(w - W.before(at.a, lo));
   }
-  int k0 = (int)(w - W.before(a, t));
-  // running counts, the same in every role that uses them: ring entries, tiles, fixed tiles,
-  // trades. The producer runs ahead into the next piece; the others meet at its end.
-  uint32_t ring = 0, tile = 0, fixes = 0, trades = 0;
-  int piece_no = 0, late = -1;
+  // the next row tile (the place after the last unit is not asked for)
+  auto advance = [&](Place& x) {
+    x.k0 = 0;
+    if (++x.t < x.a.tiles) return;
+    x.t = 0;
+    if (++x.g < p.Hkv) return;
+    x.g = 0;
+    do {
+      x.a = W.seg(p, ++x.s);
+    } while (x.a.tiles == 0);
+  };
+
+  // A piece is the part of one row tile that this CTA computes. Each role walks the pieces for
+  // itself, so the copies and products of one run into the next; counts that several roles
+  // follow: ring entries, tiles, fixed tiles, trades, pieces.
+  uint32_t ring = 0, tile = 0, fixes = 0, trades = 0, piece_no = 0;
+  int late = -1;
+  [[maybe_unused]] bool first = true;
 
   while (true) {
-    // ================= one piece: row tile t of kv head g, key tiles k0 .. k1 - 1 of nk
-    ++piece_no;
+    const Seg& a = at.a;
+    const int g = at.g, t = at.t, k0 = at.k0;
     const int nk = W.units(a, t);
     const int k1 = (int)min((long long)nk, k0 + (u1 - u));
     const int n = k1 - k0;
-    const int first_row = a.row0 + (t << W.log_tpt);                   // packed row
-    const int packed = min(W.tpt(), a.n - (t << W.log_tpt));             // packed rows in the tile
+    const bool more = u + n < u1;
+    const int first_row = a.row0 + (t << W.log_tpt);            // packed row
+    const int packed = min(W.tpt(), a.n - (t << W.log_tpt));    // packed rows in the tile
     const int seen_max = W.seen(a, t);                          // keys past it are nobody's
     int seen_min;                                               // keys before it are everybody's
     if (W.prompt) {
@@ -390,13 +450,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       seen_min = __reduce_min_sync(0xffffffffu, m);
     }
-    const int32_t* pt = p.page_table + (size_t)(W.prompt ? s : a.row0) * p.max_pages;
+    const int32_t* pt = p.page_table + (size_t)(W.prompt ? at.s : a.row0) * p.max_pages;
 
     if (warp == kProducer) {
       // ---- K and V tiles in the order of the products. A lane's cache rows of a tile are
       // looked up once, for K and V, a tile ahead of their use. TMA: lane l, box l / 2 and
       // dims 64 (l & 1); asynchronous copies: keys l, l + 32, ... (-1: past the keys)
-      constexpr int kAhead = NT == 1 ? 2 : 1;   // K tiles issued before the first V tile
       constexpr int kMine = 4;
       struct Look {
         int row[kMine];
@@ -474,23 +533,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       // NaN and infinities in the others taken out
       // (the issuer says when: a slot's own barrier may be several phases behind a tile that is
       // still to come, which a wait on its parity cannot tell)
-      uint32_t r = ring + (NT == 1 && n > 1 ? 2 : 1), fx = fixes;
+      uint32_t r = ring + (n > 1 ? kAhead : 1);
       for (int i = 0; i < n; ++i) {
         const int key0 = (k0 + i) * kKeys;
         if (key0 + kKeys > seen_min) {
           const uint32_t slot = r % kRing;
-          wait(v_go, fx++ & 1);
+          wait(v_go, fixes++ & 1);
           wait(&full[slot], (r / kRing) & 1);   // done; orders the copy before this thread's reads
           unsigned char* v = data + (kQ + slot) * kSlot;
           const int lo = max(0, seen_min - key0), hi = seen_max - key0;
 #pragma unroll 4
           for (int e = lo * 16 + tid - 32 * kFixer; e < kKeys * 16; e += 64) {
             const int key = e >> 4, c = e & 15;
-            uint4* at = (uint4*)(v + (c >> 3) * kChunk + tc::sw128_off(key, c & 7));
+            uint4* cell = (uint4*)(v + (c >> 3) * kChunk + tc::sw128_off(key, c & 7));
             if (key >= hi) {
-              *at = make_uint4(0u, 0u, 0u, 0u);
+              *cell = make_uint4(0u, 0u, 0u, 0u);
             } else {
-              uint32_t x[4] = {at->x, at->y, at->z, at->w};
+              uint32_t x[4] = {cell->x, cell->y, cell->z, cell->w};
               bool hit = false;
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
@@ -498,168 +557,117 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if ((x[j] & 0x7f800000u) == 0x7f800000u) { x[j] &= 0xffffu; hit = true; }
               }
               if (hit) {
-                *at = make_uint4(x[0], x[1], x[2], x[3]);
-                *(volatile int*)s_patch = piece_no;
+                *cell = make_uint4(x[0], x[1], x[2], x[3]);
+                *(volatile int*)(s_patch + (piece_no & 1)) = (int)piece_no + 1;
               }
             }
           }
           fence_proxy_async_smem();
           mbar_arrive(v_fixed);
         }
-        r += i + (NT == 1 ? 2 : 1) < n ? 2 : 1;
+        r += i + kAhead < n ? 2 : 1;
       }
-    }
-
-    if (warp < kSoftWarps) {
-      // ---- Q
-      const T* q = (const T*)p.q;
-      const int rows = packed << p.log_rep;
-      if constexpr (PARTS == 1) {
-        // warp w copies rows 16 NT w .. of the row tile(s) as they are, two rows at a time
-        constexpr int kPer = 16 * NT;
-        const uint32_t d0 = smem_u32(data);
-        const int c = lane & 15;
-#pragma unroll 4
-        for (int i = 0; i < kPer; i += 2) {
-          const int r = warp * kPer + i + (lane >> 4);
-          const bool ok = r < rows;
-          const T* src = q + (long long)(first_row + (ok ? r >> p.log_rep : 0)) * p.q_stride +
-                         (long long)((g << p.log_rep) + (ok ? r & (p.rep - 1) : 0)) * kD + 8 * c;
-          cp16(d0 + (r >> 7) * kSlot + (c >> 3) * kChunk + tc::sw128_off(r & (kRows - 1), c & 7), src, ok ? 16 : 0);
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        if (p.q_sign < 0.f) {   // a negative scale: this thread's pieces negated
-          for (int i = 0; i < kPer; i += 2) {
-            const int r = warp * kPer + i + (lane >> 4);
-            uint4* at = (uint4*)(data + (r >> 7) * kSlot + (c >> 3) * kChunk + tc::sw128_off(r & (kRows - 1), c & 7));
-            const uint4 v = *at;
-            *at = make_uint4(v.x ^ 0x80008000u, v.y ^ 0x80008000u, v.z ^ 0x80008000u, v.w ^ 0x80008000u);
-          }
-        }
-      } else {
-        // warp w splits rows 16 w ..; lane: dims 4 lane .. + 3
-        float4 f[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int r = warp * 16 + i;
-          const bool ok = r < rows;
-          const T* src = q + (long long)(first_row + (ok ? r >> p.log_rep : 0)) * p.q_stride +
-                         (long long)((g << p.log_rep) + (ok ? r & (p.rep - 1) : 0)) * kD + 4 * lane;
-          f[i] = ok ? *(const float4*)src : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint32_t o = (uint32_t)((lane >> 4) * kChunk) + tc::sw128_off(warp * 16 + i, (lane & 15) >> 1) +
-                             (uint32_t)((lane & 1) * 8);
-          float x[4] = {f[i].x * p.q_sign, f[i].y * p.q_sign, f[i].z * p.q_sign, f[i].w * p.q_sign};
-#pragma unroll
-          for (int part = 0; part < PARTS; ++part) {
-            const uint32_t b0 = bf2(x[0], x[1]), b1 = bf2(x[2], x[3]);
-            *(uint2*)(data + part * kSlot + o) = make_uint2(b0, b1);
-            x[0] -= bf_lo(b0); x[1] -= bf_hi(b0); x[2] -= bf_lo(b1); x[3] -= bf_hi(b1);
-          }
-        }
-      }
-      fence_proxy_async_smem();
-    }
-    if (warp <= kIssuer) bar_sync(1, kSoft + 32);   // Q is there
-
-    if (warp == kIssuer) {
+      ring += 2 * n;
+    } else if (warp == kIssuer) {
       if (lane == 0) {
         // ---- the products, in the order K0 (K1) V0 K2 V1 ... of the ring
-        const uint32_t dq = smem_u32(data);
-        uint32_t r = ring, fx = fixes;
+        const uint64_t dq = tc::desc_sw128(smem_u32(data + (kQBufs == 2 ? piece_no & 1 : 0) * kQ1 * kSlot));
         auto slot_of = [&](uint32_t c) { return smem_u32(data + (kQ + c % kRing) * kSlot); };
+        auto wait_full = [&](uint32_t c) { wait(&full[c % kRing], (c / kRing) & 1); };
         auto live = [&] { return *(volatile int*)s_abort == 0; };
-        // S of row tile j (buffer b) from the K tile in slot c
+        // S of row tile j into buffer b from a K tile; small parts first
         auto mma_s = [&](int j, int b, uint32_t kaddr) {
-#pragma unroll
-          for (int part = PARTS - 1; part >= 0; --part)
+          const uint64_t dk = tc::desc_sw128(kaddr);
+          uint32_t acc = 0;
+#pragma unroll 1
+          for (int part = PARTS - 1; part >= 0; --part) {
+            const uint64_t da = dq + (uint64_t)((j + part) * kSlot >> 4);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
-              const uint32_t o = (kk >> 2) * kChunk + (kk & 3) * 32;
-              tc::mma<kKeys>(tS + 128 * b, tc::desc_sw128(dq + (j + part) * kSlot + o), tc::desc_sw128(kaddr + o),
-                             part != PARTS - 1 || kk != 0);
+              constexpr int kHalf = kChunk >> 4;
+              const uint64_t o = (kk >> 2) * kHalf + (kk & 3) * 2;
+              tc::mma<kKeys>(tS + 128 * b, da + o, dk + o, acc);
+              acc = 1;
             }
+          }
           tc::commit(&s_full[b]);
         };
-        auto mma_o = [&](int b, uint32_t to, uint32_t vaddr, bool first) {
-#pragma unroll
-          for (int part = PARTS - 1; part >= 0; --part)
+        auto mma_o = [&](int b, uint32_t to, uint32_t vaddr, uint32_t acc) {
+          const uint64_t dv = desc_v(vaddr);
+#pragma unroll 1
+          for (int part = PARTS - 1; part >= 0; --part) {
+            // NT 2: 64 columns of pairs of keys; NT 1: 32 keys' weights over their own 32 scores
+            const uint32_t ta = part < 2 ? tS + 128 * b + 16 * part : tX + 64 * b;
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
-              uint32_t ta = tS + 128 * b + 8 * kk;   // NT 2: 64 columns of pairs of keys
-              if (NT == 1)                           // NT 1: 32 keys' weights over their own 32 scores
-                ta = part < 2 ? tS + 128 * b + 32 * (kk >> 1) + 16 * part + 8 * (kk & 1) : tX + 64 * b + 8 * kk;
-              mma_pv(to, ta, desc_v(vaddr + kk * 2048), !first || part != PARTS - 1 || kk != 0);
+              const uint32_t o = NT == 2 || part == 2 ? 8 * kk : 32 * (kk >> 1) + 8 * (kk & 1);
+              mma_pv(to, ta + o, dv + (uint64_t)(kk * 2048 >> 4), acc);
+              acc = 1;
             }
+          }
           tc::commit(&o_done[b]);
         };
-        auto s_tile = [&](int i) {   // takes the next K tile of the ring
-          wait(&full[r % kRing], (r / kRing) & 1);
-          tc::fence_after();
-          if (live()) {
-            mma_s(0, (tile + i) & 1, slot_of(r));
-            tc::commit(&empty[r % kRing]);
+        auto v_ready = [&](int i, uint32_t c) {
+          wait_full(c);
+          if ((k0 + i + 1) * kKeys > seen_min) {
+            mbar_arrive(v_go);
+            wait(v_fixed, fixes++ & 1);
           }
-          ++r;
         };
+        if (kQBufs == 2) wait(&q_full[piece_no & 1], (piece_no >> 1) & 1);
+        else wait(&q_full[0], piece_no & 1);
         if constexpr (NT == 1) {
-          s_tile(0);
-          if (n > 1) s_tile(1);
-          for (int i = 0; i < n; ++i) {
-            const int b = (tile + i) & 1;
-            wait(&full[r % kRing], (r / kRing) & 1);
-            if ((k0 + i + 1) * kKeys > seen_min) {
-              mbar_arrive(v_go);
-              wait(v_fixed, fx++ & 1);
-            }
-            wait(&p_full[b], ((tile + i) >> 1) & 1);
-            tc::fence_after();
-            if (live()) {
-              mma_o(b, tO, slot_of(r), kFresh || i == 0);
-              tc::commit(&empty[r % kRing]);
-            }
-            ++r;
-            if (i + 2 < n) s_tile(i + 2);
-          }
-        } else {
-          wait(&full[r % kRing], (r / kRing) & 1);
-          tc::fence_after();
-          if (live()) {
-            mma_s(0, 0, slot_of(r));
-            mma_s(1, 1, slot_of(r));
-            tc::commit(&empty[r % kRing]);
-          }
-          ++r;
-          for (int i = 0; i < n; ++i) {
-            const uint32_t rv = r, rk = r + 1;
-            wait(&full[rv % kRing], (rv / kRing) & 1);
-            if ((k0 + i + 1) * kKeys > seen_min) {
-              mbar_arrive(v_go);
-              wait(v_fixed, fx++ & 1);
-            }
-            if (i + 1 < n) wait(&full[rk % kRing], (rk / kRing) & 1);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              wait(&p_full[j], (tile + i) & 1);
+          // S runs two tiles ahead of P V
+#pragma unroll 1
+          for (int i = -2; i < n; ++i) {
+            if (i >= 0) {
+              const uint32_t ct = tile + i;
+              v_ready(i, ring);
+              wait(&p_full[ct & 1], (ct >> 1) & 1);
               tc::fence_after();
               if (live()) {
-                mma_o(j, tO + 128 * j, slot_of(rv), i == 0);
-                if (j) tc::commit(&empty[rv % kRing]);
+                mma_o(ct & 1, tO, slot_of(ring), !kFresh && i > 0);
+                tc::commit(&empty[ring % kRing]);
+              }
+              ++ring;
+            }
+            if (i + 2 < n) {
+              wait_full(ring);
+              tc::fence_after();
+              if (live()) {
+                mma_s(0, (tile + i + 2) & 1, slot_of(ring));
+                tc::commit(&empty[ring % kRing]);
+              }
+              ++ring;
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int i = -1; i < n; ++i) {
+            const uint32_t rv = ring, rk = ring + (i >= 0);
+            if (i >= 0) v_ready(i, rv);
+            if (i + 1 < n) wait_full(rk);
+#pragma unroll 1
+            for (int j = 0; j < 2; ++j) {
+              if (i >= 0) wait(&p_full[j], (tile + i) & 1);
+              tc::fence_after();
+              if (live()) {
+                if (i >= 0) {
+                  mma_o(j, tO + 128 * j, slot_of(rv), i > 0);
+                  if (j) tc::commit(&empty[rv % kRing]);
+                }
                 if (i + 1 < n) {
                   mma_s(j, j, slot_of(rk));
                   if (j) tc::commit(&empty[rk % kRing]);
                 }
               }
             }
-            r += i + 1 < n ? 2 : 1;
+            ring += (i >= 0) + (i + 1 < n);
           }
         }
       }
       __syncwarp();
-    } else if (warp < kSoftWarps) {
+    } else {
       // ---- softmax. NT 1: warps w and w + 4 hold the same rows (TMEM lanes), 64 keys and 64
       // O columns each; NT 2: warps 4 .. 7 hold the second row tile.
       const int hf = warp >> 2, lr = (warp & 3) * 32 + lane;
@@ -667,7 +675,84 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rows = packed << p.log_rep;
       const bool valid = row < rows;
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-      const uint32_t to = NT == 2 ? tO + 128 * hf : tO + 64 * hf;
+      const uint32_t to = (NT == 2 ? tO + 128 * hf : tO + 64 * hf) + lanes;
+      unsigned char* qbuf = data + (kQBufs == 2 ? piece_no & 1 : 0) * kQ1 * kSlot;
+
+      // Q of the row tile at x; the copies are waited for in q_ready
+      auto q_load = [&](const Place& x, unsigned char* dst) {
+        const T* q = (const T*)p.q + (long long)(x.a.row0 + (x.t << W.log_tpt)) * p.q_stride +
+                     (long long)(x.g << p.log_rep) * kD;
+        const int qrows = min(W.tpt(), x.a.n - (x.t << W.log_tpt)) << p.log_rep;
+        if constexpr (PARTS == 1) {
+          // warp w copies rows 16 NT w .. of the row tile(s) as they are, two rows at a time
+          constexpr int kPer = 16 * NT;
+          const uint32_t d0 = smem_u32(dst);
+          const int c = lane & 15;
+#pragma unroll 4
+          for (int i = 0; i < kPer; i += 2) {
+            const int r = warp * kPer + i + (lane >> 4), ok = r < qrows ? r : 0;
+            cp16(d0 + (r >> 7) * kSlot + (c >> 3) * kChunk + tc::sw128_off(r & (kRows - 1), c & 7),
+                 q + (long long)(ok >> p.log_rep) * p.q_stride + (ok & (p.rep - 1)) * kD + 8 * c, r < qrows ? 16 : 0);
+          }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+        } else {
+          // warp w splits rows 16 w ..; lane: dims 4 lane .. + 3
+#pragma unroll 1
+          for (int i0 = 0; i0 < 16; i0 += 8) {
+            float4 f[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int r = warp * 16 + i0 + i;
+              f[i] = r < qrows ? *(const float4*)(q + (long long)(r >> p.log_rep) * p.q_stride + (r & (p.rep - 1)) * kD + 4 * lane)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t o = (uint32_t)((lane >> 4) * kChunk) + tc::sw128_off(warp * 16 + i0 + i, (lane & 15) >> 1) +
+                                 (uint32_t)((lane & 1) * 8);
+              float x4[4] = {f[i].x * p.q_sign, f[i].y * p.q_sign, f[i].z * p.q_sign, f[i].w * p.q_sign};
+#pragma unroll
+              for (int part = 0; part < PARTS; ++part) {
+                const uint32_t b0 = bf2(x4[0], x4[1]), b1 = bf2(x4[2], x4[3]);
+                *(uint2*)(dst + part * kSlot + o) = make_uint2(b0, b1);
+                x4[0] -= bf_lo(b0); x4[1] -= bf_hi(b0); x4[2] -= bf_lo(b1); x4[3] -= bf_hi(b1);
+              }
+            }
+          }
+        }
+      };
+      auto q_ready = [&](unsigned char* dst, uint64_t* bar) {
+        if constexpr (PARTS == 1) {
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
+          if (p.q_sign <= 0.f) {   // a negative scale: this thread's pieces negated; none: zeros
+            constexpr int kPer = 16 * NT;
+            const int c = lane & 15;
+            const uint32_t keep = p.q_sign < 0.f ? 0xffffffffu : 0u, flip = p.q_sign < 0.f ? 0x80008000u : 0u;
+#pragma unroll 1
+            for (int i = 0; i < kPer; i += 2) {
+              const int r = warp * kPer + i + (lane >> 4);
+              uint4* cell = (uint4*)(dst + (r >> 7) * kSlot + (c >> 3) * kChunk + tc::sw128_off(r & (kRows - 1), c & 7));
+              const uint4 v = *cell;
+              *cell = make_uint4((v.x & keep) ^ flip, (v.y & keep) ^ flip, (v.z & keep) ^ flip, (v.w & keep) ^ flip);
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bar);
+      };
+      Place nx = at;
+      if (first) {
+        q_load(at, qbuf);
+        q_ready(qbuf, &q_full[0]);
+        first = false;
+      }
+      if (more) advance(nx);
+      unsigned char* qnext = data + (kQBufs == 2 ? ~piece_no & 1 : 0) * kQ1 * kSlot;
+      if (kQBufs == 2 && more) {
+        bar_sync(6, kSoft);   // nobody still uses the place for the piece before
+        q_load(nx, qnext);
+      }
+
       int lim = 0;   // keys this row sees
       if (valid) {
         const int j = (t << W.log_tpt) + (row >> p.log_rep);
@@ -678,9 +763,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           lim = l < 0 || l > p.cap ? 0 : min(l, a.len);
         }
       }
+      // what all valid rows of the warp see (rows that are not valid hold anything)
+      const int warp_min = __reduce_min_sync(0xffffffffu, valid ? lim : INT32_MAX);
       const float c = p.scale_log2;
       float ms = -INFINITY, l = 0.f;
-      float osum[kFresh ? kOCols : 1];
+      [[maybe_unused]] float osum[kFresh ? kOCols : 1];
       if constexpr (kFresh) {
 #pragma unroll
         for (int k = 0; k < kOCols; ++k) osum[k] = 0.f;
@@ -692,35 +779,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         bar_sync(2 + (warp & 3), 64);
         return xm[(par * 2 + (hf ^ 1)) * kRows + lr];
       };
+#pragma unroll 1
       for (int i = 0; i < n; ++i) {
         const uint32_t ct = tile + i;
         const int b = NT == 2 ? hf : (int)(ct & 1);
-        const uint32_t ph = NT == 2 ? ct & 1 : (ct >> 1) & 1;
-        wait(&s_full[b], ph);
-        tc::fence_after();
         const int key0 = (k0 + i) * kKeys + (NT == 2 ? 0 : 64 * hf);
         const uint32_t ts = tS + 128 * b + lanes + (NT == 2 ? 0 : 64 * hf);
-        const bool masked = (k0 + i + 1) * kKeys > seen_min;   // the same for the whole CTA
-        // the scores are read twice, 64 at a time (for the maximum, for the weights): registers
-        // for all of them are not left beside O
-        float mx = -INFINITY;
+        // 32 scores; those of keys that the row does not see become -inf
+        auto mask = [&](float* sv, int key) {
+          if (key + 32 > warp_min) {
 #pragma unroll
-        for (int e0 = 0; e0 < kCols; e0 += 64) {
-          float sv[64];
-          ld32(ts + e0, sv);
-          ld32(ts + e0 + 32, sv + 32);
-          wait_ld();
-          if (masked) {
-#pragma unroll
-            for (int e = 0; e < 64; ++e)
-              if (key0 + e0 + e >= lim) sv[e] = -INFINITY;
+            for (int e = 0; e < 32; ++e) sv[e] = key + e < lim ? sv[e] : -INFINITY;
           }
-          float m4[4] = {mx, mx, mx, mx};
+        };
+        auto top = [&](const float* sv, float m) {
+          float m4[4] = {m, m, m, m};
 #pragma unroll
-          for (int e = 0; e < 64; e += 8)
+          for (int e = 0; e < 32; e += 8)
 #pragma unroll
             for (int k = 0; k < 4; ++k) m4[k] = max3(m4[k], sv[e + 2 * k], sv[e + 2 * k + 1]);
-          mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
+          return fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
+        };
+        wait(&s_full[b], NT == 2 ? ct & 1 : (ct >> 1) & 1);
+        tc::fence_after();
+        float mx = -INFINITY;
+        // f32: the scores are read twice (for the maximum, for the weights), since registers for
+        // all of them are not left beside O
+        constexpr bool kOnce = !kFresh;
+        float sv[kOnce ? kCols : 32];
+        if constexpr (kOnce) {
+#pragma unroll
+          for (int e = 0; e < kCols; e += 32) ld32(ts + e, sv + e);
+          wait_ld();
+#pragma unroll
+          for (int e = 0; e < kCols; e += 32) {
+            mask(sv + e, key0 + e);
+            mx = top(sv + e, mx);
+          }
+        } else {
+#pragma unroll 1
+          for (int e = 0; e < kCols; e += 32) {
+            ld32(ts + e, sv);
+            wait_ld();
+            mask(sv, key0 + e);
+            mx = top(sv, mx);
+          }
         }
         if (NT == 1) mx = fmaxf(mx, trade(mx));
         mx = mx == -INFINITY ? mx : mx * c;
@@ -729,64 +832,66 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (!kFresh) {
           // the barrier of the products before the last ones: already complete (they were issued
           // before this S), waited for so that the phases are followed one by one
-          if (NT == 1 && ct >= 2) wait(&o_done[b], ((ct - 2) >> 1) & 1);
+          if (NT == 1 && i >= 2) wait(&o_done[b], ((ct - 2) >> 1) & 1);
           if (NT == 2 && i > 0) wait(&o_done[b], (ct - 1) & 1);
           if (i > 0 && __any_sync(0xffffffffu, move)) {
             if (NT == 1) wait(&o_done[b ^ 1], ((ct - 1) >> 1) & 1);
             tc::fence_after();
+#pragma unroll 1
+            for (int e = 0; e < kOCols; e += 16) {
+              float ov[16];
+              ld16(to + e, ov);
+              wait_ld();
 #pragma unroll
-            for (int e = 0; e < kOCols; e += 32) {
-              float ov[32];
-              tc::ld_32x32(to + lanes + e, ov);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) ov[k] *= alpha;
-              tc::st_32x32(to + lanes + e, ov);
+              for (int k = 0; k < 16; ++k) ov[k] *= alpha;
+              st16(to + e, (const uint32_t*)ov);
             }
+            wait_st();
           }
         }
         if (move) {
           l *= alpha;
           ms = mx;
         }
-        const uint64_t c2 = pack2(c, c), nm2 = pack2(-ms, -ms);
+        // a row that has seen nothing yet: weights 2^(-inf - 0)
+        const float neg = ms == -INFINITY ? 0.f : -ms;
+        const uint64_t c2 = pack2(c, c), nm2 = pack2(neg, neg);
         uint64_t ps[2] = {0, 0};   // pairs of sums, +0 each
-        auto weights = [&](auto with_mask) {
+        auto weights = [&](const float* s32, int e0) {
+          uint32_t w0[16];
+          [[maybe_unused]] uint32_t w1[PARTS == 3 ? 16 : 1], w2[PARTS == 3 ? 16 : 1];
 #pragma unroll
-          for (int e0 = 0; e0 < kCols; e0 += 32) {
-            float sv[32];
-            ld32(ts + e0, sv);
-            wait_ld();
-            uint32_t w0[16];
-            [[maybe_unused]] uint32_t w1[PARTS == 3 ? 16 : 1], w2[PARTS == 3 ? 16 : 1];
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float x, y;
-              unpack2(fma2(pack2(sv[e], sv[e + 1]), c2, nm2), x, y);
-              x = ex2(x);
-              y = ex2(y);
-              if constexpr (decltype(with_mask)::value) {   // a masked score gives 0 (also where ms is still -inf, or c is 0)
-                x = key0 + e0 + e < lim ? x : 0.f;
-                y = key0 + e0 + e + 1 < lim ? y : 0.f;
-              }
-              ps[(e >> 1) & 1] = add2(ps[(e >> 1) & 1], pack2(x, y));
-              w0[e / 2] = bf2(x, y);
-              if constexpr (PARTS == 3) {
-                x -= bf_lo(w0[e / 2]);
-                y -= bf_hi(w0[e / 2]);
-                w1[e / 2] = bf2(x, y);
-                w2[e / 2] = bf2(x - bf_lo(w1[e / 2]), y - bf_hi(w1[e / 2]));
-              }
-            }
-            st16(NT == 2 ? ts + e0 / 2 : ts + e0, w0);   // over scores that have been read
+          for (int e = 0; e < 32; e += 2) {
+            float x, y;
+            unpack2(fma2(pack2(s32[e], s32[e + 1]), c2, nm2), x, y);
+            x = ex2(x);
+            y = ex2(y);
+            ps[(e >> 1) & 1] = add2(ps[(e >> 1) & 1], pack2(x, y));
+            w0[e / 2] = bf2(x, y);
             if constexpr (PARTS == 3) {
-              st16(ts + e0 + 16, w1);
-              st16(tX + 64 * b + lanes + 32 * hf + e0 / 2, w2);
+              x -= bf_lo(w0[e / 2]);
+              y -= bf_hi(w0[e / 2]);
+              w1[e / 2] = bf2(x, y);
+              w2[e / 2] = bf2(x - bf_lo(w1[e / 2]), y - bf_hi(w1[e / 2]));
             }
           }
+          st16(NT == 2 ? ts + e0 / 2 : ts + e0, w0);   // over scores that have been read
+          if constexpr (PARTS == 3) {
+            st16(ts + e0 + 16, w1);
+            st16(tX + 64 * b + lanes + 32 * hf + e0 / 2, w2);
+          }
         };
-        if (masked) weights(std::true_type{});
-        else weights(std::false_type{});
-        if constexpr (kFresh) {
+        if constexpr (kOnce) {
+#pragma unroll
+          for (int e = 0; e < kCols; e += 32) weights(sv + e, e);
+        } else {
+#pragma unroll 1
+          for (int e = 0; e < kCols; e += 32) {
+            ld32(ts + e, sv);
+            wait_ld();
+            mask(sv, key0 + e);
+            weights(sv, e);
+          }
           // O of the tile before, while S of the tile after is made; the next P V products,
           // which overwrite it, wait for this thread
           if (i > 0) {
@@ -795,11 +900,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool any = __any_sync(0xffffffffu, move);
 #pragma unroll
             for (int e = 0; e < kOCols; e += 32) {
-              float ov[32];
-              ld32(to + lanes + e, ov);
+              ld32(to + e, sv);
               wait_ld();
 #pragma unroll
-              for (int k = 0; k < 32; ++k) osum[e + k] += ov[k];
+              for (int k = 0; k < 32; ++k) osum[e + k] += sv[k];
             }
             if (any)
 #pragma unroll
@@ -815,107 +919,104 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_before();
         mbar_arrive(&p_full[b]);
       }
+      if (kQBufs == 2 && more) q_ready(qnext, &q_full[~piece_no & 1]);
+
       // ---- the piece's O, m, l
+      const uint32_t ce = tile + n;
       if (NT == 1) {
-        if (!kFresh && tile + n >= 2) wait(&o_done[(tile + n) & 1], ((tile + n - 2) >> 1) & 1);
-        wait(&o_done[(tile + n - 1) & 1], ((tile + n - 1) >> 1) & 1);
+        if (!kFresh && n >= 2) wait(&o_done[ce & 1], ((ce - 2) >> 1) & 1);
+        wait(&o_done[(ce - 1) & 1], ((ce - 1) >> 1) & 1);
         const float other = trade(l);
         l = hf == 0 ? l + other : other + l;
       } else {
-        wait(&o_done[hf], (tile + n - 1) & 1);
+        wait(&o_done[hf], (ce - 1) & 1);
       }
       tc::fence_after();
-      const bool dead_now = *(volatile int*)s_abort != 0;
+      const bool dead = *(volatile int*)s_abort != 0;
       const bool whole = k0 == 0 && k1 == nk;
       float* part = p.part + ((size_t)blockIdx.x * 2 + (k0 == 0 ? 1 : 0)) * kPartFloats;
-      const bool patch = *(volatile int*)s_patch == piece_no;
-      const int pr = valid ? row >> p.log_rep : 0;
-      const size_t orow = ((size_t)(first_row + pr) * p.Hq + (g << p.log_rep) + (valid ? row & (p.rep - 1) : 0));
+      const bool patch = *(volatile int*)(s_patch + (piece_no & 1)) == (int)piece_no + 1;
+      auto out_row = [&](int r) {   // (packed row, q head) of row r of the tile
+        return (size_t)(first_row + (r >> p.log_rep)) * p.Hq + (g << p.log_rep) + (r & (p.rep - 1));
+      };
       const int col0 = NT == 2 ? 0 : 64 * hf;
       const float inv = l == 0.f ? 0.f : 1.0f / l;   // a row that saw nothing gives 0
+      const bool final_out = whole && W.prompt;      // else O as it is, with m and l
+      // bf16 results and the f32 form's values go out by whole rows, through the place of this
+      // piece's Q (its products are done): 16-byte pieces, swizzled
+      float* dst_f32 = !whole ? part + (size_t)row * kD : p.pre_o + (valid && !W.prompt ? out_row(row) * kD : 0);
 #pragma unroll(kFresh ? kOCols / 32 : 1)
       for (int e = 0; e < kOCols; e += 32) {
         float ov[32];
-        tc::ld_32x32(to + lanes + e, ov);
+        ld32(to + e, ov);
+        wait_ld();
         if constexpr (kFresh) {
 #pragma unroll
           for (int k = 0; k < 32; ++k) ov[k] += osum[e + k];
         }
-        // a value that is not finite: which of V's own NaN and infinities the row sees decides
-        // (a product of a weight's part and an infinity may have given NaN)
-        bool odd = patch;
+        float z = 0.f;   // 0 unless a value is not finite
 #pragma unroll
-        for (int k = 0; k < 32; ++k) odd = odd || !(fabsf(ov[k]) < INFINITY);
-        if (odd && valid && l == l) {
-          float add[32];
-          uint32_t any = 0;
+        for (int k = 0; k < 32; ++k) z = fmaf(ov[k], 0.f, z);
+        if ((patch || z != 0.f) && valid && l == l) {
+          float tmp[32];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) add[k] = 0.f;
-          const int last = min(lim, k1 * kKeys);
-          for (int key = k0 * kKeys; key < last; ++key) {
-            const PagedSlot sl = paged_slot(pt, key, p.page_size, p.n_pages);
-            const uint4* v = (const uint4*)(p.v_pages + (((size_t)sl.page * p.Hkv + g) * p.page_size + sl.slot) * kD + col0 + e);
+          for (int k = 0; k < 32; ++k) tmp[k] = ov[k];
+          patch_row(p, pt, g, k0 * kKeys, min(lim, k1 * kKeys), col0 + e, tmp);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint4 x = v[k];
-              const uint32_t h[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float f0 = bf_lo(h[j]), f1 = bf_hi(h[j]);
-                if (!(fabsf(f0) < INFINITY)) { add[8 * k + 2 * j] += f0; any |= 1u << (8 * k + 2 * j); }
-                if (!(fabsf(f1) < INFINITY)) { add[8 * k + 2 * j + 1] += f1; any |= 2u << (8 * k + 2 * j); }
-              }
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if ((any >> k) & 1) ov[k] = add[k];
+          for (int k = 0; k < 32; ++k) ov[k] = tmp[k];
         }
-        if (valid && !dead_now) {
-          if (!whole) {
-            float4* o = (float4*)(part + (size_t)row * kD + col0 + e);
+        if (final_out && PARTS == 1) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) o[k] = make_float4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
-          } else if (!W.prompt) {
-            float4* o = (float4*)(p.pre_o + orow * kD + col0 + e);
+          for (int k = 0; k < 4; ++k)
+            *(uint4*)(qbuf + row * 256 + ((((col0 + e) / 8 + k) ^ (row & 15)) << 4)) =
+                make_uint4(bf2(ov[8 * k] * inv, ov[8 * k + 1] * inv), bf2(ov[8 * k + 2] * inv, ov[8 * k + 3] * inv),
+                           bf2(ov[8 * k + 4] * inv, ov[8 * k + 5] * inv), bf2(ov[8 * k + 6] * inv, ov[8 * k + 7] * inv));
+        } else if (PARTS == 3) {
+          const float f = final_out ? inv : 1.f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) o[k] = make_float4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
-          } else if constexpr (PARTS == 1) {   // through the place of Q, 256 bytes a row, pieces swizzled
+          for (int k = 0; k < 8; ++k)
+            *(float4*)(qbuf + row * 512 + ((((col0 + e) / 4 + k) ^ (row & 31)) << 4)) =
+                make_float4(ov[4 * k] * f, ov[4 * k + 1] * f, ov[4 * k + 2] * f, ov[4 * k + 3] * f);
+        } else if (valid && !dead) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              *(uint4*)(data + row * 256 + ((((col0 + e) / 8 + k) ^ (row & 15)) << 4)) =
-                  make_uint4(bf2(ov[8 * k] * inv, ov[8 * k + 1] * inv), bf2(ov[8 * k + 2] * inv, ov[8 * k + 3] * inv),
-                             bf2(ov[8 * k + 4] * inv, ov[8 * k + 5] * inv), bf2(ov[8 * k + 6] * inv, ov[8 * k + 7] * inv));
-          } else {
-            float4* o = (float4*)((float*)p.out + orow * kD + col0 + e);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              o[k] = make_float4(ov[4 * k] * inv, ov[4 * k + 1] * inv, ov[4 * k + 2] * inv, ov[4 * k + 3] * inv);
-          }
+          for (int k = 0; k < 8; ++k)
+            *((float4*)(dst_f32 + col0 + e) + k) = make_float4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
         }
       }
-      if (valid && !dead_now && (NT == 2 || hf == 0)) {
+      if (valid && !dead && !final_out && (NT == 2 || hf == 0)) {
         if (!whole) {
           part[(size_t)kPartRows * kD + row] = ms;
           part[(size_t)kPartRows * kD + kPartRows + row] = l;
-        } else if (!W.prompt) {
-          p.pre_m[orow] = ms;
-          p.pre_l[orow] = l;
+        } else {
+          p.pre_m[out_row(row)] = ms;
+          p.pre_l[out_row(row)] = l;
         }
       }
-      if constexpr (PARTS == 1) {
-        if (whole && W.prompt) {   // out by whole rows, two at a time
-          if (NT == 2) __syncwarp();
-          else bar_sync(2 + (warp & 3), 64);
-          constexpr int kPer = NT == 2 ? 32 : 16;
-          const int r0 = NT == 2 ? warp * 32 : (warp & 3) * 32 + hf * 16;
+      if (final_out || PARTS == 3) {
+        // the rows that this warp's lanes (and their other holders') wrote
+        if (NT == 2) __syncwarp();
+        else bar_sync(2 + (warp & 3), 64);
+        constexpr int kPer = NT == 2 ? 32 : 16;
+        const int r0 = NT == 2 ? warp * 32 : (warp & 3) * 32 + hf * 16;
+        if (!dead) {
+          if constexpr (PARTS == 1) {
+            const int pc = lane & 15;
 #pragma unroll 4
-          for (int i = 0; i < kPer; i += 2) {
-            const int r = r0 + i + (lane >> 4), pc = lane & 15;
-            if (r < rows && !dead_now)
-              *(uint4*)((__nv_bfloat16*)p.out +
-                        ((size_t)(first_row + (r >> p.log_rep)) * p.Hq + (g << p.log_rep) + (r & (p.rep - 1))) * kD + pc * 8) =
-                  *(const uint4*)(data + r * 256 + ((pc ^ (r & 15)) << 4));
+            for (int i = 0; i < kPer; i += 2) {
+              const int r = r0 + i + (lane >> 4);
+              if (r < rows)
+                *(uint4*)((__nv_bfloat16*)p.out + out_row(r) * kD + pc * 8) =
+                    *(const uint4*)(qbuf + r * 256 + ((pc ^ (r & 15)) << 4));
+            }
+          } else {
+#pragma unroll 4
+            for (int i = 0; i < kPer; ++i) {
+              const int r = r0 + i;
+              if (r < rows) {
+                float* d = !whole ? part + (size_t)r * kD : (W.prompt ? (float*)p.out : p.pre_o) + out_row(r) * kD;
+                *(float4*)(d + 4 * lane) = *(const float4*)(qbuf + r * 512 + ((lane ^ (r & 31)) << 4));
+              }
+            }
           }
         }
       }
@@ -932,30 +1033,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int np = c1 - c0 + 1;
           // weights [pieces][batch of rows] and sums [batch] in the place of Q, as many rows at
           // a time as fit
-          const int batch = min(rows, kQ * kSlot / 4 / (np + 1));
-          float* wt = (float*)data;
+          const int batch = min(rows, kQ1 * kSlot / 4 / (np + 1));
+          float* wt = (float*)qbuf;
           float* total = wt + (size_t)np * batch;
           auto piece = [&](int k) { return p.part + ((size_t)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * kPartFloats; };
           for (int r0 = 0; r0 < rows; r0 += batch) {
             const int nb = min(batch, rows - r0);
             for (int r = tid; r < nb; r += kSoft) {
               float M = -INFINITY, L = 0.f;
+#pragma unroll 4
               for (int k = 0; k < np; ++k) {
                 const float m = __ldcg(piece(k) + (size_t)kPartRows * kD + r0 + r);
                 wt[k * batch + r] = m;
                 M = fmaxf(M, m);
               }
+#pragma unroll 4
               for (int k = 0; k < np; ++k) {
                 const float m = wt[k * batch + r], x = m == -INFINITY ? 0.f : ex2(m - M);
+                const float lk = __ldcg(piece(k) + (size_t)kPartRows * kD + kPartRows + r0 + r);
                 wt[k * batch + r] = x;
-                if (x != 0.f) L = fmaf(x, __ldcg(piece(k) + (size_t)kPartRows * kD + kPartRows + r0 + r), L);
+                if (x != 0.f) L = fmaf(x, lk, L);
               }
               total[r] = L;
               if (!W.prompt) {
-                const int rr = r0 + r;
-                const size_t o = (size_t)(first_row + (rr >> p.log_rep)) * p.Hq + (g << p.log_rep) + (rr & (p.rep - 1));
-                p.pre_m[o] = M;
-                p.pre_l[o] = L;
+                p.pre_m[out_row(r0 + r)] = M;
+                p.pre_l[out_row(r0 + r)] = L;
               }
             }
             bar_sync(6, kSoft);
@@ -973,8 +1075,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   acc.w = fmaf(x, v.w, acc.w);
                 }
               }
-              const size_t o =
-                  ((size_t)(first_row + (rr >> p.log_rep)) * p.Hq + (g << p.log_rep) + (rr & (p.rep - 1))) * kD + 4 * c4;
+              const size_t o = out_row(rr) * kD + 4 * c4;
               if (!W.prompt) {
                 *(float4*)(p.pre_o + o) = acc;
               } else {
@@ -991,26 +1092,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc::fence_before();
-    }
-    // counts of the piece, for every role
-    ring = ring + (warp == kProducer ? 0 : 2 * n);
-    tile += n;
-    for (int i = 0; i < n; ++i) fixes += (k0 + i + 1) * kKeys > seen_min;
-    if (warp != kProducer) bar_sync(7, kThreads - 32);
-    tc::fence_after();
-    u += n;
-    if (u >= u1 || *(volatile int*)s_abort) break;
-    // the next piece starts a row tile
-    k0 = 0;
-    if (++t == a.tiles) {
-      t = 0;
-      if (++g == p.Hkv) {
-        g = 0;
-        do {
-          a = W.seg(p, ++s);
-        } while (a.tiles == 0);
+      if (kQBufs == 1 && more) {
+        bar_sync(6, kSoft);   // everybody is done with Q's place
+        q_load(nx, data);
+        q_ready(data, &q_full[0]);
       }
     }
+    tile += n;
+    ++piece_no;
+    u += n;
+    if (!more) break;
+    advance(at);
   }
   __syncwarp();
   if (warp == kProducer && *(volatile int*)s_abort && p.box && lane == 0) {
@@ -1018,6 +1110,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (uint32_t c = ring > kRing ? ring - kRing : 0; c < ring; ++c)
       mbar_wait_limit(&full[c % kRing], (c / kRing) & 1, p.err, 10000000ull);
   }
+  tc::fence_before();
   __syncthreads();
   if (warp == 0) {
     tc::fence_after();
@@ -1047,8 +1140,9 @@ cudaError_t run(const AttnRowsArgs& a, float* pre_o, const Launch& L) {
   while ((1 << p.log_rep) < p.rep) ++p.log_rep;
   p.page_size = a.page_size; p.max_pages = a.max_pages; p.n_pages = a.n_pages;
   p.cap = (long long)a.max_pages * a.page_size;
-  p.scale_log2 = fabsf(a.scale) * kLog2e;
-  p.q_sign = a.scale < 0.f ? -1.f : 1.f;
+  // q takes the sign; a scale of 0 makes q 0, so that masked scores stay -inf times something
+  p.scale_log2 = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;
+  p.q_sign = a.scale < 0.f ? -1.f : a.scale == 0.f ? 0.f : 1.f;
   p.out = a.out;
   p.tickets = (int*)a.workspace;
   p.part = (float*)((unsigned char*)a.workspace + kTicketBytes);
