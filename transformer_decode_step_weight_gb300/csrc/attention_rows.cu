@@ -429,28 +429,48 @@ __global__ void __launch_bounds__(kThreads, 1)
   int late = -1;
   [[maybe_unused]] bool first = true;
 
-  while (true) {
-    const Seg& a = at.a;
-    const int g = at.g, t = at.t, k0 = at.k0;
-    const int nk = W.units(a, t);
-    const int k1 = (int)min((long long)nk, k0 + (u1 - u));
-    const int n = k1 - k0;
-    const bool more = u + n < u1;
-    const int first_row = a.row0 + (t << W.log_tpt);            // packed row
-    const int packed = min(W.tpt(), a.n - (t << W.log_tpt));    // packed rows in the tile
-    const int seen_max = W.seen(a, t);                          // keys past it are nobody's
-    int seen_min;                                               // keys before it are everybody's
+  struct Piece {
+    int g, t, k0, k1, nk, n;
+    bool more;                 // another piece follows
+    int first_row, packed;     // packed rows of the tile: the first, how many
+    int seen_max, seen_min;    // keys past the first are nobody's, keys before the second everybody's
+    const int32_t* pt;
+  };
+  auto piece_at = [&](const Place& x) {
+    const Seg& a = x.a;
+    Piece q;
+    q.g = x.g;
+    q.t = x.t;
+    q.k0 = x.k0;
+    q.nk = W.units(a, x.t);
+    q.k1 = (int)min((long long)q.nk, x.k0 + (u1 - u));
+    q.n = q.k1 - x.k0;
+    q.more = u + q.n < u1;
+    q.first_row = a.row0 + (x.t << W.log_tpt);
+    q.packed = min(W.tpt(), a.n - (x.t << W.log_tpt));
+    q.seen_max = W.seen(a, x.t);
     if (W.prompt) {
-      seen_min = max(0, a.off + (t << W.log_tpt) + 1);
+      q.seen_min = max(0, a.off + (x.t << W.log_tpt) + 1);
     } else {
       int m = a.len;
-      for (int i = lane; i < packed; i += 32) {
-        const int l = p.seq_lens[first_row + i];
+      for (int i = lane; i < q.packed; i += 32) {
+        const int l = p.seq_lens[q.first_row + i];
         m = min(m, l < 0 || l > p.cap ? 0 : l);
       }
-      seen_min = __reduce_min_sync(0xffffffffu, m);
+      q.seen_min = __reduce_min_sync(0xffffffffu, m);
     }
-    const int32_t* pt = p.page_table + (size_t)(W.prompt ? at.s : a.row0) * p.max_pages;
+    q.pt = p.page_table + (size_t)(W.prompt ? x.s : a.row0) * p.max_pages;
+    return q;
+  };
+
+  if (warp >= kSoftWarps) {
+    // the softmax warps take the registers that the others leave (256 x 200 + 128 x 104 of the
+    // 384 x 168 of the launch)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    while (true) {
+    const Piece pc = piece_at(at);
+    const int g = pc.g, k0 = pc.k0, n = pc.n, seen_max = pc.seen_max, seen_min = pc.seen_min;
+    const int32_t* pt = pc.pt;
 
     if (warp == kProducer) {
       // ---- K and V tiles in the order of the products. A lane's cache rows of a tile are
@@ -542,26 +562,35 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait(&full[slot], (r / kRing) & 1);   // done; orders the copy before this thread's reads
           unsigned char* v = data + (kQ + slot) * kSlot;
           const int lo = max(0, seen_min - key0), hi = seen_max - key0;
-#pragma unroll 4
-          for (int e = lo * 16 + tid - 32 * kFixer; e < kKeys * 16; e += 64) {
-            const int key = e >> 4, c = e & 15;
-            uint4* cell = (uint4*)(v + (c >> 3) * kChunk + tc::sw128_off(key, c & 7));
-            if (key >= hi) {
-              *cell = make_uint4(0u, 0u, 0u, 0u);
-            } else {
-              uint32_t x[4] = {cell->x, cell->y, cell->z, cell->w};
-              bool hit = false;
+          // thread: 16-byte piece c of every fourth key, four cells at a time
+          const int ft = tid - 32 * kFixer, c = ft & 15;
+          unsigned char* col = v + (c >> 3) * kChunk;
+          const int split = min(hi, kKeys);
+          int key = lo + (ft >> 4);
+          for (; key < split; key += 16) {
+            uint4 x[4];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                if ((x[j] & 0x7f80u) == 0x7f80u) { x[j] &= 0xffff0000u; hit = true; }
-                if ((x[j] & 0x7f800000u) == 0x7f800000u) { x[j] &= 0xffffu; hit = true; }
-              }
-              if (hit) {
-                *cell = make_uint4(x[0], x[1], x[2], x[3]);
+            for (int j = 0; j < 4; ++j)
+              if (key + 4 * j < split) x[j] = *(const uint4*)(col + tc::sw128_off(key + 4 * j, c & 7));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (key + 4 * j >= split) break;
+              // a half with all exponent bits set borrows into its top bit
+              auto odd = [](uint32_t w) { return ((w & 0x7f807f80u) ^ 0x7f807f80u) - 0x00010001u; };
+              if ((odd(x[j].x) | odd(x[j].y) | odd(x[j].z) | odd(x[j].w)) & 0x80008000u) {
+                uint32_t h[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  if ((h[k] & 0x7f80u) == 0x7f80u) h[k] &= 0xffff0000u;
+                  if ((h[k] & 0x7f800000u) == 0x7f800000u) h[k] &= 0xffffu;
+                }
+                *(uint4*)(col + tc::sw128_off(key + 4 * j, c & 7)) = make_uint4(h[0], h[1], h[2], h[3]);
                 *(volatile int*)(s_patch + (piece_no & 1)) = (int)piece_no + 1;
               }
             }
           }
+          for (key = max(lo, max(hi, 0)) + (ft >> 4); key < kKeys; key += 4)
+            *(uint4*)(col + tc::sw128_off(key, c & 7)) = make_uint4(0u, 0u, 0u, 0u);
           fence_proxy_async_smem();
           mbar_arrive(v_fixed);
         }
@@ -667,7 +696,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-    } else {
+    }
+    tile += n;
+    ++piece_no;
+    u += n;
+    if (!pc.more) break;
+    advance(at);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    while (true) {
+    const Piece pc = piece_at(at);
+    const Seg& a = at.a;
+    const int g = pc.g, t = pc.t, k0 = pc.k0, k1 = pc.k1, nk = pc.nk, n = pc.n;
+    const bool more = pc.more;
+    const int first_row = pc.first_row, packed = pc.packed;
+    const int32_t* pt = pc.pt;
       // ---- softmax. NT 1: warps w and w + 4 hold the same rows (TMEM lanes), 64 keys and 64
       // O columns each; NT 2: warps 4 .. 7 hold the second row tile.
       const int hf = warp >> 2, lr = (warp & 3) * 32 + lane;
@@ -1097,12 +1141,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         q_load(nx, data);
         q_ready(data, &q_full[0]);
       }
-    }
     tile += n;
     ++piece_no;
     u += n;
     if (!more) break;
-    advance(at);
+    at = nx;
+    }
   }
   __syncwarp();
   if (warp == kProducer && *(volatile int*)s_abort && p.box && lane == 0) {
