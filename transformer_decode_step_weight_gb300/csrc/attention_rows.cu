@@ -21,9 +21,13 @@
 //   * f32 q: q and the weights as three bf16 parts each (24 bits; two would leave
 //     2.4e-6 of each weight, above what an f32 sum of the same length loses), three times
 //     the products.
-// Two tile shapes. One row tile per CTA (NT 1): each row is held by two threads that take
-// 64 of the 128 keys each and trade maxima; S is double-buffered. Two (NT 2, bf16 only, 256
-// rows): one thread per row, the two tiles' products and softmaxes alternate.
+// Each row is held by two threads, which take 64 of the 128 keys each and trade maxima. S is
+// double-buffered and runs two tiles ahead, so the products of one tile cover the softmax of
+// the next; the one lane that issues them is what bounds a long prompt (each tcgen05
+// instruction takes it 50 cycles and more, and 16 products of 64 cycles are a tile).
+// Two row tiles per CTA with one thread per row and S once per row tile, which halves the
+// K/V reads, measured slower: 643 against 623 us at 8192 tokens, since every product then
+// waits for a whole softmax.
 //
 // Keys a row must not see: scores are masked by selection, and V rows that only some rows
 // of the tile see are checked for NaN and infinities (0 * NaN would reach every row):
@@ -48,7 +52,7 @@ constexpr int kChunk = 128 * 128;        // [128 rows x 64 bf16], 128-byte swizz
 constexpr int kSlot = 2 * kChunk;        // a K or V tile, or one part of a row tile of Q
 constexpr int kSoftWarps = 8;
 constexpr int kSoft = 32 * kSoftWarps;
-constexpr int kIssuer = kSoftWarps;      // warp roles behind the softmax warps
+// warp roles behind the softmax warps: the first issues the products
 constexpr int kProducer = kSoftWarps + 1;
 constexpr int kFixer = kSoftWarps + 2;   // and the one after it
 constexpr int kThreads = 32 * (kSoftWarps + 4);
@@ -60,8 +64,7 @@ constexpr int kMinUnits = 2;             // units per CTA below which fewer CTAs
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMove = 8.0f;            // log2 units a score may pass the reference maximum
 constexpr int kMaxGrid = 192;            // CTAs (SMs) the workspace has room for
-constexpr int kPartRows = 2 * kRows;     // rows of a partial (NT 2)
-constexpr size_t kPartFloats = (size_t)kPartRows * (kD + 2);
+constexpr size_t kPartFloats = (size_t)kRows * (kD + 2);
 
 struct Params {
   const void* q;
@@ -89,6 +92,25 @@ QD_DEV uint32_t bf2(float lo, float hi) {
   uint32_t u;
   memcpy(&u, &v, 4);
   return u;
+}
+// Up to 1024 polls of a barrier's phase.
+QD_DEV bool mbar_try_some(uint64_t* bar, uint32_t phase) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, 1024;\n"
+      "AGAIN:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE;\n\t"
+      "sub.u32 n, n, 1;\n\t"
+      "setp.ne.u32 q, n, 0;\n\t"
+      "@q bra AGAIN;\n"
+      "DONE:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(phase)
+      : "memory");
+  return ok != 0;
 }
 QD_DEV void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 
@@ -133,13 +155,34 @@ QD_DEV uint64_t desc_v(uint32_t saddr) {
   return (uint64_t)((saddr >> 4) & 0x3FFF) | (uint64_t)(kChunk >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
-QD_DEV void mma_pv(uint32_t tmem_d, uint32_t tmem_a, uint64_t db, uint32_t accumulate) {
+// The products are issued by one lane of a warp whose lanes all walk the same way, so that
+// descriptors stay in uniform registers; `lead` says which lane.
+QD_DEV void mma_pv(bool lead, uint32_t tmem_d, uint32_t tmem_a, uint64_t db, uint32_t accumulate) {
   constexpr uint32_t kIdesc = tc::idesc_m128(kD) | (1u << 16);   // B MN-major
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "r"(tmem_a), "l"(db), "r"(kIdesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(db), "r"(kIdesc), "r"(accumulate), "r"((uint32_t)lead)
+      : "memory");
+}
+QD_DEV void mma_qk(bool lead, uint32_t tmem_d, uint64_t da, uint64_t db, uint32_t accumulate) {
+  constexpr uint32_t kIdesc = tc::idesc_m128(kKeys);
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "l"(da), "l"(db), "r"(kIdesc), "r"(accumulate), "r"((uint32_t)lead)
+      : "memory");
+}
+QD_DEV void commit(bool lead, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"((uint32_t)lead)
       : "memory");
 }
 
@@ -161,7 +204,6 @@ QD_DEV long long quot(long long a, long long b) {
   return ((unsigned long long)(a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-template <int NT>
 struct Work {
   int log_tpt;   // 2^log_tpt packed rows (tokens or sequences) per row tile
   bool prompt;
@@ -199,10 +241,7 @@ struct Work {
     const long long c = (long long)a.off + ((long long)(one + 1) << log_tpt) + kKeys - 1;
     const long long rest = full - one;
     if (rest > 0) {
-      if (log_tpt <= 7)   // tpt divides 128
-        sum += floor_sum((c >> log_tpt) + rest, 7 - log_tpt) - floor_sum(c >> log_tpt, 7 - log_tpt);
-      else
-        sum += rest * (c >> 7) + ((rest * (rest - 1) / 2) << (log_tpt - 7));
+      sum += floor_sum((c >> log_tpt) + rest, 7 - log_tpt) - floor_sum(c >> log_tpt, 7 - log_tpt);   // tpt divides 128
     }
     return sum;
   }
@@ -259,18 +298,18 @@ __device__ __noinline__ void patch_row(const Params& p, const int32_t* pt, int g
     if ((any >> k) & 1) ov[k] = add[k];
 }
 
-template <typename T, int PARTS, int NT>
+template <typename T, int PARTS>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ Params p) {
-  static_assert(PARTS == 1 || NT == 1, "");
-  constexpr int kQBufs = PARTS == 1 ? 2 : 1;  // Q of the next piece is loaded during this one
-  constexpr int kQ1 = PARTS * NT;             // slots of one Q
-  constexpr int kQ = kQ1 * kQBufs;
+  // bf16: a slot of its own for what goes out, so that Q of the next piece can be copied as
+  // soon as this one's last S is there; f32: what goes out takes Q's place
+  constexpr bool kEarlyQ = PARTS == 1;
+  constexpr int kQ1 = PARTS;                  // slots of Q
+  constexpr int kQ = kQ1 + kEarlyQ;           // ... and of what goes out
   constexpr int kRing = 7 - kQ;
-  constexpr int kAhead = NT == 1 ? 2 : 1;     // K tiles in the ring before the first V tile
-  constexpr int kCols = NT == 2 ? 128 : 64;   // keys of a tile per softmax thread
-  constexpr int kOCols = NT == 2 ? 128 : 64;  // O columns per softmax thread
+  constexpr int kAhead = 2;                   // K tiles in the ring before the first V tile
+  constexpr int kCols = 64;                   // keys of a tile, and O columns, per softmax thread
   constexpr bool kFresh = PARTS == 3;         // O of each tile alone in TMEM, summed in registers
   static_assert(kRing >= 3 && kRing <= kMaxSlots, "");
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -280,10 +319,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* s_full = empty + kMaxSlots;  // [2] S in buffer b
   uint64_t* p_full = s_full + 2;         // [2] the weights in buffer b, O rescaled
   uint64_t* o_done = p_full + 2;         // [2] the P V products of buffer b done
-  uint64_t* q_full = o_done + 2;         // [kQBufs] Q of a piece
-  uint64_t* v_go = q_full + 2;           // a masked V tile landed (the issuer saw it)
+  uint64_t* q_full = o_done + 2;         // Q of a piece
+  uint64_t* v_go = q_full + 1;           // a masked V tile landed (the issuer saw it)
   uint64_t* v_fixed = v_go + 1;          // ... and was put right
-  uint32_t* tslot = (uint32_t*)(v_fixed + 1);
+  uint64_t* drained = v_fixed + 1;       // after a timeout: the products issued so far are done
+  uint32_t* tslot = (uint32_t*)(drained + 1);
   int* s_abort = (int*)(tslot + 1);
   int* s_patch = s_abort + 1;            // [2] the last piece with NaN or infinities in a masked V tile
   int* s_last = s_patch + 2;
@@ -291,10 +331,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   long long* s_scan = (long long*)(smem + 320);   // [warps] sums of the scan
   float* xm = (float*)(smem + 512);               // [2][2][128] traded maxima and sums
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  Work<NT> W;
+  // the warp's number from one lane: the roles' branches are then known to be taken by whole
+  // warps, and the issuers' descriptors can stay in uniform registers
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  Work W;
   W.prompt = p.shared_lens == nullptr;
-  W.log_tpt = (NT == 2 ? 8 : 7) - p.log_rep;
+  W.log_tpt = 7 - p.log_rep;
   pdl_launch_dependents();
   if (smem_u32(smem) & 1023u) {   // the swizzled tiles rest on it (there is no static shared memory)
     if (tid == 0) set_error(p.err, QD_DEVERR_TIMEOUT);
@@ -359,12 +401,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], NT == 2 ? kRows : kSoft);
+      mbar_init(&p_full[i], kSoft);
       mbar_init(&o_done[i], 1);
-      mbar_init(&q_full[i], kSoft);
       s_patch[i] = 0;
     }
+    mbar_init(q_full, kSoft);
     mbar_init(v_go, 1);
+    mbar_init(drained, 1);
     mbar_init(v_fixed, 64);
     fence_mbar_init();
   }
@@ -373,25 +416,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after();
   const uint32_t tb = *tslot;
-  const uint32_t tS = tb, tO = tb + 256, tX = tb + 384;   // NT 2: O of tile j at tO + 128 j
+  const uint32_t tS = tb, tO = tb + 256, tX = tb + 384;
   const long long U = s_find[2];
   const long long G = min((long long)gridDim.x, (U + kMinUnits - 1) / kMinUnits);
   const long long u1 = quot((blockIdx.x + 1) * U, G);
   long long u = quot(blockIdx.x * U, G);
 
-  // a bounded wait; after a timeout anywhere in the CTA it returns at once
+  // a bounded wait of a whole warp; after a timeout anywhere in the CTA it returns at once
   auto wait = [&](uint64_t* bar, uint32_t ph) {
-    if (mbar_try_wait(bar, ph)) return;
-    const uint64_t t0 = global_ns();
-    for (int i = 0; i < (1 << 24); ++i) {
-      if (mbar_try_wait(bar, ph)) return;
-      if ((i & 63) == 63) {
-        if (*(volatile int*)s_abort) return;
-        if (global_ns() - t0 > 1000000000ull) break;
+    uint64_t t0 = 0;
+    while (!__all_sync(0xffffffffu, mbar_try_some(bar, ph))) {
+      if (*(volatile int*)s_abort) break;
+      const uint64_t now = global_ns();   // slow to read (about 1000 cycles): only in long waits
+      if (t0 == 0) t0 = now;
+      if (now - t0 > 1000000000ull) {
+        set_error(p.err, QD_DEVERR_TIMEOUT);
+        *(volatile int*)s_abort = 1;
+        break;
       }
     }
-    set_error(p.err, QD_DEVERR_TIMEOUT);
-    *(volatile int*)s_abort = 1;
+    __syncwarp();
   };
 
   // the place of unit u
@@ -427,6 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // follow: ring entries, tiles, fixed tiles, trades, pieces.
   uint32_t ring = 0, tile = 0, fixes = 0, trades = 0, piece_no = 0;
   int late = -1;
+  uint32_t slot = 0, slot_ph = 0;
   [[maybe_unused]] bool first = true;
 
   struct Piece {
@@ -534,11 +579,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       Look l0 = look(0), l1 = look(1);
       load(&tmK, p.k_pages, l0);
-      if (kAhead == 2 && n > 1) load(&tmK, p.k_pages, l1);
+      if (n > 1) load(&tmK, p.k_pages, l1);
       for (int i = 0; i < n; ++i) {
         const Look l2 = look(i + 2);
         load(&tmV, p.v_pages, l0);
-        if (i + kAhead < n) load(&tmK, p.k_pages, kAhead == 2 ? l2 : l1);
+        if (i + kAhead < n) load(&tmK, p.k_pages, l2);
         l0 = l1;
         l1 = l2;
       }
@@ -563,18 +608,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           unsigned char* v = data + (kQ + slot) * kSlot;
           const int lo = max(0, seen_min - key0), hi = seen_max - key0;
           // thread: 16-byte piece c of every fourth key, four cells at a time
+          constexpr int kStep = 4;
           const int ft = tid - 32 * kFixer, c = ft & 15;
           unsigned char* col = v + (c >> 3) * kChunk;
           const int split = min(hi, kKeys);
           int key = lo + (ft >> 4);
-          for (; key < split; key += 16) {
+          for (; key < split; key += 4 * kStep) {
             uint4 x[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              if (key + 4 * j < split) x[j] = *(const uint4*)(col + tc::sw128_off(key + 4 * j, c & 7));
+              if (key + kStep * j < split) x[j] = *(const uint4*)(col + tc::sw128_off(key + kStep * j, c & 7));
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              if (key + 4 * j >= split) break;
+              if (key + kStep * j >= split) break;
               // a half with all exponent bits set borrows into its top bit
               auto odd = [](uint32_t w) { return ((w & 0x7f807f80u) ^ 0x7f807f80u) - 0x00010001u; };
               if ((odd(x[j].x) | odd(x[j].y) | odd(x[j].z) | odd(x[j].w)) & 0x80008000u) {
@@ -584,12 +630,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                   if ((h[k] & 0x7f80u) == 0x7f80u) h[k] &= 0xffff0000u;
                   if ((h[k] & 0x7f800000u) == 0x7f800000u) h[k] &= 0xffffu;
                 }
-                *(uint4*)(col + tc::sw128_off(key + 4 * j, c & 7)) = make_uint4(h[0], h[1], h[2], h[3]);
+                *(uint4*)(col + tc::sw128_off(key + kStep * j, c & 7)) = make_uint4(h[0], h[1], h[2], h[3]);
                 *(volatile int*)(s_patch + (piece_no & 1)) = (int)piece_no + 1;
               }
             }
           }
-          for (key = max(lo, max(hi, 0)) + (ft >> 4); key < kKeys; key += 4)
+          for (key = max(lo, max(hi, 0)) + (ft >> 4); key < kKeys; key += kStep)
             *(uint4*)(col + tc::sw128_off(key, c & 7)) = make_uint4(0u, 0u, 0u, 0u);
           fence_proxy_async_smem();
           mbar_arrive(v_fixed);
@@ -597,105 +643,75 @@ __global__ void __launch_bounds__(kThreads, 1)
         r += i + kAhead < n ? 2 : 1;
       }
       ring += 2 * n;
-    } else if (warp == kIssuer) {
-      if (lane == 0) {
-        // ---- the products, in the order K0 (K1) V0 K2 V1 ... of the ring
-        const uint64_t dq = tc::desc_sw128(smem_u32(data + (kQBufs == 2 ? piece_no & 1 : 0) * kQ1 * kSlot));
-        auto slot_of = [&](uint32_t c) { return smem_u32(data + (kQ + c % kRing) * kSlot); };
-        auto wait_full = [&](uint32_t c) { wait(&full[c % kRing], (c / kRing) & 1); };
-        auto live = [&] { return *(volatile int*)s_abort == 0; };
-        // S of row tile j into buffer b from a K tile; small parts first
-        auto mma_s = [&](int j, int b, uint32_t kaddr) {
-          const uint64_t dk = tc::desc_sw128(kaddr);
-          uint32_t acc = 0;
+    } else {
+      // ---- the products, in the order K0 K1 V0 K2 V1 ... of the ring: S runs two tiles ahead
+      // of P V. What this warp does between two products is time the tensor cores may idle (a
+      // tcgen05 instruction takes it 50 cycles or more), so waits that are usually over come
+      // early and slots are counted, not divided.
+      const bool lead = lane == 0;
+      const uint64_t dq = tc::desc_sw128(smem_u32(data));
+      const uint32_t ring0 = smem_u32(data) + kQ * kSlot;
+      auto quick = [&](uint64_t* bar, uint32_t ph) {   // a wait that is likely over
+        if (!__all_sync(0xffffffffu, mbar_try_wait(bar, ph))) wait(bar, ph);
+      };
+      auto step = [&] {
+        if (++slot == kRing) {
+          slot = 0;
+          slot_ph ^= 1;
+        }
+      };
+      // S into buffer b from a K tile; small parts first
+      auto mma_s = [&](int b, uint32_t kaddr) {
+        const uint64_t dk = tc::desc_sw128(kaddr);
 #pragma unroll 1
-          for (int part = PARTS - 1; part >= 0; --part) {
-            const uint64_t da = dq + (uint64_t)((j + part) * kSlot >> 4);
+        for (int part = PARTS - 1; part >= 0; --part) {
+          const uint64_t da = dq + (uint64_t)(part * kSlot >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              constexpr int kHalf = kChunk >> 4;
-              const uint64_t o = (kk >> 2) * kHalf + (kk & 3) * 2;
-              tc::mma<kKeys>(tS + 128 * b, da + o, dk + o, acc);
-              acc = 1;
-            }
-          }
-          tc::commit(&s_full[b]);
-        };
-        auto mma_o = [&](int b, uint32_t to, uint32_t vaddr, uint32_t acc) {
-          const uint64_t dv = desc_v(vaddr);
-#pragma unroll 1
-          for (int part = PARTS - 1; part >= 0; --part) {
-            // NT 2: 64 columns of pairs of keys; NT 1: 32 keys' weights over their own 32 scores
-            const uint32_t ta = part < 2 ? tS + 128 * b + 16 * part : tX + 64 * b;
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              const uint32_t o = NT == 2 || part == 2 ? 8 * kk : 32 * (kk >> 1) + 8 * (kk & 1);
-              mma_pv(to, ta + o, dv + (uint64_t)(kk * 2048 >> 4), acc);
-              acc = 1;
-            }
-          }
-          tc::commit(&o_done[b]);
-        };
-        auto v_ready = [&](int i, uint32_t c) {
-          wait_full(c);
-          if ((k0 + i + 1) * kKeys > seen_min) {
-            mbar_arrive(v_go);
-            wait(v_fixed, fixes++ & 1);
-          }
-        };
-        if (kQBufs == 2) wait(&q_full[piece_no & 1], (piece_no >> 1) & 1);
-        else wait(&q_full[0], piece_no & 1);
-        if constexpr (NT == 1) {
-          // S runs two tiles ahead of P V
-#pragma unroll 1
-          for (int i = -2; i < n; ++i) {
-            if (i >= 0) {
-              const uint32_t ct = tile + i;
-              v_ready(i, ring);
-              wait(&p_full[ct & 1], (ct >> 1) & 1);
-              tc::fence_after();
-              if (live()) {
-                mma_o(ct & 1, tO, slot_of(ring), !kFresh && i > 0);
-                tc::commit(&empty[ring % kRing]);
-              }
-              ++ring;
-            }
-            if (i + 2 < n) {
-              wait_full(ring);
-              tc::fence_after();
-              if (live()) {
-                mma_s(0, (tile + i + 2) & 1, slot_of(ring));
-                tc::commit(&empty[ring % kRing]);
-              }
-              ++ring;
-            }
-          }
-        } else {
-#pragma unroll 1
-          for (int i = -1; i < n; ++i) {
-            const uint32_t rv = ring, rk = ring + (i >= 0);
-            if (i >= 0) v_ready(i, rv);
-            if (i + 1 < n) wait_full(rk);
-#pragma unroll 1
-            for (int j = 0; j < 2; ++j) {
-              if (i >= 0) wait(&p_full[j], (tile + i) & 1);
-              tc::fence_after();
-              if (live()) {
-                if (i >= 0) {
-                  mma_o(j, tO + 128 * j, slot_of(rv), i > 0);
-                  if (j) tc::commit(&empty[rv % kRing]);
-                }
-                if (i + 1 < n) {
-                  mma_s(j, j, slot_of(rk));
-                  if (j) tc::commit(&empty[rk % kRing]);
-                }
-              }
-            }
-            ring += (i >= 0) + (i + 1 < n);
+          for (int kk = 0; kk < 8; ++kk) {
+            constexpr int kHalf = kChunk >> 4;
+            const uint64_t o = (kk >> 2) * kHalf + (kk & 3) * 2;
+            mma_qk(lead, tS + 128 * b, da + o, dk + o, kk != 0 || part != PARTS - 1);
           }
         }
+        commit(lead, &s_full[b]);
+        commit(lead, &empty[slot]);
+      };
+      auto mma_o = [&](int b, uint32_t vaddr, bool first) {
+        const uint64_t dv = desc_v(vaddr);
+#pragma unroll 1
+        for (int part = PARTS - 1; part >= 0; --part) {
+          // 32 keys' weights over their own 32 scores
+          const uint32_t ta = part < 2 ? tS + 128 * b + 16 * part : tX + 64 * b;
+          const uint32_t t32 = part < 2 ? 32 : 16;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_pv(lead, tO, ta + t32 * (kk >> 1) + 8 * (kk & 1), dv + (uint64_t)(kk * 2048 >> 4),
+                   kk != 0 || part != PARTS - 1 || !first);
+        }
+        commit(lead, &o_done[b]);
+        commit(lead, &empty[slot]);
+      };
+      wait(q_full, piece_no & 1);
+#pragma unroll 1
+      for (int i = -2; i < n; ++i) {
+        if (i >= 0) {
+          const uint32_t ct = tile + i;
+          quick(&full[slot], slot_ph);
+          if ((k0 + i + 1) * kKeys > seen_min) {
+            if (lead) mbar_arrive(v_go);
+            wait(v_fixed, fixes++ & 1);
+          }
+          quick(&p_full[ct & 1], (ct >> 1) & 1);
+          tc::fence_after();
+          mma_o(ct & 1, ring0 + slot * kSlot, kFresh || i == 0);
+          step();
+        }
+        if (i + 2 < n) {
+          quick(&full[slot], slot_ph);
+          mma_s((tile + i + 2) & 1, ring0 + slot * kSlot);
+          step();
+        }
       }
-      __syncwarp();
     }
     tile += n;
     ++piece_no;
@@ -712,30 +728,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool more = pc.more;
     const int first_row = pc.first_row, packed = pc.packed;
     const int32_t* pt = pc.pt;
-      // ---- softmax. NT 1: warps w and w + 4 hold the same rows (TMEM lanes), 64 keys and 64
-      // O columns each; NT 2: warps 4 .. 7 hold the second row tile.
-      const int hf = warp >> 2, lr = (warp & 3) * 32 + lane;
-      const int row = NT == 2 ? hf * kRows + lr : lr;
+      // ---- softmax: warps w and w + 4 hold the same rows (TMEM lanes), 64 keys and 64 O columns
+      // each
+      const int hf = warp >> 2, row = (warp & 3) * 32 + lane;
       const int rows = packed << p.log_rep;
       const bool valid = row < rows;
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-      const uint32_t to = (NT == 2 ? tO + 128 * hf : tO + 64 * hf) + lanes;
-      unsigned char* qbuf = data + (kQBufs == 2 ? piece_no & 1 : 0) * kQ1 * kSlot;
+      const uint32_t to = tO + 64 * hf + lanes;
+      unsigned char* stage = data + (kEarlyQ ? kQ1 * kSlot : 0);
 
       // Q of the row tile at x; the copies are waited for in q_ready
-      auto q_load = [&](const Place& x, unsigned char* dst) {
+      auto q_load = [&](const Place& x) {
+        unsigned char* dst = data;
         const T* q = (const T*)p.q + (long long)(x.a.row0 + (x.t << W.log_tpt)) * p.q_stride +
                      (long long)(x.g << p.log_rep) * kD;
         const int qrows = min(W.tpt(), x.a.n - (x.t << W.log_tpt)) << p.log_rep;
         if constexpr (PARTS == 1) {
-          // warp w copies rows 16 NT w .. of the row tile(s) as they are, two rows at a time
-          constexpr int kPer = 16 * NT;
+          // warp w copies rows 16 w .. as they are, two rows at a time
+          constexpr int kPer = 16;
           const uint32_t d0 = smem_u32(dst);
           const int c = lane & 15;
 #pragma unroll 4
           for (int i = 0; i < kPer; i += 2) {
             const int r = warp * kPer + i + (lane >> 4), ok = r < qrows ? r : 0;
-            cp16(d0 + (r >> 7) * kSlot + (c >> 3) * kChunk + tc::sw128_off(r & (kRows - 1), c & 7),
+            cp16(d0 + (c >> 3) * kChunk + tc::sw128_off(r, c & 7),
                  q + (long long)(ok >> p.log_rep) * p.q_stride + (ok & (p.rep - 1)) * kD + 8 * c, r < qrows ? 16 : 0);
           }
           asm volatile("cp.async.commit_group;" ::: "memory");
@@ -765,37 +781,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       };
-      auto q_ready = [&](unsigned char* dst, uint64_t* bar) {
+      auto q_ready = [&] {
+        [[maybe_unused]] unsigned char* dst = data;
         if constexpr (PARTS == 1) {
           asm volatile("cp.async.wait_group 0;" ::: "memory");
           if (p.q_sign <= 0.f) {   // a negative scale: this thread's pieces negated; none: zeros
-            constexpr int kPer = 16 * NT;
+            constexpr int kPer = 16;
             const int c = lane & 15;
             const uint32_t keep = p.q_sign < 0.f ? 0xffffffffu : 0u, flip = p.q_sign < 0.f ? 0x80008000u : 0u;
 #pragma unroll 1
             for (int i = 0; i < kPer; i += 2) {
               const int r = warp * kPer + i + (lane >> 4);
-              uint4* cell = (uint4*)(dst + (r >> 7) * kSlot + (c >> 3) * kChunk + tc::sw128_off(r & (kRows - 1), c & 7));
+              uint4* cell = (uint4*)(dst + (c >> 3) * kChunk + tc::sw128_off(r, c & 7));
               const uint4 v = *cell;
               *cell = make_uint4((v.x & keep) ^ flip, (v.y & keep) ^ flip, (v.z & keep) ^ flip, (v.w & keep) ^ flip);
             }
           }
         }
         fence_proxy_async_smem();
-        mbar_arrive(bar);
+        mbar_arrive(q_full);
       };
       Place nx = at;
       if (first) {
-        q_load(at, qbuf);
-        q_ready(qbuf, &q_full[0]);
+        q_load(at);
+        q_ready();
         first = false;
       }
       if (more) advance(nx);
-      unsigned char* qnext = data + (kQBufs == 2 ? ~piece_no & 1 : 0) * kQ1 * kSlot;
-      if (kQBufs == 2 && more) {
-        bar_sync(6, kSoft);   // nobody still uses the place for the piece before
-        q_load(nx, qnext);
-      }
 
       int lim = 0;   // keys this row sees
       if (valid) {
@@ -811,24 +823,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int warp_min = __reduce_min_sync(0xffffffffu, valid ? lim : INT32_MAX);
       const float c = p.scale_log2;
       float ms = -INFINITY, l = 0.f;
-      [[maybe_unused]] float osum[kFresh ? kOCols : 1];
+      [[maybe_unused]] float osum[kFresh ? kCols : 1];
       if constexpr (kFresh) {
 #pragma unroll
-        for (int k = 0; k < kOCols; ++k) osum[k] = 0.f;
+        for (int k = 0; k < kCols; ++k) osum[k] = 0.f;
       }
       auto trade = [&](float v) -> float {   // with the other holder of the row
         const int par = trades & 1;
         ++trades;
-        xm[(par * 2 + hf) * kRows + lr] = v;
+        xm[(par * 2 + hf) * kRows + row] = v;
         bar_sync(2 + (warp & 3), 64);
-        return xm[(par * 2 + (hf ^ 1)) * kRows + lr];
+        return xm[(par * 2 + (hf ^ 1)) * kRows + row];
       };
 #pragma unroll 1
       for (int i = 0; i < n; ++i) {
         const uint32_t ct = tile + i;
-        const int b = NT == 2 ? hf : (int)(ct & 1);
-        const int key0 = (k0 + i) * kKeys + (NT == 2 ? 0 : 64 * hf);
-        const uint32_t ts = tS + 128 * b + lanes + (NT == 2 ? 0 : 64 * hf);
+        const int b = (int)(ct & 1);
+        const int key0 = (k0 + i) * kKeys + 64 * hf;
+        const uint32_t ts = tS + 128 * b + lanes + 64 * hf;
         // 32 scores; those of keys that the row does not see become -inf
         auto mask = [&](float* sv, int key) {
           if (key + 32 > warp_min) {
@@ -844,8 +856,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 4; ++k) m4[k] = max3(m4[k], sv[e + 2 * k], sv[e + 2 * k + 1]);
           return fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
         };
-        wait(&s_full[b], NT == 2 ? ct & 1 : (ct >> 1) & 1);
+        wait(&s_full[b], (ct >> 1) & 1);
         tc::fence_after();
+        // the piece's last products with Q are done
+        if (kEarlyQ && more && i == n - 1) q_load(nx);
         float mx = -INFINITY;
         // f32: the scores are read twice (for the maximum, for the weights), since registers for
         // all of them are not left beside O
@@ -869,20 +883,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             mx = top(sv, mx);
           }
         }
-        if (NT == 1) mx = fmaxf(mx, trade(mx));
+        mx = fmaxf(mx, trade(mx));
         mx = mx == -INFINITY ? mx : mx * c;
         const bool move = mx > ms + kMove;
         const float alpha = move ? ex2(ms - mx) : 1.f;   // 0 while ms is -inf
         if constexpr (!kFresh) {
           // the barrier of the products before the last ones: already complete (they were issued
           // before this S), waited for so that the phases are followed one by one
-          if (NT == 1 && i >= 2) wait(&o_done[b], ((ct - 2) >> 1) & 1);
-          if (NT == 2 && i > 0) wait(&o_done[b], (ct - 1) & 1);
+          if (i >= 2) wait(&o_done[b], ((ct - 2) >> 1) & 1);
           if (i > 0 && __any_sync(0xffffffffu, move)) {
-            if (NT == 1) wait(&o_done[b ^ 1], ((ct - 1) >> 1) & 1);
+            wait(&o_done[b ^ 1], ((ct - 1) >> 1) & 1);
             tc::fence_after();
 #pragma unroll 1
-            for (int e = 0; e < kOCols; e += 16) {
+            for (int e = 0; e < kCols; e += 16) {
               float ov[16];
               ld16(to + e, ov);
               wait_ld();
@@ -919,7 +932,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               w2[e / 2] = bf2(x - bf_lo(w1[e / 2]), y - bf_hi(w1[e / 2]));
             }
           }
-          st16(NT == 2 ? ts + e0 / 2 : ts + e0, w0);   // over scores that have been read
+          st16(ts + e0, w0);   // over scores that have been read
           if constexpr (PARTS == 3) {
             st16(ts + e0 + 16, w1);
             st16(tX + 64 * b + lanes + 32 * hf + e0 / 2, w2);
@@ -943,7 +956,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::fence_after();
             const bool any = __any_sync(0xffffffffu, move);
 #pragma unroll
-            for (int e = 0; e < kOCols; e += 32) {
+            for (int e = 0; e < kCols; e += 32) {
               ld32(to + e, sv);
               wait_ld();
 #pragma unroll
@@ -951,7 +964,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (any)
 #pragma unroll
-              for (int k = 0; k < kOCols; ++k) osum[k] *= alpha;
+              for (int k = 0; k < kCols; ++k) osum[k] *= alpha;
           }
         }
         {
@@ -963,18 +976,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_before();
         mbar_arrive(&p_full[b]);
       }
-      if (kQBufs == 2 && more) q_ready(qnext, &q_full[~piece_no & 1]);
+      if (kEarlyQ && more) q_ready();
 
       // ---- the piece's O, m, l
       const uint32_t ce = tile + n;
-      if (NT == 1) {
-        if (!kFresh && n >= 2) wait(&o_done[ce & 1], ((ce - 2) >> 1) & 1);
-        wait(&o_done[(ce - 1) & 1], ((ce - 1) >> 1) & 1);
-        const float other = trade(l);
-        l = hf == 0 ? l + other : other + l;
-      } else {
-        wait(&o_done[hf], (ce - 1) & 1);
-      }
+      if (!kFresh && n >= 2) wait(&o_done[ce & 1], ((ce - 2) >> 1) & 1);
+      wait(&o_done[(ce - 1) & 1], ((ce - 1) >> 1) & 1);
+      const float l_other = trade(l);
+      l = hf == 0 ? l + l_other : l_other + l;
       tc::fence_after();
       const bool dead = *(volatile int*)s_abort != 0;
       const bool whole = k0 == 0 && k1 == nk;
@@ -983,14 +992,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto out_row = [&](int r) {   // (packed row, q head) of row r of the tile
         return (size_t)(first_row + (r >> p.log_rep)) * p.Hq + (g << p.log_rep) + (r & (p.rep - 1));
       };
-      const int col0 = NT == 2 ? 0 : 64 * hf;
+      const int col0 = 64 * hf;
       const float inv = l == 0.f ? 0.f : 1.0f / l;   // a row that saw nothing gives 0
       const bool final_out = whole && W.prompt;      // else O as it is, with m and l
-      // bf16 results and the f32 form's values go out by whole rows, through the place of this
-      // piece's Q (its products are done): 16-byte pieces, swizzled
+      // bf16 results and the f32 form's values go out by whole rows, through shared memory:
+      // 16-byte pieces, swizzled
       float* dst_f32 = !whole ? part + (size_t)row * kD : p.pre_o + (valid && !W.prompt ? out_row(row) * kD : 0);
-#pragma unroll(kFresh ? kOCols / 32 : 1)
-      for (int e = 0; e < kOCols; e += 32) {
+#pragma unroll(kFresh ? kCols / 32 : 1)
+      for (int e = 0; e < kCols; e += 32) {
         float ov[32];
         ld32(to + e, ov);
         wait_ld();
@@ -1012,14 +1021,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (final_out && PARTS == 1) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            *(uint4*)(qbuf + row * 256 + ((((col0 + e) / 8 + k) ^ (row & 15)) << 4)) =
+            *(uint4*)(stage + row * 256 + ((((col0 + e) / 8 + k) ^ (row & 15)) << 4)) =
                 make_uint4(bf2(ov[8 * k] * inv, ov[8 * k + 1] * inv), bf2(ov[8 * k + 2] * inv, ov[8 * k + 3] * inv),
                            bf2(ov[8 * k + 4] * inv, ov[8 * k + 5] * inv), bf2(ov[8 * k + 6] * inv, ov[8 * k + 7] * inv));
         } else if (PARTS == 3) {
           const float f = final_out ? inv : 1.f;
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            *(float4*)(qbuf + row * 512 + ((((col0 + e) / 4 + k) ^ (row & 31)) << 4)) =
+            *(float4*)(stage + row * 512 + ((((col0 + e) / 4 + k) ^ (row & 31)) << 4)) =
                 make_float4(ov[4 * k] * f, ov[4 * k + 1] * f, ov[4 * k + 2] * f, ov[4 * k + 3] * f);
         } else if (valid && !dead) {
 #pragma unroll
@@ -1027,38 +1036,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             *((float4*)(dst_f32 + col0 + e) + k) = make_float4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
         }
       }
-      if (valid && !dead && !final_out && (NT == 2 || hf == 0)) {
+      if (valid && !dead && !final_out && hf == 0) {
         if (!whole) {
-          part[(size_t)kPartRows * kD + row] = ms;
-          part[(size_t)kPartRows * kD + kPartRows + row] = l;
+          part[(size_t)kRows * kD + row] = ms;
+          part[(size_t)kRows * kD + kRows + row] = l;
         } else {
           p.pre_m[out_row(row)] = ms;
           p.pre_l[out_row(row)] = l;
         }
       }
       if (final_out || PARTS == 3) {
-        // the rows that this warp's lanes (and their other holders') wrote
-        if (NT == 2) __syncwarp();
-        else bar_sync(2 + (warp & 3), 64);
-        constexpr int kPer = NT == 2 ? 32 : 16;
-        const int r0 = NT == 2 ? warp * 32 : (warp & 3) * 32 + hf * 16;
+        // the rows that this warp's lanes and their other holders' wrote
+        bar_sync(2 + (warp & 3), 64);
+        const int r0 = (warp & 3) * 32 + hf * 16;
         if (!dead) {
           if constexpr (PARTS == 1) {
             const int pc = lane & 15;
 #pragma unroll 4
-            for (int i = 0; i < kPer; i += 2) {
+            for (int i = 0; i < 16; i += 2) {
               const int r = r0 + i + (lane >> 4);
               if (r < rows)
                 *(uint4*)((__nv_bfloat16*)p.out + out_row(r) * kD + pc * 8) =
-                    *(const uint4*)(qbuf + r * 256 + ((pc ^ (r & 15)) << 4));
+                    *(const uint4*)(stage + r * 256 + ((pc ^ (r & 15)) << 4));
             }
           } else {
 #pragma unroll 4
-            for (int i = 0; i < kPer; ++i) {
+            for (int i = 0; i < 16; ++i) {
               const int r = r0 + i;
               if (r < rows) {
                 float* d = !whole ? part + (size_t)r * kD : (W.prompt ? (float*)p.out : p.pre_o) + out_row(r) * kD;
-                *(float4*)(d + 4 * lane) = *(const float4*)(qbuf + r * 512 + ((lane ^ (r & 31)) << 4));
+                *(float4*)(d + 4 * lane) = *(const float4*)(stage + r * 512 + ((lane ^ (r & 31)) << 4));
               }
             }
           }
@@ -1075,10 +1082,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         bar_sync(6, kSoft);
         if (*(volatile int*)s_last) {
           const int np = c1 - c0 + 1;
-          // weights [pieces][batch of rows] and sums [batch] in the place of Q, as many rows at
-          // a time as fit
-          const int batch = min(rows, kQ1 * kSlot / 4 / (np + 1));
-          float* wt = (float*)qbuf;
+          // weights [pieces][batch of rows] and sums [batch] where results are staged, as many
+          // rows at a time as fit
+          const int batch = min(rows, (kEarlyQ ? 1 : kQ1) * kSlot / 4 / (np + 1));
+          float* wt = (float*)stage;
           float* total = wt + (size_t)np * batch;
           auto piece = [&](int k) { return p.part + ((size_t)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * kPartFloats; };
           for (int r0 = 0; r0 < rows; r0 += batch) {
@@ -1087,14 +1094,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               float M = -INFINITY, L = 0.f;
 #pragma unroll 4
               for (int k = 0; k < np; ++k) {
-                const float m = __ldcg(piece(k) + (size_t)kPartRows * kD + r0 + r);
+                const float m = __ldcg(piece(k) + (size_t)kRows * kD + r0 + r);
                 wt[k * batch + r] = m;
                 M = fmaxf(M, m);
               }
 #pragma unroll 4
               for (int k = 0; k < np; ++k) {
                 const float m = wt[k * batch + r], x = m == -INFINITY ? 0.f : ex2(m - M);
-                const float lk = __ldcg(piece(k) + (size_t)kPartRows * kD + kPartRows + r0 + r);
+                const float lk = __ldcg(piece(k) + (size_t)kRows * kD + kRows + r0 + r);
                 wt[k * batch + r] = x;
                 if (x != 0.f) L = fmaf(x, lk, L);
               }
@@ -1136,10 +1143,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc::fence_before();
-      if (kQBufs == 1 && more) {
+      if (!kEarlyQ && more) {
         bar_sync(6, kSoft);   // everybody is done with Q's place
-        q_load(nx, data);
-        q_ready(data, &q_full[0]);
+        q_load(nx);
+        q_ready();
       }
     tile += n;
     ++piece_no;
@@ -1154,6 +1161,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (uint32_t c = ring > kRing ? ring - kRing : 0; c < ring; ++c)
       mbar_wait_limit(&full[c % kRing], (c / kRing) & 1, p.err, 10000000ull);
   }
+  if (warp == kSoftWarps && *(volatile int*)s_abort) {   // ... and the products (bounded)
+    commit(lane == 0, drained);
+    mbar_wait_limit(drained, 0, p.err, 10000000ull);
+  }
   tc::fence_before();
   __syncthreads();
   if (warp == 0) {
@@ -1164,9 +1175,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 int grid_ctas() { return std::min(dev_info().sm_count, kMaxGrid); }
 
-template <typename T, int PARTS, int NT>
+template <typename T, int PARTS>
 cudaError_t launch(const Params& p, const CUtensorMap& tk, const CUtensorMap& tv, const Launch& L) {
-  auto k = attn_rows_kernel<T, PARTS, NT>;
+  auto k = attn_rows_kernel<T, PARTS>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
   return launch_ex(k, dim3(grid_ctas()), dim3(kThreads), kSmem, L, tk, tv, p);
@@ -1206,10 +1217,7 @@ cudaError_t run(const AttnRowsArgs& a, float* pre_o, const Launch& L) {
     if (e == cudaSuccess) e = encode_tmap_bf16_2d(&tv, a.v_pages, rows, kD, p.box);
     if (e != cudaSuccess) return e;
   }
-  if (a.q_f32) return launch<float, 3, 1>(p, tk, tv, L);
-  // two row tiles per CTA where the segments have the rows for them on average
-  const bool two = (long long)a.n_rows * p.rep > (long long)a.n_seg * kRows;
-  return two ? launch<__nv_bfloat16, 1, 2>(p, tk, tv, L) : launch<__nv_bfloat16, 1, 1>(p, tk, tv, L);
+  return a.q_f32 ? launch<float, 3>(p, tk, tv, L) : launch<__nv_bfloat16, 1>(p, tk, tv, L);
 }
 
 }  // namespace
