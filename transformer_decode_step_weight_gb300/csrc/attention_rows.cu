@@ -4,8 +4,8 @@
 // A row tile is 128 rows of one kv head: consecutive packed tokens (prompt form) or
 // sequences (shared form) times the Hq / Hkv q heads that read it, so a K/V tile is read
 // once for all of them. Work is counted in units of one row tile times 128 keys, ordered
-// by (segment, kv head, row tile, keys); CTA c of the one-per-SM grid takes the units
-// [c U / G, (c + 1) U / G). So ragged prompts, one long prompt and one row behind a long
+// by (segment, kv head, row tile, keys), and each CTA of the one-per-SM grid takes an equal run
+// of them. So ragged prompts, one long prompt and one row behind a long
 // cache all split evenly without the host knowing a length; a row tile that several CTAs
 // share is joined, in key order, by the last of them (ticket). A causal row tile counts
 // only the tiles that some row of it sees.
@@ -92,25 +92,6 @@ QD_DEV uint32_t bf2(float lo, float hi) {
   uint32_t u;
   memcpy(&u, &v, 4);
   return u;
-}
-// Up to 1024 polls of a barrier's phase.
-QD_DEV bool mbar_try_some(uint64_t* bar, uint32_t phase) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
-      "mov.u32 n, 1024;\n"
-      "AGAIN:\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "@p bra DONE;\n\t"
-      "sub.u32 n, n, 1;\n\t"
-      "setp.ne.u32 q, n, 0;\n\t"
-      "@q bra AGAIN;\n"
-      "DONE:\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(phase)
-      : "memory");
-  return ok != 0;
 }
 QD_DEV void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 
@@ -199,10 +180,15 @@ struct Seg {
   bool bad;
 };
 
-// a / b; 64-bit divisions are long, and few calls need them
-QD_DEV long long quot(long long a, long long b) {
-  return ((unsigned long long)(a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
-}
+// The units' split: CTA c of G takes per + (c < rem) of them.
+struct Split {
+  uint32_t per, rem;
+  QD_DEV uint32_t first(uint32_t c) const { return c * per + min(c, rem); }
+  QD_DEV int owner(uint32_t u) const {
+    const uint32_t big = rem * (per + 1);
+    return (int)(u < big ? u / (per + 1) : rem + (u - big) / per);
+  }
+};
 
 struct Work {
   int log_tpt;   // 2^log_tpt packed rows (tokens or sequences) per row tile
@@ -308,7 +294,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kQ1 = PARTS;                  // slots of Q
   constexpr int kQ = kQ1 + kEarlyQ;           // ... and of what goes out
   constexpr int kRing = 7 - kQ;
-  constexpr int kAhead = 2;                   // K tiles in the ring before the first V tile
   constexpr int kCols = 64;                   // keys of a tile, and O columns, per softmax thread
   constexpr bool kFresh = PARTS == 3;         // O of each tile alone in TMEM, summed in registers
   static_assert(kRing >= 3 && kRing <= kMaxSlots, "");
@@ -327,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* s_abort = (int*)(tslot + 1);
   int* s_patch = s_abort + 1;            // [2] the last piece with NaN or infinities in a masked V tile
   int* s_last = s_patch + 2;
-  long long* s_find = (long long*)(smem + 256);   // [0] segment, [1] units before it, [2] U
+  long long* s_find = (long long*)(smem + 256);   // [0] segment, [1] unit within it, [2] the split
   long long* s_scan = (long long*)(smem + 320);   // [warps] sums of the scan
   float* xm = (float*)(smem + 512);               // [2][2][128] traded maxima and sums
 
@@ -375,11 +360,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (w < warp) base += s_scan[w];
       total += s_scan[w];
     }
-    const long long G = min((long long)gridDim.x, (total + kMinUnits - 1) / kMinUnits);
-    if ((long long)blockIdx.x >= G) return;
-    const long long u0 = quot(blockIdx.x * total, G);
+    if (total >= (1LL << 31)) {
+      if (blockIdx.x == 0 && tid == 0) set_error(p.err, QD_DEVERR_POS);
+      return;
+    }
+    const uint32_t G = min(gridDim.x, ((uint32_t)total + kMinUnits - 1) / kMinUnits);
+    if (blockIdx.x >= G) return;
+    const Split sp = {(uint32_t)total / G, (uint32_t)total % G};
+    const uint32_t u0 = sp.first(blockIdx.x);
     long long at = base + v - own;
-    if (tid == 0) s_find[2] = total;
+    if (tid == 0) s_find[2] = (long long)sp.per << 32 | sp.rem;
     if (own > 0 && at <= u0 && u0 < at + own) {
       for (int i = 0; i < per; ++i) {
         const int s = tid * per + i;
@@ -387,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long n = a.tiles ? W.before(a, a.tiles) * p.Hkv : 0;
         if (u0 < at + n) {
           s_find[0] = s;
-          s_find[1] = at;
+          s_find[1] = u0 - at;
           break;
         }
         at += n;
@@ -417,25 +407,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_after();
   const uint32_t tb = *tslot;
   const uint32_t tS = tb, tO = tb + 256, tX = tb + 384;
-  const long long U = s_find[2];
-  const long long G = min((long long)gridDim.x, (U + kMinUnits - 1) / kMinUnits);
-  const long long u1 = quot((blockIdx.x + 1) * U, G);
-  long long u = quot(blockIdx.x * U, G);
+  const Split sp = {(uint32_t)(s_find[2] >> 32), (uint32_t)s_find[2]};
+  const uint32_t u1 = sp.first(blockIdx.x + 1);
+  uint32_t u = sp.first(blockIdx.x);
 
-  // a bounded wait of a whole warp; after a timeout anywhere in the CTA it returns at once
+  // a wait of a whole warp, bounded by its polls (some 40 cycles each at least: about half a
+  // second); after a timeout anywhere in the CTA it returns soon
   auto wait = [&](uint64_t* bar, uint32_t ph) {
-    uint64_t t0 = 0;
-    while (!__all_sync(0xffffffffu, mbar_try_some(bar, ph))) {
-      if (*(volatile int*)s_abort) break;
-      const uint64_t now = global_ns();   // slow to read (about 1000 cycles): only in long waits
-      if (t0 == 0) t0 = now;
-      if (now - t0 > 1000000000ull) {
-        set_error(p.err, QD_DEVERR_TIMEOUT);
+    for (int i = 1; !__all_sync(0xffffffffu, mbar_try_wait(bar, ph)); ++i)
+      if ((i & 1023) == 0 && (i == 1 << 24 || __any_sync(0xffffffffu, *(volatile int*)s_abort))) {
+        if (i == 1 << 24) set_error(p.err, QD_DEVERR_TIMEOUT);
         *(volatile int*)s_abort = 1;
         break;
       }
-    }
-    __syncwarp();
   };
 
   // the place of unit u
@@ -443,9 +427,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   {
     at.s = (int)s_find[0];
     at.a = W.seg(p, at.s);
-    const long long head_units = W.before(at.a, at.a.tiles);
-    at.g = (int)quot(u - s_find[1], head_units);
-    const long long w = u - s_find[1] - at.g * head_units;
+    const uint32_t head_units = (uint32_t)W.before(at.a, at.a.tiles), v = (uint32_t)s_find[1];
+    at.g = (int)(v / head_units);
+    const uint32_t w = v % head_units;
     int lo = 0;
     for (int hi = at.a.tiles; hi - lo > 1;) {   // the last row tile whose units start at or before w
       const int mid = (lo + hi) / 2;
@@ -488,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     q.t = x.t;
     q.k0 = x.k0;
     q.nk = W.units(a, x.t);
-    q.k1 = (int)min((long long)q.nk, x.k0 + (u1 - u));
+    q.k1 = (int)min((uint32_t)q.nk, x.k0 + (u1 - u));
     q.n = q.k1 - x.k0;
     q.more = u + q.n < u1;
     q.first_row = a.row0 + (x.t << W.log_tpt);
@@ -561,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t d0 = smem_u32(dst);
 #pragma unroll
           for (int j = 0; j < kMine; ++j)
-#pragma unroll 4
+#pragma unroll 2
             for (int i = 0; i < 32; i += 2) {
               const int r = i + (lane >> 4), c = lane & 15;
               const int row = __shfl_sync(0xffffffffu, x.row[j], r);
@@ -577,15 +561,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           late = (int)slot;
         }
       };
-      Look l0 = look(0), l1 = look(1);
-      load(&tmK, p.k_pages, l0);
-      if (n > 1) load(&tmK, p.k_pages, l1);
-      for (int i = 0; i < n; ++i) {
-        const Look l2 = look(i + 2);
-        load(&tmV, p.v_pages, l0);
-        if (i + kAhead < n) load(&tmK, p.k_pages, l2);
+      Look l0 = {}, l1 = {}, l2 = {}, l3 = {};   // tiles i .. i + 3
+#pragma unroll 1
+      for (int i = -3; i < n; ++i) {
         l0 = l1;
         l1 = l2;
+        l2 = l3;
+        l3 = look(i + 3);
+        if (i < -2) continue;
+#pragma unroll 1
+        for (int v = 1; v >= 0; --v)
+          if (v ? i >= 0 : i + 2 < n) load(v ? &tmV : &tmK, v ? p.v_pages : p.k_pages, v ? l0 : l2);
       }
       if (late >= 0) {
         asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -598,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // NaN and infinities in the others taken out
       // (the issuer says when: a slot's own barrier may be several phases behind a tile that is
       // still to come, which a wait on its parity cannot tell)
-      uint32_t r = ring + (n > 1 ? kAhead : 1);
+      uint32_t r = ring + (n > 1 ? 2 : 1);
       for (int i = 0; i < n; ++i) {
         const int key0 = (k0 + i) * kKeys;
         if (key0 + kKeys > seen_min) {
@@ -640,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
           mbar_arrive(v_fixed);
         }
-        r += i + kAhead < n ? 2 : 1;
+        r += i + 2 < n ? 2 : 1;
       }
       ring += 2 * n;
     } else {
@@ -651,9 +637,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool lead = lane == 0;
       const uint64_t dq = tc::desc_sw128(smem_u32(data));
       const uint32_t ring0 = smem_u32(data) + kQ * kSlot;
-      auto quick = [&](uint64_t* bar, uint32_t ph) {   // a wait that is likely over
-        if (!__all_sync(0xffffffffu, mbar_try_wait(bar, ph))) wait(bar, ph);
-      };
       auto step = [&] {
         if (++slot == kRing) {
           slot = 0;
@@ -696,18 +679,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = -2; i < n; ++i) {
         if (i >= 0) {
           const uint32_t ct = tile + i;
-          quick(&full[slot], slot_ph);
+          wait(&full[slot], slot_ph);
           if ((k0 + i + 1) * kKeys > seen_min) {
             if (lead) mbar_arrive(v_go);
             wait(v_fixed, fixes++ & 1);
           }
-          quick(&p_full[ct & 1], (ct >> 1) & 1);
+          wait(&p_full[ct & 1], (ct >> 1) & 1);
           tc::fence_after();
           mma_o(ct & 1, ring0 + slot * kSlot, kFresh || i == 0);
           step();
         }
         if (i + 2 < n) {
-          quick(&full[slot], slot_ph);
+          wait(&full[slot], slot_ph);
           mma_s((tile + i + 2) & 1, ring0 + slot * kSlot);
           step();
         }
@@ -1074,9 +1057,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- a shared row tile: the last of its CTAs joins the pieces in key order
       if (!whole) {   // the same in all softmax threads
         // where the tile's units lie: the CTAs of its first and last
-        const long long ua = u - k0, ub = ua + nk - 1;
-        const int c0 = k0 == 0 ? (int)blockIdx.x : (int)quot((ua + 1) * G - 1, U);
-        const int c1 = k1 == nk ? (int)blockIdx.x : (int)quot((ub + 1) * G - 1, U);
+        const int c0 = k0 == 0 ? (int)blockIdx.x : sp.owner(u - k0);
+        const int c1 = k1 == nk ? (int)blockIdx.x : sp.owner(u - k0 + nk - 1);
         bar_sync(6, kSoft);
         if (tid == 0) *s_last = !*(volatile int*)s_abort && atom_add_acq_rel_gpu(p.tickets + c0, 1) == c1 - c0;
         bar_sync(6, kSoft);
@@ -1092,13 +1074,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int nb = min(batch, rows - r0);
             for (int r = tid; r < nb; r += kSoft) {
               float M = -INFINITY, L = 0.f;
-#pragma unroll 4
+#pragma unroll 2
               for (int k = 0; k < np; ++k) {
                 const float m = __ldcg(piece(k) + (size_t)kRows * kD + r0 + r);
                 wt[k * batch + r] = m;
                 M = fmaxf(M, m);
               }
-#pragma unroll 4
+#pragma unroll 2
               for (int k = 0; k < np; ++k) {
                 const float m = wt[k * batch + r], x = m == -INFINITY ? 0.f : ex2(m - M);
                 const float lk = __ldcg(piece(k) + (size_t)kRows * kD + kRows + r0 + r);
