@@ -1064,28 +1064,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         bar_sync(6, kSoft);
         if (*(volatile int*)s_last) {
           const int np = c1 - c0 + 1;
-          // weights [pieces][batch of rows] and sums [batch] where results are staged, as many
-          // rows at a time as fit
-          const int batch = min(rows, (kEarlyQ ? 1 : kQ1) * kSlot / 4 / (np + 1));
+          // maxima, then weights, [pieces][batch of rows], sums likewise, and the rows' totals
+          // [batch] where results are staged, as many rows at a time as fit. Everything is read
+          // from L2 once, so what counts is how many loads are under way: pieces are read side
+          // by side for the statistics, eight rows of two pieces per thread for O.
+          const int batch = min(rows, (kEarlyQ ? 1 : kQ1) * kSlot / 4 / (2 * np + 1));
           float* wt = (float*)stage;
-          float* total = wt + (size_t)np * batch;
+          float* ls = wt + (size_t)np * batch;
+          float* total = ls + (size_t)np * batch;
           auto piece = [&](int k) { return p.part + ((size_t)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * kPartFloats; };
+#pragma unroll 1
           for (int r0 = 0; r0 < rows; r0 += batch) {
             const int nb = min(batch, rows - r0);
+#pragma unroll 4
+            for (int e = tid; e < np * nb; e += kSoft) {
+              const int k = e / nb, r = e - k * nb;
+              const float* st = piece(k) + (size_t)kRows * kD + r0 + r;
+              wt[k * batch + r] = __ldcg(st);
+              ls[k * batch + r] = __ldcg(st + kRows);
+            }
+            bar_sync(6, kSoft);
             for (int r = tid; r < nb; r += kSoft) {
               float M = -INFINITY, L = 0.f;
-#pragma unroll 2
-              for (int k = 0; k < np; ++k) {
-                const float m = __ldcg(piece(k) + (size_t)kRows * kD + r0 + r);
-                wt[k * batch + r] = m;
-                M = fmaxf(M, m);
-              }
-#pragma unroll 2
+#pragma unroll 1
+              for (int k = 0; k < np; ++k) M = fmaxf(M, wt[k * batch + r]);
+#pragma unroll 1
               for (int k = 0; k < np; ++k) {
                 const float m = wt[k * batch + r], x = m == -INFINITY ? 0.f : ex2(m - M);
-                const float lk = __ldcg(piece(k) + (size_t)kRows * kD + kRows + r0 + r);
                 wt[k * batch + r] = x;
-                if (x != 0.f) L = fmaf(x, lk, L);
+                if (x != 0.f) L = fmaf(x, ls[k * batch + r], L);
               }
               total[r] = L;
               if (!W.prompt) {
@@ -1094,29 +1101,45 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
             bar_sync(6, kSoft);
-            for (int e = tid; e < nb * (kD / 4); e += kSoft) {
-              const int r = e >> 5, rr = r0 + r, c4 = e & 31;
-              float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+            // warp w: rows w, w + 8, ...; a lane has four columns
+#pragma unroll 1
+            for (int rb = warp; rb < nb; rb += 8 * kSoftWarps) {
+              float4 acc[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
               for (int k = 0; k < np; ++k) {
-                const float x = wt[k * batch + r];
-                const float4 v = __ldcg((const float4*)(piece(k) + (size_t)rr * kD) + c4);
-                if (x != 0.f) {
-                  acc.x = fmaf(x, v.x, acc.x);
-                  acc.y = fmaf(x, v.y, acc.y);
-                  acc.z = fmaf(x, v.z, acc.z);
-                  acc.w = fmaf(x, v.w, acc.w);
+                const float4* src = (const float4*)(piece(k) + (size_t)(r0 + rb) * kD) + lane;
+                float4 v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  if (rb + j * kSoftWarps < nb) v[j] = __ldcg(src + j * kSoftWarps * (kD / 4));
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  const float x = rb + j * kSoftWarps < nb ? wt[k * batch + rb + j * kSoftWarps] : 0.f;
+                  if (x != 0.f) {
+                    acc[j].x = fmaf(x, v[j].x, acc[j].x);
+                    acc[j].y = fmaf(x, v[j].y, acc[j].y);
+                    acc[j].z = fmaf(x, v[j].z, acc[j].z);
+                    acc[j].w = fmaf(x, v[j].w, acc[j].w);
+                  }
                 }
               }
-              const size_t o = out_row(rr) * kD + 4 * c4;
-              if (!W.prompt) {
-                *(float4*)(p.pre_o + o) = acc;
-              } else {
-                const float L = total[r], iv = L == 0.f ? 0.f : 1.0f / L;
-                if constexpr (PARTS == 1)
-                  *(uint2*)((__nv_bfloat16*)p.out + o) = make_uint2(bf2(acc.x * iv, acc.y * iv), bf2(acc.z * iv, acc.w * iv));
-                else
-                  *(float4*)((float*)p.out + o) = make_float4(acc.x * iv, acc.y * iv, acc.z * iv, acc.w * iv);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const int r = rb + j * kSoftWarps;
+                if (r >= nb) break;
+                const size_t o = out_row(r0 + r) * kD + 4 * lane;
+                if (!W.prompt) {
+                  *(float4*)(p.pre_o + o) = acc[j];
+                } else {
+                  const float L = total[r], iv = L == 0.f ? 0.f : 1.0f / L;
+                  if constexpr (PARTS == 1)
+                    *(uint2*)((__nv_bfloat16*)p.out + o) =
+                        make_uint2(bf2(acc[j].x * iv, acc[j].y * iv), bf2(acc[j].z * iv, acc[j].w * iv));
+                  else
+                    *(float4*)((float*)p.out + o) = make_float4(acc[j].x * iv, acc[j].y * iv, acc[j].z * iv, acc[j].w * iv);
+                }
               }
             }
             bar_sync(6, kSoft);
