@@ -334,6 +334,29 @@ def test_attention_in_a_graph_and_on_another_stream(cuda_lib, op):
     assert api.check_device_error() == 0
 
 
+def test_one_workspace_for_calls_of_different_sizes(cuda_lib):
+    # split sequences (tickets) of one batch size after another, in one workspace
+    g = _gen(24)
+    hq, hkv, ps = 8, 2, 16
+    ws = torch.zeros(max(api.attn_shared_workspace_bytes(b, hq, hkv) for b in (1, 3, 40)), dtype=torch.uint8,
+                     device=DEV)
+    for B in (40, 1, 3, 40, 2):
+        lens = [700 + 40 * i for i in range(B)]
+        lens[0] = 5000
+        kp, vp, pt = _cache(g, lens, hkv, ps, [(0, 10)] * B)
+        q = torch.randn((B, hq, D), generator=g, device=DEV)
+        for _ in range(2):
+            out = api.attn_decode_shared(q, kp, vp, pt, _ints(lens), _ints([0, B]), _ints([160]), SCALE, workspace=ws)
+        _check_rows(out, q, kp, vp, pt, list(range(B)), lens, sorted({0, B // 2, B - 1}))
+    ws = torch.zeros(api.verify_sample_workspace_bytes(9), dtype=torch.uint8, device=DEV)
+    for B in (2, 9, 1, 5, 9):
+        p = torch.softmax(torch.randn((B, 2, 9000), generator=g, device=DEV), -1)
+        q = torch.softmax(torch.randn((B, 1, 9000), generator=g, device=DEV), -1)
+        d = torch.randint(0, 9000, (B, 1), generator=g, device=DEV).int()
+        _verify(p, q, d, torch.rand((B, 2), generator=g, device=DEV), workspace=ws)
+    assert api.check_device_error() == 0
+
+
 # ------------------------------------------------------------------------------------------ page operations
 
 
@@ -474,13 +497,13 @@ def test_page_operations_in_a_graph(cuda_lib):
 # -------------------------------------------------------------------------------------- sampled verification
 
 
-def _verify(p, q, draft, u, n_draft=None, steps=12, start=None):
+def _verify(p, q, draft, u, n_draft=None, steps=12, start=None, workspace=None):
     B, k, V = p.shape
     step = start.clone() if start is not None else torch.zeros(B, dtype=torch.int32, device=DEV)
     tok, pos = torch.full((B,), -5, dtype=torch.int32, device=DEV), torch.arange(B, dtype=torch.int32, device=DEV)
     out = torch.full((B, steps), -1, dtype=torch.int32, device=DEV)
     first, n0 = step.tolist(), pos.tolist()
-    m = api.verify_sample(p, q, draft, u, tok, pos, step, out, n_draft=n_draft)
+    m = api.verify_sample(p, q, draft, u, tok, pos, step, out, n_draft=n_draft, workspace=workspace)
     host = [x.double().cpu().numpy() if x is not None else None for x in (p, q, u)]
     d = draft.cpu().numpy() if draft is not None else np.zeros((B, 0), int)
     err = 0

@@ -64,7 +64,7 @@ constexpr int kMinUnits = 2;             // units per CTA below which fewer CTAs
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMove = 8.0f;            // log2 units a score may pass the reference maximum
 constexpr int kMaxGrid = 192;            // CTAs (SMs) the workspace has room for
-constexpr size_t kPartFloats = (size_t)kRows * (kD + 2);
+constexpr size_t kPartFloats = kPieceFloats;
 
 struct Params {
   const void* q;
@@ -79,6 +79,8 @@ struct Params {
   float* part;             // [grid][2][kPartFloats]: O [rows][128], m [rows], l [rows]
   int* tickets;            // [grid], zero between calls
   float *pre_o, *pre_m, *pre_l;   // shared form: O, m, l of each (sequence, q head)
+  AttnFrom* from;                 // ... or where their pieces are, per (sequence, kv head)
+  PageDiv div;
   int* err;
 };
 
@@ -270,7 +272,7 @@ __device__ __noinline__ void patch_row(const Params& p, const int32_t* pt, int g
   uint32_t any = 0;
   for (int k = 0; k < 32; ++k) add[k] = 0.f;
   for (int key = first; key < last; ++key) {
-    const PagedSlot sl = paged_slot(pt, key, p.page_size, p.n_pages);
+    const PagedSlot sl = paged_slot(pt, key, p.page_size, p.div, p.n_pages);
     const __nv_bfloat16* v = p.v_pages + (((size_t)sl.page * p.Hkv + g) * p.page_size + sl.slot) * kD + d0;
     for (int k = 0; k < 32; ++k) {
       const float f = __bfloat162float(v[k]);
@@ -517,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int key = p.box ? key0 + (lane >> 1) * p.box : key0 + 32 * j + lane;
           x.row[j] = -1;
           if (i < n && key < min(seen_max, key0 + kKeys) && (j == 0 || !p.box)) {
-            const PagedSlot sl = paged_slot(pt, key, p.page_size, p.n_pages);
+            const PagedSlot sl = paged_slot(pt, key, p.page_size, p.div, p.n_pages);
             if (!sl.ok) set_error(p.err, QD_DEVERR_PAGE);
             x.row[j] = (sl.page * p.Hkv + g) * p.page_size + sl.slot;
           }
@@ -1054,8 +1056,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      // ---- a shared row tile: the last of its CTAs joins the pieces in key order
-      if (!whole) {   // the same in all softmax threads
+      if (!W.prompt && k0 == 0 && tid < packed) {   // the kernel that reads the rest joins the pieces
+        AttnFrom* f = p.from + (size_t)(first_row + tid) * p.Hkv + g;
+        f->first = blockIdx.x;
+        f->pieces = whole ? 0 : sp.owner(u + nk - 1) - (int)blockIdx.x + 1;
+        f->row = tid << p.log_rep;
+      }
+      // ---- a prompt's row tile of several CTAs: the last of them joins the pieces in key order
+      if (W.prompt && !whole) {   // the same in all softmax threads
         // where the tile's units lie: the CTAs of its first and last
         const int c0 = k0 == 0 ? (int)blockIdx.x : sp.owner(u - k0);
         const int c1 = k1 == nk ? (int)blockIdx.x : sp.owner(u - k0 + nk - 1);
@@ -1095,10 +1103,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (x != 0.f) L = fmaf(x, ls[k * batch + r], L);
               }
               total[r] = L;
-              if (!W.prompt) {
-                p.pre_m[out_row(r0 + r)] = M;
-                p.pre_l[out_row(r0 + r)] = L;
-              }
             }
             bar_sync(6, kSoft);
             // warp w: rows w, w + 8, ...; a lane has four columns
@@ -1130,16 +1134,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int r = rb + j * kSoftWarps;
                 if (r >= nb) break;
                 const size_t o = out_row(r0 + r) * kD + 4 * lane;
-                if (!W.prompt) {
-                  *(float4*)(p.pre_o + o) = acc[j];
-                } else {
-                  const float L = total[r], iv = L == 0.f ? 0.f : 1.0f / L;
-                  if constexpr (PARTS == 1)
-                    *(uint2*)((__nv_bfloat16*)p.out + o) =
-                        make_uint2(bf2(acc[j].x * iv, acc[j].y * iv), bf2(acc[j].z * iv, acc[j].w * iv));
-                  else
-                    *(float4*)((float*)p.out + o) = make_float4(acc[j].x * iv, acc[j].y * iv, acc[j].z * iv, acc[j].w * iv);
-                }
+                const float L = total[r], iv = L == 0.f ? 0.f : 1.0f / L;
+                if constexpr (PARTS == 1)
+                  *(uint2*)((__nv_bfloat16*)p.out + o) =
+                      make_uint2(bf2(acc[j].x * iv, acc[j].y * iv), bf2(acc[j].z * iv, acc[j].w * iv));
+                else
+                  *(float4*)((float*)p.out + o) = make_float4(acc[j].x * iv, acc[j].y * iv, acc[j].z * iv, acc[j].w * iv);
               }
             }
             bar_sync(6, kSoft);
@@ -1191,7 +1191,7 @@ cudaError_t launch(const Params& p, const CUtensorMap& tk, const CUtensorMap& tv
 // Workspace: tickets, then the partials; the shared form's prefix results behind them.
 constexpr size_t kTicketBytes = 1024;
 
-cudaError_t run(const AttnRowsArgs& a, float* pre_o, const Launch& L) {
+cudaError_t run(const AttnRowsArgs& a, float* pre_o, AttnFrom* from, const Launch& L) {
   Params p = {};
   p.q = a.q; p.q_stride = a.q_stride;
   p.k_pages = (const __nv_bfloat16*)a.k_pages; p.v_pages = (const __nv_bfloat16*)a.v_pages;
@@ -1207,6 +1207,8 @@ cudaError_t run(const AttnRowsArgs& a, float* pre_o, const Launch& L) {
   p.tickets = (int*)a.workspace;
   p.part = (float*)((unsigned char*)a.workspace + kTicketBytes);
   p.pre_o = pre_o;
+  p.from = from;
+  p.div = make_page_div(a.page_size);
   p.pre_m = pre_o ? pre_o + (size_t)a.n_rows * a.Hq * kD : nullptr;
   p.pre_l = pre_o ? p.pre_m + (size_t)a.n_rows * a.Hq : nullptr;
   p.err = L.err;
@@ -1229,7 +1231,12 @@ cudaError_t run(const AttnRowsArgs& a, float* pre_o, const Launch& L) {
 
 size_t attn_rows_workspace_bytes() { return kTicketBytes + (size_t)grid_ctas() * 2 * kPartFloats * 4; }
 
-cudaError_t launch_attn_prompt(const AttnRowsArgs& a, const Launch& L) { return run(a, nullptr, L); }
-cudaError_t launch_attn_prefix(const AttnRowsArgs& a, float* pre, const Launch& L) { return run(a, pre, L); }
+cudaError_t launch_attn_prompt(const AttnRowsArgs& a, const Launch& L) { return run(a, nullptr, nullptr, L); }
+
+cudaError_t launch_attn_prefix(const AttnRowsArgs& a, float* pre, AttnFrom* from, AttnPieces* pieces,
+                               const Launch& L) {
+  *pieces = {(const float*)((const unsigned char*)a.workspace + kTicketBytes), grid_ctas()};
+  return run(a, pre, from, L);
+}
 
 }  // namespace qd

@@ -98,6 +98,15 @@ QD_DEV PagedSlot paged_slot(const int32_t* pt_row, int t, int ps, int n_pages) {
   return PagedSlot{ok ? page : 0, t - lp * ps, ok};
 }
 
+// The same with the division by the page size as a multiplication: q = t * mul >> (31 + shift)
+// for 0 <= t < 2^31, mul = ceil(2^(31 + shift) / ps), shift = ceil(log2 ps).
+QD_DEV PagedSlot paged_slot(const int32_t* pt_row, int t, int ps, const PageDiv& d, int n_pages) {
+  const int lp = (int)((uint64_t)(uint32_t)t * d.mul >> (31 + d.shift));
+  const int page = pt_row[lp];
+  const bool ok = page >= 0 && page < n_pages;
+  return PagedSlot{ok ? page : 0, t - lp * ps, ok};
+}
+
 // Sticky device error word (bits QD_DEVERR_*), one per process.
 QD_DEV void set_error(int* err, int bit) {
   if (err) atomicOr(err, bit);

@@ -291,6 +291,16 @@ cudaError_t launch_prefill_finish(int32_t* pos, int n, const Launch& L);
 // segment's page-table row. Prompt form (shared_lens null): segment i is sequence i, row
 // j of its n rows sees keys 0 .. seq_lens[i] - n + j. Shared form: the segments are groups
 // of sequences (row = sequence) whose first shared_lens[i] tokens lie in the same pages.
+struct PageDiv {
+  uint32_t mul;
+  int shift;
+};
+inline PageDiv make_page_div(int ps) {
+  int s = 0;
+  while ((1LL << s) < ps) ++s;
+  return PageDiv{(uint32_t)((((1ULL << (31 + s)) + ps - 1)) / ps), s};
+}
+
 struct AttnRowsArgs {
   const void* q;           // f32 or bf16 [n_rows, Hq, D], rows q_stride elements apart
   int q_f32;
@@ -309,9 +319,21 @@ struct AttnRowsArgs {
 size_t attn_rows_workspace_bytes();
 size_t attn_shared_workspace_bytes(int B, int Hq, int Hkv);
 cudaError_t launch_attn_prompt(const AttnRowsArgs& a, const Launch& L);
-// The groups' shared tokens alone: pre = O [n_rows, Hq, D], m, l [n_rows, Hq] (f32; reference
-// maximum in log2 units) of every row whose group shares any.
-cudaError_t launch_attn_prefix(const AttnRowsArgs& a, float* pre, const Launch& L);
+// The groups' shared tokens alone, of every row whose group shares any, with one entry of
+// `from` per (row, kv head). pieces 0: O [Hq, D], m, l [Hq] of the row in pre (O [n_rows, Hq,
+// D], m, l [n_rows, Hq]; f32, reference maximum in log2 units). Otherwise they are still in
+// that many pieces (AttnPieces): piece k's rows from `row` on, one per q head.
+struct AttnFrom {
+  int first, pieces, row;
+};
+struct AttnPieces {
+  const float* base;       // [n][2][kPieceFloats]: O [kPieceRows][D], m, l [kPieceRows]
+  int n;                   // CTAs
+};
+constexpr int kPieceRows = 128;
+constexpr size_t kPieceFloats = (size_t)kPieceRows * (128 + 2);
+cudaError_t launch_attn_prefix(const AttnRowsArgs& a, float* pre, AttnFrom* from, AttnPieces* pieces,
+                               const Launch& L);
 cudaError_t launch_attn_shared(const AttnRowsArgs& a, const Launch& L);
 
 // ----------------------------------------------------------------- cache pages (pages.cu)

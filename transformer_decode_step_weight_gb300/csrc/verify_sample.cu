@@ -317,10 +317,13 @@ __global__ void __launch_bounds__(kTh) verify_sample_kernel(const VsParams p) {
 }
 
 constexpr int kMaxChunks = 1024;   // chunk sums per sequence in the workspace
+constexpr size_t kTicketBytes = 65536 * 4;
 
 }  // namespace
 
-size_t verify_sample_workspace_bytes(int B) { return (size_t)B * kMaxChunks * 8 + (((size_t)B * 4 + 15) & ~(size_t)15); }
+// Tickets first, with room for every batch (their place must not depend on the call: they are
+// zero between calls of different sizes), then the chunk sums.
+size_t verify_sample_workspace_bytes(int B) { return kTicketBytes + (size_t)B * kMaxChunks * 8; }
 int verify_sample_max_vocab() { return kMaxChunks * kTh * 16; }
 
 cudaError_t launch_verify_sample(const VerifySampleArgs& a, const Launch& L) {
@@ -331,8 +334,8 @@ cudaError_t launch_verify_sample(const VerifySampleArgs& a, const Launch& L) {
   p.B = a.B; p.k = a.k; p.V = a.V;
   p.tok = a.tok; p.pos = a.pos; p.step = a.step; p.out = a.out_tokens; p.max_steps = a.max_steps;
   p.n_accept = a.n_accept;
-  p.part = (double*)a.workspace;
-  p.cnt = (int*)((unsigned char*)a.workspace + (size_t)a.B * kMaxChunks * 8);
+  p.cnt = (int*)a.workspace;
+  p.part = (double*)((unsigned char*)a.workspace + kTicketBytes);
   p.err = L.err;
   p.vec = ((uintptr_t)a.target & 15u) == 0 && a.t_stride % 4 == 0 &&
           (a.k == 1 || (((uintptr_t)a.draft_probs & 15u) == 0 && a.d_stride % 4 == 0));
