@@ -265,25 +265,39 @@ struct Place {
 };
 
 // Values of O that are not finite: what the row sees of V's own NaN and infinities in dims
-// [d0, d0 + 32) of the keys [first, last) decides (the product of a weight's part and an
-// infinity may have given NaN, or an entry was taken out of a masked tile).
-__device__ __noinline__ void patch_row(const Params& p, const int32_t* pt, int g, int first, int last, int d0, float* ov) {
-  float add[32];
-  uint32_t any = 0;
-  for (int k = 0; k < 32; ++k) add[k] = 0.f;
+// [d0, d0 + 64) of the keys [first, last) decides (the product of a weight's part and an
+// infinity may have given NaN, or an entry was taken out of a masked tile). The row's values
+// are in memory by now, f32 or (half) bf16, 16-byte piece c at c ^ xr.
+__device__ __noinline__ void patch_row(const Params& p, const int32_t* pt, int g, int first, int last, int d0,
+                                       unsigned char* row, int xr, bool half) {
+  float add[64];
+  unsigned long long any = 0;
+#pragma unroll 1
+  for (int k = 0; k < 64; ++k) add[k] = 0.f;
+#pragma unroll 1
   for (int key = first; key < last; ++key) {
     const PagedSlot sl = paged_slot(pt, key, p.page_size, p.div, p.n_pages);
     const __nv_bfloat16* v = p.v_pages + (((size_t)sl.page * p.Hkv + g) * p.page_size + sl.slot) * kD + d0;
-    for (int k = 0; k < 32; ++k) {
+#pragma unroll 1
+    for (int k = 0; k < 64; ++k) {
       const float f = __bfloat162float(v[k]);
       if (!(fabsf(f) < INFINITY)) {
         add[k] += f;
-        any |= 1u << k;
+        any |= 1ull << k;
       }
     }
   }
-  for (int k = 0; k < 32; ++k)
-    if ((any >> k) & 1) ov[k] = add[k];
+#pragma unroll 1
+  for (int k = 0; k < 64; ++k) {
+    if (!((any >> k) & 1)) continue;
+    if (half) {
+      const int c = (d0 + k) >> 3;
+      ((__nv_bfloat16*)(row + ((c ^ xr) << 4)))[(d0 + k) & 7] = __float2bfloat16_rn(add[k]);
+    } else {
+      const int c = (d0 + k) >> 2;
+      ((float*)(row + ((c ^ xr) << 4)))[(d0 + k) & 3] = add[k];
+    }
+  }
 }
 
 template <typename T, int PARTS>
@@ -974,85 +988,64 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = k0 == 0 && k1 == nk;
       float* part = p.part + ((size_t)blockIdx.x * 2 + (k0 == 0 ? 1 : 0)) * kPartFloats;
       const bool patch = *(volatile int*)(s_patch + (piece_no & 1)) == (int)piece_no + 1;
-      auto out_row = [&](int r) {   // (packed row, q head) of row r of the tile
-        return (size_t)(first_row + (r >> p.log_rep)) * p.Hq + (g << p.log_rep) + (r & (p.rep - 1));
-      };
+      // row r of the tile in [n_rows, Hq]: tile0 + out_row(r)
+      const size_t tile0 = (size_t)first_row * p.Hq + (g << p.log_rep);
+      auto out_row = [&](int r) { return (r >> p.log_rep) * p.Hq + (r & (p.rep - 1)); };
       const int col0 = 64 * hf;
-      const float inv = l == 0.f ? 0.f : 1.0f / l;   // a row that saw nothing gives 0
       const bool final_out = whole && W.prompt;      // else O as it is, with m and l
+      const float inv = l == 0.f ? 0.f : 1.0f / l;   // a row that saw nothing gives 0
       // bf16 results and the f32 form's values go out by whole rows, through shared memory:
-      // 16-byte pieces, swizzled
-      float* dst_f32 = !whole ? part + (size_t)row * kD : p.pre_o + (valid && !W.prompt ? out_row(row) * kD : 0);
+      // 16-byte pieces, swizzled; the bf16 form's partial values as they are
+      float* dst = !whole ? part : (W.prompt ? (float*)p.out : p.pre_o) + tile0 * kD;
+      const bool staged = PARTS == 3 || final_out;
+      unsigned char* mine = stage + row * (PARTS == 3 ? 512 : 256);
+      const int xr = staged ? row & (PARTS == 3 ? 31 : 15) : 0;
+      if (!staged) mine = (unsigned char*)(dst + (size_t)(whole ? out_row(valid ? row : 0) : row) * kD);
+      const float f = final_out ? inv : 1.f;
+      float z = 0.f;   // 0 unless a value is not finite
 #pragma unroll(kFresh ? kCols / 32 : 1)
       for (int e = 0; e < kCols; e += 32) {
         float ov[32];
         ld32(to + e, ov);
         wait_ld();
-        if constexpr (kFresh) {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) ov[k] += osum[e + k];
+        for (int k = 0; k < 32; ++k) {
+          if constexpr (kFresh) ov[k] += osum[e + k];
+          z = fmaf(ov[k], 0.f, z);
+          ov[k] *= f;
         }
-        float z = 0.f;   // 0 unless a value is not finite
-#pragma unroll
-        for (int k = 0; k < 32; ++k) z = fmaf(ov[k], 0.f, z);
-        if ((patch || z != 0.f) && valid && l == l) {
-          float tmp[32];
-#pragma unroll
-          for (int k = 0; k < 32; ++k) tmp[k] = ov[k];
-          patch_row(p, pt, g, k0 * kKeys, min(lim, k1 * kKeys), col0 + e, tmp);
-#pragma unroll
-          for (int k = 0; k < 32; ++k) ov[k] = tmp[k];
-        }
-        if (final_out && PARTS == 1) {
+        if (PARTS == 1 && final_out) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            *(uint4*)(stage + row * 256 + ((((col0 + e) / 8 + k) ^ (row & 15)) << 4)) =
-                make_uint4(bf2(ov[8 * k] * inv, ov[8 * k + 1] * inv), bf2(ov[8 * k + 2] * inv, ov[8 * k + 3] * inv),
-                           bf2(ov[8 * k + 4] * inv, ov[8 * k + 5] * inv), bf2(ov[8 * k + 6] * inv, ov[8 * k + 7] * inv));
-        } else if (PARTS == 3) {
-          const float f = final_out ? inv : 1.f;
+            *(uint4*)(mine + ((((col0 + e) / 8 + k) ^ xr) << 4)) =
+                make_uint4(bf2(ov[8 * k], ov[8 * k + 1]), bf2(ov[8 * k + 2], ov[8 * k + 3]),
+                           bf2(ov[8 * k + 4], ov[8 * k + 5]), bf2(ov[8 * k + 6], ov[8 * k + 7]));
+        } else if (PARTS == 3 || (valid && !dead)) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            *(float4*)(stage + row * 512 + ((((col0 + e) / 4 + k) ^ (row & 31)) << 4)) =
-                make_float4(ov[4 * k] * f, ov[4 * k + 1] * f, ov[4 * k + 2] * f, ov[4 * k + 3] * f);
-        } else if (valid && !dead) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            *((float4*)(dst_f32 + col0 + e) + k) = make_float4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
+            *(float4*)(mine + ((((col0 + e) / 4 + k) ^ xr) << 4)) = make_float4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
         }
       }
+      if ((patch || z != 0.f) && valid && !dead && l == l)
+        patch_row(p, pt, g, k0 * kKeys, min(lim, k1 * kKeys), col0, mine, xr, PARTS == 1 && final_out);
       if (valid && !dead && !final_out && hf == 0) {
-        if (!whole) {
-          part[(size_t)kRows * kD + row] = ms;
-          part[(size_t)kRows * kD + kRows + row] = l;
-        } else {
-          p.pre_m[out_row(row)] = ms;
-          p.pre_l[out_row(row)] = l;
-        }
+        float* m_at = whole ? p.pre_m + tile0 + out_row(row) : part + (size_t)kRows * kD + row;
+        float* l_at = whole ? p.pre_l + tile0 + out_row(row) : part + (size_t)kRows * (kD + 1) + row;
+        *m_at = ms;
+        *l_at = l;
       }
-      if (final_out || PARTS == 3) {
+      if (staged) {
         // the rows that this warp's lanes and their other holders' wrote
         bar_sync(2 + (warp & 3), 64);
         const int r0 = (warp & 3) * 32 + hf * 16;
-        if (!dead) {
-          if constexpr (PARTS == 1) {
-            const int pc = lane & 15;
+        constexpr int kLanes = PARTS == 3 ? 32 : 16;   // lanes per row
 #pragma unroll 4
-            for (int i = 0; i < 16; i += 2) {
-              const int r = r0 + i + (lane >> 4);
-              if (r < rows)
-                *(uint4*)((__nv_bfloat16*)p.out + out_row(r) * kD + pc * 8) =
-                    *(const uint4*)(stage + r * 256 + ((pc ^ (r & 15)) << 4));
-            }
-          } else {
-#pragma unroll 4
-            for (int i = 0; i < 16; ++i) {
-              const int r = r0 + i;
-              if (r < rows) {
-                float* d = !whole ? part + (size_t)r * kD : (W.prompt ? (float*)p.out : p.pre_o) + out_row(r) * kD;
-                *(float4*)(d + 4 * lane) = *(const float4*)(stage + r * 512 + ((lane ^ (r & 31)) << 4));
-              }
-            }
+        for (int i = 0; i < 16; i += 32 / kLanes) {
+          const int r = r0 + i + lane / kLanes, pc = lane & (kLanes - 1);
+          const uint4 v = *(const uint4*)(stage + r * (PARTS == 3 ? 512 : 256) + ((pc ^ (r & (kLanes - 1))) << 4));
+          if (r < rows && !dead) {
+            if constexpr (PARTS == 3) *(uint4*)(dst + (size_t)(whole ? out_row(r) : r) * kD + 4 * pc) = v;
+            else *(uint4*)((__nv_bfloat16*)p.out + (tile0 + out_row(r)) * kD + 8 * pc) = v;
           }
         }
       }
@@ -1084,7 +1077,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int r0 = 0; r0 < rows; r0 += batch) {
             const int nb = min(batch, rows - r0);
-#pragma unroll 4
+#pragma unroll 2
             for (int e = tid; e < np * nb; e += kSoft) {
               const int k = e / nb, r = e - k * nb;
               const float* st = piece(k) + (size_t)kRows * kD + r0 + r;
@@ -1111,7 +1104,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               float4 acc[8];
 #pragma unroll
               for (int j = 0; j < 8; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
+#pragma unroll 1
               for (int k = 0; k < np; ++k) {
                 const float4* src = (const float4*)(piece(k) + (size_t)(r0 + rb) * kD) + lane;
                 float4 v[8];
@@ -1133,7 +1126,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int j = 0; j < 8; ++j) {
                 const int r = rb + j * kSoftWarps;
                 if (r >= nb) break;
-                const size_t o = out_row(r0 + r) * kD + 4 * lane;
+                const size_t o = (tile0 + out_row(r0 + r)) * kD + 4 * lane;
                 const float L = total[r], iv = L == 0.f ? 0.f : 1.0f / L;
                 if constexpr (PARTS == 1)
                   *(uint2*)((__nv_bfloat16*)p.out + o) =
