@@ -14,8 +14,8 @@
 // keep a reference maximum that moves when a score passes it by more than 2^8 (so that O
 // is rescaled rarely), and write the weights back over S as the A operand of O += P V.
 // V is read as it lies in the cache (keys x dims) through an MN-major descriptor, so no
-// transposed copy exists. A ring of 32 KB slots holds K and V tiles in the order the
-// products need them.
+// transposed copy exists. Two rings of 32 KB slots hold K and
+// V tiles.
 //   * bf16 q: weights rounded to bf16 (each off by 2^-8 of itself at most, as the
 //     result's own rounding); sums, statistics and O in f32.
 //   * f32 q: q and the weights as three bf16 parts each (24 bits; two would leave
@@ -53,8 +53,8 @@ constexpr int kSlot = 2 * kChunk;        // a K or V tile, or one part of a row 
 constexpr int kSoftWarps = 8;
 constexpr int kSoft = 32 * kSoftWarps;
 // warp roles behind the softmax warps: the first issues the products
-constexpr int kProducer = kSoftWarps + 1;
-constexpr int kFixer = kSoftWarps + 2;   // and the one after it
+constexpr int kProducer = kSoftWarps + 1;   // K tiles; the warp after it V tiles
+constexpr int kFixer = kSoftWarps + 3;
 constexpr int kThreads = 32 * (kSoftWarps + 4);
 constexpr int kMisc = 3072;              // barriers and small arrays in front of Q and the ring
 constexpr int kData = 7 * kSlot;         // 224 KB: Q parts and ring slots
@@ -312,7 +312,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kRing = 7 - kQ;
   constexpr int kCols = 64;                   // keys of a tile, and O columns, per softmax thread
   constexpr bool kFresh = PARTS == 3;         // O of each tile alone in TMEM, summed in registers
-  static_assert(kRing >= 3 && kRing <= kMaxSlots, "");
+  constexpr int kRingK = kRing - 2, kRingV = 2;   // K slots, then V slots
+  static_assert(kRingK >= 2 && kRing <= kMaxSlots, "");
   extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char* data = smem + kMisc;
   uint64_t* full = (uint64_t*)smem;      // [kRing] a K or V tile landed
@@ -414,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(q_full, kSoft);
     mbar_init(v_go, 1);
     mbar_init(drained, 1);
-    mbar_init(v_fixed, 64);
+    mbar_init(v_fixed, 32);
     fence_mbar_init();
   }
   if (warp == 0) tc::alloc(tslot, 512);
@@ -468,10 +469,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // A piece is the part of one row tile that this CTA computes. Each role walks the pieces for
   // itself, so the copies and products of one run into the next; counts that several roles
-  // follow: ring entries, tiles, fixed tiles, trades, pieces.
-  uint32_t ring = 0, tile = 0, fixes = 0, trades = 0, piece_no = 0;
+  // follow: tiles, fixed tiles, trades, pieces.
+  uint32_t tile = 0, fixes = 0, trades = 0, piece_no = 0;
   int late = -1;
-  uint32_t slot = 0, slot_ph = 0;
+  // position and phase in a ring (the issuer walks both)
+  struct Ring {
+    uint32_t slot, ph;
+    QD_DEV void step(uint32_t n) {
+      if (++slot == n) {
+        slot = 0;
+        ph ^= 1;
+      }
+    }
+  };
+  Ring rk = {0, 0}, rv = {0, 0};
   [[maybe_unused]] bool first = true;
 
   struct Piece {
@@ -517,14 +528,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int g = pc.g, k0 = pc.k0, n = pc.n, seen_max = pc.seen_max, seen_min = pc.seen_min;
     const int32_t* pt = pc.pt;
 
-    if (warp == kProducer) {
-      // ---- K and V tiles in the order of the products. A lane's cache rows of a tile are
-      // looked up once, for K and V, a tile ahead of their use. TMA: lane l, box l / 2 and
+    if (warp == kProducer || warp == kProducer + 1) {
+      // ---- K or V tiles. Each has a warp of its own, since issuing the 16 copies of a tile in
+      // 16-row pages takes some 1700 cycles. A lane's cache rows of a tile are looked up a tile
+      // ahead of their use. TMA: lane l, box l / 2 and
       // dims 64 (l & 1); asynchronous copies: keys l, l + 32, ... (-1: past the keys)
       constexpr int kMine = 4;
       struct Look {
         int row[kMine];
       };
+      int bad_page = 0;
       auto look = [&](int i) {
         Look x;
         const int key0 = (k0 + i) * kKeys;
@@ -534,16 +547,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           x.row[j] = -1;
           if (i < n && key < min(seen_max, key0 + kKeys) && (j == 0 || !p.box)) {
             const PagedSlot sl = paged_slot(pt, key, p.page_size, p.div, p.n_pages);
-            if (!sl.ok) set_error(p.err, QD_DEVERR_PAGE);
+            if (!sl.ok) bad_page = 1;   // no branch on what is still being read
             x.row[j] = (sl.page * p.Hkv + g) * p.page_size + sl.slot;
           }
         }
         return x;
       };
-      auto load = [&](const CUtensorMap* map, const __nv_bfloat16* pages, const Look& x) {
-        const uint32_t slot = ring % kRing, use = ring / kRing;
-        ++ring;
-        if (use) wait(&empty[slot], (use - 1) & 1);
+      const bool is_v = warp != kProducer;
+      const CUtensorMap* map = is_v ? &tmV : &tmK;
+      const __nv_bfloat16* pages = is_v ? p.v_pages : p.k_pages;
+      const uint32_t slots = is_v ? kRingV : kRingK, slot0 = is_v ? kRingK : 0;
+      auto load = [&](const Look& x) {
+        const uint32_t slot = slot0 + rk.slot;
+        wait(&empty[slot], rk.ph ^ 1);   // (the first round's phase before the first is over)
+        rk.step(slots);
         unsigned char* dst = data + (kQ + slot) * kSlot;
         if (p.box) {
           const bool go = !__any_sync(0xffffffffu, *(volatile int*)s_abort != 0);
@@ -577,17 +594,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           late = (int)slot;
         }
       };
-      Look l0 = {}, l1 = {}, l2 = {}, l3 = {};   // tiles i .. i + 3
+      Look now = {}, next = {};
 #pragma unroll 1
-      for (int i = -3; i < n; ++i) {
-        l0 = l1;
-        l1 = l2;
-        l2 = l3;
-        l3 = look(i + 3);
-        if (i < -2) continue;
-#pragma unroll 1
-        for (int v = 1; v >= 0; --v)
-          if (v ? i >= 0 : i + 2 < n) load(v ? &tmV : &tmK, v ? p.v_pages : p.k_pages, v ? l0 : l2);
+      for (int i = -1; i < n; ++i) {
+        now = next;
+        next = look(i + 1);
+        if (i >= 0) load(now);
       }
       if (late >= 0) {
         asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -595,22 +607,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&full[late]);
         late = -1;
       }
-    } else if (warp >= kFixer) {
+      if (bad_page) set_error(p.err, QD_DEVERR_PAGE);
+    } else if (warp == kFixer) {
       // ---- V tiles that some row must not see whole: rows past everybody's keys to zero,
       // NaN and infinities in the others taken out
       // (the issuer says when: a slot's own barrier may be several phases behind a tile that is
       // still to come, which a wait on its parity cannot tell)
-      uint32_t r = ring + (n > 1 ? 2 : 1);
       for (int i = 0; i < n; ++i) {
         const int key0 = (k0 + i) * kKeys;
         if (key0 + kKeys > seen_min) {
-          const uint32_t slot = r % kRing;
+          const uint32_t slot = kRingK + (tile + i) % kRingV;
           wait(v_go, fixes++ & 1);
-          wait(&full[slot], (r / kRing) & 1);   // done; orders the copy before this thread's reads
+          wait(&full[slot], ((tile + i) / kRingV) & 1);   // done; orders the copy before this thread's reads
           unsigned char* v = data + (kQ + slot) * kSlot;
           const int lo = max(0, seen_min - key0), hi = seen_max - key0;
-          // thread: 16-byte piece c of every fourth key, four cells at a time
-          constexpr int kStep = 4;
+          // lane: 16-byte piece c of every second key, four cells at a time
+          constexpr int kStep = 2;
           const int ft = tid - 32 * kFixer, c = ft & 15;
           unsigned char* col = v + (c >> 3) * kChunk;
           const int split = min(hi, kKeys);
@@ -642,26 +654,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
           mbar_arrive(v_fixed);
         }
-        r += i + 2 < n ? 2 : 1;
       }
-      ring += 2 * n;
     } else {
-      // ---- the products, in the order K0 K1 V0 K2 V1 ... of the ring: S runs two tiles ahead
-      // of P V. What this warp does between two products is time the tensor cores may idle (a
+      // ---- the products: S runs two tiles ahead of P V. What this warp does between two products is time the tensor cores may idle (a
       // tcgen05 instruction takes it 50 cycles or more), so waits that are usually over come
       // early and slots are counted, not divided.
       const bool lead = lane == 0;
       const uint64_t dq = tc::desc_sw128(smem_u32(data));
       const uint32_t ring0 = smem_u32(data) + kQ * kSlot;
-      auto step = [&] {
-        if (++slot == kRing) {
-          slot = 0;
-          slot_ph ^= 1;
-        }
-      };
       // S into buffer b from a K tile; small parts first
-      auto mma_s = [&](int b, uint32_t kaddr) {
-        const uint64_t dk = tc::desc_sw128(kaddr);
+      auto mma_s = [&](int b) {
+        const uint64_t dk = tc::desc_sw128(ring0 + rk.slot * kSlot);
 #pragma unroll 1
         for (int part = PARTS - 1; part >= 0; --part) {
           const uint64_t da = dq + (uint64_t)(part * kSlot >> 4);
@@ -673,10 +676,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         commit(lead, &s_full[b]);
-        commit(lead, &empty[slot]);
+        commit(lead, &empty[rk.slot]);
+        rk.step(kRingK);
       };
-      auto mma_o = [&](int b, uint32_t vaddr, bool first) {
-        const uint64_t dv = desc_v(vaddr);
+      auto mma_o = [&](int b, bool first) {
+        const uint64_t dv = desc_v(ring0 + (kRingK + rv.slot) * kSlot);
 #pragma unroll 1
         for (int part = PARTS - 1; part >= 0; --part) {
           // 32 keys' weights over their own 32 scores
@@ -688,27 +692,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                    kk != 0 || part != PARTS - 1 || !first);
         }
         commit(lead, &o_done[b]);
-        commit(lead, &empty[slot]);
+        commit(lead, &empty[kRingK + rv.slot]);
+        rv.step(kRingV);
       };
       wait(q_full, piece_no & 1);
 #pragma unroll 1
       for (int i = -2; i < n; ++i) {
         if (i >= 0) {
           const uint32_t ct = tile + i;
-          wait(&full[slot], slot_ph);
+          wait(&full[kRingK + rv.slot], rv.ph);
           if ((k0 + i + 1) * kKeys > seen_min) {
             if (lead) mbar_arrive(v_go);
             wait(v_fixed, fixes++ & 1);
           }
           wait(&p_full[ct & 1], (ct >> 1) & 1);
           tc::fence_after();
-          mma_o(ct & 1, ring0 + slot * kSlot, kFresh || i == 0);
-          step();
+          mma_o(ct & 1, kFresh || i == 0);
         }
         if (i + 2 < n) {
-          wait(&full[slot], slot_ph);
-          mma_s((tile + i + 2) & 1, ring0 + slot * kSlot);
-          step();
+          wait(&full[rk.slot], rk.ph);
+          mma_s((tile + i + 2) & 1);
         }
       }
     }
@@ -1154,10 +1157,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncwarp();
-  if (warp == kProducer && *(volatile int*)s_abort && p.box && lane == 0) {
+  if ((warp == kProducer || warp == kProducer + 1) && *(volatile int*)s_abort && p.box && lane == 0) {
     // a timeout: the copies that are still under way land before the CTA leaves (bounded)
-    for (uint32_t c = ring > kRing ? ring - kRing : 0; c < ring; ++c)
-      mbar_wait_limit(&full[c % kRing], (c / kRing) & 1, p.err, 10000000ull);
+    const uint32_t slots = warp != kProducer ? kRingV : kRingK, slot0 = warp != kProducer ? kRingK : 0;
+    for (uint32_t i = 0; i < slots; ++i) {
+      const bool again = i < rk.slot;   // filled in this round of the ring
+      if (again || tile >= slots) mbar_wait_limit(&full[slot0 + i], again ? rk.ph : rk.ph ^ 1, p.err, 10000000ull);
+    }
   }
   if (warp == kSoftWarps && *(volatile int*)s_abort) {   // ... and the products (bounded)
     commit(lane == 0, drained);
