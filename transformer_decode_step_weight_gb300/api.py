@@ -266,46 +266,62 @@ def attn_decode_paged_noalloc(q, k_pages, v_pages, page_table, seq_lens, scale, 
     return out
 
 
-def _on(t, stream):
-    """The device of t current, and `stream` (its current stream by default) with it, so that
-    what a call allocates belongs to the stream that its kernels run on."""
-    if stream is None or stream == torch.cuda.current_stream(t.device):
-        return torch.cuda.device(t.device)
+# The serving calls below run many times per token, so their checks stay cheap: no context is
+# entered where the tensors' device is current and no stream is given.
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+
+
+def _raw_stream(device: int):
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(device) if get is not None else torch.cuda.current_stream(device).cuda_stream
+
+
+def _elsewhere(t, stream):
+    """None where t's device is current and no stream is given; else a context that makes both
+    current, so that what a call allocates belongs to the stream that its kernels run on."""
+    dev = t.get_device()
+    if stream is None:
+        return None if dev < 0 or _current_device() == dev else torch.cuda.device(dev)
     return torch.cuda.stream(stream)
 
 
 def _want(name, t, dtype, dims, device, shape=None):
-    """Refuses a tensor that the C entry could not take as it is (contiguous, on `device`)."""
-    if t.device != device or device.type != "cuda":
-        raise ValueError(f"{name}: on {t.device}, expected {device} (a CUDA device)")
+    """Refuses a tensor that the C entry could not take as it is (contiguous, on CUDA device `device`)."""
+    if (t.dtype is dtype and t.get_device() == device >= 0 and t.dim() == dims and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return
+    if device < 0 or t.get_device() != device:
+        raise ValueError(f"{name}: on {t.device}, expected the first tensor's device, a CUDA device")
     if t.dtype != dtype or t.dim() != dims or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous {dims}-dimensional {dtype} tensor, got {t.dtype} {tuple(t.shape)}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
 def _rows(fn, q, k_pages, v_pages, page_table, seq_lens, cu, out):
     """The common checks of attn_prompt and attn_decode_shared."""
+    dev = q.get_device()
     if q.dim() != 3 or q.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"{fn}: q must be [rows, heads, head_dim] in float32 or bfloat16")
-    if q.shape[0] and (q.stride(2) != 1 or q.stride(1) != q.shape[2]):
+    n, hq, d = q.shape
+    s0, s1, s2 = q.stride()
+    if n and (s2 != 1 or s1 != d):
         raise ValueError(f"{fn}: a row's heads must be contiguous (strides {q.stride()})")
-    _want(f"{fn}: k_pages", k_pages, torch.bfloat16, 4, q.device)
-    _want(f"{fn}: v_pages", v_pages, torch.bfloat16, 4, q.device, k_pages.shape)
-    if k_pages.shape[3] != q.shape[2]:
-        raise ValueError(f"{fn}: head_dim {q.shape[2]} and {k_pages.shape[3]}")
-    _want(f"{fn}: page_table", page_table, torch.int32, 2, q.device)
-    _want(f"{fn}: seq_lens", seq_lens, torch.int32, 1, q.device, page_table.shape[:1])
-    _want(f"{fn}: segment starts", cu, torch.int32, 1, q.device)
+    _want("k_pages", k_pages, torch.bfloat16, 4, dev)
+    _want("v_pages", v_pages, torch.bfloat16, 4, dev, k_pages.shape)
+    if k_pages.shape[3] != d:
+        raise ValueError(f"{fn}: head_dim {d} and {k_pages.shape[3]}")
+    _want("page_table", page_table, torch.int32, 2, dev)
+    _want("seq_lens", seq_lens, torch.int32, 1, dev, page_table.shape[:1])
+    _want("segment starts", cu, torch.int32, 1, dev)
     if out is not None:
-        _want(f"{fn}: out", out, q.dtype, 3, q.device, q.shape)
-    return q.stride(0) if q.shape[0] > 1 else q.shape[1] * q.shape[2]
+        _want("out", out, q.dtype, 3, dev, q.shape)
+    return s0 if n > 1 else hq * d
 
 
-def _scratch(fn, workspace, nbytes, device):
+def _scratch(workspace, nbytes, t):
     if workspace is None:
-        return torch.zeros(nbytes, dtype=torch.uint8, device=device)
-    _want(f"{fn}: workspace", workspace, torch.uint8, 1, device)
+        return torch.zeros(nbytes(), dtype=torch.uint8, device=t.device)
+    _want("workspace", workspace, torch.uint8, 1, t.get_device())
     return workspace
 
 
@@ -317,22 +333,25 @@ def attn_prompt(q, k_pages, v_pages, page_table, cu_rows, seq_lens, scale, out=N
     """Causal attention over the packed rows of several prompts: q f32 or bf16 [rows, Hq, D] (rows may be
     strided), sequence b's rows cu_rows[b] .. cu_rows[b + 1), the last of them at position seq_lens[b] - 1;
     caches bf16 [n_pages, Hkv, ps, D] with the rows' K/V written. -> [rows, Hq, D] of q's type."""
+    away = _elsewhere(q, stream)
+    if away is not None:
+        with away:
+            return attn_prompt(q, k_pages, v_pages, page_table, cu_rows, seq_lens, scale, out, workspace)
     q_stride = _rows("attn_prompt", q, k_pages, v_pages, page_table, seq_lens, cu_rows, out)
     n, Hq, D = q.shape
     B, max_pages = page_table.shape
     n_pages, Hkv, ps, _ = k_pages.shape
-    if cu_rows.numel() != B + 1:
+    if cu_rows.shape[0] != B + 1:
         raise ValueError(f"attn_prompt: {cu_rows.numel()} segment starts for {B} sequences")
-    with _on(q, stream):
-        if out is None:
-            out = torch.empty((n, Hq, D), dtype=q.dtype, device=q.device)
-        if n == 0:
-            return out
-        workspace = _scratch("attn_prompt", workspace, attn_prompt_workspace_bytes(), q.device)
-        _check(lib().qd_attn_prompt(_p(q), int(q.dtype == torch.float32), q_stride, _p(k_pages), _p(v_pages),
-                                    _p(page_table), _p(cu_rows), _p(seq_lens), B, n, Hq, Hkv, D, ps, max_pages,
-                                    n_pages, float(scale), _p(out), _p(workspace), workspace.numel(),
-                                    _stream(stream)))
+    if out is None:
+        out = torch.empty((n, Hq, D), dtype=q.dtype, device=q.device)
+    if n == 0:
+        return out
+    workspace = _scratch(workspace, attn_prompt_workspace_bytes, q)
+    _check(lib().qd_attn_prompt(q.data_ptr(), q.dtype is torch.float32, q_stride, k_pages.data_ptr(),
+                                v_pages.data_ptr(), page_table.data_ptr(), cu_rows.data_ptr(), seq_lens.data_ptr(),
+                                B, n, Hq, Hkv, D, ps, max_pages, n_pages, scale, out.data_ptr(),
+                                workspace.data_ptr(), workspace.numel(), _raw_stream(q.get_device())))
     return out
 
 
@@ -345,24 +364,29 @@ def attn_decode_shared(q, k_pages, v_pages, page_table, seq_lens, cu_seqs, share
     """attn_decode_paged for sequences that share prefixes: group i is the sequences cu_seqs[i] ..
     cu_seqs[i + 1), whose first shared_lens[i] tokens lie in the same pages (read once per group).
     q f32 or bf16 [B, Hq, D] -> [B, Hq, D] of q's type."""
+    away = _elsewhere(q, stream)
+    if away is not None:
+        with away:
+            return attn_decode_shared(q, k_pages, v_pages, page_table, seq_lens, cu_seqs, shared_lens, scale, out,
+                                      workspace)
     q_stride = _rows("attn_decode_shared", q, k_pages, v_pages, page_table, seq_lens, cu_seqs, out)
     B, Hq, D = q.shape
     n_pages, Hkv, ps, _ = k_pages.shape
-    _want("attn_decode_shared: shared_lens", shared_lens, torch.int32, 1, q.device)
-    if page_table.shape[0] != B or cu_seqs.numel() != shared_lens.numel() + 1:
+    _want("shared_lens", shared_lens, torch.int32, 1, q.get_device())
+    groups = shared_lens.shape[0]
+    if page_table.shape[0] != B or cu_seqs.shape[0] != groups + 1:
         raise ValueError(f"attn_decode_shared: {page_table.shape[0]} page tables for {B} rows, {cu_seqs.numel()} "
-                         f"group starts for {shared_lens.numel()} lengths")
-    with _on(q, stream):
-        if out is None:
-            out = torch.empty((B, Hq, D), dtype=q.dtype, device=q.device)
-        if B == 0:
-            return out
-        workspace = _scratch("attn_decode_shared", workspace, attn_shared_workspace_bytes(B, Hq, Hkv), q.device)
-        _check(lib().qd_attn_decode_shared(_p(q), int(q.dtype == torch.float32), q_stride, _p(k_pages), _p(v_pages),
-                                           _p(page_table), _p(seq_lens), _p(cu_seqs), _p(shared_lens),
-                                           shared_lens.numel(), B, Hq, Hkv, D, ps, page_table.shape[1], n_pages,
-                                           float(scale), _p(out), _p(workspace), workspace.numel(),
-                                           _stream(stream)))
+                         f"group starts for {groups} lengths")
+    if out is None:
+        out = torch.empty((B, Hq, D), dtype=q.dtype, device=q.device)
+    if B == 0:
+        return out
+    workspace = _scratch(workspace, lambda: attn_shared_workspace_bytes(B, Hq, Hkv), q)
+    _check(lib().qd_attn_decode_shared(q.data_ptr(), q.dtype is torch.float32, q_stride, k_pages.data_ptr(),
+                                       v_pages.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
+                                       cu_seqs.data_ptr(), shared_lens.data_ptr(), groups, B, Hq, Hkv, D, ps,
+                                       page_table.shape[1], n_pages, scale, out.data_ptr(), workspace.data_ptr(),
+                                       workspace.numel(), _raw_stream(q.get_device())))
     return out
 
 
@@ -376,41 +400,53 @@ def verify_sample(target_probs, draft_probs, draft, u, tok, pos, step, out_token
     padded), draft int32 [B, k - 1], u f32 [B, k]. Advances tok, pos, step [B] and out_tokens [B, max_steps] and
     returns n_accept int32 [B]."""
     fn = "verify_sample"
+    away = _elsewhere(target_probs, stream)
+    if away is not None:
+        with away:
+            return verify_sample(target_probs, draft_probs, draft, u, tok, pos, step, out_tokens, n_draft, n_accept,
+                                 workspace)
     if target_probs.dim() != 3 or target_probs.dtype != torch.float32:
         raise ValueError(f"{fn}: target_probs must be float32 [B, k, V]")
     B, k, V = target_probs.shape
-    dev = target_probs.device
-
-    def stride(name, t, rows):
-        if t.device != dev or t.dtype != torch.float32 or tuple(t.shape) != (B, rows, V):
-            raise ValueError(f"{fn}: {name} must be float32 {(B, rows, V)} on {dev}")
-        s = t.stride(1) if rows > 1 else (t.stride(0) if B > 1 else V)
-        if t.numel() and (t.stride(2) != 1 and V > 1 or (B > 1 and t.stride(0) != rows * s)):
-            raise ValueError(f"{fn}: {name}'s rows must be evenly spaced (strides {t.stride()})")
-        return s
-
-    t_stride = stride("target_probs", target_probs, k)
-    d_stride = stride("draft_probs", draft_probs, k - 1) if k > 1 else V
+    dev = target_probs.get_device()
+    t_stride = _row_stride("target_probs", target_probs, B, k, V, dev)
+    d_stride = _row_stride("draft_probs", draft_probs, B, k - 1, V, dev) if k > 1 else V
     if k > 1:
-        _want(f"{fn}: draft", draft, torch.int32, 2, dev, (B, k - 1))
-    _want(f"{fn}: u", u, torch.float32, 2, dev, (B, k))
-    for name, t in (("tok", tok), ("pos", pos), ("step", step), ("n_draft", n_draft), ("n_accept", n_accept)):
-        if t is not None:
-            _want(f"{fn}: {name}", t, torch.int32, 1, dev, (B,))
-    _want(f"{fn}: out_tokens", out_tokens, torch.int32, 2, dev)
+        _want("draft", draft, torch.int32, 2, dev, (B, k - 1))
+    _want("u", u, torch.float32, 2, dev, (B, k))
+    one = (B,)
+    _want("tok", tok, torch.int32, 1, dev, one)
+    _want("pos", pos, torch.int32, 1, dev, one)
+    _want("step", step, torch.int32, 1, dev, one)
+    if n_draft is not None:
+        _want("n_draft", n_draft, torch.int32, 1, dev, one)
+    if n_accept is not None:
+        _want("n_accept", n_accept, torch.int32, 1, dev, one)
+    else:
+        n_accept = torch.empty(B, dtype=torch.int32, device=target_probs.device)
+    _want("out_tokens", out_tokens, torch.int32, 2, dev)
     if out_tokens.shape[0] != B:
         raise ValueError(f"{fn}: out_tokens has {out_tokens.shape[0]} rows for {B} sequences")
-    with _on(target_probs, stream):
-        if n_accept is None:
-            n_accept = torch.empty(B, dtype=torch.int32, device=dev)
-        if B == 0:
-            return n_accept
-        workspace = _scratch(fn, workspace, verify_sample_workspace_bytes(B), dev)
-        _check(lib().qd_verify_sample(_p(target_probs), t_stride, _p(draft_probs) if k > 1 else None, d_stride,
-                                      _p(draft) if k > 1 else None, _p(n_draft), _p(u), V, B, k, _p(tok), _p(pos),
-                                      _p(step), _p(out_tokens), out_tokens.shape[1], _p(n_accept), _p(workspace),
-                                      workspace.numel(), _stream(stream)))
+    if B == 0:
+        return n_accept
+    workspace = _scratch(workspace, lambda: verify_sample_workspace_bytes(B), target_probs)
+    _check(lib().qd_verify_sample(target_probs.data_ptr(), t_stride, draft_probs.data_ptr() if k > 1 else None,
+                                  d_stride, draft.data_ptr() if k > 1 else None, _p(n_draft), u.data_ptr(), V, B, k,
+                                  tok.data_ptr(), pos.data_ptr(), step.data_ptr(), out_tokens.data_ptr(),
+                                  out_tokens.shape[1], n_accept.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                  _raw_stream(dev)))
     return n_accept
+
+
+def _row_stride(name, t, B, rows, V, dev):
+    """Elements from one row of f32 [B, rows, V] to the next; the rows must be evenly spaced."""
+    if t.dtype is not torch.float32 or t.get_device() != dev or t.shape != (B, rows, V):
+        raise ValueError(f"verify_sample: {name} must be float32 {(B, rows, V)} on the first tensor's device")
+    s0, s1, s2 = t.stride()
+    s = s1 if rows > 1 else (s0 if B > 1 else V)
+    if t.numel() and (s2 != 1 and V > 1 or (B > 1 and s0 != rows * s)):
+        raise ValueError(f"verify_sample: {name}'s rows must be evenly spaced (strides {t.stride()})")
+    return s
 
 
 class PageCache:
@@ -428,8 +464,8 @@ class PageCache:
         self.k_cache, self.v_cache = list(k_cache), list(v_cache)
         first = self.k_cache[0]
         for t in self.k_cache + self.v_cache:
-            _want("PageCache: a cache", t, torch.bfloat16, 4, first.device, first.shape)
-        self.device = first.device
+            _want("PageCache: a cache", t, torch.bfloat16, 4, first.get_device(), first.shape)
+        self.device, self._dev = first.device, first.get_device()
         L = len(self.k_cache)
         a = PageCacheArgs()
         self._k_arr = (_vp * L)(*[_p(t) for t in self.k_cache])
@@ -439,15 +475,16 @@ class PageCache:
         a.n_pages, a.n_kv_heads, a.page_size, a.head_dim = first.shape
         self.page_table, self.seq_lens, self.refs = page_table, seq_lens, refs
         if page_table is not None:
-            _want("PageCache: page_table", page_table, torch.int32, 2, self.device)
-            _want("PageCache: seq_lens", seq_lens, torch.int32, 1, self.device, page_table.shape[:1])
-            _want("PageCache: refs", refs, torch.int32, 1, self.device, first.shape[:1])
+            _want("PageCache: page_table", page_table, torch.int32, 2, self._dev)
+            _want("PageCache: seq_lens", seq_lens, torch.int32, 1, self._dev, page_table.shape[:1])
+            _want("PageCache: refs", refs, torch.int32, 1, self._dev, first.shape[:1])
             a.page_table, a.seq_lens, a.refs = _p(page_table), _p(seq_lens), _p(refs)
             a.max_seqs, a.max_pages = page_table.shape
             self.workspace = torch.zeros(int(lib().qd_pages_workspace_bytes(C.byref(a))), dtype=torch.uint8,
                                          device=self.device)
             a.workspace, a.workspace_bytes = _p(self.workspace), self.workspace.numel()
         self.args = a
+        self._ref = C.byref(a)
 
     @classmethod
     def empty(cls, k_cache, v_cache, max_seqs: int, max_pages: int):
@@ -457,40 +494,44 @@ class PageCache:
                    torch.zeros(k_cache[0].shape[0], dtype=torch.int32, device=dev))
 
     def _list(self, name, t, n=None):
-        _want(f"PageCache.{name}", t, torch.int32, 1, self.device, None if n is None else (n,))
-        return _p(t)
+        _want(name, t, torch.int32, 1, self._dev, None if n is None else (n,))
+        return t.data_ptr()
+
+    def _run(self, stream, fn, *args):
+        away = _elsewhere(self.k_cache[0], stream)
+        if away is None:
+            _check(fn(self._ref, *args, _raw_stream(self._dev)))
+        else:
+            with away:
+                _check(fn(self._ref, *args, _raw_stream(self._dev)))
 
     def copy(self, src, dst, stream=None):
         """Page src[i] to page dst[i] in every layer's K and V (device int32 lists)."""
-        s, d = self._list("copy: src", src), self._list("copy: dst", dst, src.numel())
-        with _on(self.k_cache[0], stream):
-            _check(lib().qd_pages_copy(C.byref(self.args), s, d, src.numel(), _stream(stream)))
+        n = src.numel()
+        self._run(stream, lib().qd_pages_copy, self._list("src", src), self._list("dst", dst, n), n)
 
     def fork(self, parents, children, stream=None):
         """Sequence children[i] (empty) becomes a copy of parents[i], its pages shared."""
-        a, b = self._list("fork: parents", parents), self._list("fork: children", children, parents.numel())
-        with _on(self.k_cache[0], stream):
-            _check(lib().qd_pages_fork(C.byref(self.args), a, b, parents.numel(), _stream(stream)))
+        n = parents.numel()
+        self._run(stream, lib().qd_pages_fork, self._list("parents", parents), self._list("children", children, n), n)
 
     def extend(self, n_new, stream=None):
         """Pages for n_new[s] more tokens of each sequence; shared partial pages are copied."""
-        n = self._list("extend: n_new", n_new, self.args.max_seqs)
-        with _on(self.k_cache[0], stream):
-            _check(lib().qd_pages_extend(C.byref(self.args), n, _stream(stream)))
+        self._run(stream, lib().qd_pages_extend, self._list("n_new", n_new, self.args.max_seqs))
 
     def trim(self, new_lens, stream=None):
         """Sequence s cut to new_lens[s] tokens (negative: unchanged; 0 frees it)."""
-        n = self._list("trim: new_lens", new_lens, self.args.max_seqs)
-        with _on(self.k_cache[0], stream):
-            _check(lib().qd_pages_trim(C.byref(self.args), n, _stream(stream)))
+        self._run(stream, lib().qd_pages_trim, self._list("new_lens", new_lens, self.args.max_seqs))
 
     def compact(self, n_live=None, stream=None):
         """The pages in use moved to the lowest ids; returns their number (device int32 [1])."""
-        with _on(self.k_cache[0], stream):
-            if n_live is None:
-                n_live = torch.empty(1, dtype=torch.int32, device=self.device)
-            p = self._list("compact: n_live", n_live, 1)
-            _check(lib().qd_pages_compact(C.byref(self.args), p, _stream(stream)))
+        if n_live is None:
+            away = _elsewhere(self.k_cache[0], stream)
+            if away is not None:
+                with away:
+                    return self.compact()
+            n_live = torch.empty(1, dtype=torch.int32, device=self.device)
+        self._run(stream, lib().qd_pages_compact, self._list("n_live", n_live, 1))
         return n_live
 
 

@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kRing = 7 - kQ;
   constexpr int kCols = 64;                   // keys of a tile, and O columns, per softmax thread
   constexpr bool kFresh = PARTS == 3;         // O of each tile alone in TMEM, summed in registers
-  constexpr int kRingK = kRing - 2, kRingV = 2;   // K slots, then V slots
+  constexpr int kRingV = kRing > 4 ? 3 : 2, kRingK = kRing - kRingV;   // K slots, then V slots
   static_assert(kRingK >= 2 && kRing <= kMaxSlots, "");
   extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char* data = smem + kMisc;
@@ -1181,10 +1181,9 @@ int grid_ctas() { return std::min(dev_info().sm_count, kMaxGrid); }
 
 template <typename T, int PARTS>
 cudaError_t launch(const Params& p, const CUtensorMap& tk, const CUtensorMap& tv, const Launch& L) {
-  auto k = attn_rows_kernel<T, PARTS>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  cudaError_t e = allow_smem<attn_rows_kernel<T, PARTS>>(kSmem);
   if (e != cudaSuccess) return e;
-  return launch_ex(k, dim3(grid_ctas()), dim3(kThreads), kSmem, L, tk, tv, p);
+  return launch_ex(attn_rows_kernel<T, PARTS>, dim3(grid_ctas()), dim3(kThreads), kSmem, L, tk, tv, p);
 }
 
 // Workspace: tickets, then the partials; the shared form's prefix results behind them.

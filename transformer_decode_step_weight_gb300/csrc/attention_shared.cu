@@ -471,11 +471,10 @@ size_t from_bytes(int B, int Hkv) { return round256((size_t)B * Hkv * sizeof(Att
 
 template <typename T, int PARTS>
 cudaError_t launch(const SParams& p, int n_splits, const Launch& L) {
-  auto k = attn_suffix_kernel<T, PARTS>;
   const size_t smem = (size_t)kW * kStages * kStage;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_smem<attn_suffix_kernel<T, PARTS>>(smem);
   if (e != cudaSuccess) return e;
-  return launch_ex(k, dim3(n_splits, p.Hkv, p.B), dim3(kTh), smem, L, p);
+  return launch_ex(attn_suffix_kernel<T, PARTS>, dim3(n_splits, p.Hkv, p.B), dim3(kTh), smem, L, p);
 }
 
 }  // namespace

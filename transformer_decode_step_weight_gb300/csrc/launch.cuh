@@ -3,6 +3,8 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <atomic>
+#include <stdint.h>
 #include "kernels.h"
 
 namespace qd {
@@ -49,6 +51,19 @@ inline cudaError_t launch_ex_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 b
   cfg.attrs = attr;
   cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// A kernel's dynamic shared memory limit raised on the current device, once per device.
+template <auto Kernel>
+inline cudaError_t allow_smem(size_t bytes) {
+  static std::atomic<uint64_t> done{0};   // bit d: device d
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1)) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return e;
 }
 
 inline int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
