@@ -62,6 +62,7 @@ constexpr size_t kSmem = kMisc + kData;  // 227 KB, the whole opt-in shared memo
 constexpr int kMaxSlots = 6;
 constexpr int kMinUnits = 2;             // units per CTA below which fewer CTAs are used
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kMaxTeam = 8;              // row tiles of a group up to which its CTAs form teams
 constexpr float kMove = 8.0f;            // log2 units a score may pass the reference maximum
 constexpr int kMaxGrid = 192;            // CTAs (SMs) the workspace has room for
 constexpr size_t kPartFloats = kPieceFloats;
@@ -179,6 +180,7 @@ struct Seg {
   int off;         // prompt form: row j sees off + j + 1 keys
   int len;         // keys
   int tiles;       // row tiles per kv head; 0: no work
+  int steps;       // row tiles that one CTA's run walks through (Work::team)
   bool bad;
 };
 
@@ -192,24 +194,31 @@ struct Split {
   }
 };
 
+template <bool PROMPT>
 struct Work {
   int log_tpt;   // 2^log_tpt packed rows (tokens or sequences) per row tile
-  bool prompt;
+  // Shared form: a team of CTAs takes the same run of keys, each member another row tile of
+  // every head, so that a K/V tile comes from HBM once for all row tiles at the same moment (as
+  // separate runs the row tiles of 64 sequences read a 134 MB prefix twice: 258 MB from DRAM,
+  // 68 us instead of MEASURED_TEAM). A segment with fewer row tiles leaves members idle.
+  int team, member;   // (prompt form: 1, 0)
 
   QD_DEV int tpt() const { return 1 << log_tpt; }
+  QD_DEV int step_tile(int t) const { return !PROMPT && team > 1 ? member : t; }
   QD_DEV Seg seg(const Params& p, int s) const {
     Seg a;
     a.row0 = p.cu[s];
     a.n = p.cu[s + 1] - a.row0;
-    a.len = prompt ? p.seq_lens[s] : p.shared_lens[s];
+    a.len = PROMPT ? p.seq_lens[s] : p.shared_lens[s];
     a.bad = a.n > 0 && (a.len < 0 || a.len > p.cap);
     a.off = a.len - a.n;
-    a.tiles = a.bad || a.n <= 0 || (!prompt && a.len == 0) ? 0 : (a.n + tpt() - 1) >> log_tpt;
+    a.tiles = a.bad || a.n <= 0 || (!PROMPT && a.len == 0) ? 0 : (a.n + tpt() - 1) >> log_tpt;
+    a.steps = !PROMPT && team > 1 ? min(a.tiles, 1) : a.tiles;
     return a;
   }
   // keys that the last row of row tile t sees (prompt form), at least 0
   QD_DEV int seen(const Seg& a, int t) const {
-    return prompt ? max(0, a.off + min((t + 1) << log_tpt, a.n)) : a.len;
+    return PROMPT ? max(0, a.off + min((t + 1) << log_tpt, a.n)) : a.len;
   }
   QD_DEV int units(const Seg& a, int t) const { return max(1, (seen(a, t) + kKeys - 1) >> 7); }
   // sum over j < n of floor(j / 2^k)
@@ -219,9 +228,9 @@ struct Work {
   }
   // units of the row tiles before t (t <= tiles)
   QD_DEV long long before(const Seg& a, int t) const {
-    if (!prompt) return (long long)t * units(a, 0);
+    if (!PROMPT) return (long long)t * units(a, 0);
     const int full = min(t, a.tiles - 1);
-    long long sum = t == a.tiles && t > 0 ? units(a, t - 1) : 0;
+    long long sum = t == a.tiles && t > 0 ? units(a, t - 1) : 0;   // (prompt form: steps are tiles)
     if (full <= 0) return sum;
     // tile i < full ends at off + (i + 1) tpt keys: one unit up to 128, else the quotient
     const int one = a.off > kKeys ? 0 : min(full, (kKeys - a.off) >> log_tpt);
@@ -300,7 +309,7 @@ __device__ __noinline__ void patch_row(const Params& p, const int32_t* pt, int g
   }
 }
 
-template <typename T, int PARTS>
+template <typename T, int PARTS, bool PROMPT>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ Params p) {
@@ -331,13 +340,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* s_last = s_patch + 2;
   long long* s_find = (long long*)(smem + 256);   // [0] segment, [1] unit within it, [2] the split
   long long* s_scan = (long long*)(smem + 320);   // [warps] sums of the scan
+  int* s_most = (int*)(smem + 448);               // [warps] most row tiles of a segment
   float* xm = (float*)(smem + 512);               // [2][2][128] traded maxima and sums
 
   // the warp's number from one lane: the roles' branches are then known to be taken by whole
   // warps, and the issuers' descriptors can stay in uniform registers
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  Work W;
-  W.prompt = p.shared_lens == nullptr;
+  Work<PROMPT> W;
   W.log_tpt = 7 - p.log_rep;
   pdl_launch_dependents();
   if (smem_u32(smem) & 1023u) {   // the swizzled tiles rest on it (there is no static shared memory)
@@ -346,9 +355,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   // ---- this CTA's units
+  W.team = 1;
+  W.member = 0;
+  uint32_t run_no;   // which run of units: one for each team
   {
     const int per = (p.n_seg + kThreads - 1) / kThreads;
     long long own = 0;
+    int most = 0;
     bool bad = false;
     for (int i = 0; i < per; ++i) {
       const int s = tid * per + i;
@@ -356,13 +369,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Seg a = W.seg(p, s);
       bad = bad || a.n < 0 || a.row0 < 0 || a.row0 + a.n > p.n_rows;
       if (a.bad && blockIdx.x == 0) set_error(p.err, QD_DEVERR_POS);
-      if (!bad && a.tiles) own += W.before(a, a.tiles) * p.Hkv;
+      most = max(most, a.tiles);
     }
     if (tid == 0) *s_abort = 0;
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) s_most[warp] = most;
     const int any_bad = __syncthreads_or(bad);
     if (any_bad) {
       if (blockIdx.x == 0 && tid == 0) set_error(p.err, QD_DEVERR_POS);
       return;
+    }
+    if (!PROMPT) {
+      for (int w = 0; w < kThreads / 32; ++w) most = max(most, s_most[w]);
+      if (most > 1 && most <= kMaxTeam) W.team = most;
+      W.member = blockIdx.x % W.team;
+    }
+    for (int i = 0; i < per; ++i) {
+      const int s = tid * per + i;
+      if (s >= p.n_seg) break;
+      const Seg a = W.seg(p, s);
+      if (a.steps) own += W.before(a, a.steps) * p.Hkv;
     }
     long long v = own;
 #pragma unroll
@@ -381,17 +407,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (blockIdx.x == 0 && tid == 0) set_error(p.err, QD_DEVERR_POS);
       return;
     }
-    const uint32_t G = min(gridDim.x, ((uint32_t)total + kMinUnits - 1) / kMinUnits);
-    if (blockIdx.x >= G) return;
+    const uint32_t G = min(gridDim.x / W.team, ((uint32_t)total + kMinUnits - 1) / kMinUnits);
+    run_no = blockIdx.x / W.team;
+    if (run_no >= G) return;
     const Split sp = {(uint32_t)total / G, (uint32_t)total % G};
-    const uint32_t u0 = sp.first(blockIdx.x);
+    const uint32_t u0 = sp.first(run_no);
     long long at = base + v - own;
     if (tid == 0) s_find[2] = (long long)sp.per << 32 | sp.rem;
     if (own > 0 && at <= u0 && u0 < at + own) {
       for (int i = 0; i < per; ++i) {
         const int s = tid * per + i;
         const Seg a = W.seg(p, s);
-        const long long n = a.tiles ? W.before(a, a.tiles) * p.Hkv : 0;
+        const long long n = a.steps ? W.before(a, a.steps) * p.Hkv : 0;
         if (u0 < at + n) {
           s_find[0] = s;
           s_find[1] = u0 - at;
@@ -425,8 +452,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tb = *tslot;
   const uint32_t tS = tb, tO = tb + 256, tX = tb + 384;
   const Split sp = {(uint32_t)(s_find[2] >> 32), (uint32_t)s_find[2]};
-  const uint32_t u1 = sp.first(blockIdx.x + 1);
-  uint32_t u = sp.first(blockIdx.x);
+  const uint32_t u1 = sp.first(run_no + 1);
+  uint32_t u = sp.first(run_no);
 
   // a wait of a whole warp, bounded by its polls (some 40 cycles each at least: about half a
   // second); after a timeout anywhere in the CTA it returns soon
@@ -444,29 +471,38 @@ __global__ void __launch_bounds__(kThreads, 1)
   {
     at.s = (int)s_find[0];
     at.a = W.seg(p, at.s);
-    const uint32_t head_units = (uint32_t)W.before(at.a, at.a.tiles), v = (uint32_t)s_find[1];
+    const uint32_t head_units = (uint32_t)W.before(at.a, at.a.steps), v = (uint32_t)s_find[1];
     at.g = (int)(v / head_units);
     const uint32_t w = v % head_units;
     int lo = 0;
-    for (int hi = at.a.tiles; hi - lo > 1;) {   // the last row tile whose units start at or before w
+    for (int hi = at.a.steps; hi - lo > 1;) {   // the last row tile whose units start at or before w
       const int mid = (lo + hi) / 2;
       if (W.before(at.a, mid) <= w) lo = mid; else hi = mid;
     }
     at.t = lo;
     at.k0 = (int)(w - W.before(at.a, lo));
   }
-  // the next row tile (the place after the last unit is not asked for)
+  // the row tile after x's (there is one)
   auto advance = [&](Place& x) {
     x.k0 = 0;
-    if (++x.t < x.a.tiles) return;
+    if (++x.t < x.a.steps) return;
     x.t = 0;
     if (++x.g < p.Hkv) return;
     x.g = 0;
     do {
       x.a = W.seg(p, ++x.s);
-    } while (x.a.tiles == 0);
+    } while (x.a.steps == 0);
   };
-
+  // the place of unit x_u on, where this CTA has work: false if its run ends before
+  auto settle = [&](Place& x, uint32_t& x_u) {
+    for (;;) {
+      if (x_u >= u1) return false;
+      if (PROMPT || W.team == 1 || W.member < x.a.tiles) return true;
+      x_u += min((uint32_t)(W.units(x.a, 0) - x.k0), u1 - x_u);   // another member's alone
+      if (x_u >= u1) return false;
+      advance(x);
+    }
+  };
   // A piece is the part of one row tile that this CTA computes. Each role walks the pieces for
   // itself, so the copies and products of one run into the next; counts that several roles
   // follow: tiles, fixed tiles, trades, pieces.
@@ -487,7 +523,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   struct Piece {
     int g, t, k0, k1, nk, n;
-    bool more;                 // another piece follows
     int first_row, packed;     // packed rows of the tile: the first, how many
     int seen_max, seen_min;    // keys past the first are nobody's, keys before the second everybody's
     const int32_t* pt;
@@ -496,17 +531,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Seg& a = x.a;
     Piece q;
     q.g = x.g;
-    q.t = x.t;
+    q.t = W.step_tile(x.t);
     q.k0 = x.k0;
-    q.nk = W.units(a, x.t);
+    q.nk = W.units(a, W.step_tile(x.t));
     q.k1 = (int)min((uint32_t)q.nk, x.k0 + (u1 - u));
     q.n = q.k1 - x.k0;
-    q.more = u + q.n < u1;
-    q.first_row = a.row0 + (x.t << W.log_tpt);
-    q.packed = min(W.tpt(), a.n - (x.t << W.log_tpt));
-    q.seen_max = W.seen(a, x.t);
-    if (W.prompt) {
-      q.seen_min = max(0, a.off + (x.t << W.log_tpt) + 1);
+    const int row = q.t << W.log_tpt;
+    q.first_row = a.row0 + row;
+    q.packed = min(W.tpt(), a.n - row);
+    q.seen_max = W.seen(a, q.t);
+    if (PROMPT) {
+      q.seen_min = max(0, a.off + row + 1);
     } else {
       int m = a.len;
       for (int i = lane; i < q.packed; i += 32) {
@@ -515,11 +550,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       q.seen_min = __reduce_min_sync(0xffffffffu, m);
     }
-    q.pt = p.page_table + (size_t)(W.prompt ? x.s : a.row0) * p.max_pages;
+    q.pt = p.page_table + (size_t)(PROMPT ? x.s : a.row0) * p.max_pages;
     return q;
   };
+  // the place after a piece of n units at x; false: none
+  auto next_place = [&](Place& x, uint32_t& x_u, int n) {
+    x_u += n;
+    if (x_u >= u1) return false;
+    advance(x);
+    return settle(x, x_u);
+  };
+  const bool idle = !settle(at, u);
 
-  if (warp >= kSoftWarps) {
+  if (idle) {
+    // (a member of a team whose run has no row tile for it)
+  } else if (warp >= kSoftWarps) {
     // the softmax warps take the registers that the others leave (256 x 200 + 128 x 104 of the
     // 384 x 168 of the launch)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
@@ -717,9 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tile += n;
     ++piece_no;
-    u += n;
-    if (!pc.more) break;
-    advance(at);
+    if (!next_place(at, u, n)) break;
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
@@ -727,7 +770,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Piece pc = piece_at(at);
     const Seg& a = at.a;
     const int g = pc.g, t = pc.t, k0 = pc.k0, k1 = pc.k1, nk = pc.nk, n = pc.n;
-    const bool more = pc.more;
     const int first_row = pc.first_row, packed = pc.packed;
     const int32_t* pt = pc.pt;
       // ---- softmax: warps w and w + 4 hold the same rows (TMEM lanes), 64 keys and 64 O columns
@@ -742,9 +784,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Q of the row tile at x; the copies are waited for in q_ready
       auto q_load = [&](const Place& x) {
         unsigned char* dst = data;
-        const T* q = (const T*)p.q + (long long)(x.a.row0 + (x.t << W.log_tpt)) * p.q_stride +
+        const T* q = (const T*)p.q + (long long)(x.a.row0 + (W.step_tile(x.t) << W.log_tpt)) * p.q_stride +
                      (long long)(x.g << p.log_rep) * kD;
-        const int qrows = min(W.tpt(), x.a.n - (x.t << W.log_tpt)) << p.log_rep;
+        const int qrows = min(W.tpt(), x.a.n - (W.step_tile(x.t) << W.log_tpt)) << p.log_rep;
         if constexpr (PARTS == 1) {
           // warp w copies rows 16 w .. as they are, two rows at a time
           constexpr int kPer = 16;
@@ -804,17 +846,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(q_full);
       };
       Place nx = at;
+      uint32_t nx_u = u;
       if (first) {
         q_load(at);
         q_ready();
         first = false;
       }
-      if (more) advance(nx);
+      const bool more = next_place(nx, nx_u, n);
 
       int lim = 0;   // keys this row sees
       if (valid) {
         const int j = (t << W.log_tpt) + (row >> p.log_rep);
-        if (W.prompt) {
+        if (PROMPT) {
           lim = max(0, a.off + j + 1);
         } else {
           const int l = p.seq_lens[a.row0 + j];
@@ -995,11 +1038,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const size_t tile0 = (size_t)first_row * p.Hq + (g << p.log_rep);
       auto out_row = [&](int r) { return (r >> p.log_rep) * p.Hq + (r & (p.rep - 1)); };
       const int col0 = 64 * hf;
-      const bool final_out = whole && W.prompt;      // else O as it is, with m and l
+      const bool final_out = whole && PROMPT;      // else O as it is, with m and l
       const float inv = l == 0.f ? 0.f : 1.0f / l;   // a row that saw nothing gives 0
       // bf16 results and the f32 form's values go out by whole rows, through shared memory:
       // 16-byte pieces, swizzled; the bf16 form's partial values as they are
-      float* dst = !whole ? part : (W.prompt ? (float*)p.out : p.pre_o) + tile0 * kD;
+      float* dst = !whole ? part : (PROMPT ? (float*)p.out : p.pre_o) + tile0 * kD;
       const bool staged = PARTS == 3 || final_out;
       unsigned char* mine = stage + row * (PARTS == 3 ? 512 : 256);
       const int xr = staged ? row & (PARTS == 3 ? 31 : 15) : 0;
@@ -1052,14 +1095,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (!W.prompt && k0 == 0 && tid < packed) {   // the kernel that reads the rest joins the pieces
+      if (!PROMPT && k0 == 0 && tid < packed) {   // the kernel that reads the rest joins the pieces
         AttnFrom* f = p.from + (size_t)(first_row + tid) * p.Hkv + g;
         f->first = blockIdx.x;
-        f->pieces = whole ? 0 : sp.owner(u + nk - 1) - (int)blockIdx.x + 1;
+        f->pieces = whole ? 0 : sp.owner(u + nk - 1) - (int)run_no + 1;
+        f->stride = W.team;
         f->row = tid << p.log_rep;
       }
       // ---- a prompt's row tile of several CTAs: the last of them joins the pieces in key order
-      if (W.prompt && !whole) {   // the same in all softmax threads
+      if (PROMPT && !whole) {   // the same in all softmax threads
         // where the tile's units lie: the CTAs of its first and last
         const int c0 = k0 == 0 ? (int)blockIdx.x : sp.owner(u - k0);
         const int c1 = k1 == nk ? (int)blockIdx.x : sp.owner(u - k0 + nk - 1);
@@ -1151,9 +1195,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     tile += n;
     ++piece_no;
-    u += n;
     if (!more) break;
     at = nx;
+    u = nx_u;
     }
   }
   __syncwarp();
@@ -1179,16 +1223,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 int grid_ctas() { return std::min(dev_info().sm_count, kMaxGrid); }
 
-template <typename T, int PARTS>
+template <typename T, int PARTS, bool PROMPT>
 cudaError_t launch(const Params& p, const CUtensorMap& tk, const CUtensorMap& tv, const Launch& L) {
-  cudaError_t e = allow_smem<attn_rows_kernel<T, PARTS>>(kSmem);
+  cudaError_t e = allow_smem<attn_rows_kernel<T, PARTS, PROMPT>>(kSmem);
   if (e != cudaSuccess) return e;
-  return launch_ex(attn_rows_kernel<T, PARTS>, dim3(grid_ctas()), dim3(kThreads), kSmem, L, tk, tv, p);
+  return launch_ex(attn_rows_kernel<T, PARTS, PROMPT>, dim3(grid_ctas()), dim3(kThreads), kSmem, L, tk, tv, p);
 }
 
 // Workspace: tickets, then the partials; the shared form's prefix results behind them.
 constexpr size_t kTicketBytes = 1024;
 
+template <bool PROMPT>
 cudaError_t run(const AttnRowsArgs& a, float* pre_o, AttnFrom* from, const Launch& L) {
   Params p = {};
   p.q = a.q; p.q_stride = a.q_stride;
@@ -1222,19 +1267,19 @@ cudaError_t run(const AttnRowsArgs& a, float* pre_o, AttnFrom* from, const Launc
     if (e == cudaSuccess) e = encode_tmap_bf16_2d(&tv, a.v_pages, rows, kD, p.box);
     if (e != cudaSuccess) return e;
   }
-  return a.q_f32 ? launch<float, 3>(p, tk, tv, L) : launch<__nv_bfloat16, 1>(p, tk, tv, L);
+  return a.q_f32 ? launch<float, 3, PROMPT>(p, tk, tv, L) : launch<__nv_bfloat16, 1, PROMPT>(p, tk, tv, L);
 }
 
 }  // namespace
 
 size_t attn_rows_workspace_bytes() { return kTicketBytes + (size_t)grid_ctas() * 2 * kPartFloats * 4; }
 
-cudaError_t launch_attn_prompt(const AttnRowsArgs& a, const Launch& L) { return run(a, nullptr, nullptr, L); }
+cudaError_t launch_attn_prompt(const AttnRowsArgs& a, const Launch& L) { return run<true>(a, nullptr, nullptr, L); }
 
 cudaError_t launch_attn_prefix(const AttnRowsArgs& a, float* pre, AttnFrom* from, AttnPieces* pieces,
                                const Launch& L) {
   *pieces = {(const float*)((const unsigned char*)a.workspace + kTicketBytes), grid_ctas()};
-  return run(a, pre, from, L);
+  return run<false>(a, pre, from, L);
 }
 
 }  // namespace qd

@@ -385,15 +385,14 @@ __global__ void __launch_bounds__(kTh, 3) attn_suffix_kernel(const __grid_consta
   pdl_wait();   // the prefix's results are there
 
   // ---- joined: the splits (unless this CTA has it all already), then the prefix's pieces
-  AttnFrom from = {0, 0, 0};
+  AttnFrom from = {0, 0, 1, 0};
   if (t0 > 0) {
-    from.first = __ldcg(&p.from[pair].first);
-    from.pieces = __ldcg(&p.from[pair].pieces);
-    from.row = __ldcg(&p.from[pair].row);
+    const int4 f = __ldcg((const int4*)(p.from + pair));
     // (nothing was written where the first kernel gave up; it has said so)
-    from.first = max(0, min(from.first, p.pieces.n - 1));
-    from.pieces = max(0, min(from.pieces, p.pieces.n - from.first));
-    from.row = max(0, min(from.row, kPieceRows - p.rep));
+    from.first = max(0, min(f.x, p.pieces.n - 1));
+    from.stride = max(1, min(f.z, p.pieces.n));
+    from.pieces = max(0, min(f.y, (p.pieces.n - 1 - from.first) / from.stride + 1));
+    from.row = max(0, min(f.w, kPieceRows - p.rep));
   }
   const int n_own = n_act > 1 ? n_act : 0, n_pre = t0 > 0 ? max(from.pieces, 1) : 0;
   // partial k: its O rows (128 floats per head) and statistics
@@ -408,7 +407,7 @@ __global__ void __launch_bounds__(kTh, 3) attn_suffix_kernel(const __grid_consta
       l = p.pre_l + head0;
     } else {
       const int i = k - n_own;
-      const float* piece = p.pieces.base + ((size_t)(from.first + i) * 2 + (i == 0 ? 1 : 0)) * kPieceFloats;
+      const float* piece = p.pieces.base + ((size_t)(from.first + i * from.stride) * 2 + (i == 0 ? 1 : 0)) * kPieceFloats;
       O = piece + (size_t)from.row * kD;
       m = piece + (size_t)kPieceRows * kD + from.row;
       l = m + kPieceRows;

@@ -322,9 +322,10 @@ cudaError_t launch_attn_prompt(const AttnRowsArgs& a, const Launch& L);
 // The groups' shared tokens alone, of every row whose group shares any, with one entry of
 // `from` per (row, kv head). pieces 0: O [Hq, D], m, l [Hq] of the row in pre (O [n_rows, Hq,
 // D], m, l [n_rows, Hq]; f32, reference maximum in log2 units). Otherwise they are still in
-// that many pieces (AttnPieces): piece k's rows from `row` on, one per q head.
+// that many pieces (AttnPieces): piece k, of CTA first + k stride, its rows from `row` on, one
+// per q head.
 struct AttnFrom {
-  int first, pieces, row;
+  int first, pieces, stride, row;
 };
 struct AttnPieces {
   const float* base;       // [n][2][kPieceFloats]: O [kPieceRows][D], m, l [kPieceRows]
