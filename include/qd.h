@@ -243,7 +243,9 @@ int qd_attn_prompt(const void* q, int q_is_f32, int64_t q_stride, const void* k_
 
 /* Decode attention of sequences that share prefixes: the result of                 */
 /* qd_attn_decode_paged for sequences whose page tables name the same pages at their  */
-/* start (qd_pages_fork), each shared page read once for all of them. Group i holds    */
+/* start (qd_pages_fork), each shared page read once for all of them (where that spares */
+/* less than QD_SHARED_MIN_MB, default 80, megabytes of re-reading, each sequence reads    */
+/* its own table's pages: a second kernel costs more). Group i holds    */
 /* the sequences cu_seqs[i] .. cu_seqs[i + 1); their first shared_lens[i] tokens lie in  */
 /* the pages of the group's first sequence's row (a sequence shorter than that sees its   */
 /* own seq_lens tokens of them). Sequences outside every group are left as they were.      */

@@ -233,12 +233,19 @@ SHARED = [
     ([(5, 2000), (1, 50), (7, 129)], [300, 2, 0, 90, 31, 8, 1, 2, 3, 4, 5, 6, 7], 8, 8, 64),
     ([(6, 777)], [1, 2, 3, 4, 5, 6], 4, 2, 7),
     ([(2, 3000)], [1500, 3], 2, 2, 24),
+    ([(100, 1500), (3, 700), (20, 300)], [i % 5 for i in range(123)], 8, 1, 16),   # teams of 7 CTAs
+    ([(80, 400)], [2] * 80, 8, 2, 64),
+    ([(150, 300)], [i % 2 for i in range(150)], 8, 1, 16),   # more row tiles than a team has members
 ]
 
 
+# QD_SHARED_MIN_MB 0: the prefixes are shared whatever that spares; default: at these sizes they are not
+@pytest.mark.parametrize("min_mb", ["0", None])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("groups,tails,hq,hkv,ps", SHARED)
-def test_shared_prefix_attention(cuda_lib, groups, tails, hq, hkv, ps, dtype):
+def test_shared_prefix_attention(cuda_lib, monkeypatch, groups, tails, hq, hkv, ps, dtype, min_mb):
+    if min_mb is not None:
+        monkeypatch.setenv("QD_SHARED_MIN_MB", min_mb)
     g = _gen(len(tails) + hq)
     who = [i for i, (n, _) in enumerate(groups) for _ in range(n)]
     lens = [groups[i][1] + t for i, t in zip(who, tails)]
@@ -263,8 +270,10 @@ def test_shared_prefix_attention(cuda_lib, groups, tails, hq, hkv, ps, dtype):
     assert api.check_device_error() == 0
 
 
+@pytest.mark.parametrize("min_mb", ["0", "80"])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-def test_shared_prefix_attention_short_empty_and_outside_sequences(cuda_lib, dtype):
+def test_shared_prefix_attention_short_empty_and_outside_sequences(cuda_lib, monkeypatch, dtype, min_mb):
+    monkeypatch.setenv("QD_SHARED_MIN_MB", min_mb)
     g = _gen(21)
     ps, hq, hkv, shared = 16, 8, 2, 200
     lens = [250, 0, 100, 200, 201, 5, 33]
@@ -280,7 +289,9 @@ def test_shared_prefix_attention_short_empty_and_outside_sequences(cuda_lib, dty
     assert api.check_device_error() == 0
 
 
-def test_shared_prefix_attention_device_errors(cuda_lib):
+@pytest.mark.parametrize("min_mb", ["0", "80"])
+def test_shared_prefix_attention_device_errors(cuda_lib, monkeypatch, min_mb):
+    monkeypatch.setenv("QD_SHARED_MIN_MB", min_mb)
     g = _gen(22)
     kp, vp, pt = _cache(g, [64] * 4, 2, 16, [(0, 2)] * 4)
     q = torch.randn((4, 4, D), generator=g, device=DEV)
@@ -294,7 +305,8 @@ def test_shared_prefix_attention_device_errors(cuda_lib):
 
 
 @pytest.mark.parametrize("op", ["prompt", "shared"])
-def test_attention_in_a_graph_and_on_another_stream(cuda_lib, op):
+def test_attention_in_a_graph_and_on_another_stream(cuda_lib, monkeypatch, op):
+    monkeypatch.setenv("QD_SHARED_MIN_MB", "0")
     g = _gen(23)
     hq, hkv, ps = 8, 2, 16
     lens = [500, 300, 420]
@@ -334,7 +346,9 @@ def test_attention_in_a_graph_and_on_another_stream(cuda_lib, op):
     assert api.check_device_error() == 0
 
 
-def test_one_workspace_for_calls_of_different_sizes(cuda_lib):
+@pytest.mark.parametrize("min_mb", ["0", "80"])
+def test_one_workspace_for_calls_of_different_sizes(cuda_lib, monkeypatch, min_mb):
+    monkeypatch.setenv("QD_SHARED_MIN_MB", min_mb)
     # split sequences (tickets) of one batch size after another, in one workspace
     g = _gen(24)
     hq, hkv, ps = 8, 2, 16
@@ -617,9 +631,11 @@ def test_verify_sample_in_a_graph(cuda_lib):
 # ------------------------------------------------------------------------------------------- all of them, as used
 
 
-def test_a_serving_round(cuda_lib):
+@pytest.mark.parametrize("min_mb", ["0", "80"])
+def test_a_serving_round(cuda_lib, monkeypatch, min_mb):
     """Two prompts in one call, each forked to samples, decode over the shared prefixes, drafts verified,
     rejected tokens given back, the cache compacted; attention before and after compaction is the same."""
+    monkeypatch.setenv("QD_SHARED_MIN_MB", min_mb)
     g = _gen(40)
     hq, hkv, ps, V = 8, 2, 16, 600
     n_pages, max_seqs, max_pages = 200, 12, 20

@@ -60,7 +60,7 @@ constexpr int kMisc = 3072;              // barriers and small arrays in front o
 constexpr int kData = 7 * kSlot;         // 224 KB: Q parts and ring slots
 constexpr size_t kSmem = kMisc + kData;  // 227 KB, the whole opt-in shared memory
 constexpr int kMaxSlots = 6;
-constexpr int kMinUnits = 2;             // units per CTA below which fewer CTAs are used
+constexpr int kMinUnits = 2;             // units per CTA of a prompt below which fewer CTAs are used
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxTeam = 8;              // row tiles of a group up to which its CTAs form teams
 constexpr float kMove = 8.0f;            // log2 units a score may pass the reference maximum
@@ -77,6 +77,7 @@ struct Params {
   int box;                 // rows per TMA box; 0: cp.async loads
   float scale_log2, q_sign;
   void* out;
+  long long share_min;
   float* part;             // [grid][2][kPartFloats]: O [rows][128], m [rows], l [rows]
   int* tickets;            // [grid], zero between calls
   float *pre_o, *pre_m, *pre_l;   // shared form: O, m, l of each (sequence, q head)
@@ -341,6 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   long long* s_find = (long long*)(smem + 256);   // [0] segment, [1] unit within it, [2] the split
   long long* s_scan = (long long*)(smem + 320);   // [warps] sums of the scan
   int* s_most = (int*)(smem + 448);               // [warps] most row tiles of a segment
+  long long* s_saved = (long long*)(smem + 512);  // [warps]
   float* xm = (float*)(smem + 512);               // [2][2][128] traded maxima and sums
 
   // the warp's number from one lane: the roles' branches are then known to be taken by whole
@@ -362,6 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int per = (p.n_seg + kThreads - 1) / kThreads;
     long long own = 0;
     int most = 0;
+    long long saved = 0;   // tokens that sharing spares
     bool bad = false;
     for (int i = 0; i < per; ++i) {
       const int s = tid * per + i;
@@ -370,17 +373,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       bad = bad || a.n < 0 || a.row0 < 0 || a.row0 + a.n > p.n_rows;
       if (a.bad && blockIdx.x == 0) set_error(p.err, QD_DEVERR_POS);
       most = max(most, a.tiles);
+      if (a.tiles) saved += (long long)a.len * (a.n - 1);
     }
     if (tid == 0) *s_abort = 0;
     most = __reduce_max_sync(0xffffffffu, most);
-    if (lane == 0) s_most[warp] = most;
+    if constexpr (!PROMPT) {
+#pragma unroll
+      for (int o = 16; o; o >>= 1) saved += __shfl_xor_sync(0xffffffffu, saved, o);
+    }
+    if (lane == 0) {
+      s_most[warp] = most;
+      s_saved[warp] = saved;
+    }
     const int any_bad = __syncthreads_or(bad);
     if (any_bad) {
       if (blockIdx.x == 0 && tid == 0) set_error(p.err, QD_DEVERR_POS);
       return;
     }
     if (!PROMPT) {
-      for (int w = 0; w < kThreads / 32; ++w) most = max(most, s_most[w]);
+      saved = 0;
+      for (int w = 0; w < kThreads / 32; ++w) {
+        most = max(most, s_most[w]);
+        saved += s_saved[w];
+      }
+      if (saved < p.share_min) return;   // the sequences read their prefixes for themselves
       if (most > 1 && most <= kMaxTeam) W.team = most;
       W.member = blockIdx.x % W.team;
     }
@@ -407,7 +423,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (blockIdx.x == 0 && tid == 0) set_error(p.err, QD_DEVERR_POS);
       return;
     }
-    const uint32_t G = min(gridDim.x / W.team, ((uint32_t)total + kMinUnits - 1) / kMinUnits);
+    constexpr uint32_t kMin = PROMPT ? kMinUnits : 1;
+    const uint32_t G = min(gridDim.x / W.team, ((uint32_t)total + kMin - 1) / kMin);
     run_no = blockIdx.x / W.team;
     if (run_no >= G) return;
     const Split sp = {(uint32_t)total / G, (uint32_t)total % G};
@@ -1252,6 +1269,7 @@ cudaError_t run(const AttnRowsArgs& a, float* pre_o, AttnFrom* from, const Launc
   p.pre_o = pre_o;
   p.from = from;
   p.div = make_page_div(a.page_size);
+  p.share_min = a.share_min;
   p.pre_m = pre_o ? pre_o + (size_t)a.n_rows * a.Hq * kD : nullptr;
   p.pre_l = pre_o ? p.pre_m + (size_t)a.n_rows * a.Hq : nullptr;
   p.err = L.err;

@@ -19,6 +19,7 @@
 #include "launch.cuh"
 
 #include <algorithm>
+#include <cstdlib>
 
 namespace qd {
 namespace {
@@ -51,6 +52,7 @@ struct SParams {
   const AttnFrom* from;
   AttnPieces pieces;
   PageDiv div;
+  long long share_min;
   float* part;      // [B Hkv][splits][split_floats(rep)]
   int* tickets;     // [B Hkv], zero between calls
   int* err;
@@ -104,6 +106,7 @@ __global__ void __launch_bounds__(kTh, 3) attn_suffix_kernel(const __grid_consta
   // ---- the sequence's group (every warp for itself), and whether the groups make sense
   const int len = p.seq_lens[b];
   int grp = -1, shared = 0;
+  long long saved = 0;
   bool bad = false;
   for (int i0 = 0; i0 < p.n_groups; i0 += 32) {
     const int i = i0 + lane;
@@ -113,6 +116,7 @@ __global__ void __launch_bounds__(kTh, 3) attn_suffix_kernel(const __grid_consta
       const int lo = p.cu[i], hi = p.cu[i + 1];
       n = p.shared_lens[i];
       bad = bad || lo < 0 || hi < lo || hi > p.B;
+      if (hi > lo && n > 0 && n <= p.cap) saved += (long long)n * (hi - lo - 1);
       in = lo <= b && b < hi;
     }
     const unsigned hit = __ballot_sync(0xffffffffu, in);
@@ -128,7 +132,9 @@ __global__ void __launch_bounds__(kTh, 3) attn_suffix_kernel(const __grid_consta
     pdl_wait();
     return;
   }
-  const int t0 = min(shared, len), own = len - t0;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) saved += __shfl_xor_sync(0xffffffffu, saved, d);
+  const int t0 = saved < p.share_min ? 0 : min(shared, len), own = len - t0;   // as attention_rows.cu decides
   int chunk = (own + (int)gridDim.x - 1) / (int)gridDim.x;
   chunk = max(kMinChunk, (chunk + kW * kBlock - 1) / (kW * kBlock) * (kW * kBlock));
   const int n_act = max(1, (own + chunk - 1) / chunk);
@@ -464,6 +470,15 @@ int splits(int B, int Hkv) {
   return (int)std::max(1LL, std::min((long long)kMaxSplits, (want + pairs - 1) / pairs));
 }
 
+// Sharing costs a kernel more and the joining of its pieces, some 12 us; reading everything
+// for every sequence costs the repeated bytes at about 5.5 TB/s. Measured crossing between 60 and
+// 100 MB: 64 x 256 tokens (8 kv heads) 22.8 us shared, 21.4 not; 16 x 2048 25.2 and 33.4; 4 x
+// 8192 34.7 and 36.2 (f32). QD_SHARED_MIN_MB (read per call) sets another limit.
+long long share_min(int Hkv) {
+  const char* v = getenv("QD_SHARED_MIN_MB");
+  return (v ? std::max(0LL, atoll(v)) : 80) * 1000000 / ((long long)Hkv * 2 * kD * 2);
+}
+
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 size_t pre_bytes(int B, int Hq) { return round256((size_t)B * Hq * (kD + 2) * 4); }
 size_t from_bytes(int B, int Hkv) { return round256((size_t)B * Hkv * sizeof(AttnFrom)); }
@@ -485,7 +500,9 @@ size_t attn_shared_workspace_bytes(int B, int Hq, int Hkv) {
          from_bytes(B, Hkv) + (size_t)B * Hkv * splits(B, Hkv) * split_floats(Hq / Hkv) * 4;
 }
 
-cudaError_t launch_attn_shared(const AttnRowsArgs& a, const Launch& L) {
+cudaError_t launch_attn_shared(const AttnRowsArgs& args, const Launch& L) {
+  AttnRowsArgs a = args;
+  a.share_min = share_min(a.Hkv);
   unsigned char* ws = (unsigned char*)a.workspace + round256(attn_rows_workspace_bytes());
   float* pre = (float*)(ws + kTicketBytes);
   Launch first = L;
@@ -507,6 +524,7 @@ cudaError_t launch_attn_shared(const AttnRowsArgs& a, const Launch& L) {
   p.pre_l = p.pre_m + (size_t)a.n_rows * a.Hq;
   p.from = from;
   p.div = make_page_div(a.page_size);
+  p.share_min = a.share_min;
   p.tickets = (int*)ws;
   p.part = (float*)((unsigned char*)from + from_bytes(a.n_rows, a.Hkv));
   p.err = L.err;

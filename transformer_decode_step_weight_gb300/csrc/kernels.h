@@ -315,6 +315,7 @@ struct AttnRowsArgs {
   float scale;
   void* out;               // as q's type, rows contiguous
   void* workspace;
+  long long share_min;     // shared form: tokens whose re-reading must be saved for sharing to pay
 };
 size_t attn_rows_workspace_bytes();
 size_t attn_shared_workspace_bytes(int B, int Hq, int Hkv);
