@@ -8,13 +8,15 @@
 // that are not finite count as 0.
 //
 // Which token is drawn hangs on where a sum over the vocabulary crosses a border, so the
-// sums are kept in pairs of floats (48 bits, by exact two-sums; binary64 adds run at
-// 1/64 of the binary32 rate here): a border is misplaced by about 2^-45 of the total.
+// sums are kept in pairs of floats (about 46 bits; binary64 adds run at 1/64 of the binary32
+// rate here): a border is misplaced by about 2^-45 of the total.
 //
 // One launch: CTA (chunk c, sequence b) finds m (k gathered values, the same in every
 // CTA), sums its chunk of the one or two rows that matter, and the sequence's last CTA
 // (ticket) finds the chunk that holds the border, reads that chunk again and writes the
-// state. Bytes: one or two vocabulary rows per sequence, whatever k.
+// state. Bytes: one or two vocabulary rows per sequence, whatever k. Chunks are as long as
+// about eight CTAs per SM need: all of them are then resident and wait for their m at the
+// same time.
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.cuh"
@@ -34,21 +36,11 @@ QD_DEV Pair two_sum(float a, float b) {
   const float s = __fadd_rn(a, b), z = __fsub_rn(s, a);
   return Pair{s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, z)), __fsub_rn(b, z))};
 }
-// a + b for a running sum a and one value b (three roundings of the low parts: 2^-46 of
-// the sum)
-QD_DEV Pair add_small(Pair a, Pair b) {
-  const Pair s = two_sum(a.hi, b.hi);
-  return two_sum(s.hi, __fadd_rn(__fadd_rn(s.lo, b.lo), a.lo));
-}
 QD_DEV Pair add(Pair a, Pair b) {
-  const Pair s = two_sum(a.hi, b.hi), t = two_sum(a.lo, b.lo);
-  const Pair v = two_sum(s.hi, __fadd_rn(s.lo, t.hi));
-  return two_sum(v.hi, __fadd_rn(v.lo, t.lo));
+  const Pair s = two_sum(a.hi, b.hi);
+  return two_sum(s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)));
 }
 QD_DEV double value(Pair a) { return (double)a.hi + (double)a.lo; }
-QD_DEV Pair shfl_up(Pair a, int o) {
-  return Pair{__shfl_up_sync(0xffffffffu, a.hi, o), __shfl_up_sync(0xffffffffu, a.lo, o)};
-}
 
 struct VsParams {
   const float *target, *draft_p, *u;
@@ -63,64 +55,75 @@ struct VsParams {
   int* err;
 };
 
-// r of one token, exactly (hi is p - q rounded, lo what the rounding left; hi > 0 just
-// where p > q)
-QD_DEV Pair mass(float p, float q) {
-  const Pair r = two_sum(p, -q);
-  return r.hi > 0.f && r.hi < INFINITY ? r : Pair{0.f, 0.f};
+// s + r of one token. r = p - q exactly: rounded, and what the rounding left (p > q >= 0 where
+// it counts). The low part gathers what the high part loses and is not renormalised.
+QD_DEV void add_mass(Pair& s, float p, float q) {
+  const float r = __fsub_rn(p, q);
+  const bool some = r > 0.f && r < INFINITY;
+  const float e = __fsub_rn(__fsub_rn(p, r), q);
+  const Pair t = two_sum(s.hi, some ? r : 0.f);
+  s.hi = t.hi;
+  s.lo = __fadd_rn(s.lo, __fadd_rn(t.lo, some ? e : 0.f));
 }
 
-// the 4 N values of r from token j on (j a multiple of 4), 0 past the vocabulary; q null:
-// r = p
-template <int N>
-QD_DEV void load_mass(const float* p, const float* q, int j, int V, int vec, Pair* r) {
-  float a[4 * N], b[4 * N];
-  if (vec && j + 4 * N <= V) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) *(float4*)(a + 4 * i) = *(const float4*)(p + j + 4 * i);
-    if (q)
-#pragma unroll
-      for (int i = 0; i < N; ++i) *(float4*)(b + 4 * i) = *(const float4*)(q + j + 4 * i);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4 * N; ++i) a[i] = j + i < V ? p[j + i] : 0.f;
-    if (q)
-#pragma unroll
-      for (int i = 0; i < 4 * N; ++i) b[i] = j + i < V ? q[j + i] : 0.f;
-  }
-#pragma unroll
-  for (int i = 0; i < 4 * N; ++i) r[i] = mass(a[i], q ? b[i] : 0.f);
+// four tokens from j on; 0 past `end`
+QD_DEV float4 load4(const float* p, int j, int end, int vec) {
+  if (vec && j + 4 <= end) return *(const float4*)(p + j);
+  return make_float4(j < end ? p[j] : 0.f, j + 1 < end ? p[j + 1] : 0.f, j + 2 < end ? p[j + 2] : 0.f,
+                     j + 3 < end ? p[j + 3] : 0.f);
 }
 
-// inclusive sum over the CTA's threads in thread order, in pairs; total: the whole sum
-QD_DEV Pair block_scan(Pair v, Pair* warp_sums, Pair& total) {
+// inclusive sum over the CTA's threads in thread order; total: the whole sum
+__device__ __noinline__ Pair block_scan(Pair v, Pair* warp_sums, Pair* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __syncthreads();
-#pragma unroll
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
-    const Pair x = shfl_up(v, o);
+    const Pair x = {__shfl_up_sync(0xffffffffu, v.hi, o), __shfl_up_sync(0xffffffffu, v.lo, o)};
     if (lane >= o) v = add(x, v);
   }
   if (lane == 31) warp_sums[warp] = v;
   __syncthreads();
   Pair before{0.f, 0.f}, all{0.f, 0.f};
-#pragma unroll
+#pragma unroll 1
   for (int w = 0; w < kTh / 32; ++w) {
     if (w == warp) before = all;
     all = add(all, warp_sums[w]);
   }
-  total = all;
+  *total = all;
   return add(before, v);
 }
 
-// N: float4 loads per thread, chunk = kTh * 4 N tokens
-template <int N>
-__global__ void __launch_bounds__(kTh) verify_sample_kernel(const VsParams p) {
-  __shared__ int s_m, s_n, s_last, s_tok, s_chunk;
-  __shared__ Pair warp_sums[kTh / 32];
-  __shared__ double s_before, s_total;
+// The CTA's sum of r over the tokens [j0, end): thread t takes every kTh-th group of four.
+QD_DEV double chunk_sum(const float* p, const float* q, int j0, int end, int vec, Pair* warp_sums) {
+  Pair s{0.f, 0.f}, total;
+  constexpr int kU = 4;
+  for (int j = j0 + threadIdx.x * 4; j < end; j += kTh * 4 * kU) {
+    float4 a[kU], b[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      a[u] = load4(p, j + u * kTh * 4, end, vec);
+      b[u] = q ? load4(q, j + u * kTh * 4, end, vec) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      add_mass(s, a[u].x, b[u].x);
+      add_mass(s, a[u].y, b[u].y);
+      add_mass(s, a[u].z, b[u].z);
+      add_mass(s, a[u].w, b[u].w);
+    }
+  }
+  block_scan(s, warp_sums, &total);
+  return value(total);
+}
+
+__global__ void __launch_bounds__(kTh) verify_sample_kernel(const __grid_constant__ VsParams p) {
+  __shared__ int s_m, s_n, s_last, s_tok, s_chunk, s_some;
+  __shared__ Pair warp_sums[kTh / 32], s_prev[kTh];
+  __shared__ double s_want;
   const int c = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
-  const int kd = p.k - 1;
+  const int kd = p.k - 1, nc = (int)gridDim.x;
+  const float ul = p.u[(size_t)b * p.k + kd];
   if (tid < 32) {
     int n = p.n_draft ? p.n_draft[b] : kd;
     if (n < 0 || n > kd) {
@@ -151,54 +154,26 @@ __global__ void __launch_bounds__(kTh) verify_sample_kernel(const VsParams p) {
   const int m = s_m;
   const float* pr = p.target + ((size_t)b * p.k + m) * p.t_stride;
   const float* qr = m < s_n ? p.draft_p + ((size_t)b * kd + m) * p.d_stride : nullptr;
-  // ---- the chunk's sum: thread t takes the float4 at t, t + kTh, ... of the chunk
+  double* part = p.part + (size_t)b * nc;
   {
-    Pair s{0.f, 0.f};
-    Pair r[4 * N];
-    const int j0 = c * p.chunk;
-#pragma unroll
-    for (int i = 0; i < N; ++i) load_mass<1>(pr, qr, j0 + (i * kTh + tid) * 4, p.V, p.vec, r + 4 * i);
-#pragma unroll
-    for (int i = 0; i < 4 * N; ++i) s = add_small(s, r[i]);
-    Pair total;
-    block_scan(s, warp_sums, total);
+    const double sum = chunk_sum(pr, qr, c * p.chunk, min((c + 1) * p.chunk, p.V), p.vec, warp_sums);
     if (tid == 0) {
-      p.part[(size_t)b * gridDim.x + c] = value(total);
-      s_last = atom_add_acq_rel_gpu(p.cnt + b, 1) == (int)gridDim.x - 1;
+      part[c] = sum;
+      s_last = atom_add_acq_rel_gpu(p.cnt + b, 1) == nc - 1;
     }
   }
   __syncthreads();
   if (!s_last) return;
+
   // ---- the sequence's last CTA: the chunk that holds the border
-  if (tid == 0) s_tok = -1;
-  const float ul = p.u[(size_t)b * p.k + p.k - 1];
-  for (int attempt = 0; attempt < 2; ++attempt) {
-    if (attempt == 1) {   // nothing left of p - q: draw from p, whose chunk sums nobody has made yet
-      if (qr == nullptr) break;
-      qr = nullptr;
-      for (int ch = 0; ch < (int)gridDim.x; ++ch) {
-        Pair s{0.f, 0.f}, total;
-        Pair r[4 * N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) load_mass<1>(pr, qr, ch * p.chunk + (i * kTh + tid) * 4, p.V, p.vec, r + 4 * i);
-#pragma unroll
-        for (int i = 0; i < 4 * N; ++i) s = add_small(s, r[i]);
-        block_scan(s, warp_sums, total);
-        if (tid == 0) p.part[(size_t)b * gridDim.x + ch] = value(total);
-      }
-      __threadfence();
-      __syncthreads();
-    }
+#pragma unroll 1
+  for (int attempt = 0;; ++attempt) {
     if (tid < 32) {
-      const double* part = p.part + (size_t)b * gridDim.x;
-      const int nc = (int)gridDim.x;
       double total = 0.0;
-      for (int i0 = 0; i0 < nc; i0 += 32) {
-        double v = i0 + lane < nc ? __ldcg(part + i0 + lane) : 0.0;
+#pragma unroll 4
+      for (int i = lane; i < nc; i += 32) total += __ldcg(part + i);
 #pragma unroll
-        for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        total += v;
-      }
+      for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
       // the first chunk whose running sum passes the border; the last one with any mass
       // where rounding leaves none
       const double border = (double)ul * total;
@@ -228,76 +203,69 @@ __global__ void __launch_bounds__(kTh) verify_sample_kernel(const VsParams p) {
       }
       if (lane == 0) {
         s_chunk = hit >= 0 ? hit : some;
-        s_before = hit >= 0 ? b_hit : b_some;
-        s_total = border;
+        s_want = border - (hit >= 0 ? b_hit : b_some);
       }
     }
     __syncthreads();
-    if (s_chunk >= 0) break;
+    if (s_chunk >= 0 || qr == nullptr || attempt) break;
+    // nothing left of p - q: draw from p, whose chunk sums nobody has made yet
+    qr = nullptr;
+#pragma unroll 1
+    for (int ch = 0; ch < nc; ++ch) {
+      const double sum = chunk_sum(pr, nullptr, ch * p.chunk, min((ch + 1) * p.chunk, p.V), p.vec, warp_sums);
+      if (tid == 0) part[ch] = sum;
+    }
+    __threadfence();
+    __syncthreads();
   }
+  if (tid == 0) s_tok = s_some = -1;
+  __syncthreads();
   if (s_chunk >= 0) {
-    // ---- its tokens in order: thread t takes 4 N consecutive ones
-    const int j = s_chunk * p.chunk + tid * 4 * N;
-    Pair r[4 * N];
-    load_mass<N>(pr, qr, j, p.V, p.vec, r);
+    // ---- its tokens in order: thread t takes chunk / kTh consecutive ones. Running sums never
+    // fall, so the first thread past the border holds the token; where rounding leaves none,
+    // the chunk's last token with any mass
+    const int each = p.chunk / kTh, j0 = s_chunk * p.chunk + tid * each;
+    const int end = min(p.V, j0 + each);
     Pair s{0.f, 0.f}, total;
+    int last = -1;
+#pragma unroll 4
+    for (int j = j0; j < end; j += 4) {
+      const float4 x = load4(pr, j, end, p.vec), y = qr ? load4(qr, j, end, p.vec) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-    for (int i = 0; i < 4 * N; ++i) s = add_small(s, r[i]);
-    const Pair incl = block_scan(s, warp_sums, total);
-    // the border as a pair, relative to the chunk's start
-    const double want = s_total - s_before;
-    const Pair lim{(float)want, (float)(want - (double)(float)want)};
-    const Pair neg{-lim.hi, -lim.lo};
+      for (int i = 0; i < 4; ++i) {
+        add_mass(s, xs[i], ys[i]);
+        const float r = xs[i] - ys[i];
+        if (r > 0.f && r < INFINITY) last = j + i;
+      }
+    }
+    const Pair incl = block_scan(s, warp_sums, &total);
+    s_prev[tid] = incl;
+    const double want = s_want;
+    const Pair neg{-(float)want, -(float)(want - (double)(float)want)};
     auto over = [&](Pair a) {
       const Pair d = add(a, neg);
       return d.hi > 0.f || (d.hi == 0.f && d.lo > 0.f);
     };
+    if (last >= 0) atomicMax(&s_some, last);
     const bool mine = over(incl);
-    const unsigned vote = __ballot_sync(0xffffffffu, mine);
-    __shared__ int s_first[kTh / 32], s_some[kTh / 32];
-    // running sums never fall, so the first thread past the border holds the token; where
-    // rounding leaves none, the chunk's last token with any mass
-    int last = -1;
-#pragma unroll
-    for (int i = 0; i < 4 * N; ++i)
-      if (r[i].hi > 0.f) last = j + i;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) last = max(last, __shfl_xor_sync(0xffffffffu, last, o));
-    if (lane == 0) {
-      s_first[tid >> 5] = vote ? (tid & ~31) + __ffs(vote) - 1 : kTh;
-      s_some[tid >> 5] = last;
-    }
-    __syncthreads();
-    int first = kTh, some = -1;
-#pragma unroll
-    for (int w = 0; w < kTh / 32; ++w) {
-      first = min(first, s_first[w]);
-      some = max(some, s_some[w]);
-    }
-    if (first == kTh) {
-      if (tid == 0) s_tok = some;
-    } else {
-      // the sum before thread `first`, from its left neighbour
-      __shared__ Pair s_prev[kTh];
-      s_prev[tid] = incl;
-      __syncthreads();
-      if (tid == first) {
-        Pair a = tid ? s_prev[tid - 1] : Pair{0.f, 0.f};
-        int t = -1;
-        for (int i = 0; i < 4 * N; ++i) {
-          a = add_small(a, r[i]);
-          if (r[i].hi > 0.f) {
-            t = j + i;
-            if (over(a)) break;
-          }
+    const int votes = __syncthreads_count(!mine);   // the threads before the first one past the border
+    if (tid == min(votes, kTh - 1) && mine) {
+      Pair a = tid ? s_prev[tid - 1] : Pair{0.f, 0.f};
+#pragma unroll 4
+      for (int j = j0; j < end; ++j) {
+        const float x = pr[j], y = qr ? qr[j] : 0.f, r = x - y;
+        add_mass(a, x, y);
+        if (r > 0.f && r < INFINITY) {
+          s_tok = j;
+          if (over(a)) break;
         }
-        s_tok = t >= 0 ? t : some;
       }
     }
     __syncthreads();
   }
   if (tid == 0) {
-    int t = s_tok;
+    int t = s_tok >= 0 ? s_tok : s_some;
     if (t < 0) {   // a row without any positive finite entry
       set_error(p.err, QD_DEVERR_NAN);
       t = 0;
@@ -339,12 +307,10 @@ cudaError_t launch_verify_sample(const VerifySampleArgs& a, const Launch& L) {
   p.err = L.err;
   p.vec = ((uintptr_t)a.target & 15u) == 0 && a.t_stride % 4 == 0 &&
           (a.k == 1 || (((uintptr_t)a.draft_probs & 15u) == 0 && a.d_stride % 4 == 0));
-  // chunks of 4096 tokens; of 1024 where those would leave SMs without work
-  const bool small = (long long)a.B * ceil_div(a.V, kTh * 16) < dev_info().sm_count;
-  p.chunk = kTh * (small ? 4 : 16);
-  const dim3 grid(ceil_div(a.V, p.chunk), a.B);
-  return small ? launch_ex(verify_sample_kernel<1>, grid, dim3(kTh), 0, L, p)
-               : launch_ex(verify_sample_kernel<4>, grid, dim3(kTh), 0, L, p);
+  // about eight CTAs per SM, chunks a multiple of 1024 tokens
+  const int chunks = (int)std::max(1LL, std::min((long long)kMaxChunks, 8LL * dev_info().sm_count / a.B));
+  p.chunk = ceil_div(ceil_div(a.V, chunks), kTh * 4) * kTh * 4;
+  return launch_ex(verify_sample_kernel, dim3(ceil_div(a.V, p.chunk), a.B), dim3(kTh), 0, L, p);
 }
 
 }  // namespace qd
