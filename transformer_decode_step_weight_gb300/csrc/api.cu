@@ -550,7 +550,7 @@ int qd_pages_extend(const qd_page_cache* c, const int32_t* n_new, cudaStream_t s
   const int rc = check_page_cache("qd_pages_extend", c, true, true);
   if (rc) return rc;
   if (!n_new) return fail(QD_ERR_INVALID_ARG, "qd_pages_extend: null pointer");
-  cudaError_t e = launch_pages_extend(page_state(c), page_copy(c), n_new, c->workspace, make_launch(stream, false));
+  cudaError_t e = launch_pages_extend(page_state(c), page_copy(c), n_new, c->workspace, make_launch(stream, true));
   return e == cudaSuccess ? QD_OK : cuda_fail(e, "qd_pages_extend");
 }
 
@@ -566,7 +566,7 @@ int qd_pages_compact(const qd_page_cache* c, int32_t* n_live, cudaStream_t strea
   const int rc = check_page_cache("qd_pages_compact", c, true, true);
   if (rc) return rc;
   if (!n_live) return fail(QD_ERR_INVALID_ARG, "qd_pages_compact: null pointer");
-  cudaError_t e = launch_pages_compact(page_state(c), page_copy(c), n_live, c->workspace, make_launch(stream, false));
+  cudaError_t e = launch_pages_compact(page_state(c), page_copy(c), n_live, c->workspace, make_launch(stream, true));
   return e == cudaSuccess ? QD_OK : cuda_fail(e, "qd_pages_compact");
 }
 

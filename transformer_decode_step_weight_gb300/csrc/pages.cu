@@ -181,7 +181,8 @@ __global__ void __launch_bounds__(kForkTh) pages_fork_kernel(PageState c, Ws ws,
 // last page has to be copied), a prefix sum over the sequences, the lowest free ids into
 // ws.map, then the table rows, the counts and the list of copies.
 __global__ void __launch_bounds__(kPlan) pages_extend_kernel(PageState c, Ws ws, const int32_t* n_new, int* err) {
-  extern __shared__ int32_t sh[];
+  extern __shared__ __align__(16) int32_t sh[];
+  pdl_launch_dependents();   // the copies wait for this kernel before they read the list
   int32_t* cand = sh;                     // [max_seqs] a shared last page, or -1
   int32_t* at = cand + c.max_seqs;        // [max_seqs] first new page of the sequence
   int32_t* need = at + c.max_seqs;        // [max_seqs] pages it takes; bit 30: the first is a copy
@@ -200,7 +201,10 @@ __global__ void __launch_bounds__(kPlan) pages_extend_kernel(PageState c, Ws ws,
       } else if (len % ps) {
         const int p = c.table[(size_t)s * c.max_pages + len / ps];
         if (p < 0 || p >= c.n_pages) s_bad = QD_DEVERR_CACHE | QD_DEVERR_PAGE;
-        else if (c.refs[p] > 1) q = p;
+        else if (const int r = c.refs[p]; r > 1) {
+          q = p;
+          need[s] = r;
+        }
       }
     }
     cand[s] = q;
@@ -223,9 +227,13 @@ __global__ void __launch_bounds__(kPlan) pages_extend_kernel(PageState c, Ws ws,
       const int q = cand[s];
       bool copy = false;
       if (q >= 0) {   // the sharers extended before this one have left the page
-        int before = 0;
-        for (int j = 0; j < s; ++j) before += cand[j] == q;
-        copy = c.refs[q] - before > 1;
+        int before = 0, j = 0;
+        for (; j + 4 <= s; j += 4) {
+          const int4 p = *(const int4*)(cand + j);
+          before += (p.x == q) + (p.y == q) + (p.z == q) + (p.w == q);
+        }
+        for (; j < s; ++j) before += cand[j] == q;
+        copy = need[s] - before > 1;
       }
       need[s] = w + (copy ? (1 | kCopyBit) : 0);
       w += copy;
@@ -296,6 +304,7 @@ __global__ void __launch_bounds__(kForkTh) pages_trim_kernel(PageState c, const 
 __global__ void __launch_bounds__(kPlan) pages_compact_kernel(PageState c, Ws ws, int32_t* n_live) {
   __shared__ int warp_sums[kPlan / 32];
   const int tid = threadIdx.x;
+  pdl_launch_dependents();
   const int n = walk_pages(c.refs, 0, c.n_pages, false, 0, INT32_MAX, warp_sums, [](int, int) {});
   const int holes = walk_pages(c.refs, 0, n, true, 0, INT32_MAX, warp_sums,
                                [&](int rank, int page) { ws.dst[rank] = page; });
@@ -316,6 +325,7 @@ __global__ void __launch_bounds__(kPlan) pages_compact_kernel(PageState c, Ws ws
 
 // table entries of the moved pages; one CTA per sequence, its pages only
 __global__ void __launch_bounds__(kForkTh) pages_remap_kernel(PageState c, Ws ws, int* err) {
+  pdl_launch_dependents();
   pdl_wait();
   const int s = blockIdx.x, n = ws.head[2];
   const int had = min(pages_of(max(c.lens[s], 0), c.page_size), c.max_pages);
@@ -374,7 +384,9 @@ cudaError_t launch_pages_fork(const PageState& c, const int32_t* parents, const 
 cudaError_t launch_pages_extend(const PageState& c, const PageCopy& pc, const int32_t* n_new, void* workspace,
                                 const Launch& L) {
   const Ws ws = ws_of(c, workspace);
-  cudaError_t e = launch_ex(pages_extend_kernel, dim3(1), dim3(kPlan), (size_t)c.max_seqs * 12, L, c, ws, n_new, L.err);
+  Launch first = L;
+  first.pdl = false;
+  cudaError_t e = launch_ex(pages_extend_kernel, dim3(1), dim3(kPlan), (size_t)c.max_seqs * 12, first, c, ws, n_new, L.err);
   if (e != cudaSuccess) return e;
   return copy_pairs(pc, ws.src, ws.dst, 0, ws.head + 1, c.n_pages, L);
 }
@@ -386,7 +398,9 @@ cudaError_t launch_pages_trim(const PageState& c, const int32_t* new_lens, const
 cudaError_t launch_pages_compact(const PageState& c, const PageCopy& pc, int32_t* n_live, void* workspace,
                                  const Launch& L) {
   const Ws ws = ws_of(c, workspace);
-  cudaError_t e = launch_ex(pages_compact_kernel, dim3(1), dim3(kPlan), 0, L, c, ws, n_live);
+  Launch first = L;
+  first.pdl = false;
+  cudaError_t e = launch_ex(pages_compact_kernel, dim3(1), dim3(kPlan), 0, first, c, ws, n_live);
   if (e != cudaSuccess) return e;
   e = launch_ex(pages_remap_kernel, dim3(c.max_seqs), dim3(kForkTh), 0, L, c, ws, L.err);
   if (e != cudaSuccess) return e;
