@@ -222,18 +222,20 @@ int qd_attn_decode_paged_noalloc(const float* q, const void* k_pages, const void
 /* q: [n_rows, n_q_heads, head_dim], q_stride elements from one row to the next    */
 /* (>= n_q_heads * head_dim, a multiple of 16 bytes: q may be part of the QKV       */
 /* projection's rows); q_is_f32 = 1: q and out f32 (q and the softmax weights       */
-/* enter the bf16 matrix products as hi + lo pairs), 0: both bf16 (the weights      */
+/* enter the bf16 matrix products in three parts, 24 bits), 0: both bf16 (the weights  */
 /* rounded to bf16, sums and softmax statistics in f32). out: [n_rows, n_q_heads,   */
-/* head_dim], contiguous, not q. Caches and page_table as in qd_attn_decode_paged;   */
+/* head_dim], contiguous, apart from q. Caches and page_table as in qd_attn_decode_paged; */
 /* cu_rows: int32 [batch + 1], ascending from >= 0 to <= n_rows; seq_lens: int32      */
 /* [batch] (both device). Keys a row does not see have no effect on it, NaN and       */
 /* infinities included. Errors on the device (QD_DEVERR_POS: cu_rows not ascending     */
 /* or past n_rows, which leaves all of out; a length past the table, which leaves the   */
 /* sequence's rows). workspace: device scratch of qd_attn_prompt_workspace_bytes()       */
 /* bytes for the current device, zero-filled before its first use (each call leaves it    */
-/* ready for the next); two calls that overlap on the GPU need two.                      */
+/* ready for the next, but for one that ends with QD_DEVERR_TIMEOUT: zero-fill it again);   */
+/* two calls that overlap on the GPU need two.                                              */
 /* Limits: head_dim == 128, n_q_heads / n_kv_heads in {1, 2, 4, 8}, batch <= 1024,      */
-/* n_rows <= 2^20.                                                                     */
+/* n_rows <= 2^20; the blocks of 128 q rows (a row and a q head of one kv head) by 128 keys   */
+/* that the call computes fewer than 2^31 (else QD_DEVERR_POS, and out is left as it was).    */
 size_t qd_attn_prompt_workspace_bytes(void);
 int qd_attn_prompt(const void* q, int q_is_f32, int64_t q_stride, const void* k_pages, const void* v_pages,
                    const int32_t* page_table, const int32_t* cu_rows, const int32_t* seq_lens, int batch,
@@ -243,9 +245,10 @@ int qd_attn_prompt(const void* q, int q_is_f32, int64_t q_stride, const void* k_
 
 /* Decode attention of sequences that share prefixes: the result of                 */
 /* qd_attn_decode_paged for sequences whose page tables name the same pages at their  */
-/* start (qd_pages_fork), each shared page read once for all of them (where that spares */
-/* less than QD_SHARED_MIN_MB, default 80, megabytes of re-reading, each sequence reads    */
-/* its own table's pages: a second kernel costs more). Group i holds    */
+/* start (qd_pages_fork), each shared page read once for all of them. Where that would     */
+/* spare less than 80 MB of re-reading (QD_SHARED_MIN_MB, read at every call, sets another    */
+/* limit; 0: always share) each sequence reads its own table's pages, which is then faster.    */
+/* Group i holds                                                                               */
 /* the sequences cu_seqs[i] .. cu_seqs[i + 1); their first shared_lens[i] tokens lie in  */
 /* the pages of the group's first sequence's row (a sequence shorter than that sees its   */
 /* own seq_lens tokens of them). Sequences outside every group are left as they were.      */
@@ -253,7 +256,11 @@ int qd_attn_prompt(const void* q, int q_is_f32, int64_t q_stride, const void* k_
 /* in qd_attn_prompt with one row per sequence: q, out [batch, n_q_heads, head_dim];          */
 /* page_table [batch, max_pages], seq_lens [batch]; cu_seqs: int32 [n_groups + 1],            */
 /* ascending; shared_lens: int32 [n_groups] (both device). seq_lens[b] == 0 gives out = 0.      */
-/* workspace: qd_attn_shared_workspace_bytes(...) bytes, zero-filled before its first use.       */
+/* A visible infinity in K or V may give NaN where the sum over the keys would be infinite         */
+/* (f32 splits it into parts). After an error that leaves rows unwritten in qd_attn_prompt, out      */
+/* is undefined there.                                                                             */
+/* workspace: qd_attn_shared_workspace_bytes(...) bytes, zero-filled before its first use, for       */
+/* the current device, as in qd_attn_prompt.                                                        */
 /* Limits: as qd_attn_prompt, n_groups <= 1024, batch <= 65535.                                 */
 size_t qd_attn_shared_workspace_bytes(int batch, int n_q_heads, int n_kv_heads);
 int qd_attn_decode_shared(const void* q, int q_is_f32, int64_t q_stride, const void* k_pages, const void* v_pages,
@@ -469,7 +476,7 @@ int qd_verify_step(const qd_step_args* args, const int32_t* draft, int k, float*
 /* if m < n (target_probs[b, m, :] if that is zero everywhere), r = target_probs[b, n, :] if    */
 /* m == n. Entries of r that are not finite count as 0; a row without mass gives 0 and sets       */
 /* QD_DEVERR_NAN; a draft outside the vocabulary is rejected; n_draft outside 0 .. k - 1 is        */
-/* clamped and sets QD_DEVERR_POS. Sums in 48 bits or more. The state advances as in                */
+/* clamped and sets QD_DEVERR_POS. Sums in 46 bits. The state advances as in                */
 /* qd_verify_step: n_accept[b] = m; out_tokens[b, step ..] = the m drafts, t; tok = t;               */
 /* pos += m + 1; step += m + 1 (past max_steps: QD_DEVERR_STEPS).                                    */
 /* target_probs: f32, row (b, i) at (b * k + i) * target_stride; draft_probs: f32, row (b, i) at       */

@@ -236,6 +236,7 @@ SHARED = [
     ([(100, 1500), (3, 700), (20, 300)], [i % 5 for i in range(123)], 8, 1, 16),   # teams of 7 CTAs
     ([(80, 400)], [2] * 80, 8, 2, 64),
     ([(150, 300)], [i % 2 for i in range(150)], 8, 1, 16),   # more row tiles than a team has members
+    ([(3, 150)], [1, 0, 3], 4, 1, 1),
 ]
 
 
@@ -369,6 +370,97 @@ def test_one_workspace_for_calls_of_different_sizes(cuda_lib, monkeypatch, min_m
         d = torch.randint(0, 9000, (B, 1), generator=g, device=DEV).int()
         _verify(p, q, d, torch.rand((B, 2), generator=g, device=DEV), workspace=ws)
     assert api.check_device_error() == 0
+
+
+@pytest.mark.parametrize("scale", [-0.05, 0.0, -1.0, 3e-4])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("min_mb", ["0", "80"])
+def test_attention_scales(cuda_lib, monkeypatch, scale, dtype, min_mb):
+    # the largest score is the smallest product where the scale is negative, and every key weighs the same at 0
+    monkeypatch.setenv("QD_SHARED_MIN_MB", min_mb)
+    g = _gen(25)
+    hq, hkv, ps = 8, 2, 16
+    rows, lens = [60, 2], [300, 90]
+    kp, vp, pt = _cache(g, lens, hkv, ps)
+    cu, seqs, seen = _pack(rows, lens)
+    q = torch.randn((cu[-1], hq, D), generator=g, device=DEV).to(dtype)
+    out = api.attn_prompt(q, kp, vp, pt, _ints(cu), _ints(lens), scale)
+    _check_rows(out, q, kp, vp, pt, seqs, seen, range(0, 62, 3), scale=scale)
+    lens = [300 + i for i in range(9)]
+    kp, vp, pt = _cache(g, lens, hkv, ps, [(0, 16)] * 9)
+    out = api.attn_decode_shared(q[:9], kp, vp, pt, _ints(lens), _ints([0, 9]), _ints([256]), scale)
+    _check_rows(out, q[:9], kp, vp, pt, list(range(9)), lens, scale=scale)
+    assert api.check_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_attention_of_many_short_sequences(cuda_lib, monkeypatch, dtype):
+    # more sequences, and more groups, than a CTA has threads
+    monkeypatch.setenv("QD_SHARED_MIN_MB", "0")
+    g = _gen(26)
+    hq, hkv, ps, B = 4, 2, 8, 1024
+    rows = [(7 * i) % 4 for i in range(B)]
+    lens = [n + (13 * i) % 50 for i, n in enumerate(rows)]
+    kp, vp, pt = _cache(g, lens, hkv, ps)
+    cu, seqs, seen = _pack(rows, lens)
+    q = torch.randn((cu[-1], hq, D), generator=g, device=DEV).to(dtype)
+    out = api.attn_prompt(q, kp, vp, pt, _ints(cu), _ints(lens), SCALE)
+    _check_rows(out, q, kp, vp, pt, seqs, seen, list(range(0, cu[-1], 31)) + [cu[-1] - 1])
+    members = [1 + i % 3 for i in range(B)]
+    who = [i for i, n in enumerate(members) for _ in range(n)]
+    starts = [0]
+    for n in members:
+        starts.append(starts[-1] + n)
+    shared = [8 * (i % 5) for i in range(B)]
+    lens = [shared[i] + (11 * b) % 20 for b, i in enumerate(who)]
+    kp, vp, pt = _cache(g, lens, hkv, ps, [(i, shared[i] // ps) for i in who])
+    q = torch.randn((len(who), hq, D), generator=g, device=DEV).to(dtype)
+    out = api.attn_decode_shared(q, kp, vp, pt, _ints(lens), _ints(starts), _ints(shared), SCALE)
+    pick = list(range(0, len(who), 31)) + [len(who) - 1]
+    _check_rows(out, q, kp, vp, pt, list(range(len(who))), lens, pick)
+    assert api.check_device_error() == 0
+
+
+@pytest.mark.parametrize("op", ["prompt", "shared"])
+def test_attention_calls_at_once_on_two_streams(cuda_lib, monkeypatch, op):
+    monkeypatch.setenv("QD_SHARED_MIN_MB", "0")
+    g = _gen(27)
+    hq, hkv, ps, lens = 8, 2, 16, [2000, 1700, 1900]
+    kp, vp, pt = _cache(g, lens, hkv, ps, [(0, 100)] * 3)
+    ln, cu, sl = _ints(lens), _ints([0, 1, 2, 3]), _ints([1600])
+    cu3 = _ints([0, 3])
+    qs = [torch.randn((3, hq, D), generator=g, device=DEV) for _ in range(2)]
+    nbytes = api.attn_prompt_workspace_bytes() if op == "prompt" else api.attn_shared_workspace_bytes(3, hq, hkv)
+    ws = [torch.zeros(nbytes, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    outs = [torch.zeros_like(qs[0]) for _ in range(2)]
+
+    def call(i, **kw):
+        if op == "prompt":
+            return api.attn_prompt(qs[i], kp, vp, pt, cu, ln, SCALE, workspace=ws[i], **kw)
+        return api.attn_decode_shared(qs[i], kp, vp, pt, ln, cu3, sl, SCALE, workspace=ws[i], **kw)
+
+    want = [call(i) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i in range(2):
+            call(i, out=outs[i], stream=streams[i])
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+    assert api.check_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_attention_of_one_head(cuda_lib, dtype):
+    # heads of one: the stride between heads means nothing
+    g = _gen(28)
+    kp, vp, pt = _cache(g, [70], 1, 16)
+    q = torch.randn((20, 3, 2 * D), generator=g, device=DEV).to(dtype)[:, ::2][:, :1, :D]
+    out = api.attn_prompt(q, kp, vp, pt, _ints([0, 20]), _ints([70]), SCALE)
+    _check_rows(out, q, kp, vp, pt, [0] * 20, list(range(51, 71)))
+    with pytest.raises(ValueError):
+        api.attn_prompt(torch.zeros((20, 3, 2 * D), dtype=dtype, device=DEV)[:, :2, :D], kp, vp, pt, _ints([0, 20]),
+                        _ints([70]), SCALE)
 
 
 # ------------------------------------------------------------------------------------------ page operations
@@ -508,6 +600,25 @@ def test_page_operations_in_a_graph(cuda_lib):
     assert api.check_device_error() == 0
 
 
+def test_page_operations_of_many_sequences(cuda_lib):
+    # as many sequences as there may be, most of them sharers of three pages, extended in one call
+    g, r = _gen(13), np.random.default_rng(13)
+    n = 2048
+    c = _page_cache(g, 5000, 4, n, 6, layers=1)
+    m = ref.Pages(5000, 4, n, 6)
+    contents = [x.cpu().clone() for x in c.k_cache + c.v_cache]
+    start = [6, 9, 3] + [0] * (n - 3)
+    kids = r.permutation(np.arange(3, n))[:1500].tolist()
+    par = r.integers(0, 3, 1500).tolist()
+    for grow in (start, np.where(r.random(n) < 0.7, r.integers(0, 3, n), 0).tolist(), r.integers(0, 2, n).tolist()):
+        c.extend(_ints(grow))
+        assert m.extend(grow) and api.check_device_error() == 0
+        _same(c, m, contents)
+        if grow is start:
+            c.fork(_ints(par), _ints(kids))
+            assert m.fork(par, kids)
+
+
 # -------------------------------------------------------------------------------------- sampled verification
 
 
@@ -601,6 +712,16 @@ def test_verify_sample_entries_that_are_not_finite(cuda_lib):
     _, tok, _ = _verify(p, None, None, torch.full((3, 1), 0.4, device=DEV))
     assert tok.tolist() == [4000, 0, 0]
     assert api.check_device_error() == 4
+
+
+def test_verify_sample_of_many_sequences(cuda_lib):
+    g = _gen(34)
+    B, k, V = 1500, 3, 37
+    p = torch.softmax(torch.randn((B, k, V), generator=g, device=DEV), -1)
+    q = torch.softmax(torch.randn((B, k - 1, V), generator=g, device=DEV), -1)
+    draft = torch.randint(0, V, (B, k - 1), generator=g, device=DEV).int()
+    _verify(p, q, draft, torch.rand((B, k), generator=g, device=DEV))
+    assert api.check_device_error() == 0
 
 
 def test_verify_sample_in_a_graph(cuda_lib):

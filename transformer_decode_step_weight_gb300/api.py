@@ -304,7 +304,7 @@ def _rows(fn, q, k_pages, v_pages, page_table, seq_lens, cu, out):
         raise ValueError(f"{fn}: q must be [rows, heads, head_dim] in float32 or bfloat16")
     n, hq, d = q.shape
     s0, s1, s2 = q.stride()
-    if n and (s2 != 1 or s1 != d):
+    if n and (s2 != 1 or (s1 != d and hq > 1)):
         raise ValueError(f"{fn}: a row's heads must be contiguous (strides {q.stride()})")
     _want("k_pages", k_pages, torch.bfloat16, 4, dev)
     _want("v_pages", v_pages, torch.bfloat16, 4, dev, k_pages.shape)
@@ -455,7 +455,8 @@ class PageCache:
     ``page_table`` int32 [max_seqs, max_pages] (-1 past a sequence's pages), ``seq_lens`` int32
     [max_seqs] and ``refs`` int32 [n_pages] (how many entries name each page, 0: free) are the
     state, device tensors that the calls update; without them only ``copy`` works. ``empty``
-    makes the state of an empty cache. One PageCache serves one stream at a time.
+    makes the state of an empty cache. One PageCache serves one stream at a time, and stays
+    alive until the work of its calls is done (it owns their workspace).
     """
 
     def __init__(self, k_cache, v_cache, page_table=None, seq_lens=None, refs=None):

@@ -5,17 +5,16 @@
 // sequences (shared form) times the Hq / Hkv q heads that read it, so a K/V tile is read
 // once for all of them. Work is counted in units of one row tile times 128 keys, ordered
 // by (segment, kv head, row tile, keys), and each CTA of the one-per-SM grid takes an equal run
-// of them. So ragged prompts, one long prompt and one row behind a long
-// cache all split evenly without the host knowing a length; a row tile that several CTAs
-// share is joined, in key order, by the last of them (ticket). A causal row tile counts
-// only the tiles that some row of it sees.
+// of them. So ragged prompts, one long prompt and one row behind a long cache all split
+// evenly without the host knowing a length; a prompt's row tile that several CTAs share is
+// joined, in key order, by the last of them (ticket). A causal row tile counts only the
+// tiles that some row of it sees.
 //
 // Per 128 keys: S = Q K^T (M 128, N 128) into tensor memory, the softmax warps read it,
 // keep a reference maximum that moves when a score passes it by more than 2^8 (so that O
 // is rescaled rarely), and write the weights back over S as the A operand of O += P V.
 // V is read as it lies in the cache (keys x dims) through an MN-major descriptor, so no
-// transposed copy exists. Two rings of 32 KB slots hold K and
-// V tiles.
+// transposed copy exists. Two rings of 32 KB slots hold K and V tiles.
 //   * bf16 q: weights rounded to bf16 (each off by 2^-8 of itself at most, as the
 //     result's own rounding); sums, statistics and O in f32.
 //   * f32 q: q and the weights as three bf16 parts each (24 bits; two would leave
@@ -201,7 +200,7 @@ struct Work {
   // Shared form: a team of CTAs takes the same run of keys, each member another row tile of
   // every head, so that a K/V tile comes from HBM once for all row tiles at the same moment (as
   // separate runs the row tiles of 64 sequences read a 134 MB prefix twice: 258 MB from DRAM,
-  // 68 us instead of MEASURED_TEAM). A segment with fewer row tiles leaves members idle.
+  // 68 us instead of 58). A segment with fewer row tiles leaves members idle.
   int team, member;   // (prompt form: 1, 0)
 
   QD_DEV int tpt() const { return 1 << log_tpt; }
@@ -274,6 +273,13 @@ struct Place {
   Seg a;
 };
 
+// not 0 if some of eight bf16 values is NaN or infinite: a half with all exponent bits set
+// borrows into its top bit
+QD_DEV uint32_t any_odd(const uint4& x) {
+  auto odd = [](uint32_t w) { return ((w & 0x7f807f80u) ^ 0x7f807f80u) - 0x00010001u; };
+  return (odd(x.x) | odd(x.y) | odd(x.z) | odd(x.w)) & 0x80008000u;
+}
+
 // Values of O that are not finite: what the row sees of V's own NaN and infinities in dims
 // [d0, d0 + 64) of the keys [first, last) decides (the product of a weight's part and an
 // infinity may have given NaN, or an entry was taken out of a masked tile). The row's values
@@ -288,6 +294,10 @@ __device__ __noinline__ void patch_row(const Params& p, const int32_t* pt, int g
   for (int key = first; key < last; ++key) {
     const PagedSlot sl = paged_slot(pt, key, p.page_size, p.div, p.n_pages);
     const __nv_bfloat16* v = p.v_pages + (((size_t)sl.page * p.Hkv + g) * p.page_size + sl.slot) * kD + d0;
+    uint32_t hit = 0;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) hit |= any_odd(((const uint4*)v)[c]);
+    if (!hit) continue;
 #pragma unroll 1
     for (int k = 0; k < 64; ++k) {
       const float f = __bfloat162float(v[k]);
@@ -586,209 +596,208 @@ __global__ void __launch_bounds__(kThreads, 1)
     // 384 x 168 of the launch)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     while (true) {
-    const Piece pc = piece_at(at);
-    const int g = pc.g, k0 = pc.k0, n = pc.n, seen_max = pc.seen_max, seen_min = pc.seen_min;
-    const int32_t* pt = pc.pt;
+      const Piece pc = piece_at(at);
+      const int g = pc.g, k0 = pc.k0, n = pc.n, seen_max = pc.seen_max, seen_min = pc.seen_min;
+      const int32_t* pt = pc.pt;
 
-    if (warp == kProducer || warp == kProducer + 1) {
-      // ---- K or V tiles. Each has a warp of its own, since issuing the 16 copies of a tile in
-      // 16-row pages takes some 1700 cycles. A lane's cache rows of a tile are looked up a tile
-      // ahead of their use. TMA: lane l, box l / 2 and
-      // dims 64 (l & 1); asynchronous copies: keys l, l + 32, ... (-1: past the keys)
-      constexpr int kMine = 4;
-      struct Look {
-        int row[kMine];
-      };
-      int bad_page = 0;
-      auto look = [&](int i) {
-        Look x;
-        const int key0 = (k0 + i) * kKeys;
+      if (warp == kProducer || warp == kProducer + 1) {
+        // ---- K or V tiles. Each has a warp of its own, since issuing the 16 copies of a tile in
+        // 16-row pages takes some 1700 cycles. A lane's cache rows of a tile are looked up a tile
+        // ahead of their use. TMA: lane l, box l / 2 and
+        // dims 64 (l & 1); asynchronous copies: keys l, l + 32, ... (-1: past the keys)
+        constexpr int kMine = 4;
+        struct Look {
+          int row[kMine];
+        };
+        int bad_page = 0;
+        auto look = [&](int i) {
+          Look x;
+          const int key0 = (k0 + i) * kKeys;
 #pragma unroll
-        for (int j = 0; j < kMine; ++j) {
-          const int key = p.box ? key0 + (lane >> 1) * p.box : key0 + 32 * j + lane;
-          x.row[j] = -1;
-          if (i < n && key < min(seen_max, key0 + kKeys) && (j == 0 || !p.box)) {
-            const PagedSlot sl = paged_slot(pt, key, p.page_size, p.div, p.n_pages);
-            if (!sl.ok) bad_page = 1;   // no branch on what is still being read
-            x.row[j] = (sl.page * p.Hkv + g) * p.page_size + sl.slot;
-          }
-        }
-        return x;
-      };
-      const bool is_v = warp != kProducer;
-      const CUtensorMap* map = is_v ? &tmV : &tmK;
-      const __nv_bfloat16* pages = is_v ? p.v_pages : p.k_pages;
-      const uint32_t slots = is_v ? kRingV : kRingK, slot0 = is_v ? kRingK : 0;
-      auto load = [&](const Look& x) {
-        const uint32_t slot = slot0 + rk.slot;
-        wait(&empty[slot], rk.ph ^ 1);   // (the first round's phase before the first is over)
-        rk.step(slots);
-        unsigned char* dst = data + (kQ + slot) * kSlot;
-        if (p.box) {
-          const bool go = !__any_sync(0xffffffffu, *(volatile int*)s_abort != 0);
-          const unsigned boxes = __popc(__ballot_sync(0xffffffffu, x.row[0] >= 0));   // half boxes
-          if (lane == 0) {
-            if (go && boxes) mbar_arrive_expect_tx(&full[slot], boxes * p.box * 128);
-            else mbar_arrive(&full[slot]);
-          }
-          __syncwarp();
-          if (go && x.row[0] >= 0)
-            tma_load_2d(dst + (lane & 1) * kChunk + (lane >> 1) * p.box * 128, map, (lane & 1) * 64, x.row[0], &full[slot]);
-          __syncwarp();
-        } else {
-          // 16 lanes copy one key's 256 bytes
-          const uint32_t d0 = smem_u32(dst);
-#pragma unroll
-          for (int j = 0; j < kMine; ++j)
-#pragma unroll 2
-            for (int i = 0; i < 32; i += 2) {
-              const int r = i + (lane >> 4), c = lane & 15;
-              const int row = __shfl_sync(0xffffffffu, x.row[j], r);
-              cp16(d0 + (c >> 3) * kChunk + tc::sw128_off(32 * j + r, c & 7),
-                   pages + (long long)max(row, 0) * kD + c * 8, row < 0 ? 0 : 16);
+          for (int j = 0; j < kMine; ++j) {
+            const int key = p.box ? key0 + (lane >> 1) * p.box : key0 + 32 * j + lane;
+            x.row[j] = -1;
+            if (i < n && key < min(seen_max, key0 + kKeys) && (j == 0 || !p.box)) {
+              const PagedSlot sl = paged_slot(pt, key, p.page_size, p.div, p.n_pages);
+              if (!sl.ok) bad_page = 1;   // no branch on what is still being read
+              x.row[j] = (sl.page * p.Hkv + g) * p.page_size + sl.slot;
             }
-          asm volatile("cp.async.commit_group;" ::: "memory");
-          if (late >= 0) {   // the entry before this one
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-            fence_proxy_async_smem();
-            mbar_arrive(&full[late]);
           }
-          late = (int)slot;
-        }
-      };
-      Look now = {}, next = {};
+          return x;
+        };
+        const bool is_v = warp != kProducer;
+        const CUtensorMap* map = is_v ? &tmV : &tmK;
+        const __nv_bfloat16* pages = is_v ? p.v_pages : p.k_pages;
+        const uint32_t slots = is_v ? kRingV : kRingK, slot0 = is_v ? kRingK : 0;
+        auto load = [&](const Look& x) {
+          const uint32_t slot = slot0 + rk.slot;
+          wait(&empty[slot], rk.ph ^ 1);   // (the first round's phase before the first is over)
+          rk.step(slots);
+          unsigned char* dst = data + (kQ + slot) * kSlot;
+          if (p.box) {
+            const bool go = !__any_sync(0xffffffffu, *(volatile int*)s_abort != 0);
+            const unsigned boxes = __popc(__ballot_sync(0xffffffffu, x.row[0] >= 0));   // half boxes
+            if (lane == 0) {
+              if (go && boxes) mbar_arrive_expect_tx(&full[slot], boxes * p.box * 128);
+              else mbar_arrive(&full[slot]);
+            }
+            __syncwarp();
+            if (go && x.row[0] >= 0)
+              tma_load_2d(dst + (lane & 1) * kChunk + (lane >> 1) * p.box * 128, map, (lane & 1) * 64, x.row[0],
+                          &full[slot]);
+            __syncwarp();
+          } else {
+            // 16 lanes copy one key's 256 bytes
+            const uint32_t d0 = smem_u32(dst);
+#pragma unroll
+            for (int j = 0; j < kMine; ++j)
+#pragma unroll 2
+              for (int i = 0; i < 32; i += 2) {
+                const int r = i + (lane >> 4), c = lane & 15;
+                const int row = __shfl_sync(0xffffffffu, x.row[j], r);
+                cp16(d0 + (c >> 3) * kChunk + tc::sw128_off(32 * j + r, c & 7),
+                     pages + (long long)max(row, 0) * kD + c * 8, row < 0 ? 0 : 16);
+              }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            if (late >= 0) {   // the entry before this one
+              asm volatile("cp.async.wait_group 1;" ::: "memory");
+              fence_proxy_async_smem();
+              mbar_arrive(&full[late]);
+            }
+            late = (int)slot;
+          }
+        };
+        Look now = {}, next = {};
 #pragma unroll 1
-      for (int i = -1; i < n; ++i) {
-        now = next;
-        next = look(i + 1);
-        if (i >= 0) load(now);
-      }
-      if (late >= 0) {
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        fence_proxy_async_smem();
-        mbar_arrive(&full[late]);
-        late = -1;
-      }
-      if (bad_page) set_error(p.err, QD_DEVERR_PAGE);
-    } else if (warp == kFixer) {
-      // ---- V tiles that some row must not see whole: rows past everybody's keys to zero,
-      // NaN and infinities in the others taken out
-      // (the issuer says when: a slot's own barrier may be several phases behind a tile that is
-      // still to come, which a wait on its parity cannot tell)
-      for (int i = 0; i < n; ++i) {
-        const int key0 = (k0 + i) * kKeys;
-        if (key0 + kKeys > seen_min) {
-          const uint32_t slot = kRingK + (tile + i) % kRingV;
-          wait(v_go, fixes++ & 1);
-          wait(&full[slot], ((tile + i) / kRingV) & 1);   // done; orders the copy before this thread's reads
-          unsigned char* v = data + (kQ + slot) * kSlot;
-          const int lo = max(0, seen_min - key0), hi = seen_max - key0;
-          // lane: 16-byte piece c of every second key, four cells at a time
-          constexpr int kStep = 2;
-          const int ft = tid - 32 * kFixer, c = ft & 15;
-          unsigned char* col = v + (c >> 3) * kChunk;
-          const int split = min(hi, kKeys);
-          int key = lo + (ft >> 4);
-          for (; key < split; key += 4 * kStep) {
-            uint4 x[4];
+        for (int i = -1; i < n; ++i) {
+          now = next;
+          next = look(i + 1);
+          if (i >= 0) load(now);
+        }
+        if (late >= 0) {
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
+          fence_proxy_async_smem();
+          mbar_arrive(&full[late]);
+          late = -1;
+        }
+        if (bad_page) set_error(p.err, QD_DEVERR_PAGE);
+      } else if (warp == kFixer) {
+        // ---- V tiles that some row must not see whole: rows past everybody's keys to zero,
+        // NaN and infinities in the others taken out
+        // (the issuer says when: a slot's own barrier may be several phases behind a tile that is
+        // still to come, which a wait on its parity cannot tell)
+        for (int i = 0; i < n; ++i) {
+          const int key0 = (k0 + i) * kKeys;
+          if (key0 + kKeys > seen_min) {
+            const uint32_t slot = kRingK + (tile + i) % kRingV;
+            wait(v_go, fixes++ & 1);
+            wait(&full[slot], ((tile + i) / kRingV) & 1);   // done; orders the copy before this thread's reads
+            unsigned char* v = data + (kQ + slot) * kSlot;
+            const int lo = max(0, seen_min - key0), hi = seen_max - key0;
+            // lane: 16-byte piece c of every second key, four cells at a time
+            constexpr int kStep = 2;
+            const int ft = tid - 32 * kFixer, c = ft & 15;
+            unsigned char* col = v + (c >> 3) * kChunk;
+            const int split = min(hi, kKeys);
+            int key = lo + (ft >> 4);
+            for (; key < split; key += 4 * kStep) {
+              uint4 x[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (key + kStep * j < split) x[j] = *(const uint4*)(col + tc::sw128_off(key + kStep * j, c & 7));
+              for (int j = 0; j < 4; ++j)
+                if (key + kStep * j < split) x[j] = *(const uint4*)(col + tc::sw128_off(key + kStep * j, c & 7));
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (key + kStep * j >= split) break;
-              // a half with all exponent bits set borrows into its top bit
-              auto odd = [](uint32_t w) { return ((w & 0x7f807f80u) ^ 0x7f807f80u) - 0x00010001u; };
-              if ((odd(x[j].x) | odd(x[j].y) | odd(x[j].z) | odd(x[j].w)) & 0x80008000u) {
-                uint32_t h[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+              for (int j = 0; j < 4; ++j) {
+                if (key + kStep * j >= split) break;
+                if (any_odd(x[j])) {
+                  uint32_t h[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  if ((h[k] & 0x7f80u) == 0x7f80u) h[k] &= 0xffff0000u;
-                  if ((h[k] & 0x7f800000u) == 0x7f800000u) h[k] &= 0xffffu;
+                  for (int k = 0; k < 4; ++k) {
+                    if ((h[k] & 0x7f80u) == 0x7f80u) h[k] &= 0xffff0000u;
+                    if ((h[k] & 0x7f800000u) == 0x7f800000u) h[k] &= 0xffffu;
+                  }
+                  *(uint4*)(col + tc::sw128_off(key + kStep * j, c & 7)) = make_uint4(h[0], h[1], h[2], h[3]);
+                  *(volatile int*)(s_patch + (piece_no & 1)) = (int)piece_no + 1;
                 }
-                *(uint4*)(col + tc::sw128_off(key + kStep * j, c & 7)) = make_uint4(h[0], h[1], h[2], h[3]);
-                *(volatile int*)(s_patch + (piece_no & 1)) = (int)piece_no + 1;
               }
             }
+            for (key = max(lo, max(hi, 0)) + (ft >> 4); key < kKeys; key += kStep)
+              *(uint4*)(col + tc::sw128_off(key, c & 7)) = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+            mbar_arrive(v_fixed);
           }
-          for (key = max(lo, max(hi, 0)) + (ft >> 4); key < kKeys; key += kStep)
-            *(uint4*)(col + tc::sw128_off(key, c & 7)) = make_uint4(0u, 0u, 0u, 0u);
-          fence_proxy_async_smem();
-          mbar_arrive(v_fixed);
+        }
+      } else {
+        // ---- the products: S runs two tiles ahead of P V. What this warp does between two
+        // products is time the tensor cores may idle (a tcgen05 instruction takes it 50 cycles or
+        // more), so waits that are usually over come early and slots are counted, not divided.
+        const bool lead = lane == 0;
+        const uint64_t dq = tc::desc_sw128(smem_u32(data));
+        const uint32_t ring0 = smem_u32(data) + kQ * kSlot;
+        // S into buffer b from a K tile; small parts first
+        auto mma_s = [&](int b) {
+          const uint64_t dk = tc::desc_sw128(ring0 + rk.slot * kSlot);
+#pragma unroll 1
+          for (int part = PARTS - 1; part >= 0; --part) {
+            const uint64_t da = dq + (uint64_t)(part * kSlot >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              constexpr int kHalf = kChunk >> 4;
+              const uint64_t o = (kk >> 2) * kHalf + (kk & 3) * 2;
+              mma_qk(lead, tS + 128 * b, da + o, dk + o, kk != 0 || part != PARTS - 1);
+            }
+          }
+          commit(lead, &s_full[b]);
+          commit(lead, &empty[rk.slot]);
+          rk.step(kRingK);
+        };
+        auto mma_o = [&](int b, bool first) {
+          const uint64_t dv = desc_v(ring0 + (kRingK + rv.slot) * kSlot);
+#pragma unroll 1
+          for (int part = PARTS - 1; part >= 0; --part) {
+            // 32 keys' weights over their own 32 scores
+            const uint32_t ta = part < 2 ? tS + 128 * b + 16 * part : tX + 64 * b;
+            const uint32_t t32 = part < 2 ? 32 : 16;
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              mma_pv(lead, tO, ta + t32 * (kk >> 1) + 8 * (kk & 1), dv + (uint64_t)(kk * 2048 >> 4),
+                     kk != 0 || part != PARTS - 1 || !first);
+          }
+          commit(lead, &o_done[b]);
+          commit(lead, &empty[kRingK + rv.slot]);
+          rv.step(kRingV);
+        };
+        wait(q_full, piece_no & 1);
+#pragma unroll 1
+        for (int i = -2; i < n; ++i) {
+          if (i >= 0) {
+            const uint32_t ct = tile + i;
+            wait(&full[kRingK + rv.slot], rv.ph);
+            if ((k0 + i + 1) * kKeys > seen_min) {
+              if (lead) mbar_arrive(v_go);
+              wait(v_fixed, fixes++ & 1);
+            }
+            wait(&p_full[ct & 1], (ct >> 1) & 1);
+            tc::fence_after();
+            mma_o(ct & 1, kFresh || i == 0);
+          }
+          if (i + 2 < n) {
+            wait(&full[rk.slot], rk.ph);
+            mma_s((tile + i + 2) & 1);
+          }
         }
       }
-    } else {
-      // ---- the products: S runs two tiles ahead of P V. What this warp does between two products is time the tensor cores may idle (a
-      // tcgen05 instruction takes it 50 cycles or more), so waits that are usually over come
-      // early and slots are counted, not divided.
-      const bool lead = lane == 0;
-      const uint64_t dq = tc::desc_sw128(smem_u32(data));
-      const uint32_t ring0 = smem_u32(data) + kQ * kSlot;
-      // S into buffer b from a K tile; small parts first
-      auto mma_s = [&](int b) {
-        const uint64_t dk = tc::desc_sw128(ring0 + rk.slot * kSlot);
-#pragma unroll 1
-        for (int part = PARTS - 1; part >= 0; --part) {
-          const uint64_t da = dq + (uint64_t)(part * kSlot >> 4);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            constexpr int kHalf = kChunk >> 4;
-            const uint64_t o = (kk >> 2) * kHalf + (kk & 3) * 2;
-            mma_qk(lead, tS + 128 * b, da + o, dk + o, kk != 0 || part != PARTS - 1);
-          }
-        }
-        commit(lead, &s_full[b]);
-        commit(lead, &empty[rk.slot]);
-        rk.step(kRingK);
-      };
-      auto mma_o = [&](int b, bool first) {
-        const uint64_t dv = desc_v(ring0 + (kRingK + rv.slot) * kSlot);
-#pragma unroll 1
-        for (int part = PARTS - 1; part >= 0; --part) {
-          // 32 keys' weights over their own 32 scores
-          const uint32_t ta = part < 2 ? tS + 128 * b + 16 * part : tX + 64 * b;
-          const uint32_t t32 = part < 2 ? 32 : 16;
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_pv(lead, tO, ta + t32 * (kk >> 1) + 8 * (kk & 1), dv + (uint64_t)(kk * 2048 >> 4),
-                   kk != 0 || part != PARTS - 1 || !first);
-        }
-        commit(lead, &o_done[b]);
-        commit(lead, &empty[kRingK + rv.slot]);
-        rv.step(kRingV);
-      };
-      wait(q_full, piece_no & 1);
-#pragma unroll 1
-      for (int i = -2; i < n; ++i) {
-        if (i >= 0) {
-          const uint32_t ct = tile + i;
-          wait(&full[kRingK + rv.slot], rv.ph);
-          if ((k0 + i + 1) * kKeys > seen_min) {
-            if (lead) mbar_arrive(v_go);
-            wait(v_fixed, fixes++ & 1);
-          }
-          wait(&p_full[ct & 1], (ct >> 1) & 1);
-          tc::fence_after();
-          mma_o(ct & 1, kFresh || i == 0);
-        }
-        if (i + 2 < n) {
-          wait(&full[rk.slot], rk.ph);
-          mma_s((tile + i + 2) & 1);
-        }
-      }
-    }
-    tile += n;
-    ++piece_no;
-    if (!next_place(at, u, n)) break;
+      tile += n;
+      ++piece_no;
+      if (!next_place(at, u, n)) break;
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     while (true) {
-    const Piece pc = piece_at(at);
-    const Seg& a = at.a;
-    const int g = pc.g, t = pc.t, k0 = pc.k0, k1 = pc.k1, nk = pc.nk, n = pc.n;
-    const int first_row = pc.first_row, packed = pc.packed;
-    const int32_t* pt = pc.pt;
+      const Piece pc = piece_at(at);
+      const Seg& a = at.a;
+      const int g = pc.g, t = pc.t, k0 = pc.k0, k1 = pc.k1, nk = pc.nk, n = pc.n;
+      const int first_row = pc.first_row, packed = pc.packed;
+      const int32_t* pt = pc.pt;
       // ---- softmax: warps w and w + 4 hold the same rows (TMEM lanes), 64 keys and 64 O columns
       // each
       const int hf = warp >> 2, row = (warp & 3) * 32 + lane;
@@ -824,13 +833,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const int r = warp * 16 + i0 + i;
-              f[i] = r < qrows ? *(const float4*)(q + (long long)(r >> p.log_rep) * p.q_stride + (r & (p.rep - 1)) * kD + 4 * lane)
-                               : make_float4(0.f, 0.f, 0.f, 0.f);
+              const T* from = q + (long long)(r >> p.log_rep) * p.q_stride + (r & (p.rep - 1)) * kD + 4 * lane;
+              f[i] = r < qrows ? *(const float4*)from : make_float4(0.f, 0.f, 0.f, 0.f);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const uint32_t o = (uint32_t)((lane >> 4) * kChunk) + tc::sw128_off(warp * 16 + i0 + i, (lane & 15) >> 1) +
-                                 (uint32_t)((lane & 1) * 8);
+              const uint32_t o = (uint32_t)((lane >> 4) * kChunk + (lane & 1) * 8) +
+                                 tc::sw128_off(warp * 16 + i0 + i, (lane & 15) >> 1);
               float x4[4] = {f[i].x * p.q_sign, f[i].y * p.q_sign, f[i].z * p.q_sign, f[i].w * p.q_sign};
 #pragma unroll
               for (int part = 0; part < PARTS; ++part) {
@@ -1086,7 +1095,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (PARTS == 3 || (valid && !dead)) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            *(float4*)(mine + ((((col0 + e) / 4 + k) ^ xr) << 4)) = make_float4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
+            *(float4*)(mine + ((((col0 + e) / 4 + k) ^ xr) << 4)) =
+                make_float4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
         }
       }
       if ((patch || z != 0.f) && valid && !dead && l == l)
@@ -1196,7 +1206,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   *(uint2*)((__nv_bfloat16*)p.out + o) =
                       make_uint2(bf2(acc[j].x * iv, acc[j].y * iv), bf2(acc[j].z * iv, acc[j].w * iv));
                 else
-                  *(float4*)((float*)p.out + o) = make_float4(acc[j].x * iv, acc[j].y * iv, acc[j].z * iv, acc[j].w * iv);
+                  *(float4*)((float*)p.out + o) =
+                      make_float4(acc[j].x * iv, acc[j].y * iv, acc[j].z * iv, acc[j].w * iv);
               }
             }
             bar_sync(6, kSoft);
@@ -1210,11 +1221,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         q_load(nx);
         q_ready();
       }
-    tile += n;
-    ++piece_no;
-    if (!more) break;
-    at = nx;
-    u = nx_u;
+      tile += n;
+      ++piece_no;
+      if (!more) break;
+      at = nx;
+      u = nx_u;
     }
   }
   __syncwarp();

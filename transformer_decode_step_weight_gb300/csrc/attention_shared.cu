@@ -413,7 +413,8 @@ __global__ void __launch_bounds__(kTh, 3) attn_suffix_kernel(const __grid_consta
       l = p.pre_l + head0;
     } else {
       const int i = k - n_own;
-      const float* piece = p.pieces.base + ((size_t)(from.first + i * from.stride) * 2 + (i == 0 ? 1 : 0)) * kPieceFloats;
+      const float* piece =
+          p.pieces.base + ((size_t)(from.first + i * from.stride) * 2 + (i == 0 ? 1 : 0)) * kPieceFloats;
       O = piece + (size_t)from.row * kD;
       m = piece + (size_t)kPieceRows * kD + from.row;
       l = m + kPieceRows;
@@ -476,7 +477,7 @@ int splits(int B, int Hkv) {
 // 8192 34.7 and 36.2 (f32). QD_SHARED_MIN_MB (read per call) sets another limit.
 long long share_min(int Hkv) {
   const char* v = getenv("QD_SHARED_MIN_MB");
-  return (v ? std::max(0LL, atoll(v)) : 80) * 1000000 / ((long long)Hkv * 2 * kD * 2);
+  return (v ? std::max(0LL, std::min(atoll(v), 1000000000LL)) : 80) * 1000000 / ((long long)Hkv * 2 * kD * 2);
 }
 
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }

@@ -356,8 +356,8 @@ cudaError_t copy_pairs(const PageCopy& pc, const int32_t* src, const int32_t* ds
     const long long items = n_dev ? fill : (long long)n * 2 * nl * per_page;
     Launch Lc = L;
     Lc.pdl = l0 == 0 && L.pdl;
-    cudaError_t e = launch_ex(pages_copy_kernel, dim3((unsigned)std::min(items, fill)), dim3(kCopyTh), 0, Lc, pk, 2 * nl,
-                              src, dst, n, n_dev, n_pages, (long long)pc.page_bytes, L.err);
+    cudaError_t e = launch_ex(pages_copy_kernel, dim3((unsigned)std::min(items, fill)), dim3(kCopyTh), 0, Lc, pk,
+                              2 * nl, src, dst, n, n_dev, n_pages, (long long)pc.page_bytes, L.err);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -386,7 +386,8 @@ cudaError_t launch_pages_extend(const PageState& c, const PageCopy& pc, const in
   const Ws ws = ws_of(c, workspace);
   Launch first = L;
   first.pdl = false;
-  cudaError_t e = launch_ex(pages_extend_kernel, dim3(1), dim3(kPlan), (size_t)c.max_seqs * 12, first, c, ws, n_new, L.err);
+  cudaError_t e =
+      launch_ex(pages_extend_kernel, dim3(1), dim3(kPlan), (size_t)c.max_seqs * 12, first, c, ws, n_new, L.err);
   if (e != cudaSuccess) return e;
   return copy_pairs(pc, ws.src, ws.dst, 0, ws.head + 1, c.n_pages, L);
 }

@@ -203,7 +203,9 @@ __global__ void __launch_bounds__(kTh) verify_sample_kernel(const __grid_constan
       }
       if (lane == 0) {
         s_chunk = hit >= 0 ? hit : some;
-        s_want = border - (hit >= 0 ? b_hit : b_some);
+        // (not below 0: the scan adds in another order for each chunk, so the sum before one
+        // may pass the border by a rounding without the chunk before it having done so)
+        s_want = fmax(0.0, border - (hit >= 0 ? b_hit : b_some));
       }
     }
     __syncthreads();
