@@ -108,6 +108,27 @@ def test_prompt_attention(cuda_lib, rows, lens, hq, hkv, ps, dtype):
     assert api.check_device_error() == 0
 
 
+@pytest.mark.parametrize("seed,hq,hkv,ps,n", [(0, 8, 1, 24, 60), (1, 4, 4, 7, 60), (2, 32, 8, 16, 16), (3, 16, 2, 64, 7),
+                                              (4, 8, 8, 16, 40), (5, 8, 2, 128, 3), (6, 8, 4, 32, 1)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_prompt_attention_ragged_batches_again_and_again(cuda_lib, seed, hq, hkv, ps, n, dtype):
+    # row tiles of every length one after another in a CTA, whole and in pieces; the same bits each time
+    g, r = _gen(60 + seed), np.random.default_rng(seed)
+    lens = [int(x) for x in 2 ** r.uniform(0, 12.5, n)]
+    rows = [min(m, int(x)) for m, x in zip(lens, 2 ** r.uniform(0, 11, n))]
+    kp, vp, pt = _cache(g, lens, hkv, ps)
+    cu, seqs, seen = _pack(rows, lens)
+    q = (torch.randn((cu[-1], hq, D), generator=g, device=DEV) * (10 if seed % 3 == 0 else 1)).to(dtype)
+    args = (q, kp, vp, pt, _ints(cu), _ints(lens), SCALE)
+    ws = torch.zeros(api.attn_prompt_workspace_bytes(), dtype=torch.uint8, device=DEV)
+    first = api.attn_prompt(*args, workspace=ws)
+    for _ in range(12):
+        assert torch.equal(first, api.attn_prompt(*args, workspace=ws))
+    pick = sorted(r.choice(cu[-1], min(60, cu[-1]), replace=False).tolist())
+    _check_rows(first, q, kp, vp, pt, seqs, seen, pick)
+    assert api.check_device_error() == 0
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_prompt_attention_leaves_other_rows_and_takes_strided_q(cuda_lib, dtype):
     g = _gen(5)

@@ -20,13 +20,16 @@
 //   * f32 q: q and the weights as three bf16 parts each (24 bits; two would leave
 //     2.4e-6 of each weight, above what an f32 sum of the same length loses), three times
 //     the products.
-// Each row is held by two threads, which take 64 of the 128 keys each and trade maxima. S is
-// double-buffered and runs two tiles ahead, so the products of one tile cover the softmax of
-// the next; the one lane that issues them is what bounds a long prompt (each tcgen05
-// instruction takes it 50 cycles and more, and 16 products of 64 cycles are a tile).
-// Two row tiles per CTA with one thread per row and S once per row tile, which halves the
-// K/V reads, measured slower: 643 against 623 us at 8192 tokens, since every product then
-// waits for a whole softmax.
+// A row is held by two threads, one in each half of the softmax warps. bf16: they take whole
+// tiles in turn, S runs three tiles ahead of P V in three buffers, each product has a warp that
+// issues it, and while one half writes a row tile out the other begins the next. What bounds a
+// long prompt is then about even: 1024 cycles of products and as many of exponentials per tile,
+// some 1500 in all; 8192 tokens of 32 q heads (8 kv heads) take 394 us, 1395 TFLOP/s. Both
+// halves on one tile, 64 keys each: 558 us; one warp for both products, whatever the softmax did:
+// 2100 cycles per tile; two row tiles per CTA, whose S has one buffer each: 643 us. Short row
+// tiles (16 messages of 20 to 300 tokens: 76 us) are bound by the start and the end of each, most
+// of which is code that the instruction cache does not hold. f32: three products for each of
+// bf16's, both halves on one tile, since O is summed in registers.
 //
 // Keys a row must not see: scores are masked by selection, and V rows that only some rows
 // of the tile see are checked for NaN and infinities (0 * NaN would reach every row):
@@ -51,10 +54,18 @@ constexpr int kChunk = 128 * 128;        // [128 rows x 64 bf16], 128-byte swizz
 constexpr int kSlot = 2 * kChunk;        // a K or V tile, or one part of a row tile of Q
 constexpr int kSoftWarps = 8;
 constexpr int kSoft = 32 * kSoftWarps;
-// warp roles behind the softmax warps: the first issues the products
+// warp roles behind the softmax warps
+constexpr int kIssueS = kSoftWarps;         // issues S = Q K^T
 constexpr int kProducer = kSoftWarps + 1;   // K tiles; the warp after it V tiles
-constexpr int kFixer = kSoftWarps + 3;
+constexpr int kIssueO = kSoftWarps + 3;     // issues O += P V
 constexpr int kThreads = 32 * (kSoftWarps + 4);
+// named barriers: 1 and 6 the threads that write a piece out, 2 + quarter the holders of a row,
+// kPassed + 4 holder + quarter: the holder has written its reference (7 to 14)
+constexpr int kPassed = 7;
+// Tiles that the half which begins a row tile takes before the two alternate: about as long as the
+// other half needs to write the row tile before out. 8192 tokens with 2, 3, 4, 5, 6, 8, 12: 453,
+// 429, 413, 398, 398, 406, 418 us.
+constexpr int kSolo = 5;
 constexpr int kMisc = 3072;              // barriers and small arrays in front of Q and the ring
 constexpr int kData = 7 * kSlot;         // 224 KB: Q parts and ring slots
 constexpr size_t kSmem = kMisc + kData;  // 227 KB, the whole opt-in shared memory
@@ -96,6 +107,7 @@ QD_DEV uint32_t bf2(float lo, float hi) {
   memcpy(&u, &v, 4);
   return u;
 }
+QD_DEV void bar_arrive(int id, int n) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 QD_DEV void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 
 // ---- tensor memory
@@ -141,14 +153,15 @@ QD_DEV uint64_t desc_v(uint32_t saddr) {
 }
 // The products are issued by one lane of a warp whose lanes all walk the same way, so that
 // descriptors stay in uniform registers; `lead` says which lane.
-QD_DEV void mma_pv(bool lead, uint32_t tmem_d, uint32_t tmem_a, uint64_t db, uint32_t accumulate) {
+// Step kk of 16 keys, left out by lanes whose `steps` it is not below.
+QD_DEV void mma_pv(int steps, int kk, uint32_t tmem_d, uint32_t tmem_a, uint64_t db, uint32_t accumulate) {
   constexpr uint32_t kIdesc = tc::idesc_m128(kD) | (1u << 16);   // B MN-major
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
+      "setp.gt.s32 q, %5, %6;\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "r"(tmem_a), "l"(db), "r"(kIdesc), "r"(accumulate), "r"((uint32_t)lead)
+      "r"(tmem_a), "l"(db), "r"(kIdesc), "r"(accumulate), "r"(steps), "r"(kk)
       : "memory");
 }
 QD_DEV void mma_qk(bool lead, uint32_t tmem_d, uint64_t da, uint64_t db, uint32_t accumulate) {
@@ -267,6 +280,13 @@ QD_DEV float max3(float a, float b, float c) {
   return d;
 }
 
+// the largest magnitude, NaN if there is one
+QD_DEV float max3_abs_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // A place in the work: row tile t of kv head g of segment s, from key tile k0 on.
 struct Place {
   int s, g, t, k0;
@@ -324,36 +344,35 @@ template <typename T, int PARTS, bool PROMPT>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ Params p) {
-  // bf16: a slot of its own for what goes out, so that Q of the next piece can be copied as
-  // soon as this one's last S is there; f32: what goes out takes Q's place
+  // bf16: two buffers of Q, so that S of the next piece follows this one's; f32: three parts of
+  // one. What goes out is gathered in the place of the Q that it was made with.
   constexpr bool kEarlyQ = PARTS == 1;
-  constexpr int kQ1 = PARTS;                  // slots of Q
-  constexpr int kQ = kQ1 + kEarlyQ;           // ... and of what goes out
+  constexpr int kQ = kEarlyQ ? 2 : PARTS;     // slots of Q
   constexpr int kRing = 7 - kQ;
-  constexpr int kCols = 64;                   // keys of a tile, and O columns, per softmax thread
+  constexpr int kCols = 64;                   // O columns per softmax thread
   constexpr bool kFresh = PARTS == 3;         // O of each tile alone in TMEM, summed in registers
+  constexpr int kBufs = kFresh ? 2 : 3;       // buffers of S: how many tiles it runs ahead of P V
   constexpr int kRingV = kRing > 4 ? 3 : 2, kRingK = kRing - kRingV;   // K slots, then V slots
   static_assert(kRingK >= 2 && kRing <= kMaxSlots, "");
   extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char* data = smem + kMisc;
   uint64_t* full = (uint64_t*)smem;      // [kRing] a K or V tile landed
   uint64_t* empty = full + kMaxSlots;    // [kRing] its products are done
-  uint64_t* s_full = empty + kMaxSlots;  // [2] S in buffer b
-  uint64_t* p_full = s_full + 2;         // [2] the weights in buffer b, O rescaled
-  uint64_t* o_done = p_full + 2;         // [2] the P V products of buffer b done
-  uint64_t* q_full = o_done + 2;         // Q of a piece
-  uint64_t* v_go = q_full + 1;           // a masked V tile landed (the issuer saw it)
-  uint64_t* v_fixed = v_go + 1;          // ... and was put right
-  uint64_t* drained = v_fixed + 1;       // after a timeout: the products issued so far are done
-  uint32_t* tslot = (uint32_t*)(drained + 1);
+  uint64_t* s_full = empty + kMaxSlots;  // [kBufs] S in buffer b
+  uint64_t* p_full = s_full + kBufs;     // [kBufs] the weights in buffer b, O rescaled
+  uint64_t* o_done = p_full + kBufs;     // [kBufs] the P V products of buffer b done
+  uint64_t* o_free = o_done + kBufs;     // O of a piece has been read
+  uint64_t* q_full = o_free + 1;         // [2] Q of a piece (f32: [0])
+  uint64_t* drained = q_full + 2;        // [2] after a timeout: an issuer's products so far are done
+  uint32_t* tslot = (uint32_t*)(drained + 2);
   int* s_abort = (int*)(tslot + 1);
   int* s_patch = s_abort + 1;            // [2] the last piece with NaN or infinities in a masked V tile
-  int* s_last = s_patch + 2;
+  int* s_last = s_patch + 2;             // [2]
   long long* s_find = (long long*)(smem + 256);   // [0] segment, [1] unit within it, [2] the split
   long long* s_scan = (long long*)(smem + 320);   // [warps] sums of the scan
   int* s_most = (int*)(smem + 448);               // [warps] most row tiles of a segment
   long long* s_saved = (long long*)(smem + 512);  // [warps]
-  float* xm = (float*)(smem + 512);               // [2][2][128] traded maxima and sums
+  float* xm = (float*)(smem + 512);               // f32: [2][2][128] traded maxima and sums; bf16: [2][128] each
 
   // the warp's number from one lane: the roles' branches are then known to be taken by whole
   // warps, and the issuers' descriptors can stay in uniform registers
@@ -460,16 +479,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&full[i], p.box ? 1 : 32);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kBufs; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], kSoft);
+      mbar_init(&p_full[i], kFresh ? kSoft : kSoft / 2);
       mbar_init(&o_done[i], 1);
-      s_patch[i] = 0;
     }
-    mbar_init(q_full, kSoft);
-    mbar_init(v_go, 1);
-    mbar_init(drained, 1);
-    mbar_init(v_fixed, 32);
+    s_patch[0] = s_patch[1] = 0;
+    mbar_init(o_free, kSoft / 2);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], kEarlyQ ? kSoft / 2 : kSoft);
+      mbar_init(&drained[i], 1);
+    }
     fence_mbar_init();
   }
   if (warp == 0) tc::alloc(tslot, 512);
@@ -477,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after();
   const uint32_t tb = *tslot;
-  const uint32_t tS = tb, tO = tb + 256, tX = tb + 384;
+  const uint32_t tS = tb, tO = tb + 128 * kBufs, tX = tb + 384;   // (tX: f32 only)
   const Split sp = {(uint32_t)(s_find[2] >> 32), (uint32_t)s_find[2]};
   const uint32_t u1 = sp.first(run_no + 1);
   uint32_t u = sp.first(run_no);
@@ -532,10 +552,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   // A piece is the part of one row tile that this CTA computes. Each role walks the pieces for
   // itself, so the copies and products of one run into the next; counts that several roles
-  // follow: tiles, fixed tiles, trades, pieces.
-  uint32_t tile = 0, fixes = 0, trades = 0, piece_no = 0;
+  // follow: tiles, trades, pieces.
+  uint32_t tile = 0, piece_no = 0;
+  [[maybe_unused]] uint32_t trades = 0;
+  [[maybe_unused]] int begins = 0;   // bf16: the holder of the piece's first tile
+  [[maybe_unused]] bool behind = false;
   int late = -1;
-  // position and phase in a ring (the issuer walks both)
+  // position and phase in a ring
   struct Ring {
     uint32_t slot, ph;
     QD_DEV void step(uint32_t n) {
@@ -545,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   };
-  Ring rk = {0, 0}, rv = {0, 0};
+  Ring rk = {0, 0}, rb = {0, 0};   // K or V slots, buffers of S
   [[maybe_unused]] bool first = true;
 
   struct Piece {
@@ -681,109 +704,102 @@ __global__ void __launch_bounds__(kThreads, 1)
           late = -1;
         }
         if (bad_page) set_error(p.err, QD_DEVERR_PAGE);
-      } else if (warp == kFixer) {
-        // ---- V tiles that some row must not see whole: rows past everybody's keys to zero,
-        // NaN and infinities in the others taken out
-        // (the issuer says when: a slot's own barrier may be several phases behind a tile that is
-        // still to come, which a wait on its parity cannot tell)
-        for (int i = 0; i < n; ++i) {
-          const int key0 = (k0 + i) * kKeys;
-          if (key0 + kKeys > seen_min) {
-            const uint32_t slot = kRingK + (tile + i) % kRingV;
-            wait(v_go, fixes++ & 1);
-            wait(&full[slot], ((tile + i) / kRingV) & 1);   // done; orders the copy before this thread's reads
-            unsigned char* v = data + (kQ + slot) * kSlot;
-            const int lo = max(0, seen_min - key0), hi = seen_max - key0;
-            // lane: 16-byte piece c of every second key, four cells at a time
-            constexpr int kStep = 2;
-            const int ft = tid - 32 * kFixer, c = ft & 15;
-            unsigned char* col = v + (c >> 3) * kChunk;
-            const int split = min(hi, kKeys);
-            int key = lo + (ft >> 4);
-            for (; key < split; key += 4 * kStep) {
-              uint4 x[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                if (key + kStep * j < split) x[j] = *(const uint4*)(col + tc::sw128_off(key + kStep * j, c & 7));
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                if (key + kStep * j >= split) break;
-                if (any_odd(x[j])) {
-                  uint32_t h[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    if ((h[k] & 0x7f80u) == 0x7f80u) h[k] &= 0xffff0000u;
-                    if ((h[k] & 0x7f800000u) == 0x7f800000u) h[k] &= 0xffffu;
-                  }
-                  *(uint4*)(col + tc::sw128_off(key + kStep * j, c & 7)) = make_uint4(h[0], h[1], h[2], h[3]);
-                  *(volatile int*)(s_patch + (piece_no & 1)) = (int)piece_no + 1;
-                }
-              }
-            }
-            for (key = max(lo, max(hi, 0)) + (ft >> 4); key < kKeys; key += kStep)
-              *(uint4*)(col + tc::sw128_off(key, c & 7)) = make_uint4(0u, 0u, 0u, 0u);
-            fence_proxy_async_smem();
-            mbar_arrive(v_fixed);
-          }
-        }
-      } else {
-        // ---- the products: S runs two tiles ahead of P V. What this warp does between two
-        // products is time the tensor cores may idle (a tcgen05 instruction takes it 50 cycles or
-        // more), so waits that are usually over come early and slots are counted, not divided.
+      } else if (warp == kIssueS) {
+        // ---- S, up to kBufs tiles ahead of P V. The two products have a warp each, since what
+        // a warp does between them is time the tensor cores idle: a product of 64 cycles takes
+        // 58 to issue, and the waits and commits of a tile some 150 each (one warp for both: 2100
+        // cycles a tile, whatever the softmax and the loads did). Slots are counted, not divided.
         const bool lead = lane == 0;
-        const uint64_t dq = tc::desc_sw128(smem_u32(data));
+        const uint32_t qb = kEarlyQ ? piece_no & 1 : 0;
+        const uint64_t dq = tc::desc_sw128(smem_u32(data) + qb * kSlot);
         const uint32_t ring0 = smem_u32(data) + kQ * kSlot;
-        // S into buffer b from a K tile; small parts first
-        auto mma_s = [&](int b) {
-          const uint64_t dk = tc::desc_sw128(ring0 + rk.slot * kSlot);
+        wait(&q_full[qb], (kEarlyQ ? piece_no >> 1 : piece_no) & 1);
 #pragma unroll 1
-          for (int part = PARTS - 1; part >= 0; --part) {
+        for (int i = 0; i < n; ++i) {
+          wait(&full[rk.slot], rk.ph);
+          wait(&o_done[rb.slot], rb.ph ^ 1);   // the products that read the buffer (none in the first round)
+          tc::fence_after();
+          const uint64_t dk = tc::desc_sw128(ring0 + rk.slot * kSlot);
+          const uint32_t ts = tS + 128 * rb.slot;
+#pragma unroll 1
+          for (int part = PARTS - 1; part >= 0; --part) {   // small parts first
             const uint64_t da = dq + (uint64_t)(part * kSlot >> 4);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
               constexpr int kHalf = kChunk >> 4;
               const uint64_t o = (kk >> 2) * kHalf + (kk & 3) * 2;
-              mma_qk(lead, tS + 128 * b, da + o, dk + o, kk != 0 || part != PARTS - 1);
+              mma_qk(lead, ts, da + o, dk + o, kk != 0 || part != PARTS - 1);
             }
           }
-          commit(lead, &s_full[b]);
+          commit(lead, &s_full[rb.slot]);
           commit(lead, &empty[rk.slot]);
           rk.step(kRingK);
-        };
-        auto mma_o = [&](int b, bool first) {
-          const uint64_t dv = desc_v(ring0 + (kRingK + rv.slot) * kSlot);
+          rb.step(kBufs);
+        }
+      } else {
+        // ---- O += P V
+        const bool lead = lane == 0;
+        const uint32_t ring0 = smem_u32(data) + (kQ + kRingK) * kSlot;
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+          const uint32_t slot = kRingK + rk.slot;
+          wait(&full[slot], rk.ph);
+          const int key0 = (k0 + i) * kKeys;
+          int steps = kKeys / 16;   // of 16 keys that some row sees
+          if (key0 + kKeys > seen_min) {
+            // a V tile that some row must not see whole: NaN and infinities taken out, rows past
+            // everybody's keys to zero up to the last step's end
+            const int lo = max(0, seen_min - key0), hi = min(seen_max - key0, kKeys);
+            steps = max(1, (hi + 15) >> 4);
+            // lane: of key lane / 4 in a group of 8, 16-byte pieces lane & 3, + 4, + 8, + 12
+            const int sub = lane >> 2, cc = lane & 3;
+            unsigned char* v = data + (kQ + slot) * kSlot + sub * 128;
+            const int o4[4] = {(cc ^ sub) << 4, ((cc + 4) ^ sub) << 4, kChunk + ((cc ^ sub) << 4),
+                               kChunk + (((cc + 4) ^ sub) << 4)};
+#pragma unroll 1
+            for (int key = (lo & ~7) + sub; key < steps * 16; key += 8) {
+              unsigned char* cell = v + (key >> 3) * 1024;
+              if (key >= hi) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) *(uint4*)(cell + o4[j]) = make_uint4(0u, 0u, 0u, 0u);
+              } else if (key >= lo) {
+                uint4 x[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = *(const uint4*)(cell + o4[j]);
+                if (!(any_odd(x[0]) | any_odd(x[1]) | any_odd(x[2]) | any_odd(x[3]))) continue;
+                *(volatile int*)(s_patch + (piece_no & 1)) = (int)piece_no + 1;
+#pragma unroll 1
+                for (int j = 0; j < 32; ++j) {
+                  const int c = ((cc + 4 * ((j >> 3) & 1)) ^ sub) << 4;
+                  unsigned short* h = (unsigned short*)(cell + (j >> 4) * kChunk + c) + (j & 7);
+                  if ((*h & 0x7f80u) == 0x7f80u) *h = 0;
+                }
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          // O of the piece before has been read by everybody (f32: p_full says so)
+          if (!kFresh && i == 0 && piece_no) wait(o_free, (piece_no - 1) & 1);
+          wait(&p_full[rb.slot], rb.ph);
+          tc::fence_after();
+          const uint64_t dv = desc_v(ring0 + rk.slot * kSlot);
+          const bool first = kFresh || i == 0;
+          const int go = lead ? steps : 0;
 #pragma unroll 1
           for (int part = PARTS - 1; part >= 0; --part) {
             // 32 keys' weights over their own 32 scores
-            const uint32_t ta = part < 2 ? tS + 128 * b + 16 * part : tX + 64 * b;
+            const uint32_t ta = part < 2 ? tS + 128 * rb.slot + 16 * part : tX + 64 * rb.slot;
             const uint32_t t32 = part < 2 ? 32 : 16;
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              mma_pv(lead, tO, ta + t32 * (kk >> 1) + 8 * (kk & 1), dv + (uint64_t)(kk * 2048 >> 4),
+              mma_pv(go, kk, tO, ta + t32 * (kk >> 1) + 8 * (kk & 1), dv + (uint64_t)(kk * 2048 >> 4),
                      kk != 0 || part != PARTS - 1 || !first);
           }
-          commit(lead, &o_done[b]);
-          commit(lead, &empty[kRingK + rv.slot]);
-          rv.step(kRingV);
-        };
-        wait(q_full, piece_no & 1);
-#pragma unroll 1
-        for (int i = -2; i < n; ++i) {
-          if (i >= 0) {
-            const uint32_t ct = tile + i;
-            wait(&full[kRingK + rv.slot], rv.ph);
-            if ((k0 + i + 1) * kKeys > seen_min) {
-              if (lead) mbar_arrive(v_go);
-              wait(v_fixed, fixes++ & 1);
-            }
-            wait(&p_full[ct & 1], (ct >> 1) & 1);
-            tc::fence_after();
-            mma_o(ct & 1, kFresh || i == 0);
-          }
-          if (i + 2 < n) {
-            wait(&full[rk.slot], rk.ph);
-            mma_s((tile + i + 2) & 1);
-          }
+          commit(lead, &o_done[rb.slot]);
+          commit(lead, &empty[slot]);
+          rk.step(kRingV);
+          rb.step(kBufs);
         }
       }
       tile += n;
@@ -798,29 +814,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int g = pc.g, t = pc.t, k0 = pc.k0, k1 = pc.k1, nk = pc.nk, n = pc.n;
       const int first_row = pc.first_row, packed = pc.packed;
       const int32_t* pt = pc.pt;
-      // ---- softmax: warps w and w + 4 hold the same rows (TMEM lanes), 64 keys and 64 O columns
-      // each
+      // ---- softmax: warps w and w + 4 hold the same rows (TMEM lanes)
       const int hf = warp >> 2, row = (warp & 3) * 32 + lane;
       const int rows = packed << p.log_rep;
       const bool valid = row < rows;
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-      const uint32_t to = tO + 64 * hf + lanes;
-      unsigned char* stage = data + (kEarlyQ ? kQ1 * kSlot : 0);
 
-      // Q of the row tile at x; the copies are waited for in q_ready
-      auto q_load = [&](const Place& x) {
-        unsigned char* dst = data;
+      // Q of the row tile at x into buffer qb; the copies are waited for in q_ready
+      auto q_load = [&](const Place& x, [[maybe_unused]] uint32_t qb) {
+        unsigned char* dst = data + (kEarlyQ ? qb * kSlot : 0);
         const T* q = (const T*)p.q + (long long)(x.a.row0 + (W.step_tile(x.t) << W.log_tpt)) * p.q_stride +
                      (long long)(x.g << p.log_rep) * kD;
         const int qrows = min(W.tpt(), x.a.n - (W.step_tile(x.t) << W.log_tpt)) << p.log_rep;
         if constexpr (PARTS == 1) {
-          // warp w copies rows 16 w .. as they are, two rows at a time
-          constexpr int kPer = 16;
+          // warp w of the holder that calls it copies rows 32 w .. as they are, two at a time
+          constexpr int kPer = 32;
           const uint32_t d0 = smem_u32(dst);
           const int c = lane & 15;
 #pragma unroll 4
           for (int i = 0; i < kPer; i += 2) {
-            const int r = warp * kPer + i + (lane >> 4), ok = r < qrows ? r : 0;
+            const int r = (warp & 3) * kPer + i + (lane >> 4), ok = r < qrows ? r : 0;
             cp16(d0 + (c >> 3) * kChunk + tc::sw128_off(r, c & 7),
                  q + (long long)(ok >> p.log_rep) * p.q_stride + (ok & (p.rep - 1)) * kD + 8 * c, r < qrows ? 16 : 0);
           }
@@ -851,17 +864,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       };
-      auto q_ready = [&] {
-        [[maybe_unused]] unsigned char* dst = data;
+      auto q_ready = [&]([[maybe_unused]] uint32_t qb) {
+        [[maybe_unused]] unsigned char* dst = data + qb * kSlot;
         if constexpr (PARTS == 1) {
           asm volatile("cp.async.wait_group 0;" ::: "memory");
           if (p.q_sign <= 0.f) {   // a negative scale: this thread's pieces negated; none: zeros
-            constexpr int kPer = 16;
+            constexpr int kPer = 32;
             const int c = lane & 15;
             const uint32_t keep = p.q_sign < 0.f ? 0xffffffffu : 0u, flip = p.q_sign < 0.f ? 0x80008000u : 0u;
 #pragma unroll 1
             for (int i = 0; i < kPer; i += 2) {
-              const int r = warp * kPer + i + (lane >> 4);
+              const int r = (warp & 3) * kPer + i + (lane >> 4);
               uint4* cell = (uint4*)(dst + (c >> 3) * kChunk + tc::sw128_off(r, c & 7));
               const uint4 v = *cell;
               *cell = make_uint4((v.x & keep) ^ flip, (v.y & keep) ^ flip, (v.z & keep) ^ flip, (v.w & keep) ^ flip);
@@ -869,16 +882,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         fence_proxy_async_smem();
-        mbar_arrive(q_full);
+        mbar_arrive(&q_full[kEarlyQ ? qb : 0]);
       };
       Place nx = at;
       uint32_t nx_u = u;
-      if (first) {
-        q_load(at);
-        q_ready();
-        first = false;
+      if (first && (!kEarlyQ || hf == 0)) {
+        q_load(at, 0);
+        q_ready(0);
       }
+      first = false;
       const bool more = next_place(nx, nx_u, n);
+      const uint32_t nq = (piece_no + 1) & 1;   // the next piece's buffer of Q
+      // bf16: the holder of the last tile of the piece before, who has seen that piece's last S and
+      // written it out, fills its buffer again
+      const bool loads = kEarlyQ && more && hf != begins;
+      if (loads) q_load(nx, nq);
 
       int lim = 0;   // keys this row sees
       if (valid) {
@@ -899,53 +917,70 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < kCols; ++k) osum[k] = 0.f;
       }
-      auto trade = [&](float v) -> float {   // with the other holder of the row
-        const int par = trades & 1;
-        ++trades;
-        xm[(par * 2 + hf) * kRows + row] = v;
-        bar_sync(2 + (warp & 3), 64);
-        return xm[(par * 2 + (hf ^ 1)) * kRows + row];
+      // 32 scores; those of keys that the row does not see become -inf
+      auto mask = [&](float* sv, int key) {
+        if (key + 32 > warp_min) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) sv[e] = key + e < lim ? sv[e] : -INFINITY;
+        }
       };
+      auto top = [&](const float* sv, float m) {
+        float m4[4] = {m, m, m, m};
+#pragma unroll
+        for (int e = 0; e < 32; e += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) m4[k] = max3(m4[k], sv[e + 2 * k], sv[e + 2 * k + 1]);
+        return fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
+      };
+      // the weights of 32 scores (reference maximum nm2, negated), over the scores at ts, which
+      // have been read; their sums into ps
+      auto weights = [&](const float* s32, uint32_t ts, [[maybe_unused]] uint32_t tx, uint64_t nm2, uint64_t* ps) {
+        const uint64_t c2 = pack2(c, c);
+        uint32_t w0[16];
+        [[maybe_unused]] uint32_t w1[PARTS == 3 ? 16 : 1], w2[PARTS == 3 ? 16 : 1];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          float x, y;
+          unpack2(fma2(pack2(s32[e], s32[e + 1]), c2, nm2), x, y);
+          x = ex2(x);
+          y = ex2(y);
+          ps[(e >> 1) & 1] = add2(ps[(e >> 1) & 1], pack2(x, y));
+          w0[e / 2] = bf2(x, y);
+          if constexpr (PARTS == 3) {
+            x -= bf_lo(w0[e / 2]);
+            y -= bf_hi(w0[e / 2]);
+            w1[e / 2] = bf2(x, y);
+            w2[e / 2] = bf2(x - bf_lo(w1[e / 2]), y - bf_hi(w1[e / 2]));
+          }
+        }
+        st16(ts, w0);
+        if constexpr (PARTS == 3) {
+          st16(ts + 16, w1);
+          st16(tx, w2);
+        }
+      };
+      const uint32_t ce = tile + n;
+      if constexpr (kFresh) {
+        // both holders of a row take 64 keys of every tile
+        auto trade = [&](float v) -> float {   // with the other holder of the row
+          const int par = trades & 1;
+          ++trades;
+          xm[(par * 2 + hf) * kRows + row] = v;
+          bar_sync(2 + (warp & 3), 64);
+          return xm[(par * 2 + (hf ^ 1)) * kRows + row];
+        };
 #pragma unroll 1
-      for (int i = 0; i < n; ++i) {
-        const uint32_t ct = tile + i;
-        const int b = (int)(ct & 1);
-        const int key0 = (k0 + i) * kKeys + 64 * hf;
-        const uint32_t ts = tS + 128 * b + lanes + 64 * hf;
-        // 32 scores; those of keys that the row does not see become -inf
-        auto mask = [&](float* sv, int key) {
-          if (key + 32 > warp_min) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) sv[e] = key + e < lim ? sv[e] : -INFINITY;
-          }
-        };
-        auto top = [&](const float* sv, float m) {
-          float m4[4] = {m, m, m, m};
-#pragma unroll
-          for (int e = 0; e < 32; e += 8)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) m4[k] = max3(m4[k], sv[e + 2 * k], sv[e + 2 * k + 1]);
-          return fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
-        };
-        wait(&s_full[b], (ct >> 1) & 1);
-        tc::fence_after();
-        // the piece's last products with Q are done
-        if (kEarlyQ && more && i == n - 1) q_load(nx);
-        float mx = -INFINITY;
-        // f32: the scores are read twice (for the maximum, for the weights), since registers for
-        // all of them are not left beside O
-        constexpr bool kOnce = !kFresh;
-        float sv[kOnce ? kCols : 32];
-        if constexpr (kOnce) {
-#pragma unroll
-          for (int e = 0; e < kCols; e += 32) ld32(ts + e, sv + e);
-          wait_ld();
-#pragma unroll
-          for (int e = 0; e < kCols; e += 32) {
-            mask(sv + e, key0 + e);
-            mx = top(sv + e, mx);
-          }
-        } else {
+        for (int i = 0; i < n; ++i) {
+          const uint32_t ct = tile + i;
+          const int b = (int)(ct & 1);
+          const int key0 = (k0 + i) * kKeys + 64 * hf;
+          const uint32_t ts = tS + 128 * b + lanes + 64 * hf;
+          wait(&s_full[b], (ct >> 1) & 1);
+          tc::fence_after();
+          // the scores are read twice (for the maximum, for the weights), since registers for all
+          // of them are not left beside O
+          float mx = -INFINITY;
+          float sv[32];
 #pragma unroll 1
           for (int e = 0; e < kCols; e += 32) {
             ld32(ts + e, sv);
@@ -953,72 +988,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             mask(sv, key0 + e);
             mx = top(sv, mx);
           }
-        }
-        mx = fmaxf(mx, trade(mx));
-        mx = mx == -INFINITY ? mx : mx * c;
-        const bool move = mx > ms + kMove;
-        const float alpha = move ? ex2(ms - mx) : 1.f;   // 0 while ms is -inf
-        if constexpr (!kFresh) {
-          // the barrier of the products before the last ones: already complete (they were issued
-          // before this S), waited for so that the phases are followed one by one
-          if (i >= 2) wait(&o_done[b], ((ct - 2) >> 1) & 1);
-          if (i > 0 && __any_sync(0xffffffffu, move)) {
-            wait(&o_done[b ^ 1], ((ct - 1) >> 1) & 1);
-            tc::fence_after();
-#pragma unroll 1
-            for (int e = 0; e < kCols; e += 16) {
-              float ov[16];
-              ld16(to + e, ov);
-              wait_ld();
-#pragma unroll
-              for (int k = 0; k < 16; ++k) ov[k] *= alpha;
-              st16(to + e, (const uint32_t*)ov);
-            }
-            wait_st();
+          mx = fmaxf(mx, trade(mx));
+          mx = mx == -INFINITY ? mx : mx * c;
+          const bool move = mx > ms + kMove;
+          const float alpha = move ? ex2(ms - mx) : 1.f;   // 0 while ms is -inf
+          if (move) {
+            l *= alpha;
+            ms = mx;
           }
-        }
-        if (move) {
-          l *= alpha;
-          ms = mx;
-        }
-        // a row that has seen nothing yet: weights 2^(-inf - 0)
-        const float neg = ms == -INFINITY ? 0.f : -ms;
-        const uint64_t c2 = pack2(c, c), nm2 = pack2(neg, neg);
-        uint64_t ps[2] = {0, 0};   // pairs of sums, +0 each
-        auto weights = [&](const float* s32, int e0) {
-          uint32_t w0[16];
-          [[maybe_unused]] uint32_t w1[PARTS == 3 ? 16 : 1], w2[PARTS == 3 ? 16 : 1];
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            float x, y;
-            unpack2(fma2(pack2(s32[e], s32[e + 1]), c2, nm2), x, y);
-            x = ex2(x);
-            y = ex2(y);
-            ps[(e >> 1) & 1] = add2(ps[(e >> 1) & 1], pack2(x, y));
-            w0[e / 2] = bf2(x, y);
-            if constexpr (PARTS == 3) {
-              x -= bf_lo(w0[e / 2]);
-              y -= bf_hi(w0[e / 2]);
-              w1[e / 2] = bf2(x, y);
-              w2[e / 2] = bf2(x - bf_lo(w1[e / 2]), y - bf_hi(w1[e / 2]));
-            }
-          }
-          st16(ts + e0, w0);   // over scores that have been read
-          if constexpr (PARTS == 3) {
-            st16(ts + e0 + 16, w1);
-            st16(tX + 64 * b + lanes + 32 * hf + e0 / 2, w2);
-          }
-        };
-        if constexpr (kOnce) {
-#pragma unroll
-          for (int e = 0; e < kCols; e += 32) weights(sv + e, e);
-        } else {
+          // a row that has seen nothing yet: weights 2^(-inf - 0)
+          const float neg = ms == -INFINITY ? 0.f : -ms;
+          const uint64_t nm2 = pack2(neg, neg);
+          uint64_t ps[2] = {0, 0};   // pairs of sums, +0 each
 #pragma unroll 1
           for (int e = 0; e < kCols; e += 32) {
             ld32(ts + e, sv);
             wait_ld();
             mask(sv, key0 + e);
-            weights(sv, e);
+            weights(sv, ts + e, tX + 64 * b + lanes + 32 * hf + e / 2, nm2, ps);
           }
           // O of the tile before, while S of the tile after is made; the next P V products,
           // which overwrite it, wait for this thread
@@ -1028,7 +1015,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool any = __any_sync(0xffffffffu, move);
 #pragma unroll
             for (int e = 0; e < kCols; e += 32) {
-              ld32(to + e, sv);
+              ld32(tO + lanes + 64 * hf + e, sv);
               wait_ld();
 #pragma unroll
               for (int k = 0; k < 32; ++k) osum[e + k] += sv[k];
@@ -1037,158 +1024,316 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int k = 0; k < kCols; ++k) osum[k] *= alpha;
           }
-        }
-        {
           float x, y;
           unpack2(add2(ps[0], ps[1]), x, y);
           l += x + y;
+          wait_st();
+          tc::fence_before();
+          mbar_arrive(&p_full[b]);
         }
-        wait_st();
-        tc::fence_before();
-        mbar_arrive(&p_full[b]);
+        wait(&o_done[(ce - 1) & 1], ((ce - 1) >> 1) & 1);
+        const float l_other = trade(l);
+        l = hf == 0 ? l + l_other : l_other + l;
+      } else {
+        // The two holders of a row take whole tiles in turn, so that the exponentials of one run
+        // beside the loads and maxima of the other: the one that begins the first kSolo tiles, while
+        // the other writes out the piece before, then they alternate. The reference maximum of O goes from one to
+        // the other (xm), before either's exponentials; a holder's own sum of weights is for its
+        // last reference (ms). The holder of the piece's last tile gets the other's sum and writes
+        // the piece out, while the other begins the next one.
+        const int pass_mine = kPassed + 4 * hf + (warp & 3), pass_other = kPassed + 4 * (hf ^ 1) + (warp & 3);
+        float* ref_mine = xm + hf * kRows + row;
+        const float* ref_other = xm + (hf ^ 1) * kRows + row;
+        auto refer = [&](float m) {
+          if (m != ms) {
+            l *= ex2(ms - m);   // 0 while ms is -inf
+            ms = m;
+          }
+        };
+#pragma unroll 1
+        for (int i = hf == begins ? 0 : kSolo; i < n; i += i < kSolo - 1 ? 1 : 2) {
+          const uint32_t ct = tile + i, b = ct % kBufs;
+          const int key0 = (k0 + i) * kKeys;
+          const uint32_t ts = tS + 128 * b + lanes;
+          // (whoever has not followed the kBufs tiles before this one waits for the reference first:
+          // the barrier of S is then at this tile's phase)
+          const bool early = i == kSolo || (i == 0 && behind);
+          if (early) bar_sync(pass_other, 64);
+          wait(&s_full[b], (ct / kBufs) & 1);
+          tc::fence_after();
+          if (key0 + kKeys > warp_min) {   // keys that some row of the warp does not see become -inf
+#pragma unroll 1
+            for (int e = max(0, (warp_min - key0) & ~31); e < kKeys; e += 32) {
+              float x[32];
+              ld32(ts + e, x);
+              wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) x[k] = key0 + e + k < lim ? x[k] : -INFINITY;
+              st16(ts + e, (const uint32_t*)x);
+              st16(ts + e + 16, (const uint32_t*)x + 16);
+            }
+            wait_st();
+          }
+          float sv[kKeys];
+#pragma unroll
+          for (int e = 0; e < kKeys; e += 32) ld32(ts + e, sv + e);
+          wait_ld();
+          float mx = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < kKeys; e += 32) mx = top(sv + e, mx);
+          mx = mx == -INFINITY ? mx : mx * c;
+          float old = -INFINITY;
+          if (!early && (i > kSolo || (i == 0 && ct > 0))) bar_sync(pass_other, 64);
+          if (i > 0) old = i < kSolo ? ms : *ref_other;
+          const bool move = mx > old + kMove;
+          const float now = move ? mx : old;
+          if (i >= kSolo - 1 && i < n - 1) {   // (of the last tile: when the other's sum has been read)
+            *ref_mine = now;
+            bar_arrive(pass_mine, 64);
+          }
+          if (loads && i == kSolo) q_ready(nq);
+          if (i > 0 && __any_sync(0xffffffffu, move)) {
+            // (S of the tile before is there, so the products three tiles before it are done)
+            wait(&o_done[(ct - 1) % kBufs], ((ct - 1) / kBufs) & 1);
+            tc::fence_after();
+            const float alpha = move ? ex2(old - now) : 1.f;   // 0 while the reference is -inf
+#pragma unroll 1
+            for (int e = 0; e < kD; e += 16) {
+              float ov[16];
+              ld16(tO + lanes + e, ov);
+              wait_ld();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) ov[k] *= alpha;
+              st16(tO + lanes + e, (const uint32_t*)ov);
+            }
+            wait_st();
+          }
+          refer(now);
+          // a row that has seen nothing yet: weights 2^(-inf - 0)
+          const float neg = ms == -INFINITY ? 0.f : -ms;
+          const uint64_t nm2 = pack2(neg, neg);
+          uint64_t ps[2] = {0, 0};   // pairs of sums, +0 each
+#pragma unroll
+          for (int e = 0; e < kKeys; e += 32) weights(sv + e, ts + e, 0, nm2, ps);
+          float x, y;
+          unpack2(add2(ps[0], ps[1]), x, y);
+          l += x + y;
+          wait_st();
+          tc::fence_before();
+          mbar_arrive(&p_full[b]);
+        }
+        if (loads && n <= kSolo) q_ready(nq);   // (no tile of its own)
       }
-      if (kEarlyQ && more) q_ready();
 
-      // ---- the piece's O, m, l
-      const uint32_t ce = tile + n;
-      if (!kFresh && n >= 2) wait(&o_done[ce & 1], ((ce - 2) >> 1) & 1);
-      wait(&o_done[(ce - 1) & 1], ((ce - 1) >> 1) & 1);
-      const float l_other = trade(l);
-      l = hf == 0 ? l + l_other : l_other + l;
-      tc::fence_after();
-      const bool dead = *(volatile int*)s_abort != 0;
+      // ---- the piece's O, m, l: f32 by both holders of a row, 64 columns each; bf16 by the
+      // holder of the last tile
+      constexpr int kGroup = kFresh ? kSoft : kSoft / 2;   // threads that write a piece out
+      const int gid = tid & (kGroup - 1), gbar = kFresh || hf ? 6 : 1;
       const bool whole = k0 == 0 && k1 == nk;
+      const bool final_out = whole && PROMPT;      // else O as it is, with m and l
       float* part = p.part + ((size_t)blockIdx.x * 2 + (k0 == 0 ? 1 : 0)) * kPartFloats;
-      const bool patch = *(volatile int*)(s_patch + (piece_no & 1)) == (int)piece_no + 1;
       // row r of the tile in [n_rows, Hq]: tile0 + out_row(r)
       const size_t tile0 = (size_t)first_row * p.Hq + (g << p.log_rep);
-      auto out_row = [&](int r) { return (r >> p.log_rep) * p.Hq + (r & (p.rep - 1)); };
-      const int col0 = 64 * hf;
-      const bool final_out = whole && PROMPT;      // else O as it is, with m and l
-      const float inv = l == 0.f ? 0.f : 1.0f / l;   // a row that saw nothing gives 0
-      // bf16 results and the f32 form's values go out by whole rows, through shared memory:
-      // 16-byte pieces, swizzled; the bf16 form's partial values as they are
+      auto out_row = [&](int r) { return (r >> p.log_rep) * p.Hq + (r & (p.rep - 1)); };   // (x 128: below 2^31)
       float* dst = !whole ? part : (PROMPT ? (float*)p.out : p.pre_o) + tile0 * kD;
-      const bool staged = PARTS == 3 || final_out;
-      unsigned char* mine = stage + row * (PARTS == 3 ? 512 : 256);
-      const int xr = staged ? row & (PARTS == 3 ? 31 : 15) : 0;
-      if (!staged) mine = (unsigned char*)(dst + (size_t)(whole ? out_row(valid ? row : 0) : row) * kD);
-      const float f = final_out ? inv : 1.f;
-      float z = 0.f;   // 0 unless a value is not finite
-#pragma unroll(kFresh ? kCols / 32 : 1)
-      for (int e = 0; e < kCols; e += 32) {
-        float ov[32];
-        ld32(to + e, ov);
-        wait_ld();
+      auto put_stats = [&] {
+        float* m_at = whole ? p.pre_m + tile0 + out_row(row) : part + (size_t)kRows * kD + row;
+        float* l_at = whole ? p.pre_l + tile0 + out_row(row) : part + (size_t)kRows * (kD + 1) + row;
+        *m_at = ms;
+        *l_at = l;
+      };
+      bool writes = true;
+      if constexpr (kFresh) {
+        tc::fence_after();
+        const bool dead = *(volatile int*)s_abort != 0;
+        const bool patch = *(volatile int*)(s_patch + (piece_no & 1)) == (int)piece_no + 1;
+        const int col0 = 64 * hf;
+        const float f = !final_out ? 1.f : l == 0.f ? 0.f : 1.0f / l;   // a row that saw nothing gives 0
+        // values go out by whole rows, through Q's place: 16-byte pieces, swizzled
+        unsigned char* mine = data + row * 512;
+        const int xr = row & 31;
+        float z = 0.f;   // 0 unless a value is not finite
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          if constexpr (kFresh) ov[k] += osum[e + k];
-          z = fmaf(ov[k], 0.f, z);
-          ov[k] *= f;
-        }
-        if (PARTS == 1 && final_out) {
+        for (int e = 0; e < kCols; e += 32) {
+          float ov[32];
+          ld32(tO + lanes + col0 + e, ov);
+          wait_ld();
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            *(uint4*)(mine + ((((col0 + e) / 8 + k) ^ xr) << 4)) =
-                make_uint4(bf2(ov[8 * k], ov[8 * k + 1]), bf2(ov[8 * k + 2], ov[8 * k + 3]),
-                           bf2(ov[8 * k + 4], ov[8 * k + 5]), bf2(ov[8 * k + 6], ov[8 * k + 7]));
-        } else if (PARTS == 3 || (valid && !dead)) {
+          for (int k = 0; k < 32; ++k) {
+            ov[k] += osum[e + k];
+            z = fmaf(ov[k], 0.f, z);
+            ov[k] *= f;
+          }
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             *(float4*)(mine + ((((col0 + e) / 4 + k) ^ xr) << 4)) =
                 make_float4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
         }
-      }
-      if ((patch || z != 0.f) && valid && !dead && l == l)
-        patch_row(p, pt, g, k0 * kKeys, min(lim, k1 * kKeys), col0, mine, xr, PARTS == 1 && final_out);
-      if (valid && !dead && !final_out && hf == 0) {
-        float* m_at = whole ? p.pre_m + tile0 + out_row(row) : part + (size_t)kRows * kD + row;
-        float* l_at = whole ? p.pre_l + tile0 + out_row(row) : part + (size_t)kRows * (kD + 1) + row;
-        *m_at = ms;
-        *l_at = l;
-      }
-      if (staged) {
+        if ((patch || z != 0.f) && valid && !dead && l == l)
+          patch_row(p, pt, g, k0 * kKeys, min(lim, k1 * kKeys), col0, mine, xr, false);
+        if (valid && !dead && !final_out && hf == 0) put_stats();
         // the rows that this warp's lanes and their other holders' wrote
         bar_sync(2 + (warp & 3), 64);
         const int r0 = (warp & 3) * 32 + hf * 16;
-        constexpr int kLanes = PARTS == 3 ? 32 : 16;   // lanes per row
 #pragma unroll 4
-        for (int i = 0; i < 16; i += 32 / kLanes) {
-          const int r = r0 + i + lane / kLanes, pc = lane & (kLanes - 1);
-          const uint4 v = *(const uint4*)(stage + r * (PARTS == 3 ? 512 : 256) + ((pc ^ (r & (kLanes - 1))) << 4));
-          if (r < rows && !dead) {
-            if constexpr (PARTS == 3) *(uint4*)(dst + (size_t)(whole ? out_row(r) : r) * kD + 4 * pc) = v;
-            else *(uint4*)((__nv_bfloat16*)p.out + (tile0 + out_row(r)) * kD + 8 * pc) = v;
+        for (int i = 0; i < 16; ++i) {
+          const int r = r0 + i;
+          const uint4 v = *(const uint4*)(data + r * 512 + ((lane ^ (r & 31)) << 4));
+          if (r < rows && !dead) *(uint4*)(dst + (size_t)(whole ? out_row(r) : r) * kD + 4 * lane) = v;
+        }
+      } else {
+        float* given = xm + 2 * kRows + row;   // reference and sum of the holder without the last tile
+        // the holder of the last tile
+        const int ends = n > kSolo && !((n - 1 - kSolo) & 1) ? begins ^ 1 : begins;
+        behind = n >= kBufs && n <= kSolo;   // (of the other, who had no tile and begins the next piece)
+        begins = ends ^ 1;
+        writes = ends == hf;
+        if (!writes) {
+          given[0] = ms;
+          given[kRows] = l;
+          bar_arrive(2 + (warp & 3), 64);
+        } else {
+          bar_sync(2 + (warp & 3), 64);
+          const float om = given[0], ol = given[kRows];
+          if (more) bar_arrive(kPassed + 4 * hf + (warp & 3), 64);
+          l = fmaf(ol, om == -INFINITY ? 1.f : ex2(om - ms), l);   // (its sum is 0 or NaN while it saw nothing)
+          // (S of this tile is there, so the products three tiles before it are done)
+          wait(&o_done[(ce - 1) % kBufs], ((ce - 1) / kBufs) & 1);
+          tc::fence_after();
+          const bool dead = *(volatile int*)s_abort != 0;
+          const bool patch = *(volatile int*)(s_patch + (piece_no & 1)) == (int)piece_no + 1;
+          const float f = !final_out ? 1.f : l == 0.f ? 0.f : 1.0f / l;   // a row that saw nothing gives 0
+          const bool put = valid && !dead;
+          // bf16 results go out by whole rows, through the place of the same rows of Q (which this
+          // warp fills again); partial values as they are
+          unsigned char* old_q = data + (piece_no & 1) * kSlot;
+          unsigned char* mine = final_out ? old_q + row * 128
+                                          : (unsigned char*)(dst + (size_t)(whole ? out_row(put ? row : 0) : row) * kD);
+          const int xr = row & 7;
+          float z = 0.f;   // infinite or NaN if a value is
+#pragma unroll 1
+          for (int e = 0; e < kD; e += 32) {
+            float ov[32];
+            ld32(tO + lanes + e, ov);
+            wait_ld();
+            if (e == kD - 32) {
+              tc::fence_before();
+              mbar_arrive(o_free);
+            }
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              z = max3_abs_nan(z, ov[k], ov[k + 1]);
+              ov[k] *= f;
+              ov[k + 1] *= f;
+            }
+            if (final_out) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                *(uint4*)(mine + (e >> 6) * kChunk + ((((e & 32) / 8 + k) ^ xr) << 4)) =
+                    make_uint4(bf2(ov[8 * k], ov[8 * k + 1]), bf2(ov[8 * k + 2], ov[8 * k + 3]),
+                               bf2(ov[8 * k + 4], ov[8 * k + 5]), bf2(ov[8 * k + 6], ov[8 * k + 7]));
+            } else if (put) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                *(float4*)(mine + 4 * e + 16 * k) = make_float4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
+            }
           }
+          if ((patch || !(z < INFINITY)) && put && l == l) {
+#pragma unroll 1
+            for (int d0 = 0; d0 < kD; d0 += 64)
+              patch_row(p, pt, g, k0 * kKeys, min(lim, k1 * kKeys), d0,
+                        mine + (final_out ? (d0 >> 6) * (kChunk - 128) : 0), final_out ? xr : 0, final_out);
+          }
+          if (final_out) {
+            __syncwarp();
+            __nv_bfloat16* out = (__nv_bfloat16*)p.out + tile0 * kD + 8 * (lane & 15);
+#pragma unroll 4
+            for (int i = 0; i < 32; i += 2) {
+              const int c = lane & 15, tr = (warp & 3) * 32 + i + (lane >> 4);
+              const uint4 v = *(const uint4*)(old_q + (c >> 3) * kChunk + tc::sw128_off(tr, c & 7));
+              if (tr < rows && !dead) *(uint4*)(out + out_row(tr) * kD) = v;
+            }
+            __syncwarp();   // before the next Q
+          }
+          if (put && !final_out) put_stats();
         }
       }
-      if (!PROMPT && k0 == 0 && tid < packed) {   // the kernel that reads the rest joins the pieces
-        AttnFrom* f = p.from + (size_t)(first_row + tid) * p.Hkv + g;
+      if (!PROMPT && writes && k0 == 0 && gid < packed) {   // the kernel that reads the rest joins the pieces
+        AttnFrom* f = p.from + (size_t)(first_row + gid) * p.Hkv + g;
         f->first = blockIdx.x;
         f->pieces = whole ? 0 : sp.owner(u + nk - 1) - (int)run_no + 1;
         f->stride = W.team;
-        f->row = tid << p.log_rep;
+        f->row = gid << p.log_rep;
       }
       // ---- a prompt's row tile of several CTAs: the last of them joins the pieces in key order
-      if (PROMPT && !whole) {   // the same in all softmax threads
+      if (PROMPT && writes && !whole) {   // the same in all threads that write the piece out
         // where the tile's units lie: the CTAs of its first and last
         const int c0 = k0 == 0 ? (int)blockIdx.x : sp.owner(u - k0);
         const int c1 = k1 == nk ? (int)blockIdx.x : sp.owner(u - k0 + nk - 1);
-        bar_sync(6, kSoft);
-        if (tid == 0) *s_last = !*(volatile int*)s_abort && atom_add_acq_rel_gpu(p.tickets + c0, 1) == c1 - c0;
-        bar_sync(6, kSoft);
-        if (*(volatile int*)s_last) {
+        volatile int* last = s_last + (kFresh ? 0 : hf);
+        bar_sync(gbar, kGroup);
+        if (gid == 0) *last = !*(volatile int*)s_abort && atom_add_acq_rel_gpu(p.tickets + c0, 1) == c1 - c0;
+        bar_sync(gbar, kGroup);
+        if (*last) {
           const int np = c1 - c0 + 1;
-          // maxima, then weights, [pieces][batch of rows], sums likewise, and the rows' totals
-          // [batch] where results are staged, as many rows at a time as fit. Everything is read
-          // from L2 once, so what counts is how many loads are under way: pieces are read side
-          // by side for the statistics, eight rows of two pieces per thread for O.
-          const int batch = min(rows, (kEarlyQ ? 1 : kQ1) * kSlot / 4 / (2 * np + 1));
-          float* wt = (float*)stage;
-          float* ls = wt + (size_t)np * batch;
-          float* total = ls + (size_t)np * batch;
           auto piece = [&](int k) { return p.part + ((size_t)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * kPartFloats; };
+          // A warp joins eight rows at a time: lane k has piece k's statistics (32 pieces at a time),
+          // then four columns of O. Everything is read from L2 once, so what counts is how many
+          // loads are under way.
+          constexpr int kJoin = 8;
 #pragma unroll 1
-          for (int r0 = 0; r0 < rows; r0 += batch) {
-            const int nb = min(batch, rows - r0);
-#pragma unroll 2
-            for (int e = tid; e < np * nb; e += kSoft) {
-              const int k = e / nb, r = e - k * nb;
-              const float* st = piece(k) + (size_t)kRows * kD + r0 + r;
-              wt[k * batch + r] = __ldcg(st);
-              ls[k * batch + r] = __ldcg(st + kRows);
+          for (int r0 = (gid >> 5) * kJoin; r0 < rows; r0 += kGroup / 32 * kJoin) {
+            float M[kJoin], L[kJoin];
+            float4 acc[kJoin];
+#pragma unroll
+            for (int j = 0; j < kJoin; ++j) {
+              M[j] = -INFINITY;
+              L[j] = 0.f;
+              acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
             }
-            bar_sync(6, kSoft);
-            for (int r = tid; r < nb; r += kSoft) {
-              float M = -INFINITY, L = 0.f;
 #pragma unroll 1
-              for (int k = 0; k < np; ++k) M = fmaxf(M, wt[k * batch + r]);
-#pragma unroll 1
-              for (int k = 0; k < np; ++k) {
-                const float m = wt[k * batch + r], x = m == -INFINITY ? 0.f : ex2(m - M);
-                wt[k * batch + r] = x;
-                if (x != 0.f) L = fmaf(x, ls[k * batch + r], L);
+            for (int b0 = 0; b0 < np; b0 += 32) {
+              const int nb = min(32, np - b0);
+              float m4[kJoin], l4[kJoin];
+              const float* st = piece(b0 + min(lane, nb - 1)) + (size_t)kRows * kD + r0;
+#pragma unroll
+              for (int j = 0; j < kJoin; ++j) {
+                const bool has = lane < nb && r0 + j < rows;
+                m4[j] = has ? __ldcg(st + j) : -INFINITY;
+                l4[j] = has ? __ldcg(st + kRows + j) : 0.f;
               }
-              total[r] = L;
-            }
-            bar_sync(6, kSoft);
-            // warp w: rows w, w + 8, ...; a lane has four columns
+#pragma unroll
+              for (int j = 0; j < kJoin; ++j) {
+                float top = m4[j];
+#pragma unroll
+                for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                top = fmaxf(top, M[j]);
+                const float keep = M[j] == -INFINITY ? 1.f : ex2(M[j] - top);   // (O and L are 0 or NaN there)
+                // pieces that saw nothing: weight 1 for a sum and an O of 0 (or NaN)
+                m4[j] = m4[j] == -INFINITY ? 1.f : ex2(m4[j] - top);
+                float sum = m4[j] != 0.f ? m4[j] * l4[j] : 0.f;
+#pragma unroll
+                for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                L[j] = (keep != 0.f ? L[j] * keep : 0.f) + sum;
+                if (keep != 1.f) {
+                  acc[j].x = keep != 0.f ? acc[j].x * keep : 0.f;
+                  acc[j].y = keep != 0.f ? acc[j].y * keep : 0.f;
+                  acc[j].z = keep != 0.f ? acc[j].z * keep : 0.f;
+                  acc[j].w = keep != 0.f ? acc[j].w * keep : 0.f;
+                }
+                M[j] = top;
+              }
 #pragma unroll 1
-            for (int rb = warp; rb < nb; rb += 8 * kSoftWarps) {
-              float4 acc[8];
+              for (int k = 0; k < nb; ++k) {
+                const float4* src = (const float4*)(piece(b0 + k) + (size_t)r0 * kD) + lane;
+                float4 v[kJoin];
 #pragma unroll
-              for (int j = 0; j < 8; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-              for (int k = 0; k < np; ++k) {
-                const float4* src = (const float4*)(piece(k) + (size_t)(r0 + rb) * kD) + lane;
-                float4 v[8];
+                for (int j = 0; j < kJoin; ++j)
+                  if (r0 + j < rows) v[j] = __ldcg(src + j * (kD / 4));
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                  if (rb + j * kSoftWarps < nb) v[j] = __ldcg(src + j * kSoftWarps * (kD / 4));
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  const float x = rb + j * kSoftWarps < nb ? wt[k * batch + rb + j * kSoftWarps] : 0.f;
-                  if (x != 0.f) {
+                for (int j = 0; j < kJoin; ++j) {
+                  const float x = __shfl_sync(0xffffffffu, m4[j], k);
+                  if (x != 0.f && r0 + j < rows) {
                     acc[j].x = fmaf(x, v[j].x, acc[j].x);
                     acc[j].y = fmaf(x, v[j].y, acc[j].y);
                     acc[j].z = fmaf(x, v[j].z, acc[j].z);
@@ -1196,30 +1341,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                   }
                 }
               }
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const int r = rb + j * kSoftWarps;
-                if (r >= nb) break;
-                const size_t o = (tile0 + out_row(r0 + r)) * kD + 4 * lane;
-                const float L = total[r], iv = L == 0.f ? 0.f : 1.0f / L;
-                if constexpr (PARTS == 1)
-                  *(uint2*)((__nv_bfloat16*)p.out + o) =
-                      make_uint2(bf2(acc[j].x * iv, acc[j].y * iv), bf2(acc[j].z * iv, acc[j].w * iv));
-                else
-                  *(float4*)((float*)p.out + o) =
-                      make_float4(acc[j].x * iv, acc[j].y * iv, acc[j].z * iv, acc[j].w * iv);
-              }
             }
-            bar_sync(6, kSoft);
+#pragma unroll
+            for (int j = 0; j < kJoin; ++j) {
+              if (r0 + j >= rows) break;
+              const size_t o = (tile0 + out_row(r0 + j)) * kD + 4 * lane;
+              const float iv = L[j] == 0.f ? 0.f : 1.0f / L[j];
+              if constexpr (PARTS == 1)
+                *(uint2*)((__nv_bfloat16*)p.out + o) =
+                    make_uint2(bf2(acc[j].x * iv, acc[j].y * iv), bf2(acc[j].z * iv, acc[j].w * iv));
+              else
+                *(float4*)((float*)p.out + o) = make_float4(acc[j].x * iv, acc[j].y * iv, acc[j].z * iv, acc[j].w * iv);
+            }
           }
-          if (tid == 0) p.tickets[c0] = 0;
+          bar_sync(gbar, kGroup);
+          if (gid == 0) p.tickets[c0] = 0;
         }
       }
       tc::fence_before();
       if (!kEarlyQ && more) {
         bar_sync(6, kSoft);   // everybody is done with Q's place
-        q_load(nx);
-        q_ready();
+        q_load(nx, 0);
+        q_ready(0);
       }
       tile += n;
       ++piece_no;
@@ -1237,9 +1380,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (again || tile >= slots) mbar_wait_limit(&full[slot0 + i], again ? rk.ph : rk.ph ^ 1, p.err, 10000000ull);
     }
   }
-  if (warp == kSoftWarps && *(volatile int*)s_abort) {   // ... and the products (bounded)
-    commit(lane == 0, drained);
-    mbar_wait_limit(drained, 0, p.err, 10000000ull);
+  if ((warp == kIssueS || warp == kIssueO) && *(volatile int*)s_abort) {   // ... and the products (bounded)
+    commit(lane == 0, &drained[warp == kIssueO]);
+    mbar_wait_limit(&drained[warp == kIssueO], 0, p.err, 10000000ull);
   }
   tc::fence_before();
   __syncthreads();
