@@ -144,12 +144,30 @@ QD_DEV void st16(uint32_t taddr, const uint32_t* r) {   // 16 columns, not waite
 }
 QD_DEV void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// O += P V: A (P) in tensor memory, B (V) in shared memory as [keys][dims], i.e. MN-major:
-// 64 dims per 128-byte row, 8 keys per swizzle atom; the leading offset leads to the next
-// 64 dims, the stride offset to the next 8 keys.
+// K and V tiles lie as groups of 8 keys of 2048 bytes, one 128-byte-swizzled atom for dims 0 ..
+// 63 and one for the others, so that one copy brings whole rows of a page (with a copy for each
+// half of the dims a prefix of 32768 tokens in 16-row pages took 2 us more of 68).
+constexpr int kKeys8 = 2048, kHalf8 = 1024;
+QD_DEV uint32_t kv_off(int key, int c) {   // of 16-byte piece c of a key's row
+  return (uint32_t)((key >> 3) * kKeys8 + (c >> 3) * kHalf8 + (key & 7) * 128 + (((c & 7) ^ (key & 7)) << 4));
+}
+// K: K-major, the stride offset leads to the next 8 keys.
+QD_DEV uint64_t desc_k(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3FFF) | (uint64_t)1 << 16 | (uint64_t)(kKeys8 >> 4) << 32 | (uint64_t)1 << 46 |
+         (uint64_t)2 << 61;
+}
+// V as B of O += P V (A in tensor memory), [keys][dims], i.e. MN-major: the leading offset leads
+// to the next 64 dims, the stride offset to the next 8 keys.
 QD_DEV uint64_t desc_v(uint32_t saddr) {
-  return (uint64_t)((saddr >> 4) & 0x3FFF) | (uint64_t)(kChunk >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+  return (uint64_t)((saddr >> 4) & 0x3FFF) | (uint64_t)(kHalf8 >> 4) << 16 | (uint64_t)(kKeys8 >> 4) << 32 |
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+QD_DEV void tma_load_rows(void* dst, const CUtensorMap* map, int row, uint64_t* bar) {   // row: a multiple of 8
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3}], [%4];" ::"r"(
+          smem_u32(dst)),
+      "l"((uint64_t)map), "r"(0), "r"(row >> 3), "r"(smem_u32(bar))
+      : "memory");
 }
 // The products are issued by one lane of a warp whose lanes all walk the same way, so that
 // descriptors stay in uniform registers; `lead` says which lane.
@@ -624,10 +642,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t* pt = pc.pt;
 
       if (warp == kProducer || warp == kProducer + 1) {
-        // ---- K or V tiles. Each has a warp of its own, since issuing the 16 copies of a tile in
-        // 16-row pages takes some 1700 cycles. A lane's cache rows of a tile are looked up a tile
-        // ahead of their use. TMA: lane l, box l / 2 and
-        // dims 64 (l & 1); asynchronous copies: keys l, l + 32, ... (-1: past the keys)
+        // ---- K or V tiles, a warp each, since a copy takes some 100 cycles to issue. A lane's cache
+        // rows of a tile are looked up a tile ahead of their use. TMA: lane l, box l; asynchronous
+        // copies: keys l, l + 32, ... (-1: past the keys)
         constexpr int kMine = 4;
         struct Look {
           int row[kMine];
@@ -638,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int key0 = (k0 + i) * kKeys;
 #pragma unroll
           for (int j = 0; j < kMine; ++j) {
-            const int key = p.box ? key0 + (lane >> 1) * p.box : key0 + 32 * j + lane;
+            const int key = p.box ? key0 + lane * p.box : key0 + 32 * j + lane;
             x.row[j] = -1;
             if (i < n && key < min(seen_max, key0 + kKeys) && (j == 0 || !p.box)) {
               const PagedSlot sl = paged_slot(pt, key, p.page_size, p.div, p.n_pages);
@@ -659,15 +676,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           unsigned char* dst = data + (kQ + slot) * kSlot;
           if (p.box) {
             const bool go = !__any_sync(0xffffffffu, *(volatile int*)s_abort != 0);
-            const unsigned boxes = __popc(__ballot_sync(0xffffffffu, x.row[0] >= 0));   // half boxes
+            const unsigned boxes = __popc(__ballot_sync(0xffffffffu, x.row[0] >= 0));
             if (lane == 0) {
-              if (go && boxes) mbar_arrive_expect_tx(&full[slot], boxes * p.box * 128);
+              if (go && boxes) mbar_arrive_expect_tx(&full[slot], boxes * p.box * 256);
               else mbar_arrive(&full[slot]);
             }
             __syncwarp();
             if (go && x.row[0] >= 0)
-              tma_load_2d(dst + (lane & 1) * kChunk + (lane >> 1) * p.box * 128, map, (lane & 1) * 64, x.row[0],
-                          &full[slot]);
+              tma_load_rows(dst + lane * p.box * 256, map, x.row[0], &full[slot]);
             __syncwarp();
           } else {
             // 16 lanes copy one key's 256 bytes
@@ -678,8 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int i = 0; i < 32; i += 2) {
                 const int r = i + (lane >> 4), c = lane & 15;
                 const int row = __shfl_sync(0xffffffffu, x.row[j], r);
-                cp16(d0 + (c >> 3) * kChunk + tc::sw128_off(32 * j + r, c & 7),
-                     pages + (long long)max(row, 0) * kD + c * 8, row < 0 ? 0 : 16);
+                cp16(d0 + kv_off(32 * j + r, c), pages + (long long)max(row, 0) * kD + c * 8, row < 0 ? 0 : 16);
               }
             asm volatile("cp.async.commit_group;" ::: "memory");
             if (late >= 0) {   // the entry before this one
@@ -719,16 +734,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait(&full[rk.slot], rk.ph);
           wait(&o_done[rb.slot], rb.ph ^ 1);   // the products that read the buffer (none in the first round)
           tc::fence_after();
-          const uint64_t dk = tc::desc_sw128(ring0 + rk.slot * kSlot);
+          const uint64_t dk = desc_k(ring0 + rk.slot * kSlot);
           const uint32_t ts = tS + 128 * rb.slot;
 #pragma unroll 1
           for (int part = PARTS - 1; part >= 0; --part) {   // small parts first
             const uint64_t da = dq + (uint64_t)(part * kSlot >> 4);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
-              constexpr int kHalf = kChunk >> 4;
-              const uint64_t o = (kk >> 2) * kHalf + (kk & 3) * 2;
-              mma_qk(lead, ts, da + o, dk + o, kk != 0 || part != PARTS - 1);
+              mma_qk(lead, ts, da + (kk >> 2) * (kChunk >> 4) + (kk & 3) * 2,
+                     dk + (kk >> 2) * (kHalf8 >> 4) + (kk & 3) * 2, kk != 0 || part != PARTS - 1);
             }
           }
           commit(lead, &s_full[rb.slot]);
@@ -754,11 +768,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             // lane: of key lane / 4 in a group of 8, 16-byte pieces lane & 3, + 4, + 8, + 12
             const int sub = lane >> 2, cc = lane & 3;
             unsigned char* v = data + (kQ + slot) * kSlot + sub * 128;
-            const int o4[4] = {(cc ^ sub) << 4, ((cc + 4) ^ sub) << 4, kChunk + ((cc ^ sub) << 4),
-                               kChunk + (((cc + 4) ^ sub) << 4)};
+            const int o4[4] = {(cc ^ sub) << 4, ((cc + 4) ^ sub) << 4, kHalf8 + ((cc ^ sub) << 4),
+                               kHalf8 + (((cc + 4) ^ sub) << 4)};
 #pragma unroll 1
             for (int key = (lo & ~7) + sub; key < steps * 16; key += 8) {
-              unsigned char* cell = v + (key >> 3) * 1024;
+              unsigned char* cell = v + (key >> 3) * kKeys8;
               if (key >= hi) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) *(uint4*)(cell + o4[j]) = make_uint4(0u, 0u, 0u, 0u);
@@ -771,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int j = 0; j < 32; ++j) {
                   const int c = ((cc + 4 * ((j >> 3) & 1)) ^ sub) << 4;
-                  unsigned short* h = (unsigned short*)(cell + (j >> 4) * kChunk + c) + (j & 7);
+                  unsigned short* h = (unsigned short*)(cell + (j >> 4) * kHalf8 + c) + (j & 7);
                   if ((*h & 0x7f80u) == 0x7f80u) *h = 0;
                 }
               }
@@ -793,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t t32 = part < 2 ? 32 : 16;
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              mma_pv(go, kk, tO, ta + t32 * (kk >> 1) + 8 * (kk & 1), dv + (uint64_t)(kk * 2048 >> 4),
+              mma_pv(go, kk, tO, ta + t32 * (kk >> 1) + 8 * (kk & 1), dv + (uint64_t)(kk * 2 * kKeys8 >> 4),
                      kk != 0 || part != PARTS - 1 || !first);
           }
           commit(lead, &o_done[rb.slot]);
@@ -1435,8 +1449,8 @@ cudaError_t run(const AttnRowsArgs& a, float* pre_o, AttnFrom* from, const Launc
     p.box = 16;
     while (p.box < kKeys && a.page_size % (2 * p.box) == 0) p.box *= 2;
     const uint64_t rows = (uint64_t)a.n_pages * a.Hkv * a.page_size;
-    cudaError_t e = encode_tmap_bf16_2d(&tk, a.k_pages, rows, kD, p.box);
-    if (e == cudaSuccess) e = encode_tmap_bf16_2d(&tv, a.v_pages, rows, kD, p.box);
+    cudaError_t e = encode_tmap_bf16_rows128(&tk, a.k_pages, rows, p.box);
+    if (e == cudaSuccess) e = encode_tmap_bf16_rows128(&tv, a.v_pages, rows, p.box);
     if (e != cudaSuccess) return e;
   }
   return a.q_f32 ? launch<float, 3, PROMPT>(p, tk, tv, L) : launch<__nv_bfloat16, 1, PROMPT>(p, tk, tv, L);

@@ -906,6 +906,19 @@ cudaError_t encode_tmap_bf16_2d(void* map, const void* base, uint64_t rows, uint
   return encode_rowmajor_bf16((CUtensorMap*)map, base, rows, cols, box_rows);
 }
 
+cudaError_t encode_tmap_bf16_rows128(void* map, const void* base, uint64_t rows, uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t dims[4] = {64, 8, 2, rows / 8};
+  const cuuint64_t strides[3] = {256, 128, 2048};
+  const cuuint32_t box[4] = {64, 8, 2, box_rows / 8};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn((CUtensorMap*)map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
+                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 cudaError_t encode_tmap_u8_sw128(void* map, const void* base, uint64_t rows, uint64_t cols_bytes, uint32_t box_rows) {
   return encode_rowmajor((CUtensorMap*)map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, rows, cols_bytes, 128, box_rows,
                          CU_TENSOR_MAP_SWIZZLE_128B);
