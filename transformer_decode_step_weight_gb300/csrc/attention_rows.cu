@@ -22,12 +22,13 @@
 //     the products.
 // A row is held by two threads, one in each half of the softmax warps. bf16: they take whole
 // tiles in turn, S runs three tiles ahead of P V in three buffers, each product has a warp that
-// issues it, and while one half writes a row tile out the other begins the next. What bounds a
-// long prompt is then about even: 1024 cycles of products and as many of exponentials per tile,
-// some 1500 in all; 8192 tokens of 32 q heads (8 kv heads) take 394 us, 1395 TFLOP/s. Both
+// issues it, and while one half writes a row tile out the other begins the next. A long prompt is
+// bound by the products: they are 1024 of some 1420 cycles per tile (the tensor pipe 72 % active,
+// at the clock that power leaves), the exponentials 520, beside them; 8192 tokens of 32 q heads (8
+// kv heads) take 394 us, 1395 TFLOP/s, 0.73 of the measured bf16 rate. Both
 // halves on one tile, 64 keys each: 558 us; one warp for both products, whatever the softmax did:
 // 2100 cycles per tile; two row tiles per CTA, whose S has one buffer each: 643 us. Short row
-// tiles (16 messages of 20 to 300 tokens: 76 us) are bound by the start and the end of each, most
+// tiles (16 messages of 20 to 700 tokens: 76 us) are bound by the start and the end of each, most
 // of which is code that the instruction cache does not hold. f32: three products for each of
 // bf16's, both halves on one tile, since O is summed in registers.
 //

