@@ -67,7 +67,7 @@ constexpr int kPassed = 7;
 // other half needs to write the row tile before out. 8192 tokens with 2, 3, 4, 5, 6, 8, 12: 453,
 // 429, 413, 398, 398, 406, 418 us.
 constexpr int kSolo = 5;
-constexpr int kMisc = 3072;              // barriers and small arrays in front of Q and the ring
+constexpr int kMisc = 3 * 1024;              // barriers and small arrays in front of Q and the ring
 constexpr int kData = 7 * kSlot;         // 224 KB: Q parts and ring slots
 constexpr size_t kSmem = kMisc + kData;  // 227 KB, the whole opt-in shared memory
 constexpr int kMaxSlots = 6;
