@@ -28,7 +28,7 @@
 // kv heads) take 394 us, 1395 TFLOP/s, 0.73 of the measured bf16 rate. Both
 // halves on one tile, 64 keys each: 558 us; one warp for both products, whatever the softmax did:
 // 2100 cycles per tile; two row tiles per CTA, whose S has one buffer each: 643 us. Short row
-// tiles (16 messages of 20 to 700 tokens: 76 us) are bound by the start and the end of each, most
+// tiles (16 messages of 20 to 700 tokens: 72 us) are bound by the start and the end of each, most
 // of which is code that the instruction cache does not hold. f32: three products for each of
 // bf16's, both halves on one tile, since O is summed in registers.
 //
@@ -165,8 +165,8 @@ QD_DEV uint64_t desc_v(uint32_t saddr) {
 }
 QD_DEV void tma_load_rows(void* dst, const CUtensorMap* map, int row, uint64_t* bar) {   // row: a multiple of 8
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3}], [%4];" ::"r"(
-          smem_u32(dst)),
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3}], "
+      "[%4];" ::"r"(smem_u32(dst)),
       "l"((uint64_t)map), "r"(0), "r"(row >> 3), "r"(smem_u32(bar))
       : "memory");
 }
@@ -202,6 +202,12 @@ QD_DEV void commit(bool lead, uint64_t* bar) {
       : "memory");
 }
 
+// 32 rows of a tile's results, dims 64 half .. + 63, from shared memory as Q lies there
+QD_DEV void tma_store_rows(const CUtensorMap* map, int half, int head, int row, const void* src) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"((uint64_t)map),
+               "r"(64 * half), "r"(head), "r"(row), "r"(smem_u32(src))
+               : "memory");
+}
 QD_DEV void cp16(uint32_t dst, const void* src, int bytes) {   // bytes 0: zeros, nothing read
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
@@ -362,7 +368,7 @@ __device__ __noinline__ void patch_row(const Params& p, const int32_t* pt, int g
 template <typename T, int PARTS, bool PROMPT>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                     const __grid_constant__ Params p) {
+                     const __grid_constant__ CUtensorMap tmO, const __grid_constant__ Params p) {
   // bf16: two buffers of Q, so that S of the next piece follows this one's; f32: three parts of
   // one. What goes out is gathered in the place of the Q that it was made with.
   constexpr bool kEarlyQ = PARTS == 1;
@@ -1259,7 +1265,20 @@ __global__ void __launch_bounds__(kThreads, 1)
               patch_row(p, pt, g, k0 * kKeys, min(lim, k1 * kKeys), d0,
                         mine + (final_out ? (d0 >> 6) * (kChunk - 128) : 0), final_out ? xr : 0, final_out);
           }
-          if (final_out) {
+          // a warp whose 32 rows are all there hands them to the copy engine (row by row they took
+          // 2300 cycles of the warp, as long as a tile), the last rows of a prompt go one by one
+          if (final_out && (warp & 3) * 32 + 32 <= rows && !__any_sync(0xffffffffu, dead)) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              const int r0 = (warp & 3) * 32, head = g << p.log_rep, at_row = first_row + (r0 >> p.log_rep);
+              tma_store_rows(&tmO, 0, head, at_row, old_q + r0 * 128);
+              tma_store_rows(&tmO, 1, head, at_row, old_q + kChunk + r0 * 128);
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+              asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            }
+            __syncwarp();   // before the next Q
+          } else if (final_out) {
             __syncwarp();
             __nv_bfloat16* out = (__nv_bfloat16*)p.out + tile0 * kD + 8 * (lane & 15);
 #pragma unroll 4
@@ -1410,10 +1429,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 int grid_ctas() { return std::min(dev_info().sm_count, kMaxGrid); }
 
 template <typename T, int PARTS, bool PROMPT>
-cudaError_t launch(const Params& p, const CUtensorMap& tk, const CUtensorMap& tv, const Launch& L) {
+cudaError_t launch(const Params& p, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to,
+                   const Launch& L) {
   cudaError_t e = allow_smem<attn_rows_kernel<T, PARTS, PROMPT>>(kSmem);
   if (e != cudaSuccess) return e;
-  return launch_ex(attn_rows_kernel<T, PARTS, PROMPT>, dim3(grid_ctas()), dim3(kThreads), kSmem, L, tk, tv, p);
+  return launch_ex(attn_rows_kernel<T, PARTS, PROMPT>, dim3(grid_ctas()), dim3(kThreads), kSmem, L, tk, tv, to, p);
 }
 
 // Workspace: tickets, then the partials; the shared form's prefix results behind them.
@@ -1443,9 +1463,14 @@ cudaError_t run(const AttnRowsArgs& a, float* pre_o, AttnFrom* from, const Launc
   p.pre_l = pre_o ? p.pre_m + (size_t)a.n_rows * a.Hq : nullptr;
   p.err = L.err;
   // boxes of whole 16-row pieces of a page; other page sizes by 16-byte asynchronous copies
-  alignas(64) CUtensorMap tk, tv;
+  alignas(64) CUtensorMap tk, tv, to;
   memset(&tk, 0, sizeof(tk));
   memset(&tv, 0, sizeof(tv));
+  memset(&to, 0, sizeof(to));
+  if (PROMPT && !a.q_f32) {
+    const cudaError_t e = encode_tmap_bf16_heads(&to, a.out, a.n_rows, a.Hq, p.rep, 32 / p.rep);
+    if (e != cudaSuccess) return e;
+  }
   if (a.page_size % 16 == 0) {
     p.box = 16;
     while (p.box < kKeys && a.page_size % (2 * p.box) == 0) p.box *= 2;
@@ -1454,7 +1479,7 @@ cudaError_t run(const AttnRowsArgs& a, float* pre_o, AttnFrom* from, const Launc
     if (e == cudaSuccess) e = encode_tmap_bf16_rows128(&tv, a.v_pages, rows, p.box);
     if (e != cudaSuccess) return e;
   }
-  return a.q_f32 ? launch<float, 3, PROMPT>(p, tk, tv, L) : launch<__nv_bfloat16, 1, PROMPT>(p, tk, tv, L);
+  return a.q_f32 ? launch<float, 3, PROMPT>(p, tk, tv, to, L) : launch<__nv_bfloat16, 1, PROMPT>(p, tk, tv, to, L);
 }
 
 }  // namespace
