@@ -439,7 +439,7 @@ static int check_attn_rows(const char* fn, AttnRowsArgs& a, const void* q, int q
   if (q_is_f32 != 0 && q_is_f32 != 1) return fail(QD_ERR_INVALID_ARG, "%s: q_is_f32=%d", fn, q_is_f32);
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) || !aligned16(workspace))
     return fail(QD_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
-  if (q_stride < (int64_t)hq * hd || q_stride % (q_is_f32 ? 4 : 8) || q_stride > ((int64_t)1 << 40))
+  if (q_stride < (int64_t)hq * hd || q_stride % (q_is_f32 ? 4 : 8) || q_stride >= ((int64_t)1 << 39))
     return fail(QD_ERR_INVALID_ARG, "%s: q_stride=%lld", fn, (long long)q_stride);
   if ((int64_t)n_pages * hkv * ps > INT32_MAX)
     return fail(QD_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 (page, kv head, slot) rows in the cache", fn);

@@ -202,6 +202,13 @@ QD_DEV void commit(bool lead, uint64_t* bar) {
       : "memory");
 }
 
+QD_DEV void tma_load_rows3(void* dst, const CUtensorMap* map, int half, int head, int row, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          smem_u32(dst)),
+      "l"((uint64_t)map), "r"(64 * half), "r"(head), "r"(row), "r"(smem_u32(bar))
+      : "memory");
+}
 // 32 rows of a tile's results, dims 64 half .. + 63, from shared memory as Q lies there
 QD_DEV void tma_store_rows(const CUtensorMap* map, int half, int head, int row, const void* src) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"((uint64_t)map),
@@ -368,7 +375,8 @@ __device__ __noinline__ void patch_row(const Params& p, const int32_t* pt, int g
 template <typename T, int PARTS, bool PROMPT>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                     const __grid_constant__ CUtensorMap tmO, const __grid_constant__ Params p) {
+                     const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
+                     const __grid_constant__ Params p) {
   // bf16: two buffers of Q, so that S of the next piece follows this one's; f32: three parts of
   // one. What goes out is gathered in the place of the Q that it was made with.
   constexpr bool kEarlyQ = PARTS == 1;
@@ -512,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     s_patch[0] = s_patch[1] = 0;
     mbar_init(o_free, kSoft / 2);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], kEarlyQ ? kSoft / 2 : kSoft);
+      mbar_init(&q_full[i], !kEarlyQ ? kSoft : p.q_sign > 0.f ? 4 : kSoft / 2);
       mbar_init(&drained[i], 1);
     }
     fence_mbar_init();
@@ -582,6 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   [[maybe_unused]] uint32_t trades = 0;
   [[maybe_unused]] int begins = 0;   // bf16: the holder of the piece's first tile
   [[maybe_unused]] bool behind = false;
+  [[maybe_unused]] int q_last = -1;   // bf16: the last piece whose Q this thread's copies brought
   int late = -1;
   // position and phase in a ring
   struct Ring {
@@ -848,7 +857,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                      (long long)(x.g << p.log_rep) * kD;
         const int qrows = min(W.tpt(), x.a.n - (W.step_tile(x.t) << W.log_tpt)) << p.log_rep;
         if constexpr (PARTS == 1) {
-          // warp w of the holder that calls it copies rows 32 w .. as they are, two at a time
+          // warp w of the half that calls it copies rows 32 w .. as they are (rows of the box that
+          // are not the tile's hold anything)
+          if (p.q_sign > 0.f) {
+            fence_proxy_async_smem();   // results went out from here
+            __syncwarp();
+            if (lane == 0 && *(volatile int*)s_abort == 0) {
+              const int r0 = (warp & 3) * 32, head = x.g << p.log_rep;
+              const int at_row = x.a.row0 + (W.step_tile(x.t) << W.log_tpt) + (r0 >> p.log_rep);
+              mbar_arrive_expect_tx(&q_full[qb], 32 * 256);
+              tma_load_rows3(dst + r0 * 128, &tmQ, 0, head, at_row, &q_full[qb]);
+              tma_load_rows3(dst + kChunk + r0 * 128, &tmQ, 1, head, at_row, &q_full[qb]);
+              q_last = (int)(piece_no + (first ? 0u : 1u));
+            }
+            __syncwarp();
+            return;
+          }
+          // a scale that is not positive: through q_ready, two rows at a time
           constexpr int kPer = 32;
           const uint32_t d0 = smem_u32(dst);
           const int c = lane & 15;
@@ -888,8 +913,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto q_ready = [&]([[maybe_unused]] uint32_t qb) {
         [[maybe_unused]] unsigned char* dst = data + qb * kSlot;
         if constexpr (PARTS == 1) {
+          if (p.q_sign > 0.f) return;
           asm volatile("cp.async.wait_group 0;" ::: "memory");
-          if (p.q_sign <= 0.f) {   // a negative scale: this thread's pieces negated; none: zeros
+          {   // a negative scale: this thread's pieces negated; none: zeros
             constexpr int kPer = 32;
             const int c = lane & 15;
             const uint32_t keep = p.q_sign < 0.f ? 0xffffffffu : 0u, flip = p.q_sign < 0.f ? 0x80008000u : 0u;
@@ -1414,6 +1440,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (again || tile >= slots) mbar_wait_limit(&full[slot0 + i], again ? rk.ph : rk.ph ^ 1, p.err, 10000000ull);
     }
   }
+  if (q_last >= 0 && *(volatile int*)s_abort)
+    mbar_wait_limit(&q_full[q_last & 1], (q_last >> 1) & 1, p.err, 10000000ull);
   if ((warp == kIssueS || warp == kIssueO) && *(volatile int*)s_abort) {   // ... and the products (bounded)
     commit(lane == 0, &drained[warp == kIssueO]);
     mbar_wait_limit(&drained[warp == kIssueO], 0, p.err, 10000000ull);
@@ -1429,11 +1457,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 int grid_ctas() { return std::min(dev_info().sm_count, kMaxGrid); }
 
 template <typename T, int PARTS, bool PROMPT>
-cudaError_t launch(const Params& p, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to,
-                   const Launch& L) {
+cudaError_t launch(const Params& p, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
+                   const CUtensorMap& to, const Launch& L) {
   cudaError_t e = allow_smem<attn_rows_kernel<T, PARTS, PROMPT>>(kSmem);
   if (e != cudaSuccess) return e;
-  return launch_ex(attn_rows_kernel<T, PARTS, PROMPT>, dim3(grid_ctas()), dim3(kThreads), kSmem, L, tk, tv, to, p);
+  return launch_ex(attn_rows_kernel<T, PARTS, PROMPT>, dim3(grid_ctas()), dim3(kThreads), kSmem, L, tk, tv, tq, to,
+                   p);
 }
 
 // Workspace: tickets, then the partials; the shared form's prefix results behind them.
@@ -1463,12 +1492,15 @@ cudaError_t run(const AttnRowsArgs& a, float* pre_o, AttnFrom* from, const Launc
   p.pre_l = pre_o ? p.pre_m + (size_t)a.n_rows * a.Hq : nullptr;
   p.err = L.err;
   // boxes of whole 16-row pieces of a page; other page sizes by 16-byte asynchronous copies
-  alignas(64) CUtensorMap tk, tv, to;
+  alignas(64) CUtensorMap tk, tv, tq, to;
   memset(&tk, 0, sizeof(tk));
   memset(&tv, 0, sizeof(tv));
+  memset(&tq, 0, sizeof(tq));
   memset(&to, 0, sizeof(to));
-  if (PROMPT && !a.q_f32) {
-    const cudaError_t e = encode_tmap_bf16_heads(&to, a.out, a.n_rows, a.Hq, p.rep, 32 / p.rep);
+  if (!a.q_f32) {
+    cudaError_t e = encode_tmap_bf16_heads(&tq, a.q, a.n_rows, a.q_stride, a.Hq, p.rep, 32 / p.rep);
+    if (e == cudaSuccess && PROMPT)
+      e = encode_tmap_bf16_heads(&to, a.out, a.n_rows, (int64_t)a.Hq * kD, a.Hq, p.rep, 32 / p.rep);
     if (e != cudaSuccess) return e;
   }
   if (a.page_size % 16 == 0) {
@@ -1479,7 +1511,8 @@ cudaError_t run(const AttnRowsArgs& a, float* pre_o, AttnFrom* from, const Launc
     if (e == cudaSuccess) e = encode_tmap_bf16_rows128(&tv, a.v_pages, rows, p.box);
     if (e != cudaSuccess) return e;
   }
-  return a.q_f32 ? launch<float, 3, PROMPT>(p, tk, tv, to, L) : launch<__nv_bfloat16, 1, PROMPT>(p, tk, tv, to, L);
+  return a.q_f32 ? launch<float, 3, PROMPT>(p, tk, tv, tq, to, L)
+                 : launch<__nv_bfloat16, 1, PROMPT>(p, tk, tv, tq, to, L);
 }
 
 }  // namespace

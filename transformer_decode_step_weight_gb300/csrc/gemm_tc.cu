@@ -919,12 +919,12 @@ cudaError_t encode_tmap_bf16_rows128(void* map, const void* base, uint64_t rows,
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t encode_tmap_bf16_heads(void* map, const void* base, uint64_t rows, uint64_t heads, uint32_t box_heads,
-                                   uint32_t box_rows) {
+cudaError_t encode_tmap_bf16_heads(void* map, const void* base, uint64_t rows, uint64_t stride, uint64_t heads,
+                                   uint32_t box_heads, uint32_t box_rows) {
   auto fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
   const cuuint64_t dims[3] = {128, heads, rows};
-  const cuuint64_t strides[2] = {256, heads * 256};
+  const cuuint64_t strides[2] = {256, stride * 2};
   const cuuint32_t box[3] = {64, box_heads, box_rows};
   const cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = fn((CUtensorMap*)map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,

@@ -153,9 +153,10 @@ cudaError_t encode_tmap_bf16_2d(void* map, const void* base, uint64_t rows, uint
 // Rows of 128 elements (a multiple of 8 of them), box of box_rows whole rows: it lands as groups of
 // 8 rows, in each the 128-byte-swizzled atom of columns 0 .. 63, then that of the others.
 cudaError_t encode_tmap_bf16_rows128(void* map, const void* base, uint64_t rows, uint32_t box_rows);
-// [rows, heads, 128], box of 64 columns of box_heads heads of box_rows rows, 128-byte swizzle.
-cudaError_t encode_tmap_bf16_heads(void* map, const void* base, uint64_t rows, uint64_t heads, uint32_t box_heads,
-                                   uint32_t box_rows);
+// [rows, heads, 128], rows `stride` elements apart; box of 64 columns of box_heads heads of box_rows
+// rows, 128-byte swizzle.
+cudaError_t encode_tmap_bf16_heads(void* map, const void* base, uint64_t rows, uint64_t stride, uint64_t heads,
+                                   uint32_t box_heads, uint32_t box_rows);
 // K splits a launch of this shape takes, and the workspace they need.
 int gemm_tc_splits(int R, int K, bool q8 = false);
 size_t gemm_tc_workspace_bytes(int R, int K, bool q8 = false);
