@@ -25,10 +25,10 @@
 // issues it, and while one half writes a row tile out the other begins the next. A long prompt is
 // bound by the products: they are 1024 of some 1420 cycles per tile (the tensor pipe 72 % active,
 // at the clock that power leaves), the exponentials 520, beside them; 8192 tokens of 32 q heads (8
-// kv heads) take 394 us, 1395 TFLOP/s, 0.73 of the measured bf16 rate. Both
+// kv heads) take 390 us, 1410 TFLOP/s, 0.74 of the measured bf16 rate. Both
 // halves on one tile, 64 keys each: 558 us; one warp for both products, whatever the softmax did:
 // 2100 cycles per tile; two row tiles per CTA, whose S has one buffer each: 643 us. Short row
-// tiles (16 messages of 20 to 700 tokens: 72 us) are bound by the start and the end of each, most
+// tiles (16 messages of 20 to 700 tokens: 71 us) are bound by the start and the end of each, most
 // of which is code that the instruction cache does not hold. f32: three products for each of
 // bf16's, both halves on one tile, since O is summed in registers.
 //
@@ -64,7 +64,7 @@ constexpr int kThreads = 32 * (kSoftWarps + 4);
 // kPassed + 4 holder + quarter: the holder has written its reference (7 to 14)
 constexpr int kPassed = 7;
 // Tiles that the half which begins a row tile takes before the two alternate: about as long as the
-// other half needs to write the row tile before out. 8192 tokens with 2, 3, 4, 5, 6, 8, 12: 453,
+// other half needs to write the row tile before out. 8192 tokens, results stored row by row, with 2, 3, 4, 5, 6, 8, 12: 453,
 // 429, 413, 398, 398, 406, 418 us.
 constexpr int kSolo = 5;
 constexpr int kMisc = 3 * 1024;              // barriers and small arrays in front of Q and the ring
