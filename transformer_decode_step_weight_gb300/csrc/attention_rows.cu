@@ -64,8 +64,8 @@ constexpr int kThreads = 32 * (kSoftWarps + 4);
 // kPassed + 4 holder + quarter: the holder has written its reference (7 to 14)
 constexpr int kPassed = 7;
 // Tiles that the half which begins a row tile takes before the two alternate: about as long as the
-// other half needs to write the row tile before out. 8192 tokens, results stored row by row, with 2, 3, 4, 5, 6, 8, 12: 453,
-// 429, 413, 398, 398, 406, 418 us.
+// other half needs to write the row tile before out. 8192 tokens with 2, 3, 4, 5, 6, 8, 12, results
+// stored row by row: 453, 429, 413, 398, 398, 406, 418 us; as now with 4, 5, 6: 394, 394, 396.
 constexpr int kSolo = 5;
 constexpr int kMisc = 3 * 1024;              // barriers and small arrays in front of Q and the ring
 constexpr int kData = 7 * kSlot;         // 224 KB: Q parts and ring slots
@@ -204,8 +204,8 @@ QD_DEV void commit(bool lead, uint64_t* bar) {
 
 QD_DEV void tma_load_rows3(void* dst, const CUtensorMap* map, int half, int head, int row, uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-          smem_u32(dst)),
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(smem_u32(dst)),
       "l"((uint64_t)map), "r"(64 * half), "r"(head), "r"(row), "r"(smem_u32(bar))
       : "memory");
 }
