@@ -253,7 +253,7 @@ struct Work {
   QD_DEV Seg seg(const Params& p, int s) const {
     Seg a;
     a.row0 = p.cu[s];
-    a.n = p.cu[s + 1] - a.row0;
+    a.n = (int)((uint32_t)p.cu[s + 1] - (uint32_t)a.row0);   // (refused below where the ends make no sense)
     a.len = PROMPT ? p.seq_lens[s] : p.shared_lens[s];
     a.bad = a.n > 0 && (a.len < 0 || a.len > p.cap);
     a.off = a.len - a.n;
@@ -431,8 +431,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < per; ++i) {
       const int s = tid * per + i;
       if (s >= p.n_seg) break;
+      // the ends themselves: their difference may pass 32 bits
+      const int lo = p.cu[s], hi = p.cu[s + 1];
+      bad = bad || lo < 0 || hi < lo || hi > p.n_rows;
       const Seg a = W.seg(p, s);
-      bad = bad || a.n < 0 || a.row0 < 0 || a.row0 + a.n > p.n_rows;
       if (a.bad && blockIdx.x == 0) set_error(p.err, QD_DEVERR_POS);
       most = max(most, a.tiles);
       if (a.tiles) saved += (long long)a.len * (a.n - 1);
