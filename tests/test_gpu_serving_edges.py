@@ -30,3 +30,22 @@ def test_attention_starts_far_apart_are_refused(cuda_lib, monkeypatch, cu, dtype
     pt20 = pt[:1].expand(20, -1).contiguous()
     api.attn_decode_shared(q, kp, vp, pt20, _ints([64] * 20), _ints(cu), _ints([32] * n), SCALE, out=out)
     assert api.check_device_error() == 2 and bool((out == 3).all())
+
+
+@pytest.mark.parametrize("max_seqs,max_pages,new", [(2048, 1 << 20, 1 << 20), (1, 1 << 30, 1 << 30),
+                                                    (2, 1 << 30, 1 << 30), (2048, 1 << 19, 1 << 19)])
+def test_extension_by_more_pages_than_32_bits_count_is_refused_whole(cuda_lib, max_seqs, max_pages, new):
+    # pages of one token: 2^31, 2^30, 2^31 and 2^30 of them are wanted, 64 exist
+    g = _gen(51)
+    k = [torch.randn((64, 1, 1, 8), generator=g, device=DEV).to(torch.bfloat16)]
+    c = api.PageCache.empty(k, [k[0].clone()], max_seqs, max_pages)
+    c.extend(_ints([5] + [0] * (max_seqs - 1)))
+    before = c.refs.clone()
+    c.extend(_ints([new - 5] + [new] * (max_seqs - 1)))
+    assert api.check_device_error() == 32
+    assert torch.equal(c.refs, before) and int(c.seq_lens.sum()) == 5
+    assert c.page_table[0, :6].tolist() == [0, 1, 2, 3, 4, -1]
+    for s in range(0, max_seqs, 97):
+        assert bool((c.page_table[s, 5 if s == 0 else 0:] == -1).all())
+    c.extend(_ints([59] + [0] * (max_seqs - 1)))     # the workspace is left ready
+    assert api.check_device_error() == 0 and int(c.refs.sum()) == 64

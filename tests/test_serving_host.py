@@ -1,0 +1,36 @@
+"""Host-side checks of the serving operators' arithmetic and of refusals at the largest sizes (no GPU)."""
+import os
+import subprocess
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "transformer_decode_step_weight_gb300", "csrc")
+
+def _run(tmp_path, source):
+    src, exe = tmp_path / "check.cpp", tmp_path / "check"
+    src.write_text(source)
+    subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-I", CSRC, str(src), "-o", str(exe)], check=True)
+    return subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()
+
+def test_pages_wanted_by_the_largest_extensions(tmp_path):
+    # the plan's own arithmetic: needs of every sequence, summed as the planning kernel sums them
+    cases = [(2048, 1 << 20, 0, 1, 0), (2048, 1 << 30, 0, 1, 0), (1, 1 << 30, 0, 1, 0), (2, 1 << 30, 0, 1, 0),
+             (2048, (1 << 30) - 7, 7, 16, 1), (2048, 5, 3, 16, 1), (2048, 0, 3, 16, 0), (3, 33, 16, 16, 0)]
+    lines = "".join(f"  one({n}, {new}, {length}, {ps}, {copy});\n" for n, new, length, ps, copy in cases)
+    got = [int(x) for x in _run(tmp_path, f"""#include <stdio.h>
+#include "page_plan.h"
+using namespace qd;
+static void one(int seqs, int n_new, int len, int ps, bool copy) {{
+  PageSum sum = 0;
+  for (int s = 0; s < seqs; ++s) {{
+    const PageNeed x = page_need(len, n_new, ps, copy);
+    if (x.copy() != copy) sum -= 1;
+    sum += x.pages();
+  }}
+  printf("%lld\\n", (long long)sum);
+}}
+int main() {{
+{lines}  return 0;
+}}
+""")]
+    want = [n * (-(-(length + new) // ps) - -(-length // ps) + copy) for n, new, length, ps, copy in cases]
+    assert got == want and max(want) == 2 ** 41

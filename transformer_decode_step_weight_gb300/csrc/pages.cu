@@ -20,6 +20,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.cuh"
+#include "page_plan.h"
 
 #include <algorithm>
 
@@ -44,22 +45,21 @@ struct Ws {
   int32_t *src, *dst, *map;
 };
 
-QD_DEV int pages_of(int tokens, int ps) { return tokens / ps + (tokens % ps != 0); }
-
 // Inclusive sum over the CTA's threads in thread order; total: the whole sum.
-QD_DEV int block_scan(int v, int* warp_sums, int& total) {
+template <typename S>
+QD_DEV S block_scan(S v, S* warp_sums, S& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __syncthreads();   // warp_sums of the scan before have been read
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, v, o);
+    const S x = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += x;
   }
   if (lane == 31) warp_sums[warp] = v;
   __syncthreads();
-  int before = 0, all = 0;
+  S before = 0, all = 0;
   for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
-    const int s = warp_sums[w];
+    const S s = warp_sums[w];
     if (w < warp) before += s;
     all += s;
   }
@@ -191,9 +191,9 @@ __global__ void __launch_bounds__(kPlan) pages_extend_kernel(PageState c, Ws ws,
   pdl_launch_dependents();   // the copies wait for this kernel before they read the list
   int32_t* cand = sh;                     // [max_seqs] a shared last page, or -1
   int32_t* at = cand + c.max_seqs;        // [max_seqs] first new page of the sequence
-  int32_t* need = at + c.max_seqs;        // [max_seqs] pages it takes; bit 30: the first is a copy
+  int32_t* need = at + c.max_seqs;        // [max_seqs] the page's count, then what it takes (PageNeed)
+  __shared__ PageSum sums[kPlan / 32];
   __shared__ int warp_sums[kPlan / 32], s_bad, s_copies;
-  constexpr int kCopyBit = 1 << 30;
   const int tid = threadIdx.x, ps = c.page_size;
   const long long cap = (long long)c.max_pages * ps;
   if (tid == 0) s_bad = s_copies = 0;
@@ -223,13 +223,11 @@ __global__ void __launch_bounds__(kPlan) pages_extend_kernel(PageState c, Ws ws,
     }
     return;
   }
-  int base = 0;
+  PageSum base = 0;
   for (int s0 = 0; s0 < c.max_seqs; s0 += kPlan) {
     const int s = s0 + tid;
-    int w = 0;
+    PageSum w = 0;
     if (s < c.max_seqs) {
-      const int n = max(n_new[s], 0), len = c.lens[s];
-      if (n > 0) w = pages_of(len + n, ps) - pages_of(len, ps);
       const int q = cand[s];
       bool copy = false;
       if (q >= 0) {   // the sharers extended before this one have left the page
@@ -241,19 +239,20 @@ __global__ void __launch_bounds__(kPlan) pages_extend_kernel(PageState c, Ws ws,
         for (; j < s; ++j) before += cand[j] == q;
         copy = need[s] - before > 1;
       }
-      need[s] = w + (copy ? (1 | kCopyBit) : 0);
-      w += copy;
+      const PageNeed x = page_need(c.lens[s], max(n_new[s], 0), ps, copy);
+      need[s] = (int)x.bits;
+      w = x.pages();
     }
-    int total;
-    const int incl = block_scan(w, warp_sums, total);
-    if (s < c.max_seqs) at[s] = base + incl - w;
+    PageSum total;
+    const PageSum incl = block_scan(w, sums, total);
+    if (s < c.max_seqs) at[s] = (int)(base + incl - w);   // (used where all of them exist)
     base += total;
   }
-  const int want = base;
+  const PageSum want = base;
   // at most n_pages ids fit the list (and exist)
   const int found = want > c.n_pages
                         ? 0
-                        : walk_pages(c.refs, 0, c.n_pages, true, 0, want, warp_sums,
+                        : walk_pages(c.refs, 0, c.n_pages, true, 0, (int)want, warp_sums,
                                      [&](int rank, int page) { ws.map[rank] = page; });
   __syncthreads();
   if (found < want) {
@@ -268,8 +267,10 @@ __global__ void __launch_bounds__(kPlan) pages_extend_kernel(PageState c, Ws ws,
   for (int s = warp; s < c.max_seqs; s += kPlan / 32) {
     const int n = max(n_new[s], 0);
     if (n == 0) continue;
-    const int len = c.lens[s], had = pages_of(len, ps), w = need[s] & (kCopyBit - 1);
-    const bool copy = need[s] & kCopyBit;
+    const int len = c.lens[s], had = pages_of(len, ps);
+    const PageNeed x = {(uint32_t)need[s]};
+    const int w = x.pages();
+    const bool copy = x.copy();
     const int row0 = copy ? had - 1 : had;
     for (int i = lane; i < w; i += 32) {
       const int page = ws.map[at[s] + i];
