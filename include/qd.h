@@ -281,7 +281,8 @@ int qd_attn_decode_shared(const void* q, int q_is_f32, int64_t q_stride, const v
 /* k_cache, v_cache: host arrays of n_layers device pointers, each [n_pages,                  */
 /* n_kv_heads, page_size, head_dim] bf16. workspace: qd_pages_workspace_bytes(cache)            */
 /* bytes, zero-filled before its first use. 4-byte alignment for the int32 arrays.              */
-/* Limits: head_dim % 8 == 0, max_seqs <= 2048.                                                 */
+/* Limits: head_dim % 8 == 0, max_seqs <= 2048, max_pages * page_size <= 2^30; n_pages <= 2^30     */
+/* for all but qd_pages_copy.                                                                     */
 typedef struct {
   void* const* k_cache;
   void* const* v_cache;

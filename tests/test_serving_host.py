@@ -1,6 +1,12 @@
 """Host-side checks of the serving operators' arithmetic and of refusals at the largest sizes (no GPU)."""
+import ctypes as C
 import os
 import subprocess
+
+import pytest
+
+import test_serving_abi as abi
+from test_serving_abi import lib  # noqa: F401  (a fixture)
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "transformer_decode_step_weight_gb300", "csrc")
@@ -34,3 +40,14 @@ int main() {{
 """)]
     want = [n * (-(-(length + new) // ps) - -(-length // ps) + copy) for n, new, length, ps, copy in cases]
     assert got == want and max(want) == 2 ** 41
+
+
+@pytest.mark.parametrize("n_pages", [2 ** 30 + 1, 2 ** 31 - 1])
+def test_more_pages_than_the_walk_over_their_counts_takes_are_refused(lib, n_pages):  # noqa: F811
+    c = C.byref(abi._cache(n_pages=n_pages, workspace_bytes=1 << 40))
+    fake = abi.FAKE
+    assert lib.qd_pages_fork(c, fake, fake, 1, None) == -2
+    assert lib.qd_pages_extend(c, fake, None) == -2
+    assert lib.qd_pages_trim(c, fake, None) == -2
+    assert lib.qd_pages_compact(c, fake, None) == -2
+    assert b"n_pages" in lib.qd_last_error()

@@ -505,6 +505,7 @@ static int check_page_cache(const char* fn, const qd_page_cache* c, bool copies,
                   c->page_size);
     if (c->max_seqs > kPagesMaxSeqs)
       return fail(QD_ERR_UNSUPPORTED, "%s: max_seqs=%d (at most %d)", fn, c->max_seqs, kPagesMaxSeqs);
+    if (c->n_pages > (1 << 30)) return fail(QD_ERR_UNSUPPORTED, "%s: n_pages=%d (at most 2^30)", fn, c->n_pages);
     if (!aligned16(c->workspace)) return fail(QD_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", fn);
     if (c->workspace_bytes < pages_workspace_bytes(c->max_seqs, c->n_pages))
       return fail(QD_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, c->workspace_bytes,

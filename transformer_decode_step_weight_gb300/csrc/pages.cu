@@ -70,7 +70,8 @@ QD_DEV S block_scan(S v, S* warp_sums, S& total) {
 // One CTA walks the pages [lo, hi) in ascending order, 16 per thread at a time (each
 // warp 512 consecutive ones, 16 coalesced loads in flight), and calls put(rank, page) for
 // those with (refs == 0) == want_free, rank counting from `base`; stops once `limit` are
-// found. Returns base + the number found so far (the whole CTA).
+// found. Returns base + the number found so far (the whole CTA). hi <= 2^30: the indexes of the
+// last turn stay within 32 bits.
 template <typename Put>
 QD_DEV int walk_pages(const int32_t* refs, int lo, int hi, bool want_free, int base, int limit, int* warp_sums,
                       Put put) {
