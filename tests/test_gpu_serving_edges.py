@@ -49,3 +49,78 @@ def test_extension_by_more_pages_than_32_bits_count_is_refused_whole(cuda_lib, m
         assert bool((c.page_table[s, 5 if s == 0 else 0:] == -1).all())
     c.extend(_ints([59] + [0] * (max_seqs - 1)))     # the workspace is left ready
     assert api.check_device_error() == 0 and int(c.refs.sum()) == 64
+
+
+def _steep(g, n, hq, hkv, ps, top, prompt_rows=1):
+    """Caches of one sequence of n keys whose key `top` outweighs every other by far more than 32 bits hold."""
+    kp, vp, pt = _cache(g, [n], hkv, ps)
+    at = (pt[0, top // ps].long(), slice(None), top % ps)
+    kp[at] = 30.0
+    return kp, vp, pt
+
+
+def _is_value(got, want):
+    """A softmax of one weight w gives w v / w. f32: w v is the sum of three exact products (their adder truncates,
+    3 x 2^-23 at most), w in three parts (2^-25), the reciprocal and two products round (3 x 2^-24), together below
+    2^-20 of v. bf16: the weight's distance from 1 (a score of 490 rounded in f32, 2^-15) is below half a step of v,
+    a bf16 value, so v comes back."""
+    want = want.expand_as(got)
+    off = (got.double() - want.double()).abs()
+    assert bool((off <= (0 if got.dtype == torch.bfloat16 else 2.0 ** -20) * want.double().abs()).all())
+
+
+def _put(pages, pt, ps, key, value, dim=slice(None), row=0):
+    pages[int(pt[row, key // ps]), :, key % ps, dim] = value
+
+
+# a visible NaN or infinity whose weight is below what 32 bits hold, in a piece of its own: before and after the
+# piece that has all the weight
+@pytest.mark.parametrize("top,low", [(4990, 10), (10, 4990), (2500, 300)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_prompt_attention_joins_what_is_not_finite_in_pieces_of_no_weight(cuda_lib, top, low, dtype):
+    g = _gen(52)
+    n, hq, hkv, ps = 5000, 8, 1, 16
+    kp, vp, pt = _steep(g, n, hq, hkv, ps, top)
+    q = torch.ones((1, hq, D), dtype=dtype, device=DEV)
+    args = (q, kp, vp, pt, _ints([0, 1]), _ints([n]), SCALE)
+    _put(vp, pt, ps, low, math.nan, 3)
+    _put(vp, pt, ps, low, math.inf, 9)
+    _put(vp, pt, ps, low, -math.inf, 100)
+    out = api.attn_prompt(*args)[0]
+    assert bool(torch.isnan(out[:, 3]).all())
+    assert bool(torch.isposinf(out[:, 9]).all()) and bool(torch.isneginf(out[:, 100]).all())
+    rest = [d for d in range(D) if d not in (3, 9, 100)]
+    _is_value(out[:, rest], vp[int(pt[0, top // ps]), 0, top % ps][rest])   # one key has all the weight
+    # a key of NaN: its weight is NaN, whatever the others'
+    kp2, vp2, _ = _cache(g, [n], hkv, ps)
+    _put(kp2, pt, ps, top, 30.0)
+    _put(kp2, pt, ps, low, math.nan, 7)
+    out = api.attn_prompt(q, kp2, vp2, pt, _ints([0, 1]), _ints([n]), SCALE)
+    assert bool(torch.isnan(out).all())
+    assert api.check_device_error() == 0
+
+
+@pytest.mark.parametrize("top,low", [(2100, 10), (10, 3500), (3590, 2010), (2010, 3590), (50, 1990)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("min_mb", ["0", "80"])
+def test_shared_attention_joins_nan_in_pieces_of_no_weight(cuda_lib, monkeypatch, top, low, dtype, min_mb):
+    # keys of the prefix, of the own tokens' first split, of their last
+    monkeypatch.setenv("QD_SHARED_MIN_MB", min_mb)
+    g = _gen(53)
+    hq, hkv, ps, shared, n = 8, 2, 16, 2000, 3600
+    q = torch.ones((3, hq, D), dtype=dtype, device=DEV)
+    for what in ("value", "key"):
+        kp, vp, pt = _cache(g, [n] * 3, hkv, ps, [(0, shared // ps)] * 3)
+        for row in range(3):
+            _put(kp, pt, ps, top, 30.0, row=row)
+            _put(vp if what == "value" else kp, pt, ps, low, math.nan, 3, row=row)
+        out = api.attn_decode_shared(q, kp, vp, pt, _ints([n] * 3), _ints([0, 3]), _ints([shared]), SCALE)
+        if what == "key":
+            assert bool(torch.isnan(out).all())
+            continue
+        assert bool(torch.isnan(out[:, :, 3]).all())
+        rest = [d for d in range(D) if d != 3]
+        for row in range(3):
+            want = vp[int(pt[row, top // ps]), :, top % ps].repeat_interleave(hq // hkv, 0)
+            _is_value(out[row][:, rest], want[:, rest])
+    assert api.check_device_error() == 0

@@ -372,6 +372,29 @@ __device__ __noinline__ void patch_row(const Params& p, const int32_t* pt, int g
   }
 }
 
+// piece k of the np that CTAs c0, c0 + 1, ... computed of one row tile
+QD_DEV const float* piece_of(const Params& p, int c0, int k) {
+  return p.part + ((size_t)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * kPartFloats;
+}
+
+// Four values of a joined row that some piece reached with a weight of 0 (below what 32 bits hold):
+// the pieces' NaN and infinities count all the same.
+template <typename T>
+__device__ __noinline__ void patch_joined(const Params& p, int c0, int np, int row, T* out) {
+  float u[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int k = 0; k < np; ++k) {
+    const float4 v = __ldcg((const float4*)(piece_of(p, c0, k) + (size_t)row * kD) + (threadIdx.x & 31));
+    const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (!(fabsf(f[e]) < INFINITY)) u[e] += f[e];
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (u[e] != 0.f) out[e] = (T)u[e];
+}
+
 template <typename T, int PARTS, bool PROMPT>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -1338,7 +1361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bar_sync(gbar, kGroup);
         if (*last) {
           const int np = c1 - c0 + 1;
-          auto piece = [&](int k) { return p.part + ((size_t)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * kPartFloats; };
+          auto piece = [&](int k) { return piece_of(p, c0, k); };
           // A warp joins eight rows at a time: lane k has piece k's statistics (32 pieces at a time),
           // then four columns of O. Everything is read from L2 once, so what counts is how many
           // loads are under way.
@@ -1347,6 +1370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int r0 = (gid >> 5) * kJoin; r0 < rows; r0 += kGroup / 32 * kJoin) {
             float M[kJoin], L[kJoin];
             float4 acc[kJoin];
+            uint32_t zero = 0;   // bit j: a weight of row j was 0
 #pragma unroll
             for (int j = 0; j < kJoin; ++j) {
               M[j] = -INFINITY;
@@ -1371,17 +1395,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                 top = fmaxf(top, M[j]);
                 const float keep = M[j] == -INFINITY ? 1.f : ex2(M[j] - top);   // (O and L are 0 or NaN there)
-                // pieces that saw nothing: weight 1 for a sum and an O of 0 (or NaN)
+                // pieces that saw nothing: weight 1 for a sum and an O of 0 (or NaN); a weight of 0 (below
+                // what 32 bits hold) keeps a NaN
                 m4[j] = m4[j] == -INFINITY ? 1.f : ex2(m4[j] - top);
-                float sum = m4[j] != 0.f ? m4[j] * l4[j] : 0.f;
+                zero |= (keep == 0.f || m4[j] == 0.f ? 1u : 0u) << j;
+                float sum = m4[j] * l4[j];
 #pragma unroll
                 for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                L[j] = (keep != 0.f ? L[j] * keep : 0.f) + sum;
+                L[j] = L[j] * keep + sum;
                 if (keep != 1.f) {
-                  acc[j].x = keep != 0.f ? acc[j].x * keep : 0.f;
-                  acc[j].y = keep != 0.f ? acc[j].y * keep : 0.f;
-                  acc[j].z = keep != 0.f ? acc[j].z * keep : 0.f;
-                  acc[j].w = keep != 0.f ? acc[j].w * keep : 0.f;
+                  acc[j].x *= keep;
+                  acc[j].y *= keep;
+                  acc[j].z *= keep;
+                  acc[j].w *= keep;
                 }
                 M[j] = top;
               }
@@ -1395,7 +1421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < kJoin; ++j) {
                   const float x = __shfl_sync(0xffffffffu, m4[j], k);
-                  if (x != 0.f && r0 + j < rows) {
+                  if (r0 + j < rows) {
                     acc[j].x = fmaf(x, v[j].x, acc[j].x);
                     acc[j].y = fmaf(x, v[j].y, acc[j].y);
                     acc[j].z = fmaf(x, v[j].z, acc[j].z);
@@ -1414,7 +1440,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     make_uint2(bf2(acc[j].x * iv, acc[j].y * iv), bf2(acc[j].z * iv, acc[j].w * iv));
               else
                 *(float4*)((float*)p.out + o) = make_float4(acc[j].x * iv, acc[j].y * iv, acc[j].z * iv, acc[j].w * iv);
+              if (L[j] != L[j]) zero &= ~(1u << j);
             }
+            zero = __reduce_or_sync(0xffffffffu, zero);
+#pragma unroll 1
+            for (int j = 0; zero >> j && r0 + j < rows; ++j)
+              if ((zero >> j) & 1) patch_joined(p, c0, np, r0 + j, (T*)p.out + (tile0 + out_row(r0 + j)) * kD + 4 * lane);
           }
           bar_sync(gbar, kGroup);
           if (gid == 0) p.tickets[c0] = 0;

@@ -324,12 +324,13 @@ __global__ void __launch_bounds__(kTh, 3) attn_suffix_kernel(const __grid_consta
     if (tid < p.rep) {
       float M = s_max[tid];
       for (int k = 0; k < n; ++k) M = fmaxf(M, s_m[k][tid]);
-      const float old = s_max[tid] == -INFINITY ? 0.f : ex2(s_max[tid] - M);
-      float sum = s_sum[tid] == 0.f ? 0.f : s_sum[tid] * old;
+      // what has seen nothing yet: weight 1 for a sum and an O of 0 (or NaN)
+      const float old = s_max[tid] == -INFINITY ? 1.f : ex2(s_max[tid] - M);
+      float sum = s_sum[tid] * old;   // (a weight of 0 keeps a NaN)
       for (int k = 0; k < n; ++k) {
-        const float x = s_m[k][tid] == -INFINITY && s_l[k][tid] == 0.f ? 0.f : ex2(s_m[k][tid] - M);
+        const float x = s_m[k][tid] == -INFINITY ? 1.f : ex2(s_m[k][tid] - M);
         s_m[k][tid] = x;
-        if (x != 0.f) sum = fmaf(x, s_l[k][tid], sum);
+        sum = fmaf(x, s_l[k][tid], sum);
       }
       s_scale[tid] = old;
       s_max[tid] = M;
@@ -341,20 +342,18 @@ __global__ void __launch_bounds__(kTh, 3) attn_suffix_kernel(const __grid_consta
       if (h0 + 4 * u < p.rep) {
         const float f = s_scale[h0 + 4 * u];
         if (f != 1.f) {
-          acc[u].x = f == 0.f ? 0.f : acc[u].x * f;
-          acc[u].y = f == 0.f ? 0.f : acc[u].y * f;
-          acc[u].z = f == 0.f ? 0.f : acc[u].z * f;
-          acc[u].w = f == 0.f ? 0.f : acc[u].w * f;
+          acc[u].x *= f;
+          acc[u].y *= f;
+          acc[u].z *= f;
+          acc[u].w *= f;
         }
       }
   };
-  auto add = [&](int u, float x, const float4& v) {
-    if (x != 0.f) {
-      acc[u].x = fmaf(x, v.x, acc[u].x);
-      acc[u].y = fmaf(x, v.y, acc[u].y);
-      acc[u].z = fmaf(x, v.z, acc[u].z);
-      acc[u].w = fmaf(x, v.w, acc[u].w);
-    }
+  auto add = [&](int u, float x, const float4& v) {   // (a weight of 0 keeps a NaN)
+    acc[u].x = fmaf(x, v.x, acc[u].x);
+    acc[u].y = fmaf(x, v.y, acc[u].y);
+    acc[u].z = fmaf(x, v.z, acc[u].z);
+    acc[u].w = fmaf(x, v.w, acc[u].w);
   };
   weigh(kW);
 #pragma unroll
