@@ -229,8 +229,10 @@ int qd_attn_decode_paged_noalloc(const float* q, const void* k_pages, const void
 /* [batch] (both device). Keys a row does not see have no effect on it, NaN and       */
 /* infinities included. Errors on the device (QD_DEVERR_POS: cu_rows not ascending     */
 /* or past n_rows, which leaves all of out; a length past the table, which leaves the   */
-/* sequence's rows). workspace: device scratch of qd_attn_prompt_workspace_bytes()       */
-/* bytes for the current device, zero-filled before its first use (each call leaves it    */
+/* sequence's rows). A NaN that a row sees reaches it, however small its weight; an infinity in V  */
+/* gives that infinity, one in K a score of it (q_is_f32 = 1: NaN, since q enters in parts).        */
+/* workspace: device scratch of qd_attn_prompt_workspace_bytes() bytes for the current device,          */
+/* zero-filled before its first use (each call leaves it                                              */
 /* ready for the next, but for one that ends with QD_DEVERR_TIMEOUT: zero-fill it again);   */
 /* two calls that overlap on the GPU need two.                                              */
 /* Limits: head_dim == 128, n_q_heads / n_kv_heads in {1, 2, 4, 8}, batch <= 1024,      */
@@ -256,9 +258,9 @@ int qd_attn_prompt(const void* q, int q_is_f32, int64_t q_stride, const void* k_
 /* in qd_attn_prompt with one row per sequence: q, out [batch, n_q_heads, head_dim];          */
 /* page_table [batch, max_pages], seq_lens [batch]; cu_seqs: int32 [n_groups + 1],            */
 /* ascending; shared_lens: int32 [n_groups] (both device). seq_lens[b] == 0 gives out = 0.      */
-/* A visible infinity in K or V may give NaN where the sum over the keys would be infinite         */
-/* (f32 splits it into parts). After an error that leaves rows unwritten in qd_attn_prompt, out      */
-/* is undefined there.                                                                             */
+/* A visible NaN reaches the row, as in qd_attn_prompt; so does an infinity in V, or NaN in its      */
+/* place; one in K gives a score of it (q_is_f32 = 1: NaN, since q enters in parts). After an         */
+/* error that leaves rows unwritten in qd_attn_prompt, out is undefined there.                        */
 /* workspace: qd_attn_shared_workspace_bytes(...) bytes, zero-filled before its first use, for       */
 /* the current device, as in qd_attn_prompt.                                                        */
 /* Limits: as qd_attn_prompt, n_groups <= 1024, batch <= 65535.                                 */

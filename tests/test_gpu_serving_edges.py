@@ -124,3 +124,41 @@ def test_shared_attention_joins_nan_in_pieces_of_no_weight(cuda_lib, monkeypatch
             want = vp[int(pt[row, top // ps]), :, top % ps].repeat_interleave(hq // hkv, 0)
             _is_value(out[row][:, rest], want[:, rest])
     assert api.check_device_error() == 0
+
+
+# ---- scores of -inf (bf16 q; an f32 q splits into parts whose products with an infinity give NaN)
+
+
+def _without(kp, vp, pt, row, n, gone):
+    keep = [t for t in range(n) if t not in gone]
+    return ref.gather(kp, pt[row], n)[keep], ref.gather(vp, pt[row], n)[keep]
+
+
+def _near(got, q, k, v):
+    out, mag, vmax, dot = ref.attend(q.double().cpu(), k, v, k.shape[0], SCALE)
+    err = (got.double().cpu() - out).abs()
+    assert bool((err <= ref.attention_bound(out, mag, vmax, dot, k.shape[0], True)).all()), float(err.max())
+
+
+@pytest.mark.parametrize("gone", [[256], [0], [255, 256], [64, 65, 66], list(range(16)), list(range(0, 257, 2)),
+                                  list(range(256))])
+def test_scores_of_minus_infinity_weigh_nothing(cuda_lib, monkeypatch, gone):
+    # whole blocks and warps whose only scores are -inf beside others that are finite
+    g = _gen(54)
+    n, hq, hkv, ps = 257, 8, 2, 16
+    kp, vp, pt = _cache(g, [n], hkv, ps)
+    for t in gone:
+        _put(kp, pt, ps, t, -math.inf, 5)
+    q = torch.randn((1, hq, D), generator=g, device=DEV).to(torch.bfloat16)
+    q[:, :, 5] = 0.5
+    k, v = _without(kp, vp, pt, 0, n, gone)
+    _near(api.attn_prompt(q, kp, vp, pt, _ints([0, 1]), _ints([n]), SCALE)[0], q[0], k, v)
+    pt2 = pt.expand(2, -1).contiguous()
+    q2 = q.expand(2, -1, -1).contiguous()
+    for min_mb in ("0", "80"):
+        monkeypatch.setenv("QD_SHARED_MIN_MB", min_mb)
+        for shared in (0, 100, 256, 257):
+            out = api.attn_decode_shared(q2, kp, vp, pt2, _ints([n, n]), _ints([0, 2]), _ints([shared]), SCALE)
+            for row in range(2):
+                _near(out[row], q[0], k, v)
+    assert api.check_device_error() == 0

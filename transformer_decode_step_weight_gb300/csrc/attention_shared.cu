@@ -244,8 +244,10 @@ __global__ void __launch_bounds__(kTh, 3) attn_suffix_kernel(const __grid_consta
     }
     const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
     const float a0 = n0 == -INFINITY ? 1.f : ex2(m0 - n0), a1 = n1 == -INFINITY ? 1.f : ex2(m1 - n1);
-    float w[4] = {in0 ? ex2(sc[0] - n0) : 0.f, in0 ? ex2(sc[1] - n1) : 0.f, in1 ? ex2(sc[2] - n0) : 0.f,
-                  in1 ? ex2(sc[3] - n1) : 0.f};
+    // nothing but scores of -inf so far: weights 2^(-inf - 0)
+    const float r0 = n0 == -INFINITY ? 0.f : n0, r1 = n1 == -INFINITY ? 0.f : n1;
+    float w[4] = {in0 ? ex2(sc[0] - r0) : 0.f, in0 ? ex2(sc[1] - r1) : 0.f, in1 ? ex2(sc[2] - r0) : 0.f,
+                  in1 ? ex2(sc[3] - r1) : 0.f};
     l0 = l0 * a0 + (w[0] + w[2]);   // this lane's keys; the lanes are added at the end
     l1 = l1 * a1 + (w[1] + w[3]);
     m0 = n0;
