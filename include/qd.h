@@ -217,7 +217,8 @@ int qd_attn_decode_paged_noalloc(const float* q, const void* k_pages, const void
 /* position seq_lens[b] - n + j and sees that position and all before:            */
 /*   out[r, h, :] = sum_{t <= seq_lens[b] - n + j} softmax_t(scale * q[r,h,:].K_b[t,g,:]) */
 /*                  * V_b[t, g, :],   g = h / (n_q_heads / n_kv_heads)               */
-/* A row before position 0 (seq_lens[b] < n) sees nothing and gives 0. Rows of q  */
+/* A row before position 0 (seq_lens[b] < n) sees nothing and gives 0 (a row that    */
+/* sees keys whose scores are all -inf gives NaN, as its softmax does). Rows of q  */
 /* outside every sequence have no effect, and out is left as it was there.        */
 /* q: [n_rows, n_q_heads, head_dim], q_stride elements from one row to the next    */
 /* (>= n_q_heads * head_dim, a multiple of 16 bytes: q may be part of the QKV       */

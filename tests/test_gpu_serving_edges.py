@@ -162,3 +162,24 @@ def test_scores_of_minus_infinity_weigh_nothing(cuda_lib, monkeypatch, gone):
             for row in range(2):
                 _near(out[row], q[0], k, v)
     assert api.check_device_error() == 0
+
+
+@pytest.mark.parametrize("n", [1, 40, 300, 3000])
+def test_rows_whose_scores_are_all_minus_infinity_are_nan(cuda_lib, monkeypatch, n):
+    # keys are seen, so this is not the row of zeros that sees none: a sum of weights of 0 / 0
+    g = _gen(55)
+    hq, hkv, ps = 8, 2, 16
+    kp, vp, pt = _cache(g, [n], hkv, ps)
+    kp[:, :, :, 5] = -math.inf
+    q = torch.randn((2, hq, D), generator=g, device=DEV).to(torch.bfloat16)
+    q[:, :, 5] = 0.5
+    out = api.attn_prompt(q, kp, vp, pt, _ints([0, 2]), _ints([n]), SCALE)
+    assert bool(torch.isnan(out[1]).all())
+    assert bool((out[0] == 0).all()) if n == 1 else bool(torch.isnan(out[0]).all())
+    pt2 = pt.expand(2, -1).contiguous()
+    for min_mb in ("0", "80"):
+        monkeypatch.setenv("QD_SHARED_MIN_MB", min_mb)
+        for shared in (0, n // 2, n):
+            out = api.attn_decode_shared(q, kp, vp, pt2, _ints([n, 0]), _ints([0, 2]), _ints([shared]), SCALE)
+            assert bool(torch.isnan(out[0]).all()) and bool((out[1] == 0).all())
+    assert api.check_device_error() == 0

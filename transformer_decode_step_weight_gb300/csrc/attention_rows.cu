@@ -1220,7 +1220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool dead = *(volatile int*)s_abort != 0;
         const bool patch = *(volatile int*)(s_patch + (piece_no & 1)) == (int)piece_no + 1;
         const int col0 = 64 * hf;
-        const float f = !final_out ? 1.f : l == 0.f ? 0.f : 1.0f / l;   // a row that saw nothing gives 0
+        const float f = !final_out ? 1.f : lim == 0 ? 0.f : 1.0f / l;   // a row that sees no key gives 0
         // values go out by whole rows, through Q's place: 16-byte pieces, swizzled
         unsigned char* mine = data + row * 512;
         const int xr = row & 31;
@@ -1274,7 +1274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::fence_after();
           const bool dead = *(volatile int*)s_abort != 0;
           const bool patch = *(volatile int*)(s_patch + (piece_no & 1)) == (int)piece_no + 1;
-          const float f = !final_out ? 1.f : l == 0.f ? 0.f : 1.0f / l;   // a row that saw nothing gives 0
+          const float f = !final_out ? 1.f : lim == 0 ? 0.f : 1.0f / l;   // a row that sees no key gives 0
           const bool put = valid && !dead;
           // bf16 results go out by whole rows, through the place of the same rows of Q (which this
           // warp fills again); partial values as they are
@@ -1434,7 +1434,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < kJoin; ++j) {
               if (r0 + j >= rows) break;
               const size_t o = (tile0 + out_row(r0 + j)) * kD + 4 * lane;
-              const float iv = L[j] == 0.f ? 0.f : 1.0f / L[j];
+              const bool sees = a.off + (t << W.log_tpt) + ((r0 + j) >> p.log_rep) >= 0;   // (else 0)
+              const float iv = sees ? 1.0f / L[j] : 0.f;
               if constexpr (PARTS == 1)
                 *(uint2*)((__nv_bfloat16*)p.out + o) =
                     make_uint2(bf2(acc[j].x * iv, acc[j].y * iv), bf2(acc[j].z * iv, acc[j].w * iv));
