@@ -183,3 +183,145 @@ def test_rows_whose_scores_are_all_minus_infinity_are_nan(cuda_lib, monkeypatch,
             out = api.attn_decode_shared(q, kp, vp, pt2, _ints([n, 0]), _ints([0, 2]), _ints([shared]), SCALE)
             assert bool(torch.isnan(out[0]).all()) and bool((out[1] == 0).all())
     assert api.check_device_error() == 0
+
+
+# ---- values that are not finite, seen by some rows or by all
+
+
+@pytest.mark.parametrize("ps", [16, 24])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_prompt_attention_values_not_finite_reach_the_rows_that_see_them(cuda_lib, dtype, ps):
+    # in both halves of the dims, in tiles that only some rows of a row tile see and in tiles that all see
+    g = _gen(56)
+    n, hq, hkv = 200, 8, 2
+    kp, vp, pt = _cache(g, [n], hkv, ps)
+    cu, seqs, seen = _pack([140], [n])
+    q = torch.randn((140, hq, D), generator=g, device=DEV).to(dtype)
+    clean = vp.clone()
+    for key, value, dim in ((170, math.inf, 3), (180, -math.inf, 100), (150, math.nan, 64), (65, math.inf, 127),
+                            (75, -math.inf, 127), (70, -math.inf, 0)):
+        _put(vp, pt, ps, key, value, dim)
+        _put(clean, pt, ps, key, 0.0, dim)
+    out = api.attn_prompt(q, kp, vp, pt, _ints(cu), _ints([n]), SCALE)
+    at = torch.tensor(seen, device=DEV)[:, None]
+    assert bool((torch.isposinf(out[:, :, 3]) == (at > 170)).all())
+    assert bool((torch.isneginf(out[:, :, 100]) == (at > 180)).all())
+    assert bool((torch.isnan(out[:, :, 64]) == (at > 150)).all())
+    assert bool((torch.isposinf(out[:, :, 127]) == ((at > 65) & (at <= 75))).all())
+    assert bool((torch.isnan(out[:, :, 127]) == (at > 75)).all())
+    assert bool((torch.isneginf(out[:, :, 0]) == (at > 70)).all())
+    rest = [d for d in range(D) if d not in (0, 3, 64, 100, 127)]
+    assert bool(torch.isfinite(out[:, :, rest]).all())
+    # what is finite is right: the row's sum without the entries
+    fixed = torch.where(torch.isfinite(out), out, 0)
+    want = api.attn_prompt(q, kp, clean, pt, _ints(cu), _ints([n]), SCALE)
+    _check_rows(torch.where(torch.isfinite(out), out, want), q, kp, clean, pt, seqs, seen, range(0, 140, 9))
+    assert bool(torch.equal(fixed[:, :, rest], want[:, :, rest]))
+    assert api.check_device_error() == 0
+
+
+@pytest.mark.parametrize("rows", [1, 3])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_prompt_attention_values_not_finite_in_pieces(cuda_lib, dtype, rows):
+    # a long cache in pieces: each patches its own keys
+    g = _gen(57)
+    n, hq, hkv, ps = 9000, 8, 2, 16
+    kp, vp, pt = _cache(g, [n], hkv, ps)
+    cu, seqs, seen = _pack([rows], [n])
+    q = torch.randn((rows, hq, D), generator=g, device=DEV).to(dtype)
+    clean = vp.clone()
+    bad = ((100, math.inf, 3), (8998, -math.inf, 100), (4000, math.nan, 64), (20, math.inf, 127), (7000, -math.inf, 127),
+           (8999, math.nan, 1))
+    for key, value, dim in bad:
+        _put(vp, pt, ps, key, value, dim)
+        _put(clean, pt, ps, key, 0.0, dim)
+    out = api.attn_prompt(q, kp, vp, pt, _ints(cu), _ints([n]), SCALE)
+    want = api.attn_prompt(q, kp, clean, pt, _ints(cu), _ints([n]), SCALE)
+    for r in range(rows):
+        for dim, value in ((3, math.inf), (100, -math.inf if seen[r] > 8998 else None), (64, math.nan), (127, math.nan),
+                           (1, math.nan if seen[r] > 8999 else None)):
+            if value is None:
+                continue
+            got = out[r, :, dim]
+            assert bool(torch.isnan(got).all() if math.isnan(value) else (got == value).all()), (r, dim)
+            out[r, :, dim] = want[r, :, dim]
+    assert torch.equal(out, want)
+    assert api.check_device_error() == 0
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_shared_attention_prefix_values_that_some_rows_see(cuda_lib, monkeypatch, dtype, bad):
+    # a value between the lengths of two sequences of the group
+    monkeypatch.setenv("QD_SHARED_MIN_MB", "0")
+    g = _gen(58)
+    ps, hq, hkv, shared = 16, 8, 2, 200
+    lens = [250, 100, 200, 5, 151, 150]
+    kp, vp, pt = _cache(g, [256] * 6, hkv, ps, [(0, 13)] * 6)
+    q = torch.randn((6, hq, D), generator=g, device=DEV).to(dtype)
+    args = (_ints(lens), _ints([0, 6]), _ints([shared]), SCALE)
+    want = api.attn_decode_shared(q, kp, vp, pt, *args)
+    for dim in (3, 100):
+        _put(vp, pt, ps, 150, bad, dim)
+    out = api.attn_decode_shared(q, kp, vp, pt, *args)
+    see = torch.tensor([n > 150 for n in lens], device=DEV)
+    assert not bool(torch.isfinite(out[see][:, :, [3, 100]]).any())
+    if math.isnan(bad):
+        assert bool(torch.isnan(out[see][:, :, [3, 100]]).all())
+    out[see.nonzero()[:, 0][:, None], :, torch.tensor([3, 100], device=DEV)] = \
+        want[see.nonzero()[:, 0][:, None], :, torch.tensor([3, 100], device=DEV)]
+    # the other dims and rows to the last bit but for the zeroed entry's own products
+    _check_rows(out, q, kp, torch.where(torch.isfinite(vp), vp, 0), pt, list(range(6)), lens, [1, 3, 5])
+    assert torch.equal(out[~see], want[~see])
+    rest = [d for d in range(D) if d not in (3, 100)]
+    assert torch.equal(out[:, :, rest], want[:, :, rest])
+    assert api.check_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_prompt_attention_infinity_in_a_cache_of_300000_keys(cuda_lib, dtype):
+    # two row tiles per SM, each over all the keys, looked through for the infinity while other roles wait
+    g = _gen(59)
+    n, hq, hkv, ps = 300000, 8, 1, 128
+    rows = 2 * 152 * 16
+    kp, vp, pt = _cache(g, [n], hkv, ps)
+    _put(vp, pt, ps, 0, math.inf, 3)
+    _put(vp, pt, ps, n - rows // 2, -math.inf, 70)
+    q = torch.randn((rows, hq, D), generator=g, device=DEV).to(dtype)
+    cu, seqs, seen = _pack([rows], [n])
+    out = api.attn_prompt(q, kp, vp, pt, _ints(cu), _ints([n]), SCALE)
+    assert api.check_device_error() == 0
+    assert bool(torch.isposinf(out[:, :, 3]).all())
+    at = torch.tensor(seen, device=DEV)[:, None]
+    assert bool((torch.isneginf(out[:, :, 70]) == (at > n - rows // 2)).all())
+    rest = [d for d in range(D) if d not in (3, 70)]
+    assert bool(torch.isfinite(out[:, :, rest]).all())
+    clean = torch.where(torch.isfinite(vp), vp, 0)
+    fixed = torch.where(torch.isfinite(out), out, api.attn_prompt(q, kp, clean, pt, _ints(cu), _ints([n]), SCALE))
+    _check_rows(fixed, q, kp, clean, pt, seqs, seen, [0, rows // 2 + 1, rows - 1])
+
+
+def test_prompt_attention_looking_for_an_infinity_takes_a_few_times_the_call(cuda_lib):
+    # a warp's lanes share the search: 6 times the call without (each for its own row: 87)
+    g = _gen(60)
+    n, hq, hkv, ps = 8192, 32, 8, 64
+    kp, vp, pt = _cache(g, [n], hkv, ps)
+    q = torch.randn((n, hq, D), generator=g, device=DEV).to(torch.bfloat16)
+    ws = torch.zeros(api.attn_prompt_workspace_bytes(), dtype=torch.uint8, device=DEV)
+    out, cu, ln = torch.empty_like(q), _ints([0, n]), _ints([n])
+
+    def best():
+        times = []
+        for _ in range(5):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            api.attn_prompt(q, kp, vp, pt, cu, ln, SCALE, out=out, workspace=ws)
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+
+    clean = best()
+    _put(vp, pt, ps, 0, math.inf, 5)
+    assert best() < 25 * clean
+    assert bool(torch.isposinf(out[:, :, 5]).all()) and api.check_device_error() == 0
