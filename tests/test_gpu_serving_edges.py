@@ -325,3 +325,47 @@ def test_prompt_attention_looking_for_an_infinity_takes_a_few_times_the_call(cud
     _put(vp, pt, ps, 0, math.inf, 5)
     assert best() < 25 * clean
     assert bool(torch.isposinf(out[:, :, 5]).all()) and api.check_device_error() == 0
+
+
+# ---- sampled verification near a border
+
+
+def _near_border(r, u, tok, off):
+    """Token tok has mass, and the running sums around it hold u times the sum, but for `off` of the sum."""
+    c = np.cumsum(r.astype(np.float64))
+    border, slack = u * c[-1], off * c[-1]
+    assert r[tok] > 0 and c[tok] > border - slack and c[tok] - r[tok] <= border + slack, (tok, border, c[tok], r[tok])
+
+
+def _flat_stretch(seed, nudge):
+    """Masses whose border lies on a stretch of tokens without any: half of the sum on each side of it, up to
+    `nudge` 2^-53."""
+    g = np.random.default_rng(seed)
+    r = np.zeros((256, 4), np.float32)
+    live = g.random(100) < 0.5
+    live[0] = live[99] = False
+    live[60:] = False
+    n = int(live.sum())
+    r[:100][live] = (g.random((n, 4)) * 2.0 ** g.uniform(-12, 0, (n, 1)) / 400).astype(np.float32)
+    half = float(r.astype(np.float64).sum())
+    big = np.float32(half)
+    rest = half - float(big) + nudge * 2.0 ** -53
+    if rest < 0:
+        big = np.nextafter(big, np.float32(0))
+        rest = half - float(big) + nudge * 2.0 ** -53
+    r[200, 0], r[210, 0] = big, np.float32(rest)
+    r[220, 0] = np.float32(max(0.0, rest - float(np.float32(rest))))
+    return r.ravel()
+
+
+def test_verify_sample_border_on_a_stretch_without_mass(cuda_lib):
+    # sums added in different orders disagree there in their last bits
+    rows = [_flat_stretch(seed, k) for seed in [296] + list(range(100)) for k in range(-4, 5)]
+    p = torch.from_numpy(np.stack(rows)).to(DEV)[:, None]
+    B = len(rows)
+    tok, pos, step = (torch.zeros(B, dtype=torch.int32, device=DEV) for _ in range(3))
+    out = torch.zeros((B, 2), dtype=torch.int32, device=DEV)
+    api.verify_sample(p, None, None, torch.full((B, 1), 0.5, device=DEV), tok, pos, step, out)
+    for b, t in enumerate(tok.tolist()):
+        _near_border(rows[b], 0.5, t, 2.0 ** -43)
+    assert api.check_device_error() == 0

@@ -121,7 +121,7 @@ QD_DEV double chunk_sum(const float* p, const float* q, int j0, int end, int vec
 }
 
 __global__ void __launch_bounds__(kTh) verify_sample_kernel(const __grid_constant__ VsParams p) {
-  __shared__ int s_m, s_n, s_last, s_tok, s_chunk, s_some;
+  __shared__ int s_m, s_n, s_last, s_tok, s_chunk, s_some, s_first;
   __shared__ Pair warp_sums[kTh / 32], s_prev[kTh];
   __shared__ double s_want;
   const int c = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
@@ -223,12 +223,16 @@ __global__ void __launch_bounds__(kTh) verify_sample_kernel(const __grid_constan
     __threadfence();
     __syncthreads();
   }
-  if (tid == 0) s_tok = s_some = -1;
+  if (tid == 0) {
+    s_tok = s_some = -1;
+    s_first = kTh;
+  }
   __syncthreads();
   if (s_chunk >= 0) {
-    // ---- its tokens in order: thread t takes chunk / kTh consecutive ones. Running sums never
-    // fall, so the first thread past the border holds the token; where rounding leaves none,
-    // the chunk's last token with any mass
+    // ---- its tokens in order: thread t takes chunk / kTh consecutive ones. The first thread with any
+    // mass whose running sum passes the border holds the token (of all threads, the first: the sums
+    // are added in another order for each, so in their last bits they may fall from one to the next);
+    // where rounding leaves none, the chunk's last token with any mass
     const int each = p.chunk / kTh, j0 = s_chunk * p.chunk + tid * each;
     const int end = min(p.V, j0 + each);
     Pair s{0.f, 0.f}, total;
@@ -253,9 +257,10 @@ __global__ void __launch_bounds__(kTh) verify_sample_kernel(const __grid_constan
       return d.hi > 0.f || (d.hi == 0.f && d.lo > 0.f);
     };
     if (last >= 0) atomicMax(&s_some, last);
-    const bool mine = over(incl);
-    const int votes = __syncthreads_count(!mine);   // the threads before the first one past the border
-    if (tid == min(votes, kTh - 1) && mine) {
+    const unsigned past = __ballot_sync(0xffffffffu, last >= 0 && over(incl));
+    if (lane == 0 && past) atomicMin(&s_first, (tid & ~31) + __ffs(past) - 1);
+    __syncthreads();
+    if (tid == s_first) {
       Pair a = tid ? s_prev[tid - 1] : Pair{0.f, 0.f};
 #pragma unroll 4
       for (int j = j0; j < end; ++j) {
