@@ -480,7 +480,8 @@ int qd_verify_step(const qd_step_args* args, const int32_t* draft, int k, float*
 /* if m < n (target_probs[b, m, :] if that is zero everywhere), r = target_probs[b, n, :] if    */
 /* m == n. Entries of r that are not finite count as 0; a row without mass gives 0 and sets       */
 /* QD_DEVERR_NAN; a draft outside the vocabulary is rejected; n_draft outside 0 .. k - 1 is        */
-/* clamped and sets QD_DEVERR_POS. Sums in 46 bits. The state advances as in                */
+/* clamped and sets QD_DEVERR_POS. The border is met to 2^-39 of the sum (2^-43      */
+/* measured). The state advances as in                                                             */
 /* qd_verify_step: n_accept[b] = m; out_tokens[b, step ..] = the m drafts, t; tok = t;               */
 /* pos += m + 1; step += m + 1 (past max_steps: QD_DEVERR_STEPS).                                    */
 /* target_probs: f32, row (b, i) at (b * k + i) * target_stride; draft_probs: f32, row (b, i) at       */

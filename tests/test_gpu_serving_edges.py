@@ -369,3 +369,29 @@ def test_verify_sample_border_on_a_stretch_without_mass(cuda_lib):
     for b, t in enumerate(tok.tolist()):
         _near_border(rows[b], 0.5, t, 2.0 ** -43)
     assert api.check_device_error() == 0
+
+
+@pytest.mark.parametrize("V", [151936, 4000])
+def test_verify_sample_border_among_many_small_masses(cuda_lib, V):
+    # two tokens of a half, thousands of 2^-27 between them, multiples of 2^-48 all (exact in float32); the border 2^-41
+    # before or behind the running sum of a small one, in a batch so large that each sequence is one chunk (594 and 16
+    # tokens to a thread). A right kernel: groups of 16 are off by 120 2^-49 of their sum, half of the total at most,
+    # two of them count, 14 additions of pairs by 1.5 2^-48 each: below 2^-41 together
+    B, half, delta = 640, 1 << 47, 1 << 7
+    g = _gen(61)
+    m = torch.randint(1 << 21, 1 << 22, (B, V), generator=g, device=DEV)
+    m[:, 0], m[:, V - 2:] = half, 0
+    c = m.cumsum(1)
+    j = torch.randint(V * 3 // 5, V - 10, (B,), generator=g, device=DEV)
+    sign = torch.where(torch.arange(B, device=DEV) % 2 == 0, 1, -1)
+    rest = 2 * (c.gather(1, j[:, None])[:, 0] + sign * delta) - c[:, -1]
+    m[:, V - 2], m[:, V - 1] = rest >> 24 << 24, rest & ((1 << 24) - 1)
+    assert bool((rest >= half).all())
+    p = (m.double() * 2.0 ** -48).float()
+    assert torch.equal((p.double() * 2.0 ** 48).long(), m)
+    tok, pos, step = (torch.zeros(B, dtype=torch.int32, device=DEV) for _ in range(3))
+    out = torch.zeros((B, 2), dtype=torch.int32, device=DEV)
+    api.verify_sample(p[:, None], None, None, torch.full((B, 1), 0.5, device=DEV), tok, pos, step, out)
+    want = torch.where(sign > 0, j + 1, j).int()
+    assert torch.equal(tok, want), int((tok != want).sum())
+    assert api.check_device_error() == 0

@@ -8,8 +8,12 @@
 // that are not finite count as 0.
 //
 // Which token is drawn hangs on where a sum over the vocabulary crosses a border, so the
-// sums are kept in pairs of floats (about 46 bits; binary64 adds run at 1/64 of the binary32
-// rate here): a border is misplaced by about 2^-45 of the total.
+// sums are kept in pairs of floats (binary64 adds run at 1/64 of the binary32 rate here). A thread
+// adds up groups of at most 32 tokens, each in a pair of its own whose low part is not renormalised
+// (off by at most 496 2^-49 of the group), and where it has more of them the groups in three floats;
+// the threads' sums go through 14 additions of pairs (1.5 2^-48 each), the chunks' are added in
+// binary64. So a border is misplaced by less than 2^-39 of the total whatever the vocabulary and the
+// batch; in models of the sums by 2^-43 at most, 2^-45 where the tokens are not all alike.
 //
 // One launch: CTA (chunk c, sequence b) finds m (k gathered values, the same in every
 // CTA), sums its chunk of the one or two rows that matter, and the sequence's last CTA
@@ -30,6 +34,7 @@ namespace qd {
 namespace {
 
 constexpr int kTh = 256;
+constexpr int kGroup = 32;   // tokens whose sum one pair of floats holds
 
 // an unevaluated sum hi + lo
 struct Pair {
@@ -69,6 +74,23 @@ QD_DEV void add_mass(Pair& s, float p, float q) {
   s.lo = __fadd_rn(s.lo, __fadd_rn(t.lo, some ? e : 0.f));
 }
 
+// A thread's groups of tokens but for the last.
+struct Groups {
+  float t0 = 0.f, t1 = 0.f, t2 = 0.f;
+  QD_DEV void take(Pair& g) {
+    const Pair a = two_sum(t0, g.hi), b = two_sum(t1, a.lo), c = two_sum(b.hi, g.lo);
+    t0 = a.hi;
+    t1 = c.hi;
+    t2 = __fadd_rn(t2, __fadd_rn(b.lo, c.lo));
+    g = Pair{0.f, 0.f};
+  }
+  QD_DEV Pair with(Pair g) {   // and the last
+    take(g);
+    const Pair s = two_sum(t0, t1);
+    return two_sum(s.hi, __fadd_rn(s.lo, t2));
+  }
+};
+
 // four tokens from j on; 0 past `end`
 QD_DEV float4 load4(const float* p, int j, int end, int vec) {
   if (vec && j + 4 <= end) return *(const float4*)(p + j);
@@ -97,9 +119,12 @@ __device__ __noinline__ Pair block_scan(Pair v, Pair* warp_sums, Pair* total) {
   return add(before, v);
 }
 
-// The CTA's sum of r over the tokens [j0, end): thread t takes every kTh-th group of four.
+// The CTA's sum of r over the tokens [j0, end): thread t takes every kTh-th four of them.
+// kMany: more than kGroup for a thread.
+template <bool kMany>
 QD_DEV double chunk_sum(const float* p, const float* q, int j0, int end, int vec, Pair* warp_sums) {
   Pair s{0.f, 0.f}, total;
+  Groups before;
   constexpr int kU = 4;
   for (int j = j0 + threadIdx.x * 4; j < end; j += kTh * 4 * kU) {
     float4 a[kU], b[kU];
@@ -115,11 +140,14 @@ QD_DEV double chunk_sum(const float* p, const float* q, int j0, int end, int vec
       add_mass(s, a[u].z, b[u].z);
       add_mass(s, a[u].w, b[u].w);
     }
+    if (kMany) before.take(s);
   }
+  if (kMany) s = before.with(s);
   block_scan(s, warp_sums, &total);
   return value(total);
 }
 
+template <bool kMany>
 __global__ void __launch_bounds__(kTh) verify_sample_kernel(const __grid_constant__ VsParams p) {
   __shared__ int s_m, s_n, s_last, s_tok, s_chunk, s_some, s_first;
   __shared__ Pair warp_sums[kTh / 32], s_prev[kTh];
@@ -159,7 +187,7 @@ __global__ void __launch_bounds__(kTh) verify_sample_kernel(const __grid_constan
   const float* qr = m < s_n ? p.draft_p + ((size_t)b * kd + m) * p.d_stride : nullptr;
   double* part = p.part + (size_t)b * nc;
   {
-    const double sum = chunk_sum(pr, qr, c * p.chunk, min((c + 1) * p.chunk, p.V), p.vec, warp_sums);
+    const double sum = chunk_sum<kMany>(pr, qr, c * p.chunk, min((c + 1) * p.chunk, p.V), p.vec, warp_sums);
     if (tid == 0) {
       part[c] = sum;
       s_last = atom_add_acq_rel_gpu(p.cnt + b, 1) == nc - 1;
@@ -217,7 +245,7 @@ __global__ void __launch_bounds__(kTh) verify_sample_kernel(const __grid_constan
     qr = nullptr;
 #pragma unroll 1
     for (int ch = 0; ch < nc; ++ch) {
-      const double sum = chunk_sum(pr, nullptr, ch * p.chunk, min((ch + 1) * p.chunk, p.V), p.vec, warp_sums);
+      const double sum = chunk_sum<kMany>(pr, nullptr, ch * p.chunk, min((ch + 1) * p.chunk, p.V), p.vec, warp_sums);
       if (tid == 0) part[ch] = sum;
     }
     __threadfence();
@@ -236,6 +264,7 @@ __global__ void __launch_bounds__(kTh) verify_sample_kernel(const __grid_constan
     const int each = p.chunk / kTh, j0 = s_chunk * p.chunk + tid * each;
     const int end = min(p.V, j0 + each);
     Pair s{0.f, 0.f}, total;
+    Groups earlier;
     int last = -1;
 #pragma unroll 4
     for (int j = j0; j < end; j += 4) {
@@ -247,7 +276,9 @@ __global__ void __launch_bounds__(kTh) verify_sample_kernel(const __grid_constan
         const float r = xs[i] - ys[i];
         if (r > 0.f && r < INFINITY) last = j + i;
       }
+      if (kMany && ((j - j0) & 12) == 12) earlier.take(s);
     }
+    if (kMany) s = earlier.with(s);
     const Pair incl = block_scan(s, warp_sums, &total);
     s_prev[tid] = incl;
     const double want = s_want;
@@ -261,14 +292,20 @@ __global__ void __launch_bounds__(kTh) verify_sample_kernel(const __grid_constan
     if (lane == 0 && past) atomicMin(&s_first, (tid & ~31) + __ffs(past) - 1);
     __syncthreads();
     if (tid == s_first) {
-      Pair a = tid ? s_prev[tid - 1] : Pair{0.f, 0.f};
+      // what the tokens before it leave to the border (below 0), and the group at hand
+      Pair base = tid ? add(s_prev[tid - 1], neg) : neg, a{0.f, 0.f};
 #pragma unroll 4
       for (int j = j0; j < end; ++j) {
         const float x = pr[j], y = qr ? qr[j] : 0.f, r = x - y;
         add_mass(a, x, y);
         if (r > 0.f && r < INFINITY) {
           s_tok = j;
-          if (over(a)) break;
+          const Pair d = add(base, a);
+          if (d.hi > 0.f || (d.hi == 0.f && d.lo > 0.f)) break;
+        }
+        if (kMany && ((j - j0) & (kGroup - 1)) == kGroup - 1) {
+          base = add(base, a);
+          a = Pair{0.f, 0.f};
         }
       }
     }
@@ -320,7 +357,8 @@ cudaError_t launch_verify_sample(const VerifySampleArgs& a, const Launch& L) {
   // about eight CTAs per SM, chunks a multiple of 1024 tokens
   const int chunks = (int)std::max(1LL, std::min((long long)kMaxChunks, 8LL * dev_info().sm_count / a.B));
   p.chunk = ceil_div(ceil_div(a.V, chunks), kTh * 4) * kTh * 4;
-  return launch_ex(verify_sample_kernel, dim3(ceil_div(a.V, p.chunk), a.B), dim3(kTh), 0, L, p);
+  return launch_ex(p.chunk > kTh * kGroup ? verify_sample_kernel<true> : verify_sample_kernel<false>,
+                   dim3(ceil_div(a.V, p.chunk), a.B), dim3(kTh), 0, L, p);
 }
 
 }  // namespace qd
