@@ -280,7 +280,10 @@ int qd_attn_decode_shared(const void* q, int q_is_f32, int64_t q_stride, const v
 /*   refs int32 [n_pages]: how many page-table entries name the page (0: free).          */
 /* New pages are the lowest free ids, taken in sequence order, so a call's result           */
 /* follows from its arguments alone. A call that cannot be carried out whole changes         */
-/* nothing and sets QD_DEVERR_CACHE.                                                          */
+/* nothing and sets QD_DEVERR_CACHE. A table entry within a sequence's length that names no      */
+/* page of the cache (the state is broken) sets QD_DEVERR_PAGE where a call meets it: qd_pages_fork  */
+/* copies it as it is, qd_pages_trim drops it, qd_pages_compact leaves it, and each does the rest;     */
+/* qd_pages_extend, whose tokens would go to it, changes nothing.                                       */
 /* k_cache, v_cache: host arrays of n_layers device pointers, each [n_pages,                  */
 /* n_kv_heads, page_size, head_dim] bf16. workspace: qd_pages_workspace_bytes(cache)            */
 /* bytes, zero-filled before its first use. 4-byte alignment for the int32 arrays.              */

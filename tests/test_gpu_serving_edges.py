@@ -395,3 +395,37 @@ def test_verify_sample_border_among_many_small_masses(cuda_lib, V):
     want = torch.where(sign > 0, j + 1, j).int()
     assert torch.equal(tok, want), int((tok != want).sum())
     assert api.check_device_error() == 0
+
+
+@pytest.mark.parametrize("bad", [-1, 20, 2 ** 31 - 1, -2 ** 31])
+def test_page_operations_pass_over_table_entries_that_name_no_page(cuda_lib, bad):
+    # pages of 4: sequence 0 has 5 pages (0 .. 4), sequence 1 has 2 (5, 6); sequence 0's third entry is broken
+    g = _gen(62)
+    k = [torch.randn((20, 2, 4, 8), generator=g, device=DEV).to(torch.bfloat16)]
+    c = api.PageCache.empty(k, [k[0].clone()], 5, 6)
+    c.extend(_ints([18, 7, 0, 0, 0]))
+    assert api.check_device_error() == 0
+    c.page_table[0, 2] = bad
+    c.refs[2] = 0
+    c.fork(_ints([0, 1]), _ints([3, 4]))          # as it is, the rest shared
+    assert api.check_device_error() == 1
+    assert c.page_table[3].tolist() == [0, 1, bad, 3, 4, -1] and c.page_table[4].tolist() == [5, 6, -1, -1, -1, -1]
+    assert c.seq_lens.tolist() == [18, 7, 0, 18, 7]
+    assert c.refs.tolist() == [2, 2, 0, 2, 2, 2, 2] + [0] * 13
+    c.trim(_ints([4, -1, -1, -1, 0]))             # dropped, the rest given back
+    assert api.check_device_error() == 1
+    assert c.page_table[0].tolist() == [0] + [-1] * 5 and c.seq_lens.tolist() == [4, 7, 0, 18, 0]
+    assert c.refs.tolist() == [2, 1, 0, 1, 1, 1, 1] + [0] * 13
+    live = c.compact()                            # left, the rest moved: 6 goes to 2
+    assert api.check_device_error() == 1 and int(live) == 6
+    assert c.page_table[3].tolist() == [0, 1, bad, 3, 4, -1] and c.page_table[1, :2].tolist() == [5, 2]
+    state = [t.clone() for t in (c.page_table, c.seq_lens, c.refs)]
+    c.page_table[3, 4] = bad                      # the partly filled last page: nothing is changed
+    state[0][3, 4] = bad
+    c.extend(_ints([1, 1, 0, 1, 0]))
+    assert api.check_device_error() == 33
+    assert all(torch.equal(a, b) for a, b in zip(state, (c.page_table, c.seq_lens, c.refs)))
+    # with a length past the table beside it: both errors, whichever thread comes first
+    c.extend(_ints([1, 20, 0, 1, 0]))
+    assert api.check_device_error() == 33
+    assert all(torch.equal(a, b) for a, b in zip(state, (c.page_table, c.seq_lens, c.refs)))

@@ -10,7 +10,8 @@
 // A fork shares every page of its parent, the partly filled last one too; whoever is
 // extended first copies that page (copy on write), and the last sharer keeps it. A call
 // that cannot be carried out whole (no free pages left, a length past the table, a bad
-// sequence id) changes nothing and sets QD_DEVERR_CACHE.
+// sequence id) changes nothing and sets QD_DEVERR_CACHE. A table entry that names no page is a fault
+// of the caller's, met only where the work is under way: it is passed over and QD_DEVERR_PAGE set.
 //
 // The copies are bound by HBM (16 KB per CTA turn, eight 16-byte loads per thread under way, eight
 // CTAs per SM): 783 MB read and written in some 130 us, 6.0 TB/s. Planning is latency: one CTA,
@@ -204,10 +205,10 @@ __global__ void __launch_bounds__(kPlan) pages_extend_kernel(PageState c, Ws ws,
     int q = -1;
     if (n > 0) {
       if (len < 0 || (long long)len + n > cap) {
-        s_bad = QD_DEVERR_CACHE;
+        atomicOr(&s_bad, QD_DEVERR_CACHE);
       } else if (len % ps) {
         const int p = c.table[(size_t)s * c.max_pages + len / ps];
-        if (p < 0 || p >= c.n_pages) s_bad = QD_DEVERR_CACHE | QD_DEVERR_PAGE;
+        if (p < 0 || p >= c.n_pages) atomicOr(&s_bad, QD_DEVERR_CACHE | QD_DEVERR_PAGE);
         else if (const int r = c.refs[p]; r > 1) {
           q = p;
           need[s] = r;
