@@ -4,9 +4,11 @@ import os
 import subprocess
 
 import pytest
+import torch
 
 import test_serving_abi as abi
 from test_serving_abi import lib  # noqa: F401  (a fixture)
+from transformer_decode_step_weight_gb300 import api
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "transformer_decode_step_weight_gb300", "csrc")
@@ -51,3 +53,16 @@ def test_more_pages_than_the_walk_over_their_counts_takes_are_refused(lib, n_pag
     assert lib.qd_pages_trim(c, fake, None) == -2
     assert lib.qd_pages_compact(c, fake, None) == -2
     assert b"n_pages" in lib.qd_last_error()
+
+
+def test_a_stream_of_another_device_is_refused():
+    # entering it would make its device current, and the call would then run on the tensors' own stream
+    class Tensor:
+        def get_device(self):
+            return 1
+
+    class Stream:
+        device = torch.device("cuda", 0)
+
+    with pytest.raises(ValueError, match="cuda:0"):
+        api._elsewhere(Tensor(), Stream())

@@ -282,6 +282,8 @@ def _elsewhere(t, stream):
     dev = t.get_device()
     if stream is None:
         return None if dev < 0 or _current_device() == dev else torch.cuda.device(dev)
+    if dev >= 0 and stream.device.index != dev:
+        raise ValueError(f"stream on {stream.device}, tensors on cuda:{dev}")
     return torch.cuda.stream(stream)
 
 
