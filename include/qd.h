@@ -233,12 +233,13 @@ int qd_attn_decode_paged_noalloc(const float* q, const void* k_pages, const void
 /* sequence's rows). A NaN that a row sees reaches it, however small its weight; an infinity in V  */
 /* gives that infinity, one in K a score of it (q_is_f32 = 1: NaN, since q enters in parts).        */
 /* workspace: device scratch of qd_attn_prompt_workspace_bytes() bytes for the current device,          */
-/* zero-filled before its first use (each call leaves it                                              */
+/* its first QD_ATTN_WORKSPACE_HEAD bytes zero-filled before its first use (each call leaves it         */
 /* ready for the next, but for one that ends with QD_DEVERR_TIMEOUT: zero-fill it again);   */
 /* two calls that overlap on the GPU need two.                                              */
 /* Limits: head_dim == 128, n_q_heads / n_kv_heads in {1, 2, 4, 8}, batch <= 1024,      */
 /* n_rows <= 2^20; the blocks of 128 q rows (a row and a q head of one kv head) by 128 keys   */
 /* that the call computes fewer than 2^31 (else QD_DEVERR_POS, and out is left as it was).    */
+#define QD_ATTN_WORKSPACE_HEAD 8192
 size_t qd_attn_prompt_workspace_bytes(void);
 int qd_attn_prompt(const void* q, int q_is_f32, int64_t q_stride, const void* k_pages, const void* v_pages,
                    const int32_t* page_table, const int32_t* cu_rows, const int32_t* seq_lens, int batch,
@@ -262,8 +263,8 @@ int qd_attn_prompt(const void* q, int q_is_f32, int64_t q_stride, const void* k_
 /* A visible NaN reaches the row, as in qd_attn_prompt; so does an infinity in V, or NaN in its      */
 /* place; one in K gives a score of it (q_is_f32 = 1: NaN, since q enters in parts). After an         */
 /* error that leaves rows unwritten in qd_attn_prompt, out is undefined there.                        */
-/* workspace: qd_attn_shared_workspace_bytes(...) bytes, zero-filled before its first use, for       */
-/* the current device, as in qd_attn_prompt.                                                        */
+/* workspace: qd_attn_shared_workspace_bytes(...) bytes for the current device, its head zero-filled   */
+/* before its first use, as in qd_attn_prompt.                                                      */
 /* Limits: as qd_attn_prompt, n_groups <= 1024, batch <= 65535.                                 */
 size_t qd_attn_shared_workspace_bytes(int batch, int n_q_heads, int n_kv_heads);
 int qd_attn_decode_shared(const void* q, int q_is_f32, int64_t q_stride, const void* k_pages, const void* v_pages,
@@ -490,7 +491,8 @@ int qd_verify_step(const qd_step_args* args, const int32_t* draft, int k, float*
 /* target_probs: f32, row (b, i) at (b * k + i) * target_stride; draft_probs: f32, row (b, i) at       */
 /* (b * (k - 1) + i) * draft_stride (may be NULL with draft when k == 1); draft: int32 [batch,          */
 /* k - 1]; u: f32 [batch, k] in [0, 1); n_accept: int32 [batch]; all device. workspace:                  */
-/* qd_verify_sample_workspace_bytes(batch) bytes, zero-filled before its first use. Limits:              */
+/* qd_verify_sample_workspace_bytes(batch) bytes, the first 4 * batch of them zero-filled before its      */
+/* first use (for calls of several sizes: of the largest batch). Limits:                                */
 /* 1 <= k <= 1024, vocab <= 4194304, batch <= 65535.                                                     */
 size_t qd_verify_sample_workspace_bytes(int batch);
 int qd_verify_sample(const float* target_probs, int64_t target_stride, const float* draft_probs,

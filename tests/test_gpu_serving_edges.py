@@ -429,3 +429,38 @@ def test_page_operations_pass_over_table_entries_that_name_no_page(cuda_lib, bad
     c.extend(_ints([1, 20, 0, 1, 0]))
     assert api.check_device_error() == 33
     assert all(torch.equal(a, b) for a, b in zip(state, (c.page_table, c.seq_lens, c.refs)))
+
+
+@pytest.mark.parametrize("min_mb", ["0", "80"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_workspaces_need_zeros_in_their_head_only(cuda_lib, monkeypatch, dtype, min_mb):
+    monkeypatch.setenv("QD_SHARED_MIN_MB", min_mb)
+    g = _gen(63)
+    hq, hkv, ps = 8, 2, 16
+    lens = [3000, 2500, 900, 0, 40]
+    kp, vp, pt = _cache(g, lens, hkv, ps, [(0, 50)] * 3 + [(1, 0)] * 2)
+    q = torch.randn((5, hq, D), generator=g, device=DEV).to(dtype)
+    ones = _ints(list(range(6)))
+    shared = (q, kp, vp, pt, _ints(lens), _ints([0, 3, 5]), _ints([800, 0]), SCALE)
+    p, d = (torch.softmax(torch.randn((5, k, 20000), generator=g, device=DEV), -1) for k in (3, 2))
+    draft = torch.randint(0, 20000, (5, 2), generator=g, device=DEV).int()
+    u = torch.rand((5, 3), generator=g, device=DEV)
+
+    def verify(ws):
+        state = [torch.zeros(5, dtype=torch.int32, device=DEV) for _ in range(3)]
+        out = torch.zeros((5, 8), dtype=torch.int32, device=DEV)
+        return torch.cat([api.verify_sample(p, d, draft, u, *state, out, workspace=ws)[:, None], out], 1)
+
+    for call, nbytes, head in (
+            (lambda ws: api.attn_prompt(q, kp, vp, pt, ones, _ints(lens), SCALE, workspace=ws),
+             api.attn_prompt_workspace_bytes(), 8192),
+            (lambda ws: api.attn_decode_shared(*shared, workspace=ws), api.attn_shared_workspace_bytes(5, hq, hkv), 8192),
+            (verify, api.verify_sample_workspace_bytes(5), 20)):
+        want = call(torch.zeros(nbytes, dtype=torch.uint8, device=DEV))
+        ws = torch.full((nbytes,), 255, dtype=torch.uint8, device=DEV)
+        ws[:head] = 0
+        for _ in range(3):
+            assert torch.equal(call(ws), want)
+            assert int(ws[:head].max()) == 0     # left ready
+        assert torch.equal(call(None), want)
+    assert api.check_device_error() == 0

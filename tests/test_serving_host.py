@@ -66,3 +66,8 @@ def test_a_stream_of_another_device_is_refused():
 
     with pytest.raises(ValueError, match="cuda:0"):
         api._elsewhere(Tensor(), Stream())
+
+
+def test_the_binding_zeroes_the_head_that_the_header_names():
+    header = open(os.path.join(ROOT, "include", "qd.h")).read()
+    assert int(header.split("#define QD_ATTN_WORKSPACE_HEAD")[1].split()[0]) == api._ATTN_HEAD

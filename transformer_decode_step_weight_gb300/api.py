@@ -320,9 +320,15 @@ def _rows(fn, q, k_pages, v_pages, page_table, seq_lens, cu, out):
     return s0 if n > 1 else hq * d
 
 
-def _scratch(workspace, nbytes, t):
+# What of a workspace has to be zero before its first use (QD_ATTN_WORKSPACE_HEAD in qd.h)
+_ATTN_HEAD = 8192
+
+
+def _scratch(workspace, nbytes, t, head):
     if workspace is None:
-        return torch.zeros(nbytes(), dtype=torch.uint8, device=t.device)
+        workspace = torch.empty(nbytes(), dtype=torch.uint8, device=t.device)
+        workspace[:head].zero_()
+        return workspace
     _want("workspace", workspace, torch.uint8, 1, t.get_device())
     return workspace
 
@@ -349,7 +355,7 @@ def attn_prompt(q, k_pages, v_pages, page_table, cu_rows, seq_lens, scale, out=N
         out = torch.empty((n, Hq, D), dtype=q.dtype, device=q.device)
     if n == 0:
         return out
-    workspace = _scratch(workspace, attn_prompt_workspace_bytes, q)
+    workspace = _scratch(workspace, attn_prompt_workspace_bytes, q, _ATTN_HEAD)
     _check(lib().qd_attn_prompt(q.data_ptr(), q.dtype is torch.float32, q_stride, k_pages.data_ptr(),
                                 v_pages.data_ptr(), page_table.data_ptr(), cu_rows.data_ptr(), seq_lens.data_ptr(),
                                 B, n, Hq, Hkv, D, ps, max_pages, n_pages, scale, out.data_ptr(),
@@ -383,7 +389,7 @@ def attn_decode_shared(q, k_pages, v_pages, page_table, seq_lens, cu_seqs, share
         out = torch.empty((B, Hq, D), dtype=q.dtype, device=q.device)
     if B == 0:
         return out
-    workspace = _scratch(workspace, lambda: attn_shared_workspace_bytes(B, Hq, Hkv), q)
+    workspace = _scratch(workspace, lambda: attn_shared_workspace_bytes(B, Hq, Hkv), q, _ATTN_HEAD)
     _check(lib().qd_attn_decode_shared(q.data_ptr(), q.dtype is torch.float32, q_stride, k_pages.data_ptr(),
                                        v_pages.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
                                        cu_seqs.data_ptr(), shared_lens.data_ptr(), groups, B, Hq, Hkv, D, ps,
@@ -431,7 +437,7 @@ def verify_sample(target_probs, draft_probs, draft, u, tok, pos, step, out_token
         raise ValueError(f"{fn}: out_tokens has {out_tokens.shape[0]} rows for {B} sequences")
     if B == 0:
         return n_accept
-    workspace = _scratch(workspace, lambda: verify_sample_workspace_bytes(B), target_probs)
+    workspace = _scratch(workspace, lambda: verify_sample_workspace_bytes(B), target_probs, 4 * B)
     _check(lib().qd_verify_sample(target_probs.data_ptr(), t_stride, draft_probs.data_ptr() if k > 1 else None,
                                   d_stride, draft.data_ptr() if k > 1 else None, _p(n_draft), u.data_ptr(), V, B, k,
                                   tok.data_ptr(), pos.data_ptr(), step.data_ptr(), out_tokens.data_ptr(),

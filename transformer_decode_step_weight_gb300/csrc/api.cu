@@ -416,6 +416,7 @@ int qd_attn_decode_paged_noalloc(const float* q, const void* k_pages, const void
 }
 
 // ------------------------------------------------------------------ packed rows
+static_assert(kAttnHeadBytes == QD_ATTN_WORKSPACE_HEAD, "the head that the header names");
 size_t qd_attn_prompt_workspace_bytes(void) { return attn_rows_workspace_bytes(); }
 
 size_t qd_attn_shared_workspace_bytes(int batch, int n_q_heads, int n_kv_heads) {

@@ -1534,8 +1534,8 @@ cudaError_t launch(const Params& p, const CUtensorMap& tk, const CUtensorMap& tv
                    p);
 }
 
-// Workspace: tickets, then the partials; the shared form's prefix results behind them.
-constexpr size_t kTicketBytes = 1024;
+// Workspace: the head with the tickets, then the partials.
+static_assert(kAttnRowTickets + kMaxGrid * 4 <= kAttnSeqTickets, "");
 
 template <bool PROMPT>
 cudaError_t run(const AttnRowsArgs& a, float* pre_o, AttnFrom* from, const Launch& L) {
@@ -1551,8 +1551,8 @@ cudaError_t run(const AttnRowsArgs& a, float* pre_o, AttnFrom* from, const Launc
   p.scale_log2 = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;
   p.q_sign = a.scale < 0.f ? -1.f : a.scale == 0.f ? 0.f : 1.f;
   p.out = a.out;
-  p.tickets = (int*)a.workspace;
-  p.part = (float*)((unsigned char*)a.workspace + kTicketBytes);
+  p.tickets = (int*)((unsigned char*)a.workspace + kAttnRowTickets);
+  p.part = (float*)((unsigned char*)a.workspace + kAttnHeadBytes);
   p.pre_o = pre_o;
   p.from = from;
   p.div = make_page_div(a.page_size);
@@ -1586,13 +1586,13 @@ cudaError_t run(const AttnRowsArgs& a, float* pre_o, AttnFrom* from, const Launc
 
 }  // namespace
 
-size_t attn_rows_workspace_bytes() { return kTicketBytes + (size_t)grid_ctas() * 2 * kPartFloats * 4; }
+size_t attn_rows_workspace_bytes() { return kAttnHeadBytes + (size_t)grid_ctas() * 2 * kPartFloats * 4; }
 
 cudaError_t launch_attn_prompt(const AttnRowsArgs& a, const Launch& L) { return run<true>(a, nullptr, nullptr, L); }
 
 cudaError_t launch_attn_prefix(const AttnRowsArgs& a, float* pre, AttnFrom* from, AttnPieces* pieces,
                                const Launch& L) {
-  *pieces = {(const float*)((const unsigned char*)a.workspace + kTicketBytes), grid_ctas()};
+  *pieces = {(const float*)((const unsigned char*)a.workspace + kAttnHeadBytes), grid_ctas()};
   return run<false>(a, pre, from, L);
 }
 

@@ -466,6 +466,7 @@ __global__ void __launch_bounds__(kTh, 3) attn_suffix_kernel(const __grid_consta
 // at; their place does not depend on the call, which keeps them zero between calls of
 // different sizes.
 constexpr size_t kTicketBytes = 4096;
+static_assert(kAttnSeqTickets + kTicketBytes <= kAttnHeadBytes, "");
 int want_ctas() { return std::min(4 * dev_info().sm_count, (int)(kTicketBytes / 4)); }
 
 // Splits per (sequence, kv head): about four CTAs per SM.
@@ -497,18 +498,17 @@ cudaError_t launch(const SParams& p, int n_splits, const Launch& L) {
 
 }  // namespace
 
-// attention_rows.cu's workspace, then the tickets, the prefix results (and where they are) and
-// the splits.
+// attention_rows.cu's workspace, whose head has the tickets, then the prefix results (and where they
+// are) and the splits.
 size_t attn_shared_workspace_bytes(int B, int Hq, int Hkv) {
-  return round256(attn_rows_workspace_bytes()) + kTicketBytes + pre_bytes(B, Hq) +
+  return round256(attn_rows_workspace_bytes()) + pre_bytes(B, Hq) +
          from_bytes(B, Hkv) + (size_t)B * Hkv * splits(B, Hkv) * split_floats(Hq / Hkv) * 4;
 }
 
 cudaError_t launch_attn_shared(const AttnRowsArgs& args, const Launch& L) {
   AttnRowsArgs a = args;
   a.share_min = share_min(a.Hkv);
-  unsigned char* ws = (unsigned char*)a.workspace + round256(attn_rows_workspace_bytes());
-  float* pre = (float*)(ws + kTicketBytes);
+  float* pre = (float*)((unsigned char*)a.workspace + round256(attn_rows_workspace_bytes()));
   Launch first = L;
   first.pdl = false;   // whatever ran before in the stream is done before either kernel reads
   AttnFrom* from = (AttnFrom*)((unsigned char*)pre + pre_bytes(a.n_rows, a.Hq));
@@ -529,7 +529,7 @@ cudaError_t launch_attn_shared(const AttnRowsArgs& args, const Launch& L) {
   p.from = from;
   p.div = make_page_div(a.page_size);
   p.share_min = a.share_min;
-  p.tickets = (int*)ws;
+  p.tickets = (int*)((unsigned char*)a.workspace + kAttnSeqTickets);
   p.part = (float*)((unsigned char*)from + from_bytes(a.n_rows, a.Hkv));
   p.err = L.err;
   const int n = splits(a.n_rows, a.Hkv);

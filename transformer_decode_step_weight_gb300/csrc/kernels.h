@@ -324,6 +324,10 @@ struct AttnRowsArgs {
   void* workspace;
   long long share_min;     // shared form: tokens whose re-reading must be saved for sharing to pay
 };
+// Head of a workspace, which has to be zero before its first use: tickets, at places that do not depend
+// on the call (they are zero again after each, so calls of different sizes can share it).
+constexpr size_t kAttnHeadBytes = 8192;
+constexpr size_t kAttnRowTickets = 0, kAttnSeqTickets = 1024;   // of attention_rows.cu, of attention_shared.cu
 size_t attn_rows_workspace_bytes();
 size_t attn_shared_workspace_bytes(int B, int Hq, int Hkv);
 cudaError_t launch_attn_prompt(const AttnRowsArgs& a, const Launch& L);
