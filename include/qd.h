@@ -250,7 +250,8 @@ int qd_attn_prompt(const void* q, int q_is_f32, int64_t q_stride, const void* k_
 /* Decode attention of sequences that share prefixes: the result of                 */
 /* qd_attn_decode_paged for sequences whose page tables name the same pages at their  */
 /* start (qd_pages_fork), each shared page read once for all of them. Where that would     */
-/* spare less than 80 MB of re-reading (QD_SHARED_MIN_MB, read at every call, sets another    */
+/* spare less than 80 MB of re-reading in the whole call, over all groups (QD_SHARED_MIN_MB, read at   */
+/* every call, sets another                                                                   */
 /* limit; 0: always share) each sequence reads its own table's pages, which is then faster.    */
 /* Group i holds                                                                               */
 /* the sequences cu_seqs[i] .. cu_seqs[i + 1); their first shared_lens[i] tokens lie in  */
@@ -264,7 +265,7 @@ int qd_attn_prompt(const void* q, int q_is_f32, int64_t q_stride, const void* k_
 /* place; one in K gives a score of it (q_is_f32 = 1: NaN, since q enters in parts). After an         */
 /* error that leaves rows unwritten in qd_attn_prompt, out is undefined there.                        */
 /* workspace: qd_attn_shared_workspace_bytes(...) bytes for the current device, its head zero-filled   */
-/* before its first use, as in qd_attn_prompt.                                                      */
+/* before its first use, as in qd_attn_prompt (whose calls it can serve as well).                   */
 /* Limits: as qd_attn_prompt, n_groups <= 1024, batch <= 65535.                                 */
 size_t qd_attn_shared_workspace_bytes(int batch, int n_q_heads, int n_kv_heads);
 int qd_attn_decode_shared(const void* q, int q_is_f32, int64_t q_stride, const void* k_pages, const void* v_pages,

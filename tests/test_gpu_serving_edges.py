@@ -464,3 +464,65 @@ def test_workspaces_need_zeros_in_their_head_only(cuda_lib, monkeypatch, dtype, 
             assert int(ws[:head].max()) == 0     # left ready
         assert torch.equal(call(None), want)
     assert api.check_device_error() == 0
+
+
+# ---- calls that share a workspace, the largest sizes
+
+
+def test_one_workspace_for_both_attentions_and_two_graphs(cuda_lib, monkeypatch):
+    g = _gen(64)
+    hq, hkv, ps = 8, 2, 16
+    lens = [3000, 2500, 2900]
+    kp, vp, pt = _cache(g, lens, hkv, ps, [(0, 150)] * 3)
+    ln, ones, cu, sl = _ints(lens), _ints([0, 1, 2, 3]), _ints([0, 3]), _ints([2400])
+    ws = torch.zeros(api.attn_shared_workspace_bytes(3, hq, hkv), dtype=torch.uint8, device=DEV)
+    qs = [torch.randn((3, hq, D), generator=g, device=DEV).to(t) for t in (torch.float32, torch.bfloat16)]
+
+    def prompt(q, **kw):
+        return api.attn_prompt(q, kp, vp, pt, ones, ln, SCALE, **kw)
+
+    def shared(q, **kw):
+        return api.attn_decode_shared(q, kp, vp, pt, ln, cu, sl, SCALE, **kw)
+
+    graphs, want, outs = [], [], []
+    for min_mb in ("0", "80"):
+        monkeypatch.setenv("QD_SHARED_MIN_MB", min_mb)
+        for q in qs:
+            for call in (prompt, shared):
+                want.append(call(q))
+                for _ in range(2):
+                    assert torch.equal(call(q, workspace=ws), want[-1])
+                outs.append(torch.zeros_like(q))
+                graphs.append(torch.cuda.CUDAGraph())
+                with torch.cuda.graph(graphs[-1]):
+                    call(q, out=outs[-1], workspace=ws)
+    r = np.random.default_rng(64)
+    for i in r.integers(0, len(graphs), 40):
+        outs[i].zero_()
+        graphs[i].replay()
+        assert torch.equal(outs[i], want[i])
+    assert api.check_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_attention_of_the_most_rows_and_sequences(cuda_lib, monkeypatch, dtype):
+    g = _gen(65)
+    n, B, ps = 1 << 20, 1024, 16
+    kp, vp, _ = _cache(g, [1040], 1, ps, spare=0)
+    pt = torch.randint(0, kp.shape[0], (B, 65), generator=g, device=DEV).int()
+    lens = [1024 + b % 17 for b in range(B)]
+    q = torch.randn((n, 1, D), generator=g, device=DEV).to(dtype)
+    cu, seqs, seen = _pack([1024] * B, lens)
+    out = api.attn_prompt(q, kp, vp, pt, _ints(cu), _ints(lens), SCALE)
+    _check_rows(out, q, kp, vp, pt, seqs, seen, [0, 1023, 1024, 500000, 777777, n - 1024, n - 1])
+    B = 65535
+    pt = torch.randint(0, kp.shape[0], (B, 3), generator=g, device=DEV).int()
+    starts = [min(B, 64 * i) for i in range(1025)]
+    for i in range(0, 1024):
+        pt[starts[i]:starts[i + 1], 0] = pt[starts[i], 0]
+    lens = [16 + b % 33 for b in range(B)]
+    for min_mb in ("0", "80"):
+        monkeypatch.setenv("QD_SHARED_MIN_MB", min_mb)
+        out = api.attn_decode_shared(q[:B], kp, vp, pt, _ints(lens), _ints(starts), _ints([16] * 1024), SCALE)
+        _check_rows(out, q[:B], kp, vp, pt, list(range(B)), lens, [0, 63, 64, 30000, 65472, B - 1])
+    assert api.check_device_error() == 0
