@@ -16,7 +16,9 @@
 // V is read as it lies in the cache (keys x dims) through an MN-major descriptor, so no
 // transposed copy exists. Two rings of 32 KB slots hold K and V tiles.
 //   * bf16 q: weights rounded to bf16 (each off by 2^-8 of itself at most, as the
-//     result's own rounding); sums, statistics and O in f32.
+//     result's own rounding); sums, statistics and O in f32. Results are 2.0e-3 to 2.5e-3 off the 64-bit
+//     form (2-norms), with weights in f32 they would be 1.5e-3 to 1.7e-3; two parts of a weight would cost
+//     half as many products again, and those bound the kernel. (With an f32 q: 3e-7.)
 //   * f32 q: q and the weights as three bf16 parts each (24 bits; two would leave
 //     2.4e-6 of each weight, above what an f32 sum of the same length loses), three times
 //     the products.

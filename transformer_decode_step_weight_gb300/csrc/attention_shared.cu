@@ -1,9 +1,11 @@
 // Decode attention of sequences that share prefixes. Two launches: attention_rows.cu reads
 // each group's shared tokens once for all of its sequences and leaves (O, m, l) of every
 // (sequence, q head); the kernel here reads each sequence's own tokens and joins the two.
-// It starts while the first one runs and waits for it only to join. 64 sequences with 4096 shared
-// tokens (f32, 32 q heads, 8 kv heads): 48 us, of which the launches alone are 10, the own tokens
-// 12, the prefix and its join 26; 32768 shared tokens (bf16): 66 us, 134 MB of K and V.
+// It may be launched while the first one runs and waits for it only to join, but a CTA of the first
+// takes all of an SM's shared memory and nearly all of its registers, so that it begins early only on
+// SMs that have no prefix work left: mostly the two run one after the other. 64 sequences with 4096
+// shared tokens (f32, 32 q heads, 8 kv heads): 48 us (the own tokens alone 21, the prefix alone with its
+// join 34, either with the launches' 9); 32768 shared tokens (bf16): 66 us, 134 MB of K and V.
 //
 // Own tokens: CTA (split, kv head, sequence); HBM-bound, so the work only has to keep enough
 // bytes in flight, and most of a short sequence's time is the chain of loads before its first
