@@ -247,25 +247,23 @@ int qd_attn_prompt(const void* q, int q_is_f32, int64_t q_stride, const void* k_
                    int n_pages, float scale, void* out, void* workspace, size_t workspace_bytes,
                    cudaStream_t stream);
 
-/* Decode attention of sequences that share prefixes: the result of                 */
-/* qd_attn_decode_paged for sequences whose page tables name the same pages at their  */
-/* start (qd_pages_fork), each shared page read once for all of them. Where that would     */
-/* spare less than 80 MB of re-reading in the whole call, over all groups (QD_SHARED_MIN_MB, read at   */
-/* every call, sets another                                                                   */
-/* limit; 0: always share) each sequence reads its own table's pages, which is then faster.    */
-/* Group i holds                                                                               */
-/* the sequences cu_seqs[i] .. cu_seqs[i + 1); their first shared_lens[i] tokens lie in  */
-/* the pages of the group's first sequence's row (a sequence shorter than that sees its   */
-/* own seq_lens tokens of them). Sequences outside every group are left as they were.      */
-/* shared_lens[i] may be 0 and need not be a multiple of page_size. Arguments as            */
-/* in qd_attn_prompt with one row per sequence: q, out [batch, n_q_heads, head_dim];          */
-/* page_table [batch, max_pages], seq_lens [batch]; cu_seqs: int32 [n_groups + 1],            */
-/* ascending; shared_lens: int32 [n_groups] (both device). seq_lens[b] == 0 gives out = 0.      */
-/* A visible NaN reaches the row, as in qd_attn_prompt; so does an infinity in V, or NaN in its      */
-/* place; one in K gives a score of it (q_is_f32 = 1: NaN, since q enters in parts). After an         */
-/* error that leaves rows unwritten in qd_attn_prompt, out is undefined there.                        */
-/* workspace: qd_attn_shared_workspace_bytes(...) bytes for the current device, its head zero-filled   */
-/* before its first use, as in qd_attn_prompt (whose calls it can serve as well).                   */
+/* Decode attention of sequences that share prefixes: the result of qd_attn_decode_paged for      */
+/* sequences whose page tables name the same pages at their start (qd_pages_fork), each shared     */
+/* page read once for all of them. Where that would spare less than 80 MB of re-reading in the     */
+/* whole call, over all groups (QD_SHARED_MIN_MB, read at every call, sets another limit; 0:       */
+/* always share), each sequence reads its own table's pages, which is then faster.                 */
+/* Group i holds the sequences cu_seqs[i] .. cu_seqs[i + 1); their first shared_lens[i] tokens     */
+/* lie in the pages of the group's first sequence's row (a sequence shorter than that sees its     */
+/* own seq_lens tokens of them). Sequences outside every group are left as they were.              */
+/* shared_lens[i] may be 0 and need not be a multiple of page_size. Arguments as in                */
+/* qd_attn_prompt with one row per sequence: q, out [batch, n_q_heads, head_dim]; page_table       */
+/* [batch, max_pages], seq_lens [batch]; cu_seqs: int32 [n_groups + 1], ascending; shared_lens:    */
+/* int32 [n_groups] (both device). seq_lens[b] == 0 gives out = 0.                                 */
+/* A visible NaN reaches the row, as in qd_attn_prompt; so does an infinity in V, or NaN in its    */
+/* place; one in K gives a score of it (q_is_f32 = 1: NaN, since q enters in parts). After an      */
+/* error that leaves rows unwritten in qd_attn_prompt, out is undefined there.                     */
+/* workspace: qd_attn_shared_workspace_bytes(...) bytes for the current device, its head           */
+/* zero-filled before its first use, as in qd_attn_prompt (whose calls it can serve as well).      */
 /* Limits: as qd_attn_prompt, n_groups <= 1024, batch <= 65535.                                 */
 size_t qd_attn_shared_workspace_bytes(int batch, int n_q_heads, int n_kv_heads);
 int qd_attn_decode_shared(const void* q, int q_is_f32, int64_t q_stride, const void* k_pages, const void* v_pages,

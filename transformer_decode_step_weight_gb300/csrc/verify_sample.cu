@@ -21,8 +21,8 @@
 // state. Bytes: one or two vocabulary rows per sequence, whatever k. Chunks are as long as eight CTAs
 // per SM need; five of them (48 registers a thread) are resident at a time. 64 sequences with 5 rows of
 // 151936: 27 us for 78 MB (3, 4, 6, 8, 12, 16 CTAs per SM: 36.5, 36, 30, 27, 27, 28 us; one or two groups
-// of four tokens per thread under way instead of four: 28 to 31), bound by waits: of 8.4 cycles between
-// a warp's instructions 4.2 for memory and 4.1 at barriers (HBM 23 % busy, half the warps' places taken).
+// of four tokens per thread under way instead of four: 28 to 31), bound by waits: a
+// warp spends 4.2 cycles per instruction on memory and 4.1 at barriers (HBM 23 % busy).
 // One sequence: 10 to 11 us, a chain of dependent reads (drafts, their probabilities, the rows, the chunk
 // sums, the chunk again, the state).
 #include "common.cuh"
