@@ -273,6 +273,32 @@ int qd_attn_decode_shared(const void* q, int q_is_f32, int64_t q_stride, const v
                           void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* Packed rows into the cache: what stands between the QKV projection of several sequences'   */
+/* rows and the attention over them. Row r is [n_q_heads; n_kv_heads; n_kv_heads] heads of 128  */
+/* (q, k, v as in w_qkv). Each q and k head is normed and rotated,                              */
+/*   y = w * x / sqrt(mean(x^2) + eps),  y'[i] = y[i] c_i - y[i + 64] s_i,                      */
+/*   y'[i + 64] = y[i + 64] c_i + y[i] s_i,  (c_i, s_i) = rope_table[positions[axes[i], r], i], i < 64; */
+/* q goes to q_out, k and v in bf16 to the row's cache slot: row j of sequence b's n rows          */
+/* (cu_rows, as in qd_attn_prompt) at token seq_lens[b] - n + j. cast_bf16 = 1 rounds to bf16 after    */
+/* the division and after the weight too, as the decode step and qd_prefill of a BF16 model do.        */
+/* qkv: f32 (qkv_is_f32 = 1) or bf16, rows qkv_stride elements apart (a multiple of 16 bytes);         */
+/* q_norm, k_norm: bf16 [128]; rope_table: f32 [rope_max_pos, 64, 2] (qd_rope_table_init);               */
+/* positions: int32 [n_axes, n_rows] (device), or NULL: each row's cache slot; axes: HOST uint8 [64], the  */
+/* position axis of each frequency (time, height, width of image tokens, in sections or in any other      */
+/* order), NULL where n_axes is 1; q_out: f32 or bf16 [n_rows, n_q_heads, 128], apart from qkv; pages,       */
+/* page_table, seq_lens as in qd_attn_prompt, the pages of all rows in the table.                            */
+/* Rows outside every sequence are left as they were. A row whose slot or position lies outside the            */
+/* cache or the table is left too and sets QD_DEVERR_POS; one whose page does not exist gives q alone and       */
+/* sets QD_DEVERR_PAGE. cu_rows not ascending or past n_rows: QD_DEVERR_POS, and which rows are written is          */
+/* undefined. Needs no workspace. Limits: head_dim == 128, batch, heads <= 1024, n_rows <= 2^20, n_axes <= 4.        */
+int qd_qk_norm_rope(const void* qkv, int qkv_is_f32, int64_t qkv_stride, const void* q_norm, const void* k_norm,
+                    float eps, int cast_bf16, const float* rope_table, int rope_max_pos, const int32_t* positions,
+                    int n_axes, const uint8_t* axes, const int32_t* page_table, const int32_t* cu_rows,
+                    const int32_t* seq_lens, int batch, int n_rows, int n_q_heads, int n_kv_heads, int head_dim,
+                    int page_size, int max_pages, int n_pages, void* q_out, int out_is_f32, void* k_pages,
+                    void* v_pages, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Page operations on the K/V cache ([KL-PAGED]: fixed physical pages behind a      */
 /* page table). The state is in device memory, owned by the caller:                 */
 /*   page_table int32 [max_seqs, max_pages]: the pages of each sequence in order,     */

@@ -1,0 +1,44 @@
+"""Refusals on the host of the operators that fill and bound the cache, before any CUDA call (no GPU)."""
+import pytest
+import torch
+
+from transformer_decode_step_weight_gb300 import api, build
+
+FAKE = 1 << 20     # never dereferenced
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return api.lib()
+
+
+ROWS = dict(x=FAKE, f32=1, stride=48 * 128, qn=FAKE, kn=FAKE, eps=1e-6, cast=0, rope=FAKE, max_pos=100, pos=None,
+            n_axes=1, axes=None, table=FAKE, cu=FAKE, lens=FAKE, batch=2, rows=10, hq=32, hkv=8, hd=128, ps=16,
+            max_pages=4, n_pages=8, out=FAKE * 2, out_f32=1, k=FAKE, v=FAKE, stream=None)
+
+
+@pytest.mark.parametrize("key,value,rc", [
+    ("x", None, -1), ("qn", None, -1), ("kn", None, -1), ("rope", None, -1), ("table", None, -1), ("cu", None, -1),
+    ("lens", None, -1), ("out", None, -1), ("k", None, -1), ("v", None, -1), ("x", FAKE + 8, -1), ("out", FAKE, -1),
+    ("out", FAKE + 8, -1), ("rope", FAKE + 8, -1), ("qn", FAKE + 8, -1), ("f32", 2, -1), ("out_f32", -1, -1),
+    ("cast", 2, -1), ("stride", 48 * 128 - 4, -1), ("stride", 48 * 128 + 2, -1), ("hd", 64, -2), ("eps", -1.0, -1),
+    ("eps", float("nan"), -1), ("eps", float("inf"), -1), ("batch", 0, -1), ("batch", 1025, -2), ("rows", 0, -1),
+    ("rows", (1 << 20) + 1, -2), ("hq", 0, -1), ("hkv", 1025, -2), ("ps", 0, -1), ("max_pages", 1 << 30, -1),
+    ("max_pos", 0, -1), ("n_axes", 0, -1), ("n_axes", 5, -1), ("n_axes", 2, -1), ("axes", bytes([0] * 63 + [1]), -1)])
+def test_rows_refusals(lib, key, value, rc):
+    assert lib.qd_qk_norm_rope(*{**ROWS, key: value}.values()) == rc
+    assert lib.qd_last_error().startswith(b"qd_qk_norm_rope: ")
+
+
+def test_rows_binding_refuses():
+    x, w = torch.zeros((2, 8 * 128)), torch.ones(128, dtype=torch.bfloat16)
+    kv = torch.zeros((3, 2, 16, 128), dtype=torch.bfloat16)
+    pt, n = torch.zeros((1, 2), dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    rest = (w, w, torch.zeros((4, 64, 2)), kv, kv, pt, n, n, 1e-6)
+    with pytest.raises(ValueError, match="float32 or bfloat16"):
+        api.qk_norm_rope(x.half(), *rest)
+    with pytest.raises(ValueError, match="contiguous"):
+        api.qk_norm_rope(torch.zeros((8 * 128, 2)).T, *rest)
+    with pytest.raises(ValueError, match="CUDA device"):
+        api.qk_norm_rope(x, *rest)

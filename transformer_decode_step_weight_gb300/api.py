@@ -78,6 +78,8 @@ _SIGS = {
     "qd_attn_prompt": (_i, [_vp, _i, _l] + [_vp] * 5 + [_i] * 8 + [_f, _vp, _vp, _sz, _vp]),
     "qd_attn_shared_workspace_bytes": (_sz, [_i, _i, _i]),
     "qd_attn_decode_shared": (_i, [_vp, _i, _l] + [_vp] * 6 + [_i] * 8 + [_f, _vp, _vp, _sz, _vp]),
+    "qd_qk_norm_rope": (_i, [_vp, _i, _l, _vp, _vp, _f, _i, _vp, _i, _vp, _i, C.c_char_p, _vp, _vp, _vp] + [_i] * 8
+                        + [_vp, _i, _vp, _vp, _vp]),
     "qd_pages_workspace_bytes": (_sz, [C.POINTER(PageCacheArgs)]),
     "qd_pages_copy": (_i, [C.POINTER(PageCacheArgs), _vp, _vp, _i, _vp]),
     "qd_pages_fork": (_i, [C.POINTER(PageCacheArgs), _vp, _vp, _i, _vp]),
@@ -455,6 +457,69 @@ def _row_stride(name, t, B, rows, V, dev):
     if t.numel() and (s2 != 1 and V > 1 or (B > 1 and s0 != rows * s)):
         raise ValueError(f"verify_sample: {name}'s rows must be evenly spaced (strides {t.stride()})")
     return s
+
+
+def qk_norm_rope(qkv, q_norm, k_norm, rope, k_pages, v_pages, page_table, cu_rows, seq_lens, eps, positions=None,
+                 axes=None, cast=False, out=None, dtype=None, stream=None):
+    """The q and k heads of packed rows normed and rotated, K and V written to their cache slots: qkv f32 or bf16
+    [rows, (Hq + 2 Hkv) * 128] (rows may be strided), sequence b's rows cu_rows[b] .. cu_rows[b + 1), the last of
+    them at slot seq_lens[b] - 1. rope: rope_table(...). positions int32 [axes, rows] (None: the slots), axes: the
+    position axis of each of the 64 frequencies. cast: bf16 after the division and the weight, as a BF16 model's
+    decode step. -> q [rows, Hq, 128] of `dtype` (default: qkv's)."""
+    fn = "qk_norm_rope"
+    away = _elsewhere(qkv, stream)
+    if away is not None:
+        with away:
+            return qk_norm_rope(qkv, q_norm, k_norm, rope, k_pages, v_pages, page_table, cu_rows, seq_lens, eps,
+                                positions, axes, cast, out, dtype)
+    dev = qkv.get_device()
+    if qkv.dim() != 2 or qkv.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{fn}: qkv must be [rows, heads * 128] in float32 or bfloat16")
+    n, width = qkv.shape
+    if n and qkv.stride(1) != 1:
+        raise ValueError(f"{fn}: a row's heads must be contiguous (strides {qkv.stride()})")
+    _want("k_pages", k_pages, torch.bfloat16, 4, dev)
+    _want("v_pages", v_pages, torch.bfloat16, 4, dev, k_pages.shape)
+    n_pages, Hkv, ps, D = k_pages.shape
+    Hq = width // D - 2 * Hkv if D else 0
+    if Hq < 1 or width % D:
+        raise ValueError(f"{fn}: rows of {width} for {Hkv} kv heads of {D}")
+    _want("q_norm", q_norm, torch.bfloat16, 1, dev, (D,))
+    _want("k_norm", k_norm, torch.bfloat16, 1, dev, (D,))
+    _want("rope", rope, torch.float32, 3, dev)
+    if rope.shape[1:] != (D // 2, 2):
+        raise ValueError(f"{fn}: rope table {tuple(rope.shape)}, expected [positions, {D // 2}, 2]")
+    _want("page_table", page_table, torch.int32, 2, dev)
+    B, max_pages = page_table.shape
+    _want("seq_lens", seq_lens, torch.int32, 1, dev, (B,))
+    _want("segment starts", cu_rows, torch.int32, 1, dev, (B + 1,))
+    n_axes = 1
+    if positions is not None:
+        if positions.dim() == 1:
+            positions = positions[None]
+        _want("positions", positions, torch.int32, 2, dev)
+        n_axes = positions.shape[0]
+        if positions.shape[1] != n:
+            raise ValueError(f"{fn}: {positions.shape[1]} positions for {n} rows")
+    if axes is not None:
+        axes = bytes(axes)
+        if len(axes) != D // 2:
+            raise ValueError(f"{fn}: axes of {len(axes)} frequencies, expected {D // 2}")
+    if out is None:
+        out = torch.empty((n, Hq, D), dtype=dtype or qkv.dtype, device=qkv.device)
+    elif out.dtype not in (torch.float32, torch.bfloat16) or (dtype is not None and dtype != out.dtype):
+        raise ValueError(f"{fn}: out in {out.dtype}, expected {dtype or 'float32 or bfloat16'}")
+    _want("out", out, out.dtype, 3, dev, (n, Hq, D))
+    if out.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{fn}: dtype {out.dtype}, expected float32 or bfloat16")
+    if n == 0:
+        return out
+    _check(lib().qd_qk_norm_rope(qkv.data_ptr(), qkv.dtype is torch.float32, qkv.stride(0) if n > 1 else width,
+                                 q_norm.data_ptr(), k_norm.data_ptr(), eps, bool(cast), rope.data_ptr(), rope.shape[0],
+                                 _p(positions), n_axes, axes, page_table.data_ptr(), cu_rows.data_ptr(),
+                                 seq_lens.data_ptr(), B, n, Hq, Hkv, D, ps, max_pages, n_pages, out.data_ptr(),
+                                 out.dtype is torch.float32, k_pages.data_ptr(), v_pages.data_ptr(), _raw_stream(dev)))
+    return out
 
 
 class PageCache:

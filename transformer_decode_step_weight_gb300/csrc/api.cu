@@ -485,6 +485,50 @@ int qd_attn_decode_shared(const void* q, int q_is_f32, int64_t q_stride, const v
   return e == cudaSuccess ? QD_OK : cuda_fail(e, "qd_attn_decode_shared");
 }
 
+int qd_qk_norm_rope(const void* qkv, int qkv_is_f32, int64_t qkv_stride, const void* q_norm, const void* k_norm,
+                    float eps, int cast_bf16, const float* rope_table, int rope_max_pos, const int32_t* positions,
+                    int n_axes, const uint8_t* axes, const int32_t* page_table, const int32_t* cu_rows,
+                    const int32_t* seq_lens, int batch, int n_rows, int n_q_heads, int n_kv_heads, int head_dim,
+                    int page_size, int max_pages, int n_pages, void* q_out, int out_is_f32, void* k_pages,
+                    void* v_pages, cudaStream_t stream) {
+  const char* fn = "qd_qk_norm_rope";
+  if (batch < 1 || n_rows < 1 || n_q_heads < 1 || n_kv_heads < 1 || page_size < 1 || max_pages < 1 || n_pages < 1 ||
+      (long long)max_pages * page_size > (1LL << 30) || rope_max_pos < 1)
+    return fail(QD_ERR_INVALID_ARG, "%s: bad sizes batch=%d rows=%d hq=%d hkv=%d page_size=%d max_pages=%d n_pages=%d "
+                "rope_max_pos=%d", fn, batch, n_rows, n_q_heads, n_kv_heads, page_size, max_pages, n_pages, rope_max_pos);
+  if (head_dim != 128) return fail(QD_ERR_UNSUPPORTED, "%s: head_dim=%d (only 128)", fn, head_dim);
+  if (batch > 1024 || n_rows > (1 << 20) || n_q_heads > 1024 || n_kv_heads > 1024)
+    return fail(QD_ERR_UNSUPPORTED, "%s: %d sequences, %d q heads, %d kv heads (at most 1024), %d rows (at most 2^20)", fn,
+                batch, n_q_heads, n_kv_heads, n_rows);
+  if (!qkv || !q_norm || !k_norm || !rope_table || !page_table || !cu_rows || !seq_lens || !q_out || !k_pages || !v_pages)
+    return fail(QD_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if (!aligned16(qkv) || !aligned16(q_norm) || !aligned16(k_norm) || !aligned16(rope_table) || !aligned16(q_out) ||
+      !aligned16(k_pages) || !aligned16(v_pages))
+    return fail(QD_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
+  if ((qkv_is_f32 | out_is_f32 | cast_bf16) & ~1)
+    return fail(QD_ERR_INVALID_ARG, "%s: qkv_is_f32=%d out_is_f32=%d cast_bf16=%d", fn, qkv_is_f32, out_is_f32, cast_bf16);
+  if (qkv_stride < (int64_t)(n_q_heads + 2 * n_kv_heads) * 128 || qkv_stride % (qkv_is_f32 ? 4 : 8) ||
+      qkv_stride >= ((int64_t)1 << 39))
+    return fail(QD_ERR_INVALID_ARG, "%s: qkv_stride=%lld", fn, (long long)qkv_stride);
+  if (qkv == q_out) return fail(QD_ERR_INVALID_ARG, "%s: q_out must not be qkv", fn);
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(QD_ERR_INVALID_ARG, "%s: eps=%g", fn, (double)eps);
+  if (n_axes < 1 || n_axes > 4 || (n_axes > 1 && (!positions || !axes)))
+    return fail(QD_ERR_INVALID_ARG, "%s: n_axes=%d (1 to 4; more than one needs positions and axes)", fn, n_axes);
+  QkRowsArgs a = {};
+  if (axes)
+    for (int i = 0; i < 64; ++i) {
+      if (axes[i] >= n_axes) return fail(QD_ERR_INVALID_ARG, "%s: axes[%d]=%d of %d", fn, i, axes[i], n_axes);
+      a.axes[i / 16] |= (uint32_t)axes[i] << (2 * (i % 16));
+    }
+  a.qkv = qkv; a.in_f32 = qkv_is_f32; a.out_f32 = out_is_f32; a.cast = cast_bf16; a.stride = qkv_stride;
+  a.q_norm = q_norm; a.k_norm = k_norm; a.eps = eps; a.rope = (const float2*)rope_table; a.rope_max_pos = rope_max_pos;
+  a.positions = positions; a.n_axes = n_axes; a.page_table = page_table; a.cu = cu_rows; a.seq_lens = seq_lens;
+  a.batch = batch; a.n_rows = n_rows; a.Hq = n_q_heads; a.Hkv = n_kv_heads; a.page_size = page_size;
+  a.max_pages = max_pages; a.n_pages = n_pages; a.k_pages = k_pages; a.v_pages = v_pages; a.q_out = q_out;
+  cudaError_t e = launch_qk_rows(a, make_launch(stream, false));
+  return e == cudaSuccess ? QD_OK : cuda_fail(e, fn);
+}
+
 // ------------------------------------------------------------------ cache pages
 static int check_page_cache(const char* fn, const qd_page_cache* c, bool copies, bool state) {
   if (!c) return fail(QD_ERR_INVALID_ARG, "%s: null cache", fn);

@@ -349,6 +349,25 @@ cudaError_t launch_attn_prefix(const AttnRowsArgs& a, float* pre, AttnFrom* from
                                const Launch& L);
 cudaError_t launch_attn_shared(const AttnRowsArgs& a, const Launch& L);
 
+// ----------------------------------------------------------------- packed rows into the cache (qk_rows.cu)
+struct QkRowsArgs {
+  const void* qkv;         // f32 or bf16 [n_rows, (Hq + 2 Hkv) 128], rows stride elements apart
+  int in_f32, out_f32, cast;
+  long long stride;
+  const void *q_norm, *k_norm;   // bf16 [128]
+  float eps;
+  const float2* rope;      // [rope_max_pos][64]
+  int rope_max_pos;
+  const int32_t* positions;      // [n_axes][n_rows], or null: the slots
+  int n_axes;
+  uint32_t axes[4];        // 2 bits for each of the 64 frequencies
+  const int32_t *page_table, *cu, *seq_lens;
+  int batch, n_rows, Hq, Hkv, page_size, max_pages, n_pages;
+  void *k_pages, *v_pages;
+  void* q_out;
+};
+cudaError_t launch_qk_rows(const QkRowsArgs& a, const Launch& L);
+
 // ----------------------------------------------------------------- cache pages (pages.cu)
 struct PageState {
   int32_t *table, *lens, *refs;
