@@ -17,6 +17,8 @@
 #include "kernels.h"
 #include "launch.cuh"
 
+#include <algorithm>
+
 namespace qd {
 namespace {
 
@@ -30,6 +32,24 @@ struct F8 {
 QD_DEV F8 load8(const float* p) { return F8{*(const float4*)p, *(const float4*)(p + 64)}; }
 QD_DEV float4 widen(uint2 w) { return make_float4(bf_lo(w.x), bf_hi(w.x), bf_lo(w.y), bf_hi(w.y)); }
 QD_DEV F8 load8(const __nv_bfloat16* p) { return F8{widen(*(const uint2*)p), widen(*(const uint2*)(p + 64))}; }
+// The same as it was read, so that bf16 values wait in half the registers
+template <typename T>
+struct Raw;
+template <>
+struct Raw<float> {
+  F8 v;
+  QD_DEV void load(const float* p) { v = load8(p); }
+  QD_DEV F8 wide() const { return v; }
+};
+template <>
+struct Raw<__nv_bfloat16> {
+  uint2 a, b;
+  QD_DEV void load(const __nv_bfloat16* p) {
+    a = *(const uint2*)p;
+    b = *(const uint2*)(p + 64);
+  }
+  QD_DEV F8 wide() const { return F8{widen(a), widen(b)}; }
+};
 QD_DEV uint2 narrow(float4 v) {
   return make_uint2(f2bf_bits(v.x) | f2bf_bits(v.y) << 16, f2bf_bits(v.z) | f2bf_bits(v.w) << 16);
 }
@@ -54,30 +74,22 @@ QD_DEV int segment_of(const int32_t* cu, int batch, int r, int lane) {
   return min(first + n, batch - 1);
 }
 
-template <typename TI, typename TO, bool CAST>
-__global__ void __launch_bounds__(kTh) qk_rows_kernel(const __grid_constant__ QkRowsArgs p, const PageDiv div,
-                                                      int units, int* err) {
-  const int lane = threadIdx.x & 31, hl = lane & 15;
-  const long long item = (long long)blockIdx.x * (kTh / 32) + (threadIdx.x >> 5);
-  if (blockIdx.x == 0) {   // segments that make no sense
-    for (int i = threadIdx.x; i < p.batch; i += kTh) {
-      const int lo = p.cu[i], hi = p.cu[i + 1];
-      if (lo < 0 || hi < lo || hi > p.n_rows) set_error(err, QD_DEVERR_POS);
-    }
-  }
-  const int r = (int)(item / units);
-  if (r >= p.n_rows) return;
-  const int heads = p.Hq + 2 * p.Hkv;
-  const int h0 = (int)(item % units) * 2 * kPairs + (lane >> 4);   // heads h0, h0 + 2, ...
-  const TI* x = (const TI*)p.qkv + (long long)r * p.stride + 4 * hl;
-  F8 v[kPairs];
-#pragma unroll
-  for (int i = 0; i < kPairs; ++i)
-    if (h0 + 2 * i < heads) v[i] = load8(x + (long long)(h0 + 2 * i) * kD);
-
+// What a row's heads need besides their values.
+struct Row {
+  int r;
+  bool ok;                             // written at all
+  float4 cs[2];                        // (cos, sin) of frequencies 4 hl, + 1 and + 2, + 3
+  long long slot;                      // dim 4 hl of head 0 in the cache; -1: none
+};
+QD_DEV Row look_up(const QkRowsArgs& p, const PageDiv& div, int r, int lane, int* err) {
+  const int hl = lane & 15;
+  Row w;
+  w.r = r;
+  w.ok = false;
+  w.slot = -1;
   const int b = segment_of(p.cu, p.batch, r, lane);
   const int row0 = p.cu[b], end = p.cu[b + 1], len = p.seq_lens[b];
-  if (r < row0 || r >= end) return;   // a row outside every sequence
+  if (r < row0 || r >= end) return w;   // a row outside every sequence
   const long long cap = (long long)p.max_pages * p.page_size, at = (long long)len - end + r;
   bool ok = len <= cap && at >= 0;
   // the position of each of the lane's four frequencies
@@ -88,76 +100,124 @@ __global__ void __launch_bounds__(kTh) qk_rows_kernel(const __grid_constant__ Qk
     pos[i] = p.positions ? p.positions[(long long)((axes >> (2 * i)) & 3u) * p.n_rows + r] : (int)at;
     ok = ok && pos[i] >= 0 && pos[i] < p.rope_max_pos;
   }
-  if (!__all_sync(0xffffffffu, ok)) {
+  w.ok = __all_sync(0xffffffffu, ok);
+  if (!w.ok) {
     if (lane == 0) set_error(err, QD_DEVERR_POS);
-    return;
+    return w;
   }
-  float4 cs[2];   // (cos, sin) of frequencies 4 hl, + 1 and + 2, + 3
   if (p.n_axes == 1) {
     const float4* t = (const float4*)(p.rope + (long long)pos[0] * (kD / 2) + 4 * hl);
-    cs[0] = t[0];
-    cs[1] = t[1];
+    w.cs[0] = t[0];
+    w.cs[1] = t[1];
   } else {
     float2 t[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) t[i] = p.rope[(long long)pos[i] * (kD / 2) + 4 * hl + i];
-    cs[0] = make_float4(t[0].x, t[0].y, t[1].x, t[1].y);
-    cs[1] = make_float4(t[2].x, t[2].y, t[3].x, t[3].y);
+    w.cs[0] = make_float4(t[0].x, t[0].y, t[1].x, t[1].y);
+    w.cs[1] = make_float4(t[2].x, t[2].y, t[3].x, t[3].y);
   }
-  long long slot = -1;   // of head 0 in the cache
-  if (h0 + 2 * kPairs > p.Hq) {
-    const PagedSlot sl = paged_slot(p.page_table + (long long)b * p.max_pages, (int)at, p.page_size, div, p.n_pages);
-    if (sl.ok) slot = ((long long)sl.page * p.Hkv * p.page_size + sl.slot) * kD + 4 * hl;
-    else if (lane == 0) set_error(err, QD_DEVERR_PAGE);
+  const PagedSlot sl = paged_slot(p.page_table + (long long)b * p.max_pages, (int)at, p.page_size, div, p.n_pages);
+  if (sl.ok) w.slot = ((long long)sl.page * p.Hkv * p.page_size + sl.slot) * kD + 4 * hl;
+  else if (lane == 0) set_error(err, QD_DEVERR_PAGE);
+  return w;
+}
+
+template <typename TI, typename TO, bool CAST>
+__global__ void __launch_bounds__(kTh, 2) qk_rows_kernel(const __grid_constant__ QkRowsArgs p, const PageDiv div,
+                                                         int units, int* err) {
+  const int lane = threadIdx.x & 31, hl = lane & 15;
+  if (blockIdx.x == 0) {   // segments that make no sense
+    for (int i = threadIdx.x; i < p.batch; i += kTh) {
+      const int lo = p.cu[i], hi = p.cu[i + 1];
+      if (lo < 0 || hi < lo || hi > p.n_rows) set_error(err, QD_DEVERR_POS);
+    }
   }
+  // the warp's run of (row, 8 heads)
+  const long long items = (long long)p.n_rows * units;
+  const long long warps = (long long)gridDim.x * (kTh / 32), me = (long long)blockIdx.x * (kTh / 32) + (threadIdx.x >> 5);
+  long long it = items * me / warps;
+  const long long last = items * (me + 1) / warps;
+  if (it >= last) return;
+  const int heads = p.Hq + 2 * p.Hkv;
+  int r = (int)(it / units), u = (int)(it % units);
+  Raw<TI> v[kPairs];
+  auto load = [&](int row, int unit) {
+    const TI* x = (const TI*)p.qkv + (long long)row * p.stride + 4 * hl;
 #pragma unroll
-  for (int i = 0; i < kPairs; ++i) {
-    const int h = h0 + 2 * i;
-    F8 y = v[i];
-    // (both halves of the warp take part in the sum)
-    float ss = 0.f;
-    if (h < p.Hq + p.Hkv)
-      ss = (y.a.x * y.a.x + y.a.y * y.a.y) + (y.a.z * y.a.z + y.a.w * y.a.w) +
-           ((y.b.x * y.b.x + y.b.y * y.b.y) + (y.b.z * y.b.z + y.b.w * y.b.w));
+    for (int i = 0; i < kPairs; ++i) {
+      const int h = (unit * kPairs + i) * 2 + (lane >> 4);
+      if (h < heads) v[i].load(x + (long long)h * kD);
+    }
+  };
+  load(r, u);
+  Row w = look_up(p, div, r, lane, err);
+  const F8 gq = load8((const __nv_bfloat16*)p.q_norm + 4 * hl), gk = load8((const __nv_bfloat16*)p.k_norm + 4 * hl);
+#pragma unroll 1
+  for (;;) {
+    F8 y[kPairs];
 #pragma unroll
-    for (int o = 8; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (h >= heads) continue;
-    if (h < p.Hq + p.Hkv) {
-      const float inv = 1.0f / sqrtf(ss / (float)kD + p.eps);
-      const __nv_bfloat16* w = (const __nv_bfloat16*)(h < p.Hq ? p.q_norm : p.k_norm) + 4 * hl;
-      const F8 g = load8(w);
-      auto norm = [&](float& e, float gw) {
-        e *= inv;
-        if (CAST) e = round_bf16(e);
-        e *= gw;
-        if (CAST) e = round_bf16(e);
-      };
-      norm(y.a.x, g.a.x); norm(y.a.y, g.a.y); norm(y.a.z, g.a.z); norm(y.a.w, g.a.w);
-      norm(y.b.x, g.b.x); norm(y.b.y, g.b.y); norm(y.b.z, g.b.z); norm(y.b.w, g.b.w);
-      auto turn = [](float& lo, float& hi, float c, float s) {
-        const float l = lo * c - hi * s;
-        hi = hi * c + lo * s;
-        lo = l;
-      };
-      turn(y.a.x, y.b.x, cs[0].x, cs[0].y);
-      turn(y.a.y, y.b.y, cs[0].z, cs[0].w);
-      turn(y.a.z, y.b.z, cs[1].x, cs[1].y);
-      turn(y.a.w, y.b.w, cs[1].z, cs[1].w);
+    for (int i = 0; i < kPairs; ++i) y[i] = v[i].wide();
+    const int h0 = u * kPairs * 2 + (lane >> 4);   // heads h0, h0 + 2, ...
+    const bool more = ++it < last;
+    if (more) {
+      if (++u == units) {
+        u = 0;
+        ++r;
+      }
+      load(r, u);
     }
-    if (h < p.Hq) {
-      store8((TO*)p.q_out + ((long long)r * p.Hq + h) * kD + 4 * hl, y);
-    } else if (slot >= 0) {
-      const int g = h - p.Hq;
-      __nv_bfloat16* pages = (__nv_bfloat16*)(g < p.Hkv ? p.k_pages : p.v_pages);
-      store8(pages + slot + (long long)(g < p.Hkv ? g : g - p.Hkv) * p.page_size * kD, y);
+    if (w.ok) {
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        const int h = h0 + 2 * i;
+        // (both halves of the warp take part in the sum)
+        float ss = 0.f;
+        if (h < p.Hq + p.Hkv)
+          ss = (y[i].a.x * y[i].a.x + y[i].a.y * y[i].a.y) + (y[i].a.z * y[i].a.z + y[i].a.w * y[i].a.w) +
+               ((y[i].b.x * y[i].b.x + y[i].b.y * y[i].b.y) + (y[i].b.z * y[i].b.z + y[i].b.w * y[i].b.w));
+#pragma unroll
+        for (int o = 8; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (h >= heads) continue;
+        if (h < p.Hq + p.Hkv) {
+          const float inv = 1.0f / sqrtf(ss / (float)kD + p.eps);
+          const F8 g = h < p.Hq ? gq : gk;
+          auto norm = [&](float& e, float gw) {
+            e *= inv;
+            if (CAST) e = round_bf16(e);
+            e *= gw;
+            if (CAST) e = round_bf16(e);
+          };
+          norm(y[i].a.x, g.a.x); norm(y[i].a.y, g.a.y); norm(y[i].a.z, g.a.z); norm(y[i].a.w, g.a.w);
+          norm(y[i].b.x, g.b.x); norm(y[i].b.y, g.b.y); norm(y[i].b.z, g.b.z); norm(y[i].b.w, g.b.w);
+          auto turn = [](float& lo, float& hi, float c, float s) {
+            const float l = lo * c - hi * s;
+            hi = hi * c + lo * s;
+            lo = l;
+          };
+          turn(y[i].a.x, y[i].b.x, w.cs[0].x, w.cs[0].y);
+          turn(y[i].a.y, y[i].b.y, w.cs[0].z, w.cs[0].w);
+          turn(y[i].a.z, y[i].b.z, w.cs[1].x, w.cs[1].y);
+          turn(y[i].a.w, y[i].b.w, w.cs[1].z, w.cs[1].w);
+        }
+        if (h < p.Hq) {
+          store8((TO*)p.q_out + ((long long)w.r * p.Hq + h) * kD + 4 * hl, y[i]);
+        } else if (w.slot >= 0) {
+          const int g = h - p.Hq;
+          __nv_bfloat16* pages = (__nv_bfloat16*)(g < p.Hkv ? p.k_pages : p.v_pages);
+          store8(pages + w.slot + (long long)(g < p.Hkv ? g : g - p.Hkv) * p.page_size * kD, y[i]);
+        }
+      }
     }
+    if (!more) break;
+    if (w.r != r) w = look_up(p, div, r, lane, err);
   }
 }
 
 template <typename TI, typename TO, bool CAST>
 cudaError_t launch(const QkRowsArgs& a, const Launch& L) {
   const int units = ceil_div(a.Hq + 2 * a.Hkv, 2 * kPairs);
-  const long long ctas = ((long long)a.n_rows * units + kTh / 32 - 1) / (kTh / 32);
+  // two CTAs an SM, each warp an equal run of items
+  const long long ctas = std::min(2LL * dev_info().sm_count, ((long long)a.n_rows * units + kTh / 32 - 1) / (kTh / 32));
   return launch_ex(qk_rows_kernel<TI, TO, CAST>, dim3((unsigned)ctas), dim3(kTh), 0, L, a, make_page_div(a.page_size),
                    units, L.err);
 }
