@@ -272,6 +272,27 @@ int qd_attn_decode_shared(const void* q, int q_is_f32, int64_t q_stride, const v
                           int head_dim, int page_size, int max_pages, int n_pages, float scale, void* out,
                           void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* Decode attention over a window: the row of sequence b, at token p = seq_lens[b] - 1, sees the    */
+/* tokens t <= p with t > p - window or t < n_sinks (the first tokens of the cache stay visible);      */
+/* nothing else is read, NaN included. window >= 1 (2147483647: every token), n_sinks >= 0. q and out    */
+/* [batch, n_q_heads, head_dim], the other arguments, limits and errors as in qd_attn_decode_shared       */
+/* (q_is_f32 = 0: the softmax weights enter the products in two bf16 parts). seq_lens[b] == 0 gives out    */
+/* = 0; a length past the table sets QD_DEVERR_POS and leaves the sequence as it was.                      */
+/* key_weights: f32 [batch, n_kv_heads, max_pages * page_size], or NULL. To key_weights[b, g, t] of each     */
+/* visible token t is added its softmax weight, summed over the q heads of kv head g: attention that keys     */
+/* have drawn, which qd_pages_evict goes by. Deterministic. A visible NaN makes all of its row's weights NaN.   */
+/* workspace: qd_attn_decode_window_workspace_bytes(batch, heads, max_keys) bytes, max_keys = min(window +        */
+/* n_sinks, max_pages * page_size) with key_weights and 0 without (more is fine); its first                       */
+/* QD_ATTN_WINDOW_HEAD bytes zero-filled before its first use, each call leaves them zero; two calls that           */
+/* overlap on the GPU need two.                                                                                    */
+#define QD_ATTN_WINDOW_HEAD 16384
+size_t qd_attn_decode_window_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, int64_t max_keys);
+int qd_attn_decode_window(const void* q, int q_is_f32, int64_t q_stride, const void* k_pages, const void* v_pages,
+                          const int32_t* page_table, const int32_t* seq_lens, int batch, int n_q_heads,
+                          int n_kv_heads, int head_dim, int page_size, int max_pages, int n_pages, float scale,
+                          int window, int n_sinks, float* key_weights, void* out, void* workspace,
+                          size_t workspace_bytes, cudaStream_t stream);
+
 /* ------------------------------------------------------------------------ */
 /* Packed rows into the cache: what stands between the QKV projection of several sequences'   */
 /* rows and the attention over them. Row r is [n_q_heads; n_kv_heads; n_kv_heads] heads of 128  */

@@ -79,3 +79,34 @@ def evict(weights, n, keep, sinks, recent):
     w = np.where(np.isnan(weights[middle]), -np.inf, weights[middle])
     best = middle[np.lexsort((middle, -w))][:keep - first - last]
     return np.sort(np.concatenate([np.arange(first), best, np.arange(n - last, n)]))
+
+
+def make_cache(g, lens, hkv, ps, spare=3, room=0):
+    """Random bf16 caches and the page table (pages in random order, -1 past the end) of sequences of these lengths;
+    room: tokens of the table beyond the longest."""
+    need = [max(0, -(-n // ps)) for n in lens]
+    width, used, n_pages = max(1, -(-(max(lens) + room) // ps)), 0, sum(need) + spare
+    perm = torch.randperm(n_pages, generator=g, device=g.device).tolist()
+    table = []
+    for n in need:
+        table.append([perm[used + i] for i in range(n)] + [-1] * (width - n))
+        used += n
+    shape = (n_pages, hkv, ps, D)
+    kp = torch.randn(shape, generator=g, device=g.device).to(torch.bfloat16)
+    vp = torch.randn(shape, generator=g, device=g.device).to(torch.bfloat16)
+    return kp, vp, torch.tensor(table, dtype=torch.int32, device=g.device)
+
+
+def tokens(pages, row, n):
+    """Tokens 0 .. n - 1 of a sequence, float64 [n, kv heads, D] on the host."""
+    ps = pages.shape[2]
+    x = pages[row[:-(-n // ps)].long()].transpose(1, 2).reshape(-1, pages.shape[1], D)[:n]
+    return x.double().cpu()
+
+
+def out_bound(out, mag, dot, n, bf16, parts):
+    """How far a row of a right kernel may be from `attend`: its weights' errors (weight_bound, and their own entry
+    into the products: bf16 2^-8 in one part, 2^-16 in two, 2^-24 in three) count with sum p |v|, the sum over n keys
+    in f32 with n 2^-24 of that; the result is rounded to its type."""
+    w = weight_bound(dot, n) + 2.0 ** -(8 * parts) + n * 2.0 ** -24
+    return w * mag + out.abs() * (2.0 ** -8 if bf16 else 2.0 ** -23) + 1e-30

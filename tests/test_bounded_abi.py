@@ -42,3 +42,28 @@ def test_rows_binding_refuses():
         api.qk_norm_rope(torch.zeros((8 * 128, 2)).T, *rest)
     with pytest.raises(ValueError, match="CUDA device"):
         api.qk_norm_rope(x, *rest)
+
+
+DECODE = dict(q=FAKE, f32=0, stride=32 * 128, k=FAKE, v=FAKE, table=FAKE, lens=FAKE, batch=10, hq=32, hkv=8, hd=128,
+              ps=16, max_pages=4, n_pages=8, scale=0.1, window=10, sinks=2, weights=FAKE, out=FAKE * 2, ws=FAKE,
+              ws_bytes=1 << 40, stream=None)
+ATTN_BAD = [("q", None, -1), ("out", None, -1), ("table", None, -1), ("lens", None, -1), ("ws", None, -1),
+            ("k", FAKE + 8, -1), ("q", FAKE + 4, -1), ("out", FAKE, -1), ("f32", 2, -1), ("stride", 32 * 128 - 8, -1),
+            ("stride", 32 * 128 + 4, -1), ("hd", 64, -2), ("hq", 12, -1), ("hq", 24, -2), ("ps", 0, -1),
+            ("max_pages", 1 << 30, -1), ("scale", float("nan"), -1), ("ws_bytes", 0, -4), ("batch", 0, -1),
+            ("n_pages", 1 << 26, -2), ("window", 0, -1), ("window", -5, -1), ("sinks", -1, -1)]
+
+
+@pytest.mark.parametrize("key,value,rc", ATTN_BAD + [("batch", 65536, -2), ("weights", FAKE + 2, -1)])
+def test_decode_refusals(lib, key, value, rc):
+    assert lib.qd_attn_decode_window(*{**DECODE, key: value}.values()) == rc
+    assert lib.qd_last_error().startswith(b"qd_attn_decode_window: ")
+
+
+def test_decode_workspace(lib):
+    n = api.attn_decode_window_workspace_bytes
+    assert 0 == n(0, 8, 2) == n(1, 1, 2) == n(1, 8, 2, -1) and n(1, 8, 2) > 16384
+    assert n(4, 32, 8, 1000) >= n(4, 32, 8) + 4 * 32 * 1000 * 4
+    need = n(10, 32, 8, 12)
+    assert lib.qd_attn_decode_window(*{**DECODE, "ws_bytes": need - 1}.values()) == -4
+    assert lib.qd_attn_decode_window(*{**DECODE, "weights": None, "ws_bytes": n(10, 32, 8) - 1}.values()) == -4

@@ -1,0 +1,283 @@
+"""Attention over a sliding window and first tokens that stay visible, and the weights it gives to the keys, on the
+GPU against plain 64-bit implementations."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import bounded_reference as ref
+from transformer_decode_step_weight_gb300 import api
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+D = 128
+SCALE = 1 / math.sqrt(D)
+ALL = api.ALL_KEYS
+POS, PAGE = 2, 1
+DTYPES = [torch.float32, torch.bfloat16]
+
+
+def _gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def _ints(v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+def _q(g, n, hq, dtype, scale=1.0):
+    return (torch.randn((n, hq, D), generator=g, device=DEV) * scale).to(dtype)
+
+
+# ------------------------------------------------------------------------------------------------- single tokens
+
+
+def _check_decode(out, q, kp, vp, pt, lens, window, sinks, scale=SCALE, sums=None, before=None, only=None):
+    bf16 = q.dtype == torch.bfloat16
+    out, qd = out.double().cpu(), q.double().cpu()
+    for b, n in enumerate(lens):
+        if only is not None and b not in only:
+            continue
+        k, v = ref.tokens(kp, pt[b], n), ref.tokens(vp, pt[b], n)
+        see = ref.visible(n - 1, n, window, sinks)
+        want, w, mag, dot = ref.attend(qd[b], k, v, see, scale)
+        m = int(see.sum())
+        tol = ref.out_bound(want, mag, dot, m, bf16, 2 if bf16 else 3)
+        err = (out[b] - want).abs()
+        assert bool((err <= tol).all()), (b, n, float((err / tol).max()))
+        if sums is not None:
+            got, old = sums[b].double().cpu(), before[b].double().cpu()
+            assert torch.equal(got[:, n:], old[:, n:]) and torch.equal(got[:, :n][:, ~see], old[:, :n][:, ~see])
+            total = old[:, :n] + w
+            tol = ref.weight_bound(dot, m) * w + 2.0 ** -23 * total + 1e-30
+            err = (got[:, :n] - total).abs()
+            assert bool((err <= tol).all()), (b, n, float((err / tol).max()))
+
+
+DECODE = [   # lengths, q heads, kv heads, page size, window, first tokens
+    ([1], 4, 2, 16, 1, 0),
+    ([0, 1, 2, 3], 4, 2, 16, 2, 1),
+    ([17, 300, 64, 5], 8, 8, 16, 16, 4),
+    ([100, 101, 102, 103, 104], 8, 1, 16, 100, 3),
+    ([1000, 333], 32, 8, 16, 128, 130),
+    ([777, 1500, 15], 8, 2, 7, 333, 5),
+    ([2000, 1], 16, 2, 24, 700, 64),
+    ([900], 8, 2, 256, 64, 300),
+    ([50, 60], 2, 2, 1, 13, 2),
+    ([5000], 8, 1, 128, ALL, 0),
+    ([20000], 16, 8, 16, 1024, 4),
+    ([4000, 12, 900], 4, 4, 64, ALL, 7),
+    ([70, 33], 4, 2, 16, 5, 1000),             # more first tokens than there are
+    ([130] * 40, 32, 8, 16, 96, 4),
+]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("lens,hq,hkv,ps,window,sinks", DECODE)
+def test_decode(cuda_lib, lens, hq, hkv, ps, window, sinks, dtype):
+    g = _gen(sum(lens) + hq)
+    kp, vp, pt = ref.make_cache(g, lens, hkv, ps)
+    cap = pt.shape[1] * ps
+    q = _q(g, len(lens), hq, dtype)
+    ws = torch.zeros(api.attn_decode_window_workspace_bytes(len(lens), hq, hkv, min(window + sinks, cap)),
+                     dtype=torch.uint8, device=DEV)
+    plain = api.attn_decode_window(q, kp, vp, pt, _ints(lens), SCALE, window, sinks, workspace=ws)
+    _check_decode(plain, q, kp, vp, pt, lens, window, sinks)
+    before = torch.rand((len(lens), hkv, cap), generator=g, device=DEV) * 0.1
+    sums = before.clone()
+    out = api.attn_decode_window(q, kp, vp, pt, _ints(lens), SCALE, window, sinks, key_weights=sums, workspace=ws)
+    assert torch.equal(out, plain)             # asking for the weights changes nothing else
+    _check_decode(out, q, kp, vp, pt, lens, window, sinks, sums=sums, before=before)
+    again = before.clone()                     # the workspace is left ready, and the order of sums fixed
+    assert torch.equal(out, api.attn_decode_window(q, kp, vp, pt, _ints(lens), SCALE, window, sinks, key_weights=again))
+    assert torch.equal(again, sums)
+    assert api.check_device_error() == 0
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_decode_ragged(cuda_lib, seed):
+    g, r = _gen(seed), np.random.default_rng(seed)
+    hq, hkv = [(32, 8), (8, 8), (16, 2), (4, 2), (8, 1), (1, 1)][seed]
+    B = int(r.integers(1, 24))
+    lens = [int(x) for x in 2 ** r.uniform(0, 13, B)]
+    window, sinks, ps = int(2 ** r.uniform(0, 12)), int(r.integers(0, 200)), int(r.choice([7, 16, 24, 128]))
+    dtype = DTYPES[seed % 2]
+    kp, vp, pt = ref.make_cache(g, lens, hkv, ps)
+    q = _q(g, B, hq, dtype, 1 + 5 * (seed % 3))
+    sums = torch.zeros((B, hkv, pt.shape[1] * ps), device=DEV)
+    before = sums.clone()
+    out = api.attn_decode_window(q, kp, vp, pt, _ints(lens), SCALE, window, sinks, key_weights=sums)
+    _check_decode(out, q, kp, vp, pt, lens, window, sinks, sums=sums, before=before)
+    assert api.check_device_error() == 0
+
+
+def test_decode_equals_the_other_decode_attention(cuda_lib):
+    g = _gen(3)
+    lens = [1, 700, 64, 2100]
+    kp, vp, pt = ref.make_cache(g, lens, 2, 16)
+    q = _q(g, 4, 8, torch.float32)
+    a = api.attn_decode_window(q, kp, vp, pt, _ints(lens), SCALE)
+    b = api.attn_decode_paged(q, kp, vp, pt, _ints(lens), SCALE)
+    # (that one has q and the weights in two parts)
+    assert float((a - b).abs().max() / b.abs().max()) < 2.0 ** -13
+
+
+@pytest.mark.parametrize("scale", [-SCALE, 0.0, 1.0])
+def test_decode_scales(cuda_lib, scale):
+    g = _gen(4)
+    lens = [300, 40]
+    kp, vp, pt = ref.make_cache(g, lens, 2, 16)
+    for dtype in DTYPES:
+        q = _q(g, 2, 8, dtype)
+        sums = torch.zeros((2, 2, pt.shape[1] * 16), device=DEV)
+        out = api.attn_decode_window(q, kp, vp, pt, _ints(lens), scale, 100, 3, key_weights=sums)
+        _check_decode(out, q, kp, vp, pt, lens, 100, 3, scale, sums, torch.zeros_like(sums))
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_decode_hidden_values(cuda_lib, dtype, bad):
+    # tokens between the first ones and the window, and slots behind the last token, hold anything
+    g = _gen(5)
+    lens, window, sinks = [500, 90, 33], 70, 9
+    kp, vp, pt = ref.make_cache(g, lens, 2, 16, room=20)
+    q = _q(g, 3, 8, dtype)
+    clean_k, clean_v = kp.clone(), vp.clone()
+    for b, n in enumerate(lens):
+        for t in list(range(min(sinks, n), max(sinks, n - window))) + list(range(n, -(-n // 16) * 16)):
+            kp[int(pt[b, t // 16]), :, t % 16] = bad
+            vp[int(pt[b, t // 16]), :, t % 16] = bad
+    sums = torch.zeros((3, 2, pt.shape[1] * 16), device=DEV)
+    out = api.attn_decode_window(q, kp, vp, pt, _ints(lens), SCALE, window, sinks, key_weights=sums)
+    _check_decode(out, q, clean_k, clean_v, pt, lens, window, sinks, sums=sums, before=torch.zeros_like(sums))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_decode_visible_nan_and_infinity(cuda_lib, dtype):
+    g = _gen(6)
+    lens = [2000, 2000]
+    kp, vp, pt = ref.make_cache(g, lens, 2, 16)
+    q = _q(g, 2, 8, dtype)
+    vp[int(pt[0, 100]), 1, 3, 7] = math.nan            # token 1603
+    vp[int(pt[0, 101]), 1, 3, 9] = math.inf
+    kp[int(pt[1, 100]), 0, 3, 7] = math.nan
+    sums = torch.zeros((2, 2, 2000), device=DEV)
+    out = api.attn_decode_window(q, kp, vp, pt, _ints(lens), SCALE, 600, 4, key_weights=sums)
+    assert bool(out[0, 4:, 7].isnan().all()) and not bool(out[0, 4:, 9].isfinite().any())
+    assert int((~out[0].isfinite()).sum()) == 8 and bool(out[1, :4].isnan().all()) and bool(out[1, 4:].isfinite().all())
+    assert bool(sums[1, 0, 1400:].isnan().all()) and bool(sums[1, 0, 4:1400].eq(0).all())
+    assert bool(sums[0].isfinite().all()) and bool(sums[1, 1].isfinite().all())
+    hidden = api.attn_decode_window(q, kp, vp, pt, _ints(lens), SCALE, 300, 4)
+    assert bool(hidden.isfinite().all())
+    kp[int(pt[1, 100]), 0, 3, 7] = 0
+    q[1, 4:] = 0
+    kp[int(pt[1, 0]), 1, 0, 0] = -math.inf              # 0 * inf: NaN as the formula's
+    assert bool(api.attn_decode_window(q, kp, vp, pt, _ints(lens), SCALE, 600, 4)[1, 4:].isnan().all())
+
+
+def test_decode_large_scores(cuda_lib):
+    g = _gen(8)
+    lens = [900, 2500]
+    kp, vp, pt = ref.make_cache(g, lens, 2, 16)
+    q = _q(g, 2, 8, torch.bfloat16, 40)
+    sums = torch.zeros((2, 2, pt.shape[1] * 16), device=DEV)
+    out = api.attn_decode_window(q, kp, vp, pt, _ints(lens), SCALE, 800, 4, key_weights=sums)
+    _check_decode(out, q, kp, vp, pt, lens, 800, 4, sums=sums, before=torch.zeros_like(sums))
+
+
+def test_decode_strided_q_and_broken_lengths(cuda_lib):
+    g = _gen(9)
+    lens = [40, 33, 5]
+    kp, vp, pt = ref.make_cache(g, lens, 2, 16)
+    qkv = _q(g, 3, 12, torch.float32)
+    out = torch.full((3, 8, D), 7.0, device=DEV)
+    sums = torch.full((3, 2, 48), 7.0, device=DEV)
+    before = sums.clone()
+    api.attn_decode_window(qkv[:, :8], kp, vp, pt, _ints([40, 49, 5]), SCALE, 20, 1, key_weights=sums, out=out)
+    assert api.check_device_error() == POS
+    _check_decode(out, qkv[:, :8], kp, vp, pt, lens, 20, 1, sums=sums, before=before, only=[0, 2])
+    assert bool((out[1] == 7).all()) and bool((sums[1] == 7).all())
+    api.attn_decode_window(qkv[:, :8], kp, vp, pt, _ints([40, -1, 5]), SCALE, 20, 1, key_weights=sums, out=out)
+    assert api.check_device_error() == POS and bool((out[1] == 7).all()) and bool((sums[1] == 7).all())
+    pt[0, 2] = kp.shape[0]
+    api.attn_decode_window(qkv[:, :8], kp, vp, pt, _ints(lens), SCALE, 20, 1, out=out)
+    assert api.check_device_error() == PAGE
+
+
+def test_decode_weights_add_up_over_calls(cuda_lib):
+    g = _gen(10)
+    lens = [130, 50]
+    kp, vp, pt = ref.make_cache(g, lens, 2, 16)
+    sums = torch.zeros((2, 2, pt.shape[1] * 16), device=DEV)
+    for i in range(5):
+        api.attn_decode_window(_q(g, 2, 8, torch.bfloat16), kp, vp, pt, _ints(lens), SCALE, 64, 2, key_weights=sums)
+    total = sums.double().sum(-1)
+    assert bool((total - 5 * 4).abs().max() < 5 * 4 * 2.0 ** -16)      # every row's weights are 1 together
+
+
+def test_decode_in_graphs_that_share_a_workspace(cuda_lib):
+    g = _gen(11)
+    hq, hkv = 8, 2
+    ws = torch.zeros(api.attn_decode_window_workspace_bytes(5, hq, hkv, 1008), dtype=torch.uint8, device=DEV)
+    runs = []
+    for B, dtype in ((5, torch.float32), (2, torch.bfloat16)):
+        kp, vp, pt = ref.make_cache(g, [1000] * B, hkv, 16)
+        r = dict(kp=kp, vp=vp, pt=pt, q=_q(g, B, hq, dtype), lens=_ints([1000] * B),
+                 sums=torch.zeros((B, hkv, pt.shape[1] * 16), device=DEV), out=torch.empty((B, hq, D), dtype=dtype, device=DEV))
+
+        def call(r=r):
+            api.attn_decode_window(r["q"], r["kp"], r["vp"], r["pt"], r["lens"], SCALE, 300, 4, key_weights=r["sums"],
+                                   out=r["out"], workspace=ws)
+
+        call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        runs.append((r, graph))
+    for step in range(3):
+        for r, graph in runs:
+            B = r["q"].shape[0]
+            lens = [int(x) for x in np.random.default_rng(step).integers(0, 1001, B)]
+            r["lens"].copy_(_ints(lens))
+            r["q"].copy_(torch.randn(r["q"].shape, generator=g, device=DEV))
+            r["sums"].zero_()
+            graph.replay()
+            _check_decode(r["out"], r["q"], r["kp"], r["vp"], r["pt"], lens, 300, 4, sums=r["sums"],
+                          before=torch.zeros_like(r["sums"]))
+    assert api.check_device_error() == 0
+
+
+def test_decode_on_two_streams_at_once(cuda_lib):
+    g = _gen(12)
+    lens = [3000] * 8
+    kp, vp, pt = ref.make_cache(g, lens, 2, 16)
+    q = [_q(g, 8, 8, torch.float32) for _ in range(2)]
+    n = _ints(lens)
+    want = [api.attn_decode_window(x, kp, vp, pt, n, SCALE, 2000, 4) for x in q]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(20):
+        for x, s in zip(q, streams):
+            s.wait_stream(torch.cuda.current_stream())
+            got.append(api.attn_decode_window(x, kp, vp, pt, n, SCALE, 2000, 4, stream=s))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, want[i % 2]) for i, a in enumerate(got))
+
+
+def test_decode_many_sequences(cuda_lib):
+    # more (sequence, kv head) pairs than there are tickets
+    g, r = _gen(13), np.random.default_rng(13)
+    B = 2100
+    lens = [int(x) for x in r.integers(0, 60, B)]
+    kp, vp, pt = ref.make_cache(g, lens, 2, 16)
+    q = _q(g, B, 4, torch.bfloat16)
+    sums = torch.zeros((B, 2, pt.shape[1] * 16), device=DEV)
+    out = api.attn_decode_window(q, kp, vp, pt, _ints(lens), SCALE, 30, 2, key_weights=sums)
+    _check_decode(out, q, kp, vp, pt, lens, 30, 2, sums=sums, before=torch.zeros_like(sums),
+                  only=set(r.choice(B, 60).tolist()) | {0, B - 1})
+    assert api.attn_decode_window(q[:0], kp, vp, pt[:0], _ints([]), SCALE).shape == (0, 4, D)
+    assert api.check_device_error() == 0

@@ -78,6 +78,8 @@ _SIGS = {
     "qd_attn_prompt": (_i, [_vp, _i, _l] + [_vp] * 5 + [_i] * 8 + [_f, _vp, _vp, _sz, _vp]),
     "qd_attn_shared_workspace_bytes": (_sz, [_i, _i, _i]),
     "qd_attn_decode_shared": (_i, [_vp, _i, _l] + [_vp] * 6 + [_i] * 8 + [_f, _vp, _vp, _sz, _vp]),
+    "qd_attn_decode_window_workspace_bytes": (_sz, [_i, _i, _i, _l]),
+    "qd_attn_decode_window": (_i, [_vp, _i, _l] + [_vp] * 4 + [_i] * 7 + [_f, _i, _i, _vp, _vp, _vp, _sz, _vp]),
     "qd_qk_norm_rope": (_i, [_vp, _i, _l, _vp, _vp, _f, _i, _vp, _i, _vp, _i, C.c_char_p, _vp, _vp, _vp] + [_i] * 8
                         + [_vp, _i, _vp, _vp, _vp]),
     "qd_pages_workspace_bytes": (_sz, [C.POINTER(PageCacheArgs)]),
@@ -457,6 +459,52 @@ def _row_stride(name, t, B, rows, V, dev):
     if t.numel() and (s2 != 1 and V > 1 or (B > 1 and s0 != rows * s)):
         raise ValueError(f"verify_sample: {name}'s rows must be evenly spaced (strides {t.stride()})")
     return s
+
+
+# A window that hides nothing, and what of a windowed decode's workspace has to be zero before its
+# first use (QD_ATTN_WINDOW_HEAD in qd.h)
+ALL_KEYS = 2 ** 31 - 1
+_WINDOW_HEAD = 16384
+
+
+def attn_decode_window_workspace_bytes(batch: int, hq: int, hkv: int, max_keys: int = 0) -> int:
+    """max_keys: min(window + n_sinks, a page-table row's tokens) where key_weights are asked for, else 0."""
+    return int(lib().qd_attn_decode_window_workspace_bytes(batch, hq, hkv, max_keys))
+
+
+def attn_decode_window(q, k_pages, v_pages, page_table, seq_lens, scale, window=None, n_sinks=0, key_weights=None,
+                       out=None, workspace=None, stream=None):
+    """Decode attention in which each row sees its last `window` tokens (None: all) and the first n_sinks: q f32 or
+    bf16 [B, Hq, D] -> [B, Hq, D] of q's type. key_weights f32 [B, Hkv, max_pages * ps]: each visible key's softmax
+    weight, summed over its kv head's q heads, is added to it."""
+    fn = "attn_decode_window"
+    away = _elsewhere(q, stream)
+    if away is not None:
+        with away:
+            return attn_decode_window(q, k_pages, v_pages, page_table, seq_lens, scale, window, n_sinks, key_weights, out,
+                                      workspace)
+    dev = q.get_device()
+    q_stride = _rows(fn, q, k_pages, v_pages, page_table, seq_lens, seq_lens, out)
+    B, Hq, D = q.shape
+    n_pages, Hkv, ps, _ = k_pages.shape
+    max_pages = page_table.shape[1]
+    if page_table.shape[0] != B:
+        raise ValueError(f"{fn}: {page_table.shape[0]} page tables for {B} rows")
+    window = ALL_KEYS if window is None else window
+    keys = 0
+    if key_weights is not None:
+        _want("key_weights", key_weights, torch.float32, 3, dev, (B, Hkv, max_pages * ps))
+        keys = min(window + n_sinks, max_pages * ps)
+    if out is None:
+        out = torch.empty((B, Hq, D), dtype=q.dtype, device=q.device)
+    if B == 0:
+        return out
+    workspace = _scratch(workspace, lambda: attn_decode_window_workspace_bytes(B, Hq, Hkv, keys), q, _WINDOW_HEAD)
+    _check(lib().qd_attn_decode_window(q.data_ptr(), q.dtype is torch.float32, q_stride, k_pages.data_ptr(),
+                                       v_pages.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), B, Hq, Hkv, D,
+                                       ps, max_pages, n_pages, scale, window, n_sinks, _p(key_weights), out.data_ptr(),
+                                       workspace.data_ptr(), workspace.numel(), _raw_stream(dev)))
+    return out
 
 
 def qk_norm_rope(qkv, q_norm, k_norm, rope, k_pages, v_pages, page_table, cu_rows, seq_lens, eps, positions=None,

@@ -485,6 +485,43 @@ int qd_attn_decode_shared(const void* q, int q_is_f32, int64_t q_stride, const v
   return e == cudaSuccess ? QD_OK : cuda_fail(e, "qd_attn_decode_shared");
 }
 
+static_assert(kAttnWindowHeadBytes == QD_ATTN_WINDOW_HEAD, "the head that the header names");
+size_t qd_attn_decode_window_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, int64_t max_keys) {
+  if (batch < 1 || n_kv_heads < 1 || n_q_heads < n_kv_heads || max_keys < 0 || max_keys > (1LL << 30)) return 0;
+  return attn_window_workspace_bytes(batch, n_q_heads, n_kv_heads, max_keys);
+}
+
+static int check_window(const char* fn, AttnRowsArgs& a, int window, int n_sinks) {
+  if (window < 1 || n_sinks < 0) return fail(QD_ERR_INVALID_ARG, "%s: window=%d n_sinks=%d", fn, window, n_sinks);
+  a.window = window;
+  a.n_sinks = n_sinks;
+  return QD_OK;
+}
+
+int qd_attn_decode_window(const void* q, int q_is_f32, int64_t q_stride, const void* k_pages, const void* v_pages,
+                          const int32_t* page_table, const int32_t* seq_lens, int batch, int n_q_heads,
+                          int n_kv_heads, int head_dim, int page_size, int max_pages, int n_pages, float scale,
+                          int window, int n_sinks, float* key_weights, void* out, void* workspace,
+                          size_t workspace_bytes, cudaStream_t stream) {
+  const char* fn = "qd_attn_decode_window";
+  AttnRowsArgs a = {};
+  int rc = check_window(fn, a, window, n_sinks);
+  if (rc) return rc;
+  // (one row per sequence; up to 65535 of them, so not counted as segments)
+  rc = check_attn_rows(fn, a, q, q_is_f32, q_stride, k_pages, v_pages, page_table, seq_lens, seq_lens, 1, batch,
+                       n_q_heads, n_kv_heads, head_dim, page_size, max_pages, n_pages, scale, out, workspace,
+                       workspace_bytes, 0);
+  if (rc) return rc;
+  if (batch > 65535 || n_kv_heads > 65535)
+    return fail(QD_ERR_UNSUPPORTED, "%s: batch=%d n_kv_heads=%d (at most 65535)", fn, batch, n_kv_heads);
+  if ((uintptr_t)key_weights & 3u) return fail(QD_ERR_INVALID_ARG, "%s: key_weights must be 4-byte aligned", fn);
+  a.key_weights = key_weights;
+  const size_t need = attn_window_workspace_bytes(batch, n_q_heads, n_kv_heads, key_weights ? attn_shown_keys(a) : 0);
+  if (workspace_bytes < need) return fail(QD_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, workspace_bytes, need);
+  cudaError_t e = launch_attn_window(a, make_launch(stream, false));
+  return e == cudaSuccess ? QD_OK : cuda_fail(e, fn);
+}
+
 int qd_qk_norm_rope(const void* qkv, int qkv_is_f32, int64_t qkv_stride, const void* q_norm, const void* k_norm,
                     float eps, int cast_bf16, const float* rope_table, int rope_max_pos, const int32_t* positions,
                     int n_axes, const uint8_t* axes, const int32_t* page_table, const int32_t* cu_rows,

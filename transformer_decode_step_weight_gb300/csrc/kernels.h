@@ -323,7 +323,15 @@ struct AttnRowsArgs {
   void* out;               // as q's type, rows contiguous
   void* workspace;
   long long share_min;     // shared form: tokens whose re-reading must be saved for sharing to pay
+  // window forms: a row at token p sees t > p - window and t < n_sinks (and t <= p)
+  long long window, n_sinks;
+  float* key_weights;      // decode: f32 [n_rows, Hkv, max_pages * page_size], added to; or null
 };
+// the most keys that a row can see
+inline long long attn_shown_keys(const AttnRowsArgs& a) {
+  const long long cap = (long long)a.max_pages * a.page_size;
+  return a.window + a.n_sinks < cap ? a.window + a.n_sinks : cap;
+}
 // Head of a workspace, which has to be zero before its first use: tickets, at places that do not depend
 // on the call (they are zero again after each, so calls of different sizes can share it).
 constexpr size_t kAttnHeadBytes = 8192;
@@ -348,6 +356,11 @@ constexpr size_t kPieceFloats = (size_t)kPieceRows * (128 + 2);
 cudaError_t launch_attn_prefix(const AttnRowsArgs& a, float* pre, AttnFrom* from, AttnPieces* pieces,
                                const Launch& L);
 cudaError_t launch_attn_shared(const AttnRowsArgs& a, const Launch& L);
+// One row per sequence, window form; workspace: its first kAttnWindowHeadBytes zero before its first
+// use (tickets, zero again after each call). max_keys: 0 without key_weights.
+constexpr size_t kAttnWindowHeadBytes = 16384;
+size_t attn_window_workspace_bytes(int B, int Hq, int Hkv, long long max_keys);
+cudaError_t launch_attn_window(const AttnRowsArgs& a, const Launch& L);
 
 // ----------------------------------------------------------------- packed rows into the cache (qk_rows.cu)
 struct QkRowsArgs {
