@@ -67,3 +67,15 @@ def test_decode_workspace(lib):
     need = n(10, 32, 8, 12)
     assert lib.qd_attn_decode_window(*{**DECODE, "ws_bytes": need - 1}.values()) == -4
     assert lib.qd_attn_decode_window(*{**DECODE, "weights": None, "ws_bytes": n(10, 32, 8) - 1}.values()) == -4
+
+
+PROMPT = dict(q=FAKE, f32=0, stride=32 * 128, k=FAKE, v=FAKE, table=FAKE, cu=FAKE, lens=FAKE, batch=2, rows=10, hq=32,
+              hkv=8, hd=128, ps=16, max_pages=4, n_pages=8, scale=0.1, window=10, sinks=2, out=FAKE * 2, ws=FAKE,
+              ws_bytes=1 << 40, stream=None)
+
+
+@pytest.mark.parametrize("key,value,rc", ATTN_BAD + [("cu", None, -1), ("batch", 1025, -2), ("rows", 0, -1),
+                                                     ("rows", (1 << 20) + 1, -2)])
+def test_prompt_refusals(lib, key, value, rc):
+    assert lib.qd_attn_prompt_window(*{**PROMPT, key: value}.values()) == rc
+    assert lib.qd_last_error().startswith(b"qd_attn_prompt_window: ")

@@ -281,3 +281,205 @@ def test_decode_many_sequences(cuda_lib):
                   only=set(r.choice(B, 60).tolist()) | {0, B - 1})
     assert api.attn_decode_window(q[:0], kp, vp, pt[:0], _ints([]), SCALE).shape == (0, 4, D)
     assert api.check_device_error() == 0
+
+
+# --------------------------------------------------------------------------------------------------- packed rows
+
+
+def _pack(rows, lens):
+    cu = [0]
+    for n in rows:
+        cu.append(cu[-1] + n)
+    return cu, [b for b, n in enumerate(rows) for _ in range(n)], [m - n + j for n, m in zip(rows, lens) for j in range(n)]
+
+
+def _check_prompt(out, q, kp, vp, pt, lens, seqs, at, window, sinks, scale=SCALE, rows=None):
+    bf16 = q.dtype == torch.bfloat16
+    out, q = out.double().cpu(), q.double().cpu()
+    kv = {}
+    for r in range(len(seqs)) if rows is None else rows:
+        b, n = seqs[r], at[r] + 1
+        if b not in kv:
+            kv[b] = ref.tokens(kp, pt[b], lens[b]), ref.tokens(vp, pt[b], lens[b])
+        see = ref.visible(at[r], max(n, 0), window, sinks)
+        want, _, mag, dot = ref.attend(q[r], kv[b][0][:max(n, 0)], kv[b][1][:max(n, 0)], see, scale)
+        tol = ref.out_bound(want, mag, dot, int(see.sum()), bf16, 1 if bf16 else 3)
+        err = (out[r] - want).abs()
+        assert bool((err <= tol).all()), (r, b, n, float((err / tol).max()))
+
+
+def _pick(n, r):
+    return sorted(set(range(min(n, 20))) | set(range(max(0, n - 10), n)) | set(r.choice(n, min(60, n), replace=False).tolist()))
+
+
+PROMPT = [   # rows, lengths, q heads, kv heads, page size, window, first tokens
+    ([1], [1], 4, 2, 16, 1, 0),
+    ([1, 1, 1], [1, 17, 300], 8, 8, 16, 16, 4),
+    ([128], [128], 4, 4, 16, 1, 0),
+    ([129, 0, 127], [129, 40, 127], 4, 2, 32, 64, 3),
+    ([64, 65, 3, 31], [64, 65, 1000, 331], 32, 8, 16, 100, 130),
+    ([300, 17], [300, 900], 16, 2, 64, 200, 5),
+    ([33, 70], [729, 470], 4, 2, 7, 128, 128),
+    ([40, 200], [40, 1500], 8, 2, 24, 129, 1),
+    ([16, 20], [5, 20], 4, 2, 16, 6, 2),        # rows before position 0 see nothing
+    ([9, 4], [0, 0], 4, 1, 16, 10, 4),
+    ([1], [5000], 8, 1, 128, 700, 4),
+    ([600], [2100], 8, 2, 256, 256, 256),
+    ([2, 0, 0, 1], [2, 0, 7, 257], 2, 2, 1, 33, 2),
+    ([700], [700], 8, 2, 16, 127, 0),
+    ([1500], [3000], 4, 4, 16, 384, 64),        # one q head a kv head: tiles of 128 tokens
+    ([260], [5000], 8, 1, 16, 1111, 513),
+    ([90, 20], [150, 45], 8, 2, 16, ALL, 0),
+    ([90, 20], [150, 45], 8, 2, 16, 20, 1000),
+]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,lens,hq,hkv,ps,window,sinks", PROMPT)
+def test_prompt(cuda_lib, rows, lens, hq, hkv, ps, window, sinks, dtype):
+    g = _gen(sum(rows) + hq)
+    kp, vp, pt = ref.make_cache(g, lens, hkv, ps)
+    cu, seqs, at = _pack(rows, lens)
+    q = _q(g, cu[-1], hq, dtype)
+    ws = torch.zeros(api.attn_prompt_workspace_bytes(), dtype=torch.uint8, device=DEV)
+    args = (q, kp, vp, pt, _ints(cu), _ints(lens), SCALE, window, sinks)
+    first = api.attn_prompt_window(*args, workspace=ws)
+    assert torch.equal(first, api.attn_prompt_window(*args, workspace=ws))
+    _check_prompt(first, q, kp, vp, pt, lens, seqs, at, window, sinks, rows=_pick(cu[-1], np.random.default_rng(0)))
+    assert api.check_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("seed", range(10))
+def test_prompt_ragged(cuda_lib, seed, dtype):
+    g, r = _gen(60 + seed), np.random.default_rng(seed)
+    hq, hkv = [(8, 1), (4, 4), (32, 8), (16, 2), (8, 8)][seed % 5]
+    n = int(r.integers(1, 40))
+    lens = [int(x) for x in 2 ** r.uniform(0, 12.5, n)]
+    rows = [min(m, int(x)) for m, x in zip(lens, 2 ** r.uniform(0, 11, n))]
+    window, sinks, ps = int(2 ** r.uniform(0, 11)), int(r.integers(0, 300)), int(r.choice([7, 16, 24, 64, 128]))
+    kp, vp, pt = ref.make_cache(g, lens, hkv, ps)
+    cu, seqs, at = _pack(rows, lens)
+    q = _q(g, cu[-1], hq, dtype, 1 + 6 * (seed % 3))
+    args = (q, kp, vp, pt, _ints(cu), _ints(lens), SCALE, window, sinks)
+    ws = torch.zeros(api.attn_prompt_workspace_bytes(), dtype=torch.uint8, device=DEV)
+    first = api.attn_prompt_window(*args, workspace=ws)
+    for _ in range(5):
+        assert torch.equal(first, api.attn_prompt_window(*args, workspace=ws))
+    _check_prompt(first, q, kp, vp, pt, lens, seqs, at, window, sinks, rows=_pick(cu[-1], r))
+    assert api.check_device_error() == 0
+
+
+def _gone(pt, kp, vp, lens, first_at, window, sinks, ps, bad, drop):
+    """Everything that no row from slot first_at on sees holds `bad`; with `drop`, whole pages of it are not named."""
+    for b, n in enumerate(lens):
+        t = torch.arange(-(-n // ps) * ps)
+        hidden = ((t >= sinks) & (t <= first_at[b] - window)) | (t >= n)
+        for i in range(len(t) // ps):
+            h, page = hidden[i * ps:(i + 1) * ps].to(DEV), int(pt[b, i])
+            kp[page, :, h] = bad
+            vp[page, :, h] = bad
+            if drop and bool(h.all()):
+                pt[b, i] = [-1, kp.shape[0] + 5][i % 2]
+
+
+@pytest.mark.parametrize("ps", [16, 64, 24])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_prompt_hidden_values_and_pages(cuda_lib, dtype, bad, ps):
+    g = _gen(6)
+    rows, lens, hq, hkv, window, sinks = [90, 20, 1], [1150, 445, 700], 8, 2, 200, 20
+    kp, vp, pt = ref.make_cache(g, lens, hkv, ps)
+    cu, seqs, at = _pack(rows, lens)
+    q = _q(g, cu[-1], hq, dtype)
+    ck, cv, cpt = kp.clone(), vp.clone(), pt.clone()
+    _gone(pt, kp, vp, lens, [m - n for n, m in zip(rows, lens)], window, sinks, ps, bad, True)
+    out = api.attn_prompt_window(q, kp, vp, pt, _ints(cu), _ints(lens), SCALE, window, sinks)
+    _check_prompt(out, q, ck, cv, cpt, lens, seqs, at, window, sinks)
+    assert api.check_device_error() == 0
+    last = [cu[1] - 1, cu[2] - 1, cu[3] - 1]         # the same for single tokens
+    one = api.attn_decode_window(q[last].contiguous(), kp, vp, pt, _ints(lens), SCALE, window, sinks)
+    _check_decode(one, q[last], ck, cv, cpt, lens, window, sinks)
+    assert api.check_device_error() == 0
+
+
+@pytest.mark.parametrize("what", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_prompt_value_reaches_the_rows_that_see_it(cuda_lib, dtype, what):
+    # tokens that leave the window of some rows of a tile, and one of the first tokens
+    g = _gen(7)
+    rows, lens, hq, hkv, window, sinks = [400], [900], 4, 2, 150, 9
+    kp, vp, pt = ref.make_cache(g, lens, hkv, 16)
+    cu, seqs, at = _pack(rows, lens)
+    q = _q(g, cu[-1], hq, dtype)
+    for t, d in ((470, 3), (600, 9), (700, 70), (890, 100), (4, 120)):
+        vp[int(pt[0, t // 16]), :, t % 16, d] = what
+    out = api.attn_prompt_window(q, kp, vp, pt, _ints(cu), _ints(lens), SCALE, window, sinks)
+    p = torch.tensor(at, device=DEV)
+    hit = torch.isnan(out) if math.isnan(what) else out == what
+    for t, d in ((470, 3), (600, 9), (700, 70), (890, 100)):
+        assert bool((hit[:, :, d] == ((p >= t) & (p < t + window))[:, None]).all()), t
+    assert bool(hit[:, :, 120].all())
+    rest = [d for d in range(D) if d not in (3, 9, 70, 100, 120)]
+    assert bool(torch.isfinite(out[:, :, rest]).all())
+    clean = vp.clone()
+    clean[~torch.isfinite(clean)] = 0
+    want = api.attn_prompt_window(q, kp, clean, pt, _ints(cu), _ints(lens), SCALE, window, sinks)
+    assert bool((out[:, :, rest] == want[:, :, rest]).all())
+
+
+def test_prompt_windows_of_a_long_prompt(cuda_lib):
+    g, r = _gen(9), np.random.default_rng(9)
+    kp, vp, pt = ref.make_cache(g, [6000], 2, 16)
+    for dtype, window, sinks in ((torch.bfloat16, 1000, 4), (torch.float32, 333, 200), (torch.bfloat16, 100000, 0)):
+        q = _q(g, 6000, 8, dtype)
+        out = api.attn_prompt_window(q, kp, vp, pt, _ints([0, 6000]), _ints([6000]), SCALE, window, sinks)
+        _check_prompt(out, q, kp, vp, pt, [6000], [0] * 6000, list(range(6000)), window, sinks,
+                      rows=r.choice(6000, 50, replace=False).tolist())
+    assert api.check_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_prompt_scales_strides_and_rows_outside(cuda_lib, dtype):
+    g = _gen(5)
+    rows, lens, hq, hkv = [10, 50], [130, 50], 8, 2
+    kp, vp, pt = ref.make_cache(g, lens, hkv, 16)
+    qkv = _q(g, 70, hq + 2 * hkv, dtype)
+    qkv[:4] = math.nan
+    qkv[64:] = math.nan
+    cu, seqs, at = _pack(rows, lens)
+    for scale in (SCALE, -SCALE, 0.0):
+        out = torch.full((70, hq, D), 7.0, dtype=dtype, device=DEV)
+        api.attn_prompt_window(qkv[:, :hq], kp, vp, pt, _ints([c + 4 for c in cu]), _ints(lens), scale, 30, 2, out=out)
+        _check_prompt(out[4:64], qkv[4:64, :hq], kp, vp, pt, lens, seqs, at, 30, 2, scale)
+        assert bool((out[:4] == 7).all()) and bool((out[64:] == 7).all())
+    out.fill_(7.0)
+    api.attn_prompt_window(qkv[:, :hq], kp, vp, pt, _ints([4, 14, 64]), _ints([pt.shape[1] * 16 + 1, 50]), SCALE, 30, 2, out=out)
+    assert api.check_device_error() == POS and bool((out[:14] == 7).all())
+    _check_prompt(out[14:64], qkv[14:64, :hq], kp, vp, pt[1:], lens[1:], [0] * 50, list(range(50)), 30, 2)
+    api.attn_prompt_window(qkv[:, :hq], kp, vp, pt, _ints([4, 2, 64]), _ints(lens), SCALE, 30, 2, out=out)
+    assert api.check_device_error() == POS
+
+
+def test_prompt_in_a_graph_with_other_lengths(cuda_lib):
+    g = _gen(14)
+    kp, vp, pt = ref.make_cache(g, [1500, 1500], 2, 16)
+    ws = torch.zeros(api.attn_prompt_workspace_bytes(), dtype=torch.uint8, device=DEV)
+    cu, lens, q = _ints([0, 100, 300]), _ints([1500, 1500]), _q(g, 300, 8, torch.bfloat16)
+    out = torch.empty_like(q)
+
+    def call():
+        api.attn_prompt_window(q, kp, vp, pt, cu, lens, SCALE, 180, 5, out=out, workspace=ws)
+
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for rows, ns in (([300, 0], [301, 1500]), ([1, 299], [1, 700]), ([150, 150], [1500, 149])):
+        c, seqs, at = _pack(rows, ns)
+        cu.copy_(_ints(c))
+        lens.copy_(_ints(ns))
+        graph.replay()
+        _check_prompt(out, q, kp, vp, pt, ns, seqs, at, 180, 5, rows=range(0, 300, 7))
+    assert api.check_device_error() == 0

@@ -78,6 +78,7 @@ _SIGS = {
     "qd_attn_prompt": (_i, [_vp, _i, _l] + [_vp] * 5 + [_i] * 8 + [_f, _vp, _vp, _sz, _vp]),
     "qd_attn_shared_workspace_bytes": (_sz, [_i, _i, _i]),
     "qd_attn_decode_shared": (_i, [_vp, _i, _l] + [_vp] * 6 + [_i] * 8 + [_f, _vp, _vp, _sz, _vp]),
+    "qd_attn_prompt_window": (_i, [_vp, _i, _l] + [_vp] * 5 + [_i] * 8 + [_f, _i, _i, _vp, _vp, _sz, _vp]),
     "qd_attn_decode_window_workspace_bytes": (_sz, [_i, _i, _i, _l]),
     "qd_attn_decode_window": (_i, [_vp, _i, _l] + [_vp] * 4 + [_i] * 7 + [_f, _i, _i, _vp, _vp, _vp, _sz, _vp]),
     "qd_qk_norm_rope": (_i, [_vp, _i, _l, _vp, _vp, _f, _i, _vp, _i, _vp, _i, C.c_char_p, _vp, _vp, _vp] + [_i] * 8
@@ -465,6 +466,35 @@ def _row_stride(name, t, B, rows, V, dev):
 # first use (QD_ATTN_WINDOW_HEAD in qd.h)
 ALL_KEYS = 2 ** 31 - 1
 _WINDOW_HEAD = 16384
+
+
+def attn_prompt_window(q, k_pages, v_pages, page_table, cu_rows, seq_lens, scale, window=None, n_sinks=0, out=None,
+                       workspace=None, stream=None):
+    """attn_prompt in which each row sees its last `window` tokens (itself among them; None: all) and the first
+    n_sinks; the other arguments and the workspace are attn_prompt's."""
+    away = _elsewhere(q, stream)
+    if away is not None:
+        with away:
+            return attn_prompt_window(q, k_pages, v_pages, page_table, cu_rows, seq_lens, scale, window, n_sinks, out,
+                                      workspace)
+    fn = "attn_prompt_window"
+    q_stride = _rows(fn, q, k_pages, v_pages, page_table, seq_lens, cu_rows, out)
+    n, Hq, D = q.shape
+    B, max_pages = page_table.shape
+    n_pages, Hkv, ps, _ = k_pages.shape
+    if cu_rows.shape[0] != B + 1:
+        raise ValueError(f"{fn}: {cu_rows.numel()} segment starts for {B} sequences")
+    if out is None:
+        out = torch.empty((n, Hq, D), dtype=q.dtype, device=q.device)
+    if n == 0:
+        return out
+    workspace = _scratch(workspace, attn_prompt_workspace_bytes, q, _ATTN_HEAD)
+    _check(lib().qd_attn_prompt_window(q.data_ptr(), q.dtype is torch.float32, q_stride, k_pages.data_ptr(),
+                                       v_pages.data_ptr(), page_table.data_ptr(), cu_rows.data_ptr(),
+                                       seq_lens.data_ptr(), B, n, Hq, Hkv, D, ps, max_pages, n_pages, scale,
+                                       ALL_KEYS if window is None else window, n_sinks, out.data_ptr(),
+                                       workspace.data_ptr(), workspace.numel(), _raw_stream(q.get_device())))
+    return out
 
 
 def attn_decode_window_workspace_bytes(batch: int, hq: int, hkv: int, max_keys: int = 0) -> int:

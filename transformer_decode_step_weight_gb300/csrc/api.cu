@@ -498,6 +498,23 @@ static int check_window(const char* fn, AttnRowsArgs& a, int window, int n_sinks
   return QD_OK;
 }
 
+int qd_attn_prompt_window(const void* q, int q_is_f32, int64_t q_stride, const void* k_pages, const void* v_pages,
+                          const int32_t* page_table, const int32_t* cu_rows, const int32_t* seq_lens, int batch,
+                          int n_rows, int n_q_heads, int n_kv_heads, int head_dim, int page_size, int max_pages,
+                          int n_pages, float scale, int window, int n_sinks, void* out, void* workspace,
+                          size_t workspace_bytes, cudaStream_t stream) {
+  const char* fn = "qd_attn_prompt_window";
+  AttnRowsArgs a = {};
+  int rc = check_window(fn, a, window, n_sinks);
+  if (rc) return rc;
+  rc = check_attn_rows(fn, a, q, q_is_f32, q_stride, k_pages, v_pages, page_table, cu_rows, seq_lens, batch, n_rows,
+                       n_q_heads, n_kv_heads, head_dim, page_size, max_pages, n_pages, scale, out, workspace,
+                       workspace_bytes, attn_rows_workspace_bytes());
+  if (rc) return rc;
+  cudaError_t e = launch_attn_prompt_window(a, make_launch(stream, false));
+  return e == cudaSuccess ? QD_OK : cuda_fail(e, fn);
+}
+
 int qd_attn_decode_window(const void* q, int q_is_f32, int64_t q_stride, const void* k_pages, const void* v_pages,
                           const int32_t* page_table, const int32_t* seq_lens, int batch, int n_q_heads,
                           int n_kv_heads, int head_dim, int page_size, int max_pages, int n_pages, float scale,

@@ -96,6 +96,7 @@ struct Params {
   float *pre_o, *pre_m, *pre_l;   // shared form: O, m, l of each (sequence, q head)
   AttnFrom* from;                 // ... or where their pieces are, per (sequence, kv head)
   PageDiv div;
+  int window, sinks;       // window form (at most 2^30, more hides nothing)
   int* err;
 };
 
@@ -241,8 +242,9 @@ struct Split {
   }
 };
 
-template <bool PROMPT>
+template <bool PROMPT, bool WINDOW>
 struct Work {
+  int window, sinks;   // window form
   int log_tpt;   // 2^log_tpt packed rows (tokens or sequences) per row tile
   // Shared form: a team of CTAs takes the same run of keys, each member another row tile of
   // every head, so that a K/V tile comes from HBM once for all row tiles at the same moment (as
@@ -267,7 +269,21 @@ struct Work {
   QD_DEV int seen(const Seg& a, int t) const {
     return PROMPT ? max(0, a.off + min((t + 1) << log_tpt, a.n)) : a.len;
   }
-  QD_DEV int units(const Seg& a, int t) const { return max(1, (seen(a, t) + kKeys - 1) >> 7); }
+  // Window form: the first key of row j's window; the key tiles of the first tokens, which stay; and
+  // the tiles between them and the windows of row tile t, which no row of it sees and no unit stands for.
+  QD_DEV int start(const Seg& a, int j) const { return max(0, a.off + j + 1 - window); }
+  QD_DEV int first_tiles() const { return (sinks + kKeys - 1) >> 7; }
+  QD_DEV int skipped(const Seg& a, int t) const {
+    return WINDOW ? max(0, (start(a, t << log_tpt) >> 7) - first_tiles()) : 0;
+  }
+  QD_DEV long long skipped_before(const Seg& a, int t) const {   // by the row tiles before t
+    if (!WINDOW) return 0;
+    const long long c = (long long)a.off + 1 - window, st = first_tiles();
+    const long long i0 = max(0LL, (((st + 1) << 7) - c + tpt() - 1) >> log_tpt);   // the first that skips any
+    if (i0 >= t) return 0;
+    return floor_sum((c >> log_tpt) + t, 7 - log_tpt) - floor_sum((c >> log_tpt) + i0, 7 - log_tpt) - st * (t - i0);
+  }
+  QD_DEV int units(const Seg& a, int t) const { return max(1, (seen(a, t) + kKeys - 1) >> 7) - skipped(a, t); }
   // sum over j < n of floor(j / 2^k)
   QD_DEV static long long floor_sum(long long n, int k) {
     const long long q = n >> k;
@@ -279,6 +295,7 @@ struct Work {
     const int full = min(t, a.tiles - 1);
     long long sum = t == a.tiles && t > 0 ? units(a, t - 1) : 0;   // (prompt form: steps are tiles)
     if (full <= 0) return sum;
+    sum -= skipped_before(a, full);
     // tile i < full ends at off + (i + 1) tpt keys: one unit up to 128, else the quotient
     const int one = a.off > kKeys ? 0 : min(full, (kKeys - a.off) >> log_tpt);
     sum += one;
@@ -341,8 +358,10 @@ QD_DEV uint32_t any_odd(const uint4& x) {
 // each (last 0: none) and go through the keys together, 32 at a time, until each value that is not
 // finite is known to be NaN. A prompt of 8192 tokens with a NaN in its first value takes 1.1 ms, with
 // an infinity there 2.2 (0.39 without).
+// Window form: the lane's row sees no key from `hid0` (the first tokens' end) up to `hid1`; nobody's below `gap1`.
+template <bool WINDOW>
 __device__ __noinline__ void patch_rows(const Params& p, const int32_t* pt, int g, int first, int last, int d0,
-                                        unsigned char* row, int xr, bool half, bool taken) {
+                                        unsigned char* row, int xr, bool half, bool taken, int hid0, int hid1, int gap1) {
   const int lane = threadIdx.x & 31;
   auto cell = [&](int k) {
     const int c = (d0 + k) >> (half ? 3 : 2);
@@ -360,8 +379,9 @@ __device__ __noinline__ void patch_rows(const Params& p, const int32_t* pt, int 
 #pragma unroll 1
   for (int base = first; base < end; base += 32) {
     if (__all_sync(0xffffffffu, (open & ~nan) == 0)) break;
+    if (WINDOW && base >= hid0 && base + 32 <= gap1) base += (gap1 - base) & ~31;   // (first is a multiple of 32)
     int at = -1;   // the cache row of key base + lane
-    if (base + lane < end) {
+    if (base + lane < end && (!WINDOW || base + lane < hid0 || base + lane >= gap1)) {
       const PagedSlot sl = paged_slot(pt, base + lane, p.page_size, p.div, p.n_pages);
       at = (sl.page * p.Hkv + g) * p.page_size + sl.slot;
     }
@@ -387,6 +407,7 @@ __device__ __noinline__ void patch_rows(const Params& p, const int32_t* pt, int 
         for (int e = 0; e < 8; ++e) {
           const unsigned h = v[e];
           if (base + n >= last || (h & 0x7f80u) != 0x7f80u) continue;   // (the lane's row does not see the key)
+          if (WINDOW && base + n >= hid0 && base + n < hid1) continue;
           const unsigned long long bit = 1ull << (dim + e);
           if (h & 0x7fu) nan |= bit;
           else if (h & 0x8000u) neg |= bit;
@@ -429,7 +450,7 @@ __device__ __noinline__ void patch_joined(const Params& p, int c0, int np, int r
     if (u[e] != 0.f) out[e] = (T)u[e];
 }
 
-template <typename T, int PARTS, bool PROMPT>
+template <typename T, int PARTS, bool PROMPT, bool WINDOW>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
@@ -467,7 +488,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the warp's number from one lane: the roles' branches are then known to be taken by whole
   // warps, and the issuers' descriptors can stay in uniform registers
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  Work<PROMPT> W;
+  Work<PROMPT, WINDOW> W;
+  W.window = p.window;
+  W.sinks = p.sinks;
   W.log_tpt = 7 - p.log_rep;
   pdl_launch_dependents();
   if (smem_u32(smem) & 1023u) {   // the swizzled tiles rest on it (there is no static shared memory)
@@ -669,7 +692,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     int g, t, k0, k1, nk, n;
     int first_row, packed;     // packed rows of the tile: the first, how many
     int seen_max, seen_min;    // keys past the first are nobody's, keys before the second everybody's
+    // window form: of the keys from W.sinks on, those before gap are nobody's, those from all on everybody's
+    int gap, all, skip;
     const int32_t* pt;
+    QD_DEV int key_tile(int i, int first_tiles) const {   // of unit i
+      return WINDOW && i >= first_tiles ? i + skip : i;
+    }
   };
   auto piece_at = [&](const Place& x) {
     const Seg& a = x.a;
@@ -684,6 +712,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     q.first_row = a.row0 + row;
     q.packed = min(W.tpt(), a.n - row);
     q.seen_max = W.seen(a, q.t);
+    q.gap = q.all = q.skip = 0;
+    if (WINDOW) {
+      q.gap = W.start(a, row);
+      q.all = W.start(a, row + q.packed - 1);
+      q.skip = W.skipped(a, q.t);
+    }
     if (PROMPT) {
       q.seen_min = max(0, a.off + row + 1);
     } else {
@@ -728,12 +762,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         int bad_page = 0;
         auto look = [&](int i) {
           Look x;
-          const int key0 = (k0 + i) * kKeys;
+          const int key0 = pc.key_tile(k0 + i, W.first_tiles()) * kKeys;
 #pragma unroll
           for (int j = 0; j < kMine; ++j) {
             const int key = p.box ? key0 + lane * p.box : key0 + 32 * j + lane;
             x.row[j] = -1;
-            if (i < n && key < min(seen_max, key0 + kKeys) && (j == 0 || !p.box)) {
+            const bool some = !WINDOW || key < W.sinks || key + (p.box ? p.box : 1) > pc.gap;   // seen by some row
+            if (i < n && key < min(seen_max, key0 + kKeys) && (j == 0 || !p.box) && some) {
               const PagedSlot sl = paged_slot(pt, key, p.page_size, p.div, p.n_pages);
               if (!sl.ok) bad_page = 1;   // no branch on what is still being read
               x.row[j] = (sl.page * p.Hkv + g) * p.page_size + sl.slot;
@@ -834,12 +869,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < n; ++i) {
           const uint32_t slot = kRingK + rk.slot;
           wait(&full[slot], rk.ph);
-          const int key0 = (k0 + i) * kKeys;
+          const int key0 = pc.key_tile(k0 + i, W.first_tiles()) * kKeys;
           int steps = kKeys / 16;   // of 16 keys that some row sees
-          if (key0 + kKeys > seen_min) {
+          const bool behind_some = WINDOW && key0 < pc.all && key0 + kKeys > W.sinks;
+          if (key0 + kKeys > seen_min || behind_some) {
             // a V tile that some row must not see whole: NaN and infinities taken out, rows past
             // everybody's keys to zero up to the last step's end
-            const int lo = max(0, seen_min - key0), hi = min(seen_max - key0, kKeys);
+            int lo = max(0, seen_min - key0);
+            const int hi = min(seen_max - key0, kKeys);
+            if (behind_some) lo = min(lo, max(0, W.sinks - key0));
             steps = max(1, (hi + 15) >> 4);
             // lane: of key lane / 4 in a group of 8, 16-byte pieces lane & 3, + 4, + 8, + 12
             const int sub = lane >> 2, cc = lane & 3;
@@ -849,10 +887,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int key = (lo & ~7) + sub; key < steps * 16; key += 8) {
               unsigned char* cell = v + (key >> 3) * kKeys8;
-              if (key >= hi) {
+              const bool past_first = WINDOW && key0 + key >= W.sinks;
+              if (key >= hi || (past_first && key0 + key < pc.gap)) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) *(uint4*)(cell + o4[j]) = make_uint4(0u, 0u, 0u, 0u);
-              } else if (key >= lo) {
+              } else if (!WINDOW ? key >= lo : key0 + key >= seen_min || (past_first && key0 + key < pc.all)) {
                 uint4 x[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[j] = *(const uint4*)(cell + o4[j]);
@@ -1017,6 +1056,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // what all valid rows of the warp see (rows that are not valid hold anything)
       const int warp_min = __reduce_min_sync(0xffffffffu, valid ? lim : INT32_MAX);
+      // window form: keys from W.sinks on that lie before it the row does not see; the most of the warp's rows
+      const int from = WINDOW ? max(0, lim - W.window) : 0;
+      const int warp_from = WINDOW ? __reduce_max_sync(0xffffffffu, valid ? from : 0) : 0;
+      auto sees = [&](int key) { return key < lim && (!WINDOW || key >= from || key < W.sinks); };
+      auto masked = [&](int key, int m) {   // whether some row of the warp does not see all of m keys
+        return key + m > warp_min || (WINDOW && key < warp_from && key + m > W.sinks);
+      };
       const float c = p.scale_log2;
       float ms = -INFINITY, l = 0.f;
       [[maybe_unused]] float osum[kFresh ? kCols : 1];
@@ -1026,9 +1072,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // 32 scores; those of keys that the row does not see become -inf
       auto mask = [&](float* sv, int key) {
-        if (key + 32 > warp_min) {
+        if (masked(key, 32)) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) sv[e] = key + e < lim ? sv[e] : -INFINITY;
+          for (int e = 0; e < 32; ++e) sv[e] = sees(key + e) ? sv[e] : -INFINITY;
         }
       };
       auto top = [&](const float* sv, float m) {
@@ -1080,7 +1126,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < n; ++i) {
           const uint32_t ct = tile + i;
           const int b = (int)(ct & 1);
-          const int key0 = (k0 + i) * kKeys + 64 * hf;
+          const int key0 = pc.key_tile(k0 + i, W.first_tiles()) * kKeys + 64 * hf;
           const uint32_t ts = tS + 128 * b + lanes + 64 * hf;
           wait(&s_full[b], (ct >> 1) & 1);
           tc::fence_after();
@@ -1160,7 +1206,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int i = hf == begins ? 0 : kSolo; i < n; i += i < kSolo - 1 ? 1 : 2) {
           const uint32_t ct = tile + i, b = ct % kBufs;
-          const int key0 = (k0 + i) * kKeys;
+          const int key0 = pc.key_tile(k0 + i, W.first_tiles()) * kKeys;
           const uint32_t ts = tS + 128 * b + lanes;
           // (whoever has not followed the kBufs tiles before this one waits for the reference first:
           // the barrier of S is then at this tile's phase)
@@ -1168,14 +1214,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (early) bar_sync(pass_other, 64);
           wait(&s_full[b], (ct / kBufs) & 1);
           tc::fence_after();
-          if (key0 + kKeys > warp_min) {   // keys that some row of the warp does not see become -inf
+          if (masked(key0, kKeys)) {   // keys that some row of the warp does not see become -inf
 #pragma unroll 1
-            for (int e = max(0, (warp_min - key0) & ~31); e < kKeys; e += 32) {
+            for (int e = WINDOW ? 0 : max(0, (warp_min - key0) & ~31); e < kKeys; e += 32) {
+              if (WINDOW && !masked(key0 + e, 32)) continue;
               float x[32];
               ld32(ts + e, x);
               wait_ld();
 #pragma unroll
-              for (int k = 0; k < 32; ++k) x[k] = key0 + e + k < lim ? x[k] : -INFINITY;
+              for (int k = 0; k < 32; ++k) x[k] = sees(key0 + e + k) ? x[k] : -INFINITY;
               st16(ts + e, (const uint32_t*)x);
               st16(ts + e + 16, (const uint32_t*)x + 16);
             }
@@ -1237,6 +1284,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int kGroup = kFresh ? kSoft : kSoft / 2;   // threads that write a piece out
       const int gid = tid & (kGroup - 1), gbar = kFresh || hf ? 6 : 1;
       const bool whole = k0 == 0 && k1 == nk;
+      const int key_lo = pc.key_tile(k0, W.first_tiles()) * kKeys;   // the piece's keys
+      const int key_hi = (pc.key_tile(k1 - 1, W.first_tiles()) + 1) * kKeys;
       const bool final_out = whole && PROMPT;      // else O as it is, with m and l
       float* part = p.part + ((size_t)blockIdx.x * 2 + (k0 == 0 ? 1 : 0)) * kPartFloats;
       // row r of the tile in [n_rows, Hq]: tile0 + out_row(r)
@@ -1278,7 +1327,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const bool look = (patch || z != 0.f) && valid && !dead && l == l;
         if (__any_sync(0xffffffffu, look))
-          patch_rows(p, pt, g, k0 * kKeys, look ? min(lim, k1 * kKeys) : 0, col0, mine, xr, false, patch);
+          patch_rows<WINDOW>(p, pt, g, key_lo, look ? min(lim, key_hi) : 0, col0, mine, xr, false, patch, W.sinks, from,
+                             pc.gap);
         if (valid && !dead && !final_out && hf == 0) put_stats();
         // the rows that this warp's lanes and their other holders' wrote
         bar_sync(2 + (warp & 3), 64);
@@ -1350,8 +1400,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (__any_sync(0xffffffffu, look)) {
 #pragma unroll 1
             for (int d0 = 0; d0 < kD; d0 += 64)
-              patch_rows(p, pt, g, k0 * kKeys, look ? min(lim, k1 * kKeys) : 0, d0,
-                         mine + (final_out ? (d0 >> 6) * (kChunk - 128) : 0), final_out ? xr : 0, final_out, patch);
+              patch_rows<WINDOW>(p, pt, g, key_lo, look ? min(lim, key_hi) : 0, d0,
+                                 mine + (final_out ? (d0 >> 6) * (kChunk - 128) : 0), final_out ? xr : 0, final_out, patch,
+                                 W.sinks, from, pc.gap);
           }
           // a warp whose 32 rows are all there hands them to the copy engine (row by row they took
           // 2300 cycles of the warp, as long as a tile), the last rows of a prompt go one by one
@@ -1527,19 +1578,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 int grid_ctas() { return std::min(dev_info().sm_count, kMaxGrid); }
 
-template <typename T, int PARTS, bool PROMPT>
+template <typename T, int PARTS, bool PROMPT, bool WINDOW>
 cudaError_t launch(const Params& p, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                    const CUtensorMap& to, const Launch& L) {
-  cudaError_t e = allow_smem<attn_rows_kernel<T, PARTS, PROMPT>>(kSmem);
+  cudaError_t e = allow_smem<attn_rows_kernel<T, PARTS, PROMPT, WINDOW>>(kSmem);
   if (e != cudaSuccess) return e;
-  return launch_ex(attn_rows_kernel<T, PARTS, PROMPT>, dim3(grid_ctas()), dim3(kThreads), kSmem, L, tk, tv, tq, to,
+  return launch_ex(attn_rows_kernel<T, PARTS, PROMPT, WINDOW>, dim3(grid_ctas()), dim3(kThreads), kSmem, L, tk, tv, tq, to,
                    p);
 }
 
 // Workspace: the head with the tickets, then the partials.
 static_assert(kAttnRowTickets + kMaxGrid * 4 <= kAttnSeqTickets, "");
 
-template <bool PROMPT>
+template <bool PROMPT, bool WINDOW>
 cudaError_t run(const AttnRowsArgs& a, float* pre_o, AttnFrom* from, const Launch& L) {
   Params p = {};
   p.q = a.q; p.q_stride = a.q_stride;
@@ -1559,6 +1610,8 @@ cudaError_t run(const AttnRowsArgs& a, float* pre_o, AttnFrom* from, const Launc
   p.from = from;
   p.div = make_page_div(a.page_size);
   p.share_min = a.share_min;
+  p.window = (int)std::min(a.window, 1LL << 30);
+  p.sinks = (int)std::min(a.n_sinks, 1LL << 30);
   p.pre_m = pre_o ? pre_o + (size_t)a.n_rows * a.Hq * kD : nullptr;
   p.pre_l = pre_o ? p.pre_m + (size_t)a.n_rows * a.Hq : nullptr;
   p.err = L.err;
@@ -1582,20 +1635,25 @@ cudaError_t run(const AttnRowsArgs& a, float* pre_o, AttnFrom* from, const Launc
     if (e == cudaSuccess) e = encode_tmap_bf16_rows128(&tv, a.v_pages, rows, p.box);
     if (e != cudaSuccess) return e;
   }
-  return a.q_f32 ? launch<float, 3, PROMPT>(p, tk, tv, tq, to, L)
-                 : launch<__nv_bfloat16, 1, PROMPT>(p, tk, tv, tq, to, L);
+  return a.q_f32 ? launch<float, 3, PROMPT, WINDOW>(p, tk, tv, tq, to, L)
+                 : launch<__nv_bfloat16, 1, PROMPT, WINDOW>(p, tk, tv, tq, to, L);
 }
 
 }  // namespace
 
 size_t attn_rows_workspace_bytes() { return kAttnHeadBytes + (size_t)grid_ctas() * 2 * kPartFloats * 4; }
 
-cudaError_t launch_attn_prompt(const AttnRowsArgs& a, const Launch& L) { return run<true>(a, nullptr, nullptr, L); }
+cudaError_t launch_attn_prompt(const AttnRowsArgs& a, const Launch& L) {
+  return run<true, false>(a, nullptr, nullptr, L);
+}
+cudaError_t launch_attn_prompt_window(const AttnRowsArgs& a, const Launch& L) {
+  return run<true, true>(a, nullptr, nullptr, L);
+}
 
 cudaError_t launch_attn_prefix(const AttnRowsArgs& a, float* pre, AttnFrom* from, AttnPieces* pieces,
                                const Launch& L) {
   *pieces = {(const float*)((const unsigned char*)a.workspace + kAttnHeadBytes), grid_ctas()};
-  return run<false>(a, pre, from, L);
+  return run<false, false>(a, pre, from, L);
 }
 
 }  // namespace qd

@@ -339,6 +339,7 @@ constexpr size_t kAttnRowTickets = 0, kAttnSeqTickets = 1024;   // of attention_
 size_t attn_rows_workspace_bytes();
 size_t attn_shared_workspace_bytes(int B, int Hq, int Hkv);
 cudaError_t launch_attn_prompt(const AttnRowsArgs& a, const Launch& L);
+cudaError_t launch_attn_prompt_window(const AttnRowsArgs& a, const Launch& L);
 // The groups' shared tokens alone, of every row whose group shares any, with one entry of
 // `from` per (row, kv head). pieces 0: O [Hq, D], m, l [Hq] of the row in pre (O [n_rows, Hq,
 // D], m, l [n_rows, Hq]; f32, reference maximum in log2 units). Otherwise they are still in
