@@ -293,6 +293,21 @@ int qd_attn_decode_window(const void* q, int q_is_f32, int64_t q_stride, const v
                           int window, int n_sinks, float* key_weights, void* out, void* workspace,
                           size_t workspace_bytes, cudaStream_t stream);
 
+/* The attention that packed rows give to each key: to key_weights[b, g, t] (f32 [batch, n_kv_heads,    */
+/* max_pages * page_size]) is added the softmax weight of token t, summed over the last `last` rows of    */
+/* sequence b (0: all of its rows) and the q heads of kv head g. Rows, windows, limits and errors as in     */
+/* qd_attn_prompt_window, whose rows' attention it is (q and cache as there, V not needed); q_is_f32 = 1:     */
+/* q enters the products in three bf16 parts. Deterministic. A visible NaN makes all of its row's weights     */
+/* NaN; keys that no counted row sees keep their sums. workspace: qd_attn_key_weights_workspace_bytes(...)      */
+/* bytes (for an f32 q; a bf16 one needs about a third), with any contents; two calls that overlap on the         */
+/* GPU need two.                                                                                                  */
+size_t qd_attn_key_weights_workspace_bytes(int batch, int n_rows, int n_q_heads, int n_kv_heads, int last);
+int qd_attn_key_weights(const void* q, int q_is_f32, int64_t q_stride, const void* k_pages, const int32_t* page_table,
+                        const int32_t* cu_rows, const int32_t* seq_lens, int batch, int n_rows, int n_q_heads,
+                        int n_kv_heads, int head_dim, int page_size, int max_pages, int n_pages, float scale, int last,
+                        int window, int n_sinks, float* key_weights, void* workspace, size_t workspace_bytes,
+                        cudaStream_t stream);
+
 /* ------------------------------------------------------------------------ */
 /* Packed rows into the cache: what stands between the QKV projection of several sequences'   */
 /* rows and the attention over them. Row r is [n_q_heads; n_kv_heads; n_kv_heads] heads of 128  */

@@ -79,3 +79,23 @@ PROMPT = dict(q=FAKE, f32=0, stride=32 * 128, k=FAKE, v=FAKE, table=FAKE, cu=FAK
 def test_prompt_refusals(lib, key, value, rc):
     assert lib.qd_attn_prompt_window(*{**PROMPT, key: value}.values()) == rc
     assert lib.qd_last_error().startswith(b"qd_attn_prompt_window: ")
+
+
+WEIGHTS = dict(q=FAKE, f32=0, stride=32 * 128, k=FAKE, table=FAKE, cu=FAKE, lens=FAKE, batch=2, rows=10, hq=32, hkv=8,
+               hd=128, ps=16, max_pages=4, n_pages=8, scale=0.1, last=0, window=10, sinks=2, weights=FAKE, ws=FAKE * 2,
+               ws_bytes=1 << 40, stream=None)
+
+
+@pytest.mark.parametrize("key,value,rc", [b for b in ATTN_BAD if b[0] != "out"]
+                         + [("cu", None, -1), ("batch", 1025, -2), ("rows", 0, -1), ("rows", (1 << 20) + 1, -2),
+                            ("last", -1, -1), ("weights", None, -1), ("weights", FAKE + 2, -1), ("ws", FAKE + 8, -1)])
+def test_weights_refusals(lib, key, value, rc):
+    assert lib.qd_attn_key_weights(*{**WEIGHTS, key: value}.values()) == rc
+    assert lib.qd_last_error().startswith(b"qd_attn_key_weights: ")
+
+
+def test_weights_workspace(lib):
+    n = api.attn_key_weights_workspace_bytes
+    assert 0 == n(0, 5, 8, 2) == n(1, 0, 8, 2) == n(1, 5, 1, 2) == n(1, 5, 8, 2, -1)
+    assert n(8, 8000, 32, 8, 32) < n(8, 8000, 32, 8)
+    assert lib.qd_attn_key_weights(*{**WEIGHTS, "f32": 1, "ws_bytes": n(2, 10, 32, 8) - 1}.values()) == -4

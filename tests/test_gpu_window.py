@@ -483,3 +483,178 @@ def test_prompt_in_a_graph_with_other_lengths(cuda_lib):
         graph.replay()
         _check_prompt(out, q, kp, vp, pt, ns, seqs, at, 180, 5, rows=range(0, 300, 7))
     assert api.check_device_error() == 0
+
+
+# ------------------------------------------------------------------------------------- the weights of packed rows
+
+
+def _check_weights(sums, before, q, kp, pt, rows, lens, cu, last, window, sinks, scale=SCALE, seqs=None):
+    """Every key of the sequences: a sum of weights is off by what each is off by, and by 2^-23 of itself for every
+    addition on the way (rows in tiles of 64 columns, tiles one after another: at most 64 + rows of them)."""
+    sums, before, q = sums.double().cpu(), before.double().cpu(), q.double().cpu()
+    hkv = kp.shape[1]
+    for b, (n, m) in enumerate(zip(rows, lens)):
+        if seqs is not None and b not in seqs:
+            continue
+        used = min(n, last) if last else n
+        assert torch.equal(sums[b, :, m:], before[b, :, m:])
+        if used == 0 or m == 0:
+            assert torch.equal(sums[b], before[b])
+            continue
+        k = ref.tokens(kp, pt[b], m)
+        total, tol = torch.zeros((hkv, m), dtype=torch.float64), torch.zeros((hkv, m), dtype=torch.float64)
+        touched = torch.zeros(m, dtype=torch.bool)
+        for j in range(n - used, n):
+            see = ref.visible(m - n + j, m, window, sinks)
+            _, w, _, dot = ref.attend(q[cu[b] + j], k, k, see, scale)
+            total += w
+            tol += w * (ref.weight_bound(dot, int(see.sum())) + (64 + used) * 2.0 ** -24)
+            touched |= see
+        assert torch.equal(sums[b, :, :m][:, ~touched], before[b, :, :m][:, ~touched]), b
+        tol += 2.0 ** -23 * (before[b, :, :m] + total) + 1e-30
+        err = (sums[b, :, :m] - before[b, :, :m] - total).abs()
+        assert bool((err <= tol).all()), (b, n, m, float((err / tol).max()))
+
+
+WEIGHTS = [   # rows, lengths, q heads, kv heads, page size, last, window, first tokens
+    ([1], [1], 4, 2, 16, 0, ALL, 0),
+    ([1, 1, 1], [1, 17, 300], 8, 8, 16, 0, ALL, 0),
+    ([128], [128], 4, 4, 16, 0, ALL, 0),
+    ([129, 0, 127], [129, 40, 127], 4, 2, 32, 0, 64, 3),
+    ([64, 65, 3, 31], [64, 65, 1000, 331], 32, 8, 16, 16, ALL, 0),
+    ([300, 17], [300, 900], 16, 2, 64, 0, 200, 5),
+    ([33, 70], [729, 470], 4, 2, 7, 20, 128, 128),
+    ([40, 200], [40, 1500], 8, 2, 24, 33, ALL, 0),
+    ([16, 20], [5, 20], 4, 2, 16, 0, ALL, 0),          # rows before position 0 see nothing
+    ([9, 4], [0, 0], 4, 1, 16, 0, ALL, 0),
+    ([1], [5000], 8, 1, 128, 0, ALL, 0),
+    ([600], [900], 8, 2, 256, 0, ALL, 0),
+    ([2, 0, 0, 1], [2, 0, 7, 257], 2, 2, 1, 0, 33, 2),
+    ([500], [500], 2, 2, 16, 0, ALL, 0),
+    ([260], [2500], 8, 1, 16, 40, 311, 213),
+]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,lens,hq,hkv,ps,last,window,sinks", WEIGHTS)
+def test_weights(cuda_lib, rows, lens, hq, hkv, ps, last, window, sinks, dtype):
+    g = _gen(sum(rows) + hq)
+    kp, vp, pt = ref.make_cache(g, lens, hkv, ps)
+    cu, _, _ = _pack(rows, lens)
+    q = _q(g, cu[-1], hq, dtype)
+    before = torch.rand((len(rows), hkv, pt.shape[1] * ps), generator=g, device=DEV) * 0.1
+    ws = torch.full((api.attn_key_weights_workspace_bytes(len(rows), cu[-1], hq, hkv, last),), 255, dtype=torch.uint8, device=DEV)
+    got = []
+    for _ in range(2):
+        sums = before.clone()
+        assert api.attn_key_weights(q, kp, pt, _ints(cu), _ints(lens), SCALE, sums, last, window, sinks, workspace=ws) is sums
+        got.append(sums)
+    assert torch.equal(*got)
+    _check_weights(got[0], before, q, kp, pt, rows, lens, cu, last, window, sinks)
+    assert api.check_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("seed", range(6))
+def test_weights_ragged(cuda_lib, seed, dtype):
+    g, r = _gen(80 + seed), np.random.default_rng(seed)
+    hq, hkv = [(8, 1), (4, 4), (32, 8), (16, 2), (8, 8), (16, 8)][seed]
+    n = int(r.integers(1, 30))
+    lens = [int(x) for x in 2 ** r.uniform(0, 11, n)]
+    rows = [min(m, int(x)) for m, x in zip(lens, 2 ** r.uniform(0, 8, n))]
+    window, sinks, ps = [ALL, int(2 ** r.uniform(0, 10))][seed % 2], int(r.integers(0, 300)), int(r.choice([7, 16, 24, 128]))
+    last = [0, int(r.integers(1, 60))][seed // 2 % 2]
+    kp, vp, pt = ref.make_cache(g, lens, hkv, ps)
+    cu, _, _ = _pack(rows, lens)
+    q = _q(g, cu[-1], hq, dtype, 1 + 4 * (seed % 3))
+    sums = torch.zeros((n, hkv, pt.shape[1] * ps), device=DEV)
+    before = sums.clone()
+    api.attn_key_weights(q, kp, pt, _ints(cu), _ints(lens), SCALE, sums, last, window, sinks)
+    _check_weights(sums, before, q, kp, pt, rows, lens, cu, last, window, sinks,
+                   seqs=set(r.choice(n, min(n, 6), replace=False).tolist()))
+    assert api.check_device_error() == 0
+
+
+def test_weights_of_single_rows_are_the_decode_calls(cuda_lib):
+    g = _gen(15)
+    lens = [1, 700, 64, 2100]
+    kp, vp, pt = ref.make_cache(g, lens, 2, 16)
+    q = _q(g, 4, 8, torch.float32)
+    a, b = (torch.zeros((4, 2, pt.shape[1] * 16), device=DEV) for _ in range(2))
+    api.attn_key_weights(q, kp, pt, _ints([0, 1, 2, 3, 4]), _ints(lens), SCALE, a, window=500, n_sinks=3)
+    api.attn_decode_window(q, kp, vp, pt, _ints(lens), SCALE, 500, 3, key_weights=b)
+    assert float((a - b).abs().max()) < 2.0 ** -16 and float((a - b).norm() / b.norm()) < 2.0 ** -18
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_weights_hidden_and_visible_values(cuda_lib, dtype, bad):
+    g = _gen(16)
+    rows, lens, window, sinks = [90, 20, 1], [1150, 445, 700], 200, 20
+    kp, vp, pt = ref.make_cache(g, lens, 2, 16)
+    cu, _, _ = _pack(rows, lens)
+    q = _q(g, cu[-1], 8, dtype)
+    ck, cpt = kp.clone(), pt.clone()
+    _gone(pt, kp, vp, lens, [m - n for n, m in zip(rows, lens)], window, sinks, 16, bad, True)
+    sums = torch.zeros((3, 2, pt.shape[1] * 16), device=DEV)
+    before = sums.clone()
+    api.attn_key_weights(q, kp, pt, _ints(cu), _ints(lens), SCALE, sums, window=window, n_sinks=sinks)
+    _check_weights(sums, before, q, ck, cpt, rows, lens, cu, 0, window, sinks)
+    assert api.check_device_error() == 0
+    # one that rows 60 .. of sequence 0 (tokens 1120 ..) see, in one kv head
+    kp[int(pt[0, 70]), 1, 0, 3] = math.nan
+    sums.zero_()
+    api.attn_key_weights(q, kp, pt, _ints(cu), _ints(lens), SCALE, sums, window=window, n_sinks=sinks)
+    assert bool(sums[0, 0].isfinite().all()) and bool(sums[1:].isfinite().all())
+    nan = sums[0, 1].isnan()
+    assert bool(nan[:20].all()) and not bool(nan[20:921].any()) and bool(nan[921:1150].all()) and not bool(nan[1150:].any())
+
+
+def test_weights_refused_lengths_and_rows_outside(cuda_lib):
+    g = _gen(17)
+    rows, lens = [10, 50], [130, 50]
+    kp, vp, pt = ref.make_cache(g, lens, 2, 16)
+    qkv = _q(g, 70, 12, torch.bfloat16)
+    qkv[:4] = math.nan
+    qkv[64:] = math.nan
+    sums = torch.zeros((2, 2, pt.shape[1] * 16), device=DEV)
+    before = sums.clone()
+    api.attn_key_weights(qkv[:, :8], kp, pt, _ints([4, 14, 64]), _ints(lens), -SCALE, sums)
+    _check_weights(sums, before, qkv[4:, :8], kp, pt, rows, lens, [0, 10, 60], 0, ALL, 0, -SCALE)
+    assert api.check_device_error() == 0
+    sums.zero_()
+    api.attn_key_weights(qkv[:, :8], kp, pt, _ints([4, 14, 64]), _ints([pt.shape[1] * 16 + 1, 50]), SCALE, sums)
+    assert api.check_device_error() == POS and bool((sums[0] == 0).all())
+    _check_weights(sums, before, qkv[4:, :8], kp, pt, rows, lens, [0, 10, 60], 0, ALL, 0, seqs={1})
+    sums.zero_()
+    api.attn_key_weights(qkv[:, :8], kp, pt, _ints([4, 2, 64]), _ints(lens), SCALE, sums)
+    assert api.check_device_error() == POS and bool((sums == 0).all())
+    assert bool((api.attn_key_weights(qkv[:0, :8], kp, pt, _ints([0, 0, 0]), _ints(lens), SCALE, sums) == 0).all())
+    pt[1, 1] = -1
+    api.attn_key_weights(qkv[:, :8], kp, pt, _ints([4, 14, 64]), _ints(lens), SCALE, sums)
+    assert api.check_device_error() == PAGE
+
+
+def test_weights_in_a_graph_with_other_lengths(cuda_lib):
+    g = _gen(18)
+    kp, vp, pt = ref.make_cache(g, [600, 600], 2, 16)
+    cu, lens, q = _ints([0, 100, 200]), _ints([600, 600]), _q(g, 200, 8, torch.float32)
+    ws = torch.empty(api.attn_key_weights_workspace_bytes(2, 200, 8, 2), dtype=torch.uint8, device=DEV)
+    sums = torch.zeros((2, 2, pt.shape[1] * 16), device=DEV)
+
+    def call():
+        api.attn_key_weights(q, kp, pt, cu, lens, SCALE, sums, window=250, n_sinks=5, workspace=ws)
+
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for rows, ns in (([200, 0], [301, 600]), ([1, 199], [1, 400]), ([90, 110], [600, 109])):
+        c, _, _ = _pack(rows, ns)
+        cu.copy_(_ints(c))
+        lens.copy_(_ints(ns))
+        sums.zero_()
+        graph.replay()
+        _check_weights(sums, torch.zeros_like(sums), q, kp, pt, rows, ns, c, 0, 250, 5)
+    assert api.check_device_error() == 0

@@ -81,6 +81,8 @@ _SIGS = {
     "qd_attn_prompt_window": (_i, [_vp, _i, _l] + [_vp] * 5 + [_i] * 8 + [_f, _i, _i, _vp, _vp, _sz, _vp]),
     "qd_attn_decode_window_workspace_bytes": (_sz, [_i, _i, _i, _l]),
     "qd_attn_decode_window": (_i, [_vp, _i, _l] + [_vp] * 4 + [_i] * 7 + [_f, _i, _i, _vp, _vp, _vp, _sz, _vp]),
+    "qd_attn_key_weights_workspace_bytes": (_sz, [_i] * 5),
+    "qd_attn_key_weights": (_i, [_vp, _i, _l] + [_vp] * 4 + [_i] * 8 + [_f, _i, _i, _i, _vp, _vp, _sz, _vp]),
     "qd_qk_norm_rope": (_i, [_vp, _i, _l, _vp, _vp, _f, _i, _vp, _i, _vp, _i, C.c_char_p, _vp, _vp, _vp] + [_i] * 8
                         + [_vp, _i, _vp, _vp, _vp]),
     "qd_pages_workspace_bytes": (_sz, [C.POINTER(PageCacheArgs)]),
@@ -535,6 +537,39 @@ def attn_decode_window(q, k_pages, v_pages, page_table, seq_lens, scale, window=
                                        ps, max_pages, n_pages, scale, window, n_sinks, _p(key_weights), out.data_ptr(),
                                        workspace.data_ptr(), workspace.numel(), _raw_stream(dev)))
     return out
+
+
+def attn_key_weights_workspace_bytes(batch: int, rows: int, hq: int, hkv: int, last: int = 0) -> int:
+    return int(lib().qd_attn_key_weights_workspace_bytes(batch, rows, hq, hkv, last))
+
+
+def attn_key_weights(q, k_pages, page_table, cu_rows, seq_lens, scale, key_weights, last=0, window=None, n_sinks=0,
+                     workspace=None, stream=None):
+    """Adds to key_weights f32 [B, Hkv, max_pages * ps] the softmax weights that attn_prompt (attn_prompt_window) of
+    these rows gives to each key, summed over the last `last` rows of each sequence (0: all) and the q heads of a kv
+    head. Returns key_weights."""
+    fn = "attn_key_weights"
+    away = _elsewhere(q, stream)
+    if away is not None:
+        with away:
+            return attn_key_weights(q, k_pages, page_table, cu_rows, seq_lens, scale, key_weights, last, window, n_sinks,
+                                    workspace)
+    dev = q.get_device()
+    q_stride = _rows(fn, q, k_pages, k_pages, page_table, seq_lens, cu_rows, None)
+    n, Hq, D = q.shape
+    B, max_pages = page_table.shape
+    n_pages, Hkv, ps, _ = k_pages.shape
+    if cu_rows.shape[0] != B + 1:
+        raise ValueError(f"{fn}: {cu_rows.numel()} segment starts for {B} sequences")
+    _want("key_weights", key_weights, torch.float32, 3, dev, (B, Hkv, max_pages * ps))
+    if n == 0:
+        return key_weights
+    workspace = _scratch(workspace, lambda: attn_key_weights_workspace_bytes(B, n, Hq, Hkv, last), q, 0)
+    _check(lib().qd_attn_key_weights(q.data_ptr(), q.dtype is torch.float32, q_stride, k_pages.data_ptr(),
+                                     page_table.data_ptr(), cu_rows.data_ptr(), seq_lens.data_ptr(), B, n, Hq, Hkv, D,
+                                     ps, max_pages, n_pages, scale, last, ALL_KEYS if window is None else window, n_sinks,
+                                     key_weights.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(dev)))
+    return key_weights
 
 
 def qk_norm_rope(qkv, q_norm, k_norm, rope, k_pages, v_pages, page_table, cu_rows, seq_lens, eps, positions=None,

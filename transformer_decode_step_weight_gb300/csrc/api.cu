@@ -539,6 +539,36 @@ int qd_attn_decode_window(const void* q, int q_is_f32, int64_t q_stride, const v
   return e == cudaSuccess ? QD_OK : cuda_fail(e, fn);
 }
 
+size_t qd_attn_key_weights_workspace_bytes(int batch, int n_rows, int n_q_heads, int n_kv_heads, int last) {
+  if (batch < 1 || n_rows < 1 || n_kv_heads < 1 || n_q_heads < n_kv_heads || last < 0) return 0;
+  return attn_key_weights_workspace_bytes(batch, n_rows, n_q_heads, n_kv_heads, last, true);
+}
+
+int qd_attn_key_weights(const void* q, int q_is_f32, int64_t q_stride, const void* k_pages, const int32_t* page_table,
+                        const int32_t* cu_rows, const int32_t* seq_lens, int batch, int n_rows, int n_q_heads,
+                        int n_kv_heads, int head_dim, int page_size, int max_pages, int n_pages, float scale, int last,
+                        int window, int n_sinks, float* key_weights, void* workspace, size_t workspace_bytes,
+                        cudaStream_t stream) {
+  const char* fn = "qd_attn_key_weights";
+  AttnRowsArgs a = {};
+  int rc = check_window(fn, a, window, n_sinks);
+  if (rc) return rc;
+  if (last < 0) return fail(QD_ERR_INVALID_ARG, "%s: last=%d", fn, last);
+  if (!key_weights || (uintptr_t)key_weights & 3u)
+    return fail(QD_ERR_INVALID_ARG, "%s: key_weights null or not 4-byte aligned", fn);
+  if (!workspace) return fail(QD_ERR_INVALID_ARG, "%s: null pointer", fn);
+  // (no V and no result rows: the workspace stands for them in the common checks)
+  rc = check_attn_rows(fn, a, q, q_is_f32, q_stride, k_pages, k_pages, page_table, cu_rows, seq_lens, batch, n_rows,
+                       n_q_heads, n_kv_heads, head_dim, page_size, max_pages, n_pages, scale, workspace, workspace,
+                       workspace_bytes, 0);
+  if (rc) return rc;
+  const size_t need = attn_key_weights_workspace_bytes(batch, n_rows, n_q_heads, n_kv_heads, last, q_is_f32 != 0);
+  if (workspace_bytes < need) return fail(QD_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, workspace_bytes, need);
+  a.key_weights = key_weights;
+  cudaError_t e = launch_attn_key_weights(a, last, make_launch(stream, false));
+  return e == cudaSuccess ? QD_OK : cuda_fail(e, fn);
+}
+
 int qd_qk_norm_rope(const void* qkv, int qkv_is_f32, int64_t qkv_stride, const void* q_norm, const void* k_norm,
                     float eps, int cast_bf16, const float* rope_table, int rope_max_pos, const int32_t* positions,
                     int n_axes, const uint8_t* axes, const int32_t* page_table, const int32_t* cu_rows,

@@ -363,6 +363,11 @@ constexpr size_t kAttnWindowHeadBytes = 16384;
 size_t attn_window_workspace_bytes(int B, int Hq, int Hkv, long long max_keys);
 cudaError_t launch_attn_window(const AttnRowsArgs& a, const Launch& L);
 
+// The weights of packed rows' attention added up per key (attention_weights.cu): of the last `last` rows of
+// each sequence (0: all) into a.key_weights; out and v_pages unused.
+size_t attn_key_weights_workspace_bytes(int B, int n_rows, int Hq, int Hkv, int last, bool f32);
+cudaError_t launch_attn_key_weights(const AttnRowsArgs& a, int last, const Launch& L);
+
 // ----------------------------------------------------------------- packed rows into the cache (qk_rows.cu)
 struct QkRowsArgs {
   const void* qkv;         // f32 or bf16 [n_rows, (Hq + 2 Hkv) 128], rows stride elements apart
