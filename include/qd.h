@@ -386,6 +386,21 @@ int qd_pages_trim(const qd_page_cache* cache, const int32_t* new_lens, cudaStrea
 /* Moves the pages in use to the ids 0 .. n_live - 1 (those above go, in ascending order, to      */
 /* the free ids below), with the page tables and counts; n_live: int32 [1], device.                */
 int qd_pages_compact(const qd_page_cache* cache, int32_t* n_live, cudaStream_t stream);
+/* Cuts sequence s to keep[s] tokens (int32 [max_seqs], device; negative or not below its length:   */
+/* unchanged; 0 frees it), each layer and kv head choosing its own: the first n_sinks, the last      */
+/* n_recent, and of those between the ones of the largest key_weights (the lower token first among     */
+/* equals; NaN counts as -infinity), keep[s] in all (fewer of the last, then of the first, where       */
+/* keep[s] is below their number). The kept tokens' K and V move down in their order to tokens 0 ..     */
+/* keep[s] - 1, and so do their weights, past which zeros follow up to the old length; pages past the    */
+/* new length lose a reference as in qd_pages_trim. A token's place is then no longer its position: new     */
+/* ones are written with explicit positions (qd_qk_norm_rope).                                             */
+/* key_weights: f32 [n_layers, max_seqs, n_kv_heads, max_pages * page_size], device (each layer's part        */
+/* filled by qd_attn_decode_window and qd_attn_key_weights). A page that would be written and that others        */
+/* share (qd_pages_fork), or a length past the table, changes nothing and sets QD_DEVERR_CACHE; so does a         */
+/* table entry that names no page (with QD_DEVERR_PAGE).                                                          */
+/* Limits: head_dim <= 256, n_pages * n_kv_heads * page_size < 2^31.                                               */
+int qd_pages_evict(const qd_page_cache* cache, float* key_weights, const int32_t* keep, int n_sinks, int n_recent,
+                   cudaStream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Greedy argmax + on-device advance ([KL-DEC] "LM-head GEMV + argmax +        */

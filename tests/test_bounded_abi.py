@@ -1,4 +1,6 @@
 """Refusals on the host of the operators that fill and bound the cache, before any CUDA call (no GPU)."""
+import ctypes as C
+
 import pytest
 import torch
 
@@ -99,3 +101,30 @@ def test_weights_workspace(lib):
     assert 0 == n(0, 5, 8, 2) == n(1, 0, 8, 2) == n(1, 5, 1, 2) == n(1, 5, 8, 2, -1)
     assert n(8, 8000, 32, 8, 32) < n(8, 8000, 32, 8)
     assert lib.qd_attn_key_weights(*{**WEIGHTS, "f32": 1, "ws_bytes": n(2, 10, 32, 8) - 1}.values()) == -4
+
+
+def test_evict_refusals(lib):
+    def cache(**kw):
+        arr = (C.c_void_p * 2)(FAKE, FAKE)
+        a = api.PageCacheArgs(C.cast(arr, C.c_void_p), C.cast(arr, C.c_void_p), 2, 8, 16, 128, 64, FAKE, FAKE, FAKE, 4, 8,
+                              FAKE, 1 << 30)
+        a.keep = arr
+        for k, v in kw.items():
+            setattr(a, k, v)
+        return C.byref(a)
+
+    def call(c, w=FAKE, keep=FAKE, sinks=0, recent=0):
+        return lib.qd_pages_evict(c, w, keep, sinks, recent, None)
+
+    assert call(None) == -1
+    for kw, rc in ((dict(k_cache=None), -1), (dict(n_layers=0), -1), (dict(page_size=0), -1), (dict(head_dim=12), -2),
+                   (dict(head_dim=264), -2), (dict(page_table=None), -1),
+                   (dict(seq_lens=None), -1), (dict(refs=None), -1), (dict(workspace=None), -1), (dict(max_seqs=2049), -2),
+                   (dict(max_pages=1 << 30), -1), (dict(workspace_bytes=16), -4)):
+        c = cache(**kw)
+        assert call(c) == rc, kw
+    c = cache()
+    assert call(c, w=None) == -1 and call(c, keep=None) == -1 and call(c, w=FAKE + 2) == -1
+    assert call(c, sinks=-1) == -1 and call(c, recent=-1) == -1
+    assert lib.qd_last_error().startswith(b"qd_pages_evict: ")
+    assert call(cache(n_pages=1 << 26, workspace_bytes=1 << 40)) == -2

@@ -91,6 +91,7 @@ _SIGS = {
     "qd_pages_extend": (_i, [C.POINTER(PageCacheArgs), _vp, _vp]),
     "qd_pages_trim": (_i, [C.POINTER(PageCacheArgs), _vp, _vp]),
     "qd_pages_compact": (_i, [C.POINTER(PageCacheArgs), _vp, _vp]),
+    "qd_pages_evict": (_i, [C.POINTER(PageCacheArgs), _vp, _vp, _i, _i, _vp]),
     "qd_verify_sample_workspace_bytes": (_sz, [_i]),
     "qd_verify_sample": (_i, [_vp, _l, _vp, _l, _vp, _vp, _vp, _i, _i, _i] + [_vp] * 4 + [_i, _vp, _vp, _sz, _vp]),
     "qd_argmax_workspace_bytes": (_sz, [_i]),
@@ -720,6 +721,16 @@ class PageCache:
             n_live = torch.empty(1, dtype=torch.int32, device=self.device)
         self._run(stream, lib().qd_pages_compact, self._list("n_live", n_live, 1))
         return n_live
+
+    def evict(self, key_weights, keep, n_sinks=0, n_recent=0, stream=None):
+        """Sequence s cut to keep[s] tokens (negative or not below its length: unchanged): the first n_sinks, the last
+        n_recent and those of the largest key_weights f32 [layers, max_seqs, Hkv, max_pages * ps], each layer and kv
+        head its own. K, V and weights move down; weights past the kept ones become 0."""
+        a = self.args
+        _want("key_weights", key_weights, torch.float32, 4, self._dev,
+              (a.n_layers, a.max_seqs, a.n_kv_heads, a.max_pages * a.page_size))
+        self._run(stream, lib().qd_pages_evict, key_weights.data_ptr(), self._list("keep", keep, a.max_seqs), n_sinks,
+                  n_recent)
 
 
 def argmax_advance(logits, tok, pos, step, out_tokens, workspace=None, stream=None):

@@ -700,6 +700,22 @@ int qd_pages_compact(const qd_page_cache* c, int32_t* n_live, cudaStream_t strea
   return e == cudaSuccess ? QD_OK : cuda_fail(e, "qd_pages_compact");
 }
 
+int qd_pages_evict(const qd_page_cache* c, float* key_weights, const int32_t* keep, int n_sinks, int n_recent,
+                   cudaStream_t stream) {
+  const char* fn = "qd_pages_evict";
+  const int rc = check_page_cache(fn, c, true, true);
+  if (rc) return rc;
+  if (!key_weights || !keep) return fail(QD_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if ((uintptr_t)key_weights & 3u) return fail(QD_ERR_INVALID_ARG, "%s: key_weights must be 4-byte aligned", fn);
+  if (n_sinks < 0 || n_recent < 0) return fail(QD_ERR_INVALID_ARG, "%s: n_sinks=%d n_recent=%d", fn, n_sinks, n_recent);
+  if (c->head_dim > 256) return fail(QD_ERR_UNSUPPORTED, "%s: head_dim=%d (at most 256)", fn, c->head_dim);
+  if ((int64_t)c->n_pages * c->n_kv_heads * c->page_size > INT32_MAX)
+    return fail(QD_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 (page, kv head, slot) rows in the cache", fn);
+  const PageEvict e = {key_weights, keep, n_sinks, n_recent, c->n_kv_heads, c->head_dim};
+  cudaError_t rc2 = launch_pages_evict(page_state(c), page_copy(c), e, c->workspace, make_launch(stream, false));
+  return rc2 == cudaSuccess ? QD_OK : cuda_fail(rc2, fn);
+}
+
 // ------------------------------------------------------------------ sampled verification
 size_t qd_verify_sample_workspace_bytes(int batch) { return batch < 1 ? 0 : verify_sample_workspace_bytes(batch); }
 

@@ -399,6 +399,23 @@ struct PageCopy {
   size_t page_bytes;       // of one page of K (or V) in one layer
 };
 constexpr int kPagesMaxSeqs = 2048;
+// Cache pointers of one launch: K and V of 64 layers.
+constexpr int kPagePtrs = 128;
+struct PagePtrs {
+  unsigned char* p[kPagePtrs];
+};
+// Workspace: int32 words. [0] fork ticket (zero between calls), [1] number of page copies (or of
+// sequences that lose tokens), [2] pages in use; then two lists and a map of max(max_seqs, n_pages)
+// words each.
+struct PagesWs {
+  int32_t* head;
+  int32_t *src, *dst, *map;
+};
+inline PagesWs pages_ws(const PageState& c, void* workspace) {
+  const size_t cap = (size_t)(c.max_seqs > c.n_pages ? c.max_seqs : c.n_pages);
+  int32_t* w = (int32_t*)workspace;
+  return PagesWs{w, w + 64, w + 64 + cap, w + 64 + 2 * cap};
+}
 size_t pages_workspace_bytes(int max_seqs, int n_pages);
 cudaError_t launch_pages_copy(const PageCopy& pc, const int32_t* src, const int32_t* dst, int n, int n_pages,
                               const Launch& L);
@@ -407,6 +424,13 @@ cudaError_t launch_pages_fork(const PageState& c, const int32_t* parents, const 
 cudaError_t launch_pages_extend(const PageState& c, const PageCopy& pc, const int32_t* n_new, void* workspace,
                                 const Launch& L);
 cudaError_t launch_pages_trim(const PageState& c, const int32_t* new_lens, const Launch& L);
+struct PageEvict {
+  float* weights;          // [n_layers][max_seqs][n_kv_heads][max_pages * page_size]
+  const int32_t* keep;     // [max_seqs]
+  int n_sinks, n_recent, n_kv_heads, head_dim;
+};
+cudaError_t launch_pages_evict(const PageState& c, const PageCopy& pc, const PageEvict& e, void* workspace,
+                               const Launch& L);
 cudaError_t launch_pages_compact(const PageState& c, const PageCopy& pc, int32_t* n_live, void* workspace,
                                  const Launch& L);
 

@@ -22,6 +22,7 @@
 #include "kernels.h"
 #include "launch.cuh"
 #include "page_plan.h"
+#include "scan.cuh"
 
 #include <algorithm>
 
@@ -32,41 +33,7 @@ constexpr int kPlan = 1024;            // threads of the planning kernels (one C
 constexpr int kCopyTh = 128;
 constexpr int kCopyVec = 8;            // 16-byte pieces in flight per thread
 constexpr int kItem = kCopyTh * kCopyVec * 16;   // bytes a CTA copies at a time
-constexpr int kPtrs = 128;             // cache pointers (K and V of 64 layers) per launch
 constexpr int kForkTh = 128;
-
-struct PtrPack {
-  unsigned char* p[kPtrs];
-};
-
-// Workspace: int32 words. [0] fork ticket (zero between calls), [1] number of page
-// copies, [2] pages in use; then two lists and a map of list_cap words each.
-struct Ws {
-  int32_t* head;
-  int32_t *src, *dst, *map;
-};
-
-// Inclusive sum over the CTA's threads in thread order; total: the whole sum.
-template <typename S>
-QD_DEV S block_scan(S v, S* warp_sums, S& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  __syncthreads();   // warp_sums of the scan before have been read
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const S x = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += x;
-  }
-  if (lane == 31) warp_sums[warp] = v;
-  __syncthreads();
-  S before = 0, all = 0;
-  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
-    const S s = warp_sums[w];
-    if (w < warp) before += s;
-    all += s;
-  }
-  total = all;
-  return before + v;
-}
 
 // One CTA walks the pages [lo, hi) in ascending order, 16 per thread at a time (each
 // warp 512 consecutive ones, 16 coalesced loads in flight), and calls put(rank, page) for
@@ -110,7 +77,7 @@ QD_DEV int walk_pages(const int32_t* refs, int lo, int hi, bool want_free, int b
 // ---- page copies: pair i of the list, every cache pointer, in items of 16 KB. The
 // copies of one source (a page forked to many children) are neighbours, so it comes from
 // L2 after its first read.
-__global__ void __launch_bounds__(kCopyTh) pages_copy_kernel(const __grid_constant__ PtrPack pk, int n_ptrs,
+__global__ void __launch_bounds__(kCopyTh) pages_copy_kernel(const __grid_constant__ PagePtrs pk, int n_ptrs,
                                                              const int32_t* src, const int32_t* dst, int n,
                                                              const int32_t* n_dev, int n_pages, long long page_bytes,
                                                              int* err) {
@@ -144,7 +111,7 @@ __global__ void __launch_bounds__(kCopyTh) pages_copy_kernel(const __grid_consta
 // ---- fork: CTA i gives child i its parent's row. Each CTA checks the whole call first
 // (a bitmap of the children); the lengths are written by the last CTA to finish, so that
 // every CTA has seen the children empty.
-__global__ void __launch_bounds__(kForkTh) pages_fork_kernel(PageState c, Ws ws, const int32_t* parents,
+__global__ void __launch_bounds__(kForkTh) pages_fork_kernel(PageState c, PagesWs ws, const int32_t* parents,
                                                              const int32_t* children, int n, int* err) {
   extern __shared__ uint32_t seen[];
   __shared__ int s_bad, s_last;
@@ -188,7 +155,7 @@ __global__ void __launch_bounds__(kForkTh) pages_fork_kernel(PageState c, Ws ws,
 // ---- extend: one CTA plans. Per sequence: the pages it needs (and whether its shared
 // last page has to be copied), a prefix sum over the sequences, the lowest free ids into
 // ws.map, then the table rows, the counts and the list of copies.
-__global__ void __launch_bounds__(kPlan) pages_extend_kernel(PageState c, Ws ws, const int32_t* n_new, int* err) {
+__global__ void __launch_bounds__(kPlan) pages_extend_kernel(PageState c, PagesWs ws, const int32_t* n_new, int* err) {
   extern __shared__ __align__(16) int32_t sh[];
   pdl_launch_dependents();   // the copies wait for this kernel before they read the list
   int32_t* cand = sh;                     // [max_seqs] a shared last page, or -1
@@ -310,7 +277,7 @@ __global__ void __launch_bounds__(kForkTh) pages_trim_kernel(PageState c, const 
 
 // ---- compact: one CTA plans. n = pages in use; the used ids >= n move, in ascending
 // order, to the free ids < n.
-__global__ void __launch_bounds__(kPlan) pages_compact_kernel(PageState c, Ws ws, int32_t* n_live) {
+__global__ void __launch_bounds__(kPlan) pages_compact_kernel(PageState c, PagesWs ws, int32_t* n_live) {
   __shared__ int warp_sums[kPlan / 32];
   const int tid = threadIdx.x;
   pdl_launch_dependents();
@@ -333,7 +300,7 @@ __global__ void __launch_bounds__(kPlan) pages_compact_kernel(PageState c, Ws ws
 }
 
 // table entries of the moved pages; one CTA per sequence, its pages only
-__global__ void __launch_bounds__(kForkTh) pages_remap_kernel(PageState c, Ws ws, int* err) {
+__global__ void __launch_bounds__(kForkTh) pages_remap_kernel(PageState c, PagesWs ws, int* err) {
   pdl_launch_dependents();
   pdl_wait();
   const int s = blockIdx.x, n = ws.head[2];
@@ -345,18 +312,12 @@ __global__ void __launch_bounds__(kForkTh) pages_remap_kernel(PageState c, Ws ws
   }
 }
 
-Ws ws_of(const PageState& c, void* workspace) {
-  const size_t cap = (size_t)std::max(c.max_seqs, c.n_pages);
-  int32_t* w = (int32_t*)workspace;
-  return Ws{w, w + 64, w + 64 + cap, w + 64 + 2 * cap};
-}
-
 cudaError_t copy_pairs(const PageCopy& pc, const int32_t* src, const int32_t* dst, int n, const int32_t* n_dev,
                        int n_pages, const Launch& L) {
   const int per_page = (int)((pc.page_bytes + kItem - 1) / kItem);
-  for (int l0 = 0; l0 < pc.n_layers; l0 += kPtrs / 2) {
-    const int nl = std::min(kPtrs / 2, pc.n_layers - l0);
-    PtrPack pk = {};
+  for (int l0 = 0; l0 < pc.n_layers; l0 += kPagePtrs / 2) {
+    const int nl = std::min(kPagePtrs / 2, pc.n_layers - l0);
+    PagePtrs pk = {};
     for (int i = 0; i < nl; ++i) {
       pk.p[2 * i] = (unsigned char*)pc.k_cache[l0 + i];
       pk.p[2 * i + 1] = (unsigned char*)pc.v_cache[l0 + i];
@@ -386,13 +347,13 @@ cudaError_t launch_pages_copy(const PageCopy& pc, const int32_t* src, const int3
 cudaError_t launch_pages_fork(const PageState& c, const int32_t* parents, const int32_t* children, int n,
                               void* workspace, const Launch& L) {
   const size_t smem = (size_t)((c.max_seqs + 31) / 32) * 4;
-  return launch_ex(pages_fork_kernel, dim3(n), dim3(kForkTh), smem, L, c, ws_of(c, workspace), parents, children, n,
+  return launch_ex(pages_fork_kernel, dim3(n), dim3(kForkTh), smem, L, c, pages_ws(c, workspace), parents, children, n,
                    L.err);
 }
 
 cudaError_t launch_pages_extend(const PageState& c, const PageCopy& pc, const int32_t* n_new, void* workspace,
                                 const Launch& L) {
-  const Ws ws = ws_of(c, workspace);
+  const PagesWs ws = pages_ws(c, workspace);
   Launch first = L;
   first.pdl = false;
   cudaError_t e =
@@ -407,7 +368,7 @@ cudaError_t launch_pages_trim(const PageState& c, const int32_t* new_lens, const
 
 cudaError_t launch_pages_compact(const PageState& c, const PageCopy& pc, int32_t* n_live, void* workspace,
                                  const Launch& L) {
-  const Ws ws = ws_of(c, workspace);
+  const PagesWs ws = pages_ws(c, workspace);
   Launch first = L;
   first.pdl = false;
   cudaError_t e = launch_ex(pages_compact_kernel, dim3(1), dim3(kPlan), 0, first, c, ws, n_live);
