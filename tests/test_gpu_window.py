@@ -544,6 +544,7 @@ def test_weights(cuda_lib, rows, lens, hq, hkv, ps, last, window, sinks, dtype):
     q = _q(g, cu[-1], hq, dtype)
     before = torch.rand((len(rows), hkv, pt.shape[1] * ps), generator=g, device=DEV) * 0.1
     ws = torch.full((api.attn_key_weights_workspace_bytes(len(rows), cu[-1], hq, hkv, last),), 255, dtype=torch.uint8, device=DEV)
+    ws[:16384] = 0      # what has to be
     got = []
     for _ in range(2):
         sums = before.clone()
@@ -639,7 +640,7 @@ def test_weights_in_a_graph_with_other_lengths(cuda_lib):
     g = _gen(18)
     kp, vp, pt = ref.make_cache(g, [600, 600], 2, 16)
     cu, lens, q = _ints([0, 100, 200]), _ints([600, 600]), _q(g, 200, 8, torch.float32)
-    ws = torch.empty(api.attn_key_weights_workspace_bytes(2, 200, 8, 2), dtype=torch.uint8, device=DEV)
+    ws = torch.zeros(api.attn_key_weights_workspace_bytes(2, 200, 8, 2), dtype=torch.uint8, device=DEV)
     sums = torch.zeros((2, 2, pt.shape[1] * 16), device=DEV)
 
     def call():

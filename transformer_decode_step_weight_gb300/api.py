@@ -465,8 +465,8 @@ def _row_stride(name, t, B, rows, V, dev):
     return s
 
 
-# A window that hides nothing, and what of a windowed decode's workspace has to be zero before its
-# first use (QD_ATTN_WINDOW_HEAD in qd.h)
+# A window that hides nothing, and what of the workspaces of the windowed decode and of key weights has
+# to be zero before their first use (QD_ATTN_WINDOW_HEAD, QD_ATTN_WEIGHTS_HEAD in qd.h)
 ALL_KEYS = 2 ** 31 - 1
 _WINDOW_HEAD = 16384
 
@@ -565,7 +565,7 @@ def attn_key_weights(q, k_pages, page_table, cu_rows, seq_lens, scale, key_weigh
     _want("key_weights", key_weights, torch.float32, 3, dev, (B, Hkv, max_pages * ps))
     if n == 0:
         return key_weights
-    workspace = _scratch(workspace, lambda: attn_key_weights_workspace_bytes(B, n, Hq, Hkv, last), q, 0)
+    workspace = _scratch(workspace, lambda: attn_key_weights_workspace_bytes(B, n, Hq, Hkv, last), q, _WINDOW_HEAD)
     _check(lib().qd_attn_key_weights(q.data_ptr(), q.dtype is torch.float32, q_stride, k_pages.data_ptr(),
                                      page_table.data_ptr(), cu_rows.data_ptr(), seq_lens.data_ptr(), B, n, Hq, Hkv, D,
                                      ps, max_pages, n_pages, scale, last, ALL_KEYS if window is None else window, n_sinks,

@@ -539,6 +539,7 @@ int qd_attn_decode_window(const void* q, int q_is_f32, int64_t q_stride, const v
   return e == cudaSuccess ? QD_OK : cuda_fail(e, fn);
 }
 
+static_assert(kAttnWeightsHeadBytes == QD_ATTN_WEIGHTS_HEAD, "the head that the header names");
 size_t qd_attn_key_weights_workspace_bytes(int batch, int n_rows, int n_q_heads, int n_kv_heads, int last) {
   if (batch < 1 || n_rows < 1 || n_kv_heads < 1 || n_q_heads < n_kv_heads || last < 0) return 0;
   return attn_key_weights_workspace_bytes(batch, n_rows, n_q_heads, n_kv_heads, last, true);

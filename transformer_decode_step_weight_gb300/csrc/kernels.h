@@ -364,7 +364,9 @@ size_t attn_window_workspace_bytes(int B, int Hq, int Hkv, long long max_keys);
 cudaError_t launch_attn_window(const AttnRowsArgs& a, const Launch& L);
 
 // The weights of packed rows' attention added up per key (attention_weights.cu): of the last `last` rows of
-// each sequence (0: all) into a.key_weights; out and v_pages unused.
+// each sequence (0: all) into a.key_weights; out and v_pages unused. The workspace's first
+// kAttnWeightsHeadBytes are zero before its first use (tickets, zero again after each call).
+constexpr size_t kAttnWeightsHeadBytes = 16384;
 size_t attn_key_weights_workspace_bytes(int B, int n_rows, int Hq, int Hkv, int last, bool f32);
 cudaError_t launch_attn_key_weights(const AttnRowsArgs& a, int last, const Launch& L);
 
