@@ -175,16 +175,29 @@ QD_DEV void tma_load_rows(void* dst, const CUtensorMap* map, int row, uint64_t* 
 }
 // The products are issued by one lane of a warp whose lanes all walk the same way, so that
 // descriptors stay in uniform registers; `lead` says which lane.
-// Step kk of 16 keys, left out by lanes whose `steps` it is not below.
-QD_DEV void mma_pv(int steps, int kk, uint32_t tmem_d, uint32_t tmem_a, uint64_t db, uint32_t accumulate) {
+// Step kk of 16 keys, left out by lanes whose `steps` it is not below, and (window form) where it is below
+// `step0`.
+template <bool WINDOW>
+QD_DEV void mma_pv(int step0, int steps, int kk, uint32_t tmem_d, uint32_t tmem_a, uint64_t db, uint32_t accumulate) {
   constexpr uint32_t kIdesc = tc::idesc_m128(kD) | (1u << 16);   // B MN-major
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.gt.s32 q, %5, %6;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "r"(tmem_a), "l"(db), "r"(kIdesc), "r"(accumulate), "r"(steps), "r"(kk)
-      : "memory");
+  if constexpr (WINDOW) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.gt.s32 q, %5, %6;\n\t"
+        "setp.le.and.s32 q, %7, %6, q;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "r"(tmem_a), "l"(db), "r"(kIdesc), "r"(accumulate), "r"(steps), "r"(kk), "r"(step0)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.gt.s32 q, %5, %6;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "r"(tmem_a), "l"(db), "r"(kIdesc), "r"(accumulate), "r"(steps), "r"(kk)
+        : "memory");
+  }
 }
 QD_DEV void mma_qk(bool lead, uint32_t tmem_d, uint64_t da, uint64_t db, uint32_t accumulate) {
   constexpr uint32_t kIdesc = tc::idesc_m128(kKeys);
@@ -269,21 +282,17 @@ struct Work {
   QD_DEV int seen(const Seg& a, int t) const {
     return PROMPT ? max(0, a.off + min((t + 1) << log_tpt, a.n)) : a.len;
   }
-  // Window form: the first key of row j's window; the key tiles of the first tokens, which stay; and
-  // the tiles between them and the windows of row tile t, which no row of it sees and no unit stands for.
+  // Window form. The first key of row j's window; the first tokens' keys, up to whole boxes of 16; and
+  // the keys between them and the windows of row tile t, which no row of it sees: they are left out
+  // (whole boxes again), and keys from there on are counted `skip` lower, so that a row tile's
+  // units are those of its first tokens and windows alone. (With whole tiles left out a window of 1024
+  // took 10.9 units a row tile instead of 9, and twice as many that have to be masked.)
   QD_DEV int start(const Seg& a, int j) const { return max(0, a.off + j + 1 - window); }
-  QD_DEV int first_tiles() const { return (sinks + kKeys - 1) >> 7; }
-  QD_DEV int skipped(const Seg& a, int t) const {
-    return WINDOW ? max(0, (start(a, t << log_tpt) >> 7) - first_tiles()) : 0;
+  QD_DEV int first16() const { return (sinks + 15) & ~15; }
+  QD_DEV int skip(const Seg& a, int t) const {
+    return WINDOW ? max(0, (start(a, t << log_tpt) & ~15) - first16()) : 0;
   }
-  QD_DEV long long skipped_before(const Seg& a, int t) const {   // by the row tiles before t
-    if (!WINDOW) return 0;
-    const long long c = (long long)a.off + 1 - window, st = first_tiles();
-    const long long i0 = max(0LL, (((st + 1) << 7) - c + tpt() - 1) >> log_tpt);   // the first that skips any
-    if (i0 >= t) return 0;
-    return floor_sum((c >> log_tpt) + t, 7 - log_tpt) - floor_sum((c >> log_tpt) + i0, 7 - log_tpt) - st * (t - i0);
-  }
-  QD_DEV int units(const Seg& a, int t) const { return max(1, (seen(a, t) + kKeys - 1) >> 7) - skipped(a, t); }
+  QD_DEV int units(const Seg& a, int t) const { return max(1, (seen(a, t) - skip(a, t) + kKeys - 1) >> 7); }
   // sum over j < n of floor(j / 2^k)
   QD_DEV static long long floor_sum(long long n, int k) {
     const long long q = n >> k;
@@ -292,10 +301,16 @@ struct Work {
   // units of the row tiles before t (t <= tiles)
   QD_DEV long long before(const Seg& a, int t) const {
     if (!PROMPT) return (long long)t * units(a, 0);
-    const int full = min(t, a.tiles - 1);
+    int full = min(t, a.tiles - 1);
     long long sum = t == a.tiles && t > 0 ? units(a, t - 1) : 0;   // (prompt form: steps are tiles)
     if (full <= 0) return sum;
-    sum -= skipped_before(a, full);
+    if (WINDOW) {   // whole row tiles that leave keys out all have as many units (16 divides a row tile's tokens)
+      const int c = (a.off + 1 - window) & ~15;   // tile i's windows begin at c + i tpt, rounded down
+      const int i1 = first16() < c ? 0 : min(full, ((first16() - c) >> log_tpt) + 1);   // the first that does
+      if (i1 < full) sum += (long long)(full - i1) * units(a, i1);
+      full = i1;
+      if (full == 0) return sum;
+    }
     // tile i < full ends at off + (i + 1) tpt keys: one unit up to 128, else the quotient
     const int one = a.off > kKeys ? 0 : min(full, (kKeys - a.off) >> log_tpt);
     sum += one;
@@ -358,10 +373,11 @@ QD_DEV uint32_t any_odd(const uint4& x) {
 // each (last 0: none) and go through the keys together, 32 at a time, until each value that is not
 // finite is known to be NaN. A prompt of 8192 tokens with a NaN in its first value takes 1.1 ms, with
 // an infinity there 2.2 (0.39 without).
-// Window form: the lane's row sees no key from `hid0` (the first tokens' end) up to `hid1`; nobody's below `gap1`.
+// Window form: keys are counted as in Work::skip (from `first16` on, `skip` lower), and the lane's row sees none from
+// `hid0` (the first tokens' end) up to `hid1`.
 template <bool WINDOW>
 __device__ __noinline__ void patch_rows(const Params& p, const int32_t* pt, int g, int first, int last, int d0,
-                                        unsigned char* row, int xr, bool half, bool taken, int hid0, int hid1, int gap1) {
+                                        unsigned char* row, int xr, bool half, bool taken, int hid0, int hid1, int first16, int skip) {
   const int lane = threadIdx.x & 31;
   auto cell = [&](int k) {
     const int c = (d0 + k) >> (half ? 3 : 2);
@@ -379,10 +395,10 @@ __device__ __noinline__ void patch_rows(const Params& p, const int32_t* pt, int 
 #pragma unroll 1
   for (int base = first; base < end; base += 32) {
     if (__all_sync(0xffffffffu, (open & ~nan) == 0)) break;
-    if (WINDOW && base >= hid0 && base + 32 <= gap1) base += (gap1 - base) & ~31;   // (first is a multiple of 32)
     int at = -1;   // the cache row of key base + lane
-    if (base + lane < end && (!WINDOW || base + lane < hid0 || base + lane >= gap1)) {
-      const PagedSlot sl = paged_slot(pt, base + lane, p.page_size, p.div, p.n_pages);
+    if (base + lane < end) {
+      const int key = base + lane + (WINDOW && base + lane >= first16 ? skip : 0);
+      const PagedSlot sl = paged_slot(pt, key, p.page_size, p.div, p.n_pages);
       at = (sl.page * p.Hkv + g) * p.page_size + sl.slot;
     }
     // eight lanes read the dims of a key
@@ -692,12 +708,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     int g, t, k0, k1, nk, n;
     int first_row, packed;     // packed rows of the tile: the first, how many
     int seen_max, seen_min;    // keys past the first are nobody's, keys before the second everybody's
-    // window form: of the keys from W.sinks on, those before gap are nobody's, those from all on everybody's
+    // window form (keys counted as in Work::skip, here and from here on): of those from W.sinks on, the ones before
+    // gap are nobody's, the ones from all on everybody's
     int gap, all, skip;
     const int32_t* pt;
-    QD_DEV int key_tile(int i, int first_tiles) const {   // of unit i
-      return WINDOW && i >= first_tiles ? i + skip : i;
-    }
   };
   auto piece_at = [&](const Place& x) {
     const Seg& a = x.a;
@@ -714,12 +728,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     q.seen_max = W.seen(a, q.t);
     q.gap = q.all = q.skip = 0;
     if (WINDOW) {
-      q.gap = W.start(a, row);
-      q.all = W.start(a, row + q.packed - 1);
-      q.skip = W.skipped(a, q.t);
+      q.skip = W.skip(a, q.t);
+      q.gap = W.start(a, row) - q.skip;
+      q.all = W.start(a, row + q.packed - 1) - q.skip;
+      q.seen_max -= q.skip;
     }
     if (PROMPT) {
-      q.seen_min = max(0, a.off + row + 1);
+      q.seen_min = max(0, a.off + row + 1) - q.skip;
     } else {
       int m = a.len;
       for (int i = lane; i < q.packed; i += 32) {
@@ -762,14 +777,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         int bad_page = 0;
         auto look = [&](int i) {
           Look x;
-          const int key0 = pc.key_tile(k0 + i, W.first_tiles()) * kKeys;
+          const int key0 = (k0 + i) * kKeys;
 #pragma unroll
           for (int j = 0; j < kMine; ++j) {
             const int key = p.box ? key0 + lane * p.box : key0 + 32 * j + lane;
             x.row[j] = -1;
             const bool some = !WINDOW || key < W.sinks || key + (p.box ? p.box : 1) > pc.gap;   // seen by some row
+            const int token = key + (WINDOW && key >= W.first16() ? pc.skip : 0);
             if (i < n && key < min(seen_max, key0 + kKeys) && (j == 0 || !p.box) && some) {
-              const PagedSlot sl = paged_slot(pt, key, p.page_size, p.div, p.n_pages);
+              const PagedSlot sl = paged_slot(pt, token, p.page_size, p.div, p.n_pages);
               if (!sl.ok) bad_page = 1;   // no branch on what is still being read
               x.row[j] = (sl.page * p.Hkv + g) * p.page_size + sl.slot;
             }
@@ -869,16 +885,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < n; ++i) {
           const uint32_t slot = kRingK + rk.slot;
           wait(&full[slot], rk.ph);
-          const int key0 = pc.key_tile(k0 + i, W.first_tiles()) * kKeys;
+          const int key0 = (k0 + i) * kKeys;
           int steps = kKeys / 16;   // of 16 keys that some row sees
+          int step0 = 0;            // window form: the first of them
           const bool behind_some = WINDOW && key0 < pc.all && key0 + kKeys > W.sinks;
           if (key0 + kKeys > seen_min || behind_some) {
             // a V tile that some row must not see whole: NaN and infinities taken out, rows past
             // everybody's keys to zero up to the last step's end
-            int lo = max(0, seen_min - key0);
-            const int hi = min(seen_max - key0, kKeys);
-            if (behind_some) lo = min(lo, max(0, W.sinks - key0));
-            steps = max(1, (hi + 15) >> 4);
+            int lo = max(0, seen_min - key0), hi = min(seen_max - key0, kKeys);
+            int free0 = 0, free1 = 0;   // window form: keys that need no look
+            if (WINDOW && behind_some) {
+              const bool some_first = key0 < W.sinks;
+              if (pc.gap >= key0 + kKeys) hi = min(hi, W.sinks - key0);   // of the first tokens' tile nothing else
+              if (!some_first) step0 = max(0, pc.gap - key0) >> 4;
+              free0 = max(0, pc.all - key0);   // from here on only those behind the rows' last keys
+              free1 = max(lo, free0);
+              lo = some_first ? min(lo, W.sinks - key0) : min(lo, step0 * 16);
+            }
+            steps = max(step0 + 1, (hi + 15) >> 4);
             // lane: of key lane / 4 in a group of 8, 16-byte pieces lane & 3, + 4, + 8, + 12
             const int sub = lane >> 2, cc = lane & 3;
             unsigned char* v = data + (kQ + slot) * kSlot + sub * 128;
@@ -886,6 +910,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                kHalf8 + (((cc + 4) ^ sub) << 4)};
 #pragma unroll 1
             for (int key = (lo & ~7) + sub; key < steps * 16; key += 8) {
+              if (WINDOW && key - sub >= free0 && key - sub + 8 <= free1) {   // on to the group of key free1
+                key = (free1 & ~7) - 8 + sub;
+                continue;
+              }
               unsigned char* cell = v + (key >> 3) * kKeys8;
               const bool past_first = WINDOW && key0 + key >= W.sinks;
               if (key >= hi || (past_first && key0 + key < pc.gap)) {
@@ -922,8 +950,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t t32 = part < 2 ? 32 : 16;
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              mma_pv(go, kk, tO, ta + t32 * (kk >> 1) + 8 * (kk & 1), dv + (uint64_t)(kk * 2 * kKeys8 >> 4),
-                     kk != 0 || part != PARTS - 1 || !first);
+              mma_pv<WINDOW>(step0, go, kk, tO, ta + t32 * (kk >> 1) + 8 * (kk & 1),
+                             dv + (uint64_t)(kk * 2 * kKeys8 >> 4),
+                             (WINDOW ? kk != step0 : kk != 0) || part != PARTS - 1 || !first);
           }
           commit(lead, &o_done[rb.slot]);
           commit(lead, &empty[slot]);
@@ -1048,7 +1077,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (valid) {
         const int j = (t << W.log_tpt) + (row >> p.log_rep);
         if (PROMPT) {
-          lim = max(0, a.off + j + 1);
+          lim = max(0, a.off + j + 1) - pc.skip;
         } else {
           const int l = p.seq_lens[a.row0 + j];
           lim = l < 0 || l > p.cap ? 0 : min(l, a.len);
@@ -1057,7 +1086,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // what all valid rows of the warp see (rows that are not valid hold anything)
       const int warp_min = __reduce_min_sync(0xffffffffu, valid ? lim : INT32_MAX);
       // window form: keys from W.sinks on that lie before it the row does not see; the most of the warp's rows
-      const int from = WINDOW ? max(0, lim - W.window) : 0;
+      const int from = WINDOW ? max(0, lim - W.window) : 0;   // (windows begin behind the keys that are left out)
       const int warp_from = WINDOW ? __reduce_max_sync(0xffffffffu, valid ? from : 0) : 0;
       auto sees = [&](int key) { return key < lim && (!WINDOW || key >= from || key < W.sinks); };
       auto masked = [&](int key, int m) {   // whether some row of the warp does not see all of m keys
@@ -1126,7 +1155,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < n; ++i) {
           const uint32_t ct = tile + i;
           const int b = (int)(ct & 1);
-          const int key0 = pc.key_tile(k0 + i, W.first_tiles()) * kKeys + 64 * hf;
+          const int key0 = (k0 + i) * kKeys + 64 * hf;
           const uint32_t ts = tS + 128 * b + lanes + 64 * hf;
           wait(&s_full[b], (ct >> 1) & 1);
           tc::fence_after();
@@ -1206,7 +1235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int i = hf == begins ? 0 : kSolo; i < n; i += i < kSolo - 1 ? 1 : 2) {
           const uint32_t ct = tile + i, b = ct % kBufs;
-          const int key0 = pc.key_tile(k0 + i, W.first_tiles()) * kKeys;
+          const int key0 = (k0 + i) * kKeys;
           const uint32_t ts = tS + 128 * b + lanes;
           // (whoever has not followed the kBufs tiles before this one waits for the reference first:
           // the barrier of S is then at this tile's phase)
@@ -1284,8 +1313,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int kGroup = kFresh ? kSoft : kSoft / 2;   // threads that write a piece out
       const int gid = tid & (kGroup - 1), gbar = kFresh || hf ? 6 : 1;
       const bool whole = k0 == 0 && k1 == nk;
-      const int key_lo = pc.key_tile(k0, W.first_tiles()) * kKeys;   // the piece's keys
-      const int key_hi = (pc.key_tile(k1 - 1, W.first_tiles()) + 1) * kKeys;
       const bool final_out = whole && PROMPT;      // else O as it is, with m and l
       float* part = p.part + ((size_t)blockIdx.x * 2 + (k0 == 0 ? 1 : 0)) * kPartFloats;
       // row r of the tile in [n_rows, Hq]: tile0 + out_row(r)
@@ -1327,8 +1354,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const bool look = (patch || z != 0.f) && valid && !dead && l == l;
         if (__any_sync(0xffffffffu, look))
-          patch_rows<WINDOW>(p, pt, g, key_lo, look ? min(lim, key_hi) : 0, col0, mine, xr, false, patch, W.sinks, from,
-                             pc.gap);
+          patch_rows<WINDOW>(p, pt, g, k0 * kKeys, look ? min(lim, k1 * kKeys) : 0, col0, mine, xr, false, patch, W.sinks,
+                             from, W.first16(), pc.skip);
         if (valid && !dead && !final_out && hf == 0) put_stats();
         // the rows that this warp's lanes and their other holders' wrote
         bar_sync(2 + (warp & 3), 64);
@@ -1400,9 +1427,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (__any_sync(0xffffffffu, look)) {
 #pragma unroll 1
             for (int d0 = 0; d0 < kD; d0 += 64)
-              patch_rows<WINDOW>(p, pt, g, key_lo, look ? min(lim, key_hi) : 0, d0,
+              patch_rows<WINDOW>(p, pt, g, k0 * kKeys, look ? min(lim, k1 * kKeys) : 0, d0,
                                  mine + (final_out ? (d0 >> 6) * (kChunk - 128) : 0), final_out ? xr : 0, final_out, patch,
-                                 W.sinks, from, pc.gap);
+                                 W.sinks, from, W.first16(), pc.skip);
           }
           // a warp whose 32 rows are all there hands them to the copy engine (row by row they took
           // 2300 cycles of the warp, as long as a tile), the last rows of a prompt go one by one
@@ -1629,7 +1656,7 @@ cudaError_t run(const AttnRowsArgs& a, float* pre_o, AttnFrom* from, const Launc
   }
   if (a.page_size % 16 == 0) {
     p.box = 16;
-    while (p.box < kKeys && a.page_size % (2 * p.box) == 0) p.box *= 2;
+    while (!WINDOW && p.box < kKeys && a.page_size % (2 * p.box) == 0) p.box *= 2;   // (window form: keys are left out by 16)
     const uint64_t rows = (uint64_t)a.n_pages * a.Hkv * a.page_size;
     cudaError_t e = encode_tmap_bf16_rows128(&tk, a.k_pages, rows, p.box);
     if (e == cudaSuccess) e = encode_tmap_bf16_rows128(&tv, a.v_pages, rows, p.box);
