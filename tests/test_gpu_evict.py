@@ -106,12 +106,12 @@ def test_evict(cuda_lib, lens, layers, hkv, ps, keep, sinks, recent, ties):
     assert api.check_device_error() == 0
 
 
-@pytest.mark.parametrize("seed", range(6))
+@pytest.mark.parametrize("seed", range(8))
 def test_evict_ragged_and_again(cuda_lib, seed):
     r = np.random.default_rng(seed)
-    B = int(r.integers(1, 12))
+    B = int(r.integers(1, 12)) if seed < 6 else 40
     lens = [int(x) for x in 2 ** r.uniform(0, 11.5, B)]
-    s = State(lens, int(r.integers(1, 4)), int(r.choice([1, 2, 8])), int(r.choice([1, 7, 16, 24, 128])), seed=seed, ties=seed % 2 == 0)
+    s = State(lens, int(r.integers(1, 4)) if seed < 6 else 9, int(r.choice([1, 2, 8])) if seed < 6 else 2, int(r.choice([1, 7, 16, 24, 128])), seed=seed, ties=seed % 2 == 0)
     for _ in range(3):
         lens = s.cache.seq_lens.tolist()
         keep = [int(r.integers(-1, n + 2)) for n in lens]
@@ -156,10 +156,12 @@ def test_evict_head_sizes_and_many_layers(cuda_lib, d, layers):
     assert api.check_device_error() == 0
 
 
-def test_evict_many_sequences(cuda_lib):
+@pytest.mark.parametrize("n", [500, 1300])     # (both ways of working a row)
+def test_evict_many_sequences(cuda_lib, n):
     r = np.random.default_rng(5)
-    lens = [int(x) for x in r.integers(0, 60, 500)]
-    keep = [int(x) for x in r.integers(-1, 60, 500)]
+    lens = [int(x) for x in r.integers(0, 60, n)]
+    keep = [int(x) for x in r.integers(-1, 60, n)]
+    lens[7], keep[7] = 2500, 1203
     s = State(lens, 1, 1, 16)
     s.cache.evict(s.w, _ints(keep), 2, 5)
     s.check(keep, 2, 5)

@@ -167,20 +167,18 @@ QD_DEV Seg segment(const Params& p, int s) {
 }
 QD_DEV int row_tiles(const Params& p, const Seg& a) { return (a.n + (kTile >> p.log_rep) - 1) >> (7 - p.log_rep); }
 
-// CTAs that share each walk of `walk` tiles: those that give G CTAs the shortest run, when an item costs
-// some 3 tiles beside its walk; `most` items times shares at most.
-QD_DEV int shares_for(long long items, long long walk, int G, long long most) {
-  int best = 1;
-  float least = INFINITY;
-  const float it = (float)items, wk = (float)walk;
-  for (int n = 1; n <= kMaxShares && n <= walk && n <= G && items * n <= most; ++n) {
-    const float t = ceilf(it / (float)(G / n)) * (ceilf(wk / (float)n) + 3.f);
-    if (t < least) {
-      least = t;
-      best = n;
-    }
+// CTAs that share each walk of `walk` tiles on average: those that give G CTAs the shortest run, when an
+// item costs some 3 tiles beside its walk and, over several turns, long and short walks come to three
+// quarters of the longest; `most` items times shares at most. By a whole warp, a count a lane.
+QD_DEV int shares_for(long long items, long long walk, int G, long long most, int lane) {
+  const int n = (lane & (kMaxShares - 1)) + 1, groups = G / n;
+  uint32_t key = 0xffffffffu;
+  if (n == 1 || (n <= walk && groups > 0 && items * n <= most)) {
+    const float turns = ceilf((float)items / (float)groups), tiles = ceilf((float)walk / (float)n);
+    const float t = turns <= 1.f ? tiles + 3.f : turns * (0.75f * tiles + 3.f);
+    key = (uint32_t)fminf(4.f * t, 1e8f) << 5 | (uint32_t)n;
   }
-  return best;
+  return (int)(__reduce_min_sync(0xffffffffu, key) & 31u);
 }
 
 template <int PARTS, int PASS>
@@ -346,7 +344,7 @@ __global__ void __launch_bounds__(kTh, 1) attn_weights_kernel(const __grid_const
   const long long segs = max(1LL, p.base[2 * (kMaxSeg + 1)]);
   const long long items = (kRows ? all_keys : all_rows) * p.Hkv;
   const int shares = items == 0 ? 1 : shares_for(items, max(1LL, (kRows ? all_rows : all_keys) / segs), gridDim.x,
-                                                 PASS == kSumsOne ? INT64_MAX / kMaxShares : kMaxParts);
+                                                 PASS == kSumsOne ? INT64_MAX / kMaxShares : kMaxParts, lane);
   const int rank = blockIdx.x % shares, group = blockIdx.x / shares, groups = gridDim.x / shares;
   const int tpt = kTile >> p.log_rep;   // tokens of a row tile
   auto next_item = [&](long long& round, long long& item) {
@@ -523,10 +521,12 @@ __global__ void __launch_bounds__(kTh, 1) attn_weights_kernel(const __grid_const
           ++brought;
         }
       } else {
-        Look now, next = look(x, tile_at(x, 0));
+        Look now, next = look(x, tile_at(x, 0)), third = {};
+        if (x.n > 1) third = look(x, tile_at(x, 1));
         for (int i = 0; i < x.n; ++i) {
           now = next;
-          if (i + 1 < x.n) next = look(x, tile_at(x, i + 1));
+          next = third;
+          if (i + 2 < x.n) third = look(x, tile_at(x, i + 2));
           wait(&empty[rt.slot], rt.ph ^ 1);
           bring_keys(x, now, moving + (size_t)rt.slot * kSlot, &full[rt.slot]);
           rt.step(kStages);

@@ -9,8 +9,8 @@
 //
 // Selection: the border between kept and not by radix over the weights as ordered integers (11, 11
 // and 10 bits, a shared-memory histogram each; the row, some 10 KB, comes from L2), then one pass
-// in token order in which equal weights count from the left. Moving is bound by HBM (PERF_MOVE):
-// 64 rows of K and V at a time through a ring of asynchronous copies. A kept token's new place r is
+// in token order in which equal weights count from the left. Moving is bound by HBM (5.2 TB/s read and written):
+// 32 or 64 rows of K and V at a time through a ring of asynchronous copies. A kept token's new place r is
 // below those of all later ones, and they lie at r + 1 or behind it, so a batch may be written while
 // the loads of later ones are under way; it only has to have landed whole itself.
 #include "common.cuh"
@@ -25,11 +25,17 @@ namespace qd {
 namespace {
 
 constexpr int kPlan = 1024;
-constexpr int kTh = 512;
 constexpr int kBins = 2048;
 constexpr int kList = 1024;            // kept tokens found before they are moved
-constexpr int kBatch = 64;             // rows moved at a time
-constexpr int kStages = 3;
+// How a (layer, sequence, kv head) is worked: threads, rows moved at a time, places of the ring, CTAs an
+// SM. Few of them (one sequence of 28 layers, 8 kv heads) want the most under way in each, many (36
+// layers x 4 sequences) more CTAs, whose selections run beside other CTAs' moves: Few 51 and 361 us, Many 58 and 342.
+struct Few {
+  static constexpr int kTh = 512, kBatch = 64, kStages = 3, kCtas = 2;
+};
+struct Many {
+  static constexpr int kTh = 256, kBatch = 32, kStages = 2, kCtas = 4;
+};
 constexpr int kMaxHeadDim = 256;
 
 // The tokens that stay, of n, without asking the weights: the first and the last.
@@ -99,6 +105,7 @@ QD_DEV uint32_t order_of(float w) {
 
 // Adds the bins from the top: the bin in which the `want`-th value from above lies, and how many lie
 // above that bin (the whole CTA; 1 <= want <= all).
+template <int kTh>
 QD_DEV void find_bin(const int* hist, int want, int* warp_sums, int* s_out, int& bin, int& above) {
   constexpr int kPer = kBins / kTh;
   const int top = kBins - 1 - threadIdx.x * kPer;
@@ -119,9 +126,11 @@ QD_DEV void find_bin(const int* hist, int want, int* warp_sums, int* s_out, int&
   __syncthreads();
 }
 
-__global__ void __launch_bounds__(kTh, 2) pages_evict_kernel(const __grid_constant__ PagePtrs pk, PageState c, PagesWs ws,
+template <typename How>
+__global__ void __launch_bounds__(How::kTh, How::kCtas) pages_evict_kernel(const __grid_constant__ PagePtrs pk, PageState c, PagesWs ws,
                                                              const __grid_constant__ PageEvict e, const PageDiv div,
                                                              int layer0) {
+  constexpr int kTh = How::kTh, kBatch = How::kBatch, kStages = How::kStages;
   extern __shared__ __align__(128) unsigned char ring[];   // [kStages][K and V][kBatch rows]
   __shared__ int s_from[kList], warp_sums[kTh / 32], s_out[2];
   __shared__ float s_val[kList];
@@ -156,7 +165,7 @@ __global__ void __launch_bounds__(kTh, 2) pages_evict_kernel(const __grid_consta
         }
         __syncthreads();
         int bin, above;
-        find_bin(s_hist, left, warp_sums, s_out, bin, above);
+        find_bin<kTh>(s_hist, left, warp_sums, s_out, bin, above);
         prefix = prefix << bits | (uint32_t)bin;
         left -= above;
       }
@@ -239,6 +248,24 @@ __global__ void __launch_bounds__(kTh, 2) pages_evict_kernel(const __grid_consta
   }
 }
 
+template <typename How>
+cudaError_t move(const PageState& c, const PageCopy& pc, const PageEvict& e, const PagesWs& ws, Launch L) {
+  constexpr size_t kRowSmem = (size_t)How::kStages * 2 * How::kBatch * 2;
+  cudaError_t rc = allow_smem<pages_evict_kernel<How>>(kRowSmem * kMaxHeadDim);   // (asked for once)
+  for (int l0 = 0; rc == cudaSuccess && l0 < pc.n_layers; l0 += kPagePtrs / 2) {
+    const int nl = std::min(kPagePtrs / 2, pc.n_layers - l0);
+    PagePtrs pk = {};
+    for (int i = 0; i < nl; ++i) {
+      pk.p[2 * i] = (unsigned char*)pc.k_cache[l0 + i];
+      pk.p[2 * i + 1] = (unsigned char*)pc.v_cache[l0 + i];
+    }
+    rc = launch_ex(pages_evict_kernel<How>, dim3(e.n_kv_heads, std::min(c.max_seqs, 64), nl), dim3(How::kTh),
+                   kRowSmem * e.head_dim, L, pk, c, ws, e, make_page_div(c.page_size), l0);
+    L.pdl = false;
+  }
+  return rc;
+}
+
 }  // namespace
 
 cudaError_t launch_pages_evict(const PageState& c, const PageCopy& pc, const PageEvict& e, void* workspace,
@@ -250,21 +277,9 @@ cudaError_t launch_pages_evict(const PageState& c, const PageCopy& pc, const Pag
   cudaError_t rc = launch_ex(pages_evict_plan_kernel, dim3(1), dim3(kPlan), 0, first, c, ws, e.keep, e.n_sinks,
                              e.n_recent, L.err);
   if (rc != cudaSuccess) return rc;
-  const size_t smem = (size_t)kStages * 2 * kBatch * e.head_dim * 2;
-  rc = allow_smem<pages_evict_kernel>((size_t)kStages * 2 * kBatch * kMaxHeadDim * 2);   // (asked for once)
+  const bool few = (long long)pc.n_layers * c.max_seqs * e.n_kv_heads <= 4LL * dev_info().sm_count;
+  rc = few ? move<Few>(c, pc, e, ws, moves) : move<Many>(c, pc, e, ws, moves);
   if (rc != cudaSuccess) return rc;
-  for (int l0 = 0; l0 < pc.n_layers; l0 += kPagePtrs / 2) {
-    const int nl = std::min(kPagePtrs / 2, pc.n_layers - l0);
-    PagePtrs pk = {};
-    for (int i = 0; i < nl; ++i) {
-      pk.p[2 * i] = (unsigned char*)pc.k_cache[l0 + i];
-      pk.p[2 * i + 1] = (unsigned char*)pc.v_cache[l0 + i];
-    }
-    rc = launch_ex(pages_evict_kernel, dim3(e.n_kv_heads, std::min(c.max_seqs, 64), nl), dim3(kTh), smem, moves, pk, c, ws,
-                   e, make_page_div(c.page_size), l0);
-    if (rc != cudaSuccess) return rc;
-    moves.pdl = false;
-  }
   return launch_pages_trim(c, ws.src, last);
 }
 
