@@ -239,6 +239,7 @@ __global__ void __launch_bounds__(kTh, 1) attn_weights_kernel(const __grid_const
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
   if (tid == 0) *s_abort = 0;
+  if (PASS == kStats) pdl_launch_dependents();   // the second launch waits for this one before it reads
   if (smem_u32(smem) & 1023u) {   // the swizzled tiles rest on it (there is no static shared memory); the same in all CTAs
     if (tid == 0) set_error(p.err, QD_DEVERR_TIMEOUT);
     if (PASS != kStats) pdl_wait();
