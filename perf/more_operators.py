@@ -358,8 +358,7 @@ def _own(s):
         if "work" not in s:
             s["work"] = torch.zeros(api.attn_prompt_workspace_bytes(), dtype=torch.uint8, device=DEV)
         return api.attn_prompt_window(s["q"], s["k"], s["v"], s["table"], s["cu"], s["lens"], SCALE, s["window"],
-                                      n_sinks=s["sinks"], out=s.setdefault("out", torch.zeros_like(s["q"])),
-                                      workspace=s["work"])
+                                      n_sinks=s["sinks"], workspace=s["work"])
     if op == "weights":
         if "work" not in s:
             s["work"] = torch.zeros(api.attn_key_weights_workspace_bytes(s["batch"], sum(s["n_rows"]), s["hq"], s["hkv"],
