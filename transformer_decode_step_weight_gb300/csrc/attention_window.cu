@@ -13,11 +13,13 @@
 // rounding, since the products' own accumulation truncates. The splits are joined in their order by
 // the last of them (ticket).
 //
-// HBM-bound: 1.08 GB in 176 us at 64 sequences x 4100 keys (32 q heads, 8 kv heads).
+// HBM-bound: 1.08 GB in 174 us (6.2 TB/s) at 64 sequences x 4100 keys (32 q heads, 8 kv heads); one sequence's
+// 1028 keys 7.6 us, the launch and a chain of dependent reads (length, pages, keys, partial results).
 //
 // The weights need every split's statistics first, so the scores (f32, log2 units) are kept in the
 // workspace, a sixteenth of K and V's bytes at four q heads a kv head, and a second kernel turns
-// them into weights: reading K again would be half of all bytes. A thread owns a key, so no atomics.
+// them into weights: reading K again would be half of all bytes. A thread owns a key, so no atomics. 16
+// sequences x 4400 to 7200 keys: 84 us, of which the second kernel some 8 (13 with one key a thread at a time).
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.cuh"
@@ -375,7 +377,7 @@ __global__ void __launch_bounds__(kTh, 3) attn_window_kernel(const __grid_consta
 }
 
 // The keys' weights, from the scores and the rows' statistics: CTA (part of the keys, kv head, sequence)
-constexpr int kAddTh = 256;
+constexpr int kAddTh = 256, kAddKeys = 4;
 template <int REP>
 __global__ void __launch_bounds__(kAddTh) attn_add_weights_kernel(const __grid_constant__ Params p) {
   const int g = blockIdx.y, b = blockIdx.z;
@@ -392,19 +394,30 @@ __global__ void __launch_bounds__(kAddTh) attn_add_weights_kernel(const __grid_c
   }
   const float* scores = p.scores + pair * p.score_stride;
   float* sums = p.sums + pair * p.cap;
-  for (int i = blockIdx.x * kAddTh + threadIdx.x; i < see.n; i += gridDim.x * kAddTh) {
-    float s[REP];
-    if constexpr (REP >= 4) {
+  // kAddKeys keys a thread at a time, all their loads under way
+#pragma unroll 1
+  for (int i0 = blockIdx.x * kAddTh * kAddKeys + threadIdx.x; i0 < see.n; i0 += gridDim.x * kAddTh * kAddKeys) {
+    float s[kAddKeys][REP], old[kAddKeys];
 #pragma unroll
-      for (int h = 0; h < REP; h += 4) *(float4*)(s + h) = __ldcs((const float4*)(scores + (long long)i * REP + h));
-    } else {
+    for (int k = 0; k < kAddKeys; ++k) {
+      const int i = min(i0 + k * kAddTh, see.n - 1);
+      if constexpr (REP >= 4) {
 #pragma unroll
-      for (int h = 0; h < REP; ++h) s[h] = __ldcs(scores + (long long)i * REP + h);
+        for (int h = 0; h < REP; h += 4) *(float4*)(s[k] + h) = __ldcs((const float4*)(scores + (long long)i * REP + h));
+      } else {
+#pragma unroll
+        for (int h = 0; h < REP; ++h) s[k][h] = __ldcs(scores + (long long)i * REP + h);
+      }
+      old[k] = sums[token_of(see, i)];
     }
-    float w = 0.f;
 #pragma unroll
-    for (int h = 0; h < REP; ++h) w = fmaf(ex2(s[h] - m[h]), inv[h], w);
-    sums[token_of(see, i)] += w;
+    for (int k = 0; k < kAddKeys; ++k) {
+      const int i = i0 + k * kAddTh;
+      float w = 0.f;
+#pragma unroll
+      for (int h = 0; h < REP; ++h) w = fmaf(ex2(s[k][h] - m[h]), inv[h], w);
+      if (i < see.n) sums[token_of(see, i)] = old[k] + w;
+    }
   }
 }
 
@@ -479,7 +492,7 @@ cudaError_t launch_attn_window(const AttnRowsArgs& a, const Launch& L) {
   cudaError_t e = a.q_f32 ? launch<float, 3, 3>(p, a.n_rows, first) : launch<__nv_bfloat16, 1, 2>(p, a.n_rows, first);
   if (e != cudaSuccess || !a.key_weights) return e;
   const long long pairs = (long long)a.n_rows * a.Hkv, fill = 8LL * dev_info().sm_count;
-  const dim3 grid((unsigned)std::max(1LL, std::min((attn_shown_keys(a) + kAddTh - 1) / kAddTh, (fill + pairs - 1) / pairs)),
+  const dim3 grid((unsigned)std::max(1LL, std::min((attn_shown_keys(a) + kAddTh * kAddKeys - 1) / (kAddTh * kAddKeys), (fill + pairs - 1) / pairs)),
                   a.Hkv, a.n_rows);
   Launch second = L;
   second.pdl = true;

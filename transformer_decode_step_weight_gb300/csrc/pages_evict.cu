@@ -29,7 +29,7 @@ constexpr int kBins = 2048;
 constexpr int kList = 1024;            // kept tokens found before they are moved
 // How a (layer, sequence, kv head) is worked: threads, rows moved at a time, places of the ring, CTAs an
 // SM. Few of them (one sequence of 28 layers, 8 kv heads) want the most under way in each, many (36
-// layers x 4 sequences) more CTAs, whose selections run beside other CTAs' moves: Few 51 and 361 us, Many 58 and 342.
+// layers x 4 sequences) more CTAs, whose selections run beside other CTAs' moves: Few 49 and 361 us, Many 58 and 341.
 struct Few {
   static constexpr int kTh = 512, kBatch = 64, kStages = 3, kCtas = 2;
 };
@@ -126,17 +126,17 @@ QD_DEV void find_bin(const int* hist, int want, int* warp_sums, int* s_out, int&
   __syncthreads();
 }
 
-template <typename How>
+template <typename How, int VECS>
 __global__ void __launch_bounds__(How::kTh, How::kCtas) pages_evict_kernel(const __grid_constant__ PagePtrs pk, PageState c, PagesWs ws,
                                                              const __grid_constant__ PageEvict e, const PageDiv div,
                                                              int layer0) {
   constexpr int kTh = How::kTh, kBatch = How::kBatch, kStages = How::kStages;
   extern __shared__ __align__(128) unsigned char ring[];   // [kStages][K and V][kBatch rows]
-  __shared__ int s_from[kList], warp_sums[kTh / 32], s_out[2];
+  __shared__ int s_from[kList], s_src[kList], s_dst[kList], warp_sums[kTh / 32], s_out[2];
   __shared__ float s_val[kList];
   __shared__ int s_hist[kBins];
   const int tid = threadIdx.x, g = blockIdx.x, l = blockIdx.z;
-  const int row = e.head_dim * 2, vecs = row / 16;         // bytes of a token's K, in 16-byte pieces
+  const int vecs = VECS ? VECS : e.head_dim / 8, row = vecs * 16;   // a token's K in 16-byte pieces, and in bytes
   unsigned char *kp = pk.p[2 * l], *vp = pk.p[2 * l + 1];
   const long long cap = (long long)c.max_pages * c.page_size;
   pdl_wait();
@@ -174,9 +174,9 @@ __global__ void __launch_bounds__(How::kTh, How::kCtas) pages_evict_kernel(const
     }
 
     // ---- kept tokens in order, up to kList at a time, and their moves
-    auto place = [&](int t) {   // of a token's row, in elements of 16 bytes
+    auto place = [&](int t) {   // the cache row of a token
       const PagedSlot sl = paged_slot(c.table + (long long)s * c.max_pages, t, c.page_size, div, c.n_pages);
-      return (((long long)sl.page * e.n_kv_heads + g) * c.page_size + sl.slot) * vecs;
+      return (sl.page * e.n_kv_heads + g) * c.page_size + sl.slot;
     };
     int next = a.first, kept = a.first, on_border = 0;   // the next token to look at; kept so far
 #pragma unroll 1
@@ -203,15 +203,22 @@ __global__ void __launch_bounds__(How::kTh, How::kCtas) pages_evict_kernel(const
         next += kTh;
       }
       __syncthreads();
-      // those at the list's start that stay where they are need no move
+      for (int i = tid; i < m; i += kTh) {   // (a row that stays where it is needs no move)
+        const bool moves = s_from[i] != kept + i;
+        s_src[i] = moves ? place(s_from[i]) : -1;
+        s_dst[i] = moves ? place(kept + i) : -1;
+        if (moves) w[kept + i] = s_val[i];
+      }
+      __syncthreads();
       const int batches = (m + kBatch - 1) / kBatch;
       auto load = [&](int b) {
         if (b < batches) {
           const uint32_t dst = smem_u32(ring) + (uint32_t)(b % kStages) * (2 * kBatch * row);
+#pragma unroll 4
           for (int i = tid; i < kBatch * vecs; i += kTh) {
             const int r = b * kBatch + i / vecs, v = i % vecs;
-            if (r < m && s_from[r] != kept + r) {
-              const long long o = (place(s_from[r]) + v) * 16;
+            if (r < m && s_src[r] >= 0) {
+              const long long o = ((long long)s_src[r] * vecs + v) * 16;
               asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i * 16), "l"(kp + o) : "memory");
               asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + kBatch * row + i * 16), "l"(vp + o)
                            : "memory");
@@ -222,18 +229,17 @@ __global__ void __launch_bounds__(How::kTh, How::kCtas) pages_evict_kernel(const
       };
 #pragma unroll
       for (int b = 0; b < kStages - 1; ++b) load(b);
-      for (int i = tid; i < m; i += kTh)
-        if (s_from[i] != kept + i) w[kept + i] = s_val[i];
 #pragma unroll 1
       for (int b = 0; b < batches; ++b) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
         __syncthreads();                 // batch b has landed whole, and the one before has been written
         load(b + kStages - 1);
         const unsigned char* src = ring + (size_t)(b % kStages) * (2 * kBatch * row);
+#pragma unroll 4
         for (int i = tid; i < kBatch * vecs; i += kTh) {
           const int r = b * kBatch + i / vecs, v = i % vecs;
-          if (r < m && s_from[r] != kept + r) {
-            const long long o = (place(kept + r) + v) * 16;
+          if (r < m && s_dst[r] >= 0) {
+            const long long o = ((long long)s_dst[r] * vecs + v) * 16;
             *(uint4*)(kp + o) = *(const uint4*)(src + i * 16);
             *(uint4*)(vp + o) = *(const uint4*)(src + kBatch * row + i * 16);
           }
@@ -248,10 +254,10 @@ __global__ void __launch_bounds__(How::kTh, How::kCtas) pages_evict_kernel(const
   }
 }
 
-template <typename How>
+template <typename How, int VECS>
 cudaError_t move(const PageState& c, const PageCopy& pc, const PageEvict& e, const PagesWs& ws, Launch L) {
   constexpr size_t kRowSmem = (size_t)How::kStages * 2 * How::kBatch * 2;
-  cudaError_t rc = allow_smem<pages_evict_kernel<How>>(kRowSmem * kMaxHeadDim);   // (asked for once)
+  cudaError_t rc = allow_smem<pages_evict_kernel<How, VECS>>(kRowSmem * kMaxHeadDim);   // (asked for once)
   for (int l0 = 0; rc == cudaSuccess && l0 < pc.n_layers; l0 += kPagePtrs / 2) {
     const int nl = std::min(kPagePtrs / 2, pc.n_layers - l0);
     PagePtrs pk = {};
@@ -259,7 +265,7 @@ cudaError_t move(const PageState& c, const PageCopy& pc, const PageEvict& e, con
       pk.p[2 * i] = (unsigned char*)pc.k_cache[l0 + i];
       pk.p[2 * i + 1] = (unsigned char*)pc.v_cache[l0 + i];
     }
-    rc = launch_ex(pages_evict_kernel<How>, dim3(e.n_kv_heads, std::min(c.max_seqs, 64), nl), dim3(How::kTh),
+    rc = launch_ex(pages_evict_kernel<How, VECS>, dim3(e.n_kv_heads, std::min(c.max_seqs, 64), nl), dim3(How::kTh),
                    kRowSmem * e.head_dim, L, pk, c, ws, e, make_page_div(c.page_size), l0);
     L.pdl = false;
   }
@@ -278,7 +284,10 @@ cudaError_t launch_pages_evict(const PageState& c, const PageCopy& pc, const Pag
                              e.n_recent, L.err);
   if (rc != cudaSuccess) return rc;
   const bool few = (long long)pc.n_layers * c.max_seqs * e.n_kv_heads <= 4LL * dev_info().sm_count;
-  rc = few ? move<Few>(c, pc, e, ws, moves) : move<Many>(c, pc, e, ws, moves);
+  if (e.head_dim == 128)   // (the model's own: no division by the row's length)
+    rc = few ? move<Few, 16>(c, pc, e, ws, moves) : move<Many, 16>(c, pc, e, ws, moves);
+  else
+    rc = few ? move<Few, 0>(c, pc, e, ws, moves) : move<Many, 0>(c, pc, e, ws, moves);
   if (rc != cudaSuccess) return rc;
   return launch_pages_trim(c, ws.src, last);
 }
