@@ -72,6 +72,7 @@ DECODE = [   # lengths, q heads, kv heads, page size, window, first tokens
     ([4000, 12, 900], 4, 4, 64, ALL, 7),
     ([70, 33], 4, 2, 16, 5, 1000),             # more first tokens than there are
     ([130] * 40, 32, 8, 16, 96, 4),
+    ([2500, 1300, 2049] * 6, 32, 8, 16, 2100, 0),      # many pairs, each in a few long splits
 ]
 
 
@@ -309,7 +310,8 @@ def _check_prompt(out, q, kp, vp, pt, lens, seqs, at, window, sinks, scale=SCALE
 
 
 def _pick(n, r):
-    return sorted(set(range(min(n, 20))) | set(range(max(0, n - 10), n)) | set(r.choice(n, min(60, n), replace=False).tolist()))
+    some = r.choice(n, min(60, n), replace=False).tolist()
+    return sorted(set(range(min(n, 20))) | set(range(max(0, n - 10), n)) | set(some))
 
 
 PROMPT = [   # rows, lengths, q heads, kv heads, page size, window, first tokens
@@ -532,6 +534,9 @@ WEIGHTS = [   # rows, lengths, q heads, kv heads, page size, last, window, first
     ([2, 0, 0, 1], [2, 0, 7, 257], 2, 2, 1, 0, 33, 2),
     ([500], [500], 2, 2, 16, 0, ALL, 0),
     ([260], [2500], 8, 1, 16, 40, 311, 213),
+    ([2201], [2201], 8, 2, 16, 0, ALL, 0),
+    ([32] * 9, [1800] * 9, 16, 4, 16, 32, ALL, 0),
+    ([700, 40], [700, 90], 16, 2, 16, 0, 300, 0),
 ]
 
 
@@ -634,6 +639,58 @@ def test_weights_refused_lengths_and_rows_outside(cuda_lib):
     pt[1, 1] = -1
     api.attn_key_weights(qkv[:, :8], kp, pt, _ints([4, 14, 64]), _ints(lens), SCALE, sums)
     assert api.check_device_error() == PAGE
+
+
+def test_numbers_past_32_bits_are_refused(cuda_lib):
+    g = _gen(19)
+    kp, vp, pt = ref.make_cache(g, [20], 2, 16)
+    q, cu, n = _q(g, 1, 8, torch.float32), _ints([0, 1]), _ints([20])
+    sums = torch.zeros((1, 2, 32), device=DEV)
+    for bad in (2 ** 32 + 5, -2 ** 31 - 7):
+        for kw in (dict(window=bad), dict(n_sinks=bad)):
+            with pytest.raises(ValueError, match=str(bad)):
+                api.attn_decode_window(q, kp, vp, pt, n, SCALE, **kw)
+            with pytest.raises(ValueError, match=str(bad)):
+                api.attn_prompt_window(q, kp, vp, pt, cu, n, SCALE, **kw)
+            with pytest.raises(ValueError, match=str(bad)):
+                api.attn_key_weights(q, kp, pt, cu, n, SCALE, sums, **kw)
+        with pytest.raises(ValueError, match=str(bad)):
+            api.attn_key_weights(q, kp, pt, cu, n, SCALE, sums, last=bad)
+    for call in (lambda: api.attn_decode_window(q, kp, vp, pt, n, SCALE, 0),
+                 lambda: api.attn_prompt_window(q, kp, vp, pt, cu, n, SCALE, 5, -1)):
+        with pytest.raises(api.QDError, match="window="):
+            call()
+
+
+def test_weights_share_a_workspace_over_sizes_and_graphs(cuda_lib):
+    # one workspace for calls of several sizes, captured and replayed in turn
+    g = _gen(20)
+    ws = torch.zeros(max(api.attn_key_weights_workspace_bytes(2, 900, 8, 2), api.attn_key_weights_workspace_bytes(1, 64, 16, 8)),
+                     dtype=torch.uint8, device=DEV)
+    runs = []
+    for rows, lens, hq, hkv, dtype, last in (([700, 200], [700, 900], 8, 2, torch.float32, 0), ([64], [1500], 16, 8, torch.bfloat16, 16)):
+        kp, vp, pt = ref.make_cache(g, lens, hkv, 16)
+        cu, _, _ = _pack(rows, lens)
+        q, cu_d, n = _q(g, cu[-1], hq, dtype), _ints(cu), _ints(lens)
+        sums = torch.zeros((len(rows), hkv, pt.shape[1] * 16), device=DEV)
+
+        def call(q=q, kp=kp, pt=pt, cu_d=cu_d, n=n, sums=sums, last=last):
+            api.attn_key_weights(q, kp, pt, cu_d, n, SCALE, sums, last=last, workspace=ws)
+
+        call()
+        torch.cuda.synchronize()
+        want = sums.clone()
+        _check_weights(want, torch.zeros_like(want), q, kp, pt, rows, lens, cu, last, ALL, 0)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        runs.append((graph, sums, want, call))     # (which holds the inputs)
+    for _ in range(4):
+        for graph, sums, want, _ in runs:
+            sums.zero_()
+            graph.replay()
+            assert torch.equal(sums, want)
+    assert bool((ws[:16384] == 0).all()) and api.check_device_error() == 0
 
 
 def test_weights_in_a_graph_with_other_lengths(cuda_lib):

@@ -471,6 +471,13 @@ ALL_KEYS = 2 ** 31 - 1
 _WINDOW_HEAD = 16384
 
 
+def _counts(fn, **values):
+    """Refuses numbers that a 32-bit argument would not hold as they are."""
+    for name, n in values.items():
+        if not -ALL_KEYS <= n <= ALL_KEYS:
+            raise ValueError(f"{fn}: {name}={n}")
+
+
 def attn_prompt_window(q, k_pages, v_pages, page_table, cu_rows, seq_lens, scale, window=None, n_sinks=0, out=None,
                        workspace=None, stream=None):
     """attn_prompt in which each row sees its last `window` tokens (itself among them; None: all) and the first
@@ -487,6 +494,8 @@ def attn_prompt_window(q, k_pages, v_pages, page_table, cu_rows, seq_lens, scale
     n_pages, Hkv, ps, _ = k_pages.shape
     if cu_rows.shape[0] != B + 1:
         raise ValueError(f"{fn}: {cu_rows.numel()} segment starts for {B} sequences")
+    window = ALL_KEYS if window is None else window
+    _counts(fn, window=window, n_sinks=n_sinks)
     if out is None:
         out = torch.empty((n, Hq, D), dtype=q.dtype, device=q.device)
     if n == 0:
@@ -495,7 +504,7 @@ def attn_prompt_window(q, k_pages, v_pages, page_table, cu_rows, seq_lens, scale
     _check(lib().qd_attn_prompt_window(q.data_ptr(), q.dtype is torch.float32, q_stride, k_pages.data_ptr(),
                                        v_pages.data_ptr(), page_table.data_ptr(), cu_rows.data_ptr(),
                                        seq_lens.data_ptr(), B, n, Hq, Hkv, D, ps, max_pages, n_pages, scale,
-                                       ALL_KEYS if window is None else window, n_sinks, out.data_ptr(),
+                                       window, n_sinks, out.data_ptr(),
                                        workspace.data_ptr(), workspace.numel(), _raw_stream(q.get_device())))
     return out
 
@@ -524,6 +533,7 @@ def attn_decode_window(q, k_pages, v_pages, page_table, seq_lens, scale, window=
     if page_table.shape[0] != B:
         raise ValueError(f"{fn}: {page_table.shape[0]} page tables for {B} rows")
     window = ALL_KEYS if window is None else window
+    _counts(fn, window=window, n_sinks=n_sinks)
     keys = 0
     if key_weights is not None:
         _want("key_weights", key_weights, torch.float32, 3, dev, (B, Hkv, max_pages * ps))
@@ -563,12 +573,14 @@ def attn_key_weights(q, k_pages, page_table, cu_rows, seq_lens, scale, key_weigh
     if cu_rows.shape[0] != B + 1:
         raise ValueError(f"{fn}: {cu_rows.numel()} segment starts for {B} sequences")
     _want("key_weights", key_weights, torch.float32, 3, dev, (B, Hkv, max_pages * ps))
+    window = ALL_KEYS if window is None else window
+    _counts(fn, window=window, n_sinks=n_sinks, last=last)
     if n == 0:
         return key_weights
     workspace = _scratch(workspace, lambda: attn_key_weights_workspace_bytes(B, n, Hq, Hkv, last), q, _WINDOW_HEAD)
     _check(lib().qd_attn_key_weights(q.data_ptr(), q.dtype is torch.float32, q_stride, k_pages.data_ptr(),
                                      page_table.data_ptr(), cu_rows.data_ptr(), seq_lens.data_ptr(), B, n, Hq, Hkv, D,
-                                     ps, max_pages, n_pages, scale, last, ALL_KEYS if window is None else window, n_sinks,
+                                     ps, max_pages, n_pages, scale, last, window, n_sinks,
                                      key_weights.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(dev)))
     return key_weights
 
@@ -729,6 +741,7 @@ class PageCache:
         a = self.args
         _want("key_weights", key_weights, torch.float32, 4, self._dev,
               (a.n_layers, a.max_seqs, a.n_kv_heads, a.max_pages * a.page_size))
+        _counts("evict", n_sinks=n_sinks, n_recent=n_recent)
         self._run(stream, lib().qd_pages_evict, key_weights.data_ptr(), self._list("keep", keep, a.max_seqs), n_sinks,
                   n_recent)
 
