@@ -156,7 +156,7 @@ def test_evict_head_sizes_and_many_layers(cuda_lib, d, layers):
     assert api.check_device_error() == 0
 
 
-@pytest.mark.parametrize("n", [500, 1300])     # (both ways of working a row)
+@pytest.mark.parametrize("n", [500, 1300])
 def test_evict_many_sequences(cuda_lib, n):
     r = np.random.default_rng(5)
     lens = [int(x) for x in r.integers(0, 60, n)]

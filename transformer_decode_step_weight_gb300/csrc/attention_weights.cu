@@ -10,9 +10,10 @@
 //   kSums    a lane is a key, a tile of K stays, the row tiles are walked, so a key's sum stays in a thread
 //   kSumsOne the same sums where no sequence has more than one row tile (the last few rows of a
 //            prompt): the row tile stays and the keys are walked, each tile's sums added at once
-// Where there are few tiles, several CTAs share a tile's walk and the last of them joins their parts in
-// order (ticket). So nothing is added in an order that could change. Row tiles are written out by the first launch as
-// they lie in shared memory (an f32 q in three bf16 parts, 24 bits), and the second copies them.
+// Where there are few tiles, several CTAs share a tile's walk (with one row tile a sequence each CTA takes an
+// equal run of the (sequence, kv head, key tile) units) and the last of them joins their parts in order
+// (ticket). So nothing is added in an order that could change. Row tiles are written out by the first
+// launch as they lie in shared memory (an f32 q in three bf16 parts, 24 bits), and the second copies them.
 //
 // Sixteen warps read S, a quarter of a tile's columns each, while one warp issues the products into the other of
 // two S buffers and one brings tiles; they meet at mbarriers only. With a CTA barrier per tile, the
@@ -58,8 +59,10 @@ struct Params {
   long long cap, window, sinks;
   float scale_log2, q_sign;   // (the scale positive, its sign with q)
   int box;                 // rows per TMA box; 0: 16-byte copies
+  int one;                 // no sequence has more than one row tile
   int* tickets;            // [kMaxParts], zero between launches
-  long long* base;         // [2][kMaxSeg + 1], 1: row tiles and key tiles before each segment (of one kv head); sequences with rows
+  long long* base;         // [2][kMaxSeg + 1], 1: before each segment, of one kv head: row tiles, and key tiles (`one`: those that
+                           // its row tile sees); sequences with rows
   float2* parts;           // [kMaxParts][128]: of shared walks
   float* stats;            // [row tiles][2][128]: negated largest scores in log2 units, 1 / sums
   unsigned char* image;    // [row tiles][parts of q][kSlot]
@@ -169,6 +172,22 @@ QD_DEV Seg segment(const Params& p, int s) {
 }
 QD_DEV int row_tiles(const Params& p, const Seg& a) { return (a.n + (kTile >> p.log_rep) - 1) >> (7 - p.log_rep); }
 
+// The key tiles that row tile ft of a segment sees: the first tokens', then from jump tiles further on. Keys seen
+// by some row lie below hi, and below sinks or from lo on.
+struct Walk {
+  int lo, hi, jump_at, jump, n;
+};
+QD_DEV Walk key_walk(const Params& p, const Seg& a, int ft) {
+  const int tpt = kTile >> p.log_rep, j0 = ft * tpt, j1 = min(j0 + tpt, a.n) - 1;
+  Walk w;
+  w.hi = max(0, a.off + j1 + 1);
+  w.lo = (int)max(0LL, a.off + j0 + 1 - p.window);
+  w.jump_at = (int)((p.sinks + kTile - 1) >> 7);
+  w.jump = max(0, (w.lo >> 7) - w.jump_at);
+  w.n = ((w.hi + kTile - 1) >> 7) - w.jump;
+  return w;
+}
+
 // CTAs that share each walk of `walk` tiles on average: those that give G CTAs the shortest run, when an
 // item costs some 3 tiles beside its walk and, over several turns, long and short walks come to three
 // quarters of the longest; `most` items times shares at most. By a whole warp, a count a lane.
@@ -203,11 +222,13 @@ struct Ring {
 
 // An item: the tile that stays and the walk.
 struct Item {
-  int s, g, ft, n;         // n: tiles that this CTA walks; 0: none
+  int s, g, ft, n, i0;     // n: tiles that this CTA walks, from the walk's i0 on in steps of the shares; 0: none
   bool none;               // nobody walks any
   Seg a;
   long long first_rt;      // the first row tile of the segment and head
-  int w0, jump_at, jump;   // tile i of the walk: w0 + rank + i shares, + jump from jump_at on
+  int w0, jump_at, jump;   // tile i of the walk: w0 + i, + jump from jump_at on
+  long long unit0;         // `one`: the unit that the walk begins with, and all its tiles
+  int walk;
   int key_lo, key_hi;      // keys that some row sees: below sinks or from key_lo on, below key_hi
   const int32_t* pt;
 };
@@ -250,6 +271,7 @@ __global__ void __launch_bounds__(kTh, 1) attn_weights_kernel(const __grid_const
   }
   // ---- tiles before each segment: every CTA of the first launch for itself; they wait in the workspace for the second
   if (PASS == kStats) {
+    auto key_tiles = [&](const Seg& a) { return a.n <= 0 ? 0 : p.one ? max(0, key_walk(p, a, 0).n) : (a.len + kTile - 1) >> 7; };
     const int per = (p.n_seg + kTh - 1) / kTh;
     long long rows = 0, keys = 0;
     int some = 0;
@@ -265,7 +287,7 @@ __global__ void __launch_bounds__(kTh, 1) attn_weights_kernel(const __grid_const
       if (hi > lo && (len < 0 || len > p.cap) && blockIdx.x == 0) set_error(p.err, QD_DEVERR_POS);
       const Seg a = segment(p, s);
       rows += row_tiles(p, a);
-      keys += a.n > 0 ? (a.len + kTile - 1) >> 7 : 0;
+      keys += key_tiles(a);
       some += a.n > 0;
     }
     const int any_bad = __syncthreads_or(bad);
@@ -313,7 +335,7 @@ __global__ void __launch_bounds__(kTh, 1) attn_weights_kernel(const __grid_const
         p.base[kMaxSeg + 1 + s] = k0;
         const Seg a = segment(p, s);
         r0 += row_tiles(p, a);
-        k0 += a.n > 0 ? (a.len + kTile - 1) >> 7 : 0;
+        k0 += key_tiles(a);
       }
   }
   if (tid == 0) {
@@ -342,15 +364,26 @@ __global__ void __launch_bounds__(kTh, 1) attn_weights_kernel(const __grid_const
   }
 
   // ---- the items, and this CTA's: in turn, there and back, the long ones (late rows, early keys) of a segment first
-  const long long* base = p.base + (kRows ? kMaxSeg + 1 : 0);
+  const bool one = !kRows && p.one;
+  const long long* base = p.base + (kRows || one ? kMaxSeg + 1 : 0);
   const long long all_rows = p.base[p.n_seg], all_keys = p.base[kMaxSeg + 1 + p.n_seg];
   const long long segs = max(1LL, p.base[2 * (kMaxSeg + 1)]);
-  const long long items = (kRows ? all_keys : all_rows) * p.Hkv;
-  const int shares = items == 0 ? 1 : shares_for(items, max(1LL, (kRows ? all_rows : all_keys) / segs), gridDim.x,
-                                                 PASS == kSumsOne ? INT64_MAX / kMaxShares : kMaxParts, lane);
+  const long long items = (kRows || one ? all_keys : all_rows) * p.Hkv;   // `one`: units
+  const int shares = items == 0 || one ? 1
+                                       : shares_for(items, max(1LL, (kRows ? all_rows : all_keys) / segs), gridDim.x,
+                                                    kMaxParts, lane);
   const int rank = blockIdx.x % shares, group = blockIdx.x / shares, groups = gridDim.x / shares;
+  // `one`: CTA c takes per + (c < rem) units
+  const long long runs = min((long long)gridDim.x, items), per = runs ? items / runs : 0, rem = runs ? items % runs : 0;
+  auto first_of = [&](long long c) { return c * per + min(c, rem); };
+  auto owner = [&](long long u) { return u < rem * (per + 1) ? u / (per + 1) : rem + (u - rem * (per + 1)) / per; };
+  const long long end = blockIdx.x < runs ? first_of(blockIdx.x + 1) : 0;
   const int tpt = kTile >> p.log_rep;   // tokens of a row tile
-  auto next_item = [&](long long& round, long long& item) {
+  auto next_item = [&](long long& round, long long& item) {   // (`one`: round counts units)
+    if (one) {
+      item = round;
+      return round < end;
+    }
     for (; group < groups && round * groups < items; ++round) {
       item = round * groups + (round & 1 ? groups - 1 - group : group);
       if (item < items) {
@@ -360,7 +393,7 @@ __global__ void __launch_bounds__(kTh, 1) attn_weights_kernel(const __grid_const
     }
     return false;
   };
-  auto look_up = [&](long long item) {
+  auto look_up = [&](long long& round, long long item) {
     Item x;
     x.s = 0;   // the last segment whose tiles start at or before it
     const long long tile0 = item / p.Hkv;
@@ -372,21 +405,23 @@ __global__ void __launch_bounds__(kTh, 1) attn_weights_kernel(const __grid_const
     const Seg& a = x.a;
     const long long in = item - base[x.s] * p.Hkv;
     const int tiles = row_tiles(p, a);
-    x.g = (int)(in % p.Hkv);
-    x.ft = kRows ? (int)(in / p.Hkv) : tiles - 1 - (int)(in / p.Hkv);
     x.pt = p.page_table + (size_t)x.s * p.max_pages;
-    x.first_rt = p.base[x.s] * p.Hkv + (long long)x.g * tiles;
-    x.w0 = x.jump = 0;
+    x.w0 = x.jump = x.ft = 0;
     x.jump_at = INT32_MAX;
-    int w1;
-    if (!kRows) {   // key tiles: first ones, then a window
-      const int j0 = x.ft * tpt, j1 = min(j0 + tpt, a.n) - 1;
-      x.key_hi = max(0, a.off + j1 + 1);
-      x.key_lo = (int)max(0LL, a.off + j0 + 1 - p.window);
-      x.jump_at = (int)((p.sinks + kTile - 1) >> 7);
-      x.jump = max(0, (x.key_lo >> 7) - x.jump_at);
-      w1 = ((x.key_hi + kTile - 1) >> 7) - x.jump;
+    if (!kRows) {
+      if (!one) {
+        x.g = (int)(in % p.Hkv);
+        x.ft = tiles - 1 - (int)(in / p.Hkv);
+      }
+      const Walk w = key_walk(p, a, x.ft);
+      x.key_lo = w.lo;
+      x.key_hi = w.hi;
+      x.jump_at = w.jump_at;
+      x.jump = w.jump;
+      x.walk = w.n;
     } else {
+      x.g = (int)(in % p.Hkv);
+      x.ft = (int)(in / p.Hkv);
       const int key0 = x.ft * kTile;
       x.key_hi = a.len;
       x.key_lo = (int)max(0LL, a.off + 1 - p.window);
@@ -394,15 +429,24 @@ __global__ void __launch_bounds__(kTh, 1) attn_weights_kernel(const __grid_const
       long long j1 = a.n - 1;                    // the last
       if (key0 >= p.sinks) j1 = min(j1, key0 + kTile - 1 + p.window - 1 - a.off);
       x.w0 = j0 >> (7 - p.log_rep);
-      w1 = j1 < j0 ? x.w0 : (int)(j1 >> (7 - p.log_rep)) + 1;
+      x.walk = j1 < j0 ? 0 : (int)(j1 >> (7 - p.log_rep)) + 1 - x.w0;
     }
-    const int all = w1 - x.w0;
-    x.none = all <= 0;
-    x.n = all > rank ? (all - rank + shares - 1) / shares : 0;
+    x.none = x.walk <= 0;
+    x.i0 = rank;
+    x.n = x.walk > rank ? (x.walk - rank + shares - 1) / shares : 0;
+    x.unit0 = item;
+    if (one) {   // (a walk of no tiles has no units)
+      x.g = (int)(in / x.walk);
+      x.i0 = (int)(in - (long long)x.g * x.walk);
+      x.n = (int)min((long long)(x.walk - x.i0), end - item);
+      x.unit0 = item - x.i0;
+      round += x.n;
+    }
+    x.first_rt = p.base[x.s] * p.Hkv + (long long)x.g * tiles;
     return x;
   };
   auto tile_at = [&](const Item& x, int i) {
-    const int t = x.w0 + rank + i * shares;
+    const int t = x.w0 + x.i0 + i * shares;
     return t >= x.jump_at ? t + x.jump : t;
   };
   // a wait of a whole warp, bounded by its polls (each returns after 2 us where nothing comes); after a timeout
@@ -415,7 +459,7 @@ __global__ void __launch_bounds__(kTh, 1) attn_weights_kernel(const __grid_const
         break;
       }
   };
-  long long round = 0, item;
+  long long round = one ? first_of(blockIdx.x) : 0, item;
   Ring rt = {0, 0}, rb = {0, 0}, rf = {0, 0};   // tiles, buffers of S, items
 
   if (warp == kIssue + 1) {
@@ -499,7 +543,7 @@ __global__ void __launch_bounds__(kTh, 1) attn_weights_kernel(const __grid_const
       __syncwarp();
     };
     while (next_item(round, item)) {
-      const Item x = look_up(item);
+      const Item x = look_up(round, item);
       if (x.n == 0) continue;
       if (PASS != kStats) {
         Look k;
@@ -551,7 +595,7 @@ __global__ void __launch_bounds__(kTh, 1) attn_weights_kernel(const __grid_const
     const bool lead = lane == 0;
     const uint32_t fix = smem_u32(fixed), mov = smem_u32(moving);
     while (next_item(round, item)) {
-      const Item x = look_up(item);
+      const Item x = look_up(round, item);
       if (x.n == 0) continue;
       wait(fix_full, rf.ph);
       rf.step(1);
@@ -596,17 +640,17 @@ __global__ void __launch_bounds__(kTh, 1) attn_weights_kernel(const __grid_const
       if (lane == 0) mbar_arrive(bar);
     };
     // Whether this CTA is the last of the item's shares; its part is in p.parts. By the first quarter's 4 warps
-    auto last_share = [&](long long it) {
+    auto last_share = [&](long long it, int of) {
       bar_sync(5, kTile);
       if (tid == 0) {
-        *s_last = !*(volatile int*)s_abort && atom_add_acq_rel_gpu(p.tickets + it, 1) == shares - 1;
+        *s_last = !*(volatile int*)s_abort && atom_add_acq_rel_gpu(p.tickets + it, 1) == of - 1;
         if (*s_last) p.tickets[it] = 0;
       }
       bar_sync(5, kTile);
       return *(volatile int*)s_last != 0;
     };
     while (next_item(round, item)) {
-      const Item x = look_up(item);
+      const Item x = look_up(round, item);
       if (PASS != kStats && x.none) continue;
       const Seg& a = x.a;
       if (PASS == kStats && x.n > 0) {
@@ -638,7 +682,7 @@ __global__ void __launch_bounds__(kTh, 1) attn_weights_kernel(const __grid_const
           for (int part = 0; part < PARTS; ++part) {
             const uint2 b = make_uint2(pack(e[0], e[1]), pack(e[2], e[3]));
             *(uint2*)(fixed + part * kSlot + o) = b;
-            if (rank == 0) *(uint2*)(out + part * kSlot + o) = b;
+            if (x.i0 == 0) *(uint2*)(out + part * kSlot + o) = b;
             e[0] -= bf_lo(b.x); e[1] -= bf_hi(b.x); e[2] -= bf_lo(b.y); e[3] -= bf_hi(b.y);
           }
         }
@@ -773,10 +817,25 @@ __global__ void __launch_bounds__(kTh, 1) attn_weights_kernel(const __grid_const
 #pragma unroll
           for (int k = 0; k < 3; ++k) join(r[k * kTile], r[(k + 3) * kTile]);
           bool out = true;
-          if (shares > 1) {
+          if (one) {   // parts [CTA][2], the second where a walk begins
+            const long long c0 = owner(x.unit0), c1 = owner(x.unit0 + x.walk - 1);
+            if (c0 != c1) {
+              p.parts[(blockIdx.x * 2LL + (x.i0 == 0)) * kTile + line] = make_float2(m, l);
+              out = last_share(c0, (int)(c1 - c0) + 1);
+              if (out) {
+                const float2 first = __ldcg(p.parts + (c0 * 2 + 1) * kTile + line);
+                m = first.x;
+                l = first.y;
+                for (long long k = c0 + 1; k <= c1; ++k) {
+                  const float2 o = __ldcg(p.parts + k * 2 * kTile + line);
+                  join(o.x, o.y);
+                }
+              }
+            }
+          } else if (shares > 1) {
             float2* part = p.parts + item * shares * kTile + line;
             part[rank * kTile] = make_float2(m, l);
-            out = last_share(item);
+            out = last_share(item, shares);
             if (out) {
               const float2 first = __ldcg(part);
               m = first.x;
@@ -806,7 +865,7 @@ __global__ void __launch_bounds__(kTh, 1) attn_weights_kernel(const __grid_const
           if (shares > 1) {
             float* part = (float*)p.parts + item * shares * kTile + line;
             part[rank * kTile] = l;
-            out = last_share(item);
+            out = last_share(item, shares);
             if (out) {
               l = __ldcg(part);
               for (int k = 1; k < shares; ++k) l += __ldcg(part + k * kTile);
@@ -870,7 +929,7 @@ cudaError_t launch_attn_key_weights(const AttnRowsArgs& a, int last, const Launc
   p.sums = a.key_weights;
   p.div = make_page_div(a.page_size);
   p.err = L.err;
-  const bool one = (last > 0 && (long long)last * p.rep <= kTile) || (long long)a.n_rows * p.rep <= kTile;
+  p.one = (last > 0 && (long long)last * p.rep <= kTile) || (long long)a.n_rows * p.rep <= kTile;
   // boxes of whole 16-row pieces of a page; other page sizes by 16-byte asynchronous copies
   alignas(64) CUtensorMap tm;
   memset(&tm, 0, sizeof(tm));
@@ -885,7 +944,7 @@ cudaError_t launch_attn_key_weights(const AttnRowsArgs& a, int last, const Launc
   second.pdl = true;
   cudaError_t e = a.q_f32 ? launch<float, 3, kStats>(tm, p, first) : launch<__nv_bfloat16, 1, kStats>(tm, p, first);
   if (e != cudaSuccess) return e;
-  if (one) return a.q_f32 ? launch<float, 3, kSumsOne>(tm, p, second) : launch<__nv_bfloat16, 1, kSumsOne>(tm, p, second);
+  if (p.one) return a.q_f32 ? launch<float, 3, kSumsOne>(tm, p, second) : launch<__nv_bfloat16, 1, kSumsOne>(tm, p, second);
   return a.q_f32 ? launch<float, 3, kSums>(tm, p, second) : launch<__nv_bfloat16, 1, kSums>(tm, p, second);
 }
 

@@ -9,8 +9,8 @@
 //
 // Selection: the border between kept and not by radix over the weights as ordered integers (11, 11
 // and 10 bits, a shared-memory histogram each; the row, some 10 KB, comes from L2), then one pass
-// in token order in which equal weights count from the left. Moving is bound by HBM (5.2 TB/s read and written):
-// 32 or 64 rows of K and V at a time through a ring of asynchronous copies. A kept token's new place r is
+// in token order in which equal weights count from the left. Moving is bound by HBM (6.0 TB/s read and written):
+// 64 rows of K and V at a time through a ring of asynchronous copies. A kept token's new place r is
 // below those of all later ones, and they lie at r + 1 or behind it, so a batch may be written while
 // the loads of later ones are under way; it only has to have landed whole itself.
 #include "common.cuh"
@@ -27,15 +27,9 @@ namespace {
 constexpr int kPlan = 1024;
 constexpr int kBins = 2048;
 constexpr int kList = 1024;            // kept tokens found before they are moved
-// How a (layer, sequence, kv head) is worked: threads, rows moved at a time, places of the ring, CTAs an
-// SM. Few of them (one sequence of 28 layers, 8 kv heads) want the most under way in each, many (36
-// layers x 4 sequences) more CTAs, whose selections run beside other CTAs' moves: Few 49 and 361 us, Many 58 and 341.
-struct Few {
-  static constexpr int kTh = 512, kBatch = 64, kStages = 3, kCtas = 2;
-};
-struct Many {
-  static constexpr int kTh = 256, kBatch = 32, kStages = 2, kCtas = 4;
-};
+// Threads of a (layer, sequence, kv head), rows moved at a time, places of the ring: two CTAs an SM. One
+// sequence of 28 layers 37 us, four of 36 layers 296; 256 threads with 32 rows, two places and four CTAs 46 and 307.
+constexpr int kTh = 512, kBatch = 64, kStages = 3;
 constexpr int kMaxHeadDim = 256;
 
 // The tokens that stay, of n, without asking the weights: the first and the last.
@@ -105,7 +99,6 @@ QD_DEV uint32_t order_of(float w) {
 
 // Adds the bins from the top: the bin in which the `want`-th value from above lies, and how many lie
 // above that bin (the whole CTA; 1 <= want <= all).
-template <int kTh>
 QD_DEV void find_bin(const int* hist, int want, int* warp_sums, int* s_out, int& bin, int& above) {
   constexpr int kPer = kBins / kTh;
   const int top = kBins - 1 - threadIdx.x * kPer;
@@ -126,15 +119,15 @@ QD_DEV void find_bin(const int* hist, int want, int* warp_sums, int* s_out, int&
   __syncthreads();
 }
 
-template <typename How, int VECS>
-__global__ void __launch_bounds__(How::kTh, How::kCtas) pages_evict_kernel(const __grid_constant__ PagePtrs pk, PageState c, PagesWs ws,
+template <int VECS>
+__global__ void __launch_bounds__(kTh, 2) pages_evict_kernel(const __grid_constant__ PagePtrs pk, PageState c, PagesWs ws,
                                                              const __grid_constant__ PageEvict e, const PageDiv div,
                                                              int layer0) {
-  constexpr int kTh = How::kTh, kBatch = How::kBatch, kStages = How::kStages;
   extern __shared__ __align__(128) unsigned char ring[];   // [kStages][K and V][kBatch rows]
-  __shared__ int s_from[kList], s_src[kList], s_dst[kList], warp_sums[kTh / 32], s_out[2];
-  __shared__ float s_val[kList];
-  __shared__ int s_hist[kBins];
+  // (the bins are done with when the list begins)
+  __shared__ int s_mem[3 * kList > kBins ? 3 * kList : kBins], warp_sums[kTh / 32], s_out[2];
+  int *s_hist = s_mem, *s_src = s_mem, *s_dst = s_mem + kList;   // cache rows from and to; -1: it stays where it is
+  float* s_val = (float*)(s_mem + 2 * kList);
   const int tid = threadIdx.x, g = blockIdx.x, l = blockIdx.z;
   const int vecs = VECS ? VECS : e.head_dim / 8, row = vecs * 16;   // a token's K in 16-byte pieces, and in bytes
   unsigned char *kp = pk.p[2 * l], *vp = pk.p[2 * l + 1];
@@ -165,7 +158,7 @@ __global__ void __launch_bounds__(How::kTh, How::kCtas) pages_evict_kernel(const
         }
         __syncthreads();
         int bin, above;
-        find_bin<kTh>(s_hist, left, warp_sums, s_out, bin, above);
+        find_bin(s_hist, left, warp_sums, s_out, bin, above);
         prefix = prefix << bits | (uint32_t)bin;
         left -= above;
       }
@@ -196,20 +189,18 @@ __global__ void __launch_bounds__(How::kTh, How::kCtas) pages_evict_kernel(const
         on_border += total;
         const int at = block_scan(stays ? 1 : 0, warp_sums, total);
         if (stays) {
-          s_from[m + at - 1] = t;
-          s_val[m + at - 1] = v;
+          const int i = m + at - 1;
+          const bool moves = t != kept + i;
+          s_src[i] = moves ? place(t) : -1;
+          s_dst[i] = moves ? place(kept + i) : -1;
+          s_val[i] = v;
         }
         m += total;
         next += kTh;
       }
       __syncthreads();
-      for (int i = tid; i < m; i += kTh) {   // (a row that stays where it is needs no move)
-        const bool moves = s_from[i] != kept + i;
-        s_src[i] = moves ? place(s_from[i]) : -1;
-        s_dst[i] = moves ? place(kept + i) : -1;
-        if (moves) w[kept + i] = s_val[i];
-      }
-      __syncthreads();
+      for (int i = tid; i < m; i += kTh)
+        if (s_dst[i] >= 0) w[kept + i] = s_val[i];
       const int batches = (m + kBatch - 1) / kBatch;
       auto load = [&](int b) {
         if (b < batches) {
@@ -254,10 +245,10 @@ __global__ void __launch_bounds__(How::kTh, How::kCtas) pages_evict_kernel(const
   }
 }
 
-template <typename How, int VECS>
+template <int VECS>
 cudaError_t move(const PageState& c, const PageCopy& pc, const PageEvict& e, const PagesWs& ws, Launch L) {
-  constexpr size_t kRowSmem = (size_t)How::kStages * 2 * How::kBatch * 2;
-  cudaError_t rc = allow_smem<pages_evict_kernel<How, VECS>>(kRowSmem * kMaxHeadDim);   // (asked for once)
+  constexpr size_t kRowSmem = (size_t)kStages * 2 * kBatch * 2;
+  cudaError_t rc = allow_smem<pages_evict_kernel<VECS>>(kRowSmem * kMaxHeadDim);   // (asked for once)
   for (int l0 = 0; rc == cudaSuccess && l0 < pc.n_layers; l0 += kPagePtrs / 2) {
     const int nl = std::min(kPagePtrs / 2, pc.n_layers - l0);
     PagePtrs pk = {};
@@ -265,7 +256,7 @@ cudaError_t move(const PageState& c, const PageCopy& pc, const PageEvict& e, con
       pk.p[2 * i] = (unsigned char*)pc.k_cache[l0 + i];
       pk.p[2 * i + 1] = (unsigned char*)pc.v_cache[l0 + i];
     }
-    rc = launch_ex(pages_evict_kernel<How, VECS>, dim3(e.n_kv_heads, std::min(c.max_seqs, 64), nl), dim3(How::kTh),
+    rc = launch_ex(pages_evict_kernel<VECS>, dim3(e.n_kv_heads, std::min(c.max_seqs, 64), nl), dim3(kTh),
                    kRowSmem * e.head_dim, L, pk, c, ws, e, make_page_div(c.page_size), l0);
     L.pdl = false;
   }
@@ -283,11 +274,8 @@ cudaError_t launch_pages_evict(const PageState& c, const PageCopy& pc, const Pag
   cudaError_t rc = launch_ex(pages_evict_plan_kernel, dim3(1), dim3(kPlan), 0, first, c, ws, e.keep, e.n_sinks,
                              e.n_recent, L.err);
   if (rc != cudaSuccess) return rc;
-  const bool few = (long long)pc.n_layers * c.max_seqs * e.n_kv_heads <= 4LL * dev_info().sm_count;
-  if (e.head_dim == 128)   // (the model's own: no division by the row's length)
-    rc = few ? move<Few, 16>(c, pc, e, ws, moves) : move<Many, 16>(c, pc, e, ws, moves);
-  else
-    rc = few ? move<Few, 0>(c, pc, e, ws, moves) : move<Many, 0>(c, pc, e, ws, moves);
+  // (the model's own head size: no division by the row's length)
+  rc = e.head_dim == 128 ? move<16>(c, pc, e, ws, moves) : move<0>(c, pc, e, ws, moves);
   if (rc != cudaSuccess) return rc;
   return launch_pages_trim(c, ws.src, last);
 }
