@@ -308,7 +308,8 @@ __global__ void __launch_bounds__(kTh, 1) attn_weights_kernel(const __grid_const
     }
     __syncthreads();
     long long all_rows = 0, all_keys = 0, r0 = r - rows, k0 = k - keys, segs = 0;
-    for (int w = 0; w < kTh / 32; ++w) {
+    const int with = min(kTh / 32, (p.n_seg + 31) / 32);   // warps that have segments (the others' sums are 0)
+    for (int w = 0; w < with; ++w) {
       if (w < warp) {
         r0 += s_scan[w];
         k0 += s_scan[kTh / 32 + w];
@@ -395,11 +396,14 @@ __global__ void __launch_bounds__(kTh, 1) attn_weights_kernel(const __grid_const
   };
   auto look_up = [&](long long& round, long long item) {
     Item x;
-    x.s = 0;   // the last segment whose tiles start at or before it
+    // the last segment whose tiles start at or before it, in one or two looks of the warp
     const long long tile0 = item / p.Hkv;
-    for (int hi = p.n_seg; hi - x.s > 1;) {
-      const int mid = (x.s + hi) >> 1;
-      if (base[mid] <= tile0) x.s = mid; else hi = mid;
+    const int step = (p.n_seg + 31) >> 5;
+    const int some = __popc(__ballot_sync(0xffffffffu, lane * step < p.n_seg && base[min(lane * step, p.n_seg - 1)] <= tile0));
+    x.s = max(0, some - 1) * step;
+    if (step > 1) {
+      const int more = __popc(__ballot_sync(0xffffffffu, lane < step && x.s + lane < p.n_seg && base[min(x.s + lane, p.n_seg - 1)] <= tile0));
+      x.s += max(0, more - 1);
     }
     x.a = segment(p, x.s);
     const Seg& a = x.a;
@@ -674,20 +678,24 @@ __global__ void __launch_bounds__(kTh, 1) attn_weights_kernel(const __grid_const
             }
           }
         }
+        auto split = [&](auto put) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t o = (uint32_t)((lane >> 4) * kChunk + (lane & 1) * 8) + tc::sw128_off(warp * 8 + i, (lane & 15) >> 1);
-          float e[4] = {f[i].x * p.q_sign, f[i].y * p.q_sign, f[i].z * p.q_sign, f[i].w * p.q_sign};
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t o = (uint32_t)((lane >> 4) * kChunk + (lane & 1) * 8) + tc::sw128_off(warp * 8 + i, (lane & 15) >> 1);
+            float e[4] = {f[i].x * p.q_sign, f[i].y * p.q_sign, f[i].z * p.q_sign, f[i].w * p.q_sign};
 #pragma unroll
-          for (int part = 0; part < PARTS; ++part) {
-            const uint2 b = make_uint2(pack(e[0], e[1]), pack(e[2], e[3]));
-            *(uint2*)(fixed + part * kSlot + o) = b;
-            if (x.i0 == 0) *(uint2*)(out + part * kSlot + o) = b;
-            e[0] -= bf_lo(b.x); e[1] -= bf_hi(b.x); e[2] -= bf_lo(b.y); e[3] -= bf_hi(b.y);
+            for (int part = 0; part < PARTS; ++part) {
+              const uint2 b = make_uint2(pack(e[0], e[1]), pack(e[2], e[3]));
+              put(part * kSlot + o, b);
+              e[0] -= bf_lo(b.x); e[1] -= bf_hi(b.x); e[2] -= bf_lo(b.y); e[3] -= bf_hi(b.y);
+            }
           }
-        }
+        };
+        split([&](uint32_t o, uint2 b) { *(uint2*)(fixed + o) = b; });
         fence_proxy_async_smem();
         mbar_arrive(fix_full);
+        // (written out behind the fence, which would wait for it)
+        if (x.i0 == 0) split([&](uint32_t o, uint2 b) { *(uint2*)(out + o) = b; });
       }
       if (PASS == kSumsOne && x.n > 0) {   // the statistics came with the row tile
         wait(fix_full, rf.ph);
