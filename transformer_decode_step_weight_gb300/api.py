@@ -472,7 +472,7 @@ _WINDOW_HEAD = 16384
 
 
 def _counts(fn, **values):
-    """Refuses numbers that a 32-bit argument would not hold as they are."""
+    """Refuses numbers that a 32-bit argument would not hold as they are (the others the library refuses)."""
     for name, n in values.items():
         if not -ALL_KEYS <= n <= ALL_KEYS:
             raise ValueError(f"{fn}: {name}={n}")
@@ -495,7 +495,8 @@ def attn_prompt_window(q, k_pages, v_pages, page_table, cu_rows, seq_lens, scale
     if cu_rows.shape[0] != B + 1:
         raise ValueError(f"{fn}: {cu_rows.numel()} segment starts for {B} sequences")
     window = ALL_KEYS if window is None else window
-    _counts(fn, window=window, n_sinks=n_sinks)
+    if not (0 < window <= ALL_KEYS and 0 <= n_sinks <= ALL_KEYS):
+        _counts(fn, window=window, n_sinks=n_sinks)
     if out is None:
         out = torch.empty((n, Hq, D), dtype=q.dtype, device=q.device)
     if n == 0:
@@ -533,7 +534,8 @@ def attn_decode_window(q, k_pages, v_pages, page_table, seq_lens, scale, window=
     if page_table.shape[0] != B:
         raise ValueError(f"{fn}: {page_table.shape[0]} page tables for {B} rows")
     window = ALL_KEYS if window is None else window
-    _counts(fn, window=window, n_sinks=n_sinks)
+    if not (0 < window <= ALL_KEYS and 0 <= n_sinks <= ALL_KEYS):
+        _counts(fn, window=window, n_sinks=n_sinks)
     keys = 0
     if key_weights is not None:
         _want("key_weights", key_weights, torch.float32, 3, dev, (B, Hkv, max_pages * ps))
@@ -574,7 +576,8 @@ def attn_key_weights(q, k_pages, page_table, cu_rows, seq_lens, scale, key_weigh
         raise ValueError(f"{fn}: {cu_rows.numel()} segment starts for {B} sequences")
     _want("key_weights", key_weights, torch.float32, 3, dev, (B, Hkv, max_pages * ps))
     window = ALL_KEYS if window is None else window
-    _counts(fn, window=window, n_sinks=n_sinks, last=last)
+    if not (0 < window <= ALL_KEYS and 0 <= n_sinks <= ALL_KEYS and 0 <= last <= ALL_KEYS):
+        _counts(fn, window=window, n_sinks=n_sinks, last=last)
     if n == 0:
         return key_weights
     workspace = _scratch(workspace, lambda: attn_key_weights_workspace_bytes(B, n, Hq, Hkv, last), q, _WINDOW_HEAD)
@@ -613,7 +616,8 @@ def qk_norm_rope(qkv, q_norm, k_norm, rope, k_pages, v_pages, page_table, cu_row
     _want("q_norm", q_norm, torch.bfloat16, 1, dev, (D,))
     _want("k_norm", k_norm, torch.bfloat16, 1, dev, (D,))
     _want("rope", rope, torch.float32, 3, dev)
-    if rope.shape[1:] != (D // 2, 2):
+    rope_max, half, two = rope.shape
+    if 2 * half != D or two != 2:
         raise ValueError(f"{fn}: rope table {tuple(rope.shape)}, expected [positions, {D // 2}, 2]")
     _want("page_table", page_table, torch.int32, 2, dev)
     B, max_pages = page_table.shape
@@ -641,7 +645,7 @@ def qk_norm_rope(qkv, q_norm, k_norm, rope, k_pages, v_pages, page_table, cu_row
     if n == 0:
         return out
     _check(lib().qd_qk_norm_rope(qkv.data_ptr(), qkv.dtype is torch.float32, qkv.stride(0) if n > 1 else width,
-                                 q_norm.data_ptr(), k_norm.data_ptr(), eps, bool(cast), rope.data_ptr(), rope.shape[0],
+                                 q_norm.data_ptr(), k_norm.data_ptr(), eps, bool(cast), rope.data_ptr(), rope_max,
                                  _p(positions), n_axes, axes, page_table.data_ptr(), cu_rows.data_ptr(),
                                  seq_lens.data_ptr(), B, n, Hq, Hkv, D, ps, max_pages, n_pages, out.data_ptr(),
                                  out.dtype is torch.float32, k_pages.data_ptr(), v_pages.data_ptr(), _raw_stream(dev)))
@@ -741,7 +745,8 @@ class PageCache:
         a = self.args
         _want("key_weights", key_weights, torch.float32, 4, self._dev,
               (a.n_layers, a.max_seqs, a.n_kv_heads, a.max_pages * a.page_size))
-        _counts("evict", n_sinks=n_sinks, n_recent=n_recent)
+        if not (0 <= n_sinks <= ALL_KEYS and 0 <= n_recent <= ALL_KEYS):
+            _counts("evict", n_sinks=n_sinks, n_recent=n_recent)
         self._run(stream, lib().qd_pages_evict, key_weights.data_ptr(), self._list("keep", keep, a.max_seqs), n_sinks,
                   n_recent)
 

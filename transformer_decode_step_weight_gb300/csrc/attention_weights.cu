@@ -19,9 +19,9 @@
 // two S buffers and one brings tiles; they meet at mbarriers only. With a CTA barrier per tile, the
 // loads shared by all warps, a tile took 1900 to 2900 cycles. Bounds: the exponentials, one a (row, key) in
 // each launch, 1024 cycles a pair of tiles (MUFU), against 512 for the product of bf16 tiles; an f32
-// q's three parts take 1536. A tile takes 1430 cycles (bf16), 1600 (f32). Last 32 rows of 8 prompts (bf16,
-// 48 key tiles each): 66 us, two launches of 33, of which 20 the longest CTA's 27 tiles; all 2011 rows of one
-// prompt (f32): 62 us.
+// q's three parts take 1536. A tile takes 1100 to 1600 cycles. Last 32 rows of 8 prompts (bf16, 48
+// key tiles each): 60 us, in each launch a start of some 8 us (segments, Q, the first tile) and 20 tiles a CTA, in the
+// first at HBM's rate; all 2011 rows of one prompt (f32): 63 us.
 //
 // Every wait is bounded; after a timeout all roles run through without touching anything.
 #include "common.cuh"
