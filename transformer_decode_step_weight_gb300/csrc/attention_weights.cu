@@ -20,7 +20,7 @@
 // loads shared by all warps, a tile took 1900 to 2900 cycles. Bounds: the exponentials, one a (row, key) in
 // each launch, 1024 cycles a pair of tiles (MUFU), against 512 for the product of bf16 tiles; an f32
 // q's three parts take 1536. A tile takes 1100 to 1600 cycles. Last 32 rows of 8 prompts (bf16, 48
-// key tiles each): 60 us, in each launch a start of some 8 us (segments, Q, the first tile) and 20 tiles a CTA, in the
+// key tiles each): 59 us, in each launch a start of some 8 us (segments, Q, the first tile) and 20 tiles a CTA, in the
 // first at HBM's rate; all 2011 rows of one prompt (f32): 63 us.
 //
 // Every wait is bounded; after a timeout all roles run through without touching anything.
@@ -449,8 +449,9 @@ __global__ void __launch_bounds__(kTh, 1) attn_weights_kernel(const __grid_const
     x.first_rt = p.base[x.s] * p.Hkv + (long long)x.g * tiles;
     return x;
   };
+  // (kSumsOne: backwards, since the first launch left the last tiles in L2: 58.6 us instead of 59.4)
   auto tile_at = [&](const Item& x, int i) {
-    const int t = x.w0 + x.i0 + i * shares;
+    const int t = x.w0 + x.i0 + (PASS == kSumsOne ? x.n - 1 - i : i * shares);
     return t >= x.jump_at ? t + x.jump : t;
   };
   // a wait of a whole warp, bounded by its polls (each returns after 2 us where nothing comes); after a timeout
