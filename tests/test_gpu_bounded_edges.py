@@ -1,0 +1,41 @@
+"""Calls of the operators that fill and bound the cache at the ends of what they accept: windows and first tokens that
+hide nothing, very many sequences, shared pages of which no token goes."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import bounded_reference as ref
+from test_gpu_window import ALL, D, DEV, DTYPES, SCALE, _check_decode, _check_prompt, _check_weights, _gen, _ints, _pack, _pick, _q
+from transformer_decode_step_weight_gb300 import api
+
+pytestmark = pytest.mark.gpu
+HEAD = 16384     # what of a workspace has to be zero before its first use, at most
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("window,sinks", [(None, ALL), (2 ** 30, 2 ** 30 - 15), (2 ** 30 - 1, 2 ** 30), (None, 2 ** 30 - 16),
+                                          (1, ALL)])
+def test_neither_window_nor_first_tokens_hide_anything(cuda_lib, window, sinks, dtype):
+    # rows of several row tiles (of 32 and 128 tokens), from an empty cache and just behind its first tokens
+    for hq, hkv, rows, lens in ((8, 2, [300, 77], [300, 80]), (2, 2, [900, 130], [900, 144])):
+        g = _gen(hq)
+        kp, vp, pt = ref.make_cache(g, lens, hkv, 16)
+        cu, seqs, at = _pack(rows, lens)
+        q = _q(g, cu[-1], hq, dtype)
+        ws = torch.zeros(api.attn_prompt_workspace_bytes(), dtype=torch.uint8, device=DEV)
+        args = (q, kp, vp, pt, _ints(cu), _ints(lens), SCALE)
+        out = torch.full((cu[-1], hq, D), math.nan, dtype=dtype, device=DEV)
+        api.attn_prompt_window(*args, window, sinks, out=out, workspace=ws)
+        _check_prompt(out, q, kp, vp, pt, lens, seqs, at, ALL, 0, rows=_pick(cu[-1], np.random.default_rng(1)))
+        assert torch.equal(out, api.attn_prompt_window(*args, workspace=ws))      # the same tiles in the same order
+        assert bool((ws[:8192] == 0).all())
+        sums = torch.zeros((2, hkv, pt.shape[1] * 16), device=DEV)
+        before = sums.clone()
+        api.attn_key_weights(q, kp, pt, _ints(cu), _ints(lens), SCALE, sums, window=window, n_sinks=sinks)
+        _check_weights(sums, before, q, kp, pt, rows, lens, cu, 0, ALL, 0)
+        last, sums = q[[cu[1] - 1, cu[2] - 1]].contiguous(), before.clone()
+        one = api.attn_decode_window(last, kp, vp, pt, _ints(lens), SCALE, window, sinks, key_weights=sums)
+        _check_decode(one, last, kp, vp, pt, lens, ALL, 0, sums=sums, before=before)
+    assert api.check_device_error() == 0

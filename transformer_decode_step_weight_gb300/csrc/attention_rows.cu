@@ -311,8 +311,9 @@ struct Work {
     long long sum = t == a.tiles && t > 0 ? units(a, t - 1) : 0;   // (prompt form: steps are tiles)
     if (full <= 0) return sum;
     if (WINDOW) {   // whole row tiles that leave keys out all have as many units (16 divides a row tile's tokens)
-      const int c = (a.off + 1 - window) & ~15;   // tile i's windows begin at c + i tpt, rounded down
-      const int i1 = first16() < c ? 0 : min(full, ((first16() - c) >> log_tpt) + 1);   // the first that does
+      // tile i's windows begin at first16 - d + i tpt, rounded down (d may be 2^31: neither hides anything)
+      const long long d = (long long)first16() - ((a.off + 1 - window) & ~15);
+      const int i1 = d < 0 ? 0 : (int)min((long long)full, (d >> log_tpt) + 1);   // the first that leaves some out
       if (i1 < full) sum += (long long)(full - i1) * units(a, i1);
       full = i1;
       if (full == 0) return sum;
