@@ -247,6 +247,19 @@ int qd_attn_prompt(const void* q, int q_is_f32, int64_t q_stride, const void* k_
                    int n_pages, float scale, void* out, void* workspace, size_t workspace_bytes,
                    cudaStream_t stream);
 
+/* Attention of packed rows over a window: qd_attn_prompt in which the row at token p sees the     */
+/* tokens t <= p with t > p - window or t < n_sinks (the first tokens of the cache stay visible);    */
+/* a page of which no row of the sequence sees a token is not read, and its entry in page_table may  */
+/* name none. window >= 1 (2147483647: every token), n_sinks >= 0, else QD_ERR_INVALID_ARG; both may   */
+/* hide nothing. The other arguments, limits, errors and the workspace (which serves either call)       */
+/* are qd_attn_prompt's; so is what a row before position 0 gives, and a row that sees NaN or            */
+/* infinities.                                                                                          */
+int qd_attn_prompt_window(const void* q, int q_is_f32, int64_t q_stride, const void* k_pages, const void* v_pages,
+                          const int32_t* page_table, const int32_t* cu_rows, const int32_t* seq_lens, int batch,
+                          int n_rows, int n_q_heads, int n_kv_heads, int head_dim, int page_size, int max_pages,
+                          int n_pages, float scale, int window, int n_sinks, void* out, void* workspace,
+                          size_t workspace_bytes, cudaStream_t stream);
+
 /* Decode attention of sequences that share prefixes: the result of qd_attn_decode_paged for      */
 /* sequences whose page tables name the same pages at their start (qd_pages_fork), each shared     */
 /* page read once for all of them. Where that would spare less than 80 MB of re-reading in the     */
