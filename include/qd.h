@@ -412,9 +412,9 @@ int qd_pages_compact(const qd_page_cache* cache, int32_t* n_live, cudaStream_t s
 /* key_weights: f32 [n_layers, max_seqs, n_kv_heads, max_pages * page_size], device (each layer's part        */
 /* filled by qd_attn_decode_window and qd_attn_key_weights; they go by sequence and token, so the other page     */
 /* calls leave them: after a trim or before a slot's next sequence zero the tokens behind its length, for a      */
-/* fork copy the parent's). A page that would be written and that others                                          */
-/* share (qd_pages_fork), or a length past the table, changes nothing and sets QD_DEVERR_CACHE; so does a         */
-/* table entry that names no page (with QD_DEVERR_PAGE).                                                          */
+/* fork copy the parent's). A page that may be written (one with a token between the first ones that stay         */
+/* and the new length) and that others share (qd_pages_fork), or a length past the table, changes nothing and     */
+/* sets QD_DEVERR_CACHE; so does a table entry that names no page (with QD_DEVERR_PAGE).                          */
 /* Limits: head_dim <= 256, n_pages * n_kv_heads * page_size < 2^31.                                               */
 int qd_pages_evict(const qd_page_cache* cache, float* key_weights, const int32_t* keep, int n_sinks, int n_recent,
                    cudaStream_t stream);

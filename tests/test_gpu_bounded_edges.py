@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import bounded_reference as ref
+from test_gpu_evict import CACHE, State
 from test_gpu_window import ALL, D, DEV, DTYPES, SCALE, _check_decode, _check_prompt, _check_weights, _gen, _ints, _pack, _pick, _q
 from transformer_decode_step_weight_gb300 import api
 
@@ -39,3 +40,20 @@ def test_neither_window_nor_first_tokens_hide_anything(cuda_lib, window, sinks, 
         one = api.attn_decode_window(last, kp, vp, pt, _ints(lens), SCALE, window, sinks, key_weights=sums)
         _check_decode(one, last, kp, vp, pt, lens, ALL, 0, sums=sums, before=before)
     assert api.check_device_error() == 0
+
+
+def test_evict_to_first_tokens_on_a_shared_page(cuda_lib):
+    # nothing moves where a sequence keeps first tokens alone: a page that it shares is not written
+    s = State([90, 0, 100], 2, 2, 16)
+    s.cache.fork(_ints([0]), _ints([1]))
+    for keep, sinks, lens in (([40, -1, -1], 64, [40, 90, 100]), ([-1, 5, 30], 40, [40, 5, 30]), ([7, 0, 3], 7, [7, 0, 3])):
+        s.save()
+        s.cache.evict(s.w, _ints(keep), sinks, 3)
+        s.check(keep, sinks, 3)
+        assert api.check_device_error() == 0 and s.cache.seq_lens.tolist() == lens
+    # ... but where others stay, the page that they would move into has to be the sequence's own
+    s = State([90, 0], 2, 2, 16)
+    s.cache.fork(_ints([0]), _ints([1]))
+    s.save()
+    s.cache.evict(s.w, _ints([41, -1]), 40, 3)
+    assert api.check_device_error() == CACHE and s.same()

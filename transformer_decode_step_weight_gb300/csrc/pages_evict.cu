@@ -61,8 +61,10 @@ __global__ void __launch_bounds__(kPlan) pages_evict_plan_kernel(PageState c, Pa
       if (lane == 0) atomicOr(&s_bad, QD_DEVERR_CACHE);
       continue;
     }
-    // pages from the first token that may go on: they exist, and those that are written have one owner
-    const int p0 = always(k, n_sinks, n_recent).first / ps, written = pages_of(k, ps), all = pages_of(n, ps);
+    // pages from the first token that may go on: they exist, and those that are written have one owner (none are
+    // where first tokens alone stay)
+    const int first = always(k, n_sinks, n_recent).first;
+    const int p0 = first / ps, written = first < k ? pages_of(k, ps) : 0, all = pages_of(n, ps);
     int bad = 0;
     for (int i = p0 + lane; i < all; i += 32) {
       const int page = c.table[(size_t)s * c.max_pages + i];
