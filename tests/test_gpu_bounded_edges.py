@@ -57,3 +57,35 @@ def test_evict_to_first_tokens_on_a_shared_page(cuda_lib):
     s.save()
     s.cache.evict(s.w, _ints([41, -1]), 40, 3)
     assert api.check_device_error() == CACHE and s.same()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", [33, 577, 600, 1024])
+def test_many_sequences(cuda_lib, n, dtype):
+    # more than a warp's look takes (32), than a thread has one of (576), the most; empty ones at both ends and in runs
+    g, r = _gen(n), np.random.default_rng(n)
+    lens = [int(x) for x in r.integers(0, 90, n)]
+    rows = [int(r.integers(0, m + 1)) for m in lens]
+    for i in [0, 1, n - 1, *range(n // 3, n // 3 + 20), *r.integers(0, n, n // 8)]:
+        rows[i] = 0
+    rows[n // 2], lens[n // 2] = 150, 400                  # several row tiles
+    hq, hkv, window, sinks = 8, 2, 50, 3
+    kp, vp, pt = ref.make_cache(g, lens, hkv, 16)
+    cu, seqs, at = _pack(rows, lens)
+    q = _q(g, cu[-1], hq, dtype)
+    some = set(r.choice(n, 25, replace=False).tolist()) | {0, 2, n // 2, n - 2, n - 1}
+    for last, win in ((0, ALL), (0, window), (20, ALL), (20, window)):       # (20 rows of 4 heads: one row tile each)
+        before = torch.rand((n, hkv, pt.shape[1] * 16), generator=g, device=DEV) * 0.1
+        sums = before.clone()
+        api.attn_key_weights(q, kp, pt, _ints(cu), _ints(lens), SCALE, sums, last=last, window=win, n_sinks=sinks)
+        _check_weights(sums, before, q, kp, pt, rows, lens, cu, last, win, sinks, seqs=some)
+        # each row's weights are 1 together, and what lies behind a sequence stays
+        used = torch.tensor([min(x, last) if last else x for x in rows], dtype=torch.float64) * (hq // hkv)
+        more = (sums.double() - before.double()).cpu()
+        total = more.sum(-1)
+        assert bool(((total - used[:, None]).abs() <= 2.0 ** -14 * used[:, None] + 400 * 2.0 ** -23).all())
+        behind = torch.arange(more.shape[2])[None] >= torch.tensor(lens)[:, None]
+        assert bool((more.transpose(1, 2)[behind] == 0).all()) and bool((more[used == 0] == 0).all())
+    out = api.attn_prompt_window(q, kp, vp, pt, _ints(cu), _ints(lens), SCALE, window, sinks)
+    _check_prompt(out, q, kp, vp, pt, lens, seqs, at, window, sinks, rows=[i for i, b in enumerate(seqs) if b in some])
+    assert api.check_device_error() == 0
