@@ -727,6 +727,10 @@ __global__ void __launch_bounds__(kTh, 1) attn_weights_kernel(const __grid_const
       for (int i = 0; i < x.n; ++i) {
         const int t = tile_at(x, i);
         wait(&s_full[rb.slot], rb.ph);
+        if (kRows) {   // the row tile's statistics came with it, and only its own barrier says that they are there (s_full
+          wait(&full[rt.slot], rt.ph);   // follows from it by the products). It is not used again before this warp frees them
+          rt.step(kStages);
+        }
         tc::fence_after();
         float v[32];
         ld32(tS + 128 * rb.slot + lanes + col0, v);
