@@ -181,29 +181,16 @@ QD_DEV void tma_load_rows(void* dst, const CUtensorMap* map, int row, uint64_t* 
 }
 // The products are issued by one lane of a warp whose lanes all walk the same way, so that
 // descriptors stay in uniform registers; `lead` says which lane.
-// Step kk of 16 keys, left out by lanes whose `steps` it is not below, and (window form) where it is below
-// `step0`.
-template <bool WINDOW>
-QD_DEV void mma_pv(int step0, int steps, int kk, uint32_t tmem_d, uint32_t tmem_a, uint64_t db, uint32_t accumulate) {
+// Step kk of 16 keys, left out by lanes whose `steps` it is not below.
+QD_DEV void mma_pv(int steps, int kk, uint32_t tmem_d, uint32_t tmem_a, uint64_t db, uint32_t accumulate) {
   constexpr uint32_t kIdesc = tc::idesc_m128(kD) | (1u << 16);   // B MN-major
-  if constexpr (WINDOW) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.gt.s32 q, %5, %6;\n\t"
-        "setp.le.and.s32 q, %7, %6, q;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
-        "r"(tmem_a), "l"(db), "r"(kIdesc), "r"(accumulate), "r"(steps), "r"(kk), "r"(step0)
-        : "memory");
-  } else {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.gt.s32 q, %5, %6;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
-        "r"(tmem_a), "l"(db), "r"(kIdesc), "r"(accumulate), "r"(steps), "r"(kk)
-        : "memory");
-  }
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.gt.s32 q, %5, %6;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(db), "r"(kIdesc), "r"(accumulate), "r"(steps), "r"(kk)
+      : "memory");
 }
 QD_DEV void mma_qk(bool lead, uint32_t tmem_d, uint64_t da, uint64_t db, uint32_t accumulate) {
   constexpr uint32_t kIdesc = tc::idesc_m128(kKeys);
@@ -893,8 +880,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t slot = kRingK + rk.slot;
           wait(&full[slot], rk.ph);
           const int key0 = (k0 + i) * kKeys;
-          int steps = kKeys / 16;   // of 16 keys that some row sees
-          int step0 = 0;            // window form: the first of them
+          int steps = kKeys / 16;   // of 16 keys, up to the last that some row sees
           const bool behind_some = WINDOW && key0 < pc.all && key0 + kKeys > W.sinks;
           if (key0 + kKeys > seen_min || behind_some) {
             // a V tile that some row must not see whole: NaN and infinities taken out, rows past
@@ -904,12 +890,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (WINDOW && behind_some) {
               const bool some_first = key0 < W.sinks;
               if (pc.gap >= key0 + kKeys) hi = min(hi, W.sinks - key0);   // of the first tokens' tile nothing else
-              if (!some_first) step0 = max(0, pc.gap - key0) >> 4;
               free0 = max(0, pc.all - key0);   // from here on only those behind the rows' last keys
               free1 = max(lo, free0);
-              lo = some_first ? min(lo, W.sinks - key0) : min(lo, step0 * 16);
+              lo = some_first ? min(lo, W.sinks - key0) : 0;
             }
-            steps = max(step0 + 1, (hi + 15) >> 4);
+            steps = max(1, (hi + 15) >> 4);
             // lane: of key lane / 4 in a group of 8, 16-byte pieces lane & 3, + 4, + 8, + 12
             const int sub = lane >> 2, cc = lane & 3;
             unsigned char* v = data + (kQ + slot) * kSlot + sub * 128;
@@ -957,9 +942,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t t32 = part < 2 ? 32 : 16;
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              mma_pv<WINDOW>(step0, go, kk, tO, ta + t32 * (kk >> 1) + 8 * (kk & 1),
-                             dv + (uint64_t)(kk * 2 * kKeys8 >> 4),
-                             (WINDOW ? kk != step0 : kk != 0) || part != PARTS - 1 || !first);
+              mma_pv(go, kk, tO, ta + t32 * (kk >> 1) + 8 * (kk & 1), dv + (uint64_t)(kk * 2 * kKeys8 >> 4),
+                     kk != 0 || part != PARTS - 1 || !first);
           }
           commit(lead, &o_done[rb.slot]);
           commit(lead, &empty[slot]);
