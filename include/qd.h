@@ -312,11 +312,14 @@ int qd_attn_decode_window(const void* q, int q_is_f32, int64_t q_stride, const v
 /* qd_attn_prompt_window, whose rows' attention it is (q and cache as there, V not needed); q_is_f32 = 1:     */
 /* q enters the products in three bf16 parts. Deterministic. A visible NaN makes all of its row's weights     */
 /* NaN; keys that no counted row sees keep their sums. workspace: qd_attn_key_weights_workspace_bytes(...)      */
-/* bytes (for an f32 q; a bf16 one needs about a third), its first QD_ATTN_WEIGHTS_HEAD bytes zero-filled          */
+/* bytes, which serve either type of q (..._for: of one type; a bf16 q needs about a third: q's row tiles in one     */
+/* part instead of three), its first QD_ATTN_WEIGHTS_HEAD bytes zero-filled                                         */
 /* before its first use (each call leaves them zero, but for one that ends with QD_DEVERR_TIMEOUT: zero-fill       */
 /* them again); two calls that overlap on the GPU need two.                                                        */
 #define QD_ATTN_WEIGHTS_HEAD 16384
 size_t qd_attn_key_weights_workspace_bytes(int batch, int n_rows, int n_q_heads, int n_kv_heads, int last);
+size_t qd_attn_key_weights_workspace_bytes_for(int q_is_f32, int batch, int n_rows, int n_q_heads, int n_kv_heads,
+                                               int last);
 int qd_attn_key_weights(const void* q, int q_is_f32, int64_t q_stride, const void* k_pages, const int32_t* page_table,
                         const int32_t* cu_rows, const int32_t* seq_lens, int batch, int n_rows, int n_q_heads,
                         int n_kv_heads, int head_dim, int page_size, int max_pages, int n_pages, float scale, int last,

@@ -89,3 +89,31 @@ def test_many_sequences(cuda_lib, n, dtype):
     out = api.attn_prompt_window(q, kp, vp, pt, _ints(cu), _ints(lens), SCALE, window, sinks)
     _check_prompt(out, q, kp, vp, pt, lens, seqs, at, window, sinks, rows=[i for i, b in enumerate(seqs) if b in some])
     assert api.check_device_error() == 0
+
+
+@pytest.mark.parametrize("last", [0, 30])
+def test_weights_of_a_bf16_q_in_its_own_workspace(cuda_lib, last):
+    g = _gen(31)
+    rows, lens, hq, hkv = [700, 0, 200], [700, 5, 900], 8, 2
+    kp, vp, pt = ref.make_cache(g, lens, hkv, 16)
+    cu, _, _ = _pack(rows, lens)
+    q = _q(g, cu[-1], hq, torch.bfloat16)
+    got = []
+    for dtype in (torch.float32, torch.bfloat16, None):
+        sums = torch.zeros((3, hkv, pt.shape[1] * 16), device=DEV)
+        ws = None
+        if dtype is not None:     # with bytes behind it that have to stay
+            n = api.attn_key_weights_workspace_bytes(3, cu[-1], hq, hkv, last, dtype)
+            room = torch.full((n + 4096,), 255, dtype=torch.uint8, device=DEV)
+            room[:HEAD] = 0
+            ws = room[:n]
+        # (bytes asked for: the allocator does not split a block where less than 1 MB would be left)
+        torch.cuda.reset_peak_memory_stats()
+        start = torch.cuda.memory_stats()["requested_bytes.all.current"]
+        api.attn_key_weights(q, kp, pt, _ints(cu), _ints(lens), SCALE, sums, last=last, workspace=ws)
+        used = torch.cuda.memory_stats()["requested_bytes.all.peak"] - start
+        assert ws is None or bool((room[n:] == 255).all())
+        got.append(sums)
+    assert used <= n + 8192 and torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+    _check_weights(got[0], torch.zeros_like(got[0]), q, kp, pt, rows, lens, cu, last, ALL, 0)
+    assert api.check_device_error() == 0

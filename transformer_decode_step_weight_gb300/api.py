@@ -82,6 +82,7 @@ _SIGS = {
     "qd_attn_decode_window_workspace_bytes": (_sz, [_i, _i, _i, _l]),
     "qd_attn_decode_window": (_i, [_vp, _i, _l] + [_vp] * 4 + [_i] * 7 + [_f, _i, _i, _vp, _vp, _vp, _sz, _vp]),
     "qd_attn_key_weights_workspace_bytes": (_sz, [_i] * 5),
+    "qd_attn_key_weights_workspace_bytes_for": (_sz, [_i] * 6),
     "qd_attn_key_weights": (_i, [_vp, _i, _l] + [_vp] * 4 + [_i] * 8 + [_f, _i, _i, _i, _vp, _vp, _sz, _vp]),
     "qd_qk_norm_rope": (_i, [_vp, _i, _l, _vp, _vp, _f, _i, _vp, _i, _vp, _i, C.c_char_p, _vp, _vp, _vp] + [_i] * 8
                         + [_vp, _i, _vp, _vp, _vp]),
@@ -552,8 +553,12 @@ def attn_decode_window(q, k_pages, v_pages, page_table, seq_lens, scale, window=
     return out
 
 
-def attn_key_weights_workspace_bytes(batch: int, rows: int, hq: int, hkv: int, last: int = 0) -> int:
-    return int(lib().qd_attn_key_weights_workspace_bytes(batch, rows, hq, hkv, last))
+def attn_key_weights_workspace_bytes(batch: int, rows: int, hq: int, hkv: int, last: int = 0,
+                                     dtype=torch.float32) -> int:
+    """dtype: q's type (float32's size, three times bfloat16's, serves either)."""
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"attn_key_weights: dtype {dtype}, expected float32 or bfloat16")
+    return int(lib().qd_attn_key_weights_workspace_bytes_for(dtype is torch.float32, batch, rows, hq, hkv, last))
 
 
 def attn_key_weights(q, k_pages, page_table, cu_rows, seq_lens, scale, key_weights, last=0, window=None, n_sinks=0,
@@ -580,7 +585,8 @@ def attn_key_weights(q, k_pages, page_table, cu_rows, seq_lens, scale, key_weigh
         _counts(fn, window=window, n_sinks=n_sinks, last=last)
     if n == 0:
         return key_weights
-    workspace = _scratch(workspace, lambda: attn_key_weights_workspace_bytes(B, n, Hq, Hkv, last), q, _WINDOW_HEAD)
+    workspace = _scratch(workspace, lambda: attn_key_weights_workspace_bytes(B, n, Hq, Hkv, last, q.dtype), q,
+                         _WINDOW_HEAD)
     _check(lib().qd_attn_key_weights(q.data_ptr(), q.dtype is torch.float32, q_stride, k_pages.data_ptr(),
                                      page_table.data_ptr(), cu_rows.data_ptr(), seq_lens.data_ptr(), B, n, Hq, Hkv, D,
                                      ps, max_pages, n_pages, scale, last, window, n_sinks,

@@ -540,9 +540,13 @@ int qd_attn_decode_window(const void* q, int q_is_f32, int64_t q_stride, const v
 }
 
 static_assert(kAttnWeightsHeadBytes == QD_ATTN_WEIGHTS_HEAD, "the head that the header names");
+size_t qd_attn_key_weights_workspace_bytes_for(int q_is_f32, int batch, int n_rows, int n_q_heads, int n_kv_heads,
+                                               int last) {
+  if (q_is_f32 & ~1 || batch < 1 || n_rows < 1 || n_kv_heads < 1 || n_q_heads < n_kv_heads || last < 0) return 0;
+  return attn_key_weights_workspace_bytes(batch, n_rows, n_q_heads, n_kv_heads, last, q_is_f32 != 0);
+}
 size_t qd_attn_key_weights_workspace_bytes(int batch, int n_rows, int n_q_heads, int n_kv_heads, int last) {
-  if (batch < 1 || n_rows < 1 || n_kv_heads < 1 || n_q_heads < n_kv_heads || last < 0) return 0;
-  return attn_key_weights_workspace_bytes(batch, n_rows, n_q_heads, n_kv_heads, last, true);
+  return qd_attn_key_weights_workspace_bytes_for(1, batch, n_rows, n_q_heads, n_kv_heads, last);
 }
 
 int qd_attn_key_weights(const void* q, int q_is_f32, int64_t q_stride, const void* k_pages, const int32_t* page_table,
