@@ -43,7 +43,7 @@
 // Window form (qd_attn_prompt_window): a row sees its last `window` tokens and the first `sinks`. The keys
 // that no row of a row tile sees are left out (Work::skip), so a row tile's units are those of its
 // first tokens and its rows' windows, of which two or three are masked. 16 messages behind 3000 to 6000 keys with
-// a window of 1024: 153 us, 8192 tokens with 2048: 236 us (1046 TFLOP/s); the units' products are a third
+// a window of 1024: 153 us, 8192 tokens with 2048: 235 us (1050 TFLOP/s); the units' products are a third
 // of the first and half of the second, the rest mostly starts and ends of row tiles.
 #include "common.cuh"
 #include "kernels.h"

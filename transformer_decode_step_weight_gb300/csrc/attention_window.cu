@@ -431,6 +431,10 @@ int splits(int B, int Hkv) {
 // Keys per split at least: few pairs take short splits, since then the chain of loads is the time.
 // 8 pairs of 1028 keys: 64 8.9 us, 128 7.7, 256 9.6, 512 12.1; 128 pairs of 5700 keys with weights:
 // 256 98 us, 512 93, 1024 87, 2048 88; 512 pairs of 4100: 64 to 512 176 us, 1024 174, 2048 184.
+// The borders go by pairs alone, not by the visible keys, and lie where these were measured. With 8 kv heads
+// (bf16 q; us at 260, 1028 and 4096 visible keys): 1 sequence 7.6, 7.7, 10.9; 4 11, 13, 22; 8 14, 18, 33; 15 15, 23, 53;
+// 16 13, 29, 57; 32 15, 35, 94; 64 20, 57, 166. So just above a border a short window is split worst: 16 sequences'
+// 1028 keys go to splits of 1024 and 4, and half of the CTAs have next to nothing to do.
 int min_chunk(int B, int Hkv) {
   const long long pairs = (long long)B * Hkv;
   return pairs >= 128 ? 1024 : pairs >= 32 ? 256 : 128;
