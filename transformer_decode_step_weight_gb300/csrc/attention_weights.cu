@@ -727,8 +727,10 @@ __global__ void __launch_bounds__(kTh, 1) attn_weights_kernel(const __grid_const
       for (int i = 0; i < x.n; ++i) {
         const int t = tile_at(x, i);
         wait(&s_full[rb.slot], rb.ph);
-        if (kRows) {   // the row tile's statistics came with it, and only its own barrier says that they are there (s_full
-          wait(&full[rt.slot], rt.ph);   // follows from it by the products). It is not used again before this warp frees them
+        if (kRows) {
+          // The row tile's statistics came with it, and its own barrier alone says that they are there: s_full tells of
+          // the products. The slot is not filled again before this warp has freed the statistics (two at a time)
+          wait(&full[rt.slot], rt.ph);
           rt.step(kStages);
         }
         tc::fence_after();
